@@ -409,6 +409,238 @@ Q3KV_API int q3kv_accept_sample_nucleus(void* stream, const void* logits, int32_
                        int32_t* d_n_accepted, int32_t* d_next_token, int32_t* d_committed_len,
                        void* d_workspace, size_t workspace_bytes, int32_t* d_status);
 
+/* ---- rotary positions with several axes ------------------------------------------
+ * Rotates the step's query and key rows by their positions before the append
+ * and the verify.  The pages have no counterpart (their engine rotates inside
+ * its own projections); the call is here because after an eviction a cache row
+ * is no longer a position, so positions are given explicitly, and because rows
+ * of images and video carry one position per axis (time, height, width).
+ *
+ * The first rotary_dim of the 256 dims are rotary_dim / 2 pairs.  Pair i turns
+ * by the angle a_i = position[axis_i] * f_i:
+ *   (x, y) -> (x cos a_i - y sin a_i, x sin a_i + y cos a_i)
+ * in float32, rounded once to the output type; the other dims are copied.
+ *   - Pairs: dims (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ *     Q3KV_ROPE_ADJACENT.
+ *   - Axes: sections[a] pairs belong to axis a (their sum is rotary_dim / 2), in
+ *     runs, or dealt in turn with Q3KV_ROPE_DEAL_AXES (pair 0 to axis 0, pair 1
+ *     to axis 1, ..; an axis that has all its pairs is passed over).
+ *   - Frequencies: f_i = theta^(-i / (rotary_dim / 2)), or with
+ *     Q3KV_ROPE_AXIS_FREQS theta^(-k / sections[a]) for the k-th pair of axis a.
+ * A plan holds each pair's frequency as a 64-bit fixed-point fraction of a turn,
+ * so position * frequency is exact modulo whole turns for every int32 position
+ * (float32 angles lose whole digits beyond a few thousand positions).  It is a
+ * plain host struct; a caller may fill turns[] itself (scaled frequencies):
+ * turns[i] = round(f_i / (2 pi) * 2^64). */
+#define Q3KV_ROPE_ADJACENT   1
+#define Q3KV_ROPE_DEAL_AXES  2
+#define Q3KV_ROPE_AXIS_FREQS 4
+#define Q3KV_ROPE_MAX_AXES   4
+
+typedef struct q3kv_rope_config {
+    double theta;                            /* > 1, finite                                */
+    int32_t rotary_dim;                      /* 16 .. 256, a multiple of 16                */
+    int32_t num_axes;                        /* 1 .. 4                                     */
+    int32_t sections[Q3KV_ROPE_MAX_AXES];    /* pairs of each axis (0 allowed)             */
+    int32_t flags;                           /* Q3KV_ROPE_*                                */
+    int32_t reserved;                        /* 0                                          */
+} q3kv_rope_config;
+
+typedef struct q3kv_rope_plan {
+    uint64_t turns[128];                     /* pair i: 2^-64 turns per position           */
+    uint8_t axis[128];                       /* pair i: its axis                           */
+    int32_t rotary_dim;
+    int32_t num_axes;
+    int32_t flags;
+    int32_t reserved;
+} q3kv_rope_plan;
+
+/* Fills *plan (host only, no device work).  Q3KV_ERR_INVALID_ARG for a config
+ * outside the ranges above. */
+Q3KV_API int q3kv_rope_plan_init(const q3kv_rope_config* config, q3kv_rope_plan* plan);
+
+/* q_in / q_out [num_rows, num_q_heads, 256] and k_in / k_out [num_rows,
+ * num_kv_heads, 256], all of one dtype.  The heads of a row are contiguous; rows
+ * lie *_stride elements apart (so q and k may be slices of one projection's
+ * output).  An output may be its input (same pointer and stride); it may not
+ * overlap an input in any other way.  num_q_heads or num_kv_heads may be 0 (its
+ * pointers are then unused).  d_positions int32 [num_rows, num_axes], any values.
+ * Q3KV_ERR_INVALID_ARG for pointers that are not 16-byte aligned or strides that
+ * are below heads * 256 or not multiples of 16 bytes. */
+Q3KV_API int q3kv_rope(void* stream, const q3kv_rope_plan* plan, const int32_t* d_positions, int32_t num_rows,
+              const void* q_in, int64_t q_in_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+              const void* k_in, int64_t k_in_stride, void* k_out, int64_t k_out_stride, int32_t num_kv_heads,
+              int32_t dtype);
+
+/* ---- verify and prefill attention with the softmax statistic ---------------------
+ * As q3kv_verify_attn, q3kv_prefill_attn, q3kv_fp8_verify_attn and
+ * q3kv_t5k_verify_attn, and the same bits in out, plus
+ *   lse   device float32 [rows, num_q_heads]: log of the sum over the visible
+ *         positions of e^(q . k_hat / 16) (natural log), the statistic that
+ *         q3kv_attn_mass needs; rows of skipped slots are left as they were. */
+Q3KV_API int q3kv_verify_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer,
+                     const void* q, int32_t dtype, float* out, float* lse,
+                     int32_t impl, int32_t split_positions,
+                     void* d_workspace, size_t workspace_bytes, int32_t* d_status);
+Q3KV_API int q3kv_prefill_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_new, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_new, int32_t layer,
+                     const void* q, int32_t dtype, float* out, float* lse,
+                     int32_t impl, int32_t split_positions,
+                     void* d_workspace, size_t workspace_bytes, int32_t* d_status);
+Q3KV_API int q3kv_fp8_verify_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer,
+                     const void* q, int32_t dtype, float* out, float* lse,
+                     int32_t impl, int32_t split_positions,
+                     void* d_workspace, size_t workspace_bytes, int32_t* d_status);
+Q3KV_API int q3kv_t5k_verify_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer,
+                     const void* q, int32_t dtype, float* out, float* lse,
+                     int32_t impl, int32_t split_positions,
+                     void* d_workspace, size_t workspace_bytes, int32_t* d_status);
+
+/* ---- attention mass ------------------------------------------------------------
+ * The attention weight each cached position received, summed over the query
+ * heads of its kv head and accumulated over steps: what an eviction goes by.
+ * The pages have no counterpart (their slots never evict).  For slot b with
+ * L = d_ctx_len[b] and T = d_n_q[b] query tokens (the slot's last T positions),
+ * every kv head g and every position j in [0, L):
+ *   mass[b, g, j] = decay * old + sum over tokens t with j <= L - T + t and the 8
+ *                   query heads h of g of e^(q_th . k_hat_j / 16 - lse[t, h])
+ * where old = mass[b, g, j] for j < L - T and 0 for the step's own positions
+ * (they have no history; what a rolled-back draft left there is dropped).  After
+ * an acceptance, call it with the committed lengths and n_accepted + 1 tokens:
+ * lse and the query rows of the kept tokens are unchanged by the rollback.
+ *   q, dtype, d_q_offsets   as in q3kv_verify_attn (the same unrotated queries)
+ *   lse      float32 [rows, num_q_heads], as q3kv_verify_attn_lse stores it; a
+ *            row whose lse is not finite contributes nothing and sets
+ *            Q3KV_STATUS_NONFINITE_INPUT
+ *   decay    in [0, 1]; with 0 the old values are not read (they may be anything)
+ *   d_mass   float32 [num_slots, num_kv_heads, mass_stride], updated in place;
+ *            entries at or past L and slots with T == 0 are left as they were;
+ *            mass_stride >= max_ctx_len.  It must not overlap the other buffers.
+ * max_n_q <= 16.  T > max_n_q, T > L, L > max_ctx_len or L beyond the slot's page
+ * table set Q3KV_STATUS_BAD_LENGTH and leave the slot's mass as it was.  Positions
+ * of a page whose id is out of range keep decay * old and set
+ * Q3KV_STATUS_BAD_PAGE.  Sums run in a fixed order: equal inputs give equal bits.
+ * The cache's scales must be finite and non-negative, as an append without
+ * Q3KV_STATUS_SCALE_OVERFLOW leaves them. */
+Q3KV_API int q3kv_attn_mass(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer,
+                     const void* q, int32_t dtype, const float* lse, float decay,
+                     float* d_mass, int64_t mass_stride, int32_t* d_status);
+Q3KV_API int q3kv_fp8_attn_mass(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer,
+                     const void* q, int32_t dtype, const float* lse, float decay,
+                     float* d_mass, int64_t mass_stride, int32_t* d_status);
+Q3KV_API int q3kv_t5k_attn_mass(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer,
+                     const void* q, int32_t dtype, const float* lse, float decay,
+                     float* d_mass, int64_t mass_stride, int32_t* d_status);
+
+/* ---- eviction by attention mass --------------------------------------------------
+ * Brings each slot down to a budget of positions: per (layer, slot, kv head) the
+ * last n_recent positions, the first n_sink, and the positions between them with
+ * the largest mass (the lowest position on equal masses) are kept, and their
+ * records are compacted, in ascending order of position, into the pages of
+ * another page table.  The attention calls go by order only, so a slot continues
+ * with the destination row of pages and the new length (keys carry their rotary
+ * positions); the source pages can then be freed.
+ * With L = d_ctx_len[b] and n = min(L, d_budget[b]): if n_recent + n_sink > n, the
+ * recent positions are kept first, then the sinks.
+ *   layers    [layer, layer + num_call_layers): every layer of a slot must be
+ *             evicted before its old pages are freed
+ *   d_mass    float32 [num_call_layers, num_slots, num_kv_heads, mass_stride],
+ *             mass_stride >= max_ctx_len; a NaN counts as less than everything
+ *             and sets Q3KV_STATUS_NONFINITE_INPUT
+ *   d_budget  int32 [num_slots]; 0 or less leaves the slot out: only
+ *             d_new_len[b] = d_ctx_len[b] is written
+ *   d_dst_page_table  int32 [num_slots, dst_max_pages_per_slot]: ceil(n / 256)
+ *             pages per slot, each used once in this call and part of no slot's
+ *             source pages
+ *   d_kept    int32 [num_call_layers, num_slots, num_kv_heads, max_budget]: the kept
+ *             positions, ascending (entries past n are left as they were)
+ *   d_mass_out  float32, same layout, the kept positions' masses; may be NULL; must
+ *             not overlap d_mass
+ *   d_new_len int32 [num_slots]: n; may be the array d_ctx_len
+ * d_budget[b] > max_budget, L < 0, L > max_ctx_len, L beyond the slot's page table
+ * or n beyond its destination pages set Q3KV_STATUS_BAD_LENGTH and leave the slot
+ * out.  A record whose source or destination page id is out of range is skipped
+ * with Q3KV_STATUS_BAD_PAGE.  No workspace. */
+Q3KV_API int q3kv_evict(void* stream, const q3kv_cache_desc* desc, void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, int32_t num_slots, int64_t max_ctx_len,
+                     const int32_t* d_budget, int32_t max_budget, int32_t n_sink, int32_t n_recent,
+                     int32_t layer, int32_t num_call_layers, const float* d_mass, int64_t mass_stride,
+                     const int32_t* d_dst_page_table, int32_t dst_max_pages_per_slot,
+                     int32_t* d_kept, float* d_mass_out, int32_t* d_new_len, int32_t* d_status);
+Q3KV_API int q3kv_fp8_evict(void* stream, const q3kv_cache_desc* desc, void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, int32_t num_slots, int64_t max_ctx_len,
+                     const int32_t* d_budget, int32_t max_budget, int32_t n_sink, int32_t n_recent,
+                     int32_t layer, int32_t num_call_layers, const float* d_mass, int64_t mass_stride,
+                     const int32_t* d_dst_page_table, int32_t dst_max_pages_per_slot,
+                     int32_t* d_kept, float* d_mass_out, int32_t* d_new_len, int32_t* d_status);
+Q3KV_API int q3kv_t5k_evict(void* stream, const q3kv_cache_desc* desc, void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, int32_t num_slots, int64_t max_ctx_len,
+                     const int32_t* d_budget, int32_t max_budget, int32_t n_sink, int32_t n_recent,
+                     int32_t layer, int32_t num_call_layers, const float* d_mass, int64_t mass_stride,
+                     const int32_t* d_dst_page_table, int32_t dst_max_pages_per_slot,
+                     int32_t* d_kept, float* d_mass_out, int32_t* d_new_len, int32_t* d_status);
+
+/* ---- acceptance of sampled drafts --------------------------------------------------
+ * Source: the same "Model tool protocol" bullet as q3kv_accept_sample, for a
+ * drafter that samples: draft d_{j+1} was drawn from the distribution
+ * q_j = draft_probs row j, and the step's output has to follow the target
+ * p_j = softmax(logits row j / temperature).
+ *   draft d_{j+1} is accepted iff u_j q_j(d_{j+1}) < p_j(d_{j+1}),  u_j = d_uniforms[row j]
+ *   (for u_j uniform in [0, 1): with probability min(1, p / q));
+ *   at the first rejected row a, next = argmax over x with r(x) > 0 of
+ *     r(x) / E(row, x),  r = max(p_a - q_a, 0),  E = -log U
+ *   (a sample of the normalised r: the smallest of exponential clocks E / r rings
+ *   first); if r is 0 everywhere, and for the bonus token of a slot whose drafts
+ *   were all accepted, the same argmax with p in place of r;
+ *   U(row, x) as in q3kv_accept_sample (equal keys: the lowest index).
+ * Same arguments, outputs and errors as q3kv_accept_sample, plus:
+ *   draft_probs   device [num_rows, vocab] of draft_dtype (f32 or bf16), the same row
+ *                 indexing as logits (a slot's last row is unused); values >= 0, taken
+ *                 as they are (not renormalised)
+ *   d_accept_prob float [num_rows] or NULL: min(1, p_j(d_{j+1}) / q_j(d_{j+1})) in the
+ *                 row of every tested draft (1 or 0 for q = 0: whether p > 0), other
+ *                 rows left as they were -- what a draft-depth controller goes by
+ *   workspace     at least q3kv_accept_draft_workspace_bytes(...) bytes, 16-byte
+ *                 aligned, no initial contents needed; calls sharing it must not
+ *                 overlap on the GPU
+ * A draft token outside [0, vocab) is rejected with acceptance probability 0.  A
+ * logit of -inf is a token of probability 0; a NaN or +inf logit sets
+ * Q3KV_STATUS_NONFINITE_INPUT, and so does a NaN, infinite or negative draft
+ * probability where one is read (the slot's results are then unspecified but in
+ * range).  A row whose logits are all -inf has p = 0 everywhere: its draft is
+ * rejected, and next is then -1. */
+Q3KV_API int q3kv_accept_draft_workspace_bytes(int32_t num_slots, int32_t num_rows, int32_t vocab, size_t* bytes);
+Q3KV_API int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, int32_t vocab,
+                       const void* draft_probs, int32_t draft_dtype,
+                       const int32_t* d_q_offsets, const int32_t* d_n_q, const int32_t* d_tokens,
+                       int32_t num_slots, int32_t num_rows, int32_t max_n_q, const int32_t* d_ctx_len,
+                       float temperature, const float* d_uniforms, uint64_t seed,
+                       int32_t* d_n_accepted, int32_t* d_next_token, int32_t* d_committed_len,
+                       float* d_accept_prob, void* d_workspace, size_t workspace_bytes, int32_t* d_status);
+
 #ifdef __cplusplus
 }
 #endif

@@ -217,3 +217,71 @@ def sample_accept_nucleus(logits: np.ndarray, q_offsets, n_q, tokens, ctx_len, t
         nxt[b] = int(np.argmax(keys))
         committed[b] = int(ctx_len[b]) - (T - 1 - a)
     return n_acc, nxt, committed
+
+
+# ----------------------------------------------------------------------------- sampled drafts
+# The same rejection rule for a drafter that samples (draft d_{j+1} drawn from
+# q_j): accepted iff u_j q_j(d) < p_j(d); the residual of the first rejected row
+# is max(p_a - q_a, 0), drawn by racing exponential clocks (the largest
+# r(x) / E(x), E = -log U of the same noise stream); p_a where the residual is 0
+# everywhere and for the bonus token.
+
+
+def target_probs(logits_row: np.ndarray, tau: float) -> np.ndarray:
+    """softmax(logits_row / tau) in float64; zeros for a row of -inf only."""
+    l = np.asarray(logits_row, np.float64)
+    m = l.max()
+    if m == -np.inf:
+        return np.zeros_like(l)
+    e = np.exp((l - m) / tau)
+    return e / e.sum()
+
+
+def draft_race(p: np.ndarray, q, seed: int, row: int):
+    """(winner or -1, runner-up's key / winner's key) of the residual race (q None: the bonus race)."""
+    r = p if q is None else np.maximum(p - np.asarray(q, np.float64), 0.0)
+    if not np.any(r > 0):
+        r = p
+    if not np.any(r > 0):
+        return -1, 0.0
+    key = r / -np.log(noise_uniform(seed, row, np.arange(r.shape[0])))
+    x = int(np.argmax(key))
+    rest = np.delete(key, x)
+    return x, float(rest.max() / key[x]) if rest.size else 0.0
+
+
+def draft_accept(logits: np.ndarray, draft: np.ndarray, q_offsets, n_q, tokens, ctx_len, tau: float, uniforms, seed: int):
+    """Acceptance of sampled drafts for every slot.
+
+    Returns (n_accepted, next_token, committed_len, accept_prob, margin): accept_prob [rows] with NaN where no draft
+    is tested, and margin[b], how far the slot's decisions are from a tie (the smallest relative gap of a tested
+    u q against p, and of the race's two best keys).
+    """
+    S, V = len(n_q), logits.shape[1]
+    n_acc = np.zeros(S, np.int32)
+    nxt = np.full(S, -1, np.int32)
+    committed = np.array(ctx_len, np.int64).astype(np.int32)
+    prob = np.full(logits.shape[0], np.nan)
+    margin = np.full(S, np.inf)
+    for b in range(S):
+        T = int(n_q[b])
+        if T <= 0:
+            continue
+        r0 = int(q_offsets[b])
+        a = None
+        for j in range(T - 1):
+            p = target_probs(logits[r0 + j], tau)
+            d = int(tokens[r0 + j + 1])
+            pd, qd = (float(p[d]), float(draft[r0 + j, d])) if 0 <= d < V else (0.0, 0.0)
+            prob[r0 + j] = min(1.0, pd / qd) if qd > 0 else float(pd > 0)
+            uq = float(uniforms[r0 + j]) * qd
+            if a is None:
+                margin[b] = min(margin[b], abs(uq - pd) / max(uq, pd, 1e-300) if max(uq, pd) > 0 else np.inf)
+                if not uq < pd:
+                    a = j
+        bonus = a is None
+        a = T - 1 if bonus else a
+        x, second = draft_race(target_probs(logits[r0 + a], tau), None if bonus else draft[r0 + a], seed, r0 + a)
+        margin[b] = min(margin[b], 1.0 - second)
+        n_acc[b], nxt[b], committed[b] = a, x, int(ctx_len[b]) - (T - 1 - a)
+    return n_acc, nxt, committed, prob, margin

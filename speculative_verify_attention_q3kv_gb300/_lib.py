@@ -47,6 +47,33 @@ class CacheDesc(ctypes.Structure):
 
 P_desc = ctypes.POINTER(CacheDesc)
 
+Q3KV_ROPE_ADJACENT = 1
+Q3KV_ROPE_DEAL_AXES = 2
+Q3KV_ROPE_AXIS_FREQS = 4
+Q3KV_ROPE_MAX_AXES = 4
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_double), ("rotary_dim", c_int32), ("num_axes", c_int32),
+                ("sections", c_int32 * Q3KV_ROPE_MAX_AXES), ("flags", c_int32), ("reserved", c_int32)]
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_uint64 * 128), ("axis", ctypes.c_uint8 * 128), ("rotary_dim", c_int32),
+                ("num_axes", c_int32), ("flags", c_int32), ("reserved", c_int32)]
+
+
+P_rope_config = ctypes.POINTER(RopeConfig)
+P_rope_plan = ctypes.POINTER(RopePlan)
+
+# argument lists that several formats share
+_VERIFY_LSE = [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int32,
+               c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_size_t, c_void_p]
+_MASS = [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int32, c_int32,
+         c_void_p, c_int32, c_void_p, ctypes.c_float, c_void_p, c_int64, c_void_p]
+_EVICT = [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int32, c_int32,
+          c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
+
 # name -> (restype, argtypes); mirrors include/q3kv.h
 PROTOTYPES = {
     "q3kv_version": (c_int32, []),
@@ -98,6 +125,24 @@ PROTOTYPES = {
                                              c_int32, c_int32, c_int32, c_void_p, ctypes.c_float, ctypes.c_float,
                                              c_void_p, ctypes.c_uint64, c_void_p, c_void_p, c_void_p, c_void_p,
                                              ctypes.c_size_t, c_void_p]),
+    "q3kv_rope_plan_init": (c_int32, [P_rope_config, P_rope_plan]),
+    "q3kv_rope": (c_int32, [c_void_p, P_rope_plan, c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_int32,
+                            c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32]),
+    "q3kv_verify_attn_lse": (c_int32, _VERIFY_LSE),
+    "q3kv_prefill_attn_lse": (c_int32, _VERIFY_LSE),
+    "q3kv_fp8_verify_attn_lse": (c_int32, _VERIFY_LSE),
+    "q3kv_t5k_verify_attn_lse": (c_int32, _VERIFY_LSE),
+    "q3kv_attn_mass": (c_int32, _MASS),
+    "q3kv_fp8_attn_mass": (c_int32, _MASS),
+    "q3kv_t5k_attn_mass": (c_int32, _MASS),
+    "q3kv_evict": (c_int32, _EVICT),
+    "q3kv_fp8_evict": (c_int32, _EVICT),
+    "q3kv_t5k_evict": (c_int32, _EVICT),
+    "q3kv_accept_draft_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, ctypes.POINTER(c_size_t)]),
+    "q3kv_accept_draft": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
+                                    c_void_p, c_int32, c_int32, c_int32, c_void_p, ctypes.c_float, c_void_p,
+                                    ctypes.c_uint64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                    c_void_p]),
 }
 
 Q3KV_NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -13,7 +13,7 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import CacheDesc, Q3KVError, check  # noqa: F401  (re-exported)
+from ._lib import CacheDesc, Q3KVError, RopePlan, check  # noqa: F401  (re-exported)
 
 HEAD_DIM = 256
 PAGE_SIZE = 256
@@ -401,3 +401,248 @@ def accept_sample_nucleus(logits: torch.Tensor, q_offsets: torch.Tensor, n_q: to
                                                 _ptr(next_token), _ptr(committed_len), _ptr(workspace), nbytes,
                                                 _ptr(status))
     check(rc, "q3kv_accept_sample_nucleus")
+
+
+def verify_attn_lse(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                    n_q: torch.Tensor, q_offsets: torch.Tensor, max_ctx_len: int, max_n_q: int, layer: int,
+                    q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                    impl: int = _lib.Q3KV_IMPL_AUTO, split_positions: int = 0,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_verify_attn_lse: verify_attn that also stores lse[rows, q_heads] (float32) for attn_mass."""
+    _verify_lse("q3kv_verify_attn_lse", pool_bytes, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len, max_n_q,
+                layer, q, out, lse, workspace, impl, split_positions, status, stream)
+
+
+def prefill_attn_lse(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                     n_new: torch.Tensor, q_offsets: torch.Tensor, max_ctx_len: int, max_n_new: int, layer: int,
+                     q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                     impl: int = _lib.Q3KV_IMPL_AUTO, split_positions: int = 0,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_prefill_attn_lse: prefill_attn that also stores lse[rows, q_heads] (float32)."""
+    _verify_lse("q3kv_prefill_attn_lse", pool_bytes, desc, pool, page_table, ctx_len, n_new, q_offsets, max_ctx_len,
+                max_n_new, layer, q, out, lse, workspace, impl, split_positions, status, stream)
+
+
+def fp8_verify_attn_lse(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                        n_q: torch.Tensor, q_offsets: torch.Tensor, max_ctx_len: int, max_n_q: int, layer: int,
+                        q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                        impl: int = _lib.Q3KV_IMPL_AUTO, split_positions: int = 0,
+                        status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_fp8_verify_attn_lse: fp8_verify_attn that also stores lse[rows, q_heads] (float32)."""
+    _verify_lse("q3kv_fp8_verify_attn_lse", fp8_pool_bytes, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len,
+                max_n_q, layer, q, out, lse, workspace, impl, split_positions, status, stream)
+
+
+def t5k_verify_attn_lse(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                        n_q: torch.Tensor, q_offsets: torch.Tensor, max_ctx_len: int, max_n_q: int, layer: int,
+                        q: torch.Tensor, out: torch.Tensor, lse: torch.Tensor, workspace: torch.Tensor,
+                        impl: int = _lib.Q3KV_IMPL_AUTO, split_positions: int = 0,
+                        status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_t5k_verify_attn_lse: t5k_verify_attn (AUTO: the tensor-core leg) that also stores lse[rows, q_heads]."""
+    _verify_lse("q3kv_t5k_verify_attn_lse", t5k_pool_bytes, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len,
+                max_n_q, layer, q, out, lse, workspace, impl, split_positions, status, stream)
+
+
+def _check_lse(lse: torch.Tensor, q: torch.Tensor, heads: int, dev: int) -> None:
+    _on_gpu("lse", lse, dev, torch.float32)
+    if lse.dim() != 2 or lse.shape[1] != heads or lse.shape[0] < q.shape[0]:
+        raise ValueError(f"lse must be [rows >= {q.shape[0]}, {heads}], got {tuple(lse.shape)}")
+
+
+def _verify_lse(name, pool_bytes_fn, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len, max_n_q, layer, q, out,
+                lse, workspace, impl, split_positions, status, stream) -> None:
+    _check_verify(desc, pool, pool_bytes_fn, page_table, ctx_len, n_q, q_offsets, q, out, workspace, status)
+    _check_lse(lse, q, desc.num_q_heads, _current_device())
+    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), _ptr(pool), _ptr(page_table),
+                                    page_table.shape[1], _ptr(ctx_len), _ptr(n_q), _ptr(q_offsets), ctx_len.shape[0],
+                                    max_ctx_len, max_n_q, layer, _ptr(q), _dtype_code(q), _ptr(out), _ptr(lse), impl,
+                                    split_positions, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _ptr(status))
+    check(rc, name)
+
+
+def attn_mass(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor, n_q: torch.Tensor,
+              q_offsets: torch.Tensor, max_ctx_len: int, max_n_q: int, layer: int, q: torch.Tensor, lse: torch.Tensor,
+              decay: float, mass: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_attn_mass: mass[slots, kv_heads, >= max_ctx_len] (float32) = decay * mass + the step's attention weights."""
+    _attn_mass("q3kv_attn_mass", pool_bytes, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len, max_n_q, layer,
+               q, lse, decay, mass, status, stream)
+
+
+def fp8_attn_mass(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                  n_q: torch.Tensor, q_offsets: torch.Tensor, max_ctx_len: int, max_n_q: int, layer: int,
+                  q: torch.Tensor, lse: torch.Tensor, decay: float, mass: torch.Tensor,
+                  status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_fp8_attn_mass: attn_mass over the fp8 comparison cache."""
+    _attn_mass("q3kv_fp8_attn_mass", fp8_pool_bytes, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len,
+               max_n_q, layer, q, lse, decay, mass, status, stream)
+
+
+def t5k_attn_mass(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                  n_q: torch.Tensor, q_offsets: torch.Tensor, max_ctx_len: int, max_n_q: int, layer: int,
+                  q: torch.Tensor, lse: torch.Tensor, decay: float, mass: torch.Tensor,
+                  status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_t5k_attn_mass: attn_mass over the turbo5k-style cache."""
+    _attn_mass("q3kv_t5k_attn_mass", t5k_pool_bytes, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len,
+               max_n_q, layer, q, lse, decay, mass, status, stream)
+
+
+def _attn_mass(name, pool_bytes_fn, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len, max_n_q, layer, q, lse,
+               decay, mass, status, stream) -> None:
+    dev = _current_device()
+    n = _check_cache_args(desc, pool, pool_bytes_fn(desc), page_table, ctx_len, n_q, q_offsets, status, dev)
+    _check_rows("q", q, desc.num_q_heads, dev)
+    _check_lse(lse, q, desc.num_q_heads, dev)
+    _on_gpu("mass", mass, dev, torch.float32)
+    if mass.dim() != 3 or mass.shape[0] < n or mass.shape[1] != desc.num_kv_heads or mass.shape[2] < max_ctx_len:
+        raise ValueError(f"mass must be [slots >= {n}, {desc.num_kv_heads}, positions >= {max_ctx_len}], "
+                         f"got {tuple(mass.shape)}")
+    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), _ptr(pool), _ptr(page_table),
+                                    page_table.shape[1], _ptr(ctx_len), _ptr(n_q), _ptr(q_offsets), n, max_ctx_len,
+                                    max_n_q, layer, _ptr(q), _dtype_code(q), _ptr(lse), float(decay), _ptr(mass),
+                                    mass.shape[2], _ptr(status))
+    check(rc, name)
+
+
+def evict(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor, max_ctx_len: int,
+          budget: torch.Tensor, max_budget: int, n_sink: int, n_recent: int, layer: int, mass: torch.Tensor,
+          dst_page_table: torch.Tensor, kept: torch.Tensor, mass_out: Optional[torch.Tensor], new_len: torch.Tensor,
+          status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_evict: keep budget[b] positions of every slot by mass[layers, slots, kv_heads, >= max_ctx_len] and compact
+    their records into the pages of dst_page_table; kept and mass_out are [layers, slots, kv_heads, max_budget]."""
+    _evict("q3kv_evict", pool_bytes, desc, pool, page_table, ctx_len, max_ctx_len, budget, max_budget, n_sink, n_recent,
+           layer, mass, dst_page_table, kept, mass_out, new_len, status, stream)
+
+
+def fp8_evict(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor, max_ctx_len: int,
+              budget: torch.Tensor, max_budget: int, n_sink: int, n_recent: int, layer: int, mass: torch.Tensor,
+              dst_page_table: torch.Tensor, kept: torch.Tensor, mass_out: Optional[torch.Tensor], new_len: torch.Tensor,
+              status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_fp8_evict: evict over the fp8 comparison cache."""
+    _evict("q3kv_fp8_evict", fp8_pool_bytes, desc, pool, page_table, ctx_len, max_ctx_len, budget, max_budget, n_sink,
+           n_recent, layer, mass, dst_page_table, kept, mass_out, new_len, status, stream)
+
+
+def t5k_evict(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor, max_ctx_len: int,
+              budget: torch.Tensor, max_budget: int, n_sink: int, n_recent: int, layer: int, mass: torch.Tensor,
+              dst_page_table: torch.Tensor, kept: torch.Tensor, mass_out: Optional[torch.Tensor], new_len: torch.Tensor,
+              status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_t5k_evict: evict over the turbo5k-style cache."""
+    _evict("q3kv_t5k_evict", t5k_pool_bytes, desc, pool, page_table, ctx_len, max_ctx_len, budget, max_budget, n_sink,
+           n_recent, layer, mass, dst_page_table, kept, mass_out, new_len, status, stream)
+
+
+def _evict(name, pool_bytes_fn, desc, pool, page_table, ctx_len, max_ctx_len, budget, max_budget, n_sink, n_recent, layer,
+           mass, dst_page_table, kept, mass_out, new_len, status, stream) -> None:
+    dev = _current_device()
+    n = _check_cache_args(desc, pool, pool_bytes_fn(desc), page_table, ctx_len, ctx_len, ctx_len, status, dev)
+    _on_gpu("budget", budget, dev, torch.int32, n)
+    _on_gpu("new_len", new_len, dev, torch.int32, n)
+    _on_gpu("dst_page_table", dst_page_table, dev, torch.int32)
+    if dst_page_table.dim() != 2 or dst_page_table.shape[1] < 1 or dst_page_table.shape[0] < n:
+        raise ValueError(f"dst_page_table must be int32 [num_slots >= {n}, max_pages_per_slot >= 1], "
+                         f"got {tuple(dst_page_table.shape)}")
+    _on_gpu("mass", mass, dev, torch.float32)
+    heads = desc.num_kv_heads
+    if mass.dim() != 4 or mass.shape[1] != n or mass.shape[2] != heads or mass.shape[3] < max_ctx_len:
+        raise ValueError(f"mass must be [layers, {n}, {heads}, positions >= {max_ctx_len}], got {tuple(mass.shape)}")
+    want = (mass.shape[0], n, heads, max_budget)
+    _on_gpu("kept", kept, dev, torch.int32)
+    _on_gpu("mass_out", mass_out, dev, torch.float32, optional=True)
+    for what, t in (("kept", kept), ("mass_out", mass_out)):
+        if t is not None and tuple(t.shape) != want:
+            raise ValueError(f"{what} must be {want}, got {tuple(t.shape)}")
+    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), _ptr(pool), _ptr(page_table),
+                                    page_table.shape[1], _ptr(ctx_len), n, max_ctx_len, _ptr(budget), max_budget, n_sink,
+                                    n_recent, layer, mass.shape[0], _ptr(mass), mass.shape[3], _ptr(dst_page_table),
+                                    dst_page_table.shape[1], _ptr(kept), _ptr(mass_out), _ptr(new_len), _ptr(status))
+    check(rc, name)
+
+
+def make_rope_plan(rotary_dim: int, theta: float, sections, deal_axes: bool = False, axis_freqs: bool = False,
+                   adjacent: bool = False) -> RopePlan:
+    """q3kv_rope_plan_init: sections[a] pairs turn with axis a's position (their sum is rotary_dim / 2)."""
+    if len(sections) > _lib.Q3KV_ROPE_MAX_AXES:
+        raise ValueError(f"at most {_lib.Q3KV_ROPE_MAX_AXES} axes, got {len(sections)}")
+    flags = ((_lib.Q3KV_ROPE_ADJACENT if adjacent else 0) | (_lib.Q3KV_ROPE_DEAL_AXES if deal_axes else 0)
+             | (_lib.Q3KV_ROPE_AXIS_FREQS if axis_freqs else 0))
+    config = _lib.RopeConfig(theta, rotary_dim, len(sections), (ctypes.c_int32 * 4)(*sections), flags, 0)
+    plan = RopePlan()
+    check(_lib.load().q3kv_rope_plan_init(ctypes.byref(config), ctypes.byref(plan)), "q3kv_rope_plan_init")
+    return plan
+
+
+def _strided_rows(name: str, t: torch.Tensor, rows: int, dev: int):
+    """Pointer, row stride and heads of [rows, heads, 256] rows whose heads are contiguous; rows may be strided."""
+    _on_gpu(name, t, dev)
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(t.shape)}")
+    heads = t.shape[1]
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    stride = t.stride(0) if rows > 1 else heads * HEAD_DIM
+    return t.data_ptr(), stride, heads
+
+
+def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.Tensor, k: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_rope: rotate q and k [rows, heads, 256] by positions int32 [rows, axes] into q_out and k_out.
+
+    Rows may be strided (slices of one projection); an output may be its input.
+    """
+    dev = _current_device()
+    if positions.dim() != 2 or positions.shape[1] != plan.num_axes:
+        raise ValueError(f"positions must be [rows, {plan.num_axes}], got {tuple(positions.shape)}")
+    rows = positions.shape[0]
+    _on_gpu("positions", positions, dev, torch.int32)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out come together")
+    args = []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            args += [None, 0, None, 0, 0]
+            continue
+        src, src_stride, heads = _strided_rows(name, x, rows, dev)
+        dst, dst_stride, out_heads = _strided_rows(name + "_out", y, rows, dev)
+        if heads != out_heads or x.dtype != q.dtype or y.dtype != q.dtype:
+            raise ValueError(f"{name} and {name}_out must have the heads of one another and the dtype of q")
+        if rows and heads:
+            # extents in bytes; an exact in-place call is fine, any other overlap is not
+            size = x.element_size()
+            src_end = src + ((rows - 1) * src_stride + heads * HEAD_DIM) * size
+            dst_end = dst + ((rows - 1) * dst_stride + heads * HEAD_DIM) * size
+            if src < dst_end and dst < src_end and not (src == dst and src_stride == dst_stride):
+                raise ValueError(f"{name}_out overlaps {name} without being the same rows")
+        args += [src, src_stride, dst, dst_stride, heads]
+    rc = _lib.load().q3kv_rope(_stream(stream), ctypes.byref(plan), _ptr(positions), rows, *args, _dtype_code(q))
+    check(rc, "q3kv_rope")
+
+
+def accept_draft_workspace_bytes(num_slots: int, num_rows: int, vocab: int) -> int:
+    n = ctypes.c_size_t()
+    check(_lib.load().q3kv_accept_draft_workspace_bytes(num_slots, num_rows, vocab, ctypes.byref(n)),
+          "q3kv_accept_draft_workspace_bytes")
+    return n.value
+
+
+def accept_draft(logits: torch.Tensor, draft_probs: torch.Tensor, q_offsets: torch.Tensor, n_q: torch.Tensor,
+                 tokens: torch.Tensor, max_n_q: int, ctx_len: torch.Tensor, temperature: float, uniforms: torch.Tensor,
+                 seed: int, n_accepted: torch.Tensor, next_token: torch.Tensor, committed_len: torch.Tensor,
+                 workspace: Optional[torch.Tensor], accept_prob: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_accept_draft: rejection-sampled acceptance of drafts drawn from draft_probs [rows, vocab] (f32 or bf16)."""
+    rows, vocab = _check_accept(logits, q_offsets, n_q, tokens, ctx_len, n_accepted, next_token, committed_len,
+                                workspace, status)
+    dev = _current_device()
+    _on_gpu("draft_probs", draft_probs, dev)
+    if draft_probs.shape != logits.shape:
+        raise ValueError(f"draft_probs must be {tuple(logits.shape)}, got {tuple(draft_probs.shape)}")
+    _on_gpu("uniforms", uniforms, dev, torch.float32, rows)
+    _on_gpu("accept_prob", accept_prob, dev, torch.float32, rows, optional=True)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _lib.load().q3kv_accept_draft(_stream(stream), _ptr(logits), _dtype_code(logits), vocab, _ptr(draft_probs),
+                                       _dtype_code(draft_probs), _ptr(q_offsets), _ptr(n_q), _ptr(tokens), n_q.shape[0],
+                                       rows, max_n_q, _ptr(ctx_len), float(temperature), _ptr(uniforms),
+                                       int(seed) & ((1 << 64) - 1), _ptr(n_accepted), _ptr(next_token),
+                                       _ptr(committed_len), _ptr(accept_prob), _ptr(workspace), nbytes, _ptr(status))
+    check(rc, "q3kv_accept_draft")

@@ -20,6 +20,7 @@
 #include <math_constants.h>
 
 #include "q3kv_internal.h"
+#include "q3kv_sampling.cuh"
 
 namespace q3kv {
 namespace {
@@ -31,11 +32,6 @@ struct Best {
     int i;
 };
 
-// a beats b: larger value, or the same value at a lower index
-__device__ __forceinline__ bool beats(float av, int ai, float bv, int bi) {
-    return av > bv || (av == bv && ai < bi);
-}
-
 __device__ __forceinline__ Best warp_best(Best b) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -45,9 +41,6 @@ __device__ __forceinline__ Best warp_best(Best b) {
     }
     return b;
 }
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T>
 __global__ void __launch_bounds__(kArgThreads) argmax_kernel(AcceptArgs a) {
@@ -172,15 +165,6 @@ __global__ void __launch_bounds__(32) accept_kernel(AcceptArgs a) {
 // over all x of the last row's keys.  G = -log(-log U), U from the counter-based
 // SplitMix64 stream: U = ((z >> 41) + 0.5) / 2^23 with z output number
 // row * 2^32 + x of the stream seeded with `seed`.
-
-__device__ __forceinline__ float noise_uniform(uint64_t seed, uint32_t row, uint32_t x) {
-    const uint64_t k = ((uint64_t)row << 32) + x;
-    uint64_t z = seed + (k + 1ull) * 0x9E3779B97F4A7C15ull;
-    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
-    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
-    z ^= z >> 31;
-    return ((float)(uint32_t)(z >> 41) + 0.5f) * (1.0f / 8388608.0f);
-}
 
 // f(k, logit) for every vocabulary entry k of [c0, c1) of one row, with four
 // loads of each thread in flight at once: 16-byte loads when the rows are

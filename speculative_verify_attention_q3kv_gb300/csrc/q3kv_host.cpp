@@ -19,6 +19,10 @@ namespace {
 constexpr int kVersion = 1;
 thread_local cudaError_t g_last_cuda = cudaSuccess;   // last CUDA failure seen by this host thread
 
+}  // namespace
+
+namespace q3kv {
+
 int cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return Q3KV_OK;
     g_last_cuda = e;
@@ -35,14 +39,16 @@ int check_desc(const q3kv_cache_desc* d) {
     return Q3KV_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int device_sm_count(int* sms) {
     int dev = 0;
     int e = cuda_status(cudaGetDevice(&dev));
     if (e != Q3KV_OK) return e;
     return cuda_status(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
 }
+
+}  // namespace q3kv
+
+namespace {
 
 struct Plan {
     int impl;
@@ -262,7 +268,7 @@ int verify_impl(int fmt, void* stream, const q3kv_cache_desc* desc, const void* 
                 const int32_t* d_q_offsets, int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q,
                 int32_t layer, const void* q, int32_t dtype, float* out, int32_t impl,
                 int32_t split_positions, void* d_workspace, size_t workspace_bytes, int32_t* d_status,
-                int32_t max_tokens = kMaxNq) {
+                int32_t max_tokens = kMaxNq, float* lse = nullptr) {
     int e = check_desc(desc);
     if (e != Q3KV_OK) return e;
     if (num_slots < 0 || max_pages_per_slot <= 0 || layer < 0 || layer >= desc->num_layers)
@@ -301,6 +307,7 @@ int verify_impl(int fmt, void* stream, const q3kv_cache_desc* desc, const void* 
     a.q = q;
     a.dtype = dtype;
     a.out = out;
+    a.lse = lse;
     a.max_n_q = max_n_q;
     a.split_pages = p.split_pages;
     a.num_splits = p.num_splits;
@@ -427,6 +434,51 @@ int q3kv_prefill_attn(void* stream, const q3kv_cache_desc* desc, const void* d_p
     return verify_impl(kFmtQ3, stream, desc, d_pool, d_page_table, max_pages_per_slot, d_ctx_len, d_n_new,
                        d_q_offsets, num_slots, max_ctx_len, max_n_new, layer, q, dtype, out, impl, split_positions,
                        d_workspace, workspace_bytes, d_status, kMaxPrefillNq);
+}
+
+
+int q3kv_verify_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool, const int32_t* d_page_table,
+           int32_t max_pages_per_slot, const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+           int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer, const void* q, int32_t dtype,
+           float* out, float* lse, int32_t impl, int32_t split_positions, void* d_workspace, size_t workspace_bytes,
+           int32_t* d_status) {
+    if (num_slots > 0 && max_n_q > 0 && max_ctx_len > 0 && !lse) return Q3KV_ERR_INVALID_ARG;
+    return verify_impl(kFmtQ3, stream, desc, d_pool, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q,
+                       d_q_offsets, num_slots, max_ctx_len, max_n_q, layer, q, dtype, out, impl, split_positions,
+                       d_workspace, workspace_bytes, d_status, kMaxNq, lse);
+}
+
+int q3kv_prefill_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool, const int32_t* d_page_table,
+           int32_t max_pages_per_slot, const int32_t* d_ctx_len, const int32_t* d_n_new, const int32_t* d_q_offsets,
+           int32_t num_slots, int64_t max_ctx_len, int32_t max_n_new, int32_t layer, const void* q, int32_t dtype,
+           float* out, float* lse, int32_t impl, int32_t split_positions, void* d_workspace, size_t workspace_bytes,
+           int32_t* d_status) {
+    if (num_slots > 0 && max_n_new > 0 && max_ctx_len > 0 && !lse) return Q3KV_ERR_INVALID_ARG;
+    return verify_impl(kFmtQ3, stream, desc, d_pool, d_page_table, max_pages_per_slot, d_ctx_len, d_n_new,
+                       d_q_offsets, num_slots, max_ctx_len, max_n_new, layer, q, dtype, out, impl, split_positions,
+                       d_workspace, workspace_bytes, d_status, kMaxPrefillNq, lse);
+}
+
+int q3kv_fp8_verify_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool, const int32_t* d_page_table,
+           int32_t max_pages_per_slot, const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+           int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer, const void* q, int32_t dtype,
+           float* out, float* lse, int32_t impl, int32_t split_positions, void* d_workspace, size_t workspace_bytes,
+           int32_t* d_status) {
+    if (num_slots > 0 && max_n_q > 0 && max_ctx_len > 0 && !lse) return Q3KV_ERR_INVALID_ARG;
+    return verify_impl(kFmtFp8, stream, desc, d_pool, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q,
+                       d_q_offsets, num_slots, max_ctx_len, max_n_q, layer, q, dtype, out, impl, split_positions,
+                       d_workspace, workspace_bytes, d_status, kMaxNq, lse);
+}
+
+int q3kv_t5k_verify_attn_lse(void* stream, const q3kv_cache_desc* desc, const void* d_pool, const int32_t* d_page_table,
+           int32_t max_pages_per_slot, const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+           int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer, const void* q, int32_t dtype,
+           float* out, float* lse, int32_t impl, int32_t split_positions, void* d_workspace, size_t workspace_bytes,
+           int32_t* d_status) {
+    if (num_slots > 0 && max_n_q > 0 && max_ctx_len > 0 && !lse) return Q3KV_ERR_INVALID_ARG;
+    return verify_impl(kFmtT5k, stream, desc, d_pool, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q,
+                       d_q_offsets, num_slots, max_ctx_len, max_n_q, layer, q, dtype, out, impl, split_positions,
+                       d_workspace, workspace_bytes, d_status, kMaxNq, lse);
 }
 
 }  // extern "C"

@@ -71,6 +71,7 @@ struct VerifyArgs {
     const void* q;
     int32_t dtype;
     float* out;
+    float* lse;                // [rows, q heads] softmax statistic, or null
     int32_t max_n_q;
     int32_t split_pages;       // pages per split-K unit (a fixed size; unused when split_auto)
     int32_t num_splits;        // split slots per unit in the grid and the workspace (an upper bound)
@@ -82,6 +83,32 @@ struct VerifyArgs {
     void* q_prep;              // tensor-core leg: [unit][hi|lo][64 x 256] fp16 (rotated) queries
     int32_t fmt;               // kFmtQ3, kFmtFp8 or kFmtT5k
     int32_t* status;
+    T5kTable t5k;              // turbo5k only
+};
+
+// Everything an attention-mass launch needs, resolved on the host.
+struct MassArgs {
+    const uint8_t* pool;
+    const int32_t* page_table;
+    int32_t max_pages_per_slot;
+    const int32_t* ctx_len;
+    const int32_t* n_q;
+    const int32_t* q_offsets;
+    int32_t num_slots;
+    int64_t max_ctx_len;
+    int32_t max_n_q;
+    int32_t num_layers;
+    int32_t num_kv_heads;
+    int32_t num_pages;
+    int32_t layer;
+    const void* q;
+    int32_t dtype;
+    const float* lse;
+    float decay;
+    float* mass;
+    int64_t mass_stride;
+    int32_t* status;
+    int32_t fmt;
     T5kTable t5k;              // turbo5k only
 };
 
@@ -138,6 +165,13 @@ struct AcceptArgs {
 constexpr size_t kNucleusRowBytes = 64;
 constexpr size_t kNucleusHistBytes = 256 * 8;
 constexpr size_t kAcceptPartialBytes = 24;   // largest per-chunk record (sampled acceptance)
+// Host checks shared by the entry points (q3kv_host.cpp): the cache shape, and
+// a CUDA result as a return code (kept for q3kv_last_cuda_error).
+int check_desc(const q3kv_cache_desc* d);
+int cuda_status(cudaError_t e);
+int device_sm_count(int* sms);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);
 cudaError_t launch_accept_sample(const AcceptArgs& a, cudaStream_t stream);
 cudaError_t launch_accept_nucleus(const AcceptArgs& a, cudaStream_t stream);

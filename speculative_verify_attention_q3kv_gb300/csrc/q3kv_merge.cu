@@ -178,6 +178,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(VerifyArgs a, int 
     if (ROT) rotate_row_regs(x);
     const int ra = row0 + r;
     const int Hq = a.num_kv_heads * kGroup;
+    // ln sum e^s over all splits, in the leg's units
+    if (a.lse && lane == 0)
+        a.lse[((int64_t)a.q_offsets[slot] + ra / kGroup) * Hq + g * kGroup + ra % kGroup] =
+            LOG2 ? 0.6931471805599453f * (M + log2f(den)) : M + logf(den);
     float* dst = a.out + (((int64_t)a.q_offsets[slot] + ra / kGroup) * Hq + g * kGroup + ra % kGroup) * kHeadDim + 8 * lane;
     constexpr float kS = ROT ? 0.0625f : 1.0f;
     reinterpret_cast<float4*>(dst)[0] = make_float4(x[0] * kS, x[1] * kS, x[2] * kS, x[3] * kS);

@@ -256,6 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_fma_kernel(VerifyArgs a) {
     const int unit = (slot * a.num_kv_heads + g) * a.row_chunks + chunk;
     float* out = a.out;
     if (n_splits == 1) {
+        if (a.lse && tid < Rc) {
+            const int ra = row0 + tid;
+            a.lse[(q_base + ra / kGroup) * Hq + g * kGroup + ra % kGroup] = sm.m_run[tid] + logf(sm.l_run[tid]);
+        }
         // normalise into shared memory, rotate back, store
 #pragma unroll
         for (int j = 0; j < 16; ++j) {

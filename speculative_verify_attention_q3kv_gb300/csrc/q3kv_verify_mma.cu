@@ -888,6 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1) verify_mma_kernel(VerifyArgs a) {
                 for (int k = 0; k < 16; ++k)
                     if (c + k < Rc) dst[(c + k) * kHeadDim + d] = v[k] * sm.alpha[c + k];
             }
+            if (n_splits == 1 && a.lse && tid < Rc) {
+                // scores are in log2 units: ln sum e^s = ln 2 (m + log2 l)
+                const int ra = row0 + tid;
+                a.lse[(q_base + ra / kGroup) * Hq + g * kGroup + ra % kGroup] =
+                    0.6931471805599453f * (sm.m_run[tid] + log2f(sm.l_run[tid]));
+            }
             if (n_splits > 1 && tid < Rc) {
                 float* pml = a.part_ml + ((int64_t)unit * a.num_splits + split) * kRows * 2;
                 pml[2 * tid] = sm.m_run[tid];

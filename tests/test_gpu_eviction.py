@@ -1,0 +1,428 @@
+"""GPU parity of the attention mass, its softmax statistic and the eviction.
+
+Tolerances.  A score is a sum of 256 products; with A = sum |q_d k_d| / 16 over the
+rotated values, every float32 evaluation of at most 512 terms is within
+512 2^-24 A = 2^-15 A of the exact one (any order), and an fp16 hi / lo split of an
+operand adds 2^-22 A.  A weight e^(s - lse) then carries that absolute error of s as
+a relative one, plus 2^-22 (1 + |s| + |lse|) for the exponent's own roundings: the
+bound of a position is the sum of its rows' bounds and 2^-23 of the result per
+addition (at most 129).  The statistic's bound is the largest score bound of the row.
+"""
+import numpy as np
+import pytest
+import torch
+
+from operator_harness import EVICT, MASS, VERIFY, VERIFY_LSE, Cache, i32, offsets, queries
+from oracle import eviction as ev
+from speculative_verify_attention_q3kv_gb300 import _lib, api
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def _reference(c, lengths, widths, q, layer, b, g):
+    """(scores, bound of each score) of one slot and kv head."""
+    r0 = sum(widths[:b])
+    n, t = lengths[b], widths[b]
+    qb = c.q_basis(q[r0:r0 + t, 8 * g:8 * g + 8].double().cpu().numpy())
+    kh = c.k_hat(b, layer, g, n)
+    s = ev.scores(qb, kh, n - t, 8)
+    size = np.abs(qb.reshape(8 * t, 256)) @ np.abs(kh).T / 16.0
+    return s, size * (2.0 ** -15 + 2.0 ** -22)
+
+
+def _lse_of(c, lengths, widths, q, layer):
+    lse = torch.full((q.shape[0], q.shape[1]), float("nan"), device="cuda")
+    for b, t in enumerate(widths):
+        r0 = sum(widths[:b])
+        for g in range(c.kv):
+            if t:
+                s, _ = _reference(c, lengths, widths, q, layer, b, g)
+                lse[r0:r0 + t, 8 * g:8 * g + 8] = torch.from_numpy(ev.log_sum_exp(s).reshape(t, 8)).float().cuda()
+    return lse
+
+
+def _mass_call(c, lengths, widths, q, lse, decay, mass, layer=0, status=None, **kw):
+    MASS[c.fmt](c.desc, c.pool, c.page_table, i32(lengths), i32(widths), offsets(widths), kw.pop("max_ctx", max(lengths)),
+                kw.pop("max_n_q", max(max(widths), 1)), layer, q, lse, decay, mass, status, **kw)
+
+
+def _check_mass(c, got, old, lengths, widths, q, lse, decay, layer=0):
+    for b, (n, t) in enumerate(zip(lengths, widths)):
+        for g in range(c.kv):
+            row = got[b, g].double().cpu().numpy()
+            was = old[b, g].double().cpu().numpy()
+            assert np.array_equal(row[n if t else 0:], was[n if t else 0:], equal_nan=True)      # not this step's: left as it was
+            if not t:
+                continue
+            s, bound = _reference(c, lengths, widths, q, layer, b, g)
+            r0 = sum(widths[:b])
+            l = lse[r0:r0 + t, 8 * g:8 * g + 8].double().cpu().numpy().reshape(-1)
+            want = ev.mass(was[:n], s, l, float(np.float32(decay)), n - t)
+            w = np.exp(s - l[:, None])
+            seen = np.isfinite(s)
+            rel = np.where(seen, bound + 2.0 ** -22 * (1 + np.abs(np.where(seen, s, 0)) + np.abs(l[:, None])), 0)
+            tol = (w * rel).sum(axis=0) + 130 * 2.0 ** -23 * np.abs(want) + 1e-37
+            err = np.abs(row[:n] - want)
+            assert np.all(err <= tol), (b, g, float((err / np.maximum(tol, 1e-300)).max()))
+
+
+MASS_CASES = [
+    # fmt, lengths, widths, kv heads, dtype, decay, layers
+    ("q3", [1], [1], 1, torch.float32, 1.0, 1),
+    ("q3", [300], [4], 2, torch.bfloat16, 1.0, 1),
+    ("q3", [256, 257, 1023], [1, 16, 7], 2, torch.float32, 0.5, 2),
+    ("q3", [5, 900, 700, 640], [5, 0, 8, 9], 3, torch.bfloat16, 0.0, 1),
+    ("q3", [4097], [2], 1, torch.bfloat16, 0.9, 1),
+    ("fp8", [700, 130], [3, 16], 2, torch.float32, 1.0, 2),
+    ("fp8", [513], [1], 4, torch.bfloat16, 0.25, 1),
+    ("t5k", [700, 130], [3, 16], 2, torch.float32, 1.0, 2),
+    ("t5k", [2000], [8], 1, torch.bfloat16, 0.0, 1),
+]
+
+
+@pytest.mark.parametrize("fmt,lengths,widths,kv,dtype,decay,layers", MASS_CASES)
+def test_mass(fmt, lengths, widths, kv, dtype, decay, layers):
+    c = Cache(fmt, lengths, kv, layers, seed=len(lengths) + lengths[0])
+    q = queries(sum(widths), 8 * kv, 4, dtype)
+    layer = layers - 1
+    lse = _lse_of(c, lengths, widths, q, layer)
+    mass = torch.rand((len(lengths), kv, max(lengths) + 9), device="cuda")
+    if decay == 0.0:
+        mass.fill_(float("nan"))                     # never read
+    else:
+        for b, (n, t) in enumerate(zip(lengths, widths)):
+            if t:
+                mass[b, :, n - t:] = float("nan")    # the step's own positions have no history; later ones are not this call's
+    old = mass.clone()
+    _mass_call(c, lengths, widths, q, lse, decay, mass, layer, c.status)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    _check_mass(c, mass, old, lengths, widths, q, lse, decay, layer)
+    # without a history, a row's weights add up to one
+    if decay == 0.0:
+        for b, (n, t) in enumerate(zip(lengths, widths)):
+            if t:
+                assert torch.allclose(mass[b, :, :n].double().sum(dim=1), torch.full((kv,), 8.0 * t, device="cuda", dtype=torch.float64),
+                                      rtol=1e-3)
+
+
+@pytest.mark.parametrize("fmt", ["q3", "fp8", "t5k"])
+def test_mass_with_extreme_scores(fmt):
+    """One position takes a row's whole weight, others underflow to nothing."""
+    lengths, widths = [600], [2]
+    c = Cache(fmt, lengths, 1, seed=2, scale=6.0)
+    q = queries(2, 8, 9, scale=12.0)
+    lse = _lse_of(c, lengths, widths, q, 0)
+    mass = torch.zeros((1, 1, 600), device="cuda")
+    old = mass.clone()
+    _mass_call(c, lengths, widths, q, lse, 1.0, mass)
+    torch.cuda.synchronize()
+    _check_mass(c, mass, old, lengths, widths, q, lse, 1.0)
+
+
+def test_mass_batch_equals_solo_and_repeats_bitwise():
+    lengths, widths = [900, 130, 2048], [6, 16, 1]
+    c = Cache("q3", lengths, 2, seed=5)
+    q = queries(sum(widths), 16, 6, torch.bfloat16)
+    lse = _lse_of(c, lengths, widths, q, 0)
+    both = torch.zeros((3, 2, 2048), device="cuda")
+    _mass_call(c, lengths, widths, q, lse, 1.0, both)
+    again = torch.zeros_like(both)
+    _mass_call(c, lengths, widths, q, lse, 1.0, again)
+    torch.cuda.synchronize()
+    assert torch.equal(both, again)
+    for b in range(3):
+        w = [widths[b] if i == b else 0 for i in range(3)]
+        one = torch.zeros_like(both)
+        MASS["q3"](c.desc, c.pool, c.page_table, i32(lengths), i32(w), offsets(widths), 2048, 16, 0, q, lse, 1.0, one)
+        torch.cuda.synchronize()
+        assert torch.equal(one[b], both[b])
+
+
+def test_mass_after_a_rollback():
+    """With the committed lengths, only the kept tokens' rows count and rolled-back positions have no history."""
+    L, T, acc = 700, 6, 3
+    c = Cache("q3", [L], 2, seed=8)
+    q = queries(T, 16, 7)
+    lse = _lse_of(c, [L], [T], q, 0)
+    mass = torch.rand((1, 2, L), device="cuda")
+    old = mass.clone()
+    kept = acc + 1
+    MASS["q3"](c.desc, c.pool, c.page_table, i32([L - (T - kept)]), i32([kept]), i32([0, kept]), L, T, 0, q, lse, 1.0, mass)
+    torch.cuda.synchronize()
+    _check_mass(c, mass, old, [L - (T - kept)], [kept], q, lse, 1.0)
+
+
+def test_mass_status_bits():
+    lengths, widths = [600, 520], [2, 3]
+    c = Cache("q3", lengths, 2, seed=3)
+    q = queries(5, 16, 1)
+    lse = _lse_of(c, lengths, widths, q, 0)
+    start = torch.rand((2, 2, 600), device="cuda")
+
+    def run(**kw):
+        mass, st = start.clone(), i32([0])
+        a = dict(lengths=lengths, widths=widths, lse=lse, table=c.page_table, max_ctx=600, max_n_q=16)
+        a.update(kw)
+        MASS["q3"](c.desc, c.pool, a["table"], i32(a["lengths"]), i32(a["widths"]), offsets(widths), a["max_ctx"], a["max_n_q"], 0, q,
+                   a["lse"], 1.0, mass, st)
+        torch.cuda.synchronize()
+        return mass, int(st.item())
+
+    good, st = run()
+    assert st == 0
+    # too many tokens for the host bound, for the length; a length beyond the host bound, beyond the page table
+    for kw in (dict(max_n_q=2), dict(lengths=[600, 2]), dict(max_ctx=599, lengths=[599, 600]), dict(lengths=[600, 800], max_ctx=600)):
+        mass, st = run(**kw)
+        assert st == _lib.Q3KV_STATUS_BAD_LENGTH
+        assert torch.equal(mass[1], start[1])
+    # a page id out of range: its positions keep their history
+    for bad in (-1, c.num_pages, 1 << 30):
+        table = c.page_table.clone()
+        table[0, 1] = bad
+        mass, st = run(table=table)
+        assert st == _lib.Q3KV_STATUS_BAD_PAGE
+        assert torch.equal(mass[0, :, 256:512], start[0, :, 256:512])
+        assert torch.equal(mass[0, :, :256], good[0, :, :256]) and torch.equal(mass[1], good[1])
+    # statistics that are not finite: the row is left out
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        l2 = lse.clone()
+        l2[0, 3] = bad
+        mass, st = run(lse=l2)
+        assert st == _lib.Q3KV_STATUS_NONFINITE_INPUT
+        l3 = lse.clone()
+        l3[0, 3] = 3.0e38                            # e^(s - 3e38) = 0
+        assert torch.equal(mass, run(lse=l3)[0])
+
+
+@pytest.mark.parametrize("fmt", ["q3", "fp8", "t5k"])
+@pytest.mark.parametrize("impl,split", [(0, 0), (2, 256), (1, 256), (1, 2048)])
+def test_verify_lse(fmt, impl, split):
+    """The statistic against float64, and the outputs bit for bit those of the call without it."""
+    if fmt == "fp8" and impl == 1:
+        pytest.skip("the fp8 cache has the tensor-core leg only")
+    lengths, widths = [1300, 700, 9], [5, 0, 9]
+    c = Cache(fmt, lengths, 2, 2, seed=12)
+    q = queries(sum(widths), 16, 2, torch.bfloat16, scale=1.0)
+    ws = torch.zeros(max(16, api.workspace_bytes(c.desc, 3, 1300, 9, impl, split)), dtype=torch.uint8, device="cuda")
+    args = (c.desc, c.pool, c.page_table, i32(lengths), i32(widths), offsets(widths), 1300, 9, 1, q)
+    plain = torch.full((q.shape[0], 16, 256), float("nan"), device="cuda")
+    out, lse = plain.clone(), torch.full((q.shape[0] + 2, 16), -5.0, device="cuda")
+    VERIFY[fmt](*args, plain, ws, impl, split, c.status)
+    VERIFY_LSE[fmt](*args, out, lse, ws, impl, split, c.status)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    assert torch.equal(out, plain)
+    assert torch.all(lse[q.shape[0]:] == -5.0)
+    for b in (0, 2):
+        for g in range(2):
+            s, bound = _reference(c, lengths, widths, q, 1, b, g)
+            r0 = sum(widths[:b])
+            got = lse[r0:r0 + widths[b], 8 * g:8 * g + 8].double().cpu().numpy().reshape(-1)
+            want = ev.log_sum_exp(s)
+            # the legs drop the product of two low halves, 2^-20 of A
+            tol = bound.max(axis=1) * 1.04 + 2.0 ** -20 * (1 + np.abs(want))
+            assert np.all(np.abs(got - want) <= tol)
+
+
+def test_prefill_lse():
+    L, T = 900, 200
+    c = Cache("q3", [L], 2, seed=13)
+    q = queries(T, 16, 3, torch.bfloat16, scale=1.0)
+    args = (c.desc, c.pool, c.page_table, i32([L]), i32([T]), i32([0, T]), L, T, 0, q)
+    for impl, split in ((0, 0), (1, 256)):
+        ws = torch.zeros(max(16, api.prefill_workspace_bytes(c.desc, 1, L, T, impl, split)), dtype=torch.uint8, device="cuda")
+        plain = torch.empty((T, 16, 256), device="cuda")
+        out, lse = plain.clone(), torch.empty((T, 16), device="cuda")
+        api.prefill_attn(*args, plain, ws, impl, split, c.status)
+        api.prefill_attn_lse(*args, out, lse, ws, impl, split, c.status)
+        torch.cuda.synchronize()
+        assert torch.equal(out, plain)
+        for g in range(2):
+            s, bound = _reference(c, [L], [T], q, 0, 0, g)
+            want = ev.log_sum_exp(s)
+            got = lse[:, 8 * g:8 * g + 8].double().cpu().numpy().reshape(-1)
+            assert np.all(np.abs(got - want) <= bound.max(axis=1) * 1.04 + 2.0 ** -20 * (1 + np.abs(want)))
+
+
+# ------------------------------------------------------------------ eviction
+def _evict_call(c, lengths, budgets, sink, recent, mass, layer=0, status=None, max_budget=None, with_mass=True, table=None, dst=None,
+                max_ctx=None, in_place=False):
+    S = len(lengths)
+    most = max(max(budgets), 1) if max_budget is None else max_budget
+    room = [(max(0, min(n, k)) + 255) // 256 for n, k in zip(lengths, budgets)]
+    if dst is None:
+        d = np.full((S, max(max(room), 1)), -1, np.int32)
+        at = 0
+        for b, r in enumerate(room):
+            d[b, :r] = c.free[at:at + r]
+            at += r
+        dst = torch.from_numpy(d).cuda()
+    layers = mass.shape[0]
+    kept = torch.full((layers, S, c.kv, most), -9, dtype=torch.int32, device="cuda")
+    out = torch.full((layers, S, c.kv, most), -9.0, device="cuda") if with_mass else None
+    ctx = i32(lengths)
+    new_len = ctx if in_place else i32([-9] * S)
+    EVICT[c.fmt](c.desc, c.pool, c.page_table if table is None else table, ctx, mass.shape[3] if max_ctx is None else max_ctx,
+                 i32(budgets), most, sink, recent, layer, mass, dst, kept, out, new_len, status)
+    torch.cuda.synchronize()
+    return kept.cpu().numpy(), None if out is None else out.cpu().numpy(), new_len.cpu().numpy(), dst.cpu().numpy()
+
+
+def _check_evict(c, before, lengths, budgets, sink, recent, mass, layer, got):
+    """Kept positions, masses, lengths and records; every other byte of the pool is as it was."""
+    kept, out, new_len, dst = got
+    m = mass.cpu().numpy()
+    pool_now = c.pool.clone()
+    for b, (n, k) in enumerate(zip(lengths, budgets)):
+        if k <= 0:
+            assert new_len[b] == n and np.all(kept[:, b] == -9)
+            continue
+        assert new_len[b] == min(n, k)
+        for la in range(m.shape[0]):
+            for g in range(c.kv):
+                want = ev.keep(m[la, b, g, :n], k, sink, recent)
+                assert np.array_equal(kept[la, b, g, :len(want)], want)
+                assert np.all(kept[la, b, g, len(want):] == -9)
+                if out is not None:
+                    assert np.array_equal(out[la, b, g, :len(want)], m[la, b, g, want], equal_nan=True)
+                    assert np.all(out[la, b, g, len(want):] == -9.0)
+                for kv in range(2):
+                    c.pool = before
+                    src = c.records(c.pt[b], layer + la, g, kv, want)
+                    c.pool = pool_now
+                    assert np.array_equal(c.records(dst[b], layer + la, g, kv, np.arange(len(want))), src)
+    c.pool = pool_now
+
+
+EVICT_CASES = [
+    # fmt, lengths, budgets, sink, recent, kv heads, layers of the pool, first layer, layers of the call
+    ("q3", [1], [1], 0, 0, 1, 1, 0, 1),
+    ("q3", [600], [300], 4, 32, 2, 1, 0, 1),
+    ("q3", [700, 90, 513], [256, 200, 257], 4, 16, 2, 3, 1, 2),
+    ("q3", [700, 90, 513], [0, 1, 512], 0, 0, 1, 2, 0, 2),
+    ("q3", [400], [50], 40, 30, 1, 1, 0, 1),                 # protected positions alone exceed the budget
+    ("q3", [400], [70], 40, 30, 1, 1, 0, 1),                 # and fill it exactly
+    ("q3", [20000, 9000], [3000, 8999], 16, 100, 2, 1, 0, 1),
+    ("fp8", [600, 300], [100, 299], 1, 1, 2, 2, 1, 1),
+    ("t5k", [600, 300], [100, 299], 1, 1, 2, 2, 0, 2),
+]
+
+
+@pytest.mark.parametrize("fmt,lengths,budgets,sink,recent,kv,layers,first,count", EVICT_CASES)
+@pytest.mark.parametrize("kind", ["random", "ties", "special"])
+def test_evict(fmt, lengths, budgets, sink, recent, kv, layers, first, count, kind):
+    room = sum((max(0, min(n, k)) + 255) // 256 for n, k in zip(lengths, budgets))
+    c = Cache(fmt, lengths, kv, layers, seed=21, extra_pages=room + 1)
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    mass = torch.rand((count, len(lengths), kv, max(lengths) + 5), generator=gen, device="cuda")
+    want_status = 0
+    if kind == "ties":
+        mass = (mass * 3).floor() / 3                        # three values
+    elif kind == "special":
+        mass = mass - 0.5
+        mass[..., ::7] = 0.0
+        mass[..., 1::7] = -0.0
+        mass[..., 2::11] = float("inf")
+        mass[..., 3::13] = -float("inf")
+        mass[..., 5::17] = 1e-40                             # subnormal
+        if kind == "special" and fmt == "q3" and lengths[0] == 600:
+            mass[..., 6::19] = float("nan")
+            want_status = _lib.Q3KV_STATUS_NONFINITE_INPUT
+    before = c.pool.clone()
+    got = _evict_call(c, lengths, budgets, sink, recent, mass, first, c.status)
+    assert int(c.status.item()) == want_status
+    _check_evict(c, before, lengths, budgets, sink, recent, mass, first, got)
+    # outside the destination pages' first records nothing changes
+    changed = (c.pool != before).nonzero().flatten()
+    per_page = c.pool.numel() // c.num_pages
+    pages = set((changed // per_page).unique().tolist())
+    assert pages <= set(got[3][got[3] >= 0].tolist())
+
+
+def test_evict_all_equal_and_all_nan():
+    c = Cache("q3", [900], 1, seed=1, extra_pages=2)
+    for value, status in ((0.25, 0), (float("nan"), _lib.Q3KV_STATUS_NONFINITE_INPUT)):
+        mass = torch.full((1, 1, 1, 900), value, device="cuda")
+        st = i32([0])
+        kept, _, n, _ = _evict_call(c, [900], [300], 2, 10, mass, 0, st)
+        want = np.concatenate([np.arange(290), np.arange(890, 900)])
+        assert np.array_equal(kept[0, 0, 0], want) and n[0] == 300 and int(st.item()) == status
+
+
+def test_evict_without_masses_in_place_length_and_repeats():
+    lengths, budgets = [5000, 3000], [1000, 700]
+    c = Cache("q3", lengths, 2, seed=4, extra_pages=8)
+    mass = torch.rand((1, 2, 2, 5000), device="cuda")
+    first = _evict_call(c, lengths, budgets, 4, 64, mass)
+    pool = c.pool.clone()
+    for _ in range(3):
+        again = _evict_call(c, lengths, budgets, 4, 64, mass, with_mass=False, in_place=True)
+        assert np.array_equal(first[0], again[0]) and again[1] is None and np.array_equal(first[2], again[2])
+        assert torch.equal(c.pool, pool)
+
+
+def test_evict_status_bits():
+    lengths, budgets = [600, 700], [300, 290]
+    c = Cache("q3", lengths, 1, seed=6, extra_pages=4)
+    mass = torch.rand((1, 2, 1, 700), device="cuda")
+    good = c.pool.clone()
+    bad_len, bad_page = _lib.Q3KV_STATUS_BAD_LENGTH, _lib.Q3KV_STATUS_BAD_PAGE
+
+    def run(lens=lengths, buds=budgets, **kw):
+        c.pool.copy_(good)
+        st = i32([0])
+        got = _evict_call(c, lens, buds, 1, 2, mass, status=st, **kw)
+        return got, int(st.item())
+
+    (kept, _, n, dst), st = run()
+    assert st == 0 and n.tolist() == [300, 290]
+    for kw in (dict(max_budget=295), dict(max_ctx=650), dict(lens=[600, 800], max_ctx=700), dict(lens=[600, -1])):
+        (k2, _, n2, _), st = run(**kw)
+        slot = 0 if "max_budget" in kw else 1
+        assert st == bad_len and n2[slot] == kw.get("lens", lengths)[slot] and np.all(k2[:, slot] == -9)
+        assert np.array_equal(k2[:, 1 - slot, :, :290], kept[:, 1 - slot, :, :290])
+    narrow = torch.from_numpy(np.ascontiguousarray(dst[:, :1])).cuda()
+    (_, _, n2, _), st = run(dst=narrow)              # 300 and 290 records do not fit one page
+    assert st == bad_len and n2.tolist() == lengths and torch.equal(c.pool, good)
+    for bad in (-1, c.num_pages):
+        d = torch.from_numpy(dst).cuda()
+        d[0, 0] = bad
+        (k2, _, n2, _), st = run(dst=d)
+        assert st == bad_page and np.array_equal(k2, kept) and n2.tolist() == [300, 290]
+        table = c.page_table.clone()
+        table[1, 1] = bad
+        (k2, _, _, _), st = run(table=table)
+        assert st == bad_page and np.array_equal(k2, kept)
+
+
+def test_evict_captured_and_replayed():
+    lengths, budgets = [3000, 1000], [500, 400]
+    c = Cache("q3", lengths, 2, seed=9, extra_pages=4)
+    mass = torch.rand((1, 2, 2, 3000), device="cuda")
+    dst = torch.tensor([[int(c.free[0]), int(c.free[1])], [int(c.free[2]), int(c.free[3])]], dtype=torch.int32, device="cuda")
+    ctx, bud = i32(lengths), i32(budgets)
+    kept = torch.zeros((1, 2, 2, 500), dtype=torch.int32, device="cuda")
+    out, n = torch.zeros((1, 2, 2, 500), device="cuda"), i32([0, 0])
+    call = lambda: api.evict(c.desc, c.pool, c.page_table, ctx, 3000, bud, 500, 2, 50, 0, mass, dst, kept, out, n)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    mass.copy_(torch.rand_like(mass))
+    before = c.pool.clone()
+    g.replay()
+    torch.cuda.synchronize()
+    kept_h = kept.cpu().numpy()
+    for b in range(2):
+        kept_h[:, b, :, budgets[b]:] = -9
+    outs = out.cpu().numpy()
+    outs[:, 1, :, 400:] = -9.0
+    _check_evict(c, before, lengths, budgets, 2, 50, mass, 0, (kept_h, outs, n.cpu().numpy(), dst.cpu().numpy()))
