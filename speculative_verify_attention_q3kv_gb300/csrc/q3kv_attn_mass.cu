@@ -21,18 +21,23 @@
 // 64 at a time): D_b[p][r] = sum over dims d of block b of code[p][d] (q_hi + q_lo)[r][d];
 // A = codes in TMEM (lane = position), B = queries in shared memory (K-major).  A
 // tile's 256 dims are four parts of 64 dims; a part's accumulators (128 columns for
-// the 3-bit cache: two blocks of 64 rows) form one slot of a ring of three, so the
-// epilogue of a part overlaps the products of the next ones.
+// the 3-bit cache at 64 rows) form one slot of a ring, so the epilogue of a part overlaps
+// the products of the next ones.
 //
 // Warp roles (16 warps, 128 registers each):
-//   E   warps 0-7    epilogue: thread = position (lane quarter warp & 3), rows 0-31 or
-//                    32-63 of the chunk (warp >> 2); score sums start at -lse in log2
-//                    units, weights 2^s, rows summed in the thread
-//   D   warps 8-11   thread = position: its record in registers a tile (or a part)
-//                    ahead, converted part by part into TMEM
+//   E   warps 0-7    epilogue: thread = position (lane quarter warp & 3), all rows of the
+//                    chunk; the two warps of a lane quarter take every other tile.  Score
+//                    sums start at -lse in log2 units, weights 2^s, rows summed in the
+//                    thread.  Issue slots bound this kernel, so a tile's waits, addresses
+//                    and barrier traffic are paid by one warp per lane quarter.
+//   D   warps 8-11   thread = position: its staged record converted part by part into
+//                    TMEM (the next part is converted while the last one's stores are in
+//                    flight); warp 8 also copies the records of the tiles ahead into
+//                    shared memory (cp.async.bulk, one stage per tile)
 //   M   warps 12-15  one thread each issues the products of one part: an issuing
 //                    thread starts a K = 16 MMA about every 54 cycles, so four issue
-// TMEM (512 columns): operand (128, turbo5k 256) | ring of three slots (3 x 128, or x 64).
+// TMEM (512 columns): operand (128, turbo5k 256) | ring of accumulator slots (3 for more
+// than 32 rows, 6, or 12 for at most 16).
 //
 // Work: the tiles of all (slot, kv head) pairs in one sequence, an equal share per
 // CTA (one per SM), whatever the slots' lengths; a CTA rotates and splits the
@@ -55,19 +60,25 @@ namespace q3kv {
 namespace {
 
 constexpr int kWarps = 16;
+constexpr int kWarpD = 8, kWarpM = 12;      // first warps of the roles
+constexpr int kTurns = 2;                   // E warps of a lane quarter
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileP = 128;                 // positions per tile
 constexpr int kChunkRows = 64;              // query rows per pass over a tile
 constexpr int kMaxChunks = kMaxRows / kChunkRows;
 constexpr int kParts = 4;                   // parts of 64 dims
-constexpr int kSlots = 3;                   // accumulator slots
-constexpr int kFreeBars = 12;               // consumption events: a multiple of kParts and kSlots
+constexpr int kAccCols = 192;               // accumulator columns per scale group of a part
+constexpr int kFreeBars = 12;               // consumption events: a multiple of kParts and of every slot count
+constexpr int kDoneBars = 4;                // generations of a part's completion barrier
 
 template <int FMT>
 struct Mf {                                 // 3-bit cache
     static constexpr int kGroups = 2;       // accumulators (scale groups) of a part
     static constexpr int kOps = 1;          // fp16 operands per value
     static constexpr int kRecB = kRecordBytes;
+    static constexpr int kStride = kRecordBytes;   // of a staged record in shared memory
+    static constexpr int kStages = 5;              // staged tiles (with scales: more than the E warps' turns)
+    static constexpr bool kScales = true;
     static constexpr bool kRot = true;
 };
 template <>
@@ -75,6 +86,9 @@ struct Mf<kFmtFp8> {
     static constexpr int kGroups = 1;
     static constexpr int kOps = 1;
     static constexpr int kRecB = kFp8RecordBytes;
+    static constexpr int kStride = kFp8RecordBytes + 16;   // 16-byte loads of 8 lanes hit 8 bank groups
+    static constexpr int kStages = 2;
+    static constexpr bool kScales = false;
     static constexpr bool kRot = false;
 };
 template <>
@@ -82,23 +96,35 @@ struct Mf<kFmtT5k> {
     static constexpr int kGroups = 1;
     static constexpr int kOps = 2;
     static constexpr int kRecB = kT5kKRecordBytes;
+    static constexpr int kStride = kT5kKRecordBytes;
+    static constexpr int kStages = 4;
+    static constexpr bool kScales = true;
     static constexpr bool kRot = true;
 };
 constexpr uint32_t kPartCols = 32;          // TMEM columns of a part's operand (64 fp16 values)
 constexpr uint32_t kTmemCols = 512;
 
+constexpr int kMaxStages = 5;
+constexpr int kAhead = 2;                   // tiles whose old masses are loaded ahead
+
+// An epilogue group that skips tiles, and an issuer that is up to a tile ahead,
+// must not mistake an older phase for the one they wait for (only its parity is
+// tested): hence several generations of done and acc_free.
 struct Bars {
-    unsigned long long a_full[kParts];      // operand part in TMEM (4 D warps)
-    unsigned long long done[kParts];        // products of a part and chunk (1 commit): accumulators ready
-    unsigned long long a_free[kParts];      // every chunk's products of a part (1 commit): operand read
-    unsigned long long acc_free[kFreeBars]; // accumulators of the event read (8 E warps)
-    unsigned long long drain[kParts];       // everything an issuer started is done (1 commit)
+    unsigned long long a_full[kParts];             // operand part in TMEM (4 D warps)
+    unsigned long long done[kParts][kDoneBars];    // products of a part in pass ph (1 commit), by ph % 4
+    unsigned long long a_free[kParts];             // every chunk's products of a part (1 commit): operand read
+    unsigned long long acc_free[kFreeBars];        // accumulators of event c read (4 E warps), by c % 12
+    unsigned long long drain[kParts];              // everything an issuer started is done (1 commit)
+    unsigned long long r_full[kMaxStages];         // a tile's records landed (copy bytes)
+    unsigned long long r_free[kMaxStages];         // and were read (4 D warps; with scales, 4 E warps)
 };
 
+template <int FMT>
 struct __align__(16) MassSmem {
     __half q[kMaxChunks][2][kChunkRows * kHeadDim];   // [chunk][hi | lo], B operand
+    uint8_t rec[Mf<FMT>::kStages][kTileP * Mf<FMT>::kStride];   // staged records
     float nlse[kMaxRows];                             // -lse in log2 units; -inf leaves a row out
-    float part[2][kTileP];                            // sums of rows 32..63, double-buffered by tile
     Bars bar;
     uint32_t tmem_base;
     int abort;
@@ -132,6 +158,12 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long x, unsigne
     return r;
 }
 
+__device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigned long long y) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
 // One segment: tiles [t0, t1) of a (slot, kv head) pair.
 struct Segment {
     int slot, g, t0, t1;
@@ -142,7 +174,7 @@ struct Segment {
 // Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e), split
 // into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  One row per warp.
 template <typename TIn, int FMT>
-__device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem& sm) {
+__device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = kGroup * s.T;
     const int Hq = a.num_kv_heads * kGroup;
@@ -195,95 +227,284 @@ __device__ __forceinline__ const uint8_t* k_record(const MassArgs& a, const Segm
                                                     Mf<FMT>::kRecB));
 }
 
-// Words of a part of a record that a D thread holds ahead.
+// Words of a part (64 dims) of a record.
 template <int FMT>
 struct Words {
     static constexpr int kN = FMT == kFmtFp8 ? 16 : (FMT == kFmtT5k ? 10 : 6);
 };
 
+// Part q of a staged record.
 template <int FMT>
-__device__ __forceinline__ void fetch_part(const uint8_t* rec, int q, uint32_t (&w)[Words<FMT>::kN]) {
+__device__ __forceinline__ void read_part(const uint8_t* rec, int q, uint32_t (&w)[Words<FMT>::kN]) {
     if constexpr (FMT == kFmtFp8) {
         const uint4* p = reinterpret_cast<const uint4*>(rec) + 4 * q;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const uint4 u = rec ? __ldg(p + m) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 u = p[m];
             w[4 * m] = u.x; w[4 * m + 1] = u.y; w[4 * m + 2] = u.z; w[4 * m + 3] = u.w;
         }
     } else if constexpr (FMT == kFmtT5k) {
         const uint32_t* p = reinterpret_cast<const uint32_t*>(rec);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) w[m] = rec ? __ldg(p + 8 * q + m) : 0u;
+        for (int m = 0; m < 8; ++m) w[m] = p[8 * q + m];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) w[8 + m] = rec ? __ldg(p + 32 + 2 * q + m) : 0u;
+        for (int m = 0; m < 2; ++m) w[8 + m] = p[32 + 2 * q + m];
     } else {
         const uint2* p = reinterpret_cast<const uint2*>(rec) + 3 * q;      // 24 bytes
 #pragma unroll
         for (int m = 0; m < 3; ++m) {
-            const uint2 u = rec ? __ldg(p + m) : make_uint2(0u, 0u);
+            const uint2 u = p[m];
             w[2 * m] = u.x; w[2 * m + 1] = u.y;
         }
     }
 }
 
-// 64 dims of this thread's position into the TMEM columns at col.
+// Copies the records of tile i of the segment into its stage (one warp; the whole
+// warp calls).  A tile's 128 records are contiguous; padded stages take them one by
+// one.  A page out of range completes the phase without data: its scores are unused.
 template <int FMT>
-__device__ __forceinline__ void store_part(const uint32_t (&w)[Words<FMT>::kN], float cent, uint32_t col) {
+__device__ __forceinline__ void stage_tile(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, int i, int counter) {
+    const int lane = threadIdx.x & 31;
+    const int st = counter % Mf<FMT>::kStages;
+    const int pos0 = (s.t0 + i) * kTileP;
+    const int32_t page = page_of(a, s.pt, pos0);
+    if (page < 0) {
+        if (lane == 0) {
+            if (a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+            mbar_arrive(&sm.bar.r_full[st]);
+        }
+        return;
+    }
+    const uint8_t* src = k_record<FMT>(a, s, page, pos0);
+    fence_proxy_async();
+    if (lane == 0) mbar_arrive_expect_tx(&sm.bar.r_full[st], (uint32_t)(kTileP * Mf<FMT>::kRecB));
+    __syncwarp();
+    if (Mf<FMT>::kStride == Mf<FMT>::kRecB) {
+        if (lane == 0) bulk_g2s(sm.rec[st], src, (uint32_t)(kTileP * Mf<FMT>::kRecB), &sm.bar.r_full[st]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kTileP / 32; ++k) {
+            const int r = 32 * k + lane;
+            bulk_g2s(sm.rec[st] + r * Mf<FMT>::kStride, src + r * Mf<FMT>::kRecB, (uint32_t)Mf<FMT>::kRecB, &sm.bar.r_full[st]);
+        }
+    }
+    __syncwarp();
+}
+
+// 64 dims of this thread's position as fp16 pairs, K order (turbo5k: hi, then lo).
+template <int FMT>
+__device__ __forceinline__ void convert_part(const uint32_t (&w)[Words<FMT>::kN], float cent,
+                                             uint32_t (&h)[kPartCols * Mf<FMT>::kOps]) {
     if constexpr (FMT == kFmtFp8) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t h8[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) e4m3x4_to_f16(w[4 * c + k], h8[2 * k], h8[2 * k + 1]);
-            tmem_st8(col + 8 * c, h8);
-        }
+        for (int k = 0; k < 16; ++k) e4m3x4_to_f16(w[k], h[2 * k], h[2 * k + 1]);
     } else if constexpr (FMT == kFmtT5k) {
         // lane l holds centroid l: a code's value by shuffle, split into fp16 hi / lo
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int mm = 0; mm < 8; ++mm) {
-                const int m = 8 * c + mm;                      // pair of the part
-                const uint32_t nw = w[m / 4], top = w[8 + m / 16];
-                const uint32_t c0 = ((nw >> (8 * (m % 4))) & 0xFu) | (((top >> (2 * (m % 16))) & 1u) << 4);
-                const uint32_t c1 = ((nw >> (8 * (m % 4) + 4)) & 0xFu) | (((top >> (2 * (m % 16) + 1)) & 1u) << 4);
-                const float v0 = __shfl_sync(0xffffffffu, cent, (int)c0);
-                const float v1 = __shfl_sync(0xffffffffu, cent, (int)c1);
-                const __half2 h2 = __floats2half2_rn(v0, v1);
-                const float2 hf = __half22float2(h2);
-                hi[mm] = as_u32(h2);
-                lo[mm] = as_u32(__floats2half2_rn(v0 - hf.x, v1 - hf.y));
-            }
-            tmem_st8(col + 8 * c, hi);
-            tmem_st8(col + kParts * kPartCols + 8 * c, lo);
+        for (int m = 0; m < 32; ++m) {                         // pair of the part
+            const uint32_t nw = w[m / 4], top = w[8 + m / 16];
+            const uint32_t c0 = ((nw >> (8 * (m % 4))) & 0xFu) | (((top >> (2 * (m % 16))) & 1u) << 4);
+            const uint32_t c1 = ((nw >> (8 * (m % 4) + 4)) & 0xFu) | (((top >> (2 * (m % 16) + 1)) & 1u) << 4);
+            const float v0 = __shfl_sync(0xffffffffu, cent, (int)c0);
+            const float v1 = __shfl_sync(0xffffffffu, cent, (int)c1);
+            const __half2 h2 = __floats2half2_rn(v0, v1);
+            const float2 hf = __half22float2(h2);
+            h[m] = as_u32(h2);
+            h[kPartCols + m] = as_u32(__floats2half2_rn(v0 - hf.x, v1 - hf.y));
         }
     } else {
-        const __half2 m12 = __half2half2(__ushort_as_half((unsigned short)0xCA00u));   // -12
+        // A code pair at bits (o, o + 16) of a word, under the exponent of 2^(10 - o), is
+        // 2^(10 - o) + c: for o = 3 and 6 an and-or and one exact subtraction give c - 3.5.
+        // The fields at 0, 9 and 12 come to 3, 3 and 6 with one shift for the first and one
+        // for the other two.
+        const __half2 m3 = __half2half2(__ushort_as_half((unsigned short)0xD81Cu));   // -131.5
+        const __half2 m6 = __half2half2(__ushort_as_half((unsigned short)0xCCE0u));   // -19.5
+        const __half2 m12 = __half2half2(__ushort_as_half((unsigned short)0xCA00u));  // -12
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            uint32_t h16[16];
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const uint32_t x = m < 15 ? code_pair_word(w[3 * b + m / 5], 3 * (m % 5))
-                                          : code_pair_last(w[3 * b], w[3 * b + 1], w[3 * b + 2]);
-                h16[m] = as_u32(__hadd2(as_h2(x), m12));       // (8.5 + c) - 12, exact
+            for (int k = 0; k < 3; ++k) {
+                const uint32_t u = w[3 * b + k], l = u << 3, r = u >> 6;
+                h[16 * b + 5 * k] = as_u32(__hadd2(as_h2((l & 0x00380038u) | 0x58005800u), m3));
+                h[16 * b + 5 * k + 1] = as_u32(__hadd2(as_h2((u & 0x00380038u) | 0x58005800u), m3));
+                h[16 * b + 5 * k + 2] = as_u32(__hadd2(as_h2((u & 0x01C001C0u) | 0x4C004C00u), m6));
+                h[16 * b + 5 * k + 3] = as_u32(__hadd2(as_h2((r & 0x00380038u) | 0x58005800u), m3));
+                h[16 * b + 5 * k + 4] = as_u32(__hadd2(as_h2((r & 0x01C001C0u) | 0x4C004C00u), m6));
             }
-            tmem_st16(col + 16 * b, h16);
+            // (8.5 + c) - 12, exact
+            h[16 * b + 15] = as_u32(__hadd2(as_h2(code_pair_last(w[3 * b], w[3 * b + 1], w[3 * b + 2])), m12));
         }
     }
+}
+
+template <int FMT>
+__device__ __forceinline__ void store_part(const uint32_t (&h)[kPartCols * Mf<FMT>::kOps], uint32_t col) {
+#pragma unroll
+    for (int o = 0; o < Mf<FMT>::kOps; ++o) {
+        tmem_st16(col + kParts * kPartCols * o, *reinterpret_cast<const uint32_t(*)[16]>(&h[kPartCols * o]));
+        tmem_st16(col + kParts * kPartCols * o + 16, *reinterpret_cast<const uint32_t(*)[16]>(&h[kPartCols * o + 16]));
+    }
+}
+
+// What the epilogue of a segment needs besides the segment.
+struct EpiState {
+    uint32_t tmem_acc;           // first accumulator column, this warp's lanes
+    int tiles_done, phases, n;
+    volatile int* abort;
+};
+
+// Scale of group gi of a part, from the position's scale words.
+template <int FMT>
+__device__ __forceinline__ float part_scale(const uint4& sc, int part, int gi) {
+    if (FMT == kFmtQ3) {
+        const uint32_t word = part == 0 ? sc.x : (part == 1 ? sc.y : (part == 2 ? sc.z : sc.w));
+        return __half2float(__ushort_as_half((unsigned short)(gi ? word >> 16 : word & 0xFFFFu)));
+    }
+    if (FMT == kFmtT5k) return __half2float(__ushort_as_half((unsigned short)(part >= 2 ? sc.x >> 16 : sc.x & 0xFFFFu)));
+    return 1.0f;
+}
+
+// Epilogue of this warp's tiles of a segment; COLS accumulator columns per group
+// (16, 32 or 64 query rows of a pass).
+template <int FMT, int COLS>
+__device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, const EpiState& e, bool ok) {
+    constexpr int G = Mf<FMT>::kGroups, ST = Mf<FMT>::kStages, SLOTS = kAccCols / COLS;
+    constexpr int LD = COLS < 32 ? 16 : 32;                  // columns of one TMEM load
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int turn = warp >> 2;
+    const int p = 32 * (warp & 3) + lane;
+    const int Nctx = s.L - s.T, R = kGroup * s.T;
+    Bars& bar = sm.bar;
+    float* mass = a.mass + ((int64_t)s.slot * a.num_kv_heads + s.g) * a.mass_stride;
+    // old masses and page checks of the next tiles, ahead of their use
+    auto old_of = [&](int i) {
+        const int pos = (s.t0 + i) * kTileP + p;
+        return (i < e.n && a.decay > 0.0f && pos < Nctx) ? mass[pos] : 0.0f;
+    };
+    float old_q[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) old_q[k] = old_of(turn + k * kTurns);
+    int32_t page_next = turn < e.n ? page_of(a, s.pt, (s.t0 + turn) * kTileP) : -1;
+#pragma unroll 1
+    for (int i = turn; i < e.n; i += kTurns) {
+        const float old = old_q[0];
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) old_q[k] = old_q[k + 1];
+        old_q[kAhead - 1] = old_of(i + kAhead * kTurns);
+        const int pos0 = (s.t0 + i) * kTileP;
+        const int pos = pos0 + p;
+        const bool page_ok = page_next >= 0;
+        if (i + kTurns < e.n) page_next = page_of(a, s.pt, pos0 + kTurns * kTileP);
+        uint4 sc = make_uint4(0u, 0u, 0u, 0u);
+        if (Mf<FMT>::kScales) {
+            // this position's scales from the staged record
+            const int rc = e.tiles_done + i;
+            ok = ok && warp_wait(&bar.r_full[rc % ST], (uint32_t)((rc / ST) & 1), e.abort);
+            const uint8_t* rec = sm.rec[rc % ST] + p * Mf<FMT>::kStride;
+            if (FMT == kFmtQ3) sc = *reinterpret_cast<const uint4*>(rec + 96);
+            if (FMT == kFmtT5k) sc.x = *reinterpret_cast<const uint32_t*>(rec + 160);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.r_free[rc % ST]);
+        }
+        unsigned long long sum0 = 0ull, sum1 = 0ull;         // pairs of zeros
+#pragma unroll 1
+        for (int j = 0; j < s.chunks; ++j) {
+            const int ph = e.phases + i * s.chunks + j;
+            const int halves = COLS == 64 && R - kChunkRows * j <= 32 ? 1 : COLS / LD;   // loads of a group
+            unsigned long long acc[COLS / 2];
+#pragma unroll
+            for (int k = 0; k < COLS / 4; ++k) {
+                const float4 u = *reinterpret_cast<const float4*>(&sm.nlse[kChunkRows * j + 4 * k]);
+                acc[2 * k] = pack2(u.x, u.y);
+                acc[2 * k + 1] = pack2(u.z, u.w);
+            }
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                const int c = kParts * ph + part;
+                ok = ok && warp_wait(&bar.done[part][ph % kDoneBars], (uint32_t)((ph / kDoneBars) & 1), e.abort);
+                tc_fence_after();
+                const uint32_t col = e.tmem_acc + (uint32_t)((c % SLOTS) * G * COLS);
+                if (COLS <= 32) {
+                    // the whole part in one round trip
+                    float x[G][LD];
+#pragma unroll
+                    for (int gi = 0; gi < G; ++gi) {
+                        if (LD == 16) tmem_ld16(col + COLS * gi, x[gi]);
+                        else tmem_ld32(col + COLS * gi, x[gi]);
+                    }
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.acc_free[c % kFreeBars]);
+#pragma unroll
+                    for (int gi = 0; gi < G; ++gi) {
+                        const float scale = part_scale<FMT>(sc, part, gi);
+                        const unsigned long long s2 = pack2(scale, scale);
+#pragma unroll
+                        for (int k = 0; k < LD / 2; ++k) acc[k] = fma2(pack2(x[gi][2 * k], x[gi][2 * k + 1]), s2, acc[k]);
+                    }
+                } else {
+#pragma unroll
+                    for (int gi = 0; gi < G; ++gi) {
+                        const float scale = part_scale<FMT>(sc, part, gi);
+                        const unsigned long long s2 = pack2(scale, scale);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (h < halves) {
+                                float x[LD];
+                                tmem_ld32(col + COLS * gi + 32 * h, x);
+                                tmem_ld_wait();
+                                if (gi == G - 1 && h == halves - 1) {
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive(&bar.acc_free[c % kFreeBars]);
+                                }
+#pragma unroll
+                                for (int k = 0; k < LD / 2; ++k)
+                                    acc[16 * h + k] = fma2(pack2(x[2 * k], x[2 * k + 1]), s2, acc[16 * h + k]);
+                            }
+                    }
+                }
+            }
+            // weights; padding rows start at -inf and weigh nothing.  Row r (token r / 8) sees
+            // positions <= Nctx + r / 8.
+            const int r_min = pos0 + kTileP - 1 > Nctx ? kGroup * (pos - Nctx) - kChunkRows * j : 0;
+            if (pos0 + kTileP - 1 > Nctx) {
+#pragma unroll
+                for (int k = 0; k < COLS / 2; ++k) {
+                    float x0, x1;
+                    unpack2(acc[k], x0, x1);
+                    if (2 * k < r_min) x0 = -CUDART_INF_F;
+                    if (2 * k + 1 < r_min) x1 = -CUDART_INF_F;
+                    acc[k] = pack2(x0, x1);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < COLS / 2; ++k) {
+                float x0, x1;
+                unpack2(acc[k], x0, x1);
+                const unsigned long long w2 = pack2(fast_exp2(x0), fast_exp2(x1));
+                if (k & 1) sum1 = add2(sum1, w2);
+                else sum0 = add2(sum0, w2);
+            }
+        }
+        float a0, a1;
+        unpack2(add2(sum0, sum1), a0, a1);
+        if (pos < s.L) mass[pos] = fmaf(a.decay, old, page_ok ? a0 + a1 : 0.0f);
+    }
+    return ok;
 }
 
 template <typename TIn, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant__ MassArgs a) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    MassSmem& sm = *reinterpret_cast<MassSmem*>(smem_raw);
+    MassSmem<FMT>& sm = *reinterpret_cast<MassSmem<FMT>*>(smem_raw);
     Bars& bar = sm.bar;
+    constexpr int ST = Mf<FMT>::kStages;
     volatile int* abort = &sm.abort;
     constexpr int G = Mf<FMT>::kGroups, OPS = Mf<FMT>::kOps;
     constexpr uint32_t kColAcc = kParts * kPartCols * OPS;
-    constexpr uint32_t kSlotCols = G * kChunkRows;
-    static_assert(kColAcc + kSlots * kSlotCols <= kTmemCols, "TMEM");
+    static_assert(kColAcc + G * kAccCols <= kTmemCols, "TMEM");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -291,15 +512,19 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (tid == 0) {
         for (int q = 0; q < kParts; ++q) {
             mbar_init(&bar.a_full[q], 4);
-            mbar_init(&bar.done[q], 1);
+            for (int e = 0; e < kDoneBars; ++e) mbar_init(&bar.done[q][e], 1);
             mbar_init(&bar.a_free[q], 1);
             mbar_init(&bar.drain[q], 1);
         }
-        for (int e = 0; e < kFreeBars; ++e) mbar_init(&bar.acc_free[e], 8);
+        for (int e = 0; e < kFreeBars; ++e) mbar_init(&bar.acc_free[e], 4);
+        for (int e = 0; e < ST; ++e) {
+            mbar_init(&bar.r_full[e], 1);
+            mbar_init(&bar.r_free[e], Mf<FMT>::kScales ? 8 : 4);
+        }
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 12) tmem_alloc(&sm.tmem_base, kTmemCols);
+    if (warp == kWarpM) tmem_alloc(&sm.tmem_base, kTmemCols);
     if (warp == 0) {
         // this CTA's share [w0, w1) of the sequence, and the slot it starts in
         bool bad = false;
@@ -344,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     int slot = sm.first_slot;
     int tiles_done = 0;                      // tiles of earlier segments (a_full and a_free phases)
     int phases = 0;                          // (tile, chunk) passes of earlier segments (done phases)
+    int staged = -1;
     bool ok = true;
     const float cent = FMT == kFmtT5k ? a.t5k.c[lane] : 0.0f;
 
@@ -360,161 +586,90 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         s.L = a.ctx_len[slot];
         s.chunks = (kGroup * s.T + kChunkRows - 1) / kChunkRows;
         s.pt = a.page_table + (int64_t)slot * a.max_pages_per_slot;
+        const int n = s.t1 - s.t0;
+        if (warp == kWarpD)                  // the first tiles' records are in flight while the queries are prepared
+            for (int k = 0; k < min(n, ST); ++k) stage_tile<FMT>(a, s, sm, k, tiles_done + k);
         load_queries<TIn, FMT>(a, s, sm);
         __syncthreads();
-        const int n = s.t1 - s.t0;
         const int Nctx = s.L - s.T;
 
-        if (warp < 8) {
+        // accumulator columns per group (query rows of a pass, rounded up) and slots of the ring
+        const int cols = kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : 64);
+        const int slots = kAccCols / cols;
+
+        if (warp < kWarpD) {
             // ============================================================ E: epilogue
-            const int q4 = warp & 3, rh = warp >> 2, r0 = 32 * rh;
-            const int p = 32 * q4 + lane;
-            const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-            float* mass = a.mass + ((int64_t)s.slot * a.num_kv_heads + s.g) * a.mass_stride;
-            // this thread's scales of a tile, a tile ahead
-            auto fetch_scales = [&](int i, uint4& sc) {
-                const int pos0 = (s.t0 + i) * kTileP;
-                const int32_t page = i < n ? page_of(a, s.pt, pos0) : -1;
-                sc = make_uint4(0u, 0u, 0u, 0u);
-                if (page >= 0 && pos0 + p < s.L) {
-                    const uint8_t* rec = k_record<FMT>(a, s, page, pos0 + p);
-                    if (FMT == kFmtQ3) sc = __ldg(reinterpret_cast<const uint4*>(rec + 96));
-                    if (FMT == kFmtT5k) sc.x = __ldg(reinterpret_cast<const uint32_t*>(rec + 160));
-                }
-            };
-            uint4 next;
-            fetch_scales(0, next);
-            for (int i = 0; i < n; ++i) {
-                const uint4 sc = next;
-                fetch_scales(i + 1, next);
-                const int pos0 = (s.t0 + i) * kTileP;
-                const int pos = pos0 + p;
-                const bool page_ok = page_of(a, s.pt, pos0) >= 0;
-                if (!page_ok && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
-                float old = 0.0f;
-                if (rh == 0 && a.decay > 0.0f && pos < Nctx) old = mass[pos];
-                const bool interior = pos0 + kTileP - 1 <= Nctx;
-                float sum = 0.0f;
-                for (int j = 0; j < s.chunks; ++j) {
-                    const int rows = min(kChunkRows, kGroup * s.T - kChunkRows * j);
-                    const int N = (rows + 15) & ~15;
-                    const int ph = phases + i * s.chunks + j;
-                    unsigned long long acc[16];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float4 u = *reinterpret_cast<const float4*>(&sm.nlse[kChunkRows * j + r0 + 4 * k]);
-                        acc[2 * k] = pack2(u.x, u.y);
-                        acc[2 * k + 1] = pack2(u.z, u.w);
-                    }
-#pragma unroll
-                    for (int part = 0; part < kParts; ++part) {
-                        const int c = kParts * ph + part;
-                        ok = ok && warp_wait(&bar.done[part], (uint32_t)(ph & 1), abort);
-                        tc_fence_after();
-                        const uint32_t col = tmem + lane_base + kColAcc + (uint32_t)(c % kSlots) * kSlotCols + r0;
-#pragma unroll
-                        for (int gi = 0; gi < G; ++gi) {
-                            float scale = 1.0f;
-                            if (FMT == kFmtQ3) {
-                                const uint32_t word = part == 0 ? sc.x : (part == 1 ? sc.y : (part == 2 ? sc.z : sc.w));
-                                scale = __half2float(__ushort_as_half((unsigned short)(gi ? word >> 16 : word & 0xFFFFu)));
-                            } else if (FMT == kFmtT5k) {
-                                scale = __half2float(__ushort_as_half((unsigned short)(part >= 2 ? sc.x >> 16 : sc.x & 0xFFFFu)));
-                            }
-                            const unsigned long long s2 = pack2(scale, scale);
-                            float x[32];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (r0 + 16 * h < N) tmem_ld16(col + kChunkRows * gi + 16 * h, &x[16 * h]);
-                            tmem_ld_wait();
-                            if (gi == G - 1) {
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(&bar.acc_free[c % kFreeBars]);
-                            }
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (r0 + 16 * h < N)
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        acc[8 * h + k] = fma2(pack2(x[16 * h + 2 * k], x[16 * h + 2 * k + 1]), s2, acc[8 * h + k]);
-                        }
-                    }
-                    // weights; row r (token r / 8) sees positions <= Nctx + r / 8
-                    const int r_min = interior ? 0 : kGroup * (pos - Nctx) - kChunkRows * j - r0;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (r0 + 16 * h < N)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                float x0, x1;
-                                unpack2(acc[8 * h + k], x0, x1);
-                                const int r = 16 * h + 2 * k;
-                                sum += r >= r_min ? fast_exp2(x0) : 0.0f;
-                                sum += r + 1 >= r_min ? fast_exp2(x1) : 0.0f;
-                            }
-                }
-                if (rh == 1) sm.part[i & 1][p] = sum;
-                named_sync(1 + q4, 64);
-                if (rh == 0 && pos < s.L) {
-                    const float t = page_ok ? sum + sm.part[i & 1][p] : 0.0f;
-                    mass[pos] = fmaf(a.decay, old, t);
-                }
-            }
-        } else if (warp < 12) {
+            const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColAcc, tiles_done, phases, n, abort};
+            if (cols == 16) ok = epilogue<FMT, 16>(a, s, sm, e, ok);
+            else if (cols == 32) ok = epilogue<FMT, 32>(a, s, sm, e, ok);
+            else ok = epilogue<FMT, 64>(a, s, sm, e, ok);
+        } else if (warp < kWarpM) {
             // ============================================================ D: keys -> TMEM
             const int p = 32 * (warp & 3) + lane;
             const uint32_t col0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-            auto record = [&](int i) -> const uint8_t* {
-                const int pos0 = (s.t0 + i) * kTileP;
-                const int32_t page = i < n ? page_of(a, s.pt, pos0) : -1;
-                return (page >= 0 && pos0 + p < s.L) ? k_record<FMT>(a, s, page, pos0 + p) : nullptr;
+            staged = tiles_done + min(n, ST) - 1;            // warp kWarpD: the last tile it copied
+            int stored = -1;                                 // part whose stores are in flight
+            auto publish = [&]() {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.a_full[stored]);
             };
-            const uint8_t* rec = record(0);
-            uint32_t wn[kParts][Words<FMT>::kN];
-#pragma unroll
-            for (int part = 0; part < kParts; ++part) fetch_part<FMT>(rec, part, wn[part]);
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                rec = record(i + 1);
-#pragma unroll
+                const int rc = tiles_done + i;
+                // the stage that tile i - 2 left is refilled
+                if (warp == kWarpD && i >= 2 && i - 2 + ST < n) {
+                    ok = ok && warp_wait(&bar.r_free[(rc - 2) % ST], (uint32_t)(((rc - 2) / ST) & 1), abort);
+                    if (ok) {
+                        stage_tile<FMT>(a, s, sm, i - 2 + ST, rc - 2 + ST);
+                        staged = rc - 2 + ST;
+                    }
+                }
+                ok = ok && warp_wait(&bar.r_full[rc % ST], (uint32_t)((rc / ST) & 1), abort);
+                const uint8_t* rec = sm.rec[rc % ST] + p * Mf<FMT>::kStride;
+#pragma unroll 1
                 for (int part = 0; part < kParts; ++part) {
-                    uint32_t wc[Words<FMT>::kN];
-#pragma unroll
-                    for (int m = 0; m < Words<FMT>::kN; ++m) wc[m] = wn[part][m];
-                    fetch_part<FMT>(rec, part, wn[part]);
+                    uint32_t wc[Words<FMT>::kN], h[kPartCols * OPS];
+                    read_part<FMT>(rec, part, wc);
+                    convert_part<FMT>(wc, cent, h);
+                    if (part == kParts - 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.r_free[rc % ST]);
+                    }
+                    if (stored >= 0) publish();
                     // the previous tile's products have read the operand
                     if (i > 0) ok = ok && warp_wait(&bar.a_free[part], (uint32_t)((tiles_done + i - 1) & 1), abort);
                     tc_fence_after();
-                    store_part<FMT>(wc, cent, col0 + kPartCols * part);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.a_full[part]);
+                    store_part<FMT>(h, col0 + kPartCols * part);
+                    stored = part;
                 }
             }
+            publish();
         } else {
             // ============================================================ M: products of one part
-            const int part = warp - 12;
+            const int part = warp - kWarpM;
             const uint32_t aop = tmem + kPartCols * part;
             for (int i = 0; ok && i < n; ++i) {
                 ok = warp_wait(&bar.a_full[part], (uint32_t)((tiles_done + i) & 1), abort);
                 for (int j = 0; ok && j < s.chunks; ++j) {
                     const int rows = min(kChunkRows, kGroup * s.T - kChunkRows * j);
-                    const uint32_t idesc = make_idesc((rows + 15) & ~15, false, false);
-                    const int c = kParts * (phases + i * s.chunks + j) + part;
-                    // the slot's last accumulators (event c - 3) are read
-                    if (c >= kSlots)
-                        ok = warp_wait(&bar.acc_free[(c - kSlots) % kFreeBars], (uint32_t)(((c - kSlots) / kFreeBars) & 1), abort);
+                    const uint32_t idesc = make_idesc(cols < 64 ? cols : (rows + 31) & ~31, false, false);
+                    const int ph = phases + i * s.chunks + j;
+                    const int c = kParts * ph + part;
+                    // the slot's last accumulators (event c - slots) are read; earlier segments' all are
+                    if (c - slots >= kParts * phases)
+                        ok = warp_wait(&bar.acc_free[(c - slots) % kFreeBars], (uint32_t)(((c - slots) / kFreeBars) & 1), abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + kColAcc + (uint32_t)(c % kSlots) * kSlotCols;
+                    const uint32_t d = tmem + kColAcc + (uint32_t)((c % slots) * G * cols);
                     // dims 64 part ..: two 8-dim cores (256 bytes) per K step, start address in 16-byte units
                     const uint64_t bh = make_desc(smem_u32(sm.q[j][0]) + part * 1024, kQLbo, kQSbo);
                     const uint64_t bl = make_desc(smem_u32(sm.q[j][1]) + part * 1024, kQLbo, kQSbo);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t dg = d + (G == 2 ? kChunkRows * (k / 2) : 0);
+                            const uint32_t dg = d + (G == 2 ? (uint32_t)(cols * (k / 2)) : 0u);
                             const uint32_t first = (G == 2 ? (k & 1) : k) == 0 ? 0u : 1u;
                             mma_ts(dg, aop + 8 * k, bh + 16 * k, idesc, first);
                             mma_ts(dg, aop + 8 * k, bl + 16 * k, idesc, 1u);
@@ -523,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                                 mma_ts(dg, aop + kParts * kPartCols + 8 * k, bl + 16 * k, idesc, 1u);
                             }
                         }
-                        mma_commit(&bar.done[part]);
+                        mma_commit(&bar.done[part][ph % kDoneBars]);
                         if (j == s.chunks - 1) mma_commit(&bar.a_free[part]);
                     }
                     __syncwarp();
@@ -541,14 +696,16 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             while (slot_tiles(a, slot, &ignore) == 0);
         }
     }
-    if (warp >= 12) {
-        if (elect_one()) mma_commit(&bar.drain[warp - 12]);
+    if (warp == kWarpD && *abort)                 // copies in flight land before the CTA leaves
+        for (int k = max(0, staged - ST + 1); k <= staged; ++k) mbar_drain(&bar.r_full[k % ST], (uint32_t)((k / ST) & 1));
+    if (warp >= kWarpM) {
+        if (elect_one()) mma_commit(&bar.drain[warp - kWarpM]);
         __syncwarp();
-        mbar_drain(&bar.drain[warp - 12], 0);
+        mbar_drain(&bar.drain[warp - kWarpM], 0);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kWarpM) tmem_dealloc(tmem, kTmemCols);
     if (*abort && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_TIMEOUT);
 }
 
@@ -559,7 +716,7 @@ cudaError_t launch_mass(const MassArgs& a, int sms, cudaStream_t stream) {
     static std::atomic<bool> attr_set[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    const int smem = (int)sizeof(MassSmem);
+    const int smem = (int)sizeof(MassSmem<FMT>);
     if (!attr_set[dev].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(mass_kernel<TIn, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
