@@ -24,18 +24,17 @@
 // the 3-bit cache at 64 rows) form one slot of a ring, so the epilogue of a part overlaps
 // the products of the next ones.
 //
-// Warp roles (16 warps, 128 registers each):
+// Warp roles (20 warps; registers are moved between the roles with setmaxnreg):
 //   E   warps 0-7    epilogue: thread = position (lane quarter warp & 3), all rows of the
 //                    chunk; the two warps of a lane quarter take every other tile.  Score
 //                    sums start at -lse in log2 units, weights 2^s, rows summed in the
-//                    thread.  Issue slots bound this kernel, so a tile's waits, addresses
-//                    and barrier traffic are paid by one warp per lane quarter.
-//   D   warps 8-11   thread = position: its staged record converted part by part into
-//                    TMEM (the next part is converted while the last one's stores are in
-//                    flight); warp 8 also copies the records of the tiles ahead into
-//                    shared memory (cp.async.bulk, one stage per tile)
-//   M   warps 12-15  one thread each issues the products of one part: an issuing
-//                    thread starts a K = 16 MMA about every 54 cycles, so four issue
+//                    thread.
+//   D   warps 8-15   thread = position: its staged record converted into TMEM, one warp of
+//                    a lane quarter for the even parts and one for the odd ones
+//   M   warps 16-17  one thread each issues the products of the even or the odd parts: an
+//                    issuing thread starts a K = 16 MMA about every 54 cycles, so two issue
+//   P   warps 18-19  copy the records of the tiles ahead into shared memory, one stage per
+//                    tile (one bulk copy; 16-byte cp.async where the stage is padded)
 // TMEM (512 columns): operand (128, turbo5k 256) | ring of accumulator slots (3 for more
 // than 32 rows, 6, or 12 for at most 16).
 //
@@ -59,8 +58,13 @@
 namespace q3kv {
 namespace {
 
-constexpr int kWarps = 16;
-constexpr int kWarpD = 8, kWarpM = 12;      // first warps of the roles
+constexpr int kWarps = 20;
+constexpr int kWarpD = 8, kWarpM = 16, kWarpP = 18;     // first warps of the roles
+constexpr int kIssuers = kWarpP - kWarpM;
+constexpr int kCopyThreads = 32 * (kWarps - kWarpP);
+// registers: launched with 96 a thread, 61,440 in all; the split gives E more out of the others' share
+constexpr int kRegsE = 144, kRegsD = 64, kRegsMP = 64;
+static_assert(256 * (kRegsE + kRegsD) + 128 * kRegsMP <= kWarps * 32 * 96, "register split");
 constexpr int kTurns = 2;                   // E warps of a lane quarter
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileP = 128;                 // positions per tile
@@ -78,6 +82,7 @@ struct Mf {                                 // 3-bit cache
     static constexpr int kRecB = kRecordBytes;
     static constexpr int kStride = kRecordBytes;   // of a staged record in shared memory
     static constexpr int kStages = 5;              // staged tiles (with scales: more than the E warps' turns)
+    static constexpr bool kPadded = false;         // staged record by record
     static constexpr bool kScales = true;
     static constexpr bool kRot = true;
 };
@@ -88,6 +93,7 @@ struct Mf<kFmtFp8> {
     static constexpr int kRecB = kFp8RecordBytes;
     static constexpr int kStride = kFp8RecordBytes + 16;   // 16-byte loads of 8 lanes hit 8 bank groups
     static constexpr int kStages = 2;
+    static constexpr bool kPadded = true;
     static constexpr bool kScales = false;
     static constexpr bool kRot = false;
 };
@@ -98,6 +104,7 @@ struct Mf<kFmtT5k> {
     static constexpr int kRecB = kT5kKRecordBytes;
     static constexpr int kStride = kT5kKRecordBytes;
     static constexpr int kStages = 4;
+    static constexpr bool kPadded = false;
     static constexpr bool kScales = true;
     static constexpr bool kRot = true;
 };
@@ -115,9 +122,9 @@ struct Bars {
     unsigned long long done[kParts][kDoneBars];    // products of a part in pass ph (1 commit), by ph % 4
     unsigned long long a_free[kParts];             // every chunk's products of a part (1 commit): operand read
     unsigned long long acc_free[kFreeBars];        // accumulators of event c read (4 E warps), by c % 12
-    unsigned long long drain[kParts];              // everything an issuer started is done (1 commit)
-    unsigned long long r_full[kMaxStages];         // a tile's records landed (copy bytes)
-    unsigned long long r_free[kMaxStages];         // and were read (4 D warps; with scales, 4 E warps)
+    unsigned long long drain[kIssuers];            // everything an issuer started is done (1 commit)
+    unsigned long long r_full[kMaxStages];         // a tile's records landed (copy bytes, or every P thread)
+    unsigned long long r_free[kMaxStages];         // and were read (8 D warps; with scales, 4 E warps)
 };
 
 template <int FMT>
@@ -171,15 +178,56 @@ struct Segment {
     const int32_t* pt;
 };
 
+// A CTA's way through its share [w, w1) of the tile sequence.
+struct Walk {
+    long long w, w1, base;                   // base: where the slot's tiles begin
+    int slot, tiles;
+    int tiles_done;                          // tiles of earlier segments (phases of a_full, a_free and the stages)
+    int phases;                              // (tile, chunk) passes of earlier segments (phases of done)
+    template <typename Smem>
+    __device__ void start(const Smem& sm) {
+        w = sm.w0;
+        w1 = sm.w1;
+        base = sm.first_base;
+        slot = sm.first_slot;
+        tiles_done = phases = tiles = 0;
+    }
+    __device__ bool next(const MassArgs& a, Segment& s) {
+        if (w >= w1) return false;
+        bool ignore = false;
+        tiles = slot_tiles(a, slot, &ignore);
+        while (tiles == 0 || w >= base + (long long)tiles * a.num_kv_heads) {   // the next slot with tiles
+            base += (long long)tiles * a.num_kv_heads;
+            tiles = slot_tiles(a, ++slot, &ignore);
+        }
+        const long long off = w - base;
+        s.slot = slot;
+        s.g = (int)(off / tiles);
+        s.t0 = (int)(off - (long long)s.g * tiles);
+        s.t1 = (int)min((long long)tiles, s.t0 + (w1 - w));
+        s.T = a.n_q[slot];
+        s.L = a.ctx_len[slot];
+        s.chunks = (kGroup * s.T + kChunkRows - 1) / kChunkRows;
+        s.pt = a.page_table + (int64_t)slot * a.max_pages_per_slot;
+        return true;
+    }
+    __device__ void advance(const Segment& s) {
+        const int n = s.t1 - s.t0;
+        w += n;
+        tiles_done += n;
+        phases += n * s.chunks;
+    }
+};
+
 // Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e), split
-// into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  One row per warp.
+// into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  One row per E or D warp.
 template <typename TIn, int FMT>
 __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = kGroup * s.T;
     const int Hq = a.num_kv_heads * kGroup;
     const int64_t q_base = a.q_offsets[s.slot];
-    for (int r = warp; r < s.chunks * kChunkRows; r += kWarps) {
+    for (int r = warp; r < s.chunks * kChunkRows; r += kWarpM) {
         const int chunk = r / kChunkRows, rr = r % kChunkRows;
         const int64_t row = (q_base + r / kGroup) * Hq + s.g * kGroup + r % kGroup;
         float y[8];
@@ -259,59 +307,65 @@ __device__ __forceinline__ void read_part(const uint8_t* rec, int q, uint32_t (&
     }
 }
 
-// Copies the records of tile i of the segment into its stage (one warp; the whole
-// warp calls).  A tile's 128 records are contiguous; padded stages take them one by
-// one.  A page out of range completes the phase without data: its scores are unused.
+// Copies the records of tile i of the segment into its stage.  A tile's 128 records
+// are contiguous: one bulk copy by one thread; a padded stage takes 16 bytes a
+// thread and step (both P warps).  A page out of range completes the phase without
+// data: its scores are unused.
 template <int FMT>
 __device__ __forceinline__ void stage_tile(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, int i, int counter) {
-    const int lane = threadIdx.x & 31;
+    const int t = threadIdx.x - 32 * kWarpP;
     const int st = counter % Mf<FMT>::kStages;
     const int pos0 = (s.t0 + i) * kTileP;
     const int32_t page = page_of(a, s.pt, pos0);
-    if (page < 0) {
-        if (lane == 0) {
-            if (a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+    if (page < 0 && t == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+    if (Mf<FMT>::kPadded) {
+        if (page >= 0) {
+            const uint8_t* src = k_record<FMT>(a, s, page, pos0);
+            constexpr int kVecs = Mf<FMT>::kRecB / 16;
+#pragma unroll 4
+            for (int k = 0; k < kTileP * kVecs / kCopyThreads; ++k) {
+                const int v = kCopyThreads * k + t;
+                cp_async16(sm.rec[st] + (v / kVecs) * Mf<FMT>::kStride + (v % kVecs) * 16, src + (size_t)v * 16);
+            }
+        }
+        cp_async_mbar_arrive(&sm.bar.r_full[st]);
+    } else if (t == 0) {
+        if (page >= 0) {
+            fence_proxy_async();
+            mbar_arrive_expect_tx(&sm.bar.r_full[st], (uint32_t)(kTileP * Mf<FMT>::kRecB));
+            bulk_g2s(sm.rec[st], k_record<FMT>(a, s, page, pos0), (uint32_t)(kTileP * Mf<FMT>::kRecB), &sm.bar.r_full[st]);
+        } else {
             mbar_arrive(&sm.bar.r_full[st]);
         }
-        return;
     }
-    const uint8_t* src = k_record<FMT>(a, s, page, pos0);
-    fence_proxy_async();
-    if (lane == 0) mbar_arrive_expect_tx(&sm.bar.r_full[st], (uint32_t)(kTileP * Mf<FMT>::kRecB));
-    __syncwarp();
-    if (Mf<FMT>::kStride == Mf<FMT>::kRecB) {
-        if (lane == 0) bulk_g2s(sm.rec[st], src, (uint32_t)(kTileP * Mf<FMT>::kRecB), &sm.bar.r_full[st]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kTileP / 32; ++k) {
-            const int r = 32 * k + lane;
-            bulk_g2s(sm.rec[st] + r * Mf<FMT>::kStride, src + r * Mf<FMT>::kRecB, (uint32_t)Mf<FMT>::kRecB, &sm.bar.r_full[st]);
-        }
-    }
-    __syncwarp();
 }
 
-// 64 dims of this thread's position as fp16 pairs, K order (turbo5k: hi, then lo).
+// Half a part (32 dims) of this thread's position as fp16 pairs in K order, to the
+// TMEM columns at col (turbo5k: hi there, lo one operand further).
 template <int FMT>
-__device__ __forceinline__ void convert_part(const uint32_t (&w)[Words<FMT>::kN], float cent,
-                                             uint32_t (&h)[kPartCols * Mf<FMT>::kOps]) {
+__device__ __forceinline__ void store_half(const uint32_t (&w)[Words<FMT>::kN], int b, float cent, uint32_t col) {
+    uint32_t h[16];
     if constexpr (FMT == kFmtFp8) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) e4m3x4_to_f16(w[k], h[2 * k], h[2 * k + 1]);
+        for (int k = 0; k < 8; ++k) e4m3x4_to_f16(w[8 * b + k], h[2 * k], h[2 * k + 1]);
+        tmem_st16(col, h);
     } else if constexpr (FMT == kFmtT5k) {
         // lane l holds centroid l: a code's value by shuffle, split into fp16 hi / lo
+        uint32_t lo[16];
 #pragma unroll
-        for (int m = 0; m < 32; ++m) {                         // pair of the part
-            const uint32_t nw = w[m / 4], top = w[8 + m / 16];
-            const uint32_t c0 = ((nw >> (8 * (m % 4))) & 0xFu) | (((top >> (2 * (m % 16))) & 1u) << 4);
-            const uint32_t c1 = ((nw >> (8 * (m % 4) + 4)) & 0xFu) | (((top >> (2 * (m % 16) + 1)) & 1u) << 4);
+        for (int m = 0; m < 16; ++m) {
+            const uint32_t nw = w[4 * b + m / 4], top = w[8 + b];
+            const uint32_t c0 = ((nw >> (8 * (m % 4))) & 0xFu) | (((top >> (2 * m)) & 1u) << 4);
+            const uint32_t c1 = ((nw >> (8 * (m % 4) + 4)) & 0xFu) | (((top >> (2 * m + 1)) & 1u) << 4);
             const float v0 = __shfl_sync(0xffffffffu, cent, (int)c0);
             const float v1 = __shfl_sync(0xffffffffu, cent, (int)c1);
             const __half2 h2 = __floats2half2_rn(v0, v1);
             const float2 hf = __half22float2(h2);
             h[m] = as_u32(h2);
-            h[kPartCols + m] = as_u32(__floats2half2_rn(v0 - hf.x, v1 - hf.y));
+            lo[m] = as_u32(__floats2half2_rn(v0 - hf.x, v1 - hf.y));
         }
+        tmem_st16(col, h);
+        tmem_st16(col + kParts * kPartCols, lo);
     } else {
         // A code pair at bits (o, o + 16) of a word, under the exponent of 2^(10 - o), is
         // 2^(10 - o) + c: for o = 3 and 6 an and-or and one exact subtraction give c - 3.5.
@@ -321,28 +375,17 @@ __device__ __forceinline__ void convert_part(const uint32_t (&w)[Words<FMT>::kN]
         const __half2 m6 = __half2half2(__ushort_as_half((unsigned short)0xCCE0u));   // -19.5
         const __half2 m12 = __half2half2(__ushort_as_half((unsigned short)0xCA00u));  // -12
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                const uint32_t u = w[3 * b + k], l = u << 3, r = u >> 6;
-                h[16 * b + 5 * k] = as_u32(__hadd2(as_h2((l & 0x00380038u) | 0x58005800u), m3));
-                h[16 * b + 5 * k + 1] = as_u32(__hadd2(as_h2((u & 0x00380038u) | 0x58005800u), m3));
-                h[16 * b + 5 * k + 2] = as_u32(__hadd2(as_h2((u & 0x01C001C0u) | 0x4C004C00u), m6));
-                h[16 * b + 5 * k + 3] = as_u32(__hadd2(as_h2((r & 0x00380038u) | 0x58005800u), m3));
-                h[16 * b + 5 * k + 4] = as_u32(__hadd2(as_h2((r & 0x01C001C0u) | 0x4C004C00u), m6));
-            }
-            // (8.5 + c) - 12, exact
-            h[16 * b + 15] = as_u32(__hadd2(as_h2(code_pair_last(w[3 * b], w[3 * b + 1], w[3 * b + 2])), m12));
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t u = w[3 * b + k], l = u << 3, r = u >> 6;
+            h[5 * k] = as_u32(__hadd2(as_h2((l & 0x00380038u) | 0x58005800u), m3));
+            h[5 * k + 1] = as_u32(__hadd2(as_h2((u & 0x00380038u) | 0x58005800u), m3));
+            h[5 * k + 2] = as_u32(__hadd2(as_h2((u & 0x01C001C0u) | 0x4C004C00u), m6));
+            h[5 * k + 3] = as_u32(__hadd2(as_h2((r & 0x00380038u) | 0x58005800u), m3));
+            h[5 * k + 4] = as_u32(__hadd2(as_h2((r & 0x01C001C0u) | 0x4C004C00u), m6));
         }
-    }
-}
-
-template <int FMT>
-__device__ __forceinline__ void store_part(const uint32_t (&h)[kPartCols * Mf<FMT>::kOps], uint32_t col) {
-#pragma unroll
-    for (int o = 0; o < Mf<FMT>::kOps; ++o) {
-        tmem_st16(col + kParts * kPartCols * o, *reinterpret_cast<const uint32_t(*)[16]>(&h[kPartCols * o]));
-        tmem_st16(col + kParts * kPartCols * o + 16, *reinterpret_cast<const uint32_t(*)[16]>(&h[kPartCols * o + 16]));
+        // (8.5 + c) - 12, exact
+        h[15] = as_u32(__hadd2(as_h2(code_pair_last(w[3 * b], w[3 * b + 1], w[3 * b + 2])), m12));
+        tmem_st16(col, h);
     }
 }
 
@@ -399,7 +442,7 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
         if (Mf<FMT>::kScales) {
             // this position's scales from the staged record
             const int rc = e.tiles_done + i;
-            ok = ok && warp_wait(&bar.r_full[rc % ST], (uint32_t)((rc / ST) & 1), e.abort);
+            ok = ok && mbar_wait_fast(&bar.r_full[rc % ST], (uint32_t)((rc / ST) & 1), e.abort);
             const uint8_t* rec = sm.rec[rc % ST] + p * Mf<FMT>::kStride;
             if (FMT == kFmtQ3) sc = *reinterpret_cast<const uint4*>(rec + 96);
             if (FMT == kFmtT5k) sc.x = *reinterpret_cast<const uint32_t*>(rec + 160);
@@ -421,7 +464,8 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
 #pragma unroll
             for (int part = 0; part < kParts; ++part) {
                 const int c = kParts * ph + part;
-                ok = ok && warp_wait(&bar.done[part][ph % kDoneBars], (uint32_t)((ph / kDoneBars) & 1), e.abort);
+                ok = ok && mbar_wait_fast(&bar.done[part][ph % kDoneBars], (uint32_t)((ph / kDoneBars) & 1), e.abort);
+                __syncwarp();
                 tc_fence_after();
                 const uint32_t col = e.tmem_acc + (uint32_t)((c % SLOTS) * G * COLS);
                 if (COLS <= 32) {
@@ -514,12 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             mbar_init(&bar.a_full[q], 4);
             for (int e = 0; e < kDoneBars; ++e) mbar_init(&bar.done[q][e], 1);
             mbar_init(&bar.a_free[q], 1);
-            mbar_init(&bar.drain[q], 1);
         }
         for (int e = 0; e < kFreeBars; ++e) mbar_init(&bar.acc_free[e], 4);
+        for (int e = 0; e < kIssuers; ++e) mbar_init(&bar.drain[e], 1);
         for (int e = 0; e < ST; ++e) {
-            mbar_init(&bar.r_full[e], 1);
-            mbar_init(&bar.r_free[e], Mf<FMT>::kScales ? 8 : 4);
+            mbar_init(&bar.r_full[e], Mf<FMT>::kPadded ? kCopyThreads : 1);
+            mbar_init(&bar.r_free[e], Mf<FMT>::kScales ? 12 : 8);
         }
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -564,147 +608,166 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    const long long w1 = sm.w1;
-    long long w = sm.w0, base = sm.first_base;
-    int slot = sm.first_slot;
-    int tiles_done = 0;                      // tiles of earlier segments (a_full and a_free phases)
-    int phases = 0;                          // (tile, chunk) passes of earlier segments (done phases)
-    int staged = -1;
+
+    // Every role walks the CTA's segments on its own; the block meets when a segment's
+    // queries are in place and when it is done.
+    Walk wk;
+    wk.start(sm);
     bool ok = true;
-    const float cent = FMT == kFmtT5k ? a.t5k.c[lane] : 0.0f;
-
-    while (w < w1) {
+    if (warp < kWarpD) {
+        // ================================================================ E: epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsE));
         Segment s;
-        bool ignore = false;
-        const int tiles = slot_tiles(a, slot, &ignore);
-        const long long off = w - base;
-        s.slot = slot;
-        s.g = (int)(off / tiles);
-        s.t0 = (int)(off - (long long)s.g * tiles);
-        s.t1 = (int)min((long long)tiles, s.t0 + (w1 - w));
-        s.T = a.n_q[slot];
-        s.L = a.ctx_len[slot];
-        s.chunks = (kGroup * s.T + kChunkRows - 1) / kChunkRows;
-        s.pt = a.page_table + (int64_t)slot * a.max_pages_per_slot;
-        const int n = s.t1 - s.t0;
-        if (warp == kWarpD)                  // the first tiles' records are in flight while the queries are prepared
-            for (int k = 0; k < min(n, ST); ++k) stage_tile<FMT>(a, s, sm, k, tiles_done + k);
-        load_queries<TIn, FMT>(a, s, sm);
-        __syncthreads();
-        const int Nctx = s.L - s.T;
-
-        // accumulator columns per group (query rows of a pass, rounded up) and slots of the ring
-        const int cols = kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : 64);
-        const int slots = kAccCols / cols;
-
-        if (warp < kWarpD) {
-            // ============================================================ E: epilogue
-            const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColAcc, tiles_done, phases, n, abort};
-            if (cols == 16) ok = epilogue<FMT, 16>(a, s, sm, e, ok);
-            else if (cols == 32) ok = epilogue<FMT, 32>(a, s, sm, e, ok);
+        while (wk.next(a, s)) {
+            load_queries<TIn, FMT>(a, s, sm);
+            named_sync(0, kThreads);
+            const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColAcc, wk.tiles_done, wk.phases, s.t1 - s.t0, abort};
+            const int rows = kGroup * s.T;
+            if (rows <= 16) ok = epilogue<FMT, 16>(a, s, sm, e, ok);
+            else if (rows <= 32) ok = epilogue<FMT, 32>(a, s, sm, e, ok);
             else ok = epilogue<FMT, 64>(a, s, sm, e, ok);
-        } else if (warp < kWarpM) {
-            // ============================================================ D: keys -> TMEM
-            const int p = 32 * (warp & 3) + lane;
-            const uint32_t col0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-            staged = tiles_done + min(n, ST) - 1;            // warp kWarpD: the last tile it copied
-            int stored = -1;                                 // part whose stores are in flight
-            auto publish = [&]() {
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.a_full[stored]);
-            };
+            named_sync(0, kThreads);
+            if (*abort) break;
+            wk.advance(s);
+        }
+    } else if (warp < kWarpM) {
+        // ================================================================ D: keys -> TMEM
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsD));
+        const float cent = FMT == kFmtT5k ? a.t5k.c[lane] : 0.0f;
+        const int odd = (warp - kWarpD) >> 2;                // this warp's parts: odd and odd + 2
+        const int p = 32 * (warp & 3) + lane;
+        const uint32_t col0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        Segment s;
+        while (wk.next(a, s)) {
+            load_queries<TIn, FMT>(a, s, sm);
+            named_sync(0, kThreads);
+            const int n = s.t1 - s.t0;
+            int rs = wk.tiles_done % ST;                     // stage and its phase
+            uint32_t rp = (uint32_t)(wk.tiles_done / ST) & 1u;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
-                const int rc = tiles_done + i;
-                // the stage that tile i - 2 left is refilled
-                if (warp == kWarpD && i >= 2 && i - 2 + ST < n) {
-                    ok = ok && warp_wait(&bar.r_free[(rc - 2) % ST], (uint32_t)(((rc - 2) / ST) & 1), abort);
-                    if (ok) {
-                        stage_tile<FMT>(a, s, sm, i - 2 + ST, rc - 2 + ST);
-                        staged = rc - 2 + ST;
-                    }
-                }
-                ok = ok && warp_wait(&bar.r_full[rc % ST], (uint32_t)((rc / ST) & 1), abort);
-                const uint8_t* rec = sm.rec[rc % ST] + p * Mf<FMT>::kStride;
+                ok = ok && mbar_wait_fast(&bar.r_full[rs], rp, abort);
+                const uint8_t* rec = sm.rec[rs] + p * Mf<FMT>::kStride;
 #pragma unroll 1
-                for (int part = 0; part < kParts; ++part) {
-                    uint32_t wc[Words<FMT>::kN], h[kPartCols * OPS];
+                for (int part = odd; part < kParts; part += 2) {
+                    uint32_t wc[Words<FMT>::kN];
                     read_part<FMT>(rec, part, wc);
-                    convert_part<FMT>(wc, cent, h);
-                    if (part == kParts - 1) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.r_free[rc % ST]);
-                    }
-                    if (stored >= 0) publish();
                     // the previous tile's products have read the operand
-                    if (i > 0) ok = ok && warp_wait(&bar.a_free[part], (uint32_t)((tiles_done + i - 1) & 1), abort);
+                    if (i > 0) ok = ok && mbar_wait_fast(&bar.a_free[part], (uint32_t)((wk.tiles_done + i - 1) & 1), abort);
+                    __syncwarp();
                     tc_fence_after();
-                    store_part<FMT>(h, col0 + kPartCols * part);
-                    stored = part;
+                    store_half<FMT>(wc, 0, cent, col0 + kPartCols * part);
+                    store_half<FMT>(wc, 1, cent, col0 + kPartCols * part + 16);
+                    if (part >= kParts - 2 && lane == 0) mbar_arrive(&bar.r_free[rs]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.a_full[part]);
+                }
+                if (++rs == ST) {
+                    rs = 0;
+                    rp ^= 1u;
                 }
             }
-            publish();
-        } else {
-            // ============================================================ M: products of one part
-            const int part = warp - kWarpM;
-            const uint32_t aop = tmem + kPartCols * part;
+            named_sync(0, kThreads);
+            if (*abort) break;
+            wk.advance(s);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMP));   // one warpgroup: M and P together
+        if (warp < kWarpP) {
+        // ================================================================ M: products of one part
+        const int first_part = warp - kWarpM;                // this issuer's parts: every kIssuers-th
+        Segment s;
+        while (wk.next(a, s)) {
+            named_sync(0, kThreads);
+            const int n = s.t1 - s.t0;
+            // accumulator columns per group (query rows of a pass, rounded up) and slots of the ring
+            const int cols = kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : 64);
+            const int slots = kAccCols / cols;
+            const int c_first = kParts * wk.phases;
+#pragma unroll 1
             for (int i = 0; ok && i < n; ++i) {
-                ok = warp_wait(&bar.a_full[part], (uint32_t)((tiles_done + i) & 1), abort);
+#pragma unroll 1
                 for (int j = 0; ok && j < s.chunks; ++j) {
                     const int rows = min(kChunkRows, kGroup * s.T - kChunkRows * j);
                     const uint32_t idesc = make_idesc(cols < 64 ? cols : (rows + 31) & ~31, false, false);
-                    const int ph = phases + i * s.chunks + j;
-                    const int c = kParts * ph + part;
-                    // the slot's last accumulators (event c - slots) are read; earlier segments' all are
-                    if (c - slots >= kParts * phases)
-                        ok = warp_wait(&bar.acc_free[(c - slots) % kFreeBars], (uint32_t)(((c - slots) / kFreeBars) & 1), abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t d = tmem + kColAcc + (uint32_t)((c % slots) * G * cols);
-                    // dims 64 part ..: two 8-dim cores (256 bytes) per K step, start address in 16-byte units
-                    const uint64_t bh = make_desc(smem_u32(sm.q[j][0]) + part * 1024, kQLbo, kQSbo);
-                    const uint64_t bl = make_desc(smem_u32(sm.q[j][1]) + part * 1024, kQLbo, kQSbo);
-                    if (elect_one()) {
+                    const int ph = wk.phases + i * s.chunks + j;
+#pragma unroll 1
+                    for (int part = first_part; ok && part < kParts; part += kIssuers) {
+                        const int c = kParts * ph + part;
+                        if (j == 0) ok = mbar_wait_all(&bar.a_full[part], (uint32_t)((wk.tiles_done + i) & 1), abort);
+                        // the slot's last accumulators (event c - slots) are read; earlier segments' all are
+                        if (ok && c - slots >= c_first)
+                            ok = mbar_wait_all(&bar.acc_free[(c - slots) % kFreeBars], (uint32_t)(((c - slots) / kFreeBars) & 1), abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + kColAcc + (uint32_t)((c % slots) * G * cols);
+                        const uint32_t aop = tmem + kPartCols * part;
+                        // dims 64 part ..: two 8-dim cores (256 bytes) per K step, start address in 16-byte units
+                        const uint64_t bh = make_desc(smem_u32(sm.q[j][0]) + part * 1024, kQLbo, kQSbo);
+                        const uint64_t bl = make_desc(smem_u32(sm.q[j][1]) + part * 1024, kQLbo, kQSbo);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t dg = d + (G == 2 ? (uint32_t)(cols * (k / 2)) : 0u);
-                            const uint32_t first = (G == 2 ? (k & 1) : k) == 0 ? 0u : 1u;
-                            mma_ts(dg, aop + 8 * k, bh + 16 * k, idesc, first);
-                            mma_ts(dg, aop + 8 * k, bl + 16 * k, idesc, 1u);
-                            if (OPS == 2) {
-                                mma_ts(dg, aop + kParts * kPartCols + 8 * k, bh + 16 * k, idesc, 1u);
-                                mma_ts(dg, aop + kParts * kPartCols + 8 * k, bl + 16 * k, idesc, 1u);
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t dg = d + (G == 2 ? (uint32_t)(cols * (k / 2)) : 0u);
+                                const uint32_t first = (G == 2 ? (k & 1) : k) == 0 ? 0u : 1u;
+                                mma_ts(dg, aop + 8 * k, bh + 16 * k, idesc, first);
+                                mma_ts(dg, aop + 8 * k, bl + 16 * k, idesc, 1u);
+                                if (OPS == 2) {
+                                    mma_ts(dg, aop + kParts * kPartCols + 8 * k, bh + 16 * k, idesc, 1u);
+                                    mma_ts(dg, aop + kParts * kPartCols + 8 * k, bl + 16 * k, idesc, 1u);
+                                }
                             }
+                            mma_commit(&bar.done[part][ph % kDoneBars]);
+                            if (j == s.chunks - 1) mma_commit(&bar.a_free[part]);
                         }
-                        mma_commit(&bar.done[part][ph % kDoneBars]);
-                        if (j == s.chunks - 1) mma_commit(&bar.a_free[part]);
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
+            named_sync(0, kThreads);
+            if (*abort) break;
+            wk.advance(s);
         }
-        tiles_done += n;
-        phases += n * s.chunks;
-        __syncthreads();                     // queries and barriers are free for the next segment
-        if (*abort) break;
-        w += n;
-        if (w >= base + (long long)tiles * a.num_kv_heads && w < w1) {
-            base += (long long)tiles * a.num_kv_heads;
-            do ++slot;
-            while (slot_tiles(a, slot, &ignore) == 0);
-        }
-    }
-    if (warp == kWarpD && *abort)                 // copies in flight land before the CTA leaves
-        for (int k = max(0, staged - ST + 1); k <= staged; ++k) mbar_drain(&bar.r_full[k % ST], (uint32_t)((k / ST) & 1));
-    if (warp >= kWarpM) {
-        if (elect_one()) mma_commit(&bar.drain[warp - kWarpM]);
+        if (elect_one()) mma_commit(&bar.drain[first_part]);
         __syncwarp();
-        mbar_drain(&bar.drain[warp - kWarpM], 0);
+        mbar_drain(&bar.drain[first_part], 0);
+        } else {
+        // ================================================================ P: records -> shared memory
+        Segment s;
+        while (wk.next(a, s)) {
+            const int n = s.t1 - s.t0;
+            // the first tiles' records are in flight while the queries are prepared: their stages are free
+            const int pre = min(n, ST);
+            int staged = wk.tiles_done + pre;                // next tile to copy
+            if (Mf<FMT>::kPadded || warp == kWarpP)
+                for (int k = 0; k < pre; ++k) stage_tile<FMT>(a, s, sm, k, wk.tiles_done + k);
+            named_sync(0, kThreads);
+            if (Mf<FMT>::kPadded || warp == kWarpP) {
+#pragma unroll 1
+                for (int i = pre; i < n; ++i) {
+                    const int rc = wk.tiles_done + i;
+                    ok = ok && mbar_wait_all(&bar.r_free[rc % ST], (uint32_t)((rc / ST - 1) & 1), abort);
+                    if (!ok) break;
+                    stage_tile<FMT>(a, s, sm, i, rc);
+                    staged = rc + 1;
+                }
+            }
+            named_sync(0, kThreads);
+            if (*abort) {
+                // copies in flight land before the CTA leaves
+                if (Mf<FMT>::kPadded) asm volatile("cp.async.wait_all;" ::: "memory");
+                else if (warp == kWarpP)
+                    for (int k = max(wk.tiles_done, staged - ST); k < staged; ++k) mbar_drain(&bar.r_full[k % ST], (uint32_t)((k / ST) & 1));
+                break;
+            }
+            wk.advance(s);
+        }
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    named_sync(0, kThreads);
     if (warp == kWarpM) tmem_dealloc(tmem, kTmemCols);
     if (*abort && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_TIMEOUT);
 }

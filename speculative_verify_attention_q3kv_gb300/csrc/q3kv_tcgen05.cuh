@@ -67,8 +67,31 @@ static __device__ bool mbar_wait(unsigned long long* bar, uint32_t parity, volat
     return true;
 }
 
+// The rest of a wait that was not over at once.
+static __device__ __forceinline__ bool mbar_wait_slow(unsigned long long* bar, uint32_t parity, volatile int* abort) {
+    if (*abort) return false;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (clock64() - t0 > kWaitCycles) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// mbar_wait with the test inline.
+__device__ __forceinline__ bool mbar_wait_fast(unsigned long long* bar, uint32_t parity, volatile int* abort) {
+    return mbar_test_wait(bar, parity) || mbar_wait_slow(bar, parity, abort);
+}
+
+// All lanes wait and agree on the outcome.
+__device__ __forceinline__ bool mbar_wait_all(unsigned long long* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_fast(bar, parity, abort));
+}
+
 // Bounded wait used while draining after an abort.
-static __device__ void mbar_drain(unsigned long long* bar, uint32_t parity) {
+static __device__ __forceinline__ void mbar_drain(unsigned long long* bar, uint32_t parity) {
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity) && clock64() - t0 <= kWaitCycles) {
     }
@@ -85,6 +108,15 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
                      smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
+}
+
+// 16 bytes global -> shared; and an arrival on bar (counted in its phase) once this
+// thread's copies so far have landed.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_mbar_arrive(unsigned long long* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // One lane of the (converged) warp, chosen by the hardware.
