@@ -24,16 +24,16 @@
 // the 3-bit cache at 64 rows) form one slot of a ring, so the epilogue of a part overlaps
 // the products of the next ones.
 //
-// Warp roles (20 warps; registers are moved between the roles with setmaxnreg):
+// Warp roles (24 warps; registers are moved between the roles with setmaxnreg):
 //   E   warps 0-7    epilogue: thread = position (lane quarter warp & 3), all rows of the
 //                    chunk; the two warps of a lane quarter take every other tile.  Score
 //                    sums start at -lse in log2 units, weights 2^s, rows summed in the
 //                    thread.
 //   D   warps 8-15   thread = position: its staged record converted into TMEM, one warp of
 //                    a lane quarter for the even parts and one for the odd ones
-//   M   warps 16-17  one thread each issues the products of the even or the odd parts: an
-//                    issuing thread starts a K = 16 MMA about every 54 cycles, so two issue
-//   P   warps 18-19  copy the records of the tiles ahead into shared memory, one stage per
+//   M   warps 16-19  one thread each issues the products of one part: an issuing thread
+//                    starts a K = 16 MMA about every 45 cycles, so four issue
+//   P   warps 20-23  copy the records of the tiles ahead into shared memory, one stage per
 //                    tile (one bulk copy; 16-byte cp.async where the stage is padded)
 // TMEM (512 columns): operand (128, turbo5k 256) | ring of accumulator slots (3 for more
 // than 32 rows, 6, or 12 for at most 16).
@@ -58,13 +58,13 @@
 namespace q3kv {
 namespace {
 
-constexpr int kWarps = 20;
-constexpr int kWarpD = 8, kWarpM = 16, kWarpP = 18;     // first warps of the roles
+constexpr int kWarps = 24;
+constexpr int kWarpD = 8, kWarpM = 16, kWarpP = 20;     // first warps of the roles
 constexpr int kIssuers = kWarpP - kWarpM;
 constexpr int kCopyThreads = 32 * (kWarps - kWarpP);
-// registers: launched with 96 a thread, 61,440 in all; the split gives E more out of the others' share
-constexpr int kRegsE = 144, kRegsD = 64, kRegsMP = 64;
-static_assert(256 * (kRegsE + kRegsD) + 128 * kRegsMP <= kWarps * 32 * 96, "register split");
+// registers: launched with 80 a thread, 61,440 in all; the split gives E more out of the others' share
+constexpr int kRegsE = 144, kRegsD = 56, kRegsMP = 40;
+static_assert(256 * (kRegsE + kRegsD + kRegsMP) <= kWarps * 32 * 80, "register split");
 constexpr int kTurns = 2;                   // E warps of a lane quarter
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileP = 128;                 // positions per tile
@@ -127,6 +127,20 @@ struct Bars {
     unsigned long long r_free[kMaxStages];         // and were read (8 D warps; with scales, 4 E warps)
 };
 
+// One segment: tiles [t0, t0 + n) of a (slot, kv head) pair; n = 0: no more work.
+struct Segment {
+    int slot, g, t0, n;
+    int T, L, chunks;
+    int tiles_done;                          // tiles of earlier segments (phases of a_full, a_free and the stages)
+    int phases;                              // (tile, chunk) passes of earlier segments (phases of done)
+};
+
+// A CTA's way through its share [w, w1) of the tile sequence; base: where the slot's tiles begin.
+struct Walk {
+    long long w, w1, base;
+    int slot, tiles_done, phases;
+};
+
 template <int FMT>
 struct __align__(16) MassSmem {
     __half q[kMaxChunks][2][kChunkRows * kHeadDim];   // [chunk][hi | lo], B operand
@@ -135,8 +149,8 @@ struct __align__(16) MassSmem {
     Bars bar;
     uint32_t tmem_base;
     int abort;
-    int first_slot;
-    long long first_base, w0, w1;
+    Walk walk;
+    Segment seg[2];
 };
 
 // Tiles of a slot's kv head; 0 for a slot with nothing to do.
@@ -171,53 +185,33 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigne
     return r;
 }
 
-// One segment: tiles [t0, t1) of a (slot, kv head) pair.
-struct Segment {
-    int slot, g, t0, t1;
-    int T, L, chunks;
-    const int32_t* pt;
-};
-
-// A CTA's way through its share [w, w1) of the tile sequence.
-struct Walk {
-    long long w, w1, base;                   // base: where the slot's tiles begin
-    int slot, tiles;
-    int tiles_done;                          // tiles of earlier segments (phases of a_full, a_free and the stages)
-    int phases;                              // (tile, chunk) passes of earlier segments (phases of done)
-    template <typename Smem>
-    __device__ void start(const Smem& sm) {
-        w = sm.w0;
-        w1 = sm.w1;
-        base = sm.first_base;
-        slot = sm.first_slot;
-        tiles_done = phases = tiles = 0;
+// The segment at the walk's position, for every role to read (one thread calls).
+template <int FMT>
+__device__ void next_segment(const MassArgs& a, MassSmem<FMT>& sm, int k) {
+    Segment& s = sm.seg[k & 1];
+    s.n = 0;
+    Walk& wk = sm.walk;
+    if (wk.w >= wk.w1) return;
+    bool ignore = false;
+    int tiles = slot_tiles(a, wk.slot, &ignore);
+    while (tiles == 0 || wk.w >= wk.base + (long long)tiles * a.num_kv_heads) {   // the next slot with tiles
+        wk.base += (long long)tiles * a.num_kv_heads;
+        tiles = slot_tiles(a, ++wk.slot, &ignore);
     }
-    __device__ bool next(const MassArgs& a, Segment& s) {
-        if (w >= w1) return false;
-        bool ignore = false;
-        tiles = slot_tiles(a, slot, &ignore);
-        while (tiles == 0 || w >= base + (long long)tiles * a.num_kv_heads) {   // the next slot with tiles
-            base += (long long)tiles * a.num_kv_heads;
-            tiles = slot_tiles(a, ++slot, &ignore);
-        }
-        const long long off = w - base;
-        s.slot = slot;
-        s.g = (int)(off / tiles);
-        s.t0 = (int)(off - (long long)s.g * tiles);
-        s.t1 = (int)min((long long)tiles, s.t0 + (w1 - w));
-        s.T = a.n_q[slot];
-        s.L = a.ctx_len[slot];
-        s.chunks = (kGroup * s.T + kChunkRows - 1) / kChunkRows;
-        s.pt = a.page_table + (int64_t)slot * a.max_pages_per_slot;
-        return true;
-    }
-    __device__ void advance(const Segment& s) {
-        const int n = s.t1 - s.t0;
-        w += n;
-        tiles_done += n;
-        phases += n * s.chunks;
-    }
-};
+    const long long off = wk.w - wk.base;
+    s.slot = wk.slot;
+    s.g = (int)(off / tiles);
+    s.t0 = (int)(off - (long long)s.g * tiles);
+    s.n = (int)min((long long)(tiles - s.t0), wk.w1 - wk.w);
+    s.T = a.n_q[wk.slot];
+    s.L = a.ctx_len[wk.slot];
+    s.chunks = (kGroup * s.T + kChunkRows - 1) / kChunkRows;
+    s.tiles_done = wk.tiles_done;
+    s.phases = wk.phases;
+    wk.w += s.n;
+    wk.tiles_done += s.n;
+    wk.phases += s.n * s.chunks;
+}
 
 // Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e), split
 // into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  One row per E or D warp.
@@ -263,8 +257,8 @@ __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>&
     fence_proxy_async();
 }
 
-__device__ __forceinline__ int32_t page_of(const MassArgs& a, const int32_t* pt, int pos0) {
-    const int32_t page = pt[pos0 / kPageSize];
+__device__ __forceinline__ int32_t page_of(const MassArgs& a, const Segment& s, int pos0) {
+    const int32_t page = a.page_table[(int64_t)s.slot * a.max_pages_per_slot + pos0 / kPageSize];
     return (page >= 0 && page < a.num_pages) ? page : -1;
 }
 
@@ -309,14 +303,14 @@ __device__ __forceinline__ void read_part(const uint8_t* rec, int q, uint32_t (&
 
 // Copies the records of tile i of the segment into its stage.  A tile's 128 records
 // are contiguous: one bulk copy by one thread; a padded stage takes 16 bytes a
-// thread and step (both P warps).  A page out of range completes the phase without
+// thread and step (all P warps).  A page out of range completes the phase without
 // data: its scores are unused.
 template <int FMT>
 __device__ __forceinline__ void stage_tile(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, int i, int counter) {
     const int t = threadIdx.x - 32 * kWarpP;
     const int st = counter % Mf<FMT>::kStages;
     const int pos0 = (s.t0 + i) * kTileP;
-    const int32_t page = page_of(a, s.pt, pos0);
+    const int32_t page = page_of(a, s, pos0);
     if (page < 0 && t == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
     if (Mf<FMT>::kPadded) {
         if (page >= 0) {
@@ -392,7 +386,6 @@ __device__ __forceinline__ void store_half(const uint32_t (&w)[Words<FMT>::kN], 
 // What the epilogue of a segment needs besides the segment.
 struct EpiState {
     uint32_t tmem_acc;           // first accumulator column, this warp's lanes
-    int tiles_done, phases, n;
     volatile int* abort;
 };
 
@@ -422,14 +415,14 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
     // old masses and page checks of the next tiles, ahead of their use
     auto old_of = [&](int i) {
         const int pos = (s.t0 + i) * kTileP + p;
-        return (i < e.n && a.decay > 0.0f && pos < Nctx) ? mass[pos] : 0.0f;
+        return (i < s.n && a.decay > 0.0f && pos < Nctx) ? mass[pos] : 0.0f;
     };
     float old_q[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) old_q[k] = old_of(turn + k * kTurns);
-    int32_t page_next = turn < e.n ? page_of(a, s.pt, (s.t0 + turn) * kTileP) : -1;
+    int32_t page_next = turn < s.n ? page_of(a, s, (s.t0 + turn) * kTileP) : -1;
 #pragma unroll 1
-    for (int i = turn; i < e.n; i += kTurns) {
+    for (int i = turn; i < s.n; i += kTurns) {
         const float old = old_q[0];
 #pragma unroll
         for (int k = 0; k + 1 < kAhead; ++k) old_q[k] = old_q[k + 1];
@@ -437,11 +430,11 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
         const int pos0 = (s.t0 + i) * kTileP;
         const int pos = pos0 + p;
         const bool page_ok = page_next >= 0;
-        if (i + kTurns < e.n) page_next = page_of(a, s.pt, pos0 + kTurns * kTileP);
+        if (i + kTurns < s.n) page_next = page_of(a, s, pos0 + kTurns * kTileP);
         uint4 sc = make_uint4(0u, 0u, 0u, 0u);
         if (Mf<FMT>::kScales) {
             // this position's scales from the staged record
-            const int rc = e.tiles_done + i;
+            const int rc = s.tiles_done + i;
             ok = ok && mbar_wait_fast(&bar.r_full[rc % ST], (uint32_t)((rc / ST) & 1), e.abort);
             const uint8_t* rec = sm.rec[rc % ST] + p * Mf<FMT>::kStride;
             if (FMT == kFmtQ3) sc = *reinterpret_cast<const uint4*>(rec + 96);
@@ -452,7 +445,7 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
         unsigned long long sum0 = 0ull, sum1 = 0ull;         // pairs of zeros
 #pragma unroll 1
         for (int j = 0; j < s.chunks; ++j) {
-            const int ph = e.phases + i * s.chunks + j;
+            const int ph = s.phases + i * s.chunks + j;
             const int halves = COLS == 64 && R - kChunkRows * j <= 32 ? 1 : COLS / LD;   // loads of a group
             unsigned long long acc[COLS / 2];
 #pragma unroll
@@ -598,10 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) {
-            sm.first_slot = slot;
-            sm.first_base = base;
-            sm.w0 = w0;
-            sm.w1 = w1;
+            sm.walk = Walk{w0, w1, base, slot, 0, 0};
+            next_segment<FMT>(a, sm, 0);
         }
     }
     tc_fence_before();
@@ -609,26 +600,24 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
-    // Every role walks the CTA's segments on its own; the block meets when a segment's
-    // queries are in place and when it is done.
-    Walk wk;
-    wk.start(sm);
+    // Every role runs through the CTA's segments; the block meets when a segment's queries
+    // are in place and when it is done, by when the next one is known.
     bool ok = true;
     if (warp < kWarpD) {
         // ================================================================ E: epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsE));
-        Segment s;
-        while (wk.next(a, s)) {
+#pragma unroll 1
+        for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
+            const Segment s = sm.seg[k & 1];
             load_queries<TIn, FMT>(a, s, sm);
             named_sync(0, kThreads);
-            const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColAcc, wk.tiles_done, wk.phases, s.t1 - s.t0, abort};
+            const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColAcc, abort};
             const int rows = kGroup * s.T;
             if (rows <= 16) ok = epilogue<FMT, 16>(a, s, sm, e, ok);
             else if (rows <= 32) ok = epilogue<FMT, 32>(a, s, sm, e, ok);
             else ok = epilogue<FMT, 64>(a, s, sm, e, ok);
             named_sync(0, kThreads);
             if (*abort) break;
-            wk.advance(s);
         }
     } else if (warp < kWarpM) {
         // ================================================================ D: keys -> TMEM
@@ -637,13 +626,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         const int odd = (warp - kWarpD) >> 2;                // this warp's parts: odd and odd + 2
         const int p = 32 * (warp & 3) + lane;
         const uint32_t col0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        Segment s;
-        while (wk.next(a, s)) {
+#pragma unroll 1
+        for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
+            const Segment s = sm.seg[k & 1];
             load_queries<TIn, FMT>(a, s, sm);
             named_sync(0, kThreads);
-            const int n = s.t1 - s.t0;
-            int rs = wk.tiles_done % ST;                     // stage and its phase
-            uint32_t rp = (uint32_t)(wk.tiles_done / ST) & 1u;
+            const int n = s.n;
+            int rs = s.tiles_done % ST;                     // stage and its phase
+            uint32_t rp = (uint32_t)(s.tiles_done / ST) & 1u;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 ok = ok && mbar_wait_fast(&bar.r_full[rs], rp, abort);
@@ -653,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                     uint32_t wc[Words<FMT>::kN];
                     read_part<FMT>(rec, part, wc);
                     // the previous tile's products have read the operand
-                    if (i > 0) ok = ok && mbar_wait_fast(&bar.a_free[part], (uint32_t)((wk.tiles_done + i - 1) & 1), abort);
+                    if (i > 0) ok = ok && mbar_wait_fast(&bar.a_free[part], (uint32_t)((s.tiles_done + i - 1) & 1), abort);
                     __syncwarp();
                     tc_fence_after();
                     store_half<FMT>(wc, 0, cent, col0 + kPartCols * part);
@@ -671,32 +661,32 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             }
             named_sync(0, kThreads);
             if (*abort) break;
-            wk.advance(s);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMP));   // one warpgroup: M and P together
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMP));
         if (warp < kWarpP) {
         // ================================================================ M: products of one part
         const int first_part = warp - kWarpM;                // this issuer's parts: every kIssuers-th
-        Segment s;
-        while (wk.next(a, s)) {
+#pragma unroll 1
+        for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
+            const Segment s = sm.seg[k & 1];
             named_sync(0, kThreads);
-            const int n = s.t1 - s.t0;
+            const int n = s.n;
             // accumulator columns per group (query rows of a pass, rounded up) and slots of the ring
             const int cols = kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : 64);
             const int slots = kAccCols / cols;
-            const int c_first = kParts * wk.phases;
+            const int c_first = kParts * s.phases;
 #pragma unroll 1
             for (int i = 0; ok && i < n; ++i) {
 #pragma unroll 1
                 for (int j = 0; ok && j < s.chunks; ++j) {
                     const int rows = min(kChunkRows, kGroup * s.T - kChunkRows * j);
                     const uint32_t idesc = make_idesc(cols < 64 ? cols : (rows + 31) & ~31, false, false);
-                    const int ph = wk.phases + i * s.chunks + j;
+                    const int ph = s.phases + i * s.chunks + j;
 #pragma unroll 1
                     for (int part = first_part; ok && part < kParts; part += kIssuers) {
                         const int c = kParts * ph + part;
-                        if (j == 0) ok = mbar_wait_all(&bar.a_full[part], (uint32_t)((wk.tiles_done + i) & 1), abort);
+                        if (j == 0) ok = mbar_wait_all(&bar.a_full[part], (uint32_t)((s.tiles_done + i) & 1), abort);
                         // the slot's last accumulators (event c - slots) are read; earlier segments' all are
                         if (ok && c - slots >= c_first)
                             ok = mbar_wait_all(&bar.acc_free[(c - slots) % kFreeBars], (uint32_t)(((c - slots) / kFreeBars) & 1), abort);
@@ -728,26 +718,27 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             }
             named_sync(0, kThreads);
             if (*abort) break;
-            wk.advance(s);
         }
         if (elect_one()) mma_commit(&bar.drain[first_part]);
         __syncwarp();
         mbar_drain(&bar.drain[first_part], 0);
         } else {
         // ================================================================ P: records -> shared memory
-        Segment s;
-        while (wk.next(a, s)) {
-            const int n = s.t1 - s.t0;
+#pragma unroll 1
+        for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
+            const Segment s = sm.seg[k & 1];
+            const int n = s.n;
             // the first tiles' records are in flight while the queries are prepared: their stages are free
             const int pre = min(n, ST);
-            int staged = wk.tiles_done + pre;                // next tile to copy
+            int staged = s.tiles_done + pre;                // next tile to copy
             if (Mf<FMT>::kPadded || warp == kWarpP)
-                for (int k = 0; k < pre; ++k) stage_tile<FMT>(a, s, sm, k, wk.tiles_done + k);
+                for (int i = 0; i < pre; ++i) stage_tile<FMT>(a, s, sm, i, s.tiles_done + i);
+            if (tid == 32 * kWarpP + 32) next_segment<FMT>(a, sm, k + 1);
             named_sync(0, kThreads);
             if (Mf<FMT>::kPadded || warp == kWarpP) {
 #pragma unroll 1
                 for (int i = pre; i < n; ++i) {
-                    const int rc = wk.tiles_done + i;
+                    const int rc = s.tiles_done + i;
                     ok = ok && mbar_wait_all(&bar.r_free[rc % ST], (uint32_t)((rc / ST - 1) & 1), abort);
                     if (!ok) break;
                     stage_tile<FMT>(a, s, sm, i, rc);
@@ -759,10 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 // copies in flight land before the CTA leaves
                 if (Mf<FMT>::kPadded) asm volatile("cp.async.wait_all;" ::: "memory");
                 else if (warp == kWarpP)
-                    for (int k = max(wk.tiles_done, staged - ST); k < staged; ++k) mbar_drain(&bar.r_full[k % ST], (uint32_t)((k / ST) & 1));
+                    for (int k = max(s.tiles_done, staged - ST); k < staged; ++k) mbar_drain(&bar.r_full[k % ST], (uint32_t)((k / ST) & 1));
                 break;
             }
-            wk.advance(s);
         }
         }
     }
