@@ -71,8 +71,7 @@ constexpr int kTileP = 128;                 // positions per tile
 constexpr int kChunkRows = 64;              // query rows per pass over a tile
 constexpr int kMaxChunks = kMaxRows / kChunkRows;
 constexpr int kParts = 4;                   // parts of 64 dims
-constexpr int kAccCols = 192;               // accumulator columns per scale group of a part
-constexpr int kFreeBars = 12;               // consumption events: a multiple of kParts and of every slot count
+constexpr int kFreeBars = 48;               // consumption events: a multiple of kParts and of every slot count
 constexpr int kDoneBars = 4;                // generations of a part's completion barrier
 
 template <int FMT>
@@ -118,10 +117,12 @@ constexpr int kAhead = 2;                   // tiles whose old masses are loaded
 // must not mistake an older phase for the one they wait for (only its parity is
 // tested): hence several generations of done and acc_free.
 struct Bars {
-    unsigned long long a_full[kParts];             // operand part in TMEM (4 D warps)
+    unsigned long long a_full[kParts];             // one operand buffer: a part is in TMEM (4 D warps)
     unsigned long long done[kParts][kDoneBars];    // products of a part in pass ph (1 commit), by ph % 4
     unsigned long long a_free[kParts];             // every chunk's products of a part (1 commit): operand read
-    unsigned long long acc_free[kFreeBars];        // accumulators of event c read (4 E warps), by c % 12
+    unsigned long long b_full[2][2];               // two buffers: [buffer] the even / odd parts are in TMEM (4 D warps)
+    unsigned long long b_free[2][2];               // and their products are done (2 commits)
+    unsigned long long acc_free[kFreeBars];        // accumulators of event c read (4 E warps), by c % 48
     unsigned long long drain[kIssuers];            // everything an issuer started is done (1 commit)
     unsigned long long r_full[kMaxStages];         // a tile's records landed (copy bytes, or every P thread)
     unsigned long long r_free[kMaxStages];         // and were read (8 D warps; with scales, 4 E warps)
@@ -131,14 +132,16 @@ struct Bars {
 struct Segment {
     int slot, g, t0, n;
     int T, L, chunks;
-    int tiles_done;                          // tiles of earlier segments (phases of a_full, a_free and the stages)
+    int buffers;                             // operand buffers in TMEM
+    int tiles_done;                          // tiles of earlier segments (phases of the stages)
+    int tiles_single, tiles_double;          // of those with one operand buffer (a_full, a_free) and with two
     int phases;                              // (tile, chunk) passes of earlier segments (phases of done)
 };
 
 // A CTA's way through its share [w, w1) of the tile sequence; base: where the slot's tiles begin.
 struct Walk {
     long long w, w1, base;
-    int slot, tiles_done, phases;
+    int slot, tiles_done, tiles_single, tiles_double, phases;
 };
 
 template <int FMT>
@@ -185,6 +188,22 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigne
     return r;
 }
 
+// With at most 32 query rows the accumulators leave TMEM for a second operand buffer, so
+// the conversion of a tile overlaps the products of the one before it (8 slots x 1 token of
+// 655,360 positions: 74 -> 64 us; more rows need the columns for a deeper ring).  A
+// turbo5k operand has two fp16 parts and no room for that.
+template <int FMT>
+__host__ __device__ constexpr bool double_buffered(int tokens) {
+    return Mf<FMT>::kOps == 1 && kGroup * tokens <= 32;
+}
+// First accumulator column and slots of the ring.
+template <int FMT>
+__host__ __device__ constexpr uint32_t acc_col(int buffers) { return kParts * kPartCols * Mf<FMT>::kOps * buffers; }
+template <int FMT>
+__host__ __device__ constexpr int acc_slots(int buffers, int cols) {
+    return buffers == 2 ? 256 / (Mf<FMT>::kGroups * cols) : 192 / cols;
+}
+
 // The segment at the walk's position, for every role to read (one thread calls).
 template <int FMT>
 __device__ void next_segment(const MassArgs& a, MassSmem<FMT>& sm, int k) {
@@ -206,10 +225,14 @@ __device__ void next_segment(const MassArgs& a, MassSmem<FMT>& sm, int k) {
     s.T = a.n_q[wk.slot];
     s.L = a.ctx_len[wk.slot];
     s.chunks = (kGroup * s.T + kChunkRows - 1) / kChunkRows;
+    s.buffers = double_buffered<FMT>(s.T) ? 2 : 1;
     s.tiles_done = wk.tiles_done;
+    s.tiles_single = wk.tiles_single;
+    s.tiles_double = wk.tiles_double;
     s.phases = wk.phases;
     wk.w += s.n;
     wk.tiles_done += s.n;
+    (s.buffers == 2 ? wk.tiles_double : wk.tiles_single) += s.n;
     wk.phases += s.n * s.chunks;
 }
 
@@ -402,9 +425,9 @@ __device__ __forceinline__ float part_scale(const uint4& sc, int part, int gi) {
 
 // Epilogue of this warp's tiles of a segment; COLS accumulator columns per group
 // (16, 32 or 64 query rows of a pass).
-template <int FMT, int COLS>
+template <int FMT, int COLS, int BUFFERS>
 __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, const EpiState& e, bool ok) {
-    constexpr int G = Mf<FMT>::kGroups, ST = Mf<FMT>::kStages, SLOTS = kAccCols / COLS;
+    constexpr int G = Mf<FMT>::kGroups, ST = Mf<FMT>::kStages, SLOTS = acc_slots<FMT>(BUFFERS, COLS);
     constexpr int LD = COLS < 32 ? 16 : 32;                  // columns of one TMEM load
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int turn = warp >> 2;
@@ -540,8 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     constexpr int ST = Mf<FMT>::kStages;
     volatile int* abort = &sm.abort;
     constexpr int G = Mf<FMT>::kGroups, OPS = Mf<FMT>::kOps;
-    constexpr uint32_t kColAcc = kParts * kPartCols * OPS;
-    static_assert(kColAcc + G * kAccCols <= kTmemCols, "TMEM");
+    static_assert(acc_col<FMT>(1) + 192 * G <= kTmemCols && acc_col<kFmtQ3>(2) + 256 <= kTmemCols, "TMEM");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -551,6 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             mbar_init(&bar.a_full[q], 4);
             for (int e = 0; e < kDoneBars; ++e) mbar_init(&bar.done[q][e], 1);
             mbar_init(&bar.a_free[q], 1);
+            mbar_init(&bar.b_full[q >> 1][q & 1], 4);
+            mbar_init(&bar.b_free[q >> 1][q & 1], 2);
         }
         for (int e = 0; e < kFreeBars; ++e) mbar_init(&bar.acc_free[e], 4);
         for (int e = 0; e < kIssuers; ++e) mbar_init(&bar.drain[e], 1);
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) {
-            sm.walk = Walk{w0, w1, base, slot, 0, 0};
+            sm.walk = Walk{w0, w1, base, slot, 0, 0, 0, 0};
             next_segment<FMT>(a, sm, 0);
         }
     }
@@ -611,11 +635,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             const Segment s = sm.seg[k & 1];
             load_queries<TIn, FMT>(a, s, sm);
             named_sync(0, kThreads);
-            const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColAcc, abort};
+            const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc_col<FMT>(s.buffers), abort};
+            constexpr int B = double_buffered<FMT>(1) ? 2 : 1;
             const int rows = kGroup * s.T;
-            if (rows <= 16) ok = epilogue<FMT, 16>(a, s, sm, e, ok);
-            else if (rows <= 32) ok = epilogue<FMT, 32>(a, s, sm, e, ok);
-            else ok = epilogue<FMT, 64>(a, s, sm, e, ok);
+            if (rows <= 16) ok = epilogue<FMT, 16, B>(a, s, sm, e, ok);
+            else if (rows <= 32) ok = epilogue<FMT, 32, B>(a, s, sm, e, ok);
+            else ok = epilogue<FMT, 64, 1>(a, s, sm, e, ok);
             named_sync(0, kThreads);
             if (*abort) break;
         }
@@ -634,8 +659,37 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             const int n = s.n;
             int rs = s.tiles_done % ST;                     // stage and its phase
             uint32_t rp = (uint32_t)(s.tiles_done / ST) & 1u;
+            if (s.buffers == 2) {
 #pragma unroll 1
-            for (int i = 0; i < n; ++i) {
+                for (int i = 0; i < n; ++i) {
+                    const int use = (s.tiles_double + i) >> 1, buf = (s.tiles_double + i) & 1;
+                    const uint8_t* rec = sm.rec[rs] + p * Mf<FMT>::kStride;
+                    // the records are there, and the products of this buffer's last tile have read it
+                    ok = ok && (use > 0 ? mbar_wait_two(&bar.r_full[rs], rp, &bar.b_free[buf][odd], (uint32_t)((use - 1) & 1), abort)
+                                        : mbar_wait_all(&bar.r_full[rs], rp, abort));
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t col = col0 + kPartCols * (kParts * buf + odd);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t wc[Words<FMT>::kN];
+                        read_part<FMT>(rec, odd + 2 * h, wc);
+                        store_half<FMT>(wc, 0, cent, col + 2 * kPartCols * h);
+                        store_half<FMT>(wc, 1, cent, col + 2 * kPartCols * h + 16);
+                    }
+                    if (lane == 0) mbar_arrive(&bar.r_free[rs]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.b_full[buf][odd]);
+                    if (++rs == ST) {
+                        rs = 0;
+                        rp ^= 1u;
+                    }
+                }
+            }
+#pragma unroll 1
+            for (int i = 0; s.buffers == 1 && i < n; ++i) {
                 ok = ok && mbar_wait_fast(&bar.r_full[rs], rp, abort);
                 const uint8_t* rec = sm.rec[rs] + p * Mf<FMT>::kStride;
 #pragma unroll 1
@@ -643,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                     uint32_t wc[Words<FMT>::kN];
                     read_part<FMT>(rec, part, wc);
                     // the previous tile's products have read the operand
-                    if (i > 0) ok = ok && mbar_wait_fast(&bar.a_free[part], (uint32_t)((s.tiles_done + i - 1) & 1), abort);
+                    if (i > 0) ok = ok && mbar_wait_fast(&bar.a_free[part], (uint32_t)((s.tiles_single + i - 1) & 1), abort);
                     __syncwarp();
                     tc_fence_after();
                     store_half<FMT>(wc, 0, cent, col0 + kPartCols * part);
@@ -674,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             const int n = s.n;
             // accumulator columns per group (query rows of a pass, rounded up) and slots of the ring
             const int cols = kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : 64);
-            const int slots = kAccCols / cols;
+            const int slots = acc_slots<FMT>(s.buffers, cols);
             const int c_first = kParts * s.phases;
 #pragma unroll 1
             for (int i = 0; ok && i < n; ++i) {
@@ -686,14 +740,17 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
 #pragma unroll 1
                     for (int part = first_part; ok && part < kParts; part += kIssuers) {
                         const int c = kParts * ph + part;
-                        if (j == 0) ok = mbar_wait_all(&bar.a_full[part], (uint32_t)((s.tiles_done + i) & 1), abort);
+                        const int td = s.tiles_double + i, buf = s.buffers == 2 ? td & 1 : 0;
+                        if (j == 0)
+                            ok = s.buffers == 2 ? mbar_wait_all(&bar.b_full[buf][part & 1], (uint32_t)((td >> 1) & 1), abort)
+                                                : mbar_wait_all(&bar.a_full[part], (uint32_t)((s.tiles_single + i) & 1), abort);
                         // the slot's last accumulators (event c - slots) are read; earlier segments' all are
                         if (ok && c - slots >= c_first)
                             ok = mbar_wait_all(&bar.acc_free[(c - slots) % kFreeBars], (uint32_t)(((c - slots) / kFreeBars) & 1), abort);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t d = tmem + kColAcc + (uint32_t)((c % slots) * G * cols);
-                        const uint32_t aop = tmem + kPartCols * part;
+                        const uint32_t d = tmem + acc_col<FMT>(s.buffers) + (uint32_t)((c % slots) * G * cols);
+                        const uint32_t aop = tmem + kPartCols * (kParts * buf + part);
                         // dims 64 part ..: two 8-dim cores (256 bytes) per K step, start address in 16-byte units
                         const uint64_t bh = make_desc(smem_u32(sm.q[j][0]) + part * 1024, kQLbo, kQSbo);
                         const uint64_t bl = make_desc(smem_u32(sm.q[j][1]) + part * 1024, kQLbo, kQSbo);
@@ -710,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                                 }
                             }
                             mma_commit(&bar.done[part][ph % kDoneBars]);
-                            if (j == s.chunks - 1) mma_commit(&bar.a_free[part]);
+                            if (j == s.chunks - 1) mma_commit(s.buffers == 2 ? &bar.b_free[buf][part & 1] : &bar.a_free[part]);
                         }
                         __syncwarp();
                     }

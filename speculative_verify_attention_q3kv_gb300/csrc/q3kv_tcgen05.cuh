@@ -85,6 +85,13 @@ __device__ __forceinline__ bool mbar_wait_fast(unsigned long long* bar, uint32_t
     return mbar_test_wait(bar, parity) || mbar_wait_slow(bar, parity, abort);
 }
 
+// Two waits in one round trip: odd lanes wait for the second barrier.  All lanes agree.
+__device__ __forceinline__ bool mbar_wait_two(unsigned long long* bar0, uint32_t parity0, unsigned long long* bar1,
+                                              uint32_t parity1, volatile int* abort) {
+    const bool odd = threadIdx.x & 1;
+    return __all_sync(0xffffffffu, mbar_wait_fast(odd ? bar1 : bar0, odd ? parity1 : parity0, abort));
+}
+
 // All lanes wait and agree on the outcome.
 __device__ __forceinline__ bool mbar_wait_all(unsigned long long* bar, uint32_t parity, volatile int* abort) {
     return __all_sync(0xffffffffu, mbar_wait_fast(bar, parity, abort));
