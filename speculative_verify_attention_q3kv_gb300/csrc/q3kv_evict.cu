@@ -9,14 +9,17 @@
 // and writes positions and masses at their final ranks: the CTAs before it hold
 // known counts above and at the threshold, and of the positions at the threshold
 // the lowest ones are taken.  No float is added, so nothing depends on an order.
+// A segment of at most 8,192 positions stays in registers over the four passes;
+// longer ones are read again, from L2, with eight loads of a thread in flight.
 //
-// gather_kernel: 16-byte units (4-byte ones for the 164-byte K records) of the
-// kept records from their source rows to the destination pages; a record's
-// destination is contiguous with its neighbours', so stores coalesce, and a
-// thread has four independent loads in flight.
+// gather_kernel: a CTA moves up to 256 kept records, one destination page, of K and V:
+// their source offsets go to shared memory first, so all 16-byte loads (4-byte ones
+// for the 164-byte K records) of a thread are independent, and the stores, to
+// consecutive records, coalesce.
 //
 // Bound: memory (masses read once from HBM and again from L2, kept records read
-// and written once).
+// and written once; a 112-byte record scattered over 64-byte DRAM bursts costs about
+// half as much again to read).
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
@@ -121,10 +124,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     const int64_t row = blockIdx.x / C;                    // (layer, slot, kv head)
     const int slot = (int)(row / a.num_kv_heads) % a.num_slots;
     const SlotPlan s = slot_plan(a, slot);
-    if (rank == 0 && tid == 0 && row % a.num_kv_heads == 0 && row / a.num_kv_heads < a.num_slots) {
-        // one writer per slot; the other rows' plans never read new_len, and ctx_len may be the
-        // same array, so it is written by the gather kernel, after every row has its plan
+    if (rank == 0 && tid == 0 && row % a.num_kv_heads == 0 && row / a.num_kv_heads < a.num_slots) {   // one per slot
         if (s.bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
+        // where new_len is the array ctx_len, length_kernel writes it when every kernel has read it
+        if (a.new_len != a.ctx_len) a.new_len[slot] = s.n > 0 ? s.n : s.L;
     }
     if (s.n == 0) return;                                  // the whole cluster agrees
 
@@ -150,17 +153,34 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     uint32_t prefix = 0u;                                  // key bits found so far
     int want = k;                                          // entries still to take at or below the prefix's range
     bool nan = false;
+    // tile t0 of the segment: a warp has 32 * kPerLane consecutive positions, 32 at a time
+    float x[kPerLane];
+    auto load_tile = [&](int t0) {
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            const int i = t0 + warp * 32 * kPerLane + 32 * j + lane;
+            x[j] = i < end ? __ldg(m + i) : 0.0f;
+        }
+    };
+    const bool resident = end - begin <= kTileElems;       // one tile: loaded once
+    if (resident) load_tile(begin);
     if (k > 0 && k < count) {
 #pragma unroll 1
         for (int level = 0; level < 3; ++level) {
             const int shift = level == 0 ? 21 : (level == 1 ? 10 : 0);
             const int bins = level == 2 ? 1024 : 2048;
-            for (int i = begin + tid; i < end; i += kSelThreads) {
-                const float x = m[i];
-                nan |= x != x;
-                const uint32_t key = mass_key(x);
-                const bool in = level == 0 || (level == 1 ? (key >> 21) == prefix : (key >> 10) == prefix);
-                if (in) atomicAdd(&sm.hist[level][(key >> shift) & (bins - 1)], 1);
+            int* hist = sm.hist[level];
+#pragma unroll 1
+            for (int t0 = begin; t0 < end; t0 += kTileElems) {
+                if (!resident) load_tile(t0);
+#pragma unroll
+                for (int j = 0; j < kPerLane; ++j) {
+                    const int i = t0 + warp * 32 * kPerLane + 32 * j + lane;
+                    const uint32_t key = mass_key(x[j]);
+                    const bool in = i < end && (level == 0 || (level == 1 ? (key >> 21) == prefix : (key >> 10) == prefix));
+                    if (in) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+                    nan |= x[j] != x[j];
+                }
             }
             cluster.sync();
             // totals over the cluster: two bins per thread; then the bin, from the top, that holds the
@@ -200,7 +220,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     } else {
         // everything or nothing between the protected ends
         if (k > 0)
-            for (int i = begin + tid; i < end; i += kSelThreads) nan |= m[i] != m[i];
+            for (int i = begin + tid; i < end; i += kSelThreads) {
+                const float v = __ldg(m + i);
+                nan |= v != v;
+            }
         if (tid == 0) sm.local[0] = k > 0 ? end - begin : 0;
         __syncthreads();
     }
@@ -214,17 +237,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
         ties_before += l[1];
     }
     if (k > 0) {
-        // ordered pass: a warp takes 32 * kPerLane consecutive positions per tile, 32 at a time
+        // ordered pass
 #pragma unroll 1
         for (int t0 = begin; t0 < end; t0 += kTileElems) {
             const int w0 = t0 + warp * 32 * kPerLane;
             uint32_t gt[kPerLane], eq[kPerLane];
-            float x[kPerLane];
             int ngt = 0, neq = 0;
+            if (!resident) load_tile(t0);
 #pragma unroll
             for (int j = 0; j < kPerLane; ++j) {
                 const int i = w0 + 32 * j + lane;
-                x[j] = i < end ? m[i] : 0.0f;
                 const uint32_t key = mass_key(x[j]);
                 gt[j] = __ballot_sync(0xffffffffu, i < end && (all || key > prefix));
                 eq[j] = __ballot_sync(0xffffffffu, i < end && !all && key == prefix);
@@ -270,51 +292,66 @@ __device__ __forceinline__ size_t rec_at(const EvictArgs& a, int64_t page, int l
 }
 
 constexpr int kGatherThreads = 256;
-constexpr int kGatherUnroll = 4;
 
-template <int FMT, typename U, int UNITS, int KV0, int KVS>
+// Copies n records of UNITS units each from the offsets off[] to consecutive records at dst.
+template <typename U, int UNITS>
+__device__ __forceinline__ void move_records(uint8_t* pool, const size_t* off, int n, uint8_t* dst) {
+    constexpr int kU = sizeof(U) == 16 ? 7 : 8;              // loads of a thread in flight
+    const int total = n * UNITS;
+#pragma unroll 1
+    for (int u0 = threadIdx.x; u0 < total; u0 += kGatherThreads * kU) {
+        U v[kU];
+        bool ok[kU];
+#pragma unroll
+        for (int r = 0; r < kU; ++r) {
+            const int u = u0 + r * kGatherThreads;
+            ok[r] = u < total;
+            if (!ok[r]) continue;
+            const int i = u / UNITS, part = u - i * UNITS;
+            const size_t o = off[i];
+            ok[r] = o != ~(size_t)0;
+            if (ok[r]) v[r] = *reinterpret_cast<const U*>(pool + o + part * sizeof(U));
+        }
+#pragma unroll
+        for (int r = 0; r < kU; ++r)
+            if (ok[r]) *reinterpret_cast<U*>(dst + (size_t)(u0 + r * kGatherThreads) * sizeof(U)) = v[r];
+    }
+}
+
+// CTA: kept records [256 x, 256 x + 256) of one (layer, slot, kv head) row: one destination page.
+template <int FMT>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const EvictArgs a) {
+    __shared__ size_t off[2][kPageSize];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t row = blockIdx.y + (int64_t)gridDim.y * (blockIdx.z / KVS);
-    const int kv = KV0 + blockIdx.z % KVS;
+    const int64_t row = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
     if (row >= (int64_t)a.num_call_layers * a.num_slots * a.num_kv_heads) return;
     const int head = (int)(row % a.num_kv_heads);
     const int slot = (int)(row / a.num_kv_heads) % a.num_slots;
     const int layer = a.layer + (int)(row / a.num_kv_heads / a.num_slots);
     const SlotPlan s = slot_plan(a, slot);
-    if (s.n == 0) return;
-    const int32_t* kept = a.kept + row * a.max_budget;
-    const int32_t* src_row = a.page_table + (int64_t)slot * a.max_pages_per_slot;
-    const int32_t* dst_row = a.dst_table + (int64_t)slot * a.dst_max_pages;
-    const int64_t total = (int64_t)s.n * UNITS;
-    bool bad = false;
-    for (int64_t u0 = (int64_t)blockIdx.x * kGatherThreads * kGatherUnroll + threadIdx.x; u0 < total;
-         u0 += (int64_t)gridDim.x * kGatherThreads * kGatherUnroll) {
-        U v[kGatherUnroll];
-        size_t to[kGatherUnroll];
-        bool ok[kGatherUnroll];
-#pragma unroll
-        for (int r = 0; r < kGatherUnroll; ++r) {
-            const int64_t u = u0 + (int64_t)r * kGatherThreads;
-            ok[r] = u < total;
-            if (!ok[r]) continue;
-            const int i = (int)(u / UNITS), part = (int)(u - (int64_t)i * UNITS);
-            const int pos = kept[i];
-            const int32_t sp = src_row[pos / kPageSize], dp = dst_row[i / kPageSize];
-            if (sp < 0 || sp >= a.num_pages || dp < 0 || dp >= a.num_pages) {
-                ok[r] = false;
-                bad = true;
-                continue;
-            }
-            v[r] = *reinterpret_cast<const U*>(a.pool + rec_at<FMT>(a, sp, layer, head, kv, pos % kPageSize) + part * sizeof(U));
-            to[r] = rec_at<FMT>(a, dp, layer, head, kv, i % kPageSize) + part * sizeof(U);
-        }
-#pragma unroll
-        for (int r = 0; r < kGatherUnroll; ++r)
-            if (ok[r]) *reinterpret_cast<U*>(a.pool + to[r]) = v[r];
+    const int first = blockIdx.x * kPageSize;
+    const int n = min(kPageSize, s.n - first);
+    if (n <= 0) return;
+    const int32_t dp = a.dst_table[(int64_t)slot * a.dst_max_pages + blockIdx.x];
+    const bool dst_ok = dp >= 0 && dp < a.num_pages;
+    bool bad = !dst_ok;
+    if (threadIdx.x < n) {
+        const int pos = a.kept[row * a.max_budget + first + threadIdx.x];
+        const int32_t sp = a.page_table[(int64_t)slot * a.max_pages_per_slot + pos / kPageSize];
+        const bool ok = sp >= 0 && sp < a.num_pages;
+        bad |= !ok;
+        off[0][threadIdx.x] = ok ? rec_at<FMT>(a, sp, layer, head, 0, pos % kPageSize) : ~(size_t)0;
+        off[1][threadIdx.x] = ok ? rec_at<FMT>(a, sp, layer, head, 1, pos % kPageSize) : ~(size_t)0;
     }
     if (bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+    __syncthreads();
+    if (!dst_ok) return;
+    uint8_t* dk = a.pool + rec_at<FMT>(a, dp, layer, head, 0, 0);
+    uint8_t* dv = a.pool + rec_at<FMT>(a, dp, layer, head, 1, 0);
+    if (FMT == kFmtT5k) move_records<uint32_t, kT5kKRecordBytes / 4>(a.pool, off[0], n, dk);
+    else move_records<uint4, (FMT == kFmtFp8 ? kFp8RecordBytes : kRecordBytes) / 16>(a.pool, off[0], n, dk);
+    move_records<uint4, (FMT == kFmtFp8 ? kFp8RecordBytes : kRecordBytes) / 16>(a.pool, off[1], n, dv);
 }
 
 // New lengths, after every other kernel of the call has read ctx_len (which may
@@ -346,14 +383,12 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, int cluster, const Evic
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int FMT, typename U, int UNITS, int KV0, int KVS>
+template <int FMT>
 cudaError_t launch_gather(const EvictArgs& a, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.num_call_layers * a.num_slots * a.num_kv_heads;
     const int64_t most = std::min<int64_t>(a.max_budget, a.max_ctx_len);
-    const int64_t per = (int64_t)kGatherThreads * kGatherUnroll;
-    const int64_t x = std::max<int64_t>(1, (most * UNITS + per - 1) / per);
     const int64_t gy = std::min<int64_t>(rows, 32768), gz = (rows + gy - 1) / gy;
-    return launch_pdl(gather_kernel<FMT, U, UNITS, KV0, KVS>, dim3((unsigned)std::min<int64_t>(x, 1 << 20), (unsigned)gy, (unsigned)(gz * KVS)),
+    return launch_pdl(gather_kernel<FMT>, dim3((unsigned)((most + kPageSize - 1) / kPageSize), (unsigned)gy, (unsigned)gz),
                       kGatherThreads, 0, a, stream);
 }
 
@@ -412,16 +447,11 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
         while (c > 1 && (rows * c > 2 * (int64_t)sms || (int64_t)c * kTileElems > max_ctx_len)) c >>= 1;
         cudaError_t ce = launch_pdl(select_kernel, dim3((unsigned)(rows * c)), kSelThreads, c, a, st);
         if (ce != cudaSuccess) return cuda_status(ce);
-        if (fmt == kFmtFp8) {
-            ce = launch_gather<kFmtFp8, uint4, kFp8RecordBytes / 16, 0, 2>(a, st);
-        } else if (fmt == kFmtQ3) {
-            ce = launch_gather<kFmtQ3, uint4, kRecordBytes / 16, 0, 2>(a, st);
-        } else {
-            ce = launch_gather<kFmtT5k, uint32_t, kT5kKRecordBytes / 4, 0, 1>(a, st);
-            if (ce == cudaSuccess) ce = launch_gather<kFmtT5k, uint4, kRecordBytes / 16, 1, 1>(a, st);
-        }
+        ce = fmt == kFmtFp8 ? launch_gather<kFmtFp8>(a, st)
+                            : (fmt == kFmtT5k ? launch_gather<kFmtT5k>(a, st) : launch_gather<kFmtQ3>(a, st));
         if (ce != cudaSuccess) return cuda_status(ce);
     }
+    if (work && d_new_len != d_ctx_len) return Q3KV_OK;      // the select kernel wrote the lengths
     return cuda_status(launch_pdl(length_kernel, dim3((unsigned)std::min(64, (num_slots + 255) / 256)), 256, 0, a, st));
 }
 
