@@ -2,15 +2,20 @@
 //
 // select_kernel, one thread-block cluster per (layer, slot, kv head) row: a radix
 // select over the masses' order keys finds the k-th largest (k = budget minus the
-// protected positions) exactly, 11 + 11 + 10 bits.  Every CTA of the cluster counts
-// its own contiguous segment in shared memory; the cluster adds the histograms
-// through distributed shared memory and every CTA walks the totals itself.  Then
+// protected positions) exactly, 8 bits at a time.  Every CTA of the cluster counts its
+// own contiguous segment into a shared-memory histogram with a column, and so a
+// bank, per lane: masses bunch in a few bins, and one counter per bin would serialise
+// the lanes of a warp (2,048 single counters, three levels: 231 us at 32 rows of
+// 655,360, against 14 us at one of 5,000).  The cluster adds the totals through
+// distributed shared memory and every CTA walks them itself.  Then
 // each CTA takes its segment in order (ballots within a warp, a scan over the warps)
 // and writes positions and masses at their final ranks: the CTAs before it hold
 // known counts above and at the threshold, and of the positions at the threshold
 // the lowest ones are taken.  No float is added, so nothing depends on an order.
-// A segment of at most 8,192 positions stays in registers over the four passes;
-// longer ones are read again, from L2, with eight loads of a thread in flight.
+// A segment of at most 4,096 positions stays in registers over the five passes;
+// longer ones are read again, from L2, with eight loads of a thread in flight.  512
+// threads of at most 64 registers let two CTAs share an SM, so that the clusters of
+// 38 rows run at once (one CTA of 1,024 threads per SM left room for a dozen).
 //
 // gather_kernel: a CTA moves up to 256 kept records, one destination page, of K and V:
 // their source offsets go to shared memory first, so all 16-byte loads (4-byte ones
@@ -32,11 +37,12 @@ namespace cg = cooperative_groups;
 namespace q3kv {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kPerLane = 8;                               // elements of a lane per ordered tile
 constexpr int kTileElems = kSelThreads * kPerLane;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
+constexpr int kLevels = 4;
 constexpr int kMaxCluster = 8;
 
 struct EvictArgs {
@@ -83,9 +89,9 @@ __device__ __forceinline__ SlotPlan slot_plan(const EvictArgs& a, int slot) {
 
 // Order key of a mass: larger masses have larger keys, -0 equals +0, NaN is below all.
 __device__ __forceinline__ uint32_t mass_key(float x) {
-    if (x != x) return 0u;
-    const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(x + 0.0f);          // -0 + 0 = +0
+    const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return x == x ? key : 0u;
 }
 
 __device__ __forceinline__ int warp_sum(int v) {
@@ -103,9 +109,9 @@ __device__ __forceinline__ int warp_scan(int v) {   // inclusive
     return v;
 }
 
-struct SelectSmem {
-    int hist[3][kBins];
-    int total[kBins];
+struct __align__(16) SelectSmem {
+    int hist[kBins][32];        // a column per lane
+    int total[kLevels][kBins];  // this CTA's counts
     int warp_a[kSelWarps];
     int warp_b[kSelWarps];
     int found_bin;
@@ -113,7 +119,7 @@ struct SelectSmem {
     int local[2];               // this CTA's entries above the threshold, and at it
 };
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs a) {
     __shared__ SelectSmem sm;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -147,7 +153,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     const int seg = ((count + C - 1) / C + 31) / 32 * 32;
     const int begin = min(hi, lo + rank * seg), end = min(hi, begin + seg);
 
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
     if (tid < 2) sm.local[tid] = 0;
     __syncthreads();
     uint32_t prefix = 0u;                                  // key bits found so far
@@ -156,65 +161,79 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
     // tile t0 of the segment: a warp has 32 * kPerLane consecutive positions, 32 at a time
     float x[kPerLane];
     auto load_tile = [&](int t0) {
+        const int i0 = t0 + warp * 32 * kPerLane + lane;
+        if (t0 + kTileElems <= end) {
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j) x[j] = __ldg(m + i0 + 32 * j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j) x[j] = i0 + 32 * j < end ? __ldg(m + i0 + 32 * j) : 0.0f;
+        }
+    };
+    // one pass of a radix level over the tile in x: counts the keys that begin with the prefix
+    auto count_tile = [&](int t0, int level) {
+        const int i0 = t0 + warp * 32 * kPerLane + lane;
+        const int left = end - i0;                         // entry j exists if 32 j < left
+        const int shift = 24 - 8 * level;
 #pragma unroll
         for (int j = 0; j < kPerLane; ++j) {
-            const int i = t0 + warp * 32 * kPerLane + 32 * j + lane;
-            x[j] = i < end ? __ldg(m + i) : 0.0f;
+            const uint32_t key = mass_key(x[j]);
+            const bool in = level == 0 || (key >> (shift + 8)) == prefix;
+            if (in && 32 * j < left) atomicAdd(&sm.hist[(key >> shift) & (kBins - 1)][lane], 1);
+            if (level == 0) nan |= x[j] != x[j];
         }
     };
     const bool resident = end - begin <= kTileElems;       // one tile: loaded once
     if (resident) load_tile(begin);
     if (k > 0 && k < count) {
 #pragma unroll 1
-        for (int level = 0; level < 3; ++level) {
-            const int shift = level == 0 ? 21 : (level == 1 ? 10 : 0);
-            const int bins = level == 2 ? 1024 : 2048;
-            int* hist = sm.hist[level];
+        for (int level = 0; level < kLevels; ++level) {
+            for (int i = tid; i < kBins * 32 / 4; i += kSelThreads) reinterpret_cast<int4*>(&sm.hist[0][0])[i] = make_int4(0, 0, 0, 0);
+            __syncthreads();
 #pragma unroll 1
             for (int t0 = begin; t0 < end; t0 += kTileElems) {
                 if (!resident) load_tile(t0);
+                count_tile(t0, level);
+            }
+            __syncthreads();
+            {   // two threads add a bin's 32 columns, 16 bytes at a time
+                const int b = tid >> 1, c0 = tid & 1;
+                int t = 0;
 #pragma unroll
-                for (int j = 0; j < kPerLane; ++j) {
-                    const int i = t0 + warp * 32 * kPerLane + 32 * j + lane;
-                    const uint32_t key = mass_key(x[j]);
-                    const bool in = i < end && (level == 0 || (level == 1 ? (key >> 21) == prefix : (key >> 10) == prefix));
-                    if (in) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
-                    nan |= x[j] != x[j];
+                for (int c = 0; c < 4; ++c) {
+                    const int4 u = reinterpret_cast<const int4*>(&sm.hist[b][0])[2 * ((c + b) & 3) + c0];
+                    t += (u.x + u.y) + (u.z + u.w);
                 }
+                t += __shfl_xor_sync(0xffffffffu, t, 1);
+                if (c0 == 0) sm.total[level][b] = t;
             }
             cluster.sync();
-            // totals over the cluster: two bins per thread; then the bin, from the top, that holds the
-            // want-th entry.  Thread t covers bins from the top: 2t and 2t + 1 of the reversed order.
-            int t0 = 0, t1 = 0;
-            const int b0 = bins - 1 - 2 * tid, b1 = b0 - 1;
-            if (b0 > 0) {
-                for (int c = 0; c < C; ++c) {
-                    const int* h = cluster.map_shared_rank(&sm.hist[level][0], c);
-                    t0 += h[b0];
-                    t1 += h[b1];
-                }
-            }
-            const int incl = warp_scan(t0 + t1);
+            // the bin, from the top, that holds the want-th entry of the cluster
+            const int bin = kBins - 1 - tid;
+            int t = 0;
+            if (tid < kBins)
+                for (int c = 0; c < C; ++c) t += cluster.map_shared_rank(&sm.total[level][0], c)[bin];
+            const int incl = warp_scan(t);
             if (lane == 31) sm.warp_a[warp] = incl;
             __syncthreads();
-            if (warp == 0) sm.warp_b[lane] = warp_scan(sm.warp_a[lane]);
-            __syncthreads();
-            const int before = incl - t0 - t1 + (warp ? sm.warp_b[warp - 1] : 0);
-            if (before < want && before + t0 + t1 >= want) {
-                const bool first = before + t0 >= want;
-                sm.found_bin = first ? b0 : b1;
-                sm.found_above = first ? before : before + t0;
+            if (tid < kBins) {
+                int before = incl - t;
+                for (int w = 0; w < warp; ++w) before += sm.warp_a[w];
+                if (before < want && before + t >= want) {
+                    sm.found_bin = bin;
+                    sm.found_above = before;
+                }
             }
             __syncthreads();
-            const int bin = sm.found_bin;
+            const int found = sm.found_bin;
             want -= sm.found_above;
             // this CTA's entries above the bin
-            int above = 0;
-            for (int i = bin + 1 + tid; i < bins; i += kSelThreads) above += sm.hist[level][i];
-            above = warp_sum(above);
-            if (lane == 0 && above) atomicAdd(&sm.local[0], above);
-            if (level == 2 && tid == 0) sm.local[1] = sm.hist[2][bin];
-            prefix = (prefix << (level == 2 ? 10 : 11)) | (uint32_t)bin;
+            if (warp < kBins / 32) {
+                const int above = warp_sum(tid > found ? sm.total[level][tid] : 0);
+                if (lane == 0 && above) atomicAdd(&sm.local[0], above);
+            }
+            if (level == kLevels - 1 && tid == 0) sm.local[1] = sm.total[level][found];
+            prefix = (prefix << 8) | (uint32_t)found;
             __syncthreads();
         }
     } else {
@@ -259,7 +278,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictArgs a) 
                 sm.warp_b[warp] = neq;
             }
             __syncthreads();
-            const int ca = sm.warp_a[lane], cb = sm.warp_b[lane];
+            const int ca = lane < kSelWarps ? sm.warp_a[lane] : 0, cb = lane < kSelWarps ? sm.warp_b[lane] : 0;
             int g = above_before + warp_sum(lane < warp ? ca : 0);
             int e = ties_before + warp_sum(lane < warp ? cb : 0);
             above_before += warp_sum(ca);
