@@ -68,11 +68,17 @@ def _on_gpu(name: str, t: Optional[torch.Tensor], dev: int, dtype=None, min_nume
 
 def _device_index(t: torch.Tensor) -> Optional[int]:
     """CUDA device index of a tensor; None for a tensor in host (or any other) memory."""
-    return t.device.index if t.is_cuda else None
+    return t.get_device() if t.is_cuda else None
+
+
+_cuda_seen = False                # asking torch whether CUDA is there costs microseconds; a yes stays a yes
 
 
 def _current_device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+    global _cuda_seen
+    if not _cuda_seen:
+        _cuda_seen = torch.cuda.is_available()
+    return torch.cuda.current_device() if _cuda_seen else -1
 
 
 def _nbytes(t: torch.Tensor) -> int:
@@ -130,9 +136,47 @@ def _check_verify(desc, pool, pool_bytes_fn, page_table, ctx_len, n_q, q_offsets
     _on_gpu("workspace", workspace, dev, optional=True)
 
 
+def _pointers(dev: int, *args):
+    """Checks of several tensors in one pass (a call of a step costs microseconds): for every (name, tensor, dtype or
+    None, elements needed) what _on_gpu and _ptr check, and the data pointers.  A tensor of None gives None."""
+    out = []
+    for name, t, dtype, need in args:
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if _device_index(t) != dev or (dtype is not None and t.dtype != dtype) or t.numel() < need:
+            _on_gpu(name, t, dev, dtype, need)
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to q3kv must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _cache_pointers(desc: CacheDesc, pool, need_pool_bytes: int, page_table, lens, counts, offsets, status, dev: int):
+    """_check_cache_args with the pointers: (num_slots, pool, page_table, lens, counts, offsets, status)."""
+    for name, t in (("pool", pool), ("page_table", page_table), ("lengths", lens), ("per-slot token counts", counts),
+                    ("row offsets", offsets)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    if lens.dim() != 1:
+        raise ValueError("per-slot lengths must be one-dimensional")
+    n = lens.shape[0]
+    ptrs = _pointers(dev, ("pool", pool, None, 0), ("page_table", page_table, torch.int32, 0), ("lengths", lens, torch.int32, 0),
+                     ("per-slot token counts", counts, torch.int32, n), ("row offsets", offsets, torch.int32, n),
+                     ("status", status, torch.int32, 1))
+    if page_table.dim() != 2 or page_table.shape[1] < 1 or (n > 0 and page_table.shape[0] < n):
+        raise ValueError(f"page_table must be int32 [num_slots >= {n}, max_pages_per_slot >= 1], "
+                         f"got {tuple(page_table.shape)}")
+    if _nbytes(pool) < need_pool_bytes:
+        raise ValueError(f"pool holds {_nbytes(pool)} bytes, the cache needs {need_pool_bytes}")
+    return n, ptrs
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -490,17 +534,24 @@ def t5k_attn_mass(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor,
 def _attn_mass(name, pool_bytes_fn, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len, max_n_q, layer, q, lse,
                decay, mass, status, stream) -> None:
     dev = _current_device()
-    n = _check_cache_args(desc, pool, pool_bytes_fn(desc), page_table, ctx_len, n_q, q_offsets, status, dev)
-    _check_rows("q", q, desc.num_q_heads, dev)
-    _check_lse(lse, q, desc.num_q_heads, dev)
-    _on_gpu("mass", mass, dev, torch.float32)
-    if mass.dim() != 3 or mass.shape[0] < n or mass.shape[1] != desc.num_kv_heads or mass.shape[2] < max_ctx_len:
-        raise ValueError(f"mass must be [slots >= {n}, {desc.num_kv_heads}, positions >= {max_ctx_len}], "
-                         f"got {tuple(mass.shape)}")
-    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), _ptr(pool), _ptr(page_table),
-                                    page_table.shape[1], _ptr(ctx_len), _ptr(n_q), _ptr(q_offsets), n, max_ctx_len,
-                                    max_n_q, layer, _ptr(q), _dtype_code(q), _ptr(lse), float(decay), _ptr(mass),
-                                    mass.shape[2], _ptr(status))
+    n, (p_pool, p_table, p_ctx, p_nq, p_off, p_status) = _cache_pointers(desc, pool, pool_bytes_fn(desc), page_table, ctx_len,
+                                                                        n_q, q_offsets, status, dev)
+    for what, t in (("q", q), ("lse", lse), ("mass", mass)):
+        if t is None:
+            raise ValueError(f"{what} is required")
+    p_q, p_lse, p_mass = _pointers(dev, ("q", q, None, 0), ("lse", lse, torch.float32, 0), ("mass", mass, torch.float32, 0))
+    hq, hk = desc.num_q_heads, desc.num_kv_heads
+    shape = q.shape
+    if len(shape) != 3 or shape[1] != hq or shape[2] != HEAD_DIM:
+        raise ValueError(f"q must be [rows, {hq}, {HEAD_DIM}], got {tuple(shape)}")
+    if lse.dim() != 2 or lse.shape[1] != hq or lse.shape[0] < shape[0]:
+        raise ValueError(f"lse must be [rows >= {shape[0]}, {hq}], got {tuple(lse.shape)}")
+    shape = mass.shape
+    if len(shape) != 3 or shape[0] < n or shape[1] != hk or shape[2] < max_ctx_len:
+        raise ValueError(f"mass must be [slots >= {n}, {hk}, positions >= {max_ctx_len}], got {tuple(shape)}")
+    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), p_pool, p_table, page_table.shape[1], p_ctx, p_nq, p_off,
+                                    n, max_ctx_len, max_n_q, layer, p_q, _dtype_code(q), p_lse, float(decay), p_mass, shape[2],
+                                    p_status)
     check(rc, name)
 
 
@@ -535,27 +586,28 @@ def t5k_evict(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx
 def _evict(name, pool_bytes_fn, desc, pool, page_table, ctx_len, max_ctx_len, budget, max_budget, n_sink, n_recent, layer,
            mass, dst_page_table, kept, mass_out, new_len, status, stream) -> None:
     dev = _current_device()
-    n = _check_cache_args(desc, pool, pool_bytes_fn(desc), page_table, ctx_len, ctx_len, ctx_len, status, dev)
-    _on_gpu("budget", budget, dev, torch.int32, n)
-    _on_gpu("new_len", new_len, dev, torch.int32, n)
-    _on_gpu("dst_page_table", dst_page_table, dev, torch.int32)
+    n, (p_pool, p_table, p_ctx, _, _, p_status) = _cache_pointers(desc, pool, pool_bytes_fn(desc), page_table, ctx_len, ctx_len,
+                                                                 ctx_len, status, dev)
+    for what, t in (("budget", budget), ("new_len", new_len), ("dst_page_table", dst_page_table), ("mass", mass), ("kept", kept)):
+        if t is None:
+            raise ValueError(f"{what} is required")
+    i32, f32 = torch.int32, torch.float32
+    p_budget, p_new, p_dst, p_mass, p_kept, p_out = _pointers(
+        dev, ("budget", budget, i32, n), ("new_len", new_len, i32, n), ("dst_page_table", dst_page_table, i32, 0),
+        ("mass", mass, f32, 0), ("kept", kept, i32, 0), ("mass_out", mass_out, f32, 0))
     if dst_page_table.dim() != 2 or dst_page_table.shape[1] < 1 or dst_page_table.shape[0] < n:
         raise ValueError(f"dst_page_table must be int32 [num_slots >= {n}, max_pages_per_slot >= 1], "
                          f"got {tuple(dst_page_table.shape)}")
-    _on_gpu("mass", mass, dev, torch.float32)
-    heads = desc.num_kv_heads
-    if mass.dim() != 4 or mass.shape[1] != n or mass.shape[2] != heads or mass.shape[3] < max_ctx_len:
-        raise ValueError(f"mass must be [layers, {n}, {heads}, positions >= {max_ctx_len}], got {tuple(mass.shape)}")
-    want = (mass.shape[0], n, heads, max_budget)
-    _on_gpu("kept", kept, dev, torch.int32)
-    _on_gpu("mass_out", mass_out, dev, torch.float32, optional=True)
+    heads, shape = desc.num_kv_heads, mass.shape
+    if len(shape) != 4 or shape[1] != n or shape[2] != heads or shape[3] < max_ctx_len:
+        raise ValueError(f"mass must be [layers, {n}, {heads}, positions >= {max_ctx_len}], got {tuple(shape)}")
+    want = (shape[0], n, heads, max_budget)
     for what, t in (("kept", kept), ("mass_out", mass_out)):
         if t is not None and tuple(t.shape) != want:
             raise ValueError(f"{what} must be {want}, got {tuple(t.shape)}")
-    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), _ptr(pool), _ptr(page_table),
-                                    page_table.shape[1], _ptr(ctx_len), n, max_ctx_len, _ptr(budget), max_budget, n_sink,
-                                    n_recent, layer, mass.shape[0], _ptr(mass), mass.shape[3], _ptr(dst_page_table),
-                                    dst_page_table.shape[1], _ptr(kept), _ptr(mass_out), _ptr(new_len), _ptr(status))
+    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), p_pool, p_table, page_table.shape[1], p_ctx, n, max_ctx_len,
+                                    p_budget, max_budget, n_sink, n_recent, layer, shape[0], p_mass, shape[3], p_dst,
+                                    dst_page_table.shape[1], p_kept, p_out, p_new, p_status)
     check(rc, name)
 
 
@@ -574,14 +626,15 @@ def make_rope_plan(rotary_dim: int, theta: float, sections, deal_axes: bool = Fa
 
 def _strided_rows(name: str, t: torch.Tensor, rows: int, dev: int):
     """Pointer, row stride and heads of [rows, heads, 256] rows whose heads are contiguous; rows may be strided."""
-    _on_gpu(name, t, dev)
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(t.shape)}")
-    heads = t.shape[1]
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM):
+    if not isinstance(t, torch.Tensor) or _device_index(t) != dev:
+        _on_gpu(name, t, dev)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != rows or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(shape)}")
+    heads = shape[1]
+    if stride[2] != 1 or (heads > 1 and stride[1] != HEAD_DIM):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    stride = t.stride(0) if rows > 1 else heads * HEAD_DIM
-    return t.data_ptr(), stride, heads
+    return t.data_ptr(), stride[0] if rows > 1 else heads * HEAD_DIM, heads
 
 
 def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.Tensor, k: Optional[torch.Tensor] = None,
@@ -591,30 +644,29 @@ def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.
     Rows may be strided (slices of one projection); an output may be its input.
     """
     dev = _current_device()
-    if positions.dim() != 2 or positions.shape[1] != plan.num_axes:
-        raise ValueError(f"positions must be [rows, {plan.num_axes}], got {tuple(positions.shape)}")
+    p_pos, = _pointers(dev, ("positions", positions, torch.int32, 0))
+    if p_pos is None or positions.dim() != 2 or positions.shape[1] != plan.num_axes:
+        raise ValueError(f"positions must be [rows, {plan.num_axes}]"
+                         + (f", got {tuple(positions.shape)}" if positions is not None else ""))
     rows = positions.shape[0]
-    _on_gpu("positions", positions, dev, torch.int32)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out come together")
     args = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            args += [None, 0, None, 0, 0]
-            continue
+    for name, x, y in (("q", q, q_out),) if k is None else (("q", q, q_out), ("k", k, k_out)):
         src, src_stride, heads = _strided_rows(name, x, rows, dev)
         dst, dst_stride, out_heads = _strided_rows(name + "_out", y, rows, dev)
         if heads != out_heads or x.dtype != q.dtype or y.dtype != q.dtype:
             raise ValueError(f"{name} and {name}_out must have the heads of one another and the dtype of q")
-        if rows and heads:
+        if rows and heads and not (src == dst and src_stride == dst_stride):
             # extents in bytes; an exact in-place call is fine, any other overlap is not
             size = x.element_size()
-            src_end = src + ((rows - 1) * src_stride + heads * HEAD_DIM) * size
-            dst_end = dst + ((rows - 1) * dst_stride + heads * HEAD_DIM) * size
-            if src < dst_end and dst < src_end and not (src == dst and src_stride == dst_stride):
+            if (src < dst + ((rows - 1) * dst_stride + heads * HEAD_DIM) * size
+                    and dst < src + ((rows - 1) * src_stride + heads * HEAD_DIM) * size):
                 raise ValueError(f"{name}_out overlaps {name} without being the same rows")
-        args += [src, src_stride, dst, dst_stride, heads]
-    rc = _lib.load().q3kv_rope(_stream(stream), ctypes.byref(plan), _ptr(positions), rows, *args, _dtype_code(q))
+        args += (src, src_stride, dst, dst_stride, heads)
+    if k is None:
+        args += (None, 0, None, 0, 0)
+    rc = _lib.load().q3kv_rope(_stream(stream), ctypes.byref(plan), p_pos, rows, *args, _dtype_code(q))
     check(rc, "q3kv_rope")
 
 
@@ -631,18 +683,25 @@ def accept_draft(logits: torch.Tensor, draft_probs: torch.Tensor, q_offsets: tor
                  workspace: Optional[torch.Tensor], accept_prob: Optional[torch.Tensor] = None,
                  status: Optional[torch.Tensor] = None, stream=None) -> None:
     """q3kv_accept_draft: rejection-sampled acceptance of drafts drawn from draft_probs [rows, vocab] (f32 or bf16)."""
-    rows, vocab = _check_accept(logits, q_offsets, n_q, tokens, ctx_len, n_accepted, next_token, committed_len,
-                                workspace, status)
-    dev = _current_device()
-    _on_gpu("draft_probs", draft_probs, dev)
+    for what, t in (("logits", logits), ("draft_probs", draft_probs), ("q_offsets", q_offsets), ("n_q", n_q), ("tokens", tokens),
+                    ("ctx_len", ctx_len), ("uniforms", uniforms), ("n_accepted", n_accepted), ("next_token", next_token),
+                    ("committed_len", committed_len)):
+        if t is None:
+            raise ValueError(f"{what} is required")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, vocab], got {tuple(logits.shape)}")
+    if n_q.dim() != 1:
+        raise ValueError("n_q must be one-dimensional")
+    rows, vocab = logits.shape
+    n, i32, f32 = n_q.shape[0], torch.int32, torch.float32
+    p = _pointers(_current_device(), ("logits", logits, None, 0), ("draft_probs", draft_probs, None, 0),
+                  ("q_offsets", q_offsets, i32, n), ("n_q", n_q, i32, 0), ("tokens", tokens, i32, rows), ("ctx_len", ctx_len, i32, n),
+                  ("uniforms", uniforms, f32, rows), ("n_accepted", n_accepted, i32, n), ("next_token", next_token, i32, n),
+                  ("committed_len", committed_len, i32, n), ("accept_prob", accept_prob, f32, rows),
+                  ("workspace", workspace, None, 0), ("status", status, i32, 1))
     if draft_probs.shape != logits.shape:
         raise ValueError(f"draft_probs must be {tuple(logits.shape)}, got {tuple(draft_probs.shape)}")
-    _on_gpu("uniforms", uniforms, dev, torch.float32, rows)
-    _on_gpu("accept_prob", accept_prob, dev, torch.float32, rows, optional=True)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = _lib.load().q3kv_accept_draft(_stream(stream), _ptr(logits), _dtype_code(logits), vocab, _ptr(draft_probs),
-                                       _dtype_code(draft_probs), _ptr(q_offsets), _ptr(n_q), _ptr(tokens), n_q.shape[0],
-                                       rows, max_n_q, _ptr(ctx_len), float(temperature), _ptr(uniforms),
-                                       int(seed) & ((1 << 64) - 1), _ptr(n_accepted), _ptr(next_token),
-                                       _ptr(committed_len), _ptr(accept_prob), _ptr(workspace), nbytes, _ptr(status))
+    rc = _lib.load().q3kv_accept_draft(_stream(stream), p[0], _dtype_code(logits), vocab, p[1], _dtype_code(draft_probs), p[2], p[3],
+                                       p[4], n, rows, max_n_q, p[5], float(temperature), p[6], int(seed) & ((1 << 64) - 1), p[7],
+                                       p[8], p[9], p[10], p[11], 0 if workspace is None else _nbytes(workspace), p[12])
     check(rc, "q3kv_accept_draft")

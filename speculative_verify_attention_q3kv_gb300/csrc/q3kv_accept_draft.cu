@@ -9,17 +9,22 @@
 //   first rejected row a: argmax of r(x) / E(x), r = max(p_a - q_a, 0), E = -log U
 //   (r / E is e^(log r + Gumbel): one logarithm instead of two); bonus: p / E.
 //
-// Bound: memory.  Every target row is read once for its (max, sum of exp); the
-// residual needs one target row (now in L2) and one draft row per slot.  Two
-// launches: stats_kernel, grid (vocabulary chunks, rows); residual_kernel, grid
-// (chunks, slots), in which every CTA merges its slot's row statistics and runs
-// the acceptance chain itself (a few hundred loads that hit L2), then races its
-// chunk of row a.  The race's winner is a 64-bit atomic maximum of (key,
+// Bound: memory and latency.  Every target row is read once for its (max, sum of
+// exp); the residual needs one target row (now in L2) and one draft row per slot.
+// Two launches: stats_kernel, grid (vocabulary chunks, rows); residual_kernel,
+// grid (chunks, slots), in which every CTA merges its slot's row statistics and
+// runs the acceptance chain itself (a few hundred loads that hit L2), then races
+// its chunk of row a.  The race's winner is a 64-bit atomic maximum of (key,
 // ~index) per slot, whatever the order; the slot's last CTA stores the results.
 //
+// Issue slots decide beside that: the statistics take six instructions an entry
+// (bad logits show in the sum, not per entry), and the race computes a clock only
+// where it can win: E = -log U >= 1 - U, so r / E <= r / (1 - U), which the noise's
+// integer gives without a logarithm.
+//
 // Exponents: e^((l - max) / tau) with l - max taken on the raw logits (exact for
-// the ones that count) and log2(e) / tau split in two floats, so a probability
-// is within a few float32 roundings of its definition.
+// the ones that count); a tested probability has log2(e) / tau split in two floats,
+// so it is within a few float32 roundings of its definition.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -73,6 +78,10 @@ __device__ __forceinline__ float weight(const DraftArgs& a, float l, float m) {
     const float d = l - m;
     return exp2_approx(d == -CUDART_INF_F ? d : fmaf(d, a.c_hi, d * a.c_lo));
 }
+
+// the same for a term of the sum, with log2(e) / tau in one float: 2^-25 of an exponent that
+// counts (below 20) is lost
+__device__ __forceinline__ float term(const DraftArgs& a, float l, float m) { return exp2_approx((l - m) * a.c_hi); }
 
 // (max, sum) of two parts of a row
 __device__ __forceinline__ float2 merge(const DraftArgs& a, float2 x, float2 y) {
@@ -130,34 +139,34 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const DraftArgs a) {
     const int c1 = min(a.vocab, c0 + a.chunk1);
     const T* lg = static_cast<const T*>(a.logits) + (int64_t)row * a.vocab;
     float m = -CUDART_INF_F, s = 0.0f;
-    bool bad = false;
     constexpr int kU = 4;                                  // 32 entries of a thread in flight
     for (int k0 = c0 + 8 * threadIdx.x; k0 < c1; k0 += 8 * kU * kThreads) {
         float x[kU][8];
 #pragma unroll
         for (int r = 0; r < kU; ++r) load8(lg, a.vec_logits, k0 + 8 * r * kThreads, c1, -CUDART_INF_F, x[r]);
-        float bm = -CUDART_INF_F;
+        float bm = x[0][0];
 #pragma unroll
         for (int r = 0; r < kU; ++r)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                bad |= !(x[r][i] < CUDART_INF_F);          // NaN or +inf
-                bm = fmaxf(bm, x[r][i]);
-            }
+            for (int i = 0; i < 8; ++i) bm = fmaxf(bm, x[r][i]);
         if (bm > m) {
             s = m == -CUDART_INF_F ? 0.0f : s * weight(a, m, bm);
             m = bm;
         }
-        if (m > -CUDART_INF_F) {
-            float t = 0.0f;
+        // a row of -inf so far: 0 in place of the maximum keeps the terms at 0, and NaN at NaN
+        const float mm = m == -CUDART_INF_F ? 0.0f : m;
+        float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-            for (int r = 0; r < kU; ++r)
+        for (int r = 0; r < kU; ++r)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t += weight(a, x[r][i], m);
-            s += t;
-        }
+            for (int i = 0; i < 8; i += 2) {
+                t0 += term(a, x[r][i], mm);
+                t1 += term(a, x[r][i + 1], mm);
+            }
+        s += t0 + t1;
     }
-    if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0 && a.status)
+    // a NaN logit makes its sum NaN, and so does +inf (inf - inf)
+    if (__any_sync(0xffffffffu, s != s) && (threadIdx.x & 31) == 0 && a.status)
         atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
     float2 v = warp_merge(a, make_float2(m, s));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -194,6 +203,18 @@ __global__ void __launch_bounds__(kThreads) residual_kernel(const DraftArgs a) {
     const bool skip = n <= 0 || n > a.max_n_q || n > L || r0 < 0 || r0 > a.num_rows - n;
     int acc = 0;
     if (!skip) {
+        // lane j of warp 0 tests the draft that follows query token j; its values are on the way
+        // while the rows' statistics are merged
+        const bool drafted = warp == 0 && lane < n - 1;
+        const int d = drafted ? a.tokens[r0 + lane + 1] : -1;
+        const bool known = drafted && d >= 0 && d < a.vocab;
+        float ld = 0.0f, q = 0.0f, u = 1.0f;
+        if (known) {
+            const int64_t at = (int64_t)(r0 + lane) * a.vocab + d;
+            ld = to_f(static_cast<const T*>(a.logits)[at]);
+            q = to_f(static_cast<const Q*>(a.draft)[at]);
+            u = a.uniforms[r0 + lane];
+        }
         // the rows' statistics: one warp per row, its lanes over the chunks
         for (int j = warp; j < n; j += kWarps) {
             const float2* p = a.stats + (int64_t)(r0 + j) * a.num_chunks1;
@@ -204,17 +225,8 @@ __global__ void __launch_bounds__(kThreads) residual_kernel(const DraftArgs a) {
         }
         __syncthreads();
         if (warp == 0) {
-            // lane j tests the draft that follows query token j
-            const bool drafted = lane < n - 1;
-            const int d = drafted ? a.tokens[r0 + lane + 1] : -1;
-            float p = 0.0f, q = 0.0f, u = 1.0f;
-            if (drafted && d >= 0 && d < a.vocab) {
-                const int64_t at = (int64_t)(r0 + lane) * a.vocab + d;
-                const float2 v = st[lane];
-                if (v.y > 0.0f) p = weight(a, to_f(static_cast<const T*>(a.logits)[at]), v.x) / v.y;
-                q = to_f(static_cast<const Q*>(a.draft)[at]);
-                u = a.uniforms[r0 + lane];
-            }
+            const float2 v = st[drafted ? lane : 0];
+            const float p = known && v.y > 0.0f ? weight(a, ld, v.x) / v.y : 0.0f;
             const bool pass = drafted && u * q < p;
             const unsigned miss = __ballot_sync(0xffffffffu, drafted && !pass);
             const int first = miss ? __ffs(miss) - 1 : n - 1;
@@ -236,23 +248,40 @@ __global__ void __launch_bounds__(kThreads) residual_kernel(const DraftArgs a) {
         const int c0 = chunk * a.chunk2;
         const int c1 = min(a.vocab, c0 + a.chunk2);
         unsigned long long best_r = 0ull, best_p = 0ull;
+        // bounds that a candidate has to reach: the warp's best keys so far
+        float top_r = 0.0f, top_p = 0.0f;
         bool bad = false;
         if (v.x > -CUDART_INF_F) {
-            for (int k = c0 + 8 * threadIdx.x; k < c1; k += 8 * kThreads) {
-                float x[8], q[8];
-                load8(lg, a.vec_logits, k, c1, -CUDART_INF_F, x);
-                if (!bonus) load8(dr, a.vec_draft, k, c1, 0.0f, q);
+            constexpr int kU = 2;                          // 16 entries of a thread in flight
+            for (int k0 = c0 + 8 * (threadIdx.x & ~31); k0 < c1; k0 += 8 * kU * kThreads) {   // warp-uniform
+                float x[kU][8], q[kU][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = weight(a, x[i], v.x) * inv;
-                    if (!(p > 0.0f)) continue;
-                    const float e = -logf(noise_uniform(a.seed, (uint32_t)row, (uint32_t)(k + i)));
-                    best_p = max(best_p, candidate(p / e, k + i));
-                    if (!bonus) {
-                        bad |= !(q[i] >= 0.0f && q[i] < CUDART_INF_F);
-                        const float r = p - q[i];
-                        if (r > 0.0f) best_r = max(best_r, candidate(r / e, k + i));
+                for (int r = 0; r < kU; ++r) {
+                    const int k = k0 + 8 * lane + 8 * r * kThreads;
+                    load8(lg, a.vec_logits, k, c1, -CUDART_INF_F, x[r]);
+                    if (!bonus) load8(dr, a.vec_draft, k, c1, 0.0f, q[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < kU; ++r) {
+                    const int k = k0 + 8 * lane + 8 * r * kThreads;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p = weight(a, x[r][i], v.x) * inv;
+                        const float rest = bonus ? 0.0f : p - q[r][i];
+                        if (!bonus) bad |= !(q[r][i] >= 0.0f && q[r][i] < CUDART_INF_F);
+                        // U = (n + 1/2) / 2^23, 1 - U = (2^23 - n - 1/2) / 2^23; the bound is a little generous
+                        const float n = noise_level(a.seed, (uint32_t)row, (uint32_t)(k + i));
+                        const float gap = (8388607.5f - n) * (0.9999f / 8388608.0f);
+                        const bool try_p = p > 0.0f && p >= top_p * gap, try_r = rest > 0.0f && rest >= top_r * gap;
+                        // p can only be wanted while no residual is positive
+                        if (try_r || (try_p && (bonus || top_r == 0.0f))) {
+                            const float e = -logf((n + 0.5f) * (1.0f / 8388608.0f));
+                            if (try_r) best_r = max(best_r, candidate(rest / e, k + i));
+                            if (try_p) best_p = max(best_p, candidate(p / e, k + i));
+                        }
                     }
+                    top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best_r >> 32)));
+                    top_p = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best_p >> 32)));
                 }
             }
         }

@@ -2,12 +2,9 @@
 //
 // select_kernel, one thread-block cluster per (layer, slot, kv head) row: a radix
 // select over the masses' order keys finds the k-th largest (k = budget minus the
-// protected positions) exactly, 8 bits at a time.  Every CTA of the cluster counts its
-// own contiguous segment into a shared-memory histogram with a column, and so a
-// bank, per lane: masses bunch in a few bins, and one counter per bin would serialise
-// the lanes of a warp (2,048 single counters, three levels: 231 us at 32 rows of
-// 655,360, against 14 us at one of 5,000).  The cluster adds the totals through
-// distributed shared memory and every CTA walks them itself.  Then
+// protected positions) exactly, 11 + 11 + 10 bits.  Every CTA of the cluster counts
+// its own contiguous segment in shared memory; the cluster adds the histograms
+// through distributed shared memory and every CTA walks the totals itself.  Then
 // each CTA takes its segment in order (ballots within a warp, a scan over the warps)
 // and writes positions and masses at their final ranks: the CTAs before it hold
 // known counts above and at the threshold, and of the positions at the threshold
@@ -41,8 +38,8 @@ constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kPerLane = 8;                               // elements of a lane per ordered tile
 constexpr int kTileElems = kSelThreads * kPerLane;
-constexpr int kBins = 256;
-constexpr int kLevels = 4;
+constexpr int kBins = 2048;
+constexpr int kLevels = 3;
 constexpr int kMaxCluster = 8;
 
 struct EvictArgs {
@@ -110,8 +107,8 @@ __device__ __forceinline__ int warp_scan(int v) {   // inclusive
 }
 
 struct __align__(16) SelectSmem {
-    int hist[kBins][32];        // a column per lane
-    int total[kLevels][kBins];  // this CTA's counts
+    int hist[kLevels][kBins];   // this CTA's counts
+    int coarse[kLevels][64];    // and of 32 bins each
     int warp_a[kSelWarps];
     int warp_b[kSelWarps];
     int found_bin;
@@ -154,6 +151,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs 
     const int begin = min(hi, lo + rank * seg), end = min(hi, begin + seg);
 
     if (tid < 2) sm.local[tid] = 0;
+    for (int i = tid; i < kLevels * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(&sm.hist[0][0])[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
     uint32_t prefix = 0u;                                  // key bits found so far
     int want = k;                                          // entries still to take at or below the prefix's range
@@ -174,66 +172,75 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs 
     auto count_tile = [&](int t0, int level) {
         const int i0 = t0 + warp * 32 * kPerLane + lane;
         const int left = end - i0;                         // entry j exists if 32 j < left
-        const int shift = 24 - 8 * level;
 #pragma unroll
         for (int j = 0; j < kPerLane; ++j) {
             const uint32_t key = mass_key(x[j]);
-            const bool in = level == 0 || (key >> (shift + 8)) == prefix;
-            if (in && 32 * j < left) atomicAdd(&sm.hist[(key >> shift) & (kBins - 1)][lane], 1);
+            const bool in = level == 0 || (level == 1 ? key >> 21 : key >> 10) == prefix;
+            const uint32_t bin = level == 0 ? key >> 21 : (level == 1 ? (key >> 10) & 2047u : key & 1023u);
+            if (in && 32 * j < left) atomicAdd(&sm.hist[level][bin], 1);
             if (level == 0) nan |= x[j] != x[j];
         }
     };
     const bool resident = end - begin <= kTileElems;       // one tile: loaded once
     if (resident) load_tile(begin);
     if (k > 0 && k < count) {
-#pragma unroll 1
+#pragma unroll
         for (int level = 0; level < kLevels; ++level) {
-            for (int i = tid; i < kBins * 32 / 4; i += kSelThreads) reinterpret_cast<int4*>(&sm.hist[0][0])[i] = make_int4(0, 0, 0, 0);
-            __syncthreads();
 #pragma unroll 1
             for (int t0 = begin; t0 < end; t0 += kTileElems) {
                 if (!resident) load_tile(t0);
                 count_tile(t0, level);
             }
             __syncthreads();
-            {   // two threads add a bin's 32 columns, 16 bytes at a time
-                const int b = tid >> 1, c0 = tid & 1;
+            {   // thread t adds bins 4 t .. 4 t + 3, eight threads a coarse bin
+                const int4 u = reinterpret_cast<const int4*>(&sm.hist[level][0])[tid];
+                int t = (u.x + u.y) + (u.z + u.w);
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                if ((tid & 7) == 0) sm.coarse[level][tid >> 3] = t;
+            }
+            if (C > 1) cluster.sync();
+            else __syncthreads();
+            if (warp == 0) {
+                // from the top: the coarse bin that holds the want-th entry of the cluster, then the bin
+                int hi_t = 0, lo_t = 0;
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < C) {
+                        const int* p = cluster.map_shared_rank(&sm.coarse[level][0], c);
+                        hi_t += p[63 - 2 * lane];
+                        lo_t += p[62 - 2 * lane];
+                    }
+                int incl = warp_scan(hi_t + lo_t);
+                int before = incl - hi_t - lo_t;
+                int hit = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
+                const bool second = before + hi_t < want;            // of the hitting lane's two
+                const int cb = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), hit);
+                const int above_c = __shfl_sync(0xffffffffu, before + (second ? hi_t : 0), hit);
                 int t = 0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int4 u = reinterpret_cast<const int4*>(&sm.hist[b][0])[2 * ((c + b) & 3) + c0];
-                    t += (u.x + u.y) + (u.z + u.w);
-                }
-                t += __shfl_xor_sync(0xffffffffu, t, 1);
-                if (c0 == 0) sm.total[level][b] = t;
-            }
-            cluster.sync();
-            // the bin, from the top, that holds the want-th entry of the cluster
-            const int bin = kBins - 1 - tid;
-            int t = 0;
-            if (tid < kBins)
-                for (int c = 0; c < C; ++c) t += cluster.map_shared_rank(&sm.total[level][0], c)[bin];
-            const int incl = warp_scan(t);
-            if (lane == 31) sm.warp_a[warp] = incl;
-            __syncthreads();
-            if (tid < kBins) {
-                int before = incl - t;
-                for (int w = 0; w < warp; ++w) before += sm.warp_a[w];
-                if (before < want && before + t >= want) {
-                    sm.found_bin = bin;
-                    sm.found_above = before;
+                for (int c = 0; c < kMaxCluster; ++c)
+                    if (c < C) t += cluster.map_shared_rank(&sm.hist[level][0], c)[32 * cb + 31 - lane];
+                incl = above_c + warp_scan(t);
+                hit = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
+                if (lane == hit) {
+                    sm.found_bin = 32 * cb + 31 - lane;
+                    sm.found_above = incl - t;
                 }
             }
             __syncthreads();
             const int found = sm.found_bin;
             want -= sm.found_above;
             // this CTA's entries above the bin
-            if (warp < kBins / 32) {
-                const int above = warp_sum(tid > found ? sm.total[level][tid] : 0);
+            int above = 0;
+            if (tid < 64) above = tid > (found >> 5) ? sm.coarse[level][tid] : 0;
+            else if (tid < 96) above = (tid & 31) > (found & 31) ? sm.hist[level][(found & ~31) + (tid & 31)] : 0;
+            if (warp < 3) {
+                above = warp_sum(above);
                 if (lane == 0 && above) atomicAdd(&sm.local[0], above);
             }
-            if (level == kLevels - 1 && tid == 0) sm.local[1] = sm.total[level][found];
-            prefix = (prefix << 8) | (uint32_t)found;
+            if (level == kLevels - 1 && tid == 0) sm.local[1] = sm.hist[level][found];
+            prefix = (prefix << (level == 2 ? 10 : 11)) | (uint32_t)found;
             __syncthreads();
         }
     } else {
@@ -248,7 +255,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs 
     }
     if (__any_sync(0xffffffffu, nan) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
     const bool all = k == count;
-    cluster.sync();                                        // local counts are complete everywhere
+    if (C > 1) cluster.sync();                             // local counts are complete everywhere
     int above_before = 0, ties_before = 0;
     for (int c = 0; c < rank; ++c) {
         const int* l = cluster.map_shared_rank(&sm.local[0], c);
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs 
             }
         }
     }
-    cluster.sync();                                        // no CTA leaves while its counts are read
+    if (C > 1) cluster.sync();                             // no CTA leaves while its counts are read
 }
 
 // Units of U bytes of the kept K (kv = 0) or V (kv = 1) records.
@@ -460,10 +467,10 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
     const int64_t rows = (int64_t)num_call_layers * num_slots * desc->num_kv_heads;
     if (rows * kMaxCluster > INT32_MAX) return Q3KV_ERR_UNSUPPORTED;
     if (work) {
-        // cluster size: enough CTAs to cover the GPU about twice (two of 1,024 threads fit an
-        // SM), and no CTA with less than one tile
+        // cluster size: segments of one tile (registers) where eight CTAs reach that, and no
+        // more CTAs than run at once (two per SM)
         int c = kMaxCluster;
-        while (c > 1 && (rows * c > 2 * (int64_t)sms || (int64_t)c * kTileElems > max_ctx_len)) c >>= 1;
+        while (c > 1 && (rows * c > 2 * (int64_t)sms || (int64_t)(c / 2) * kTileElems >= max_ctx_len)) c >>= 1;
         cudaError_t ce = launch_pdl(select_kernel, dim3((unsigned)(rows * c)), kSelThreads, c, a, st);
         if (ce != cudaSuccess) return cuda_status(ce);
         ce = fmt == kFmtFp8 ? launch_gather<kFmtFp8>(a, st)

@@ -15,15 +15,20 @@ __device__ __forceinline__ bool beats(float av, int ai, float bv, int bi) {
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// U of the counter-based SplitMix64 stream: ((z >> 41) + 0.5) / 2^23 with z
-// output number row * 2^32 + x of the stream seeded with `seed`.
-__device__ __forceinline__ float noise_uniform(uint64_t seed, uint32_t row, uint32_t x) {
+// z >> 41 with z output number row * 2^32 + x of the counter-based SplitMix64
+// stream seeded with `seed`.
+__device__ __forceinline__ float noise_level(uint64_t seed, uint32_t row, uint32_t x) {
     const uint64_t k = ((uint64_t)row << 32) + x;
     uint64_t z = seed + (k + 1ull) * 0x9E3779B97F4A7C15ull;
     z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
     z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
     z ^= z >> 31;
-    return ((float)(uint32_t)(z >> 41) + 0.5f) * (1.0f / 8388608.0f);
+    return (float)(uint32_t)(z >> 41);
+}
+
+// U = ((z >> 41) + 0.5) / 2^23.
+__device__ __forceinline__ float noise_uniform(uint64_t seed, uint32_t row, uint32_t x) {
+    return (noise_level(seed, row, x) + 0.5f) * (1.0f / 8388608.0f);
 }
 
 }  // namespace q3kv
