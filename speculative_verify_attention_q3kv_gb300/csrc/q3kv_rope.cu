@@ -200,7 +200,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
 uint64_t turns_of(double f) {
     const double two_pi = 6.283185307179586476925286766559;
     const double x = f / two_pi * 18446744073709551616.0;
-    return (uint64_t)x;
+    return (uint64_t)(x + 0.5);
 }
 
 bool rows_ok(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int32_t heads, size_t esize) {

@@ -224,3 +224,17 @@ def test_output_follows_the_target():
     assert np.all(np.abs(bonus - p.cpu().numpy()) < 0.03), bonus
     # accepted with probability sum min(p, q) = 0.1 + 0.3 + 0.15 + 0.05
     assert abs((acc == 1).mean() - 0.6) < 0.02
+
+
+def test_no_rows_and_no_slots():
+    """Idle slots with no logits rows at all, and a call without slots."""
+    lg = torch.zeros((0, 77), device="cuda")
+    z = torch.zeros(0, device="cuda")
+    ws = torch.full((api.accept_draft_workspace_bytes(3, 0, 77),), 9, dtype=torch.uint8, device="cuda")
+    acc, nxt, com = i32([5] * 3), i32([5] * 3), i32([5] * 3)
+    api.accept_draft(lg, lg, i32([0] * 3), i32([0] * 3), i32([]), 4, i32([10, 20, 30]), 1.0, z, 1, acc, nxt, com, ws)
+    torch.cuda.synchronize()
+    assert acc.tolist() == [0] * 3 and nxt.tolist() == [-1] * 3 and com.tolist() == [10, 20, 30]
+    e = i32([])
+    api.accept_draft(lg, lg, e, e, i32([]), 4, e, 1.0, z, 1, e, e, e, None)
+    torch.cuda.synchronize()

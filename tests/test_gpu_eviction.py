@@ -426,3 +426,69 @@ def test_evict_captured_and_replayed():
     outs = out.cpu().numpy()
     outs[:, 1, :, 400:] = -9.0
     _check_evict(c, before, lengths, budgets, 2, 50, mass, 0, (kept_h, outs, n.cpu().numpy(), dst.cpu().numpy()))
+
+
+def test_mass_many_slots_with_invalid_ones_between():
+    """More slots than a warp, more segments than CTAs; invalid and idle slots take no part."""
+    rng = np.random.default_rng(2)
+    lengths = [int(x) for x in rng.integers(1, 700, 75)]
+    widths = [int(min(n, t)) for n, t in zip(lengths, rng.integers(0, 17, 75))]
+    c = Cache("q3", lengths, 2, seed=33)
+    q = queries(sum(widths), 16, 5, torch.bfloat16)
+    lse = _lse_of(c, lengths, widths, q, 0)
+    told = list(widths)
+    told[3] = 17                                        # above the host bound
+    told[40] = lengths[40] + 1 if lengths[40] < 16 else 99
+    mass = torch.rand((75, 2, 800), device="cuda")
+    old = mass.clone()
+    st = i32([0])
+    MASS["q3"](c.desc, c.pool, c.page_table, i32(lengths), i32(told), offsets(widths), 700, 16, 0, q, lse, 1.0, mass, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == _lib.Q3KV_STATUS_BAD_LENGTH
+    for b in (3, 40):
+        assert torch.equal(mass[b], old[b])
+    for b in range(75):
+        if b not in (3, 40) and widths[b] and b % 7 < 2:
+            _check_one(c, mass, old, lengths, widths, q, lse, b)
+        elif not widths[b]:
+            assert torch.equal(mass[b], old[b])
+
+
+def _check_one(c, got, old, lengths, widths, q, lse, b):
+    n, t, r0 = lengths[b], widths[b], sum(widths[:b])
+    for g in range(c.kv):
+        s, bound = _reference(c, lengths, widths, q, 0, b, g)
+        l = lse[r0:r0 + t, 8 * g:8 * g + 8].double().cpu().numpy().reshape(-1)
+        want = ev.mass(old[b, g].double().cpu().numpy()[:n], s, l, 1.0, n - t)
+        w, seen = np.exp(s - l[:, None]), np.isfinite(s)
+        rel = np.where(seen, bound + 2.0 ** -22 * (1 + np.abs(np.where(seen, s, 0)) + np.abs(l[:, None])), 0)
+        tol = (w * rel).sum(axis=0) + 130 * 2.0 ** -23 * np.abs(want) + 1e-37
+        assert np.all(np.abs(got[b, g].double().cpu().numpy()[:n] - want) <= tol)
+
+
+def test_mass_captured_replayed_and_on_another_stream():
+    lengths, widths = [1000, 400], [4, 9]
+    c = Cache("fp8", lengths, 2, seed=14)
+    q = queries(13, 16, 8)
+    lse = _lse_of(c, lengths, widths, q, 0)
+    ctx, nq, off = i32(lengths), i32(widths), offsets(widths)
+    mass = torch.zeros((2, 2, 1000), device="cuda")
+    call = lambda m: api.fp8_attn_mass(c.desc, c.pool, c.page_table, ctx, nq, off, 1000, 9, 0, q, lse, 1.0, m)  # noqa: E731
+    call(mass)
+    torch.cuda.synchronize()
+    want = mass.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(mass)
+    mass.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(mass, want)
+    side, other = torch.cuda.Stream(), torch.zeros_like(mass)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        call(other)
+    third = torch.zeros_like(mass)
+    call(third)                                         # two calls at once, on two streams
+    torch.cuda.synchronize()
+    assert torch.equal(other, want) and torch.equal(third, want)
