@@ -507,7 +507,6 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
 #pragma unroll
                     for (int gi = 0; gi < G; ++gi) {
                         const float scale = part_scale<FMT>(sc, part, gi);
-                        const unsigned long long s2 = pack2(scale, scale);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             if (h < halves) {
@@ -520,8 +519,13 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
                                     if (lane == 0) mbar_arrive(&bar.acc_free[c % kFreeBars]);
                                 }
 #pragma unroll
-                                for (int k = 0; k < LD / 2; ++k)
-                                    acc[16 * h + k] = fma2(pack2(x[2 * k], x[2 * k + 1]), s2, acc[16 * h + k]);
+                                for (int k = 0; k < LD / 2; ++k) {
+                                    // single multiply-adds here: 512 a tile spread over both FMA pipes, where
+                                    // the paired form goes to one of them (8 tokens: 110 -> 106 us)
+                                    float a0, a1;
+                                    unpack2(acc[16 * h + k], a0, a1);
+                                    acc[16 * h + k] = pack2(fmaf(x[2 * k], scale, a0), fmaf(x[2 * k + 1], scale, a1));
+                                }
                             }
                     }
                 }
