@@ -38,8 +38,8 @@
 // TMEM (512 columns): operand (128, turbo5k 256) | ring of accumulator slots (3 for more
 // than 32 rows, 6, or 12 for at most 16).
 //
-// Work: the tiles of all (slot, kv head) pairs in one sequence, an equal share per
-// CTA (one per SM), whatever the slots' lengths; a CTA rotates and splits the
+// Work: the tiles of all (slot, kv head) pairs in one sequence, a share of about equal
+// size per CTA (one per SM), whatever the slots' lengths; a CTA rotates and splits the
 // queries of a pair itself when it enters it.
 //
 // Every mbarrier wait is bounded; on a timeout the CTA sets Q3KV_STATUS_TIMEOUT, stops
@@ -186,6 +186,53 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigne
     unsigned long long r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
+}
+
+// Shares that stay within one (slot, kv head) pair, where the CTAs reach: the smallest d for
+// which giving every pair ceil(tiles / d) CTAs takes no more than the grid.  A pair change
+// drains the pipeline and prepares other queries, some 4 us (8 ragged slots x 2 heads on
+// 152 CTAs: 19.5 us with even shares, 16.1 us).  One warp, a lane per slot; false if there are more
+// than 32 slots or more pairs than CTAs (even shares are then better).
+__device__ inline bool whole_shares(const MassArgs& a, int* slot, long long* base, long long* w0, long long* w1, bool* bad) {
+    if (a.num_slots > 32) return false;
+    const int lane = threadIdx.x & 31, G = gridDim.x, H = a.num_kv_heads;
+    const int tiles = lane < a.num_slots ? slot_tiles(a, lane, bad) : 0;
+    const int slots = __popc(__ballot_sync(0xffffffffu, tiles > 0)), per = G / H;   // CTAs per kv head
+    if (slots > per || slots == 0) return slots == 0;
+    // d = ceil(total / (per - slots)) fits, as ceil(x / d) <= x / d + 1; d below total / per does not
+    const int total = warp_sum_i(tiles);
+    int lo = (total + per - 1) / per - 1;                  // does not fit
+    int hi = slots < per ? (total + (per - slots) - 1) / (per - slots) : warp_max_i(tiles);
+    if (hi > lo + 1 && warp_sum_i((tiles + lo) / (lo + 1)) <= per) hi = lo + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (warp_sum_i((tiles + mid - 1) / mid) <= per) hi = mid;
+        else lo = mid;
+    }
+    const int ctas = (tiles + hi - 1) / hi;                // per pair of this lane's slot
+    int incl = ctas * H;
+    long long tincl = (long long)tiles * H;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        const long long t = __shfl_up_sync(0xffffffffu, tincl, o);
+        if (lane >= o) {
+            incl += u;
+            tincl += t;
+        }
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > (int)blockIdx.x);
+    if (!hit) return true;                                 // no tiles are left for this CTA
+    const int l = __ffs(hit) - 1;
+    const int n = __shfl_sync(0xffffffffu, tiles, l), k = __shfl_sync(0xffffffffu, ctas, l);
+    const int r = (int)blockIdx.x - __shfl_sync(0xffffffffu, incl - ctas * H, l);
+    const int i = r % k;
+    *slot = l;
+    *base = __shfl_sync(0xffffffffu, tincl - (long long)tiles * H, l);
+    const long long first = *base + (long long)(r / k) * n;
+    *w0 = first + (long long)n * i / k;
+    *w1 = first + (long long)n * (i + 1) / k;
+    return true;
 }
 
 // With at most 32 query rows the accumulators leave TMEM for a second operand buffer, so
@@ -593,31 +640,37 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (warp == 0) {
         // this CTA's share [w0, w1) of the sequence, and the slot it starts in
         bool bad = false;
-        long long total = 0;
-        for (int b0 = 0; b0 < a.num_slots; b0 += 32)
-            total += warp_sum_i(b0 + lane < a.num_slots ? slot_tiles(a, b0 + lane, &bad) : 0);
-        if (blockIdx.x == 0 && bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
-        total *= a.num_kv_heads;
-        const long long w0 = total * blockIdx.x / gridDim.x, w1 = total * (blockIdx.x + 1) / gridDim.x;
-        long long base = 0;
-        int slot = a.num_slots;
-        for (int b0 = 0; b0 < a.num_slots && w0 < w1; b0 += 32) {
-            const long long mine = b0 + lane < a.num_slots ? (long long)slot_tiles(a, b0 + lane, &bad) * a.num_kv_heads : 0;
-            long long incl = mine;
+        long long w0 = 0, w1 = 0, base = 0;
+        int slot = 0;
+        if (!whole_shares(a, &slot, &base, &w0, &w1, &bad)) {
+            long long total = 0;
+            for (int b0 = 0; b0 < a.num_slots; b0 += 32)
+                total += warp_sum_i(b0 + lane < a.num_slots ? slot_tiles(a, b0 + lane, &bad) : 0);
+            total *= a.num_kv_heads;
+            w0 = total * blockIdx.x / gridDim.x;
+            w1 = total * (blockIdx.x + 1) / gridDim.x;
+            slot = a.num_slots;
+            bool ignore = false;
+            for (int b0 = 0; b0 < a.num_slots && w0 < w1; b0 += 32) {
+                const long long mine =
+                    b0 + lane < a.num_slots ? (long long)slot_tiles(a, b0 + lane, &ignore) * a.num_kv_heads : 0;
+                long long incl = mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += u;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += u;
+                }
+                const unsigned hit = __ballot_sync(0xffffffffu, base + incl > w0);
+                if (hit) {
+                    const int l = __ffs(hit) - 1;
+                    slot = b0 + l;
+                    base += __shfl_sync(0xffffffffu, incl - mine, l);
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, base + incl > w0);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                slot = b0 + l;
-                base += __shfl_sync(0xffffffffu, incl - mine, l);
-                break;
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
         }
+        if (blockIdx.x == 0 && bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
         if (lane == 0) {
             sm.walk = Walk{w0, w1, base, slot, 0, 0, 0, 0};
             next_segment<FMT>(a, sm, 0);
