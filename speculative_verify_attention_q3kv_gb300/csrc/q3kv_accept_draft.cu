@@ -17,6 +17,9 @@
 // its chunk of row a.  The race's winner is a 64-bit atomic maximum of (key,
 // ~index) per slot, whatever the order; the slot's last CTA stores the results.
 //
+// 8 slots x 1 to 8 tokens, vocab 248,320, bf16: 22.0 us, of which the bytes alone are 3.2;
+// 1 slot x 6 tokens 13.5 us: two launches and about eight dependent trips to L2 or HBM.
+//
 // Issue slots decide beside that: the statistics take six instructions an entry
 // (bad logits show in the sum, not per entry), and the race computes a clock only
 // where it can win: E = -log U >= 1 - U, so r / E <= r / (1 - U), which the noise's

@@ -35,12 +35,20 @@
 //                    starts a K = 16 MMA about every 45 cycles, so four issue
 //   P   warps 20-23  copy the records of the tiles ahead into shared memory, one stage per
 //                    tile (one bulk copy; 16-byte cp.async where the stage is padded)
-// TMEM (512 columns): operand (128, turbo5k 256) | ring of accumulator slots (3 for more
-// than 32 rows, 6, or 12 for at most 16).
+// TMEM (512 columns): one or two operand buffers (128 columns each, turbo5k 256) | ring of
+// accumulator slots (see `double_buffered` and `acc_slots`).
 //
 // Work: the tiles of all (slot, kv head) pairs in one sequence, a share of about equal
 // size per CTA (one per SM), whatever the slots' lengths; a CTA rotates and splits the
 // queries of a pair itself when it enters it.
+//
+// Bound: not memory.  655,360 positions x 8 tokens x 2 kv heads take 106.7 us, 1,470 GB/s
+// of K records and masses (the bytes alone: 23 us; the tensor pipe is 24 % active).  A tile
+// of 64 rows takes about 3,100 cycles a CTA: its epilogue multiplies 128 x 64 x 8
+// accumulators by their scales and takes 8,192 exponentials, about 5,300 cycles for each
+// of two warps a lane quarter, and the ring holds three parts.  At 16 rows (68.9 us) the
+// conversion of the records decides, about 2,100 cycles a tile.  With 28 or 32 warps or one
+// event per accumulator the chain of waits gets longer (118 to 142 us).
 //
 // Every mbarrier wait is bounded; on a timeout the CTA sets Q3KV_STATUS_TIMEOUT, stops
 // issuing, waits (bounded) for its MMAs in flight, frees its TMEM and returns.
@@ -236,9 +244,9 @@ __device__ inline bool whole_shares(const MassArgs& a, int* slot, long long* bas
 }
 
 // With at most 32 query rows the accumulators leave TMEM for a second operand buffer, so
-// the conversion of a tile overlaps the products of the one before it (8 slots x 1 token of
-// 655,360 positions: 74 -> 64 us; more rows need the columns for a deeper ring).  A
-// turbo5k operand has two fp16 parts and no room for that.
+// the conversion of a tile overlaps the products of the one before it (655,360 positions, 2 kv
+// heads: 74 -> 69 us with 1 token, 79 -> 76 us with 4; more rows need the columns for a
+// deeper ring).  A turbo5k operand has two fp16 parts and no room for that.
 template <int FMT>
 __host__ __device__ constexpr bool double_buffered(int tokens) {
     return Mf<FMT>::kOps == 1 && kGroup * tokens <= 32;

@@ -2,30 +2,40 @@
 //
 // select_kernel, one thread-block cluster per (layer, slot, kv head) row: a radix
 // select over the masses' order keys finds the k-th largest (k = budget minus the
-// protected positions) exactly, 11 + 11 + 10 bits.  Every CTA of the cluster counts
-// its own contiguous segment in shared memory; the cluster adds the histograms
-// through distributed shared memory and every CTA walks the totals itself.  Then
-// each CTA takes its segment in order (ballots within a warp, a scan over the warps)
-// and writes positions and masses at their final ranks: the CTAs before it hold
-// known counts above and at the threshold, and of the positions at the threshold
-// the lowest ones are taken.  No float is added, so nothing depends on an order.
-// A segment of at most 4,096 positions stays in registers over the five passes;
-// longer ones are read again, from L2, with eight loads of a thread in flight.  512
-// threads of at most 64 registers let two CTAs share an SM, so that the clusters of
-// 38 rows run at once (one CTA of 1,024 threads per SM left room for a dozen).
+// protected positions) exactly, 11 + 11 + 10 bits.  A warp has a consecutive share of
+// the row: the first pass (HBM) counts the leading 11 bits in shared memory; the second
+// (L2) counts what lies above the found bin and puts the bin's own masses, compared as
+// floats, into the warp's list, from which the other two levels count; the last (L2)
+// writes positions and masses at their final ranks, with no barrier inside, as the
+// warps before it have known counts above the threshold and at it, of which the lowest
+// positions are taken.  A list that overflows (more than 512 masses of a warp in one bin)
+// is replaced by reading the share again.  A share of at most 256 masses stays in
+// registers.  No float is added, so nothing depends on an order.
+//
+// A level's bin: 64 coarse counts go to every CTA of the cluster (distributed shared
+// memory), then one warp finds the coarse bin that holds the k-th and reads its 32 bins
+// from every CTA; reading all bins of all CTAs took longer than counting.
+//
+// 512 threads of at most 64 registers let two CTAs share an SM.  The lists are short
+// because the L1 lines that loads in flight need come out of the same 256 KB: with lists of
+// 1,024 masses 32 rows of 655,360 took 60 us more.
 //
 // gather_kernel: a CTA moves up to 256 kept records, one destination page, of K and V:
 // their source offsets go to shared memory first, so all 16-byte loads (4-byte ones
 // for the 164-byte K records) of a thread are independent, and the stores, to
 // consecutive records, coalesce.
 //
-// Bound: memory (masses read once from HBM and again from L2, kept records read
-// and written once; a 112-byte record scattered over 64-byte DRAM bursts costs about
-// half as much again to read).
+// Bound: memory.  32 rows of 655,360 masses, 65,536 kept, take 269 us: select 71 us (84 MB
+// from HBM once and from L2 twice; about a third each for the first pass, the second with
+// the levels, and the last), gather 198 us (470 MB of records read and written; a
+// scattered 112-byte record touches 64-byte DRAM bursts worth half as much again, with
+// which the traffic alone takes 173 us).  2 rows of 5,000: 13.7 us, where each of the three
+// levels costs a cluster barrier and a trip to the other CTAs, 1.5 us.
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "q3kv_internal.h"
 
@@ -36,11 +46,15 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kPerLane = 8;                               // elements of a lane per ordered tile
-constexpr int kTileElems = kSelThreads * kPerLane;
+constexpr int kPerLane = 8;                               // masses of a lane per tile
+constexpr int kTile = 32 * kPerLane;                      // a warp's
 constexpr int kBins = 2048;
+constexpr int kCoarse = kBins / 32;
 constexpr int kLevels = 3;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+constexpr int kListCap = 512;
+constexpr uint32_t kKeyInf = 0xff800000u, kKeyMinusInf = 0x007fffffu;   // order keys of the infinities
+static_assert(kBins == 4 * kSelThreads && kMaxCluster <= 32, "find_bin");
 
 struct EvictArgs {
     uint8_t* pool;
@@ -60,6 +74,7 @@ struct EvictArgs {
     int32_t* kept;
     float* mass_out;
     int32_t* new_len;
+    int32_t late_len;            // new_len is ctx_len or budget: length_kernel writes it
     int32_t* status;
     int32_t num_layers, num_kv_heads, num_pages;
 };
@@ -91,6 +106,11 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
     return x == x ? key : 0u;
 }
 
+// The float with an order key (of a number that is not NaN).
+__device__ __forceinline__ float key_float(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
 __device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -107,30 +127,32 @@ __device__ __forceinline__ int warp_scan(int v) {   // inclusive
 }
 
 struct __align__(16) SelectSmem {
-    int hist[kLevels][kBins];   // this CTA's counts
-    int coarse[kLevels][64];    // and of 32 bins each
-    int warp_a[kSelWarps];
-    int warp_b[kSelWarps];
+    int hist[kLevels][kBins];                  // this CTA's counts
+    int coarse[2][kMaxCluster][kCoarse];       // every CTA's counts of 32 bins each, by level % 2
+    int2 total[kMaxCluster];                   // every CTA's entries above the threshold, and at it
+    int2 warp[kSelWarps];                      // the same of this CTA's warps
     int found_bin;
-    int found_above;            // entries in bins above it
-    int local[2];               // this CTA's entries above the threshold, and at it
+    int found_above;                           // entries in bins above it
+    float list[kSelWarps][kListCap];           // a warp's masses in the first level's bin
 };
 
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs a) {
-    __shared__ SelectSmem sm;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_raw);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks();
     const int rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t below = (1u << lane) - 1u;
     const int64_t row = blockIdx.x / C;                    // (layer, slot, kv head)
     const int slot = (int)(row / a.num_kv_heads) % a.num_slots;
     const SlotPlan s = slot_plan(a, slot);
     if (rank == 0 && tid == 0 && row % a.num_kv_heads == 0 && row / a.num_kv_heads < a.num_slots) {   // one per slot
         if (s.bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
-        // where new_len is the array ctx_len, length_kernel writes it when every kernel has read it
-        if (a.new_len != a.ctx_len) a.new_len[slot] = s.n > 0 ? s.n : s.L;
+        // where new_len is an array the plans read, length_kernel writes it when every kernel has read it
+        if (!a.late_len) a.new_len[slot] = s.n > 0 ? s.n : s.L;
     }
     if (s.n == 0) return;                                  // the whole cluster agrees
 
@@ -146,167 +168,252 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs 
         kept[dst] = pos;
         if (mass_out) mass_out[dst] = m[pos];
     }
+    if (k == 0) return;
+    if (C > 1) cluster.barrier_arrive();                   // waited for before the first access to another CTA
+    // a warp's share of the free positions, consecutive in the order (CTA, warp)
     const int count = hi - lo;
-    const int seg = ((count + C - 1) / C + 31) / 32 * 32;
-    const int begin = min(hi, lo + rank * seg), end = min(hi, begin + seg);
+    const int parts = C * kSelWarps;
+    const int seg = ((count + parts - 1) / parts + 31) / 32 * 32;
+    const int begin = min(hi, lo + (rank * kSelWarps + warp) * seg), end = min(hi, begin + seg);
+    const bool resident = seg <= kTile;                    // one tile: loaded once
+    const float kNan = __int_as_float(0x7fffffff);
 
-    if (tid < 2) sm.local[tid] = 0;
-    for (int i = tid; i < kLevels * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(&sm.hist[0][0])[i] = make_int4(0, 0, 0, 0);
-    __syncthreads();
-    uint32_t prefix = 0u;                                  // key bits found so far
-    int want = k;                                          // entries still to take at or below the prefix's range
-    bool nan = false;
-    // tile t0 of the segment: a warp has 32 * kPerLane consecutive positions, 32 at a time
-    float x[kPerLane];
-    auto load_tile = [&](int t0) {
-        const int i0 = t0 + warp * 32 * kPerLane + lane;
-        if (t0 + kTileElems <= end) {
+    // A tile: kTile consecutive positions of a warp, 32 at a time; NaN behind the end.
+    auto load = [&](float (&x)[kPerLane], int t0) {
+        const float* p = m + t0 + lane;
+        if (t0 + kTile <= end) {
 #pragma unroll
-            for (int j = 0; j < kPerLane; ++j) x[j] = __ldg(m + i0 + 32 * j);
+            for (int j = 0; j < kPerLane; ++j) x[j] = __ldg(p + 32 * j);
         } else {
 #pragma unroll
-            for (int j = 0; j < kPerLane; ++j) x[j] = i0 + 32 * j < end ? __ldg(m + i0 + 32 * j) : 0.0f;
+            for (int j = 0; j < kPerLane; ++j) x[j] = t0 + 32 * j + lane < end ? __ldg(p + 32 * j) : kNan;
         }
     };
-    // one pass of a radix level over the tile in x: counts the keys that begin with the prefix
-    auto count_tile = [&](int t0, int level) {
-        const int i0 = t0 + warp * 32 * kPerLane + lane;
-        const int left = end - i0;                         // entry j exists if 32 j < left
-#pragma unroll
-        for (int j = 0; j < kPerLane; ++j) {
-            const uint32_t key = mass_key(x[j]);
-            const bool in = level == 0 || (level == 1 ? key >> 21 : key >> 10) == prefix;
-            const uint32_t bin = level == 0 ? key >> 21 : (level == 1 ? (key >> 10) & 2047u : key & 1023u);
-            if (in && 32 * j < left) atomicAdd(&sm.hist[level][bin], 1);
-            if (level == 0) nan |= x[j] != x[j];
+    float x[kPerLane];
+    // f(first position) over the warp's tiles in x, the next tile's loads in flight
+    auto tiles = [&](auto&& f) {
+        if (resident) {
+            if (begin < end) f(begin);
+            return;
         }
-    };
-    const bool resident = end - begin <= kTileElems;       // one tile: loaded once
-    if (resident) load_tile(begin);
-    if (k > 0 && k < count) {
-#pragma unroll
-        for (int level = 0; level < kLevels; ++level) {
+        float y[kPerLane];
+        if (begin < end) load(x, begin);
 #pragma unroll 1
-            for (int t0 = begin; t0 < end; t0 += kTileElems) {
-                if (!resident) load_tile(t0);
-                count_tile(t0, level);
-            }
-            __syncthreads();
-            {   // thread t adds bins 4 t .. 4 t + 3, eight threads a coarse bin
-                const int4 u = reinterpret_cast<const int4*>(&sm.hist[level][0])[tid];
-                int t = (u.x + u.y) + (u.z + u.w);
+        for (int t0 = begin; t0 < end; t0 += kTile) {
+            if (t0 + kTile < end) load(y, t0 + kTile);
+            f(t0);
 #pragma unroll
-                for (int o = 1; o < 8; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                if ((tid & 7) == 0) sm.coarse[level][tid >> 3] = t;
-            }
-            if (C > 1) cluster.sync();
-            else __syncthreads();
-            if (warp == 0) {
-                // from the top: the coarse bin that holds the want-th entry of the cluster, then the bin
-                int hi_t = 0, lo_t = 0;
-#pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < C) {
-                        const int* p = cluster.map_shared_rank(&sm.coarse[level][0], c);
-                        hi_t += p[63 - 2 * lane];
-                        lo_t += p[62 - 2 * lane];
-                    }
-                int incl = warp_scan(hi_t + lo_t);
-                int before = incl - hi_t - lo_t;
-                int hit = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
-                const bool second = before + hi_t < want;            // of the hitting lane's two
-                const int cb = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), hit);
-                const int above_c = __shfl_sync(0xffffffffu, before + (second ? hi_t : 0), hit);
-                int t = 0;
-#pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c)
-                    if (c < C) t += cluster.map_shared_rank(&sm.hist[level][0], c)[32 * cb + 31 - lane];
-                incl = above_c + warp_scan(t);
-                hit = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
-                if (lane == hit) {
-                    sm.found_bin = 32 * cb + 31 - lane;
-                    sm.found_above = incl - t;
-                }
-            }
-            __syncthreads();
-            const int found = sm.found_bin;
-            want -= sm.found_above;
-            // this CTA's entries above the bin
-            int above = 0;
-            if (tid < 64) above = tid > (found >> 5) ? sm.coarse[level][tid] : 0;
-            else if (tid < 96) above = (tid & 31) > (found & 31) ? sm.hist[level][(found & ~31) + (tid & 31)] : 0;
-            if (warp < 3) {
-                above = warp_sum(above);
-                if (lane == 0 && above) atomicAdd(&sm.local[0], above);
-            }
-            if (level == kLevels - 1 && tid == 0) sm.local[1] = sm.hist[level][found];
-            prefix = (prefix << (level == 2 ? 10 : 11)) | (uint32_t)found;
-            __syncthreads();
+            for (int j = 0; j < kPerLane; ++j) x[j] = y[j];
         }
-    } else {
-        // everything or nothing between the protected ends
-        if (k > 0)
-            for (int i = begin + tid; i < end; i += kSelThreads) {
-                const float v = __ldg(m + i);
-                nan |= v != v;
-            }
-        if (tid == 0) sm.local[0] = k > 0 ? end - begin : 0;
+    };
+    if (resident) load(x, begin);
+
+    int want = k;                                          // entries still to take at or below the prefix's range
+    uint32_t prefix = 0u;                                  // key bits found so far
+    // Finds the bin of hist[level] that holds the cluster's want-th entry from the top.
+    auto find_bin = [&](int level) {
         __syncthreads();
+        {   // thread t adds bins 4 t .. 4 t + 3, eight threads a coarse bin, given to every CTA
+            const int4 u = reinterpret_cast<const int4*>(&sm.hist[level][0])[tid];
+            int t = (u.x + u.y) + (u.z + u.w);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            for (int c = tid & 7; c < C; c += 8) *cluster.map_shared_rank(&sm.coarse[level & 1][rank][tid >> 3], c) = t;
+        }
+        if (C > 1) cluster.sync();
+        else __syncthreads();
+        if (warp == 0) {
+            // the coarse bin that holds the want-th entry, then the bin
+            int2 t2 = make_int2(0, 0);                     // bins 62 - 2 lane, 63 - 2 lane
+            for (int c = 0; c < C; ++c) {
+                const int2 u = *reinterpret_cast<const int2*>(&sm.coarse[level & 1][c][62 - 2 * lane]);
+                t2.x += u.x;
+                t2.y += u.y;
+            }
+            int incl = warp_scan(t2.x + t2.y);
+            const int before = incl - t2.x - t2.y;
+            int hit = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
+            const bool second = before + t2.y < want;      // of the hitting lane's two
+            const int cb = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), hit);
+            const int above_c = __shfl_sync(0xffffffffu, before + (second ? t2.y : 0), hit);
+            int t = 0;
+#pragma unroll 1
+            for (int c0 = 0; c0 < C; c0 += 8)              // eight remote loads in flight
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c0 + c < C) t += cluster.map_shared_rank(&sm.hist[level][0], c0 + c)[32 * cb + 31 - lane];
+            incl = above_c + warp_scan(t);
+            hit = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
+            if (lane == hit) {
+                sm.found_bin = 32 * cb + 31 - lane;
+                sm.found_above = incl - t;
+            }
+        }
+        __syncthreads();
+        want -= sm.found_above;
+        return (uint32_t)sm.found_bin;
+    };
+
+    bool nan = false;
+    const bool all = k == count;                           // everything between the protected ends
+    bool nan_thr = false;                                  // the k-th is a NaN
+    float thr = 0.0f;
+    int n_gt = 0, n_eq = 0;                                // the warp's entries above the threshold, and at it
+    if (all) {
+        tiles([&](int t0) {
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j) nan |= x[j] != x[j] && t0 + 32 * j + lane < end;
+        });
+        n_gt = end - begin;
+        if (C > 1) cluster.barrier_wait();
+    } else {
+        for (int i = tid; i < kLevels * kBins / 4; i += kSelThreads)
+            reinterpret_cast<int4*>(&sm.hist[0][0])[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        tiles([&](int t0) {
+            if (t0 + kTile <= end) {
+#pragma unroll
+                for (int j = 0; j < kPerLane; ++j) {
+                    nan |= x[j] != x[j];
+                    atomicAdd(&sm.hist[0][mass_key(x[j]) >> 21], 1);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPerLane; ++j)
+                    if (t0 + 32 * j + lane < end) {
+                        nan |= x[j] != x[j];
+                        atomicAdd(&sm.hist[0][mass_key(x[j]) >> 21], 1);
+                    }
+            }
+        });
+        if (C > 1) cluster.barrier_wait();
+        prefix = find_bin(0);
+        nan_thr = prefix == 0u;                            // NaN is alone in bin 0: every number is taken
+        if (!nan_thr) {
+            // the bin's numbers are those of [f_lo, f_hi]; -0 belongs to +0's
+            const float f_lo = key_float(max(prefix << 21, kKeyMinusInf));
+            uint32_t key_hi = min(prefix << 21 | 0x1fffffu, kKeyInf);
+            key_hi -= key_hi == 0x7fffffffu;
+            const float f_hi = key_float(key_hi);
+            int n = 0, above = 0;
+            if (!resident) {
+                float* list = sm.list[warp];
+                tiles([&](int) {
+#pragma unroll
+                    for (int j = 0; j < kPerLane; ++j) {
+                        above += x[j] > f_hi;
+                        const bool in = x[j] >= f_lo && x[j] <= f_hi;
+                        const uint32_t who = __ballot_sync(0xffffffffu, in);
+                        const int at = n + __popc(who & below);
+                        if (in && at < kListCap) list[at] = x[j];
+                        n += __popc(who);
+                    }
+                });
+                __syncwarp();
+            }
+            const bool listed = !resident && n <= kListCap;
+#pragma unroll 1
+            for (int level = 1; level < kLevels; ++level) {
+                const int shift = level == 1 ? 10 : 0, bits = level == 1 ? 11 : 10;
+                auto count_key = [&](float v) {
+                    const uint32_t key = mass_key(v);
+                    if (key >> shift >> bits == prefix) atomicAdd(&sm.hist[level][key >> shift & ((1u << bits) - 1u)], 1);
+                };
+                if (listed) {
+                    for (int i = lane; i < n; i += 32) count_key(sm.list[warp][i]);
+                } else {
+                    tiles([&](int) {                       // NaN (behind the end too) is in no bin but 0
+#pragma unroll
+                        for (int j = 0; j < kPerLane; ++j) count_key(x[j]);
+                    });
+                }
+                prefix = prefix << bits | find_bin(level);
+            }
+            thr = key_float(prefix);
+            if (listed) {
+                for (int i = lane; i < n; i += 32) {
+                    const float v = sm.list[warp][i];
+                    above += v > thr;
+                    n_eq += v == thr;
+                }
+                n_gt = warp_sum(above);
+                n_eq = warp_sum(n_eq);
+            }
+            if (!listed) {
+                above = 0;
+                tiles([&](int) {
+#pragma unroll
+                    for (int j = 0; j < kPerLane; ++j) {
+                        above += x[j] > thr;
+                        n_eq += x[j] == thr;
+                    }
+                });
+                n_gt = warp_sum(above);
+                n_eq = warp_sum(n_eq);
+            }
+        } else {
+            tiles([&](int) {
+#pragma unroll
+                for (int j = 0; j < kPerLane; ++j) n_gt += x[j] == x[j];
+            });
+            n_gt = warp_sum(n_gt);
+            n_eq = end - begin - n_gt;
+        }
     }
     if (__any_sync(0xffffffffu, nan) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
-    const bool all = k == count;
-    if (C > 1) cluster.sync();                             // local counts are complete everywhere
-    int above_before = 0, ties_before = 0;
-    for (int c = 0; c < rank; ++c) {
-        const int* l = cluster.map_shared_rank(&sm.local[0], c);
-        above_before += l[0];
-        ties_before += l[1];
+    // the entries taken before this warp's
+    if (lane == 0) sm.warp[warp] = make_int2(n_gt, n_eq);
+    __syncthreads();
+    if (warp == 0) {
+        const int2 u = lane < kSelWarps ? sm.warp[lane] : make_int2(0, 0);
+        const int2 t = make_int2(warp_sum(u.x), warp_sum(u.y));
+        if (lane < C) *cluster.map_shared_rank(&sm.total[rank], lane) = t;
     }
-    if (k > 0) {
-        // ordered pass
-#pragma unroll 1
-        for (int t0 = begin; t0 < end; t0 += kTileElems) {
-            const int w0 = t0 + warp * 32 * kPerLane;
-            uint32_t gt[kPerLane], eq[kPerLane];
-            int ngt = 0, neq = 0;
-            if (!resident) load_tile(t0);
+    if (C > 1) cluster.sync();                             // the last remote access is done: a CTA may leave
+    else __syncthreads();
+    int2 u = lane < warp ? sm.warp[lane] : make_int2(0, 0);
+    if (lane < rank) {
+        u.x += sm.total[lane].x;
+        u.y += sm.total[lane].y;
+    }
+    int ties = warp_sum(u.y);
+    int at = s.sink + warp_sum(u.x) + min(ties, want);     // where the next taken entry goes
+    tiles([&](int t0) {
+        bool tie = false;
+        uint32_t take[kPerLane];
+        if (all || nan_thr) {
 #pragma unroll
             for (int j = 0; j < kPerLane; ++j) {
-                const int i = w0 + 32 * j + lane;
-                const uint32_t key = mass_key(x[j]);
-                gt[j] = __ballot_sync(0xffffffffu, i < end && (all || key > prefix));
-                eq[j] = __ballot_sync(0xffffffffu, i < end && !all && key == prefix);
-                ngt += __popc(gt[j]);
-                neq += __popc(eq[j]);
+                const bool in = t0 + 32 * j + lane < end;
+                take[j] = __ballot_sync(0xffffffffu, all ? in : x[j] == x[j]);
+                tie |= nan_thr && in && x[j] != x[j];
             }
-            __syncthreads();                               // the previous tile's totals are read
-            if (lane == 0) {
-                sm.warp_a[warp] = ngt;
-                sm.warp_b[warp] = neq;
-            }
-            __syncthreads();
-            const int ca = lane < kSelWarps ? sm.warp_a[lane] : 0, cb = lane < kSelWarps ? sm.warp_b[lane] : 0;
-            int g = above_before + warp_sum(lane < warp ? ca : 0);
-            int e = ties_before + warp_sum(lane < warp ? cb : 0);
-            above_before += warp_sum(ca);
-            ties_before += warp_sum(cb);
-            const uint32_t below = (1u << lane) - 1u;
+        } else {
 #pragma unroll
             for (int j = 0; j < kPerLane; ++j) {
-                const int my_e = e + __popc(eq[j] & below);
-                const bool is_gt = (gt[j] >> lane) & 1u;
-                const bool is_eq = ((eq[j] >> lane) & 1u) && my_e < want;
-                if (is_gt || is_eq) {
-                    const int dst = s.sink + g + __popc(gt[j] & below) + min(my_e, want);
-                    kept[dst] = w0 + 32 * j + lane;
-                    if (mass_out) mass_out[dst] = x[j];
-                }
-                g += __popc(gt[j]);
-                e += __popc(eq[j]);
+                take[j] = __ballot_sync(0xffffffffu, x[j] > thr);
+                tie |= x[j] == thr;
             }
         }
-    }
-    if (C > 1) cluster.sync();                             // no CTA leaves while its counts are read
+        if (__any_sync(0xffffffffu, tie)) {                // the first ones at the threshold
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j) {
+                const bool eq = nan_thr ? x[j] != x[j] && t0 + 32 * j + lane < end : x[j] == thr;
+                const uint32_t who = __ballot_sync(0xffffffffu, eq);
+                take[j] |= __ballot_sync(0xffffffffu, eq && ties + __popc(who & below) < want);
+                ties += __popc(who);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            if (take[j] >> lane & 1u) {
+                const int dst = at + __popc(take[j] & below);
+                kept[dst] = t0 + 32 * j + lane;
+                if (mass_out) mass_out[dst] = x[j];
+            }
+            at += __popc(take[j]);
+        }
+    });
 }
 
 // Units of U bytes of the kept K (kv = 0) or V (kv = 1) records.
@@ -380,7 +487,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const EvictArgs 
     move_records<uint4, (FMT == kFmtFp8 ? kFp8RecordBytes : kRecordBytes) / 16>(a.pool, off[1], n, dv);
 }
 
-// New lengths, after every other kernel of the call has read ctx_len (which may
+// New lengths, after every other kernel of the call has read ctx_len and budget (which may
 // be the same array).
 __global__ void __launch_bounds__(256) length_kernel(const EvictArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -388,12 +495,14 @@ __global__ void __launch_bounds__(256) length_kernel(const EvictArgs a) {
     for (int b = blockIdx.x * 256 + threadIdx.x; b < a.num_slots; b += gridDim.x * 256) {
         const SlotPlan s = slot_plan(a, b);
         a.new_len[b] = s.n > 0 ? s.n : s.L;
+        if (s.bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);   // also of a call without rows
     }
 }
 
 template <typename K>
-cudaError_t launch_pdl(K kernel, dim3 grid, int threads, int cluster, const EvictArgs& a, cudaStream_t stream) {
+cudaError_t launch_pdl(K kernel, dim3 grid, int threads, int cluster, const EvictArgs& a, cudaStream_t stream, size_t smem = 0) {
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
@@ -407,6 +516,21 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, int cluster, const Evic
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+cudaError_t launch_select(const EvictArgs& a, unsigned rows, int cluster, cudaStream_t stream) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelectSmem));
+        if (e != cudaSuccess) return e;
+        const cudaError_t e2 = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e2 != cudaSuccess) return e2;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    return launch_pdl(select_kernel, dim3(rows * (unsigned)cluster), kSelThreads, cluster, a, stream, sizeof(SelectSmem));
 }
 
 template <int FMT>
@@ -429,7 +553,7 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
         n_sink < 0 || n_recent < 0 || layer < 0 || num_call_layers < 0 || mass_stride < max_ctx_len)
         return Q3KV_ERR_INVALID_ARG;
     if (layer > desc->num_layers || num_call_layers > desc->num_layers - layer) return Q3KV_ERR_INVALID_ARG;
-    if (max_ctx_len > (int64_t)INT32_MAX - kPageSize) return Q3KV_ERR_INVALID_ARG;
+    if (max_ctx_len > (int64_t)INT32_MAX - 65536) return Q3KV_ERR_INVALID_ARG;   // positions behind a tile's end are ints
     if (num_slots > 65535) return Q3KV_ERR_UNSUPPORTED;
     if (num_slots == 0) return Q3KV_OK;
     if (!d_ctx_len || !d_budget || !d_new_len) return Q3KV_ERR_INVALID_ARG;
@@ -459,6 +583,7 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
     a.kept = d_kept;
     a.mass_out = d_mass_out;
     a.new_len = d_new_len;
+    a.late_len = d_new_len == d_ctx_len || d_new_len == d_budget;
     a.status = d_status;
     a.num_layers = desc->num_layers;
     a.num_kv_heads = desc->num_kv_heads;
@@ -467,17 +592,18 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
     const int64_t rows = (int64_t)num_call_layers * num_slots * desc->num_kv_heads;
     if (rows * kMaxCluster > INT32_MAX) return Q3KV_ERR_UNSUPPORTED;
     if (work) {
-        // cluster size: segments of one tile (registers) where eight CTAs reach that, and no
-        // more CTAs than run at once (two per SM)
+        // cluster size: up to 16 CTAs a row while each has an SM of its own (2 rows of 655,360: 71 -> 50 us a call,
+        // 8 rows 109 -> 94), else up to 8 of two per SM (16 rows: 165 us, with 16 CTAs 172); half while half keeps a
+        // row in registers
         int c = kMaxCluster;
-        while (c > 1 && (rows * c > 2 * (int64_t)sms || (int64_t)(c / 2) * kTileElems >= max_ctx_len)) c >>= 1;
-        cudaError_t ce = launch_pdl(select_kernel, dim3((unsigned)(rows * c)), kSelThreads, c, a, st);
+        while (c > 1 && (rows * c > (c > 8 ? 1 : 2) * (int64_t)sms || (int64_t)(c / 2) * kSelWarps * kTile >= max_ctx_len)) c >>= 1;
+        cudaError_t ce = launch_select(a, (unsigned)rows, c, st);
         if (ce != cudaSuccess) return cuda_status(ce);
         ce = fmt == kFmtFp8 ? launch_gather<kFmtFp8>(a, st)
                             : (fmt == kFmtT5k ? launch_gather<kFmtT5k>(a, st) : launch_gather<kFmtQ3>(a, st));
         if (ce != cudaSuccess) return cuda_status(ce);
     }
-    if (work && d_new_len != d_ctx_len) return Q3KV_OK;      // the select kernel wrote the lengths
+    if (work && !a.late_len) return Q3KV_OK;      // the select kernel wrote the lengths
     return cuda_status(launch_pdl(length_kernel, dim3((unsigned)std::min(64, (num_slots + 255) / 256)), 256, 0, a, st));
 }
 

@@ -492,3 +492,61 @@ def test_mass_captured_replayed_and_on_another_stream():
     call(third)                                         # two calls at once, on two streams
     torch.cuda.synchronize()
     assert torch.equal(other, want) and torch.equal(third, want)
+
+
+def _long_masses(kind, n, gen):
+    """[2 rows] of n masses: the threshold in a wide first-level bin, in a narrow one, among NaN, and among equal ones."""
+    m = torch.rand((1, 1, 2, n), generator=gen, device="cuda")
+    if kind == "decades":
+        m = 10.0 ** (-12 * m)
+    elif kind == "signed":
+        m = m - 0.5
+        m[..., ::5] = 0.0
+        m[..., 1::5] = -0.0
+        m[..., 7::10007] = float("inf")
+        m[..., 8::10007] = -float("inf")
+    elif kind == "nan":
+        m[..., ::2] = float("nan")
+        m[..., 1::3] = float("nan")
+    elif kind == "equal":
+        m = (m * 2).floor() + 1.0                            # 1 or 2
+    elif kind == "crowded":
+        m = 1.0 + m * 2.0 ** -9                              # one first-level bin holds everything
+    return m
+
+
+@pytest.mark.parametrize("kind", ["decades", "signed", "nan", "equal", "crowded"])
+@pytest.mark.parametrize("n,budget", [(70001, 7000), (70001, 69990), (70001, 35001), (150000, 200)])
+def test_evict_long_rows(kind, n, budget):
+    # more positions per warp than stay in its registers: its masses are read again, or filtered into its list
+    gen = torch.Generator(device="cuda").manual_seed(n + budget)
+    mass = _long_masses(kind, n, gen)
+    c = Cache("q3", [n], 2, seed=13, extra_pages=(budget + 255) // 256)
+    before = c.pool.clone()
+    got = _evict_call(c, [n], [budget], 3, 11, mass, 0, c.status)
+    assert int(c.status.item()) == (_lib.Q3KV_STATUS_NONFINITE_INPUT if kind == "nan" else 0)
+    kept, out, new_len, _ = got
+    assert new_len[0] == budget
+    for g in range(2):
+        want = ev.keep(mass[0, 0, g].cpu().numpy(), budget, 3, 11)
+        assert np.array_equal(kept[0, 0, g], want)
+        assert np.array_equal(out[0, 0, g], mass[0, 0, g].cpu().numpy()[want], equal_nan=True)
+    _check_evict(c, before, [n], [budget], 3, 11, mass, 0, got)
+
+
+def test_evict_length_in_the_budgets_place_and_without_layers():
+    c = Cache("q3", [900, 700], 1, seed=1, extra_pages=4)
+    mass = torch.rand((1, 2, 1, 900), device="cuda")
+    dst = torch.from_numpy(np.asarray(c.free[:4], np.int32).reshape(2, 2)).cuda()
+    kept = torch.zeros((1, 2, 1, 400), dtype=torch.int32, device="cuda")
+    ctx, bud, st = i32([900, 700]), i32([300, 400]), i32([0])
+    api.evict(c.desc, c.pool, c.page_table, ctx, 900, bud, 400, 0, 5, 0, mass, dst, kept, None, bud, st)
+    assert bud.tolist() == [300, 400] and ctx.tolist() == [900, 700] and int(st.item()) == 0
+    for b, n in enumerate((300, 400)):
+        m = mass[0, b, 0, :ctx[b].item()].cpu().numpy()
+        assert np.array_equal(kept[0, b, 0, :n].cpu().numpy(), ev.keep(m, n, 0, 5))
+    bud, new = i32([600, 0]), i32([-1, -1])                  # a budget above max_budget, in a call of no layers
+    none = torch.zeros((0, 2, 1, 900), device="cuda")
+    api.evict(c.desc, c.pool, c.page_table, ctx, 900, bud, 500, 0, 5, 0, none, dst,
+              torch.zeros((0, 2, 1, 500), dtype=torch.int32, device="cuda"), None, new, st)
+    assert new.tolist() == [900, 700] and int(st.item()) == _lib.Q3KV_STATUS_BAD_LENGTH
