@@ -7,6 +7,7 @@ caller owns; the library never allocates device memory.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import numpy as np
@@ -56,7 +57,7 @@ def _on_gpu(name: str, t: Optional[torch.Tensor], dev: int, dtype=None, min_nume
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     idx = _device_index(t)
-    if idx is None:
+    if idx < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if idx != dev:
         raise ValueError(f"{name} is on cuda:{idx}, the current device is cuda:{dev}")
@@ -66,19 +67,21 @@ def _on_gpu(name: str, t: Optional[torch.Tensor], dev: int, dtype=None, min_nume
         raise ValueError(f"{name} holds {t.numel()} elements, the call needs at least {min_numel}")
 
 
-def _device_index(t: torch.Tensor) -> Optional[int]:
-    """CUDA device index of a tensor; None for a tensor in host (or any other) memory."""
-    return t.get_device() if t.is_cuda else None
-
+# CUDA device index of a tensor; -1 for a tensor in host memory
+_device_index = torch.Tensor.get_device
 
 _cuda_seen = False                # asking torch whether CUDA is there costs microseconds; a yes stays a yes
 
 
 def _current_device() -> int:
+    """The current CUDA device; -2, which no tensor is on, where there is none."""
     global _cuda_seen
     if not _cuda_seen:
-        _cuda_seen = torch.cuda.is_available()
-    return torch.cuda.current_device() if _cuda_seen else -1
+        if not torch.cuda.is_available():
+            return -2
+        torch.cuda.init()
+        _cuda_seen = True
+    return torch._C._cuda_getDevice()
 
 
 def _nbytes(t: torch.Tensor) -> int:
@@ -140,13 +143,14 @@ def _pointers(dev: int, *args):
     """Checks of several tensors in one pass (a call of a step costs microseconds): for every (name, tensor, dtype or
     None, elements needed) what _on_gpu and _ptr check, and the data pointers.  A tensor of None gives None."""
     out = []
+    index, tensor = _device_index, torch.Tensor
     for name, t, dtype, need in args:
         if t is None:
             out.append(None)
             continue
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        if _device_index(t) != dev or (dtype is not None and t.dtype != dtype) or t.numel() < need:
+        if index(t) != dev or (dtype is not None and t.dtype != dtype) or (need and t.numel() < need):
             _on_gpu(name, t, dev, dtype, need)
         if not t.is_contiguous():
             raise ValueError("tensors passed to q3kv must be contiguous")
@@ -154,29 +158,40 @@ def _pointers(dev: int, *args):
     return out
 
 
-def _cache_pointers(desc: CacheDesc, pool, need_pool_bytes: int, page_table, lens, counts, offsets, status, dev: int):
-    """_check_cache_args with the pointers: (num_slots, pool, page_table, lens, counts, offsets, status)."""
-    for name, t in (("pool", pool), ("page_table", page_table), ("lengths", lens), ("per-slot token counts", counts),
-                    ("row offsets", offsets)):
-        if t is None:
-            raise ValueError(f"{name} is required")
+def _cache_pointers(desc: CacheDesc, pool, need_pool_bytes: int, page_table, lens, counts, offsets, status, dev: int,
+                    names=("per-slot token counts", "row offsets")):
+    """_check_cache_args with the pointers: (num_slots, max_pages_per_slot, [pool, page_table, lens, counts, offsets, status])."""
+    if pool is None or page_table is None or lens is None or counts is None or offsets is None:
+        _required(**{"pool": pool, "page_table": page_table, "lengths": lens, names[0]: counts, names[1]: offsets})
     if lens.dim() != 1:
         raise ValueError("per-slot lengths must be one-dimensional")
-    n = lens.shape[0]
+    n = lens.numel()
     ptrs = _pointers(dev, ("pool", pool, None, 0), ("page_table", page_table, torch.int32, 0), ("lengths", lens, torch.int32, 0),
-                     ("per-slot token counts", counts, torch.int32, n), ("row offsets", offsets, torch.int32, n),
-                     ("status", status, torch.int32, 1))
-    if page_table.dim() != 2 or page_table.shape[1] < 1 or (n > 0 and page_table.shape[0] < n):
+                     (names[0], counts, torch.int32, n), (names[1], offsets, torch.int32, n), ("status", status, torch.int32, 1))
+    shape = page_table.shape
+    if len(shape) != 2 or shape[1] < 1 or (n > 0 and shape[0] < n):
         raise ValueError(f"page_table must be int32 [num_slots >= {n}, max_pages_per_slot >= 1], "
-                         f"got {tuple(page_table.shape)}")
+                         f"got {tuple(shape)}")
     if _nbytes(pool) < need_pool_bytes:
         raise ValueError(f"pool holds {_nbytes(pool)} bytes, the cache needs {need_pool_bytes}")
-    return n, ptrs
+    return n, shape[1], ptrs
+
+
+@functools.lru_cache(maxsize=64)
+def _pool_need(pool_bytes_fn, lib, desc_bytes: bytes) -> int:
+    """The pool size that a format's function and the library `lib` give for a CacheDesc with these bytes."""
+    return pool_bytes_fn(CacheDesc.from_buffer_copy(desc_bytes))
+
+
+def _required(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
 
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -533,23 +548,23 @@ def t5k_attn_mass(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor,
 
 def _attn_mass(name, pool_bytes_fn, desc, pool, page_table, ctx_len, n_q, q_offsets, max_ctx_len, max_n_q, layer, q, lse,
                decay, mass, status, stream) -> None:
-    dev = _current_device()
-    n, (p_pool, p_table, p_ctx, p_nq, p_off, p_status) = _cache_pointers(desc, pool, pool_bytes_fn(desc), page_table, ctx_len,
-                                                                        n_q, q_offsets, status, dev)
-    for what, t in (("q", q), ("lse", lse), ("mass", mass)):
-        if t is None:
-            raise ValueError(f"{what} is required")
+    dev, lib = _current_device(), _lib.load()
+    n, pages, (p_pool, p_table, p_ctx, p_nq, p_off, p_status) = _cache_pointers(
+        desc, pool, _pool_need(pool_bytes_fn, lib, bytes(desc)), page_table, ctx_len, n_q, q_offsets, status, dev)
+    if q is None or lse is None or mass is None:
+        _required(q=q, lse=lse, mass=mass)
     p_q, p_lse, p_mass = _pointers(dev, ("q", q, None, 0), ("lse", lse, torch.float32, 0), ("mass", mass, torch.float32, 0))
     hq, hk = desc.num_q_heads, desc.num_kv_heads
     shape = q.shape
     if len(shape) != 3 or shape[1] != hq or shape[2] != HEAD_DIM:
         raise ValueError(f"q must be [rows, {hq}, {HEAD_DIM}], got {tuple(shape)}")
-    if lse.dim() != 2 or lse.shape[1] != hq or lse.shape[0] < shape[0]:
-        raise ValueError(f"lse must be [rows >= {shape[0]}, {hq}], got {tuple(lse.shape)}")
+    rows, shape = shape[0], lse.shape
+    if len(shape) != 2 or shape[1] != hq or shape[0] < rows:
+        raise ValueError(f"lse must be [rows >= {rows}, {hq}], got {tuple(shape)}")
     shape = mass.shape
     if len(shape) != 3 or shape[0] < n or shape[1] != hk or shape[2] < max_ctx_len:
         raise ValueError(f"mass must be [slots >= {n}, {hk}, positions >= {max_ctx_len}], got {tuple(shape)}")
-    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), p_pool, p_table, page_table.shape[1], p_ctx, p_nq, p_off,
+    rc = getattr(lib, name)(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_ctx, p_nq, p_off,
                                     n, max_ctx_len, max_n_q, layer, p_q, _dtype_code(q), p_lse, float(decay), p_mass, shape[2],
                                     p_status)
     check(rc, name)
@@ -585,29 +600,29 @@ def t5k_evict(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx
 
 def _evict(name, pool_bytes_fn, desc, pool, page_table, ctx_len, max_ctx_len, budget, max_budget, n_sink, n_recent, layer,
            mass, dst_page_table, kept, mass_out, new_len, status, stream) -> None:
-    dev = _current_device()
-    n, (p_pool, p_table, p_ctx, _, _, p_status) = _cache_pointers(desc, pool, pool_bytes_fn(desc), page_table, ctx_len, ctx_len,
-                                                                 ctx_len, status, dev)
-    for what, t in (("budget", budget), ("new_len", new_len), ("dst_page_table", dst_page_table), ("mass", mass), ("kept", kept)):
-        if t is None:
-            raise ValueError(f"{what} is required")
+    dev, lib = _current_device(), _lib.load()
+    n, pages, (p_pool, p_table, p_ctx, p_budget, p_new, p_status) = _cache_pointers(
+        desc, pool, _pool_need(pool_bytes_fn, lib, bytes(desc)), page_table, ctx_len, budget, new_len, status, dev,
+        ("budget", "new_len"))
+    if dst_page_table is None or mass is None or kept is None:
+        _required(dst_page_table=dst_page_table, mass=mass, kept=kept)
     i32, f32 = torch.int32, torch.float32
-    p_budget, p_new, p_dst, p_mass, p_kept, p_out = _pointers(
-        dev, ("budget", budget, i32, n), ("new_len", new_len, i32, n), ("dst_page_table", dst_page_table, i32, 0),
-        ("mass", mass, f32, 0), ("kept", kept, i32, 0), ("mass_out", mass_out, f32, 0))
-    if dst_page_table.dim() != 2 or dst_page_table.shape[1] < 1 or dst_page_table.shape[0] < n:
+    p_dst, p_mass, p_kept, p_out = _pointers(dev, ("dst_page_table", dst_page_table, i32, 0), ("mass", mass, f32, 0),
+                                             ("kept", kept, i32, 0), ("mass_out", mass_out, f32, 0))
+    dst_shape = dst_page_table.shape
+    if len(dst_shape) != 2 or dst_shape[1] < 1 or dst_shape[0] < n:
         raise ValueError(f"dst_page_table must be int32 [num_slots >= {n}, max_pages_per_slot >= 1], "
-                         f"got {tuple(dst_page_table.shape)}")
+                         f"got {tuple(dst_shape)}")
     heads, shape = desc.num_kv_heads, mass.shape
     if len(shape) != 4 or shape[1] != n or shape[2] != heads or shape[3] < max_ctx_len:
         raise ValueError(f"mass must be [layers, {n}, {heads}, positions >= {max_ctx_len}], got {tuple(shape)}")
     want = (shape[0], n, heads, max_budget)
-    for what, t in (("kept", kept), ("mass_out", mass_out)):
-        if t is not None and tuple(t.shape) != want:
-            raise ValueError(f"{what} must be {want}, got {tuple(t.shape)}")
-    rc = getattr(_lib.load(), name)(_stream(stream), ctypes.byref(desc), p_pool, p_table, page_table.shape[1], p_ctx, n, max_ctx_len,
+    if kept.shape != want or (mass_out is not None and mass_out.shape != want):
+        what, t = ("kept", kept) if kept.shape != want else ("mass_out", mass_out)
+        raise ValueError(f"{what} must be {want}, got {tuple(t.shape)}")
+    rc = getattr(lib, name)(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_ctx, n, max_ctx_len,
                                     p_budget, max_budget, n_sink, n_recent, layer, shape[0], p_mass, shape[3], p_dst,
-                                    dst_page_table.shape[1], p_kept, p_out, p_new, p_status)
+                                    dst_shape[1], p_kept, p_out, p_new, p_status)
     check(rc, name)
 
 
@@ -628,13 +643,14 @@ def _strided_rows(name: str, t: torch.Tensor, rows: int, dev: int):
     """Pointer, row stride and heads of [rows, heads, 256] rows whose heads are contiguous; rows may be strided."""
     if not isinstance(t, torch.Tensor) or _device_index(t) != dev:
         _on_gpu(name, t, dev)
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != rows or shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(shape)}")
-    heads = shape[1]
-    if stride[2] != 1 or (heads > 1 and stride[1] != HEAD_DIM):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(t.shape)}")
+    (n, heads, dim), (row, head, one) = t.shape, t.stride()
+    if n != rows or dim != HEAD_DIM:
+        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(t.shape)}")
+    if one != 1 or (heads > 1 and head != HEAD_DIM):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), stride[0] if rows > 1 else heads * HEAD_DIM, heads
+    return t.data_ptr(), row if rows > 1 else heads * HEAD_DIM, heads
 
 
 def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.Tensor, k: Optional[torch.Tensor] = None,
@@ -645,28 +661,33 @@ def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.
     """
     dev = _current_device()
     p_pos, = _pointers(dev, ("positions", positions, torch.int32, 0))
-    if p_pos is None or positions.dim() != 2 or positions.shape[1] != plan.num_axes:
+    if p_pos is None or positions.dim() != 2:
         raise ValueError(f"positions must be [rows, {plan.num_axes}]"
                          + (f", got {tuple(positions.shape)}" if positions is not None else ""))
-    rows = positions.shape[0]
+    rows, axes = positions.shape
+    if axes != plan.num_axes:
+        raise ValueError(f"positions must be [rows, {plan.num_axes}], got {(rows, axes)}")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out come together")
+    if not isinstance(q, torch.Tensor):
+        _on_gpu("q", q, dev)
     args = []
+    code = _dtype_code(q)
+    dtype, size = q.dtype, 4 if code == _lib.Q3KV_F32 else 2
     for name, x, y in (("q", q, q_out),) if k is None else (("q", q, q_out), ("k", k, k_out)):
         src, src_stride, heads = _strided_rows(name, x, rows, dev)
         dst, dst_stride, out_heads = _strided_rows(name + "_out", y, rows, dev)
-        if heads != out_heads or x.dtype != q.dtype or y.dtype != q.dtype:
+        if heads != out_heads or x.dtype != dtype or y.dtype != dtype:
             raise ValueError(f"{name} and {name}_out must have the heads of one another and the dtype of q")
         if rows and heads and not (src == dst and src_stride == dst_stride):
             # extents in bytes; an exact in-place call is fine, any other overlap is not
-            size = x.element_size()
             if (src < dst + ((rows - 1) * dst_stride + heads * HEAD_DIM) * size
                     and dst < src + ((rows - 1) * src_stride + heads * HEAD_DIM) * size):
                 raise ValueError(f"{name}_out overlaps {name} without being the same rows")
         args += (src, src_stride, dst, dst_stride, heads)
     if k is None:
         args += (None, 0, None, 0, 0)
-    rc = _lib.load().q3kv_rope(_stream(stream), ctypes.byref(plan), p_pos, rows, *args, _dtype_code(q))
+    rc = _lib.load().q3kv_rope(_stream(stream), ctypes.byref(plan), p_pos, rows, *args, code)
     check(rc, "q3kv_rope")
 
 
@@ -683,25 +704,25 @@ def accept_draft(logits: torch.Tensor, draft_probs: torch.Tensor, q_offsets: tor
                  workspace: Optional[torch.Tensor], accept_prob: Optional[torch.Tensor] = None,
                  status: Optional[torch.Tensor] = None, stream=None) -> None:
     """q3kv_accept_draft: rejection-sampled acceptance of drafts drawn from draft_probs [rows, vocab] (f32 or bf16)."""
-    for what, t in (("logits", logits), ("draft_probs", draft_probs), ("q_offsets", q_offsets), ("n_q", n_q), ("tokens", tokens),
-                    ("ctx_len", ctx_len), ("uniforms", uniforms), ("n_accepted", n_accepted), ("next_token", next_token),
-                    ("committed_len", committed_len)):
-        if t is None:
-            raise ValueError(f"{what} is required")
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [rows, vocab], got {tuple(logits.shape)}")
+    if (logits is None or draft_probs is None or q_offsets is None or n_q is None or tokens is None or ctx_len is None
+            or uniforms is None or n_accepted is None or next_token is None or committed_len is None):
+        _required(logits=logits, draft_probs=draft_probs, q_offsets=q_offsets, n_q=n_q, tokens=tokens, ctx_len=ctx_len,
+                  uniforms=uniforms, n_accepted=n_accepted, next_token=next_token, committed_len=committed_len)
+    shape = logits.shape
+    if len(shape) != 2:
+        raise ValueError(f"logits must be [rows, vocab], got {tuple(shape)}")
     if n_q.dim() != 1:
         raise ValueError("n_q must be one-dimensional")
-    rows, vocab = logits.shape
-    n, i32, f32 = n_q.shape[0], torch.int32, torch.float32
+    rows, vocab = shape
+    n, i32, f32 = n_q.numel(), torch.int32, torch.float32
     p = _pointers(_current_device(), ("logits", logits, None, 0), ("draft_probs", draft_probs, None, 0),
                   ("q_offsets", q_offsets, i32, n), ("n_q", n_q, i32, 0), ("tokens", tokens, i32, rows), ("ctx_len", ctx_len, i32, n),
                   ("uniforms", uniforms, f32, rows), ("n_accepted", n_accepted, i32, n), ("next_token", next_token, i32, n),
                   ("committed_len", committed_len, i32, n), ("accept_prob", accept_prob, f32, rows),
                   ("workspace", workspace, None, 0), ("status", status, i32, 1))
-    if draft_probs.shape != logits.shape:
-        raise ValueError(f"draft_probs must be {tuple(logits.shape)}, got {tuple(draft_probs.shape)}")
+    if draft_probs.shape != shape:
+        raise ValueError(f"draft_probs must be {tuple(shape)}, got {tuple(draft_probs.shape)}")
     rc = _lib.load().q3kv_accept_draft(_stream(stream), p[0], _dtype_code(logits), vocab, p[1], _dtype_code(draft_probs), p[2], p[3],
                                        p[4], n, rows, max_n_q, p[5], float(temperature), p[6], int(seed) & ((1 << 64) - 1), p[7],
-                                       p[8], p[9], p[10], p[11], 0 if workspace is None else _nbytes(workspace), p[12])
+                                       p[8], p[9], p[10], p[11], 0 if workspace is None else workspace.nbytes, p[12])
     check(rc, "q3kv_accept_draft")
