@@ -576,7 +576,7 @@ Q3KV_API int q3kv_t5k_attn_mass(void* stream, const q3kv_cache_desc* desc, const
  *             positions, ascending (entries past n are left as they were)
  *   d_mass_out  float32, same layout, the kept positions' masses; may be NULL; must
  *             not overlap d_mass
- *   d_new_len int32 [num_slots]: n; may be the array d_ctx_len
+ *   d_new_len int32 [num_slots]: n; may be the array d_ctx_len or d_budget
  * d_budget[b] > max_budget, L < 0, L > max_ctx_len, L beyond the slot's page table
  * or n beyond its destination pages set Q3KV_STATUS_BAD_LENGTH and leave the slot
  * out.  A record whose source or destination page id is out of range is skipped
@@ -622,7 +622,8 @@ Q3KV_API int q3kv_t5k_evict(void* stream, const q3kv_cache_desc* desc, void* d_p
  *                 as they are (not renormalised)
  *   d_accept_prob float [num_rows] or NULL: min(1, p_j(d_{j+1}) / q_j(d_{j+1})) in the
  *                 row of every tested draft (1 or 0 for q = 0: whether p > 0), other
- *                 rows left as they were -- what a draft-depth controller goes by
+ *                 rows left as they were -- what a draft-depth controller goes by;
+ *                 it must not overlap d_uniforms (Q3KV_ERR_INVALID_ARG)
  *   workspace     at least q3kv_accept_draft_workspace_bytes(...) bytes, 16-byte
  *                 aligned, no initial contents needed; calls sharing it must not
  *                 overlap on the GPU

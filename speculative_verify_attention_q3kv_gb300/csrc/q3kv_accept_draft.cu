@@ -396,6 +396,9 @@ int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, int32_t v
     if (draft_dtype != Q3KV_F32 && draft_dtype != Q3KV_BF16) return Q3KV_ERR_INVALID_ARG;
     if (max_n_q < 0) return Q3KV_ERR_INVALID_ARG;
     if (!(temperature > 0.0f) || !(temperature < 3.0e38f)) return Q3KV_ERR_INVALID_ARG;
+    // accept_prob is written while other CTAs still read the uniforms
+    if (d_accept_prob && num_rows > 0 && d_accept_prob < d_uniforms + num_rows && d_uniforms < d_accept_prob + num_rows)
+        return Q3KV_ERR_INVALID_ARG;
     if (max_n_q > kMaxNq) return Q3KV_ERR_UNSUPPORTED;
     DraftPlan p;
     int e = draft_plan(num_slots, num_rows, vocab, &p);

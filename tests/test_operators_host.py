@@ -148,6 +148,18 @@ def test_lse_calls_need_the_output(lib, name):
     assert call(None, slots=0) == 0                  # nothing to do
 
 
+def test_accept_draft_refuses_probabilities_over_the_uniforms(lib):
+    # other CTAs read the uniforms while accept_prob is written: 8 rows of 4 bytes from either side
+    def call(prob):                                  # no slots: nothing is launched where there is a device
+        a = 1 << 20
+        return lib.q3kv_accept_draft(None, a, 0, 100, a, 0, a, a, a, 0, 8, 3, a, 1.0, 4096, 7, a, a, a, prob, a, 1 << 30, None)
+
+    for prob in (4096, 4096 + 28, 4096 - 28):
+        assert call(prob) == INVALID
+    for prob in (4096 + 32, 4096 - 32, None):
+        assert call(prob) != INVALID
+
+
 # ------------------------------------------------------------------ binding
 class _Recorder:
     def __init__(self):
