@@ -9,7 +9,9 @@ A plain, slow, obviously correct restatement of what the hot path computes:
                    exactly dequantised values, GQA group by group;
 * ``cache``     -- an oracle-side paged cache: append and read back;
 * ``accept``    -- greedy acceptance of a verify step's drafts and the commit
-                   (rollback) of the cache length;
+                   (rollback) of the cache length; acceptance of sampled drafts;
+* ``rope``      -- rotary positions with several axes, in float64;
+* ``eviction``  -- attention mass of cached positions and the choice of those to keep;
 * ``fp8``       -- the fp8 E4M3 comparison format (saturating, unscaled,
                    unrotated), its paged cache and plain-basis attention;
 * ``turbo5k``   -- the turbo5k-style cache: 5-bit Lloyd-Max K (root-mean-square

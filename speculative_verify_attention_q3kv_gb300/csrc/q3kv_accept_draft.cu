@@ -106,7 +106,7 @@ template <typename T>
 __device__ __forceinline__ void load8(const T* row, bool vec, int k, int c1, float pad, float (&x)[8]) {
     if (vec && k + 8 <= c1) {
         if (sizeof(T) == 2) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + k));
+            const uint4 u = *reinterpret_cast<const uint4*>(row + k);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -114,8 +114,8 @@ __device__ __forceinline__ void load8(const T* row, bool vec, int k, int c1, flo
                 x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
             }
         } else {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(row + k));
-            const float4 w = __ldg(reinterpret_cast<const float4*>(row + k) + 1);
+            const float4 u = reinterpret_cast<const float4*>(row + k)[0];
+            const float4 w = reinterpret_cast<const float4*>(row + k)[1];
             x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
             x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
         }

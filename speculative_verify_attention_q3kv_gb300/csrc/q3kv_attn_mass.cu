@@ -70,6 +70,7 @@ constexpr int kWarps = 24;
 constexpr int kWarpD = 8, kWarpM = 16, kWarpP = 20;     // first warps of the roles
 constexpr int kIssuers = kWarpP - kWarpM;
 constexpr int kCopyThreads = 32 * (kWarps - kWarpP);
+constexpr int kQueryThreads = 32 * (kWarpD + kIssuers);  // that meet when a segment's queries are in place
 // registers: launched with 80 a thread, 61,440 in all; the split gives E more out of the others' share
 constexpr int kRegsE = 144, kRegsD = 56, kRegsMP = 40;
 static_assert(256 * (kRegsE + kRegsD + kRegsMP) <= kWarps * 32 * 80, "register split");
@@ -110,11 +111,14 @@ struct Mf<kFmtT5k> {
     static constexpr int kOps = 2;
     static constexpr int kRecB = kT5kKRecordBytes;
     static constexpr int kStride = kT5kKRecordBytes;
-    static constexpr int kStages = 4;
+    static constexpr int kStages = 3;
     static constexpr bool kPadded = false;
     static constexpr bool kScales = true;
     static constexpr bool kRot = true;
 };
+// Query operand: core matrices (8 rows x 8 dims, 128 bytes) 144 bytes apart along K, so that the
+// 16-byte stores of a warp that holds one row meet all banks (at 128 bytes they meet four)
+constexpr uint32_t kLbo = 144, kSbo = 32 * kLbo;
 constexpr uint32_t kPartCols = 32;          // TMEM columns of a part's operand (64 fp16 values)
 constexpr uint32_t kTmemCols = 512;
 
@@ -139,7 +143,7 @@ struct Bars {
 // One segment: tiles [t0, t0 + n) of a (slot, kv head) pair; n = 0: no more work.
 struct Segment {
     int slot, g, t0, n;
-    int T, L, chunks;
+    int T, L, chunks, q_row;                 // q_row: the slot's first query row
     int buffers;                             // operand buffers in TMEM
     int tiles_done;                          // tiles of earlier segments (phases of the stages)
     int tiles_single, tiles_double;          // of those with one operand buffer (a_full, a_free) and with two
@@ -154,7 +158,7 @@ struct Walk {
 
 template <int FMT>
 struct __align__(16) MassSmem {
-    __half q[kMaxChunks][2][kChunkRows * kHeadDim];   // [chunk][hi | lo], B operand
+    uint8_t q[kMaxChunks][2][kChunkRows / 8 * kSbo];   // [chunk][hi | lo], B operand
     uint8_t rec[Mf<FMT>::kStages][kTileP * Mf<FMT>::kStride];   // staged records
     float nlse[kMaxRows];                             // -lse in log2 units; -inf leaves a row out
     Bars bar;
@@ -208,13 +212,13 @@ __device__ inline bool whole_shares(const MassArgs& a, int* slot, long long* bas
     const int slots = __popc(__ballot_sync(0xffffffffu, tiles > 0)), per = G / H;   // CTAs per kv head
     if (slots > per || slots == 0) return slots == 0;
     // d = ceil(total / (per - slots)) fits, as ceil(x / d) <= x / d + 1; d below total / per does not
-    const int total = warp_sum_i(tiles);
+    const int total = __reduce_add_sync(0xffffffffu, tiles);
     int lo = (total + per - 1) / per - 1;                  // does not fit
-    int hi = slots < per ? (total + (per - slots) - 1) / (per - slots) : warp_max_i(tiles);
-    if (hi > lo + 1 && warp_sum_i((tiles + lo) / (lo + 1)) <= per) hi = lo + 1;
+    int hi = slots < per ? (total + (per - slots) - 1) / (per - slots) : __reduce_max_sync(0xffffffffu, tiles);
+    if (hi > lo + 1 && __reduce_add_sync(0xffffffffu, (tiles + lo) / (lo + 1)) <= per) hi = lo + 1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (warp_sum_i((tiles + mid - 1) / mid) <= per) hi = mid;
+        if (__reduce_add_sync(0xffffffffu, (tiles + mid - 1) / mid) <= per) hi = mid;
         else lo = mid;
     }
     const int ctas = (tiles + hi - 1) / hi;                // per pair of this lane's slot
@@ -274,11 +278,12 @@ __device__ void next_segment(const MassArgs& a, MassSmem<FMT>& sm, int k) {
     }
     const long long off = wk.w - wk.base;
     s.slot = wk.slot;
-    s.g = (int)(off / tiles);
+    s.g = off <= UINT32_MAX ? (int)((uint32_t)off / (uint32_t)tiles) : (int)(off / tiles);
     s.t0 = (int)(off - (long long)s.g * tiles);
     s.n = (int)min((long long)(tiles - s.t0), wk.w1 - wk.w);
     s.T = a.n_q[wk.slot];
     s.L = a.ctx_len[wk.slot];
+    s.q_row = a.q_offsets[wk.slot];
     s.chunks = (kGroup * s.T + kChunkRows - 1) / kChunkRows;
     s.buffers = double_buffered<FMT>(s.T) ? 2 : 1;
     s.tiles_done = wk.tiles_done;
@@ -291,25 +296,76 @@ __device__ void next_segment(const MassArgs& a, MassSmem<FMT>& sm, int k) {
     wk.phases += s.n * s.chunks;
 }
 
+// Accumulator columns of a group: the query rows of a pass, rounded up.
+__device__ __forceinline__ int acc_cols(const Segment& s) {
+    return kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : kChunkRows);
+}
+// Query rows of pass j as the products read them.
+__device__ __forceinline__ int mma_rows(const Segment& s, int j) {
+    const int cols = acc_cols(s), rows = min(kChunkRows, kGroup * s.T - kChunkRows * j);
+    return cols < kChunkRows ? cols : (rows + 31) & ~31;
+}
+
+// 8 values of a row from their 16-byte words
+__device__ __forceinline__ void unpack8(const uint4 (&u)[2], float (&y)[8]) {
+    y[0] = __uint_as_float(u[0].x); y[1] = __uint_as_float(u[0].y); y[2] = __uint_as_float(u[0].z); y[3] = __uint_as_float(u[0].w);
+    y[4] = __uint_as_float(u[1].x); y[5] = __uint_as_float(u[1].y); y[6] = __uint_as_float(u[1].z); y[7] = __uint_as_float(u[1].w);
+}
+__device__ __forceinline__ void unpack8(const uint4 (&u)[1], float (&y)[8]) {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(w[i] << 16);
+        y[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
 // Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e), split
-// into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  One row per E or D warp.
+// into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  The E warps take a row
+// each, with the next rows' loads in flight, while the D warps convert the first records.  The
+// loop stays rolled: its code is cold when a CTA begins, and eight rows unrolled took 900
+// cycles each.
 template <typename TIn, int FMT>
 __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm) {
+    constexpr int kAheadRows = 4;
+    constexpr int kVecs = sizeof(TIn) / 2;                   // 16-byte loads of a lane's 8 dims
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int R = kGroup * s.T;
-    const int Hq = a.num_kv_heads * kGroup;
-    const int64_t q_base = a.q_offsets[s.slot];
-    for (int r = warp; r < s.chunks * kChunkRows; r += kWarpM) {
-        const int chunk = r / kChunkRows, rr = r % kChunkRows;
-        const int64_t row = (q_base + r / kGroup) * Hq + s.g * kGroup + r % kGroup;
-        float y[8];
-        if (r < R) {
-            load8(static_cast<const TIn*>(a.q) + row * kHeadDim + 8 * lane, y);
-            if (Mf<FMT>::kRot) rotate_row_regs(y);
-        } else {
+    const int R = kGroup * s.T, rows = s.chunks * kChunkRows;
+    const int64_t Hq = a.num_kv_heads * kGroup;
+    auto row_of = [&](int r) { return ((int64_t)s.q_row + r / kGroup) * Hq + s.g * kGroup + r % kGroup; };
+    // E warp w has rows w, w + 8, ..: head w of every token
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const TIn*>(a.q) + row_of(warp) * kHeadDim + 8 * lane);
+    const int64_t step = Hq * kHeadDim * (int64_t)sizeof(TIn) / 16;
+    uint4 raw[kAheadRows][kVecs];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+    for (int b = 0; b < kAheadRows; ++b)
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) raw[b][v] = b < s.T ? p[step * b + v] : make_uint4(0u, 0u, 0u, 0u);
+    // lane t: the statistic of token t's row
+    const int rl = warp + kGroup * lane;
+    if (rl < rows) {
+        float v = -CUDART_INF_F;
+        if (rl < R) {
+            const float l = a.lse[row_of(rl)];
+            if (l > -CUDART_INF_F && l < CUDART_INF_F) v = -1.4426950408889634f * l;
+            else if (a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
         }
+        sm.nlse[rl] = v;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int t = 0; kGroup * t < rows; ++t) {
+        const int r = warp + kGroup * t, chunk = r / kChunkRows, rr = r % kChunkRows;
+        float y[8];
+        unpack8(raw[0], y);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+#pragma unroll
+            for (int b = 0; b + 1 < kAheadRows; ++b) raw[b][v] = raw[b + 1][v];
+            raw[kAheadRows - 1][v] = t + kAheadRows < s.T ? p[step * (t + kAheadRows) + v] : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (rr >= mma_rows(s, chunk)) continue;
+        if (Mf<FMT>::kRot) rotate_row_regs(y);
         constexpr float kScale = Mf<FMT>::kRot ? 1.4426950408889634f / 256.0f : 1.4426950408889634f / 16.0f;
         uint32_t hw[4], lw[4];
 #pragma unroll
@@ -320,17 +376,9 @@ __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>&
             hw[i] = as_u32(h2);
             lw[i] = as_u32(__floats2half2_rn(x0 - hf.x, x1 - hf.y));
         }
-        *reinterpret_cast<uint4*>(&sm.q[chunk][0][q_off(rr, 8 * lane)]) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(&sm.q[chunk][1][q_off(rr, 8 * lane)]) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-        if (lane == 0) {
-            float v = -CUDART_INF_F;
-            if (r < R) {
-                const float l = a.lse[row];
-                if (l > -CUDART_INF_F && l < CUDART_INF_F) v = -1.4426950408889634f * l;
-                else if (a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
-            }
-            sm.nlse[r] = v;
-        }
+        const uint32_t off = (uint32_t)(rr >> 3) * kSbo + (uint32_t)lane * kLbo + (uint32_t)(rr & 7) * 16u;
+        *reinterpret_cast<uint4*>(&sm.q[chunk][0][off]) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(&sm.q[chunk][1][off]) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
     }
     fence_proxy_async();
 }
@@ -625,25 +673,25 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     static_assert(acc_col<FMT>(1) + 192 * G <= kTmemCols && acc_col<kFmtQ3>(2) + 256 <= kTmemCols, "TMEM");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    if (tid == 0) {
-        for (int q = 0; q < kParts; ++q) {
-            mbar_init(&bar.a_full[q], 4);
-            for (int e = 0; e < kDoneBars; ++e) mbar_init(&bar.done[q][e], 1);
-            mbar_init(&bar.a_free[q], 1);
-            mbar_init(&bar.b_full[q >> 1][q & 1], 4);
-            mbar_init(&bar.b_free[q >> 1][q & 1], 2);
+    if (warp == 1) {                                          // a lane per barrier
+        if (lane < kParts) {
+            mbar_init(&bar.a_full[lane], 4);
+            mbar_init(&bar.a_free[lane], 1);
+            mbar_init(&bar.b_full[lane >> 1][lane & 1], 4);
+            mbar_init(&bar.b_free[lane >> 1][lane & 1], 2);
         }
-        for (int e = 0; e < kFreeBars; ++e) mbar_init(&bar.acc_free[e], 4);
-        for (int e = 0; e < kIssuers; ++e) mbar_init(&bar.drain[e], 1);
-        for (int e = 0; e < ST; ++e) {
-            mbar_init(&bar.r_full[e], Mf<FMT>::kPadded ? kCopyThreads : 1);
-            mbar_init(&bar.r_free[e], Mf<FMT>::kScales ? 12 : 8);
+        for (int e = lane; e < kParts * kDoneBars; e += 32) mbar_init(&bar.done[e / kDoneBars][e % kDoneBars], 1);
+        for (int e = lane; e < kFreeBars; e += 32) mbar_init(&bar.acc_free[e], 4);
+        if (lane < kIssuers) mbar_init(&bar.drain[lane], 1);
+        if (lane < ST) {
+            mbar_init(&bar.r_full[lane], Mf<FMT>::kPadded ? kCopyThreads : 1);
+            mbar_init(&bar.r_free[lane], Mf<FMT>::kScales ? 12 : 8);
         }
-        sm.abort = 0;
+        if (lane == 0) sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
     if (warp == kWarpM) tmem_alloc(&sm.tmem_base, kTmemCols);
     if (warp == 0) {
         // this CTA's share [w0, w1) of the sequence, and the slot it starts in
@@ -689,8 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
-    // Every role runs through the CTA's segments; the block meets when a segment's queries
-    // are in place and when it is done, by when the next one is known.
+    // Every role runs through the CTA's segments; E and M meet when a segment's queries are in
+    // place, the block when it is done, by when the next one is known.
     bool ok = true;
     if (warp < kWarpD) {
         // ================================================================ E: epilogue
@@ -699,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
             const Segment s = sm.seg[k & 1];
             load_queries<TIn, FMT>(a, s, sm);
-            named_sync(0, kThreads);
+            named_sync(1, kQueryThreads);
             const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc_col<FMT>(s.buffers), abort};
             constexpr int B = double_buffered<FMT>(1) ? 2 : 1;
             const int rows = kGroup * s.T;
@@ -719,8 +767,6 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
 #pragma unroll 1
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
             const Segment s = sm.seg[k & 1];
-            load_queries<TIn, FMT>(a, s, sm);
-            named_sync(0, kThreads);
             const int n = s.n;
             int rs = s.tiles_done % ST;                     // stage and its phase
             uint32_t rp = (uint32_t)(s.tiles_done / ST) & 1u;
@@ -789,18 +835,16 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
 #pragma unroll 1
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
             const Segment s = sm.seg[k & 1];
-            named_sync(0, kThreads);
+            named_sync(1, kQueryThreads);
             const int n = s.n;
-            // accumulator columns per group (query rows of a pass, rounded up) and slots of the ring
-            const int cols = kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : 64);
+            const int cols = acc_cols(s);
             const int slots = acc_slots<FMT>(s.buffers, cols);
             const int c_first = kParts * s.phases;
 #pragma unroll 1
             for (int i = 0; ok && i < n; ++i) {
 #pragma unroll 1
                 for (int j = 0; ok && j < s.chunks; ++j) {
-                    const int rows = min(kChunkRows, kGroup * s.T - kChunkRows * j);
-                    const uint32_t idesc = make_idesc(cols < 64 ? cols : (rows + 31) & ~31, false, false);
+                    const uint32_t idesc = make_idesc(mma_rows(s, j), false, false);
                     const int ph = s.phases + i * s.chunks + j;
 #pragma unroll 1
                     for (int part = first_part; ok && part < kParts; part += kIssuers) {
@@ -816,19 +860,20 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                         tc_fence_after();
                         const uint32_t d = tmem + acc_col<FMT>(s.buffers) + (uint32_t)((c % slots) * G * cols);
                         const uint32_t aop = tmem + kPartCols * (kParts * buf + part);
-                        // dims 64 part ..: two 8-dim cores (256 bytes) per K step, start address in 16-byte units
-                        const uint64_t bh = make_desc(smem_u32(sm.q[j][0]) + part * 1024, kQLbo, kQSbo);
-                        const uint64_t bl = make_desc(smem_u32(sm.q[j][1]) + part * 1024, kQLbo, kQSbo);
+                        // dims 64 part ..: two 8-dim cores per K step, start address in 16-byte units
+                        const uint64_t bh = make_desc(smem_u32(sm.q[j][0]) + part * 8 * kLbo, kLbo, kSbo);
+                        const uint64_t bl = make_desc(smem_u32(sm.q[j][1]) + part * 8 * kLbo, kLbo, kSbo);
+                        constexpr uint64_t kStep = 2 * kLbo / 16;
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const uint32_t dg = d + (G == 2 ? (uint32_t)(cols * (k / 2)) : 0u);
                                 const uint32_t first = (G == 2 ? (k & 1) : k) == 0 ? 0u : 1u;
-                                mma_ts(dg, aop + 8 * k, bh + 16 * k, idesc, first);
-                                mma_ts(dg, aop + 8 * k, bl + 16 * k, idesc, 1u);
+                                mma_ts(dg, aop + 8 * k, bh + kStep * k, idesc, first);
+                                mma_ts(dg, aop + 8 * k, bl + kStep * k, idesc, 1u);
                                 if (OPS == 2) {
-                                    mma_ts(dg, aop + kParts * kPartCols + 8 * k, bh + 16 * k, idesc, 1u);
-                                    mma_ts(dg, aop + kParts * kPartCols + 8 * k, bl + 16 * k, idesc, 1u);
+                                    mma_ts(dg, aop + kParts * kPartCols + 8 * k, bh + kStep * k, idesc, 1u);
+                                    mma_ts(dg, aop + kParts * kPartCols + 8 * k, bl + kStep * k, idesc, 1u);
                                 }
                             }
                             mma_commit(&bar.done[part][ph % kDoneBars]);
@@ -850,18 +895,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
             const Segment s = sm.seg[k & 1];
             const int n = s.n;
-            // the first tiles' records are in flight while the queries are prepared: their stages are free
-            const int pre = min(n, ST);
-            int staged = s.tiles_done + pre;                // next tile to copy
-            if (Mf<FMT>::kPadded || warp == kWarpP)
-                for (int i = 0; i < pre; ++i) stage_tile<FMT>(a, s, sm, i, s.tiles_done + i);
             if (tid == 32 * kWarpP + 32) next_segment<FMT>(a, sm, k + 1);
-            named_sync(0, kThreads);
+            int staged = s.tiles_done;                      // next tile to copy
             if (Mf<FMT>::kPadded || warp == kWarpP) {
 #pragma unroll 1
-                for (int i = pre; i < n; ++i) {
+                for (int i = 0; i < n; ++i) {
                     const int rc = s.tiles_done + i;
-                    ok = ok && mbar_wait_all(&bar.r_free[rc % ST], (uint32_t)((rc / ST - 1) & 1), abort);
+                    // every stage is free when a segment begins
+                    if (i >= ST) ok = ok && mbar_wait_all(&bar.r_free[rc % ST], (uint32_t)((rc / ST - 1) & 1), abort);
                     if (!ok) break;
                     stage_tile<FMT>(a, s, sm, i, rc);
                     staged = rc + 1;

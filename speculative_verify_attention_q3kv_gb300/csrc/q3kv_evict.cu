@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs 
         const float* p = m + t0 + lane;
         if (t0 + kTile <= end) {
 #pragma unroll
-            for (int j = 0; j < kPerLane; ++j) x[j] = __ldg(p + 32 * j);
+            for (int j = 0; j < kPerLane; ++j) x[j] = p[32 * j];
         } else {
 #pragma unroll
-            for (int j = 0; j < kPerLane; ++j) x[j] = t0 + 32 * j + lane < end ? __ldg(p + 32 * j) : kNan;
+            for (int j = 0; j < kPerLane; ++j) x[j] = t0 + 32 * j + lane < end ? p[32 * j] : kNan;
         }
     };
     float x[kPerLane];
