@@ -169,8 +169,7 @@ struct __align__(16) MassSmem {
 };
 
 // Tiles of a slot's kv head; 0 for a slot with nothing to do.
-__device__ __forceinline__ int slot_tiles(const MassArgs& a, int b, bool* bad) {
-    const int T = a.n_q[b], L = a.ctx_len[b];
+__device__ __forceinline__ int tiles_of(const MassArgs& a, int T, int L, bool* bad) {
     if (T <= 0) return 0;
     if (T > a.max_n_q || T > L || L > a.max_ctx_len || L > (int64_t)a.max_pages_per_slot * kPageSize) {
         *bad = true;
@@ -178,6 +177,7 @@ __device__ __forceinline__ int slot_tiles(const MassArgs& a, int b, bool* bad) {
     }
     return (L + kTileP - 1) / kTileP;
 }
+__device__ __forceinline__ int slot_tiles(const MassArgs& a, int b, bool* bad) { return tiles_of(a, a.n_q[b], a.ctx_len[b], bad); }
 
 __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
     unsigned long long r;
@@ -200,53 +200,6 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigne
     return r;
 }
 
-// Shares that stay within one (slot, kv head) pair, where the CTAs reach: the smallest d for
-// which giving every pair ceil(tiles / d) CTAs takes no more than the grid.  A pair change
-// drains the pipeline and prepares other queries, some 4 us (8 ragged slots x 2 heads on
-// 152 CTAs: 19.5 us with even shares, 16.1 us).  One warp, a lane per slot; false if there are more
-// than 32 slots or more pairs than CTAs (even shares are then better).
-__device__ inline bool whole_shares(const MassArgs& a, int* slot, long long* base, long long* w0, long long* w1, bool* bad) {
-    if (a.num_slots > 32) return false;
-    const int lane = threadIdx.x & 31, G = gridDim.x, H = a.num_kv_heads;
-    const int tiles = lane < a.num_slots ? slot_tiles(a, lane, bad) : 0;
-    const int slots = __popc(__ballot_sync(0xffffffffu, tiles > 0)), per = G / H;   // CTAs per kv head
-    if (slots > per || slots == 0) return slots == 0;
-    // d = ceil(total / (per - slots)) fits, as ceil(x / d) <= x / d + 1; d below total / per does not
-    const int total = __reduce_add_sync(0xffffffffu, tiles);
-    int lo = (total + per - 1) / per - 1;                  // does not fit
-    int hi = slots < per ? (total + (per - slots) - 1) / (per - slots) : __reduce_max_sync(0xffffffffu, tiles);
-    if (hi > lo + 1 && __reduce_add_sync(0xffffffffu, (tiles + lo) / (lo + 1)) <= per) hi = lo + 1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__reduce_add_sync(0xffffffffu, (tiles + mid - 1) / mid) <= per) hi = mid;
-        else lo = mid;
-    }
-    const int ctas = (tiles + hi - 1) / hi;                // per pair of this lane's slot
-    int incl = ctas * H;
-    long long tincl = (long long)tiles * H;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-        const long long t = __shfl_up_sync(0xffffffffu, tincl, o);
-        if (lane >= o) {
-            incl += u;
-            tincl += t;
-        }
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, incl > (int)blockIdx.x);
-    if (!hit) return true;                                 // no tiles are left for this CTA
-    const int l = __ffs(hit) - 1;
-    const int n = __shfl_sync(0xffffffffu, tiles, l), k = __shfl_sync(0xffffffffu, ctas, l);
-    const int r = (int)blockIdx.x - __shfl_sync(0xffffffffu, incl - ctas * H, l);
-    const int i = r % k;
-    *slot = l;
-    *base = __shfl_sync(0xffffffffu, tincl - (long long)tiles * H, l);
-    const long long first = *base + (long long)(r / k) * n;
-    *w0 = first + (long long)n * i / k;
-    *w1 = first + (long long)n * (i + 1) / k;
-    return true;
-}
-
 // With at most 32 query rows the accumulators leave TMEM for a second operand buffer, so
 // the conversion of a tile overlaps the products of the one before it (655,360 positions, 2 kv
 // heads: 74 -> 69 us with 1 token, 79 -> 76 us with 4; more rows need the columns for a
@@ -261,6 +214,47 @@ __host__ __device__ constexpr uint32_t acc_col(int buffers) { return kParts * kP
 template <int FMT>
 __host__ __device__ constexpr int acc_slots(int buffers, int cols) {
     return buffers == 2 ? 256 / (Mf<FMT>::kGroups * cols) : 192 / cols;
+}
+
+// Shares that stay within one (slot, kv head) pair, where the CTAs reach: the smallest d for
+// which giving every pair ceil(tiles / d) CTAs takes no more than the grid.  A pair change
+// drains the pipeline and prepares other queries, some 4 us (8 ragged slots x 2 heads on
+// 152 CTAs: 19.5 us with even shares, 16.1 us).  One warp, a lane per slot; false if there are more
+// than 32 slots or more pairs than CTAs (even shares are then better).
+template <int FMT>
+__device__ inline bool whole_shares(const MassArgs& a, Segment& seg, bool* bad) {
+    if (a.num_slots > 32) return false;
+    const int lane = threadIdx.x & 31, G = gridDim.x, H = a.num_kv_heads;
+    const bool slot = lane < a.num_slots;
+    const int q_row = slot ? a.q_offsets[lane] : 0, T = slot ? a.n_q[lane] : 0, L = slot ? a.ctx_len[lane] : 0;
+    const int tiles = tiles_of(a, T, L, bad);
+    const int slots = __popc(__ballot_sync(0xffffffffu, tiles > 0)), per = G / H;   // CTAs per kv head
+    if (slots > per || slots == 0) return slots == 0;
+    // d = ceil(total / (per - slots)) fits, as ceil(x / d) <= x / d + 1; d below total / per does not
+    const int total = __reduce_add_sync(0xffffffffu, tiles);
+    int lo = (total + per - 1) / per - 1;                  // does not fit
+    int hi = slots < per ? (total + (per - slots) - 1) / (per - slots) : __reduce_max_sync(0xffffffffu, tiles);
+    if (hi > lo + 1 && __reduce_add_sync(0xffffffffu, (tiles + lo) / (lo + 1)) <= per) hi = lo + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__reduce_add_sync(0xffffffffu, (tiles + mid - 1) / mid) <= per) hi = mid;
+        else lo = mid;
+    }
+    const int ctas = (tiles + hi - 1) / hi;                // per pair of this lane's slot
+    int incl = ctas * H;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > (int)blockIdx.x);
+    if (hit && lane == __ffs(hit) - 1) {                   // the lane of this CTA's slot
+        const int r = (int)blockIdx.x - (incl - ctas * H), g = r / ctas, i = r - g * ctas;
+        const int t0 = (int)((long long)tiles * i / ctas), t1 = (int)((long long)tiles * (i + 1) / ctas);
+        seg = Segment{lane, g, t0, t1 - t0, T, L, (kGroup * T + kChunkRows - 1) / kChunkRows, q_row,
+                      double_buffered<FMT>(T) ? 2 : 1, 0, 0, 0, 0};
+    }
+    return true;                                           // (no tiles are left for the CTAs behind the last)
 }
 
 // The segment at the walk's position, for every role to read (one thread calls).
@@ -306,79 +300,150 @@ __device__ __forceinline__ int mma_rows(const Segment& s, int j) {
     return cols < kChunkRows ? cols : (rows + 31) & ~31;
 }
 
-// 8 values of a row from their 16-byte words
-__device__ __forceinline__ void unpack8(const uint4 (&u)[2], float (&y)[8]) {
-    y[0] = __uint_as_float(u[0].x); y[1] = __uint_as_float(u[0].y); y[2] = __uint_as_float(u[0].z); y[3] = __uint_as_float(u[0].w);
-    y[4] = __uint_as_float(u[1].x); y[5] = __uint_as_float(u[1].y); y[6] = __uint_as_float(u[1].z); y[7] = __uint_as_float(u[1].w);
+// This CTA's share of the sequence of tiles, and its first segment.  One warp.
+template <int FMT>
+__device__ void share_of(const MassArgs& a, MassSmem<FMT>& sm) {
+    const int lane = threadIdx.x & 31;
+    bool bad = false;
+    if (lane == 0) {
+        sm.seg[0].n = 0;
+        sm.walk = Walk{0, 0, 0, 0, 0, 0, 0, 0};
+    }
+    __syncwarp();
+    if (!whole_shares<FMT>(a, sm.seg[0], &bad)) {
+        // even shares [w0, w1), whatever the slots' lengths
+        long long w0, w1, base = 0, total = 0;
+        for (int b0 = 0; b0 < a.num_slots; b0 += 32)
+            total += __reduce_add_sync(0xffffffffu, b0 + lane < a.num_slots ? slot_tiles(a, b0 + lane, &bad) : 0);
+        total *= a.num_kv_heads;
+        w0 = total * blockIdx.x / gridDim.x;
+        w1 = total * (blockIdx.x + 1) / gridDim.x;
+        int slot = a.num_slots;
+        bool ignore = false;
+        for (int b0 = 0; b0 < a.num_slots && w0 < w1; b0 += 32) {
+            const long long mine = b0 + lane < a.num_slots ? (long long)slot_tiles(a, b0 + lane, &ignore) * a.num_kv_heads : 0;
+            long long incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + incl > w0);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                slot = b0 + l;
+                base += __shfl_sync(0xffffffffu, incl - mine, l);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            sm.walk = Walk{w0, w1, base, slot, 0, 0, 0, 0};
+            next_segment<FMT>(a, sm, 0);
+        }
+    }
+    if (blockIdx.x == 0 && bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
 }
-__device__ __forceinline__ void unpack8(const uint4 (&u)[1], float (&y)[8]) {
-    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+
+// The 8 or 4 values of a 16-byte word.
+__device__ __forceinline__ void unpack(const uint4& u, float* y, const __nv_bfloat16*) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         y[2 * i] = __uint_as_float(w[i] << 16);
         y[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
+__device__ __forceinline__ void unpack(const uint4& u, float* y, const float*) {
+    y[0] = __uint_as_float(u.x); y[1] = __uint_as_float(u.y); y[2] = __uint_as_float(u.z); y[3] = __uint_as_float(u.w);
+}
+
+// H y (unnormalised) of four rows of a warp, eight lanes a row.  Lane l begins with dims
+// 32 (l % 8) .. of its row: dim bits 0 to 4 are register bits.  Bits 5, 6 and 7 are exchanged into
+// register bits 3, 4 and 3, half of the registers by shuffle each (a butterfly across lanes needs all
+// of them), so that y[8 c + i] comes out as dim 8 (l % 8 + 8 (c / 2) + 16 (c % 2)) + i.
+__device__ __forceinline__ void rotate_four_rows(float (&y)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if ((i & h) == 0) {
+                const float u = y[i], v = y[i + h];
+                y[i] = u + v;
+                y[i + h] = u - v;
+            }
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+        const int h = step == 1 ? 16 : 8, m = 1 << step;
+        const bool upper = (lane & m) != 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if ((i & h) == 0) {
+                const float got = __shfl_xor_sync(0xffffffffu, upper ? y[i] : y[i + h], m);
+                const float u = upper ? got : y[i], v = upper ? y[i + h] : got;
+                y[i] = u + v;
+                y[i + h] = u - v;
+            }
+    }
+}
 
 // Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e), split
-// into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  The E warps take a row
-// each, with the next rows' loads in flight, while the D warps convert the first records.  The
-// loop stays rolled: its code is cold when a CTA begins, and eight rows unrolled took 900
-// cycles each.
+// into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  The E warps take four rows
+// each, the next ones' loads in flight, while the D warps convert the first records.  (A row per
+// warp and step took 40 shuffles a row, 8,000 cycles for 64 rows.)
 template <typename TIn, int FMT>
 __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm) {
-    constexpr int kAheadRows = 4;
-    constexpr int kVecs = sizeof(TIn) / 2;                   // 16-byte loads of a lane's 8 dims
+    constexpr int kVecs = 2 * (int)sizeof(TIn);              // 16-byte loads of a lane's 32 dims
+    constexpr int kPer = 32 / kVecs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = kGroup * s.T, rows = s.chunks * kChunkRows;
     const int64_t Hq = a.num_kv_heads * kGroup;
     auto row_of = [&](int r) { return ((int64_t)s.q_row + r / kGroup) * Hq + s.g * kGroup + r % kGroup; };
-    // E warp w has rows w, w + 8, ..: head w of every token
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const TIn*>(a.q) + row_of(warp) * kHeadDim + 8 * lane);
-    const int64_t step = Hq * kHeadDim * (int64_t)sizeof(TIn) / 16;
-    uint4 raw[kAheadRows][kVecs];
+    auto load = [&](uint4 (&raw)[kVecs], int r) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const TIn*>(a.q) + row_of(r) * kHeadDim + 32 * (lane & 7));
 #pragma unroll
-    for (int b = 0; b < kAheadRows; ++b)
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) raw[b][v] = b < s.T ? p[step * b + v] : make_uint4(0u, 0u, 0u, 0u);
-    // lane t: the statistic of token t's row
-    const int rl = warp + kGroup * lane;
-    if (rl < rows) {
+        for (int v = 0; v < kVecs; ++v) raw[v] = r < R ? p[v] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 next[kVecs];
+    load(next, 4 * warp + (lane >> 3));
+    if ((int)threadIdx.x < rows) {
+        const int r = threadIdx.x;
         float v = -CUDART_INF_F;
-        if (rl < R) {
-            const float l = a.lse[row_of(rl)];
+        if (r < R) {
+            const float l = a.lse[row_of(r)];
             if (l > -CUDART_INF_F && l < CUDART_INF_F) v = -1.4426950408889634f * l;
             else if (a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
         }
-        sm.nlse[rl] = v;
+        sm.nlse[r] = v;
     }
     __syncwarp();
 #pragma unroll 1
-    for (int t = 0; kGroup * t < rows; ++t) {
-        const int r = warp + kGroup * t, chunk = r / kChunkRows, rr = r % kChunkRows;
-        float y[8];
-        unpack8(raw[0], y);
+    for (int r0 = 4 * warp; r0 < rows; r0 += 4 * kWarpD) {
+        const int r = r0 + (lane >> 3), chunk = r0 / kChunkRows, rr = r % kChunkRows;
+        float y[32];
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-#pragma unroll
-            for (int b = 0; b + 1 < kAheadRows; ++b) raw[b][v] = raw[b + 1][v];
-            raw[kAheadRows - 1][v] = t + kAheadRows < s.T ? p[step * (t + kAheadRows) + v] : make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (rr >= mma_rows(s, chunk)) continue;
-        if (Mf<FMT>::kRot) rotate_row_regs(y);
+        for (int v = 0; v < kVecs; ++v) unpack(next[v], y + kPer * v, static_cast<const TIn*>(nullptr));
+        load(next, r + 4 * kWarpD);
+        if (r0 % kChunkRows >= mma_rows(s, chunk)) continue;
+        if (Mf<FMT>::kRot) rotate_four_rows(y);
         constexpr float kScale = Mf<FMT>::kRot ? 1.4426950408889634f / 256.0f : 1.4426950408889634f / 16.0f;
-        uint32_t hw[4], lw[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x0 = y[2 * i] * kScale, x1 = y[2 * i + 1] * kScale;
-            const __half2 h2 = __floats2half2_rn(x0, x1);
-            const float2 hf = __half22float2(h2);
-            hw[i] = as_u32(h2);
-            lw[i] = as_u32(__floats2half2_rn(x0 - hf.x, x1 - hf.y));
+        for (int c = 0; c < 4; ++c) {
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x0 = y[8 * c + 2 * i] * kScale, x1 = y[8 * c + 2 * i + 1] * kScale;
+                const __half2 h2 = __floats2half2_rn(x0, x1);
+                const float2 hf = __half22float2(h2);
+                hw[i] = as_u32(h2);
+                lw[i] = as_u32(__floats2half2_rn(x0 - hf.x, x1 - hf.y));
+            }
+            const uint32_t core = Mf<FMT>::kRot ? (lane & 7) + 8 * (c >> 1) + 16 * (c & 1) : 4 * (lane & 7) + c;
+            const uint32_t off = (uint32_t)(rr >> 3) * kSbo + core * kLbo + (uint32_t)(rr & 7) * 16u;
+            *reinterpret_cast<uint4*>(&sm.q[chunk][0][off]) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            *reinterpret_cast<uint4*>(&sm.q[chunk][1][off]) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
-        const uint32_t off = (uint32_t)(rr >> 3) * kSbo + (uint32_t)lane * kLbo + (uint32_t)(rr & 7) * 16u;
-        *reinterpret_cast<uint4*>(&sm.q[chunk][0][off]) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(&sm.q[chunk][1][off]) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
     }
     fence_proxy_async();
 }
@@ -673,69 +738,15 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     static_assert(acc_col<FMT>(1) + 192 * G <= kTmemCols && acc_col<kFmtQ3>(2) + 256 <= kTmemCols, "TMEM");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == 1) {                                          // a lane per barrier
-        if (lane < kParts) {
-            mbar_init(&bar.a_full[lane], 4);
-            mbar_init(&bar.a_free[lane], 1);
-            mbar_init(&bar.b_full[lane >> 1][lane & 1], 4);
-            mbar_init(&bar.b_free[lane >> 1][lane & 1], 2);
-        }
-        for (int e = lane; e < kParts * kDoneBars; e += 32) mbar_init(&bar.done[e / kDoneBars][e % kDoneBars], 1);
-        for (int e = lane; e < kFreeBars; e += 32) mbar_init(&bar.acc_free[e], 4);
-        if (lane < kIssuers) mbar_init(&bar.drain[lane], 1);
-        if (lane < ST) {
-            mbar_init(&bar.r_full[lane], Mf<FMT>::kPadded ? kCopyThreads : 1);
-            mbar_init(&bar.r_free[lane], Mf<FMT>::kScales ? 12 : 8);
-        }
-        if (lane == 0) sm.abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    if (warp == kWarpM) tmem_alloc(&sm.tmem_base, kTmemCols);
-    if (warp == 0) {
-        // this CTA's share [w0, w1) of the sequence, and the slot it starts in
-        bool bad = false;
-        long long w0 = 0, w1 = 0, base = 0;
-        int slot = 0;
-        if (!whole_shares(a, &slot, &base, &w0, &w1, &bad)) {
-            long long total = 0;
-            for (int b0 = 0; b0 < a.num_slots; b0 += 32)
-                total += warp_sum_i(b0 + lane < a.num_slots ? slot_tiles(a, b0 + lane, &bad) : 0);
-            total *= a.num_kv_heads;
-            w0 = total * blockIdx.x / gridDim.x;
-            w1 = total * (blockIdx.x + 1) / gridDim.x;
-            slot = a.num_slots;
-            bool ignore = false;
-            for (int b0 = 0; b0 < a.num_slots && w0 < w1; b0 += 32) {
-                const long long mine =
-                    b0 + lane < a.num_slots ? (long long)slot_tiles(a, b0 + lane, &ignore) * a.num_kv_heads : 0;
-                long long incl = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += u;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, base + incl > w0);
-                if (hit) {
-                    const int l = __ffs(hit) - 1;
-                    slot = b0 + l;
-                    base += __shfl_sync(0xffffffffu, incl - mine, l);
-                    break;
-                }
-                base += __shfl_sync(0xffffffffu, incl, 31);
-            }
-        }
-        if (blockIdx.x == 0 && bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
-        if (lane == 0) {
-            sm.walk = Walk{w0, w1, base, slot, 0, 0, 0, 0};
-            next_segment<FMT>(a, sm, 0);
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
+    // Before the first segment: a P warp finds this CTA's share, another sets the barriers up, an M
+    // warp gets the TMEM, and the E warps run the query preparation on no rows, which warms its code.
+    auto prepared = [&] {
+        tc_fence_before();
+        named_sync(0, kThreads);
+        tc_fence_after();
+        return sm.tmem_base;
+    };
 
     // Every role runs through the CTA's segments; E and M meet when a segment's queries are in
     // place, the block when it is done, by when the next one is known.
@@ -743,10 +754,15 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (warp < kWarpD) {
         // ================================================================ E: epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsE));
+        uint32_t tmem = 0;
 #pragma unroll 1
-        for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
-            const Segment s = sm.seg[k & 1];
+        for (int k = -1; k < 0 || sm.seg[k & 1].n > 0; ++k) {
+            const Segment s = k < 0 ? Segment{0, 0, 0, 0, 0, 0, 1, 0, 1, 0, 0, 0, 0} : sm.seg[k & 1];
             load_queries<TIn, FMT>(a, s, sm);
+            if (k < 0) {
+                tmem = prepared();
+                continue;
+            }
             named_sync(1, kQueryThreads);
             const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc_col<FMT>(s.buffers), abort};
             constexpr int B = double_buffered<FMT>(1) ? 2 : 1;
@@ -763,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         const float cent = FMT == kFmtT5k ? a.t5k.c[lane] : 0.0f;
         const int odd = (warp - kWarpD) >> 2;                // this warp's parts: odd and odd + 2
         const int p = 32 * (warp & 3) + lane;
+        const uint32_t tmem = prepared();
         const uint32_t col0 = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
@@ -831,6 +848,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMP));
         if (warp < kWarpP) {
         // ================================================================ M: products of one part
+        if (warp == kWarpM) tmem_alloc(&sm.tmem_base, kTmemCols);
+        const uint32_t tmem = prepared();
         const int first_part = warp - kWarpM;                // this issuer's parts: every kIssuers-th
 #pragma unroll 1
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
@@ -891,6 +910,25 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         mbar_drain(&bar.drain[first_part], 0);
         } else {
         // ================================================================ P: records -> shared memory
+        if (warp == kWarpP + 1) {                             // a lane per barrier
+            if (lane < kParts) {
+                mbar_init(&bar.a_full[lane], 4);
+                mbar_init(&bar.a_free[lane], 1);
+                mbar_init(&bar.b_full[lane >> 1][lane & 1], 4);
+                mbar_init(&bar.b_free[lane >> 1][lane & 1], 2);
+            }
+            for (int e = lane; e < kParts * kDoneBars; e += 32) mbar_init(&bar.done[e / kDoneBars][e % kDoneBars], 1);
+            for (int e = lane; e < kFreeBars; e += 32) mbar_init(&bar.acc_free[e], 4);
+            if (lane < kIssuers) mbar_init(&bar.drain[lane], 1);
+            if (lane < ST) {
+                mbar_init(&bar.r_full[lane], Mf<FMT>::kPadded ? kCopyThreads : 1);
+                mbar_init(&bar.r_free[lane], Mf<FMT>::kScales ? 12 : 8);
+            }
+            if (lane == 0) sm.abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        if (warp == kWarpP) share_of<FMT>(a, sm);
+        prepared();
 #pragma unroll 1
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
             const Segment s = sm.seg[k & 1];
@@ -921,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     }
     tc_fence_before();
     named_sync(0, kThreads);
-    if (warp == kWarpM) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kWarpM) tmem_dealloc(sm.tmem_base, kTmemCols);
     if (*abort && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_TIMEOUT);
 }
 
