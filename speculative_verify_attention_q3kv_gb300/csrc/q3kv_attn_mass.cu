@@ -28,7 +28,7 @@
 //   E   warps 0-7    epilogue: thread = position (lane quarter warp & 3), all rows of the
 //                    chunk; the two warps of a lane quarter take every other tile.  Score
 //                    sums start at -lse in log2 units, weights 2^s, rows summed in the
-//                    thread.
+//                    thread.  Before a segment they rotate and split its queries.
 //   D   warps 8-15   thread = position: its staged record converted into TMEM, one warp of
 //                    a lane quarter for the even parts and one for the odd ones
 //   M   warps 16-19  one thread each issues the products of one part: an issuing thread
@@ -39,16 +39,20 @@
 // accumulator slots (see `double_buffered` and `acc_slots`).
 //
 // Work: the tiles of all (slot, kv head) pairs in one sequence, a share of about equal
-// size per CTA (one per SM), whatever the slots' lengths; a CTA rotates and splits the
-// queries of a pair itself when it enters it.
+// size per CTA (one per SM), whatever the slots' lengths, within one pair where the CTAs
+// reach (see whole_shares); a CTA rotates and splits the queries of a pair itself when it
+// enters it.
 //
-// Bound: not memory.  655,360 positions x 8 tokens x 2 kv heads take 106.7 us, 1,470 GB/s
-// of K records and masses (the bytes alone: 23 us; the tensor pipe is 24 % active).  A tile
-// of 64 rows takes about 3,100 cycles a CTA: its epilogue multiplies 128 x 64 x 8
-// accumulators by their scales and takes 8,192 exponentials, about 5,300 cycles for each
-// of two warps a lane quarter, and the ring holds three parts.  At 16 rows (68.9 us) the
-// conversion of the records decides, about 2,100 cycles a tile.  With 28 or 32 warps or one
-// event per accumulator the chain of waits gets longer (118 to 142 us).
+// Bound: not memory.  655,360 positions x 8 tokens x 2 kv heads take 108 us, 1,450 GB/s of K
+// records and masses (the bytes alone: 23 us; the tensor pipe is 33 % active, the schedulers 65 %,
+// a third of that in waits).  A tile of 64 rows takes about 2,900 cycles a CTA: its epilogue
+// multiplies 128 x 64 x 8 accumulators by their scales and takes 8,192 exponentials in sixteen round
+// trips to TMEM, 5,300 cycles for each of two warps a lane quarter, and the ring holds three
+// parts.  Up to 48 rows a group's accumulators come in one trip (6 tokens 90 us), up to 32 a part's
+// (4 tokens 73 us, 1 token 65 us, where the conversion of the records decides, about 2,000 cycles
+// a tile).  More warps, one event per accumulator, 64 columns a trip or passes of 32 rows were
+// slower (114 to 160 us).  Short calls (32,768 positions x 6 tokens 11.9 us) wait 4,300 cycles for
+// their share and 3,000 to 6,000 for the queries before the first tile.
 //
 // Every mbarrier wait is bounded; on a timeout the CTA sets Q3KV_STATUS_TIMEOUT, stops
 // issuing, waits (bounded) for its MMAs in flight, frees its TMEM and returns.
@@ -292,7 +296,8 @@ __device__ void next_segment(const MassArgs& a, MassSmem<FMT>& sm, int k) {
 
 // Accumulator columns of a group: the query rows of a pass, rounded up.
 __device__ __forceinline__ int acc_cols(const Segment& s) {
-    return kGroup * s.T <= 16 ? 16 : (kGroup * s.T <= 32 ? 32 : kChunkRows);
+    const int rows = kGroup * s.T;
+    return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 48 ? 48 : kChunkRows));
 }
 // Query rows of pass j as the products read them.
 __device__ __forceinline__ int mma_rows(const Segment& s, int j) {
@@ -592,7 +597,7 @@ __device__ __forceinline__ float part_scale(const uint4& sc, int part, int gi) {
 }
 
 // Epilogue of this warp's tiles of a segment; COLS accumulator columns per group
-// (16, 32 or 64 query rows of a pass).
+// (16, 32, 48 or 64 query rows of a pass).
 template <int FMT, int COLS, int BUFFERS>
 __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, const EpiState& e, bool ok) {
     constexpr int G = Mf<FMT>::kGroups, ST = Mf<FMT>::kStages, SLOTS = acc_slots<FMT>(BUFFERS, COLS);
@@ -670,6 +675,28 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
                         const unsigned long long s2 = pack2(scale, scale);
 #pragma unroll
                         for (int k = 0; k < LD / 2; ++k) acc[k] = fma2(pack2(x[gi][2 * k], x[gi][2 * k + 1]), s2, acc[k]);
+                    }
+                } else if (COLS == 48) {
+                    // a group in one round trip (655,360 positions x 6 tokens: 90 us, as half of 64 rows 105)
+#pragma unroll
+                    for (int gi = 0; gi < G; ++gi) {
+                        const float scale = part_scale<FMT>(sc, part, gi);
+                        float x[32], z[16];
+                        tmem_ld32(col + COLS * gi, x);
+                        tmem_ld16(col + COLS * gi + 32, z);
+                        tmem_ld_wait();
+                        if (gi == G - 1) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bar.acc_free[c % kFreeBars]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < COLS / 2; ++k) {
+                            float a0, a1;
+                            unpack2(acc[k], a0, a1);
+                            const float x0 = k < 16 ? x[2 * k % 32] : z[(2 * k) % 16], x1 = k < 16 ? x[(2 * k + 1) % 32] : z[(2 * k + 1) % 16];
+                            acc[k] = pack2(fmaf(x0, scale, a0), fmaf(x1, scale, a1));
+                        }
                     }
                 } else {
 #pragma unroll
@@ -767,9 +794,10 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc_col<FMT>(s.buffers), abort};
             constexpr int B = double_buffered<FMT>(1) ? 2 : 1;
             const int rows = kGroup * s.T;
-            if (rows <= 16) ok = epilogue<FMT, 16, B>(a, s, sm, e, ok);
-            else if (rows <= 32) ok = epilogue<FMT, 32, B>(a, s, sm, e, ok);
-            else ok = epilogue<FMT, 64, 1>(a, s, sm, e, ok);
+            if (rows > 48) ok = epilogue<FMT, 64, 1>(a, s, sm, e, ok);
+            else if (rows > 32) ok = epilogue<FMT, 48, 1>(a, s, sm, e, ok);
+            else if (rows > 16) ok = epilogue<FMT, 32, B>(a, s, sm, e, ok);
+            else ok = epilogue<FMT, 16, B>(a, s, sm, e, ok);
             named_sync(0, kThreads);
             if (*abort) break;
         }

@@ -83,6 +83,12 @@ MASS_CASES = [
     ("fp8", [513], [1], 4, torch.bfloat16, 0.25, 1),
     ("t5k", [700, 130], [3, 16], 2, torch.float32, 1.0, 2),
     ("t5k", [2000], [8], 1, torch.bfloat16, 0.0, 1),
+    # every pass shape (16, 32, 48, 64 and 2 x 64 rows) in one call, and several tiles of each for a CTA
+    ("q3", [3001, 2600, 2801, 3100, 2222, 1999], [6, 1, 16, 3, 8, 5], 2, torch.bfloat16, 1.0, 1),
+    ("fp8", [600, 520, 811, 300, 222], [5, 16, 3, 6, 1], 2, torch.bfloat16, 1.0, 1),
+    ("t5k", [600, 520, 811, 300, 222], [6, 9, 4, 5, 2], 1, torch.float32, 0.5, 1),
+    ("q3", [20000], [6], 2, torch.float32, 1.0, 1),
+    ("q3", [19000], [13], 2, torch.bfloat16, 1.0, 1),
 ]
 
 
