@@ -160,7 +160,14 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(VerifyArgs a, int 
     }
     part[sg][c] = acc;
     __syncthreads();
-    if (warp != 0) return;
+    if (warp != 0) {
+        if (a.lse && tid == 32) {                        // ln sum e^s over all splits, in the leg's units
+            const int rl = row0 + r;
+            a.lse[((int64_t)a.q_offsets[slot] + rl / kGroup) * a.num_kv_heads * kGroup + g * kGroup + rl % kGroup] =
+                LOG2 ? 0.6931471805599453f * (M + log2f(den)) : M + logf(den);
+        }
+        return;
+    }
 
     // ---- one warp: sum the split groups, out = H o / 16 (lane holds dims 8 lane .. 8 lane + 7);
     // without ROT (the fp8 cache, unrotated) out = o
@@ -178,10 +185,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(VerifyArgs a, int 
     if (ROT) rotate_row_regs(x);
     const int ra = row0 + r;
     const int Hq = a.num_kv_heads * kGroup;
-    // ln sum e^s over all splits, in the leg's units
-    if (a.lse && lane == 0)
-        a.lse[((int64_t)a.q_offsets[slot] + ra / kGroup) * Hq + g * kGroup + ra % kGroup] =
-            LOG2 ? 0.6931471805599453f * (M + log2f(den)) : M + logf(den);
     float* dst = a.out + (((int64_t)a.q_offsets[slot] + ra / kGroup) * Hq + g * kGroup + ra % kGroup) * kHeadDim + 8 * lane;
     constexpr float kS = ROT ? 0.0625f : 1.0f;
     reinterpret_cast<float4*>(dst)[0] = make_float4(x[0] * kS, x[1] * kS, x[2] * kS, x[3] * kS);

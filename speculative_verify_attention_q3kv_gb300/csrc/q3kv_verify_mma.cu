@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(256) qprep_kernel(VerifyArgs a) {
     *reinterpret_cast<uint4*>(&qlo[q_off(r, 8 * lane)]) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
 }
 
-template <typename TIn, int FMT>
+template <typename TIn, int FMT, bool LSE>
 __global__ void __launch_bounds__(kThreads, 1) verify_mma_kernel(VerifyArgs a) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     MmaSmem<FMT>& sm = *reinterpret_cast<MmaSmem<FMT>*>(smem_raw);
@@ -631,12 +631,6 @@ __global__ void __launch_bounds__(kThreads, 1) verify_mma_kernel(VerifyArgs a) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                     if (c + k < Rc) dst[(c + k) * kHeadDim + d] = v[k] * sm.alpha[c + k];
-            }
-            if (n_splits == 1 && a.lse && tid < Rc) {
-                // scores are in log2 units: ln sum e^s = ln 2 (m + log2 l)
-                const int ra = row0 + tid;
-                a.lse[(q_base + ra / kGroup) * Hq + g * kGroup + ra % kGroup] =
-                    0.6931471805599453f * (sm.m_run[tid] + log2f(sm.l_run[tid]));
             }
             if (n_splits > 1 && tid < Rc) {
                 float* pml = a.part_ml + ((int64_t)unit * a.num_splits + split) * kRows * 2;
@@ -1023,14 +1017,21 @@ __global__ void __launch_bounds__(kThreads, 1) verify_mma_kernel(VerifyArgs a) {
             o4[0] = make_float4(y[0] * kOutScale, y[1] * kOutScale, y[2] * kOutScale, y[3] * kOutScale);
             o4[1] = make_float4(y[4] * kOutScale, y[5] * kOutScale, y[6] * kOutScale, y[7] * kOutScale);
         }
+        // scores are in log2 units: ln sum e^s = ln 2 (m + log2 l).  Its own instantiation: the branch
+        // alone costs the calls without a statistic 0.5 to 0.8 % (registers of the whole kernel)
+        if (LSE && tid < Rc) {
+            const int ra = row0 + tid;
+            a.lse[(q_base + ra / kGroup) * Hq + g * kGroup + ra % kGroup] =
+                0.6931471805599453f * (sm.m_run[tid] + log2f(sm.l_run[tid]));
+        }
     }
 }
 
-template <typename TIn, int FMT>
+template <typename TIn, int FMT, bool LSE>
 cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t stream, std::atomic<bool>& attr_set) {
     const size_t smem = sizeof(MmaSmem<FMT>);
     if (!attr_set.load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(verify_mma_kernel<TIn, FMT>,
+        const cudaError_t e = cudaFuncSetAttribute(verify_mma_kernel<TIn, FMT, LSE>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         attr_set.store(true, std::memory_order_release);
@@ -1058,7 +1059,20 @@ cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t stream, std::atomic<b
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_mma_kernel<TIn, FMT>, a);
+    return cudaLaunchKernelEx(&cfg, verify_mma_kernel<TIn, FMT, LSE>, a);
+}
+
+template <bool LSE>
+cudaError_t launch_format(const VerifyArgs& a, cudaStream_t stream, std::atomic<bool>* attr_set) {
+    const bool f32 = a.dtype == Q3KV_F32;
+    if (a.fmt == kFmtFp8)
+        return f32 ? launch_typed<float, kFmtFp8, LSE>(a, stream, attr_set[2])
+                   : launch_typed<__nv_bfloat16, kFmtFp8, LSE>(a, stream, attr_set[3]);
+    if (a.fmt == kFmtT5k)
+        return f32 ? launch_typed<float, kFmtT5k, LSE>(a, stream, attr_set[4])
+                   : launch_typed<__nv_bfloat16, kFmtT5k, LSE>(a, stream, attr_set[5]);
+    return f32 ? launch_typed<float, kFmtQ3, LSE>(a, stream, attr_set[0])
+               : launch_typed<__nv_bfloat16, kFmtQ3, LSE>(a, stream, attr_set[1]);
 }
 
 }  // namespace
@@ -1067,19 +1081,10 @@ cudaError_t launch_verify_mma(const VerifyArgs& a, cudaStream_t stream) {
     // the shared-memory opt-in is a per-device function attribute: one flag per
     // (device, instantiation)
     constexpr int kMaxDevices = 64;
-    static std::atomic<bool> flags[kMaxDevices][6];
+    static std::atomic<bool> flags[kMaxDevices][12];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    std::atomic<bool>* attr_set = flags[dev];
-    const bool f32 = a.dtype == Q3KV_F32;
-    if (a.fmt == kFmtFp8)
-        return f32 ? launch_typed<float, kFmtFp8>(a, stream, attr_set[2])
-                   : launch_typed<__nv_bfloat16, kFmtFp8>(a, stream, attr_set[3]);
-    if (a.fmt == kFmtT5k)
-        return f32 ? launch_typed<float, kFmtT5k>(a, stream, attr_set[4])
-                   : launch_typed<__nv_bfloat16, kFmtT5k>(a, stream, attr_set[5]);
-    return f32 ? launch_typed<float, kFmtQ3>(a, stream, attr_set[0])
-               : launch_typed<__nv_bfloat16, kFmtQ3>(a, stream, attr_set[1]);
+    return a.lse ? launch_format<true>(a, stream, flags[dev] + 6) : launch_format<false>(a, stream, flags[dev]);
 }
 
 size_t verify_mma_smem_bytes() { return sizeof(MmaSmem<kFmtQ3>); }
