@@ -342,7 +342,7 @@ int chunk_plan(int64_t units, int32_t vocab, int32_t* chunk, int32_t* num) {
     const int e = device_sm_count(&sms);
     if (e != Q3KV_OK) return e;
     units = std::max<int64_t>(units, 1);
-    const int64_t target = std::max<int64_t>(1, (2 * (int64_t)sms + units - 1) / units);
+    const int64_t target = std::max<int64_t>(1, 2 * (int64_t)sms / units);
     const int64_t n = std::min<int64_t>(target, ((int64_t)vocab + 2047) / 2048);
     const int64_t c = (((int64_t)vocab + n - 1) / n + 7) / 8 * 8;
     *chunk = (int32_t)c;
