@@ -17,8 +17,8 @@
 // its chunk of row a.  The race's winner is a 64-bit atomic maximum of (key,
 // ~index) per slot, whatever the order; the slot's last CTA stores the results.
 //
-// 8 slots x 1 to 8 tokens, vocab 248,320, bf16: 22.0 us, of which the bytes alone are 3.2;
-// 1 slot x 6 tokens 13.5 us: two launches and about eight dependent trips to L2 or HBM.
+// 8 slots x 1 to 8 tokens, vocab 248,320, bf16: 19.1 us, of which the bytes alone are 3.2;
+// 1 slot x 6 tokens 12.0 us: two launches and about eight dependent trips to L2 or HBM.
 //
 // Issue slots decide beside that: the statistics take six instructions an entry
 // (bad logits show in the sum, not per entry), and the race computes a clock only
@@ -334,9 +334,10 @@ cudaError_t launch_pdl(K kernel, dim3 grid, const DraftArgs& a, cudaStream_t str
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// Chunks of one vocabulary row: enough CTAs over `units` rows to cover the GPU
-// about twice, at least 2,048 entries each, a multiple of 8.  (512 threads a CTA: 8 slots
-// 26 -> 22 us, one slot 14.8 -> 13.5 us, against 256.)
+// Chunks of one vocabulary row: over `units` rows at most the two CTAs per SM that run at
+// once (a few more make a second wave: 8 slots 22.8 us, in one wave 19.1), at least 2,048
+// entries each, a multiple of 8.  (512 threads a CTA: one slot 14.8 -> 13.5 us against 256;
+// three CTAs per SM gain nothing: 19.5 us.)
 int chunk_plan(int64_t units, int32_t vocab, int32_t* chunk, int32_t* num) {
     int sms = 0;
     const int e = device_sm_count(&sms);
