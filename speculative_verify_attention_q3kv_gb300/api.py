@@ -34,10 +34,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return _lib.Q3KV_F32
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
         return _lib.Q3KV_BF16
+    if dtype is torch.float32:
+        return _lib.Q3KV_F32
     raise TypeError(f"q3kv inputs must be float32 or bfloat16, got {t.dtype}")
 
 
@@ -150,7 +151,7 @@ def _pointers(dev: int, *args):
             continue
         if not isinstance(t, tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        if index(t) != dev or (dtype is not None and t.dtype != dtype) or (need and t.numel() < need):
+        if index(t) != dev or (t.dtype is not dtype and dtype is not None) or (need and t.numel() < need):
             _on_gpu(name, t, dev, dtype, need)
         if not t.is_contiguous():
             raise ValueError("tensors passed to q3kv must be contiguous")
@@ -677,7 +678,7 @@ def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.
     for name, x, y in (("q", q, q_out),) if k is None else (("q", q, q_out), ("k", k, k_out)):
         src, src_stride, heads = _strided_rows(name, x, rows, dev)
         dst, dst_stride, out_heads = _strided_rows(name + "_out", y, rows, dev)
-        if heads != out_heads or x.dtype != dtype or y.dtype != dtype:
+        if heads != out_heads or x.dtype is not dtype or y.dtype is not dtype:
             raise ValueError(f"{name} and {name}_out must have the heads of one another and the dtype of q")
         if rows and heads and not (src == dst and src_stride == dst_stride):
             # extents in bytes; an exact in-place call is fine, any other overlap is not

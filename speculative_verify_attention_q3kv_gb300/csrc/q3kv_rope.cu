@@ -80,7 +80,7 @@ template <typename T, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int V = 16 / sizeof(T);                    // elements per 16-byte vector
     constexpr int kSlots = kHeadDim / V / 2;             // work items per head
-    __shared__ float2 cs[kMaxRowsPerCta][kMaxPairs];
+    __shared__ __align__(16) float2 cs[kMaxRowsPerCta][kMaxPairs];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int row0 = blockIdx.x * a.rows_per_cta;
@@ -169,11 +169,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float2 p = t[i];
-                const float x0 = x[i], y0 = y[i];
+            for (int i = 0; i < V; i += 2) {
+                const float4 p = *reinterpret_cast<const float4*>(t + i);
+                const float x0 = x[i], y0 = y[i], x1 = x[i + 1], y1 = y[i + 1];
                 x[i] = x0 * p.x - y0 * p.y;
                 y[i] = x0 * p.y + y0 * p.x;
+                x[i + 1] = x1 * p.z - y1 * p.w;
+                y[i + 1] = x1 * p.w + y1 * p.z;
             }
         }
         *cur.dst0 = pack(x, static_cast<const T*>(nullptr));
