@@ -22,8 +22,7 @@
 //
 // Issue slots decide beside that: the statistics take six instructions an entry
 // (bad logits show in the sum, not per entry), and the race computes a clock only
-// where it can win: E = -log U >= 1 - U, so r / E <= r / (1 - U), which the noise's
-// integer gives without a logarithm.
+// where it can win (see race).
 //
 // Exponents: e^((l - max) / tau) with l - max taken on the raw logits (exact for
 // the ones that count); a tested probability has log2(e) / tau split in two floats,
@@ -191,8 +190,40 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
     return v;
 }
 
+// The race w / E of 8 entries of every lane, from index k on, w >= 0.  With U = (n + 1/2) / 2^23,
+// E = -log U >= 1 - U = (2^23 - n - 1/2) / 2^23, so w / (1 - U), a little generous, bounds a key
+// without a logarithm.  Every lane computes the key of the entry with its largest bound, and
+// after that only those whose bound reaches the warp's best key: about one logarithm a lane and step
+// where eight tests against the keys of earlier steps took most of the eight.
+__device__ __forceinline__ void race(const float (&w)[8], const float (&n)[8], int k, unsigned long long& best, float& top) {
+    auto enter = [&](float wi, float ni, int x) {
+        const float e = -logf((ni + 0.5f) * (1.0f / 8388608.0f));
+        best = max(best, candidate(wi / e, x));
+    };
+    float bound[8];
+    float b = 0.0f, bw = 0.0f, bn = 0.0f;
+    int bi = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bound[i] = __fdividef(w[i], (8388607.5f - n[i]) * (0.9999f / 8388608.0f));
+        if (bound[i] > b) {
+            b = bound[i];
+            bw = w[i];
+            bn = n[i];
+            bi = i;
+        }
+    }
+    if (!__any_sync(0xffffffffu, b >= top && b > 0.0f)) return;
+    if (b >= top && b > 0.0f) enter(bw, bn, k + bi);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (bound[i] >= top && bound[i] > 0.0f && i != bi) enter(w[i], n[i], k + i);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32)));
+}
+
 template <typename T, typename Q>
-__global__ void __launch_bounds__(kThreads) residual_kernel(const DraftArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) residual_kernel(const DraftArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float2 st[kMaxNq];
@@ -251,33 +282,32 @@ __global__ void __launch_bounds__(kThreads) residual_kernel(const DraftArgs a) {
         const int c0 = chunk * a.chunk2;
         const int c1 = min(a.vocab, c0 + a.chunk2);
         unsigned long long best_r = 0ull, best_p = 0ull;
-        // bounds that a candidate has to reach: the warp's best keys so far
+        // the warp's best keys so far: a candidate has to reach them
         float top_r = 0.0f, top_p = 0.0f;
         bool bad = false;
         if (v.x > -CUDART_INF_F) {
             for (int k0 = c0 + 8 * (threadIdx.x & ~31); k0 < c1; k0 += 8 * kThreads) {   // warp-uniform
                 const int k = k0 + 8 * lane;
-                float x[8], q[8];
-                load8(lg, a.vec_logits, k, c1, -CUDART_INF_F, x);
-                if (!bonus) load8(dr, a.vec_draft, k, c1, 0.0f, q);
+                float p[8], r[8], n[8];
+                load8(lg, a.vec_logits, k, c1, -CUDART_INF_F, p);
+                if (!bonus) load8(dr, a.vec_draft, k, c1, 0.0f, r);
+                const uint64_t z = noise_state(a.seed, (uint32_t)row, (uint32_t)k);
+                float most = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p = weight(a, x[i], v.x) * inv;
-                    const float rest = bonus ? 0.0f : p - q[i];
-                    if (!bonus) bad |= !(q[i] >= 0.0f && q[i] < CUDART_INF_F);
-                    // U = (n + 1/2) / 2^23, 1 - U = (2^23 - n - 1/2) / 2^23; the bound is a little generous
-                    const float n = noise_level(a.seed, (uint32_t)row, (uint32_t)(k + i));
-                    const float gap = (8388607.5f - n) * (0.9999f / 8388608.0f);
-                    const bool try_p = p > 0.0f && p >= top_p * gap, try_r = rest > 0.0f && rest >= top_r * gap;
-                    // p can only be wanted while no residual is positive
-                    if (try_r || (try_p && (bonus || top_r == 0.0f))) {
-                        const float e = -logf((n + 0.5f) * (1.0f / 8388608.0f));
-                        if (try_r) best_r = max(best_r, candidate(rest / e, k + i));
-                        if (try_p) best_p = max(best_p, candidate(p / e, k + i));
+                    const float d = fmaxf(p[i] - v.x, -1e30f);               // of -inf and NaN: probability 0
+                    p[i] = exp2_approx(fmaf(d, a.c_hi, d * a.c_lo)) * inv;
+                    if (bonus) {
+                        r[i] = p[i];
+                    } else {
+                        bad |= !(r[i] >= 0.0f && r[i] < CUDART_INF_F);
+                        r[i] = fmaxf(p[i] - r[i], 0.0f);                     // NaN counts as nothing
                     }
+                    most = fmaxf(most, r[i]);
+                    n[i] = noise_level(z + (uint64_t)i * kNoiseStep);
                 }
-                top_r = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best_r >> 32)));
-                top_p = __uint_as_float(__reduce_max_sync(0xffffffffu, (uint32_t)(best_p >> 32)));
+                if (top_r > 0.0f || __any_sync(0xffffffffu, most > 0.0f)) race(r, n, k, best_r, top_r);
+                else race(p, n, k, best_p, top_p);                           // wanted if no residual is positive at all
             }
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
