@@ -17,8 +17,8 @@
 // its chunk of row a.  The race's winner is a 64-bit atomic maximum of (key,
 // ~index) per slot, whatever the order; the slot's last CTA stores the results.
 //
-// 8 slots x 1 to 8 tokens, vocab 248,320, bf16: 19.1 us, of which the bytes alone are 3.2;
-// 1 slot x 6 tokens 12.0 us: two launches and about eight dependent trips to L2 or HBM.
+// 8 slots x 1 to 8 tokens, vocab 248,320, bf16: 17.1 us, of which the bytes alone are 3.2;
+// 1 slot x 6 tokens 10.8 us: two launches and about eight dependent trips to L2 or HBM.
 //
 // Issue slots decide beside that: the statistics take six instructions an entry
 // (bad logits show in the sum, not per entry), and the race computes a clock only
@@ -194,7 +194,7 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // E = -log U >= 1 - U = (2^23 - n - 1/2) / 2^23, so w / (1 - U), a little generous, bounds a key
 // without a logarithm.  Every lane computes the key of the entry with its largest bound, and
 // after that only those whose bound reaches the warp's best key: about one logarithm a lane and step
-// where eight tests against the keys of earlier steps took most of the eight.
+// where eight tests against the keys of earlier steps took most of the eight (8 slots 19.1 -> 17.1 us).
 __device__ __forceinline__ void race(const float (&w)[8], const float (&n)[8], int k, unsigned long long& best, float& top) {
     auto enter = [&](float wi, float ni, int x) {
         const float e = -logf((ni + 0.5f) * (1.0f / 8388608.0f));
@@ -366,8 +366,7 @@ cudaError_t launch_pdl(K kernel, dim3 grid, const DraftArgs& a, cudaStream_t str
 
 // Chunks of one vocabulary row: over `units` rows at most the two CTAs per SM that run at
 // once (a few more make a second wave: 8 slots 22.8 us, in one wave 19.1), at least 2,048
-// entries each, a multiple of 8.  (512 threads a CTA: one slot 14.8 -> 13.5 us against 256;
-// three CTAs per SM gain nothing: 19.5 us.)
+// entries each (4,096: one slot 10.8 -> 12.3 us), a multiple of 8.
 int chunk_plan(int64_t units, int32_t vocab, int32_t* chunk, int32_t* num) {
     int sms = 0;
     const int e = device_sm_count(&sms);

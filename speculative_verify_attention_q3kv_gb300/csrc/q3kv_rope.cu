@@ -9,8 +9,8 @@
 // as a signed number of turns in [-1/2, 1/2), go to sincospi.  The product is
 // integer work; no float64 is needed.
 //
-// Bound: memory (a row is read and written once): 4,096 rows of 18 bf16 heads take 15.1 us,
-// 5,000 GB/s; 8,191 float32 rows 50.4 us, 6,000 GB/s; 6 rows 2.4 us, one launch.  One CTA takes kRowsPerCta
+// Bound: memory (a row is read and written once): 4,096 rows of 18 bf16 heads take 14.8 us,
+// 5,100 GB/s; 8,191 float32 rows 50.4 us, 6,000 GB/s; 6 rows 2.4 us, one launch.  One CTA takes kRowsPerCta
 // rows: its threads first fill the rows' (cos, sin) table in shared memory, once
 // per row for all its heads, with the first 32 bytes of their data already
 // in flight, then rotate.  A work item is two 16-byte vectors of one head: the
