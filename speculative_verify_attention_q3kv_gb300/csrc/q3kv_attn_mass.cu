@@ -26,7 +26,7 @@
 //
 // Warp roles (24 warps; registers are moved between the roles with setmaxnreg):
 //   E   warps 0-7    epilogue: thread = position (lane quarter warp & 3), all rows of the
-//                    chunk; the two warps of a lane quarter take every other tile.  Score
+//                    pass; the two warps of a lane quarter take every other tile.  Score
 //                    sums start at -lse in log2 units, weights 2^s, rows summed in the
 //                    thread.  Before a segment they rotate and split its queries.
 //   D   warps 8-15   thread = position: its staged record converted into TMEM, one warp of
@@ -43,15 +43,15 @@
 // reach (see whole_shares); a CTA rotates and splits the queries of a pair itself when it
 // enters it.
 //
-// Bound: not memory.  655,360 positions x 8 tokens x 2 kv heads take 108 us, 1,450 GB/s of K
+// Bound: not memory.  655,360 positions x 8 tokens x 2 kv heads take 105 us, 1,500 GB/s of K
 // records and masses (the bytes alone: 23 us; the tensor pipe is 33 % active, the schedulers 65 %,
 // a third of that in waits).  A tile of 64 rows takes about 2,900 cycles a CTA: its epilogue
 // multiplies 128 x 64 x 8 accumulators by their scales and takes 8,192 exponentials in sixteen round
 // trips to TMEM, 5,300 cycles for each of two warps a lane quarter, and the ring holds three
-// parts.  Up to 48 rows a group's accumulators come in one trip (6 tokens 90 us), up to 32 a part's
-// (4 tokens 73 us, 1 token 65 us, where the conversion of the records decides, about 2,000 cycles
+// parts.  Up to 48 rows a group's accumulators come in one trip (6 tokens 92 us), up to 32 a part's
+// (4 tokens 73 us, 1 token 67 us, where the conversion of the records decides, about 2,000 cycles
 // a tile).  More warps, one event per accumulator, 64 columns a trip or passes of 32 rows were
-// slower (114 to 160 us).  Short calls (32,768 positions x 6 tokens 11.9 us) wait 4,300 cycles for
+// slower (114 to 160 us).  Short calls (32,768 positions x 6 tokens 12.1 us) wait 4,300 cycles for
 // their share and 3,000 to 6,000 for the queries before the first tile.
 //
 // Every mbarrier wait is bounded; on a timeout the CTA sets Q3KV_STATUS_TIMEOUT, stops
@@ -220,11 +220,13 @@ __host__ __device__ constexpr int acc_slots(int buffers, int cols) {
     return buffers == 2 ? 256 / (Mf<FMT>::kGroups * cols) : 192 / cols;
 }
 
-// Shares that stay within one (slot, kv head) pair, where the CTAs reach: the smallest d for
-// which giving every pair ceil(tiles / d) CTAs takes no more than the grid.  A pair change
-// drains the pipeline and prepares other queries, some 4 us (8 ragged slots x 2 heads on
-// 152 CTAs: 19.5 us with even shares, 16.1 us).  One warp, a lane per slot; false if there are more
-// than 32 slots or more pairs than CTAs (even shares are then better).
+// Shares that stay within one (slot, kv head) pair: the smallest d for which giving every
+// pair ceil(tiles / d) CTAs takes no more than the grid.  A pair change drains the pipeline and
+// prepares other queries, about two tiles' time, so they are taken if d is at most that much above an
+// even share, once per pair that an even share meets (8 ragged slots x 2 heads x 1 token, 9
+// tiles a CTA: 13.5 us, with even shares 16.0; 8 slots of 40,000 positions x 4 heads, 79 tiles for
+// 66: 74.5 us, with even shares 66.4).  One warp, a lane per slot; false if even shares are better,
+// with more than 32 slots, or with more pairs than CTAs.
 template <int FMT>
 __device__ inline bool whole_shares(const MassArgs& a, Segment& seg, bool* bad) {
     if (a.num_slots > 32) return false;
@@ -244,6 +246,7 @@ __device__ inline bool whole_shares(const MassArgs& a, Segment& seg, bool* bad) 
         if (__reduce_add_sync(0xffffffffu, (tiles + mid - 1) / mid) <= per) hi = mid;
         else lo = mid;
     }
+    if (hi > (total + per - 1) / per + 2 + 2 * slots / per) return false;
     const int ctas = (tiles + hi - 1) / hi;                // per pair of this lane's slot
     int incl = ctas * H;
 #pragma unroll
@@ -677,7 +680,7 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
                         for (int k = 0; k < LD / 2; ++k) acc[k] = fma2(pack2(x[gi][2 * k], x[gi][2 * k + 1]), s2, acc[k]);
                     }
                 } else if (COLS == 48) {
-                    // a group in one round trip (655,360 positions x 6 tokens: 90 us, as half of 64 rows 105)
+                    // a group in one round trip (655,360 positions x 6 tokens: 92 us, in the form for 64 rows 105)
 #pragma unroll
                     for (int gi = 0; gi < G; ++gi) {
                         const float scale = part_scale<FMT>(sc, part, gi);
@@ -826,7 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                     __syncwarp();
                     tc_fence_after();
                     const uint32_t col = col0 + kPartCols * (kParts * buf + odd);
-#pragma unroll
+                    // rolled: the roles share the instruction cache (655,360 positions x 8 tokens, which do not even
+                    // take this path, 114 -> 105 us; 1 token 65 -> 67)
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         uint32_t wc[Words<FMT>::kN];
                         read_part<FMT>(rec, odd + 2 * h, wc);
