@@ -16,20 +16,20 @@
 // memory), then one warp finds the coarse bin that holds the k-th and reads its 32 bins
 // from every CTA; reading all bins of all CTAs took longer than counting.
 //
-// 512 threads of at most 64 registers let two CTAs share an SM.  The lists are short
-// because the L1 lines that loads in flight need come out of the same 256 KB: with lists of
-// 1,024 masses 32 rows of 655,360 took 60 us more.
+// 1,024 threads of an SM, in two CTAs or one, with at most 64 registers each.  The lists are
+// short because the L1 lines that loads in flight need come out of the same 256 KB: with
+// lists of 1,024 masses 32 rows of 655,360 took 60 us more.
 //
 // gather_kernel: a CTA moves up to 256 kept records, one destination page, of K and V:
 // their source offsets go to shared memory first, so all 16-byte loads (4-byte ones
 // for the 164-byte K records) of a thread are independent, and the stores, to
 // consecutive records, coalesce.
 //
-// Bound: memory.  32 rows of 655,360 masses, 65,536 kept, take 269 us: select 71 us (84 MB
+// Bound: memory.  32 rows of 655,360 masses, 65,536 kept, take 264 us: select 66 us (84 MB
 // from HBM once and from L2 twice; about a third each for the first pass, the second with
 // the levels, and the last), gather 198 us (470 MB of records read and written; a
 // scattered 112-byte record touches 64-byte DRAM bursts worth half as much again, with
-// which the traffic alone takes 173 us).  2 rows of 5,000: 13.7 us, where each of the three
+// which the traffic alone takes 173 us).  2 rows of 5,000: 13.3 us, where each of the three
 // levels costs a cluster barrier and a trip to the other CTAs, 1.5 us.
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -44,8 +44,6 @@ namespace cg = cooperative_groups;
 namespace q3kv {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kPerLane = 8;                               // masses of a lane per tile
 constexpr int kTile = 32 * kPerLane;                      // a warp's
 constexpr int kBins = 2048;
@@ -54,7 +52,7 @@ constexpr int kLevels = 3;
 constexpr int kMaxCluster = 16;
 constexpr int kListCap = 512;
 constexpr uint32_t kKeyInf = 0xff800000u, kKeyMinusInf = 0x007fffffu;   // order keys of the infinities
-static_assert(kBins == 4 * kSelThreads && kMaxCluster <= 32, "find_bin");
+static_assert(kBins == 4 * 512 && kMaxCluster <= 32, "find_bin");
 
 struct EvictArgs {
     uint8_t* pool;
@@ -126,19 +124,22 @@ __device__ __forceinline__ int warp_scan(int v) {   // inclusive
     return v;
 }
 
+template <int kWarps>
 struct __align__(16) SelectSmem {
     int hist[kLevels][kBins];                  // this CTA's counts
     int coarse[2][kMaxCluster][kCoarse];       // every CTA's counts of 32 bins each, by level % 2
     int2 total[kMaxCluster];                   // every CTA's entries above the threshold, and at it
-    int2 warp[kSelWarps];                      // the same of this CTA's warps
+    int2 warp[kWarps];                      // the same of this CTA's warps
     int found_bin;
     int found_above;                           // entries in bins above it
-    float list[kSelWarps][kListCap];           // a warp's masses in the first level's bin
+    float list[kWarps][kListCap];           // a warp's masses in the first level's bin
 };
 
-__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs a) {
+template <int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) select_kernel(const EvictArgs a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_raw);
+    constexpr int kSelWarps = kSelThreads / 32;
+    SelectSmem<kSelWarps>& sm = *reinterpret_cast<SelectSmem<kSelWarps>*>(smem_raw);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictArgs 
     // Finds the bin of hist[level] that holds the cluster's want-th entry from the top.
     auto find_bin = [&](int level) {
         __syncthreads();
-        {   // thread t adds bins 4 t .. 4 t + 3, eight threads a coarse bin, given to every CTA
+        if (tid < kBins / 4) {   // thread t adds bins 4 t .. 4 t + 3, eight threads a coarse bin, given to every CTA
             const int4 u = reinterpret_cast<const int4*>(&sm.hist[level][0])[tid];
             int t = (u.x + u.y) + (u.z + u.w);
 #pragma unroll
@@ -518,19 +519,21 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, int cluster, const Evic
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int kSelThreads>
 cudaError_t launch_select(const EvictArgs& a, unsigned rows, int cluster, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> attr_set[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    constexpr size_t smem = sizeof(SelectSmem<kSelThreads / 32>);
     if (!attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SelectSmem));
+        cudaError_t e = cudaFuncSetAttribute(select_kernel<kSelThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        const cudaError_t e2 = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e2 != cudaSuccess) return e2;
+        e = cudaFuncSetAttribute(select_kernel<kSelThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    return launch_pdl(select_kernel, dim3(rows * (unsigned)cluster), kSelThreads, cluster, a, stream, sizeof(SelectSmem));
+    return launch_pdl(select_kernel<kSelThreads>, dim3(rows * (unsigned)cluster), kSelThreads, cluster, a, stream, smem);
 }
 
 template <int FMT>
@@ -596,8 +599,12 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
         // 8 rows 109 -> 94), else up to 8 of two per SM (16 rows: 165 us, with 16 CTAs 172); half while half keeps a
         // row in registers
         int c = kMaxCluster;
-        while (c > 1 && (rows * c > (c > 8 ? 1 : 2) * (int64_t)sms || (int64_t)(c / 2) * kSelWarps * kTile >= max_ctx_len)) c >>= 1;
-        cudaError_t ce = launch_select(a, (unsigned)rows, c, st);
+        while (c > 1 && (rows * c > (c > 8 ? 1 : 2) * (int64_t)sms || (int64_t)(c / 2) * 512 * kPerLane >= max_ctx_len)) c >>= 1;
+        // where two would share an SM, one of 1,024 threads: a barrier and a remote trip have half the partners (32
+        // rows of 32,768: 44.3 -> 41.4 us a call, of 655,360 269 -> 264; with an SM each, 16 x 1,024 threads a row are
+        // slower than 16 x 512: 8 rows 109 us for 91)
+        cudaError_t ce = c > 1 && rows * c > sms ? launch_select<1024>(a, (unsigned)rows, c / 2, st)
+                                                 : launch_select<512>(a, (unsigned)rows, c, st);
         if (ce != cudaSuccess) return cuda_status(ce);
         ce = fmt == kFmtFp8 ? launch_gather<kFmtFp8>(a, st)
                             : (fmt == kFmtT5k ? launch_gather<kFmtT5k>(a, st) : launch_gather<kFmtQ3>(a, st));
