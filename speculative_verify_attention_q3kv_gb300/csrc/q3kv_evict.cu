@@ -25,11 +25,11 @@
 // for the 164-byte K records) of a thread are independent, and the stores, to
 // consecutive records, coalesce.
 //
-// Bound: memory.  32 rows of 655,360 masses, 65,536 kept, take 264 us: select 66 us (84 MB
+// Bound: memory.  32 rows of 655,360 masses, 65,536 kept, take 261 us: select 63 us (84 MB
 // from HBM once and from L2 twice; about a third each for the first pass, the second with
 // the levels, and the last), gather 198 us (470 MB of records read and written; a
 // scattered 112-byte record touches 64-byte DRAM bursts worth half as much again, with
-// which the traffic alone takes 173 us).  2 rows of 5,000: 13.3 us, where each of the three
+// which the traffic alone takes 173 us).  2 rows of 5,000: 12.9 us, where each of the three
 // levels costs a cluster barrier and a trip to the other CTAs, 1.5 us.
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -219,7 +219,9 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) select_kernel
             int t = (u.x + u.y) + (u.z + u.w);
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            for (int c = tid & 7; c < C; c += 8) *cluster.map_shared_rank(&sm.coarse[level & 1][rank][tid >> 3], c) = t;
+            if (C == 1) sm.coarse[level & 1][0][tid >> 3] = t;
+            else
+                for (int c = tid & 7; c < C; c += 8) *cluster.map_shared_rank(&sm.coarse[level & 1][rank][tid >> 3], c) = t;
         }
         if (C > 1) cluster.sync();
         else __syncthreads();
@@ -237,9 +239,9 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) select_kernel
             const bool second = before + t2.y < want;      // of the hitting lane's two
             const int cb = __shfl_sync(0xffffffffu, 63 - 2 * lane - (second ? 1 : 0), hit);
             const int above_c = __shfl_sync(0xffffffffu, before + (second ? t2.y : 0), hit);
-            int t = 0;
+            int t = C == 1 ? sm.hist[level][32 * cb + 31 - lane] : 0;
 #pragma unroll 1
-            for (int c0 = 0; c0 < C; c0 += 8)              // eight remote loads in flight
+            for (int c0 = 0; C > 1 && c0 < C; c0 += 8)     // eight remote loads in flight
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     if (c0 + c < C) t += cluster.map_shared_rank(&sm.hist[level][0], c0 + c)[32 * cb + 31 - lane];
@@ -368,7 +370,8 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) select_kernel
     if (warp == 0) {
         const int2 u = lane < kSelWarps ? sm.warp[lane] : make_int2(0, 0);
         const int2 t = make_int2(warp_sum(u.x), warp_sum(u.y));
-        if (lane < C) *cluster.map_shared_rank(&sm.total[rank], lane) = t;
+        if (C == 1) sm.total[0] = t;
+        else if (lane < C) *cluster.map_shared_rank(&sm.total[rank], lane) = t;
     }
     if (C > 1) cluster.sync();                             // the last remote access is done: a CTA may leave
     else __syncthreads();
@@ -601,9 +604,10 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
         int c = kMaxCluster;
         while (c > 1 && (rows * c > (c > 8 ? 1 : 2) * (int64_t)sms || (int64_t)(c / 2) * 512 * kPerLane >= max_ctx_len)) c >>= 1;
         // where two would share an SM, one of 1,024 threads: a barrier and a remote trip have half the partners (32
-        // rows of 32,768: 44.3 -> 41.4 us a call, of 655,360 269 -> 264; with an SM each, 16 x 1,024 threads a row are
+        // rows of 32,768: 44.3 -> 41.4 us a call, of 655,360 266 -> 261; 2 rows of 5,000, which one CTA
+        // then holds, 13.4 -> 12.9; with an SM each, 16 x 1,024 threads a row are
         // slower than 16 x 512: 8 rows 109 us for 91)
-        cudaError_t ce = c > 1 && rows * c > sms ? launch_select<1024>(a, (unsigned)rows, c / 2, st)
+        cudaError_t ce = c > 1 && (rows * c > sms || max_ctx_len <= 1024 * kPerLane) ? launch_select<1024>(a, (unsigned)rows, c / 2, st)
                                                  : launch_select<512>(a, (unsigned)rows, c, st);
         if (ce != cudaSuccess) return cuda_status(ce);
         ce = fmt == kFmtFp8 ? launch_gather<kFmtFp8>(a, st)
