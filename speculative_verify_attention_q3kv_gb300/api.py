@@ -644,11 +644,13 @@ def _strided_rows(name: str, t: torch.Tensor, rows: int, dev: int):
     """Pointer, row stride and heads of [rows, heads, 256] rows whose heads are contiguous; rows may be strided."""
     if not isinstance(t, torch.Tensor) or _device_index(t) != dev:
         _on_gpu(name, t, dev)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(t.shape)}")
-    (n, heads, dim), (row, head, one) = t.shape, t.stride()
-    if n != rows or dim != HEAD_DIM:
-        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be [{rows}, heads, {HEAD_DIM}], got {tuple(shape)}")
+    heads = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), heads * HEAD_DIM, heads
+    row, head, one = t.stride()
     if one != 1 or (heads > 1 and head != HEAD_DIM):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     return t.data_ptr(), row if rows > 1 else heads * HEAD_DIM, heads
