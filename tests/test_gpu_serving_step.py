@@ -4,6 +4,10 @@ prompt (rotate, append) -> step (rotate, append, verify with the statistic, acce
 sampled drafts, accumulate the mass over the committed tokens) -> eviction into
 fresh pages -> another step on the evicted cache.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -145,3 +149,47 @@ def test_prompt_step_evict_step():
         assert torch.allclose(grown, torch.full_like(grown, 8.0 * T), rtol=1e-3)
     torch.cuda.synchronize()
     assert int(status.item()) == 0
+
+
+_FIRST_CALLS = """
+import torch
+from speculative_verify_attention_q3kv_gb300 import api
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+desc = api.make_desc(1, 2, 8)
+pool = torch.zeros(api.pool_bytes(desc), dtype=torch.uint8, device="cuda")
+table, dst = i32(0, 1, 2, 3)[None], i32(4, 5)[None]
+q, k = torch.randn(3, 16, 256, device="cuda"), torch.randn(3, 2, 256, device="cuda")
+q2, k2 = torch.zeros_like(q), torch.zeros_like(k)
+pos, ctx, n, off = i32(1, 2, 3)[:, None], i32(900), i32(3), i32(0, 3)
+lse, mass = torch.zeros(3, 16, device="cuda"), torch.zeros(1, 1, 2, 1024, device="cuda")
+out, ws = torch.zeros(3, 16, 256, device="cuda"), torch.zeros(api.workspace_bytes(desc, 1, 900, 3), dtype=torch.uint8, device="cuda")
+kept, new, budget = torch.zeros(1, 1, 2, 300, dtype=torch.int32, device="cuda"), i32(0), i32(300)
+logits, draft = torch.randn(3, 5000, device="cuda"), torch.full((3, 5000), 1 / 5000, device="cuda")
+ws2 = torch.zeros(api.accept_draft_workspace_bytes(1, 3, 5000), dtype=torch.uint8, device="cuda")
+uni, tok, acc, nxt, com, st = torch.rand(3, device="cuda"), i32(5, 6, 7), i32(0), i32(0), i32(0), i32(0)
+plan = api.make_rope_plan(64, 1e4, (32,))
+def step():
+    api.rope(plan, pos, q, q2, k, k2)
+    api.verify_attn_lse(desc, pool, table, ctx, n, off, 900, 3, 0, q2, out, lse, ws, status=st)
+    api.attn_mass(desc, pool, table, ctx, n, off, 900, 3, 0, q2, lse, 0.0, mass[0], status=st)
+    api.evict(desc, pool, table, ctx, 900, budget, 300, 2, 9, 0, mass, dst, kept, None, new, status=st)
+    api.accept_draft(logits, draft, off, n, tok, 3, ctx, 1.0, uni, 5, acc, nxt, com, ws2, status=st)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (q2, k2, lse, mass, kept, new, acc, nxt, com, st)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (q2, k2, lse, mass, kept, new, acc, nxt, com, st)))
+assert new.item() == 300 and st.item() == 0 and abs(mass.sum().item() - 48) < 1e-2
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], capture_output=True, text=True, timeout=240, cwd=root)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
