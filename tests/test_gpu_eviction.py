@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 import torch
 
-from operator_harness import EVICT, MASS, VERIFY, VERIFY_LSE, Cache, i32, offsets, queries
+from operator_harness import APPEND, EVICT, MASS, POOL_BYTES, VERIFY, VERIFY_LSE, Cache, i32, offsets, queries
 from oracle import eviction as ev
 from speculative_verify_attention_q3kv_gb300 import _lib, api
 
@@ -556,3 +556,35 @@ def test_evict_length_in_the_budgets_place_and_without_layers():
     api.evict(c.desc, c.pool, c.page_table, ctx, 900, bud, 500, 0, 5, 0, none, dst,
               torch.zeros((0, 2, 1, 500), dtype=torch.int32, device="cuda"), None, new, st)
     assert new.tolist() == [900, 700] and int(st.item()) == _lib.Q3KV_STATUS_BAD_LENGTH
+
+
+@pytest.mark.parametrize("fmt", ["q3", "fp8", "t5k"])
+def test_records_beyond_32_bit_offsets(fmt):
+    # the same cache in the last layer and pages of a pool of more than 4 GB, and in a small pool
+    layers, n, T, keep = 64, 600, 4, 300
+    per_page = POOL_BYTES[fmt](api.make_desc(layers, 2, 1))
+    pages = int(1.1 * 2 ** 32) // per_page
+    assert pages * per_page > 2 ** 32
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    k, v = torch.randn((n, 2, 256), generator=gen, device="cuda"), torch.randn((n, 2, 256), generator=gen, device="cuda")
+    q = torch.randn((T, 16, 256), generator=gen, device="cuda")
+    results = []
+    for desc, layer, table, dst in ((api.make_desc(1, 2, 8), 0, [3, 1, 2], [5, 4]),
+                                    (api.make_desc(layers, 2, pages), layers - 1, [pages - 1, pages - 3, pages // 2], [pages - 2, 1])):
+        pool = torch.zeros(POOL_BYTES[fmt](desc), dtype=torch.uint8, device="cuda")
+        table, dst, st = i32([table]), i32([dst]), i32([0])
+        ws = torch.zeros(api.workspace_bytes(desc, 1, n, T), dtype=torch.uint8, device="cuda")
+        out, lse, mass = torch.zeros((T, 16, 256), device="cuda"), torch.zeros((T, 16), device="cuda"), torch.zeros((1, 1, 2, n), device="cuda")
+        APPEND[fmt](desc, pool, table, i32([0]), i32([n]), i32([0, n]), n, layer, k, v)
+        VERIFY_LSE[fmt](desc, pool, table, i32([n]), i32([T]), i32([0, T]), n, T, layer, q, out, lse, ws, status=st)
+        MASS[fmt](desc, pool, table, i32([n]), i32([T]), i32([0, T]), n, T, layer, q, lse, 0.0, mass[0], st)
+        kept, kept_mass, new = torch.zeros((1, 1, 2, keep), dtype=torch.int32, device="cuda"), torch.zeros((1, 1, 2, keep), device="cuda"), i32([0])
+        EVICT[fmt](desc, pool, table, i32([n]), n, i32([keep]), keep, 4, 32, layer, mass, dst, kept, kept_mass, new, st)
+        after = torch.zeros((T, 16, 256), device="cuda")
+        VERIFY[fmt](desc, pool, dst, new, i32([T]), i32([0, T]), keep, T, layer, q, after, ws, status=st)
+        assert int(st.item()) == 0 and new.tolist() == [keep]
+        results.append([x.cpu() for x in (out, lse, mass, kept, kept_mass, after)])
+        del pool
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert results[0][5].abs().max() > 0
