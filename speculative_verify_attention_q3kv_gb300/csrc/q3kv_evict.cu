@@ -25,9 +25,9 @@
 // for the 164-byte K records) of a thread are independent, and the stores, to
 // consecutive records, coalesce.
 //
-// Bound: memory.  32 rows of 655,360 masses, 65,536 kept, take 261 us: select 63 us (84 MB
+// Bound: memory.  32 rows of 655,360 masses, 65,536 kept, take 239 us: select 63 us (84 MB
 // from HBM once and from L2 twice; about a third each for the first pass, the second with
-// the levels, and the last), gather 198 us (470 MB of records read and written; a
+// the levels, and the last), gather 176 us (470 MB of records read and written; a
 // scattered 112-byte record touches 64-byte DRAM bursts worth half as much again, with
 // which the traffic alone takes 173 us).  2 rows of 5,000: 12.9 us, where each of the three
 // levels costs a cluster barrier and a trip to the other CTAs, 1.5 us.
@@ -430,6 +430,15 @@ __device__ __forceinline__ size_t rec_at(const EvictArgs& a, int64_t page, int l
 
 constexpr int kGatherThreads = 256;
 
+// A load for which L2 fetches 64 bytes from memory; a plain one fetches the 128-byte line, of
+// which a scattered record leaves half (16 layers x 655,360: gather 198 -> 176 us).
+__device__ __forceinline__ void load_64b(const void* p, uint4& v) {
+    asm volatile("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+}
+__device__ __forceinline__ void load_64b(const void* p, uint32_t& v) {
+    asm volatile("ld.global.L2::64B.u32 %0, [%1];" : "=r"(v) : "l"(p));
+}
+
 // Copies n records of UNITS units each from the offsets off[] to consecutive records at dst.
 template <typename U, int UNITS>
 __device__ __forceinline__ void move_records(uint8_t* pool, const size_t* off, int n, uint8_t* dst) {
@@ -447,7 +456,7 @@ __device__ __forceinline__ void move_records(uint8_t* pool, const size_t* off, i
             const int i = u / UNITS, part = u - i * UNITS;
             const size_t o = off[i];
             ok[r] = o != ~(size_t)0;
-            if (ok[r]) v[r] = *reinterpret_cast<const U*>(pool + o + part * sizeof(U));
+            if (ok[r]) load_64b(pool + o + part * sizeof(U), v[r]);
         }
 #pragma unroll
         for (int r = 0; r < kU; ++r)
