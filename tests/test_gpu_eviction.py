@@ -588,3 +588,50 @@ def test_records_beyond_32_bit_offsets(fmt):
     for a, b in zip(*results):
         assert torch.equal(a, b)
     assert results[0][5].abs().max() > 0
+
+
+@pytest.mark.parametrize("fmt,lengths,widths,kv", [
+    ("q3", [40000, 33000, 10000, 37001, 21000, 12345, 28000, 39999], [6, 1, 16, 3, 8, 2, 5, 9], 4),
+    ("q3", [40000, 33000, 10000, 37001, 21000, 12345, 28000, 39999], [1, 9, 4, 16, 2, 7, 1, 3], 4),
+    ("fp8", [30000, 12000, 20001, 9000], [4, 16, 1, 6], 4),
+    ("t5k", [30000, 12000, 20001, 9000], [4, 16, 1, 6], 4),
+])
+def test_mass_long_segments_of_several_pairs(fmt, lengths, widths, kv):
+    """Uneven slots in even shares: a CTA runs long segments of several (slot, kv head) pairs, of one operand buffer
+    and of two, so that every ring of the pipeline wraps inside a segment and goes on in the next.  A slot alone,
+    in shares of its own, gives the same bits; the row sums are what the definition makes them."""
+    c = Cache(fmt, lengths, kv, seed=46)
+    q = queries(sum(widths), 8 * kv, 47, torch.bfloat16)
+    n, T = max(lengths), max(widths)
+    lse = torch.zeros((q.shape[0], 8 * kv), device="cuda")
+    out = torch.empty((q.shape[0], 8 * kv, 256), device="cuda")
+    ws = torch.zeros(api.workspace_bytes(c.desc, len(lengths), n, T), dtype=torch.uint8, device="cuda")
+    VERIFY_LSE[fmt](c.desc, c.pool, c.page_table, i32(lengths), i32(widths), offsets(widths), n, T, 0, q, out, lse, ws, status=c.status)
+    mass = torch.full((len(lengths), kv, n), float("nan"), device="cuda")
+    _mass_call(c, lengths, widths, q, lse, 0.0, mass, status=c.status)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    for b, (L, t) in enumerate(zip(lengths, widths)):
+        one = torch.full_like(mass, float("nan"))
+        alone = [t if i == b else 0 for i in range(len(widths))]
+        MASS[fmt](c.desc, c.pool, c.page_table, i32(lengths), i32(alone), offsets(widths), n, T, 0, q, lse, 0.0, one, c.status)
+        torch.cuda.synchronize()
+        assert torch.equal(one[b, :, :L], mass[b, :, :L]) and bool(torch.isnan(mass[b, :, L:]).all())
+        # every row's weights add up to one, as far as the statistic and the scores are bounded (A < 2^7: 2^-8)
+        total = mass[b, :, :L].double().sum(dim=1)
+        assert torch.allclose(total, torch.full_like(total, 8.0 * t), rtol=2.0 ** -8)
+    b = len(lengths) - 1
+    _check_mass_slot(c, mass, lengths, widths, q, lse, b)
+    assert int(c.status.item()) == 0
+
+
+def _check_mass_slot(c, got, lengths, widths, q, lse, b):
+    n, t, r0 = lengths[b], widths[b], sum(widths[:b])
+    for g in range(c.kv):
+        s, bound = _reference(c, lengths, widths, q, 0, b, g)
+        l = lse[r0:r0 + t, 8 * g:8 * g + 8].double().cpu().numpy().reshape(-1)
+        want = ev.mass(np.zeros(n), s, l, 0.0, n - t)
+        w, seen = np.exp(s - l[:, None]), np.isfinite(s)
+        rel = np.where(seen, bound + 2.0 ** -22 * (1 + np.abs(np.where(seen, s, 0)) + np.abs(l[:, None])), 0)
+        tol = (w * rel).sum(axis=0) + 130 * 2.0 ** -23 * np.abs(want) + 1e-37
+        assert np.all(np.abs(got[b, g].double().cpu().numpy()[:n] - want) <= tol)
