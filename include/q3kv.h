@@ -617,6 +617,8 @@ Q3KV_API int q3kv_t5k_evict(void* stream, const q3kv_cache_desc* desc, void* d_p
  *   were all accepted, the same argmax with p in place of r;
  *   U(row, x) as in q3kv_accept_sample (equal keys: the lowest index).
  * Same arguments, outputs and errors as q3kv_accept_sample, plus:
+ *   temperature   log2(e) / temperature must be finite in float32 (4.3e-39 is, 4.2e-39
+ *                 is not: Q3KV_ERR_INVALID_ARG), and temperature below 3e38
  *   draft_probs   device [num_rows, vocab] of draft_dtype (f32 or bf16), the same row
  *                 indexing as logits (a slot's last row is unused); values >= 0, taken
  *                 as they are (not renormalised)

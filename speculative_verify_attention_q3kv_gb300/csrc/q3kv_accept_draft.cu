@@ -28,6 +28,7 @@
 // the ones that count); a tested probability has log2(e) / tau split in two floats,
 // so it is within a few float32 roundings of its definition.
 #include <cuda_bf16.h>
+#include <float.h>
 #include <math_constants.h>
 
 #include <algorithm>
@@ -57,6 +58,7 @@ struct DraftArgs {
     int32_t max_n_q;
     const int32_t* ctx_len;
     float c_hi, c_lo;            // log2(e) / tau
+    float d_min;                 // d c_hi = -160, below every exponent that counts; -inf where no float32 d is so low
     const float* uniforms;
     uint64_t seed;
     int32_t* n_accepted;
@@ -75,10 +77,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// e^((l - m) / tau); l <= m, m finite (l = -inf gives 0)
+// e^((l - m) / tau); l <= m, m finite (l = -inf gives 0).  Below d_min the result is 0 whatever the
+// exponent's second part: a finite mask at a low temperature overflows that too, to either sign.
 __device__ __forceinline__ float weight(const DraftArgs& a, float l, float m) {
     const float d = l - m;
-    return exp2_approx(d == -CUDART_INF_F ? d : fmaf(d, a.c_hi, d * a.c_lo));
+    return exp2_approx(d > a.d_min ? fmaf(d, a.c_hi, d * a.c_lo) : -CUDART_INF_F);
 }
 
 // the same for a term of the sum, with log2(e) / tau in one float: 2^-25 of an exponent that
@@ -295,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 2) residual_kernel(const DraftArgs a
                 float most = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float d = fmaxf(p[i] - v.x, -1e30f);               // of -inf and NaN: probability 0
+                    // NaN and -inf: probability 0, or NaN (where d_min is -inf), which no key is made of
+                    const float d = fmaxf(p[i] - v.x, a.d_min);
                     p[i] = exp2_approx(fmaf(d, a.c_hi, d * a.c_lo)) * inv;
                     if (bonus) {
                         r[i] = p[i];
@@ -426,6 +430,9 @@ int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, int32_t v
     if (draft_dtype != Q3KV_F32 && draft_dtype != Q3KV_BF16) return Q3KV_ERR_INVALID_ARG;
     if (max_n_q < 0) return Q3KV_ERR_INVALID_ARG;
     if (!(temperature > 0.0f) || !(temperature < 3.0e38f)) return Q3KV_ERR_INVALID_ARG;
+    const double c = 1.4426950408889634074 / (double)temperature;
+    if (c > (double)FLT_MAX) return Q3KV_ERR_INVALID_ARG;
+    const float c_hi = (float)c;
     // accept_prob is written while other CTAs still read the uniforms
     if (d_accept_prob && num_rows > 0 && d_accept_prob < d_uniforms + num_rows && d_uniforms < d_accept_prob + num_rows)
         return Q3KV_ERR_INVALID_ARG;
@@ -455,9 +462,9 @@ int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, int32_t v
     a.num_rows = num_rows;
     a.max_n_q = max_n_q;
     a.ctx_len = d_ctx_len;
-    const double c = 1.4426950408889634074 / (double)temperature;
-    a.c_hi = (float)c;
-    a.c_lo = (float)(c - (double)a.c_hi);
+    a.c_hi = c_hi;
+    a.c_lo = (float)(c - (double)c_hi);
+    a.d_min = 160.0 / c > (double)FLT_MAX ? -CUDART_INF_F : (float)(-160.0 / c);
     a.uniforms = d_uniforms;
     a.seed = seed;
     a.n_accepted = d_n_accepted;

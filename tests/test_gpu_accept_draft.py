@@ -238,3 +238,27 @@ def test_no_rows_and_no_slots():
     e = i32([])
     api.accept_draft(lg, lg, e, e, i32([]), 4, e, 1.0, z, 1, e, e, e, None)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("mask", ["-inf", "lowest"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tau", [1e-7, 3e-8, 1e-10, 1e-17, 1e-20, 1e-30, 1e-38, 1e28, 1e30, 1e37])
+def test_masked_logits_at_extreme_temperatures(tau, dtype, mask):
+    """Masks of -inf and of the type's lowest value, over whole chunks of a row, from a one-hot target to a flat one.
+
+    The bounds of this file hold at any temperature: an entry whose exponent counts lies close enough to the
+    maximum for an exact difference, or the temperature divides the difference's rounding too.
+    """
+    widths, vocab = [4, 3, 1], 5003
+    logits, draft, tokens, offs, uni = _inputs(widths, vocab, dtype, torch.float32, 23)
+    value = -float("inf") if mask == "-inf" else torch.finfo(dtype).min
+    logits[:, :2000] = value
+    logits[:, 2000::3] = value
+    tokens[1] = 17                                   # a masked draft
+    tokens[2] = int(logits[1].argmax())              # the one that a cold target takes
+    st = i32([0])
+    got = _run(logits, draft, tokens, offs, widths, uni, tau, 31, status=st)
+    _, clear = _compare(got, logits, draft, tokens, offs, widths, uni, tau, 31)
+    assert clear.any() and int(st.item()) == 0
+    if mask == "-inf":
+        assert np.all(got[1] >= 2000) and np.all((got[1] - 2000) % 3 != 0)      # a masked token never follows

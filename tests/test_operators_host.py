@@ -323,3 +323,14 @@ def test_accept_draft_and_lse_binding_rules(fake):
     for bad in (torch.zeros((4, 16)), torch.zeros((5, 8)), torch.zeros((5, 16), dtype=torch.float64), None):
         with pytest.raises((TypeError, ValueError)):
             call(bad)
+
+
+def test_accept_draft_refuses_temperatures_without_a_float32_inverse(lib):
+    def call(tau):                                   # no slots: nothing is launched where there is a device
+        a = 1 << 20
+        return lib.q3kv_accept_draft(None, a, 0, 100, a, 0, a, a, a, 0, 8, 3, a, tau, a, 7, a, a, a, None, a, 1 << 30, None)
+
+    for tau in (1e-45, 1e-40, 4.2e-39):              # log2(e) / tau is above the largest float32, 3.4028e38
+        assert call(tau) == INVALID
+    for tau in (4.3e-39, 1.2e-38, 1e-30, 2.9e38):
+        assert call(tau) != INVALID
