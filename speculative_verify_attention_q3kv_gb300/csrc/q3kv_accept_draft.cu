@@ -29,6 +29,7 @@
 // so it is within a few float32 roundings of its definition.
 #include <cuda_bf16.h>
 #include <float.h>
+#include <math.h>
 #include <math_constants.h>
 
 #include <algorithm>
@@ -464,7 +465,7 @@ int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, int32_t v
     a.ctx_len = d_ctx_len;
     a.c_hi = c_hi;
     a.c_lo = (float)(c - (double)c_hi);
-    a.d_min = 160.0 / c > (double)FLT_MAX ? -CUDART_INF_F : (float)(-160.0 / c);
+    a.d_min = 160.0 / c > (double)FLT_MAX ? -INFINITY : (float)(-160.0 / c);
     a.uniforms = d_uniforms;
     a.seed = seed;
     a.n_accepted = d_n_accepted;
