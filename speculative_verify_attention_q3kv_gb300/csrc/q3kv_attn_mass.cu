@@ -8,7 +8,8 @@
 // position do not depend on how the work is cut.
 //
 // Precision.  A weight has the absolute error of its score as a relative one, so the
-// scores are float32-exact: queries as fp16 hi + lo pairs (22 bits), keys exact.
+// scores are as good as float32's: queries as fp16 hi + lo pairs after a power of two for the (slot, kv
+// head) pair (22 bits of every value, or 2^-27 of the pair's largest: see load_queries), keys exact.
 // The 3-bit codec's value (c - 3.5) s needs 14 bits; instead of splitting it too,
 // the tensor cores contract the codes, c - 3.5 exact in fp16, and each 32-dim
 // block's sum goes to its own accumulator, which the epilogue multiplies by the
@@ -128,6 +129,7 @@ constexpr uint32_t kTmemCols = 512;
 
 constexpr int kMaxStages = 5;
 constexpr int kAhead = 2;                   // tiles whose old masses are loaded ahead
+constexpr uint32_t kQueryLimit = 0x6D800000u;   // 2^92: the rotation and the products with the scales stay in float32
 
 // An epilogue group that skips tiles, and an issuer that is up to a tile ahead,
 // must not mistake an older phase for the one they wait for (only its parity is
@@ -165,6 +167,9 @@ struct __align__(16) MassSmem {
     uint8_t q[kMaxChunks][2][kChunkRows / 8 * kSbo];   // [chunk][hi | lo], B operand
     uint8_t rec[Mf<FMT>::kStages][kTileP * Mf<FMT>::kStride];   // staged records
     float nlse[kMaxRows];                             // -lse in log2 units; -inf leaves a row out
+    uint32_t q_most[kWarpD];                          // largest |q| of a warp's rows, as float bits (query_scale)
+    float unscale;                                    // 2^-e of the queries' 2^e
+    int2 q_flags[2];                                  // [segment % 2] a value is too large for the usual scale; one is large enough
     Bars bar;
     uint32_t tmem_base;
     int abort;
@@ -191,6 +196,8 @@ __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
 __device__ __forceinline__ void unpack2(unsigned long long v, float& lo, float& hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((127 + e) << 23); }
 // two float32 fused multiply-adds in one instruction
 __device__ __forceinline__ unsigned long long fma2(unsigned long long x, unsigned long long y, unsigned long long z) {
     unsigned long long r;
@@ -396,12 +403,20 @@ __device__ __forceinline__ void rotate_four_rows(float (&y)[32]) {
     }
 }
 
-// Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e), split
+// Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e) and 2^e, split
 // into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  The E warps take four rows
 // each, the next ones' loads in flight, while the D warps convert the first records.  (A row per
 // warp and step took 40 shuffles a row, 8,000 cycles for 64 rows.)
+//
+// The power of two 2^e: hi + lo hold 22 bits of a value, but lo no finer than 2^-25.  The usual e = 8 serves a
+// pair whose largest scaled value lies in [4, 2^15): rotated queries (with the rotation's 1/16) of 0.17 to
+// 1,419 at most, for which 2^-25 is 2^-27 of the largest or less.  For others the E warps prepare the pair
+// again with an e of its own (query_scale), 1 us of a call with one token and 4 with 8.  The epilogue takes 2^e out again with the position's
+// scales; a power per row would cost it a multiply-add per row and position, and to look at all
+// rows before the first split took 0.9 us of every call.
+constexpr int kUsualExp = 8;
 template <typename TIn, int FMT>
-__device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm) {
+__device__ __forceinline__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, int exp2q, bool again, int2& flags) {
     constexpr int kVecs = 2 * (int)sizeof(TIn);              // 16-byte loads of a lane's 32 dims
     constexpr int kPer = 32 / kVecs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -415,7 +430,7 @@ __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>&
     };
     uint4 next[kVecs];
     load(next, 4 * warp + (lane >> 3));
-    if ((int)threadIdx.x < rows) {
+    if ((int)threadIdx.x < rows && !again) {
         const int r = threadIdx.x;
         float v = -CUDART_INF_F;
         if (r < R) {
@@ -426,6 +441,8 @@ __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>&
         sm.nlse[r] = v;
     }
     __syncwarp();
+    const float scale = (Mf<FMT>::kRot ? 1.4426950408889634f / 256.0f : 1.4426950408889634f / 16.0f) * two_to(exp2q);
+    __half2 most = __half2half2(__ushort_as_half((unsigned short)0));
 #pragma unroll 1
     for (int r0 = 4 * warp; r0 < rows; r0 += 4 * kWarpD) {
         const int r = r0 + (lane >> 3), chunk = r0 / kChunkRows, rr = r % kChunkRows;
@@ -435,15 +452,15 @@ __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>&
         load(next, r + 4 * kWarpD);
         if (r0 % kChunkRows >= mma_rows(s, chunk)) continue;
         if (Mf<FMT>::kRot) rotate_four_rows(y);
-        constexpr float kScale = Mf<FMT>::kRot ? 1.4426950408889634f / 256.0f : 1.4426950408889634f / 16.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint32_t hw[4], lw[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x0 = y[8 * c + 2 * i] * kScale, x1 = y[8 * c + 2 * i + 1] * kScale;
+                const float x0 = y[8 * c + 2 * i] * scale, x1 = y[8 * c + 2 * i + 1] * scale;
                 const __half2 h2 = __floats2half2_rn(x0, x1);
                 const float2 hf = __half22float2(h2);
+                most = __hmax2_nan(most, __habs2(h2));
                 hw[i] = as_u32(h2);
                 lw[i] = as_u32(__floats2half2_rn(x0 - hf.x, x1 - hf.y));
             }
@@ -453,7 +470,47 @@ __device__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>&
             *reinterpret_cast<uint4*>(&sm.q[chunk][1][off]) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
     }
+    const uint32_t m = as_u32(most), top = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
+    if (top >= 0x7800u && !again) flags.x = 1;               // 2^15, and whatever is not finite
+    if (top >= 0x4400u && !again) flags.y = 1;               // 4
     fence_proxy_async();
+}
+
+// Largest magnitude of 16 bytes, as float bits.
+__device__ __forceinline__ uint32_t largest(const uint4& u, const __nv_bfloat16*) {
+    const uint32_t lo = max(max(u.x << 16 & 0x7FFFFFFFu, u.y << 16 & 0x7FFFFFFFu), max(u.z << 16 & 0x7FFFFFFFu, u.w << 16 & 0x7FFFFFFFu));
+    return max(lo, max(max(u.x & 0x7FFF0000u, u.y & 0x7FFF0000u), max(u.z & 0x7FFF0000u, u.w & 0x7FFF0000u)));
+}
+__device__ __forceinline__ uint32_t largest(const uint4& u, const float*) {
+    return max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu));
+}
+
+// The e with which the pair's rotated and scaled queries stay below 2^15, from its largest |q|: the rotation
+// makes a value at most 256 times larger, and leaves the row's largest no smaller.  The E warps,
+// a row per warp and step; rows with values from 2^92 on (infinities and NaN among them) do not count.
+template <typename TIn, int FMT>
+__device__ __forceinline__ int query_scale(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm) {
+    constexpr int kVecs = (int)sizeof(TIn) / 2;              // 16-byte loads of a lane's part of a row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t Hq = a.num_kv_heads * kGroup;
+    uint32_t most = 0u;
+#pragma unroll 1
+    for (int r = warp; r < kGroup * s.T; r += kWarpD) {
+        const int64_t row = ((int64_t)s.q_row + r / kGroup) * Hq + s.g * kGroup + r % kGroup;
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const TIn*>(a.q) + row * kHeadDim) + lane;
+        uint32_t m = 0u;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) m = max(m, largest(p[32 * v], static_cast<const TIn*>(nullptr)));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (m < kQueryLimit) most = max(most, m);
+    }
+    if (lane == 0) sm.q_most[warp] = most;
+    named_sync(2, 32 * kWarpD);
+#pragma unroll
+    for (int w = 0; w < kWarpD; ++w) most = max(most, sm.q_most[w]);
+    if (most == 0u) return kUsualExp;
+    const float bound = __uint_as_float(most) * (Mf<FMT>::kRot ? 1.4426950408889634f : 1.4426950408889634f / 16.0f);
+    return min(100, 14 - ((int)(__float_as_uint(bound) >> 23) - 127));    // the block scales times 2^-100 are normal
 }
 
 __device__ __forceinline__ int32_t page_of(const MassArgs& a, const Segment& s, int pos0) {
@@ -642,6 +699,9 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
             if (lane == 0) mbar_arrive(&bar.r_free[rc % ST]);
         }
         unsigned long long sum0 = 0ull, sum1 = 0ull;         // pairs of zeros
+        // 2^-e, read for every tile and through a warp's maximum, after which the compiler knows that it is uniform: held
+        // in a register of the thread it made the 64-row form spill (8 tokens 110 us, so 100)
+        const float unscale = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(sm.unscale)));
 #pragma unroll 1
         for (int j = 0; j < s.chunks; ++j) {
             const int ph = s.phases + i * s.chunks + j;
@@ -674,7 +734,7 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
                     if (lane == 0) mbar_arrive(&bar.acc_free[c % kFreeBars]);
 #pragma unroll
                     for (int gi = 0; gi < G; ++gi) {
-                        const float scale = part_scale<FMT>(sc, part, gi);
+                        const float scale = part_scale<FMT>(sc, part, gi) * unscale;
                         const unsigned long long s2 = pack2(scale, scale);
 #pragma unroll
                         for (int k = 0; k < LD / 2; ++k) acc[k] = fma2(pack2(x[gi][2 * k], x[gi][2 * k + 1]), s2, acc[k]);
@@ -683,7 +743,7 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
                     // a group in one round trip (655,360 positions x 6 tokens: 92 us, in the form for 64 rows 105)
 #pragma unroll
                     for (int gi = 0; gi < G; ++gi) {
-                        const float scale = part_scale<FMT>(sc, part, gi);
+                        const float scale = part_scale<FMT>(sc, part, gi) * unscale;
                         float x[32], z[16];
                         tmem_ld32(col + COLS * gi, x);
                         tmem_ld16(col + COLS * gi + 32, z);
@@ -704,7 +764,7 @@ __device__ __forceinline__ bool epilogue(const MassArgs& a, const Segment& s, Ma
                 } else {
 #pragma unroll
                     for (int gi = 0; gi < G; ++gi) {
-                        const float scale = part_scale<FMT>(sc, part, gi);
+                        const float scale = part_scale<FMT>(sc, part, gi) * unscale;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             if (h < halves) {
@@ -788,12 +848,25 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
 #pragma unroll 1
         for (int k = -1; k < 0 || sm.seg[k & 1].n > 0; ++k) {
             const Segment s = k < 0 ? Segment{0, 0, 0, 0, 0, 0, 1, 0, 1, 0, 0, 0, 0} : sm.seg[k & 1];
-            load_queries<TIn, FMT>(a, s, sm);
+            int exp2q = kUsualExp;
+            int2& flags = sm.q_flags[k & 1];
+            bool again = false;
+#pragma unroll 1
+            do {
+                if (again) exp2q = query_scale<TIn, FMT>(a, s, sm);
+                load_queries<TIn, FMT>(a, s, sm, exp2q, again, flags);
+                if (k < 0) break;
+                if (tid == 0) {
+                    sm.unscale = two_to(-exp2q);
+                    sm.q_flags[(k + 1) & 1] = make_int2(0, 0);
+                }
+                named_sync(1, kQueryThreads);
+                again = !again && (flags.x != 0 || flags.y == 0);        // M decides the same
+            } while (again);
             if (k < 0) {
                 tmem = prepared();
                 continue;
             }
-            named_sync(1, kQueryThreads);
             const EpiState e{tmem + ((uint32_t)(32 * (warp & 3)) << 16) + acc_col<FMT>(s.buffers), abort};
             constexpr int B = double_buffered<FMT>(1) ? 2 : 1;
             const int rows = kGroup * s.T;
@@ -888,6 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         for (int k = 0; sm.seg[k & 1].n > 0; ++k) {
             const Segment s = sm.seg[k & 1];
             named_sync(1, kQueryThreads);
+            const int2 flags = sm.q_flags[k & 1];
+            if (flags.x != 0 || flags.y == 0) named_sync(1, kQueryThreads);      // E prepares them again
             const int n = s.n;
             const int cols = acc_cols(s);
             const int slots = acc_slots<FMT>(s.buffers, cols);
@@ -958,6 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 mbar_init(&bar.r_free[lane], Mf<FMT>::kScales ? 12 : 8);
             }
             if (lane == 0) sm.abort = 0;
+            if (lane < 2) sm.q_flags[lane] = make_int2(0, 0);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         if (warp == kWarpP) share_of<FMT>(a, sm);

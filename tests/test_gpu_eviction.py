@@ -635,3 +635,37 @@ def _check_mass_slot(c, got, lengths, widths, q, lse, b):
         rel = np.where(seen, bound + 2.0 ** -22 * (1 + np.abs(np.where(seen, s, 0)) + np.abs(l[:, None])), 0)
         tol = (w * rel).sum(axis=0) + 130 * 2.0 ** -23 * np.abs(want) + 1e-37
         assert np.all(np.abs(got[b, g].double().cpu().numpy()[:n] - want) <= tol)
+
+
+# Queries of one (slot, kv head) pair share a power of two before they are split into fp16 halves, with which
+# a half's finest step is at most 2^-27 of the pair's largest (rotated) value y: beside the bounds above, every
+# score may be off by 2^-27 y sum|k_hat| / 16.
+@pytest.mark.parametrize("fmt,qscale,kscale", [("q3", 1e-4, 2.8e4), ("q3", 1e-3, 1e3), ("q3", 2e6, 1e-6), ("q3", 1e-20, 1.0), ("t5k", 1e-4, 1e4),
+                                               ("t5k", 2e6, 1e-6), ("fp8", 1e-3, 100.0), ("fp8", 2e6, 0.02), ("q3", 1e12, 1e-6),
+                                               ("q3", 0.04, 30.0), ("fp8", 0.05, 10.0), ("q3", 400.0, 0.01), ("fp8", 2000.0, 0.02)])
+@pytest.mark.parametrize("widths", [[2, 1], [6, 9]])
+def test_mass_of_small_and_large_queries(fmt, qscale, kscale, widths):
+    lengths = [600, 300]
+    c = Cache(fmt, lengths, 2, seed=41, scale=kscale)
+    q = queries(sum(widths), 16, 43, scale=qscale)
+    q[0, 3] *= 3000.0                                # one row far above the others of its pair
+    lse = _lse_of(c, lengths, widths, q, 0)
+    mass = torch.rand((2, 2, 600), device="cuda")
+    old, st = mass.clone(), i32([0])
+    _mass_call(c, lengths, widths, q, lse, 1.0, mass, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and bool(torch.isfinite(mass).all())
+    for b, (n, t) in enumerate(zip(lengths, widths)):
+        r0 = sum(widths[:b])
+        for g in range(2):
+            s, bound = _reference(c, lengths, widths, q, 0, b, g)
+            most = np.abs(c.q_basis(q[r0:r0 + t, 8 * g:8 * g + 8].double().cpu().numpy())).max()
+            bound = bound + 2.0 ** -27 * most * np.abs(c.k_hat(b, 0, g, n)).sum(axis=1)[None, :] / 16.0
+            l = lse[r0:r0 + t, 8 * g:8 * g + 8].double().cpu().numpy().reshape(-1)
+            want = ev.mass(old[b, g].double().cpu().numpy()[:n], s, l, 1.0, n - t)
+            w, seen = np.exp(s - l[:, None]), np.isfinite(s)
+            rel = np.where(seen, bound + 2.0 ** -22 * (1 + np.abs(np.where(seen, s, 0)) + np.abs(l[:, None])), 0)
+            # e^x of an error x that is not small: the factor is e^x - 1
+            tol = (w * np.expm1(np.minimum(rel, 50.0))).sum(axis=0) + 130 * 2.0 ** -23 * np.abs(want) + 1e-37
+            err = np.abs(mass[b, g].double().cpu().numpy()[:n] - want)
+            assert np.all(err <= tol), (b, g, float((err / np.maximum(tol, 1e-300)).max()))
