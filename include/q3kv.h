@@ -521,8 +521,9 @@ Q3KV_API int q3kv_t5k_verify_attn_lse(void* stream, const q3kv_cache_desc* desc,
  * lse and the query rows of the kept tokens are unchanged by the rollback.
  *   q, dtype, d_q_offsets   as in q3kv_verify_attn (the same unrotated queries)
  *   lse      float32 [rows, num_q_heads], as q3kv_verify_attn_lse stores it; a
- *            row whose lse is not finite contributes nothing and sets
- *            Q3KV_STATUS_NONFINITE_INPUT
+ *            row whose lse or whose queries are not finite (a query of 2^92 or
+ *            more counts as that) contributes nothing and sets
+ *            Q3KV_STATUS_NONFINITE_INPUT; the other rows' weights do not change
  *   decay    in [0, 1]; with 0 the old values are not read (they may be anything)
  *   d_mass   float32 [num_slots, num_kv_heads, mass_stride], updated in place;
  *            entries at or past L and slots with T == 0 are left as they were;

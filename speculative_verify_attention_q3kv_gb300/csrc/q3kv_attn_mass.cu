@@ -403,6 +403,14 @@ __device__ __forceinline__ void rotate_four_rows(float (&y)[32]) {
     }
 }
 
+// Where a lane's dims 8 c .. 8 c + 7 (as rotate_four_rows leaves them) of row rr of a pass lie in the operand.
+template <int FMT>
+__device__ __forceinline__ uint32_t query_offset(int rr, int c) {
+    const int l = threadIdx.x & 7;
+    const uint32_t core = Mf<FMT>::kRot ? l + 8 * (c >> 1) + 16 * (c & 1) : 4 * l + c;
+    return (uint32_t)(rr >> 3) * kSbo + core * kLbo + (uint32_t)(rr & 7) * 16u;
+}
+
 // Queries of the segment's pair: H, then 1/16 (H) 1/16 (softmax) log2(e) and 2^e, split
 // into fp16 hi / lo, and -lse in log2 units; padding rows are zeros.  The E warps take four rows
 // each, the next ones' loads in flight, while the D warps convert the first records.  (A row per
@@ -430,15 +438,13 @@ __device__ __forceinline__ void load_queries(const MassArgs& a, const Segment& s
     };
     uint4 next[kVecs];
     load(next, 4 * warp + (lane >> 3));
+    bool out = false;                                        // a statistic that is not finite
     if ((int)threadIdx.x < rows && !again) {
         const int r = threadIdx.x;
-        float v = -CUDART_INF_F;
-        if (r < R) {
-            const float l = a.lse[row_of(r)];
-            if (l > -CUDART_INF_F && l < CUDART_INF_F) v = -1.4426950408889634f * l;
-            else if (a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
-        }
-        sm.nlse[r] = v;
+        const float l = r < R ? a.lse[row_of(r)] : CUDART_INF_F;
+        const bool finite = fabsf(l) < CUDART_INF_F;
+        out = r < R && !finite;
+        sm.nlse[r] = finite ? -1.4426950408889634f * l : -CUDART_INF_F;
     }
     __syncwarp();
     const float scale = (Mf<FMT>::kRot ? 1.4426950408889634f / 256.0f : 1.4426950408889634f / 16.0f) * two_to(exp2q);
@@ -464,14 +470,13 @@ __device__ __forceinline__ void load_queries(const MassArgs& a, const Segment& s
                 hw[i] = as_u32(h2);
                 lw[i] = as_u32(__floats2half2_rn(x0 - hf.x, x1 - hf.y));
             }
-            const uint32_t core = Mf<FMT>::kRot ? (lane & 7) + 8 * (c >> 1) + 16 * (c & 1) : 4 * (lane & 7) + c;
-            const uint32_t off = (uint32_t)(rr >> 3) * kSbo + core * kLbo + (uint32_t)(rr & 7) * 16u;
+            const uint32_t off = query_offset<FMT>(rr, c);
             *reinterpret_cast<uint4*>(&sm.q[chunk][0][off]) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
             *reinterpret_cast<uint4*>(&sm.q[chunk][1][off]) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
     }
     const uint32_t m = as_u32(most), top = max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
-    if (top >= 0x7800u && !again) flags.x = 1;               // 2^15, and whatever is not finite
+    if ((top >= 0x7800u || out) && !again) flags.x = 1;      // 2^15, and whatever is not finite
     if (top >= 0x4400u && !again) flags.y = 1;               // 4
     fence_proxy_async();
 }
@@ -485,9 +490,13 @@ __device__ __forceinline__ uint32_t largest(const uint4& u, const float*) {
     return max(max(u.x & 0x7FFFFFFFu, u.y & 0x7FFFFFFFu), max(u.z & 0x7FFFFFFFu, u.w & 0x7FFFFFFFu));
 }
 
-// The e with which the pair's rotated and scaled queries stay below 2^15, from its largest |q|: the rotation
-// makes a value at most 256 times larger, and leaves the row's largest no smaller.  The E warps,
-// a row per warp and step; rows with values from 2^92 on (infinities and NaN among them) do not count.
+// Which rows of the pair take part in its second preparation, and the e with which their rotated and scaled
+// queries stay below 2^15.  A row whose statistic is not finite, or with a query from 2^92 on (an infinity or
+// a NaN among them), is left out: its start becomes -inf, and clear_rows makes its operand zeros, as a NaN
+// there would reach the sum of every position.  The e comes from the largest |q|, of rows without a
+// finite statistic too: the rotation makes a value at most 256 times larger, and leaves the row's largest no
+// smaller.  Where the usual e is known to serve by that, it is taken: the other rows' bits are those of a call
+// without the ones left out.  The E warps, a row per warp and step.
 template <typename TIn, int FMT>
 __device__ __forceinline__ int query_scale(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm) {
     constexpr int kVecs = (int)sizeof(TIn) / 2;              // 16-byte loads of a lane's part of a row
@@ -503,14 +512,34 @@ __device__ __forceinline__ int query_scale(const MassArgs& a, const Segment& s, 
         for (int v = 0; v < kVecs; ++v) m = max(m, largest(p[32 * v], static_cast<const TIn*>(nullptr)));
         m = __reduce_max_sync(0xffffffffu, m);
         if (m < kQueryLimit) most = max(most, m);
+        if ((m >= kQueryLimit || !(fabsf(a.lse[row]) < CUDART_INF_F)) && lane == 0) {
+            sm.nlse[r] = -CUDART_INF_F;
+            if (a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
+        }
     }
     if (lane == 0) sm.q_most[warp] = most;
     named_sync(2, 32 * kWarpD);
 #pragma unroll
     for (int w = 0; w < kWarpD; ++w) most = max(most, sm.q_most[w]);
-    if (most == 0u) return kUsualExp;
     const float bound = __uint_as_float(most) * (Mf<FMT>::kRot ? 1.4426950408889634f : 1.4426950408889634f / 16.0f);
+    const float least = Mf<FMT>::kRot ? bound / 256.0f : bound;
+    if (most == 0u || (bound * two_to(kUsualExp) < 32768.0f && least * two_to(kUsualExp) >= 4.0f)) return kUsualExp;
     return min(100, 14 - ((int)(__float_as_uint(bound) >> 23) - 127));    // the block scales times 2^-100 are normal
+}
+
+// Zeros in the operand for the rows that query_scale left out, by the lanes that wrote them in load_queries.
+template <int FMT>
+__device__ __forceinline__ void clear_rows(const Segment& s, MassSmem<FMT>& sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+    for (int r = 4 * warp + (lane >> 3); r < kGroup * s.T; r += 4 * kWarpD) {
+        if (sm.nlse[r] > -CUDART_INF_F) continue;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(&sm.q[r / kChunkRows][c >> 2][query_offset<FMT>(r % kChunkRows, c & 3)]) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncwarp();
+    fence_proxy_async();
 }
 
 __device__ __forceinline__ int32_t page_of(const MassArgs& a, const Segment& s, int pos0) {
@@ -856,6 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 if (again) exp2q = query_scale<TIn, FMT>(a, s, sm);
                 load_queries<TIn, FMT>(a, s, sm, exp2q, again, flags);
                 if (k < 0) break;
+                if (again) clear_rows<FMT>(s, sm);
                 if (tid == 0) {
                     sm.unscale = two_to(-exp2q);
                     sm.q_flags[(k + 1) & 1] = make_int2(0, 0);

@@ -669,3 +669,34 @@ def test_mass_of_small_and_large_queries(fmt, qscale, kscale, widths):
             tol = (w * np.expm1(np.minimum(rel, 50.0))).sum(axis=0) + 130 * 2.0 ** -23 * np.abs(want) + 1e-37
             err = np.abs(mass[b, g].double().cpu().numpy()[:n] - want)
             assert np.all(err <= tol), (b, g, float((err / np.maximum(tol, 1e-300)).max()))
+
+
+@pytest.mark.parametrize("fmt", ["q3", "fp8", "t5k"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("width", [1, 3, 7, 16])
+def test_mass_leaves_rows_out_that_are_not_finite(fmt, dtype, width):
+    """A row with a NaN, an infinity or a value of 2^100 in its queries, with the statistic that comes of it or a finite
+    one: the bits of a call in which the row is zeros and weighs nothing."""
+    lengths, widths = [600, 300], [width, 2]
+    c = Cache(fmt, lengths, 2, seed=44)
+    q = queries(sum(widths), 16, 45, dtype)
+    lse = _lse_of(c, lengths, widths, q, 0)
+    start = torch.rand((2, 2, 600), device="cuda")
+    rows = [(0, 3), (width - 1, 8)]
+    q0, l0 = q.clone(), lse.clone()
+    for t, h in rows:
+        q0[t, h], l0[t, h] = 0.0, 3.0e38             # e^(0 - 3e38) = 0
+    want, st = start.clone(), i32([0])
+    _mass_call(c, lengths, widths, q0, l0, 1.0, want, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    nan, inf = float("nan"), float("inf")
+    for value, stat in ((nan, nan), (inf, inf), (-inf, nan), (nan, 1.5), (inf, 1.5), (2.0 ** 100, 1.5), (-2.0 ** 127, nan)):
+        q1, l1 = q.clone(), lse.clone()
+        for t, h in rows:
+            q1[t, h, 77], l1[t, h] = value, stat
+        got, st = start.clone(), i32([0])
+        _mass_call(c, lengths, widths, q1, l1, 1.0, got, status=st)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), (value, stat)
+        assert int(st.item()) == _lib.Q3KV_STATUS_NONFINITE_INPUT
