@@ -162,14 +162,21 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) select_kernel
     float* mass_out = a.mass_out ? a.mass_out + row * a.max_budget : nullptr;
     const int lo = s.sink, hi = s.L - s.recent;            // free positions [lo, hi)
     const int k = s.n - s.sink - s.recent;                 // of which k are kept
+    bool nan = false;                                      // anywhere in the row
     // protected positions keep their order at both ends
     for (int i = rank * kSelThreads + tid; i < s.sink + s.recent; i += C * kSelThreads) {
         const int pos = i < s.sink ? i : s.L - s.recent + (i - s.sink);
         const int dst = i < s.sink ? i : s.n - s.recent + (i - s.sink);
+        const float v = m[pos];
+        nan |= v != v;
         kept[dst] = pos;
-        if (mass_out) mass_out[dst] = m[pos];
+        if (mass_out) mass_out[dst] = v;
     }
-    if (k == 0) return;
+    if (k == 0) {                                          // nothing to choose
+        for (int i = lo + rank * kSelThreads + tid; i < hi; i += C * kSelThreads) nan |= m[i] != m[i];
+        if (__any_sync(0xffffffffu, nan) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
+        return;
+    }
     if (C > 1) cluster.barrier_arrive();                   // waited for before the first access to another CTA
     // a warp's share of the free positions, consecutive in the order (CTA, warp)
     const int count = hi - lo;
@@ -257,7 +264,6 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) select_kernel
         return (uint32_t)sm.found_bin;
     };
 
-    bool nan = false;
     const bool all = k == count;                           // everything between the protected ends
     bool nan_thr = false;                                  // the k-th is a NaN
     float thr = 0.0f;

@@ -700,3 +700,20 @@ def test_mass_leaves_rows_out_that_are_not_finite(fmt, dtype, width):
         torch.cuda.synchronize()
         assert torch.equal(got, want), (value, stat)
         assert int(st.item()) == _lib.Q3KV_STATUS_NONFINITE_INPUT
+
+
+@pytest.mark.parametrize("n", [600, 20000])
+@pytest.mark.parametrize("where", ["sink", "recent", "between, none of them kept", "between, all of them kept"])
+@pytest.mark.parametrize("with_mass", [True, False])
+def test_evict_status_of_a_nan_anywhere(n, where, with_mass):
+    """A NaN sets the status wherever it lies in the row, also where the selection has nothing to choose."""
+    sink, recent, budget, at = {"sink": (5, 20, 100, 3), "recent": (5, 20, 100, n - 1), "between, none of them kept": (30, 20, 50, n // 2),
+                                "between, all of them kept": (5, 20, n, n // 2)}[where]
+    c = Cache("q3", [n], 1, seed=48, extra_pages=(budget + 255) // 256)
+    mass = torch.rand((1, 1, 1, n), device="cuda")
+    for value, status in ((0.5, 0), (float("nan"), _lib.Q3KV_STATUS_NONFINITE_INPUT)):
+        mass[..., at] = value
+        before, st = c.pool.clone(), i32([0])
+        got = _evict_call(c, [n], [budget], sink, recent, mass, 0, st, with_mass=with_mass)
+        assert int(st.item()) == status
+        _check_evict(c, before, [n], [budget], sink, recent, mass, 0, got)
