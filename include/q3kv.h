@@ -575,9 +575,10 @@ Q3KV_API int q3kv_t5k_attn_mass(void* stream, const q3kv_cache_desc* desc, const
  *             source pages
  *   d_kept    int32 [num_call_layers, num_slots, num_kv_heads, max_budget]: the kept
  *             positions, ascending (entries past n are left as they were)
- *   d_mass_out  float32, same layout, the kept positions' masses; may be NULL; must
- *             not overlap d_mass
+ *   d_mass_out  float32, same layout, the kept positions' masses; may be NULL
  *   d_new_len int32 [num_slots]: n; may be the array d_ctx_len or d_budget
+ * d_kept, d_mass_out and d_mass must not overlap one another, nor d_new_len the
+ * lengths or budgets in any other way (Q3KV_ERR_INVALID_ARG).
  * d_budget[b] > max_budget, L < 0, L > max_ctx_len, L beyond the slot's page table
  * or n beyond its destination pages set Q3KV_STATUS_BAD_LENGTH and leave the slot
  * out.  A record whose source or destination page id is out of range is skipped

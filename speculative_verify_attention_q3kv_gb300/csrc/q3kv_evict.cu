@@ -581,6 +581,16 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
     const bool work = num_call_layers > 0 && max_budget > 0 && max_ctx_len > 0;
     if (work && (!d_pool || !d_page_table || !d_dst_page_table || !d_mass || !d_kept || !aligned16(d_pool)))
         return Q3KV_ERR_INVALID_ARG;
+    // a row's CTAs write kept and mass_out while others read its masses; the plans are read until the end
+    const int64_t pairs = (int64_t)num_slots * desc->num_kv_heads;
+    if (num_call_layers > 0 && pairs > INT32_MAX / kMaxCluster / num_call_layers) return Q3KV_ERR_UNSUPPORTED;
+    const int64_t rows = num_call_layers * pairs;
+    const int64_t read = rows * std::min<int64_t>(mass_stride, (int64_t)1 << 33) * 4, written = rows * max_budget * 4, lens = (int64_t)num_slots * 4;
+    if (work && (overlap(d_kept, written, d_mass, read) || overlap(d_mass_out, d_mass_out ? written : 0, d_mass, read) ||
+                 overlap(d_mass_out, d_mass_out ? written : 0, d_kept, written)))
+        return Q3KV_ERR_INVALID_ARG;
+    if ((d_new_len != d_ctx_len && overlap(d_new_len, lens, d_ctx_len, lens)) || (d_new_len != d_budget && overlap(d_new_len, lens, d_budget, lens)))
+        return Q3KV_ERR_INVALID_ARG;
     int sms = 0;
     e = device_sm_count(&sms);
     if (e != Q3KV_OK) return e;
@@ -610,8 +620,6 @@ int evict_impl(int fmt, void* stream, const q3kv_cache_desc* desc, void* d_pool,
     a.num_kv_heads = desc->num_kv_heads;
     a.num_pages = desc->num_pages;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t rows = (int64_t)num_call_layers * num_slots * desc->num_kv_heads;
-    if (rows * kMaxCluster > INT32_MAX) return Q3KV_ERR_UNSUPPORTED;
     if (work) {
         // cluster size: up to 16 CTAs a row while each has an SM of its own (2 rows of 655,360: 71 -> 50 us a call,
         // 8 rows 109 -> 94), else up to 8 of two per SM (16 rows: 165 us, with 16 CTAs 172); half while half keeps a

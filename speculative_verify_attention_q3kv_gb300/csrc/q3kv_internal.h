@@ -170,6 +170,11 @@ constexpr size_t kAcceptPartialBytes = 24;   // largest per-chunk record (sample
 int check_desc(const q3kv_cache_desc* d);
 int cuda_status(cudaError_t e);
 int device_sm_count(int* sms);
+// [a, a + an) and [b, b + bn) bytes share one
+inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);

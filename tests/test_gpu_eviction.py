@@ -717,3 +717,22 @@ def test_evict_status_of_a_nan_anywhere(n, where, with_mass):
         got = _evict_call(c, [n], [budget], sink, recent, mass, 0, st, with_mass=with_mass)
         assert int(st.item()) == status
         _check_evict(c, before, [n], [budget], sink, recent, mass, 0, got)
+
+
+def test_evict_into_buffers_that_touch():
+    """Masses, kept positions and kept masses end to end in one allocation: neighbours are no overlap."""
+    n, k = 900, 300
+    c = Cache("q3", [n], 1, seed=49, extra_pages=2)
+    buf = torch.zeros(n + 2 * k, device="cuda")
+    kept = buf[:k].view(torch.int32).view(1, 1, 1, k)
+    mass, out = buf[k:k + n].view(1, 1, 1, n), buf[k + n:].view(1, 1, 1, k)
+    mass.copy_(torch.rand_like(mass))
+    lens, was = i32([k, n, n]), mass.clone()          # budget, lengths and new lengths side by side
+    dst = torch.from_numpy(np.asarray(c.free[:2], np.int32).reshape(1, 2)).cuda()
+    api.evict(c.desc, c.pool, c.page_table, lens[1:2], n, lens[0:1], k, 3, 9, 0, mass, dst, kept, out, lens[2:3], c.status)
+    want = ev.keep(was[0, 0, 0].cpu().numpy(), k, 3, 9)
+    assert np.array_equal(kept[0, 0, 0].cpu().numpy(), want) and np.array_equal(out[0, 0, 0].cpu().numpy(), was[0, 0, 0].cpu().numpy()[want])
+    assert lens.tolist() == [k, n, k] and torch.equal(mass, was) and int(c.status.item()) == 0
+    for over in (mass[..., :k], mass[..., n - k:]):
+        with pytest.raises(api.Q3KVError):
+            api.evict(c.desc, c.pool, c.page_table, lens[1:2], n, lens[0:1], k, 3, 9, 0, mass, dst, kept, over, lens[2:3], c.status)

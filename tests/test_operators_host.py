@@ -334,3 +334,24 @@ def test_accept_draft_refuses_temperatures_without_a_float32_inverse(lib):
         assert call(tau) == INVALID
     for tau in (4.3e-39, 1.2e-38, 1e-30, 2.9e38):
         assert call(tau) != INVALID
+
+
+@pytest.mark.parametrize("name", ["q3kv_evict", "q3kv_fp8_evict", "q3kv_t5k_evict"])
+def test_evict_refuses_outputs_over_what_it_reads(lib, name):
+    # 3 layers x 2 slots x 2 kv heads: masses of 12 x 1,000 floats, kept positions and masses of 12 x 100
+    mass, kept, out, read, written = 1 << 24, 1 << 26, 1 << 28, 48000, 4800
+
+    def call(mass=mass, kept=kept, out=out, ctx=4096, budget=8192, new=12288):
+        return getattr(lib, name)(None, ctypes.byref(_desc()), 1 << 20, 4096, 4, ctx, 2, 1000, budget, 100, 1, 2, 0, 3, mass, 1000,
+                                  4096, 4, kept, out, new, None)
+
+    over = [dict(out=mass), dict(out=mass + read - 4), dict(out=mass - written + 4), dict(kept=mass), dict(kept=mass + read - 4),
+            dict(kept=mass - written + 4), dict(out=kept), dict(out=kept + written - 4), dict(new=4100), dict(new=4092), dict(new=8196),
+            dict(new=8188)]
+    for kw in over:
+        assert call(**kw) == INVALID, kw
+    if torch.cuda.is_available():
+        return                                       # these addresses go no further than a machine without a device
+    for kw in (dict(), dict(out=None), dict(out=mass + read), dict(kept=mass - written), dict(out=kept + written), dict(new=4096),
+               dict(new=8192), dict(new=4104), dict(new=4088)):
+        assert call(**kw) != INVALID, kw
