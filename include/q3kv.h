@@ -462,8 +462,9 @@ Q3KV_API int q3kv_rope_plan_init(const q3kv_rope_config* config, q3kv_rope_plan*
 /* q_in / q_out [num_rows, num_q_heads, 256] and k_in / k_out [num_rows,
  * num_kv_heads, 256], all of one dtype.  The heads of a row are contiguous; rows
  * lie *_stride elements apart (so q and k may be slices of one projection's
- * output).  An output may be its input (same pointer and stride); it may not
- * overlap an input in any other way.  num_q_heads or num_kv_heads may be 0 (its
+ * output).  An output may be its input (same pointer and stride); its rows may
+ * interleave with other operands' but not share a byte with them
+ * (Q3KV_ERR_INVALID_ARG).  num_q_heads or num_kv_heads may be 0 (its
  * pointers are then unused).  d_positions int32 [num_rows, num_axes], any values.
  * Q3KV_ERR_INVALID_ARG for pointers that are not 16-byte aligned or strides that
  * are below heads * 256 or not multiples of 16 bytes. */

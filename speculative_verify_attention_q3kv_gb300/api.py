@@ -656,6 +656,18 @@ def _strided_rows(name: str, t: torch.Tensor, rows: int, dev: int):
     return t.data_ptr(), row if rows > 1 else heads * HEAD_DIM, heads
 
 
+def _rows_meet(a: int, a_step: int, b: int, b_step: int, width: int, rows: int) -> bool:
+    """Whether rows [a + i a_step, + width) and [b + j b_step, + width) share a byte, i, j < rows, steps >= width if rows > 1."""
+    if a_step == b_step:
+        d = min((width - 1 + a - b) // b_step, rows - 1)     # the last j - i whose row of b begins before a's ends
+        return d > -rows and b - a + d * b_step > -width
+    for at in range(a, a + rows * a_step, a_step):
+        j = min((width - 1 + at - b) // b_step, rows - 1)
+        if j >= 0 and b + j * b_step + width > at:
+            return True
+    return False
+
+
 def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.Tensor, k: Optional[torch.Tensor] = None,
          k_out: Optional[torch.Tensor] = None, stream=None) -> None:
     """q3kv_rope: rotate q and k [rows, heads, 256] by positions int32 [rows, axes] into q_out and k_out.
@@ -683,9 +695,10 @@ def rope(plan: RopePlan, positions: torch.Tensor, q: torch.Tensor, q_out: torch.
         if heads != out_heads or x.dtype is not dtype or y.dtype is not dtype:
             raise ValueError(f"{name} and {name}_out must have the heads of one another and the dtype of q")
         if rows and heads and not (src == dst and src_stride == dst_stride):
-            # extents in bytes; an exact in-place call is fine, any other overlap is not
+            # an exact in-place call is fine, any other overlap is not (the library looks at the other operands)
             if (src < dst + ((rows - 1) * dst_stride + heads * HEAD_DIM) * size
-                    and dst < src + ((rows - 1) * src_stride + heads * HEAD_DIM) * size):
+                    and dst < src + ((rows - 1) * src_stride + heads * HEAD_DIM) * size
+                    and _rows_meet(src, src_stride * size, dst, dst_stride * size, heads * HEAD_DIM * size, rows)):
                 raise ValueError(f"{name}_out overlaps {name} without being the same rows")
         args += (src, src_stride, dst, dst_stride, heads)
     if k is None:

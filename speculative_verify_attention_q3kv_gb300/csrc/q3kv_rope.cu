@@ -19,6 +19,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "q3kv_internal.h"
 
 namespace q3kv {
@@ -214,6 +216,31 @@ bool rows_ok(const void* in, int64_t in_stride, const void* out, int64_t out_str
     return in_stride >= least && out_stride >= least && in_stride % step == 0 && out_stride % step == 0;
 }
 
+// Rows [p + i step, + width) in bytes, i < n; step >= width where n > 1.
+struct Rows {
+    const void* p;
+    int64_t step, width, n;
+};
+
+// Two sets of rows share a byte.  Rows may interleave (query and key rows of one projection): equal steps are
+// one division, others a division a row of a, taken only where the extents meet.
+bool rows_meet(const Rows& a, const Rows& b) {
+    if (!overlap(a.p, (a.n - 1) * a.step + a.width, b.p, (b.n - 1) * b.step + b.width)) return false;
+    const int64_t delta = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+    auto floor_div = [](int64_t x, int64_t y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
+    if (a.step == b.step) {
+        // row j of b against row i of a, d = j - i: the last one that begins before a's end
+        const int64_t d = std::min(floor_div(a.width - 1 - delta, b.step), b.n - 1);
+        return d >= 1 - a.n && delta + d * b.step > -b.width;
+    }
+    for (int64_t i = 0; i < a.n; ++i) {
+        const int64_t from = delta - i * a.step;             // b's first row from row i of a
+        const int64_t j = std::min(floor_div(a.width - 1 - from, b.step), b.n - 1);
+        if (j >= 0 && from + j * b.step > -b.width) return true;
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace q3kv
 
@@ -271,6 +298,16 @@ int q3kv_rope(void* stream, const q3kv_rope_plan* plan, const int32_t* d_positio
     const size_t esize = dtype == Q3KV_F32 ? 4 : 2;
     if (!d_positions || !rows_ok(q_in, q_in_stride, q_out, q_out_stride, num_q_heads, esize) ||
         !rows_ok(k_in, k_in_stride, k_out, k_out_stride, num_kv_heads, esize))
+        return Q3KV_ERR_INVALID_ARG;
+    // an output may lie on its own input's rows and on no other operand's
+    const int64_t es = (int64_t)esize, wq = num_q_heads * (int64_t)kHeadDim * es, wk = num_kv_heads * (int64_t)kHeadDim * es;
+    const Rows qi{q_in, q_in_stride * es, wq, num_rows}, qo{q_out, q_out_stride * es, wq, num_rows};
+    const Rows ki{k_in, k_in_stride * es, wk, num_rows}, ko{k_out, k_out_stride * es, wk, num_rows};
+    const Rows pos{d_positions, 4ll * plan->num_axes, 4ll * plan->num_axes, num_rows};
+    const bool q = num_q_heads > 0, k = num_kv_heads > 0;
+    auto same = [](const Rows& x, const Rows& y) { return x.p == y.p && (x.step == y.step || x.n == 1); };
+    if ((q && !same(qi, qo) && rows_meet(qi, qo)) || (k && !same(ki, ko) && rows_meet(ki, ko)) ||
+        (q && k && (rows_meet(qo, ki) || rows_meet(ko, qi) || rows_meet(qo, ko))) || (q && rows_meet(pos, qo)) || (k && rows_meet(pos, ko)))
         return Q3KV_ERR_INVALID_ARG;
     RopeArgs a{};
     a.plan = *plan;

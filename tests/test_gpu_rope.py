@@ -146,3 +146,24 @@ def test_captured_and_replayed():
     api.rope(plan, pos, q, want)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_rows_that_interleave_and_outputs_over_other_operands():
+    """Input and output rows side by side in one buffer; what would overwrite an operand is refused."""
+    rows = 33
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    buf = torch.randn((rows, (16 + 2 + 16 + 2) * 256), generator=gen, device="cuda")
+    at = lambda h, n: buf[:, h * 256:(h + n) * 256].unflatten(1, (n, 256))  # noqa: E731
+    q, k, qo, ko = at(0, 16), at(16, 2), at(18, 16), at(34, 2)
+    pos = torch.randint(0, 5000, (rows, 2), generator=gen, device="cuda").to(torch.int32)
+    plan = api.make_rope_plan(64, 1e4, (16, 16))
+    want_q, want_k, before = torch.empty_like(q.contiguous()), torch.empty_like(k.contiguous()), buf.clone()
+    api.rope(plan, pos, q.contiguous(), want_q, k.contiguous(), want_k)
+    api.rope(plan, pos, q, qo, k, ko)
+    assert torch.equal(qo, want_q) and torch.equal(ko, want_k) and torch.equal(buf[:, :18 * 256], before[:, :18 * 256])
+    after = buf.clone()
+    for a in ((q, qo, k, at(15, 2)), (q, at(17, 16), k, ko), (q, qo, k, at(33, 2)), (q, at(2, 16), k, ko)):
+        with pytest.raises((api.Q3KVError, ValueError)):
+            api.rope(plan, pos, *a)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, after)

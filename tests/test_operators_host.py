@@ -355,3 +355,60 @@ def test_evict_refuses_outputs_over_what_it_reads(lib, name):
     for kw in (dict(), dict(out=None), dict(out=mass + read), dict(kept=mass - written), dict(out=kept + written), dict(new=4096),
                dict(new=8192), dict(new=4104), dict(new=4088)):
         assert call(**kw) != INVALID, kw
+
+
+def _brute_meet(a, a_step, a_width, a_rows, b, b_step, b_width, b_rows):
+    first = {a + i * a_step + x for i in range(a_rows) for x in range(a_width)}
+    return any(b + j * b_step + x in first for j in range(b_rows) for x in range(b_width))
+
+
+def test_rows_meet_against_every_byte():
+    rng = np.random.default_rng(3)
+    seen = {True: 0, False: 0}
+    for _ in range(3000):
+        rows, width = int(rng.integers(1, 6)), int(rng.integers(1, 6))
+        sa, sb = width + int(rng.integers(0, 8)), width + int(rng.integers(0, 8))
+        if rng.random() < 0.5:
+            sb = sa
+        a, b = 1000, 1000 + int(rng.integers(-60, 60))
+        want = _brute_meet(a, sa, width, rows, b, sb, width, rows)
+        assert api._rows_meet(a, sa, b, sb, width, rows) == want, (a, sa, b, sb, width, rows)
+        seen[want] += 1
+    assert min(seen.values()) > 300
+
+
+def test_rope_binding_takes_rows_that_interleave(fake):
+    """Query rows and output rows side by side in one buffer share nothing; a shifted copy of the rows does."""
+    buf = torch.zeros((5, 3 * 4096))
+    pos = torch.zeros((5, 2), dtype=i32)
+    at = lambda x, n=4096: buf[:, x:x + n].unflatten(1, (n // 256, 256))  # noqa: E731
+    api.rope(fake.plan, pos, at(0), at(4096))
+    api.rope(fake.plan, pos, at(8192), at(0))
+    assert _names(fake) == ["q3kv_rope"] * 2
+    flat = torch.zeros(5 * 12288 + 8192)
+    wide, narrow = flat[:5 * 12288].view(5, 12288)[:, :4096].unflatten(1, (16, 256)), flat[4096:4096 + 5 * 8192].view(5, 8192)[:, :4096].unflatten(1, (16, 256))
+    for bad in ((at(0), at(256)), (at(4096), at(3840)), (wide, narrow)):
+        with pytest.raises(ValueError, match="overlaps"):
+            api.rope(fake.plan, pos, *bad)
+    assert _names(fake) == ["q3kv_rope"] * 2
+
+
+def test_rope_refuses_outputs_over_other_operands(lib):
+    """f32 rows of 4 q heads and 2 kv heads (4,096 and 2,048 bytes) in slices of one buffer, 8 rows."""
+    plan, base, pos = api.make_rope_plan(64, 1e4, (16, 16)), 1 << 24, 1 << 20
+
+    def call(q=(0, 4096), qo=(1 << 20, 4096), k=(4096, 4096), ko=(1 << 22, 2048), pos=pos):      # (byte offset, stride in floats)
+        return lib.q3kv_rope(None, ctypes.byref(plan), pos, 8, base + q[0], q[1], base + qo[0], qo[1], 4, base + k[0], k[1], base + ko[0],
+                             ko[1], 2, _lib.Q3KV_F32)
+
+    same = dict(q=(0, 4096), qo=(0, 4096), k=(4096, 4096), ko=(4096, 4096))       # in place in the projection's output
+    for kw in (dict(qo=(4096, 4096)), dict(qo=(2048, 4096)), dict(qo=(5120, 4096)), dict(ko=(0, 4096)), dict(ko=(3072, 4096)), dict(ko=(1 << 20, 2048)),
+               dict(qo=(16, 4096)), dict(qo=(16384, 4096)), dict(qo=(0, 1024)), dict(ko=(4112, 4096)), dict(pos=base + (1 << 20)),
+               dict(pos=base + (1 << 20) - 60), dict(pos=base + (1 << 22) + 2044), {**same, "pos": base + 4096 + 16384},
+               {**same, "ko": (6144, 4096), "k": (6128, 4096)}, dict(qo=(6128, 4096), ko=(6144, 4096), k=(1 << 23, 512))):
+        assert call(**kw) == INVALID, kw
+    if torch.cuda.is_available():
+        return                                       # these addresses go no further than a machine without a device
+    for kw in (dict(), same, dict(pos=base + (1 << 22) + 2048), dict(qo=(6144, 4096)), dict(ko=(6144, 4096)), dict(qo=(8192, 4096), ko=(6144, 4096)),
+               dict(pos=base + (1 << 20) - 64), {**same, "pos": base + 6144 + 7 * 16384}, dict(qo=(12288, 8192), q=(0, 8192), k=(4096, 8192))):
+        assert call(**kw) != INVALID, kw
