@@ -565,6 +565,9 @@ def _attn_mass(name, pool_bytes_fn, desc, pool, page_table, ctx_len, n_q, q_offs
     shape = mass.shape
     if len(shape) != 3 or shape[0] < n or shape[1] != hk or shape[2] < max_ctx_len:
         raise ValueError(f"mass must be [slots >= {n}, {hk}, positions >= {max_ctx_len}], got {tuple(shape)}")
+    end = p_mass + 4 * shape[0] * hk * shape[2]
+    if (p_mass < p_q + q.nbytes and p_q < end) or (p_mass < p_lse + lse.nbytes and p_lse < end) or (p_mass < p_pool + pool.nbytes and p_pool < end):
+        raise ValueError("mass overlaps q, lse or the pool")
     rc = getattr(lib, name)(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_ctx, p_nq, p_off,
                                     n, max_ctx_len, max_n_q, layer, p_q, _dtype_code(q), p_lse, float(decay), p_mass, shape[2],
                                     p_status)

@@ -412,3 +412,18 @@ def test_rope_refuses_outputs_over_other_operands(lib):
     for kw in (dict(), same, dict(pos=base + (1 << 22) + 2048), dict(qo=(6144, 4096)), dict(ko=(6144, 4096)), dict(qo=(8192, 4096), ko=(6144, 4096)),
                dict(pos=base + (1 << 20) - 64), {**same, "pos": base + 6144 + 7 * 16384}, dict(qo=(12288, 8192), q=(0, 8192), k=(4096, 8192))):
         assert call(**kw) != INVALID, kw
+
+
+def test_mass_binding_refuses_masses_over_what_the_call_reads(fake):
+    """Other CTAs read the queries, the statistic and the records while masses are stored."""
+    buf = torch.zeros(5 * 16 * 256 + 480 + 80)
+    q, lse, mass = buf[:20480].view(5, 16, 256), buf[20480:20560].view(5, 16), buf[20560:21040].view(2, 2, 120)
+    api.attn_mass(**{**_mass_args(), "q": q, "lse": lse, "mass": mass})       # side by side
+    n = len(_names(fake))
+    pool = torch.zeros(4096, dtype=torch.uint8)
+    for bad in (dict(q=q, mass=buf[20000:20480].view(2, 2, 120)), dict(q=q, mass=buf[20479:20959].view(2, 2, 120)),
+                dict(lse=lse, mass=buf[20559:21039].view(2, 2, 120)), dict(lse=lse, mass=buf[20001:20481].view(2, 2, 120)),
+                dict(pool=pool, mass=pool[16:1936].view(torch.float32).view(2, 2, 120))):
+        with pytest.raises(ValueError, match="mass overlaps"):
+            api.fp8_attn_mass(**{**_mass_args(), **bad})
+    assert len(_names(fake)) == n
