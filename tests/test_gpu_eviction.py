@@ -736,3 +736,27 @@ def test_evict_into_buffers_that_touch():
     for over in (mass[..., :k], mass[..., n - k:]):
         with pytest.raises(api.Q3KVError):
             api.evict(c.desc, c.pool, c.page_table, lens[1:2], n, lens[0:1], k, 3, 9, 0, mass, dst, kept, over, lens[2:3], c.status)
+
+
+def test_mass_goes_on_in_the_evicted_masses():
+    """With max_budget as large as the lengths to come, mass_out is the next attn_mass call's buffer: no copy."""
+    n, k, T, room = 900, 300, 4, 700
+    c = Cache("q3", [n], 2, seed=51, extra_pages=3)
+    mass = torch.rand((1, 1, 2, n), device="cuda")
+    dst = torch.from_numpy(np.asarray(c.free[:3], np.int32).reshape(1, 3)).cuda()
+    kept = torch.zeros((1, 1, 2, room), dtype=torch.int32, device="cuda")
+    out, new = torch.full((1, 1, 2, room), float("nan"), device="cuda"), i32([0])
+    api.evict(c.desc, c.pool, c.page_table, i32([n]), n, i32([k]), room, 4, 32, 0, mass, dst, kept, out, new, c.status)
+    L = k + T
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    kv = torch.randn((2, T, 2, 256), generator=gen, device="cuda")
+    api.append(c.desc, c.pool, dst, new, i32([T]), i32([0, T]), T, 0, kv[0], kv[1], c.status)
+    q = queries(T, 16, 53)
+    lse = torch.zeros((T, 16), device="cuda")
+    o, ws = torch.empty((T, 16, 256), device="cuda"), torch.zeros(api.workspace_bytes(c.desc, 1, L, T), dtype=torch.uint8, device="cuda")
+    api.verify_attn_lse(c.desc, c.pool, dst, i32([L]), i32([T]), i32([0, T]), L, T, 0, q, o, lse, ws, status=c.status)
+    copy = torch.zeros((1, 2, L), device="cuda")
+    copy[..., :k] = out[0, ..., :k]
+    api.attn_mass(c.desc, c.pool, dst, i32([L]), i32([T]), i32([0, T]), L, T, 0, q, lse, 0.9, copy, c.status)
+    api.attn_mass(c.desc, c.pool, dst, i32([L]), i32([T]), i32([0, T]), room, T, 0, q, lse, 0.9, out[0], c.status)
+    assert torch.equal(out[0, ..., :L], copy) and bool(torch.isnan(out[0, ..., L:]).all()) and int(c.status.item()) == 0
