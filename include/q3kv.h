@@ -428,8 +428,9 @@ Q3KV_API int q3kv_accept_sample_nucleus(void* stream, const void* logits, int32_
  *   - Frequencies: f_i = theta^(-i / (rotary_dim / 2)), or with
  *     Q3KV_ROPE_AXIS_FREQS theta^(-k / sections[a]) for the k-th pair of axis a.
  * A plan holds each pair's frequency as a 64-bit fixed-point fraction of a turn,
- * so position * frequency is exact modulo whole turns for every int32 position
- * (float32 angles lose whole digits beyond a few thousand positions).  It is a
+ * so position * turns[i] is exact modulo whole turns for every int32 position
+ * (float32 angles lose whole digits beyond a few thousand positions); the turns of
+ * q3kv_rope_plan_init are within 2^-53 of a turn, a double's roundings.  It is a
  * plain host struct; a caller may fill turns[] itself (scaled frequencies):
  * turns[i] = round(f_i / (2 pi) * 2^64). */
 #define Q3KV_ROPE_ADJACENT   1
@@ -580,6 +581,9 @@ Q3KV_API int q3kv_t5k_attn_mass(void* stream, const q3kv_cache_desc* desc, const
  *   d_new_len int32 [num_slots]: n; may be the array d_ctx_len or d_budget
  * d_kept, d_mass_out and d_mass must not overlap one another, nor d_new_len the
  * lengths or budgets in any other way (Q3KV_ERR_INVALID_ARG).
+ * With a max_budget as large as the lengths to come, a layer of d_mass_out is the
+ * d_mass of the next q3kv_attn_mass calls, without a copy: its mass_stride is
+ * max_budget, and entries past n are not read before that call has written them.
  * d_budget[b] > max_budget, L < 0, L > max_ctx_len, L beyond the slot's page table
  * or n beyond its destination pages set Q3KV_STATUS_BAD_LENGTH and leave the slot
  * out.  A record whose source or destination page id is out of range is skipped

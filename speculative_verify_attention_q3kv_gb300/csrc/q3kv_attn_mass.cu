@@ -44,15 +44,17 @@
 // reach (see whole_shares); a CTA rotates and splits the queries of a pair itself when it
 // enters it.
 //
-// Bound: not memory.  655,360 positions x 8 tokens x 2 kv heads take 105 us, 1,500 GB/s of K
-// records and masses (the bytes alone: 23 us; the tensor pipe is 33 % active, the schedulers 65 %,
-// a third of that in waits).  A tile of 64 rows takes about 2,900 cycles a CTA: its epilogue
+// Bound: not memory.  655,360 positions x 8 tokens x 2 kv heads take 100 us, 1,570 GB/s of K
+// records and masses (the bytes alone: 23 us; the tensor pipe is 32 % active, the schedulers 69 %,
+// a third of that in waits).  A tile of 64 rows takes about 2,800 cycles a CTA: its epilogue
 // multiplies 128 x 64 x 8 accumulators by their scales and takes 8,192 exponentials in sixteen round
-// trips to TMEM, 5,300 cycles for each of two warps a lane quarter, and the ring holds three
-// parts.  Up to 48 rows a group's accumulators come in one trip (6 tokens 92 us), up to 32 a part's
-// (4 tokens 73 us, 1 token 67 us, where the conversion of the records decides, about 2,000 cycles
-// a tile).  More warps, one event per accumulator, 64 columns a trip or passes of 32 rows were
-// slower (114 to 160 us).  Short calls (32,768 positions x 6 tokens 12.1 us) wait 4,300 cycles for
+// trips to TMEM, with which two warps a lane quarter were busy 5,300 of 5,800 cycles each in a build of
+// 104.5 us, and the ring holds three parts.  The time of this form moves by 5 % and more with the
+// compiler's spills (4 bytes in this build, 20 to 36 in builds of 104 to 110 us) and with code that
+// it does not run.  Up to 48 rows a group's accumulators come in one trip (6 tokens 92 us), up to
+// 32 a part's (4 tokens 74 us, 1 token 65 us, where the conversion of the records decides, about
+// 2,000 cycles a tile).  More warps, one event per accumulator, 64 columns a trip or passes of 32 rows were
+// slower (114 to 160 us).  Short calls (32,768 positions x 6 tokens 12.3 us) wait 4,300 cycles for
 // their share and 3,000 to 6,000 for the queries before the first tile.
 //
 // Every mbarrier wait is bounded; on a timeout the CTA sets Q3KV_STATUS_TIMEOUT, stops
@@ -932,8 +934,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                     __syncwarp();
                     tc_fence_after();
                     const uint32_t col = col0 + kPartCols * (kParts * buf + odd);
-                    // rolled: the roles share the instruction cache (655,360 positions x 8 tokens, which do not even
-                    // take this path, 114 -> 105 us; 1 token 65 -> 67)
+                    // rolled: 655,360 positions x 8 tokens, which do not take this path, 106 -> 100 us, fp8 49.0 -> 47.7,
+                    // 6 tokens 90.6 -> 92.1, 1 token the same.  The code is smaller and lies elsewhere; which of the two
+                    // counts was not looked into
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         uint32_t wc[Words<FMT>::kN];
