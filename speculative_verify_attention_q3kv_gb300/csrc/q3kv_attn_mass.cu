@@ -421,9 +421,9 @@ __device__ __forceinline__ uint32_t query_offset(int rr, int c) {
 // The power of two 2^e: hi + lo hold 22 bits of a value, but lo no finer than 2^-25.  The usual e = 8 serves a
 // pair whose largest scaled value lies in [4, 2^15): rotated queries (with the rotation's 1/16) of 0.17 to
 // 1,419 at most, for which 2^-25 is 2^-27 of the largest or less.  For others the E warps prepare the pair
-// again with an e of its own (query_scale), 1 us of a call with one token and 4 with 8.  The epilogue takes 2^e out again with the position's
-// scales; a power per row would cost it a multiply-add per row and position, and to look at all
-// rows before the first split took 0.9 us of every call.
+// again with an e of its own (query_scale), 1 us of a call with one token and 4 with 8.  The epilogue takes
+// 2^e out again with the position's scales; a power per row would cost it a multiply-add per row and
+// position, and to look at all rows before the first split took 0.9 us of every call.
 constexpr int kUsualExp = 8;
 template <typename TIn, int FMT>
 __device__ __forceinline__ void load_queries(const MassArgs& a, const Segment& s, MassSmem<FMT>& sm, int exp2q, bool again, int2& flags) {

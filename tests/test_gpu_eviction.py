@@ -760,3 +760,48 @@ def test_mass_goes_on_in_the_evicted_masses():
     api.attn_mass(c.desc, c.pool, dst, i32([L]), i32([T]), i32([0, T]), L, T, 0, q, lse, 0.9, copy, c.status)
     api.attn_mass(c.desc, c.pool, dst, i32([L]), i32([T]), i32([0, T]), room, T, 0, q, lse, 0.9, out[0], c.status)
     assert torch.equal(out[0, ..., :L], copy) and bool(torch.isnan(out[0, ..., L:]).all()) and int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["q3", "fp8", "t5k"])
+@pytest.mark.parametrize("slots", [75, 9])
+def test_mass_pairs_prepared_twice_between_others(fmt, slots):
+    """Slots with small, usual and large queries and with rows that are not finite, next to one another in a CTA's
+    segments: every slot's bits are those of the slot alone."""
+    rng = np.random.default_rng(slots)
+    top = 700 if slots > 32 else 9000
+    lengths = [int(x) for x in rng.integers(1, top, slots)]
+    widths = [int(min(n, t)) for n, t in zip(lengths, rng.integers(0, 17, slots))]
+    widths[0] = min(lengths[0], 3)
+    c = Cache(fmt, lengths, 2, seed=61)
+    q = queries(sum(widths), 16, 62, torch.bfloat16)
+    n = max(lengths)
+    lse = torch.zeros((q.shape[0], 16), device="cuda")
+    out = torch.empty((q.shape[0], 16, 256), device="cuda")
+    ws = torch.zeros(api.workspace_bytes(c.desc, slots, n, 16), dtype=torch.uint8, device="cuda")
+    VERIFY_LSE[fmt](c.desc, c.pool, c.page_table, i32(lengths), i32(widths), offsets(widths), n, 16, 0, q, out, lse, ws)
+    r0 = 0
+    for b, t in enumerate(widths):
+        kind = rng.integers(0, 5)
+        if kind < 3:
+            q[r0:r0 + t] *= 10.0 ** [-5, 0, 5][kind]
+        if kind == 2:
+            # above every score of queries 1e5 times larger, |q| |k| / 16 <= 1e5 * 2 * 20 * 20 / 16 = 5e6: masses stay finite
+            lse[r0:r0 + t] = 1.0e7
+        if t and kind == 3:
+            q[r0 + t - 1, 5, 9] = float("nan")
+        if t and kind == 4:
+            lse[r0, 11] = float("inf")
+        r0 += t
+    start = torch.rand((slots, 2, n), device="cuda")
+    mass = start.clone()
+    _mass_call(c, lengths, widths, q, lse, 1.0, mass)
+    again = start.clone()
+    _mass_call(c, lengths, widths, q, lse, 1.0, again)
+    torch.cuda.synchronize()
+    assert torch.equal(mass, again) and bool(torch.isfinite(mass).all())
+    for b in range(slots):
+        alone = [t if i == b else 0 for i, t in enumerate(widths)]
+        one = start.clone()
+        MASS[fmt](c.desc, c.pool, c.page_table, i32(lengths), i32(alone), offsets(widths), n, 16, 0, q, lse, 1.0, one)
+        torch.cuda.synchronize()
+        assert torch.equal(one[b], mass[b]), b
