@@ -402,7 +402,7 @@ def test_rope_refuses_outputs_over_other_operands(lib):
                              ko[1], 2, _lib.Q3KV_F32)
 
     same = dict(q=(0, 4096), qo=(0, 4096), k=(4096, 4096), ko=(4096, 4096))       # in place in the projection's output
-    for kw in (dict(qo=(4096, 4096)), dict(qo=(2048, 4096)), dict(qo=(5120, 4096)), dict(ko=(0, 4096)), dict(ko=(3072, 4096)), dict(ko=(1 << 20, 2048)),
+    for kw in (dict(qo=(4096, 4096)), dict(qo=(2048, 4096)), dict(qo=(5120, 4096)), dict(ko=(0, 4096)), dict(ko=(3088, 4096)), dict(ko=(1 << 20, 2048)),
                dict(qo=(16, 4096)), dict(qo=(16384, 4096)), dict(qo=(0, 1024)), dict(ko=(4112, 4096)), dict(pos=base + (1 << 20)),
                dict(pos=base + (1 << 20) - 60), dict(pos=base + (1 << 22) + 2044), {**same, "pos": base + 4096 + 16384},
                {**same, "ko": (6144, 4096), "k": (6128, 4096)}, dict(qo=(6128, 4096), ko=(6144, 4096), k=(1 << 23, 512))):
