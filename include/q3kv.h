@@ -69,6 +69,8 @@ extern "C" {
 #define Q3KV_STATUS_RANGE           32   /* tensor-core leg: a block scale above 5458
                                             (its exact fp16 dequantisation needs
                                             12 s in fp16 range) */
+#define Q3KV_STATUS_BAD_TOKEN       64   /* a token id outside [0, vocab), or biases not in
+                                            ascending order of their tokens */
 
 /* input dtypes */
 #define Q3KV_F32   0
@@ -140,6 +142,41 @@ Q3KV_API int q3kv_free_slot(q3kv_allocator* a, int32_t slot);
 
 /* Free pages left. */
 Q3KV_API int q3kv_free_pages(const q3kv_allocator* a, int32_t* n_free);
+
+/* ---- shared pages: forks, copies on write, trimming, compaction -------------------
+ * Source: the same PagedAttention paragraph (blocks are immutable once full, so
+ * requests with one prefix can hold the same blocks).  A page may be held by several slots; it
+ * returns to the free list when the last of them lets it go.  These calls only keep the books
+ * (no device work): q3kv_copy_pages moves the bytes.  Each writes a page-table row as
+ * q3kv_alloc_pages does, and changes nothing when it returns an error. */
+
+/* The row of a slot as it is now. */
+Q3KV_API int q3kv_slot_pages(const q3kv_allocator* a, int32_t slot, int32_t* h_page_table_row, int32_t* n_pages_out);
+
+/* Make dst_slot, which must hold no page, share the pages of src_slot's first n_positions
+ * positions (Q3KV_ERR_INVALID_ARG if dst_slot holds pages or src_slot fewer). */
+Q3KV_API int q3kv_fork_slot(q3kv_allocator* a, int32_t src_slot, int32_t dst_slot, int64_t n_positions,
+                     int32_t* h_page_table_row, int32_t* n_pages_out);
+
+/* Before slot writes positions [first_position, first_position + n_positions): make it hold
+ * pages up to there (as q3kv_alloc_pages) and own those of the range alone.  A page of the range
+ * that another slot holds too is replaced by a fresh one.  Only the page that the range begins
+ * inside keeps earlier positions: where that one is replaced, h_copy = {old page, new page,
+ * number of positions to copy}, for q3kv_copy_pages before the write and before any call that
+ * reads the new row; else h_copy = {-1, -1, 0}.  Positions behind the range in a replaced page
+ * are lost to this slot (a write at position n is an append to a slot of length n). */
+Q3KV_API int q3kv_write_pages(q3kv_allocator* a, int32_t slot, int64_t first_position, int64_t n_positions,
+                     int32_t* h_page_table_row, int32_t* n_pages_out, int32_t* h_copy);
+
+/* Let go of the pages behind the first n_positions positions (after a rollback or an eviction). */
+Q3KV_API int q3kv_trim_slot(q3kv_allocator* a, int32_t slot, int64_t n_positions, int32_t* h_page_table_row,
+                     int32_t* n_pages_out);
+
+/* Move held pages from the highest ids to the lowest free ones, at most max_moves of them, and
+ * list them: page h_src[i] becomes page h_dst[i].  No destination is another move's source or
+ * destination.  Every row that held a moved page changes (q3kv_slot_pages). */
+Q3KV_API int q3kv_compact_pages(q3kv_allocator* a, int32_t max_moves, int32_t* h_src, int32_t* h_dst,
+                     int32_t* n_moves_out);
 
 /* ---- quantise-append --------------------------------------------------------
  * Source: the "turbo3 3-bit KV cache" bullet of the "Quasar" (q27) wiki (each
@@ -650,6 +687,122 @@ Q3KV_API int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, 
                        float temperature, const float* d_uniforms, uint64_t seed,
                        int32_t* d_n_accepted, int32_t* d_next_token, int32_t* d_committed_len,
                        float* d_accept_prob, void* d_workspace, size_t workspace_bytes, int32_t* d_status);
+
+/* ---- block-scaled 8-bit cache ----------------------------------------------------------
+ * Beside the scale-free E4M3 cache of the "KV cache" stack bullet (whose pages measured scales per
+ * row to buy nothing for that engine's models): E4M3 codes with one scale for each block of 16
+ * positions of a kv head, K and V apart, so that large values do not saturate and small ones
+ * keep their digits.  Not rotated.
+ *   scale   2^e with the smallest e in [-64, 64] for which no |x| of the block exceeds 448 2^e
+ *           (-64 for a block of zeros)
+ *   code    E4M3 of x 2^-e, to nearest even, magnitudes above 448 (and infinities) to 448
+ * A block grows by appends: its scale is the larger of the one it has and the one that the new rows
+ * ask for, and if it grows the earlier rows' codes are rewritten for it (each by the rounding of
+ * code 2^(old e - new e), exact but for codes that become subnormal).  A block's first row starts
+ * it afresh; a rollback leaves its scale.
+ * Pool: per (page, layer, kv_head, kv) a unit of 65,600 bytes at
+ *   (((page*num_layers + layer)*num_kv_heads + kv_head)*2 + kv) * 65600:
+ * the code of row r = position % 256 and dim d is byte
+ *   ((r/8)*16 + d/16)*128 + (r%8)*16 + d%16,
+ * and the 16 blocks' scales are float32 at byte 65536 + 4*(r/16).  16-byte aligned.
+ * Arguments, status bits and errors of q3kv_bs8_append are those of q3kv_append
+ * (SCALE_OVERFLOW: a finite value above 448 2^64, which saturates). */
+Q3KV_API int q3kv_bs8_pool_bytes(const q3kv_cache_desc* desc, size_t* bytes);
+Q3KV_API int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_slot_len, const int32_t* d_n_new, const int32_t* d_row_offsets,
+                     int32_t num_slots, int32_t max_n_new, int32_t layer,
+                     const void* k, const void* v, int32_t dtype, int32_t* d_status);
+
+/* Verify attention over it, with q3kv_verify_attn's arguments and masks but for:
+ *   out     of q's dtype (float32 or bf16), same indexing as q
+ *   impl    Q3KV_IMPL_AUTO or Q3KV_IMPL_FMA: CUDA cores, float32 arithmetic
+ *   d_workspace   at least q3kv_bs8_workspace_bytes(...) bytes, 16-byte aligned, no initial
+ *           contents needed; its size is the same for every call on a device.  Calls that share
+ *           one must not overlap on the GPU.
+ * A slot with T_b > L_b, L_b above max_ctx_len or beyond its page table, T_b above max_n_q or a
+ * negative offset sets Q3KV_STATUS_BAD_LENGTH and its rows are left as they were.  Positions of
+ * a page out of range count as hidden (Q3KV_STATUS_BAD_PAGE); a row that sees nothing is 0.  A
+ * query row that is not finite gives NaN. */
+Q3KV_API int q3kv_bs8_workspace_bytes(const q3kv_cache_desc* desc, int32_t num_slots, int64_t max_ctx_len,
+                     int32_t max_n_q, int32_t impl, size_t* bytes);
+Q3KV_API int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
+                     const int32_t* d_page_table, int32_t max_pages_per_slot,
+                     const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                     int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer,
+                     const void* q, int32_t dtype, void* out, int32_t impl,
+                     void* d_workspace, size_t workspace_bytes, int32_t* d_status);
+
+/* ---- copies of pages ---------------------------------------------------------------------
+ * Copies n pages, all layers: page d_src[i] of the source pool to page d_dst[i] of the destination
+ * pool, or its first d_rows[i] positions (0..256; d_rows NULL: all).  Positions behind them keep
+ * what the destination held (block-scaled cache: so do their codes, while the scale of a block
+ * that begins before d_rows[i] is copied).
+ *   desc            the cache's shape; num_pages of the source pool
+ *   d_dst_pool, dst_num_pages   may be the source pool (dst_num_pages = desc->num_pages);
+ *                   pools that overlap otherwise are refused
+ *   n               at most 4096 (Q3KV_ERR_UNSUPPORTED above)
+ * All pairs are copied as if at once.  A pair with a page out of range, or whose destination is
+ * another pair's destination or (in one pool) source, sets Q3KV_STATUS_BAD_PAGE and is skipped; a row count
+ * outside 0..256 sets Q3KV_STATUS_BAD_LENGTH likewise.  A page copied to itself stays. */
+Q3KV_API int q3kv_copy_pages(void* stream, const q3kv_cache_desc* desc, const void* d_src_pool, void* d_dst_pool,
+                     int32_t dst_num_pages, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_rows,
+                     int32_t n, int32_t* d_status);
+Q3KV_API int q3kv_fp8_copy_pages(void* stream, const q3kv_cache_desc* desc, const void* d_src_pool, void* d_dst_pool,
+                     int32_t dst_num_pages, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_rows,
+                     int32_t n, int32_t* d_status);
+Q3KV_API int q3kv_t5k_copy_pages(void* stream, const q3kv_cache_desc* desc, const void* d_src_pool, void* d_dst_pool,
+                     int32_t dst_num_pages, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_rows,
+                     int32_t n, int32_t* d_status);
+Q3KV_API int q3kv_bs8_copy_pages(void* stream, const q3kv_cache_desc* desc, const void* d_src_pool, void* d_dst_pool,
+                     int32_t dst_num_pages, const int32_t* d_src, const int32_t* d_dst, const int32_t* d_rows,
+                     int32_t n, int32_t* d_status);
+
+/* ---- token counts and logits --------------------------------------------------------------
+ * What runs between the model's logits and the acceptance ("Serving", sampler paragraph; "Model
+ * tool protocol": constrained tool calls): penalties for repeated tokens, biases, grammar masks.
+ *
+ * d_counts int16 [num_slots, counts_stride], one word per vocabulary entry and slot: bits 0..14
+ * how often the token was generated (stays at 32767), bit 15 set if the prompt holds it.  A new
+ * slot's words are zeroed by the caller.  counts_stride: entries per slot, a multiple of 8, at
+ * least vocab; d_counts 16-byte aligned.
+ *
+ * q3kv_count_tokens adds slot b's tokens d_tokens[d_offsets[b] .. + d_n[b]) (prompt = 0: one per
+ * occurrence; 1: marks them as the prompt's).  d_tokens holds num_tokens; max_n bounds d_n[b].
+ * A range outside it sets Q3KV_STATUS_BAD_LENGTH and skips the slot; a token outside [0, vocab)
+ * sets Q3KV_STATUS_BAD_TOKEN and is skipped.  After a step the committed tokens are the step's
+ * t_0 .. t_a: d_offsets = d_q_offsets, d_n = n_accepted + 1.  d_counts overlapping an input is refused. */
+Q3KV_API int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_stride, int32_t vocab,
+                     const int32_t* d_tokens, int64_t num_tokens, const int32_t* d_offsets, const int32_t* d_n,
+                     int32_t num_slots, int32_t max_n, int32_t prompt, int32_t* d_status);
+
+/* Slot b's row j is row d_q_offsets[b] + j of logits [num_rows, vocab], j < d_n_q[b] <= max_n_q <= 16;
+ * it comes after the step's tokens t_0 .. t_j (d_tokens, same indexing), which d_counts does not
+ * hold yet.  With c = count + #{i <= j : t_i = x}, in float32, for every token x of the row:
+ *   y = l;  if c > 0 or the prompt holds x:  y = y > 0 ? y / repetition : y * repetition
+ *   if c > 0:  y = y - frequency c - presence
+ *   y = y + bias(x);  where the row's mask bit is 0:  y = -inf
+ * and out = y rounded to the logits' dtype (f32 or bf16).
+ *   out            [num_rows, vocab]; may be logits itself (then rows change in place), must not overlap
+ *                  any other operand.  Rows of no slot are left as they were.
+ *   d_counts       or NULL: only the step's tokens count
+ *   d_repetition, d_frequency, d_presence   float [num_slots], each or NULL (1, 0, 0)
+ *   d_bias_offsets int32 [num_slots + 1] or NULL; slot b's biases are entries
+ *                  [d_bias_offsets[b], d_bias_offsets[b + 1]) of d_bias_tokens (ascending, each once)
+ *                  and d_bias_values, which hold num_biases entries
+ *   d_mask         int32 [num_rows, ceil(vocab / 32)] or NULL: bit x % 32 of word x / 32 is 1 where x is
+ *                  allowed.  A row that allows nothing is -inf everywhere.
+ * A slot whose rows are not within num_rows, or a range of biases outside num_biases, sets
+ * Q3KV_STATUS_BAD_LENGTH (the slot, or its biases, are skipped).  A step token or a bias token
+ * outside [0, vocab), or a bias token not above the one before it, sets Q3KV_STATUS_BAD_TOKEN
+ * and is skipped. */
+Q3KV_API int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dtype, int32_t vocab,
+                     const int32_t* d_q_offsets, const int32_t* d_n_q, const int32_t* d_tokens,
+                     int32_t num_slots, int32_t num_rows, int32_t max_n_q,
+                     const int16_t* d_counts, int64_t counts_stride, const float* d_repetition,
+                     const float* d_frequency, const float* d_presence,
+                     const int32_t* d_bias_offsets, const int32_t* d_bias_tokens, const float* d_bias_values,
+                     int32_t num_biases, const int32_t* d_mask, int32_t* d_status);
 
 #ifdef __cplusplus
 }

@@ -31,6 +31,7 @@ Q3KV_STATUS_BAD_PAGE = 4
 Q3KV_STATUS_BAD_LENGTH = 8
 Q3KV_STATUS_TIMEOUT = 16
 Q3KV_STATUS_RANGE = 32
+Q3KV_STATUS_BAD_TOKEN = 64
 
 Q3KV_F32 = 0
 Q3KV_BF16 = 1
@@ -73,6 +74,7 @@ _MASS = [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_vo
          c_void_p, c_int32, c_void_p, ctypes.c_float, c_void_p, c_int64, c_void_p]
 _EVICT = [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int32, c_int32,
           c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
+_COPY = [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p]
 
 # name -> (restype, argtypes); mirrors include/q3kv.h
 PROTOTYPES = {
@@ -86,6 +88,11 @@ PROTOTYPES = {
     "q3kv_alloc_pages": (c_int32, [c_void_p, c_int32, c_int64, P_int32, P_int32]),
     "q3kv_free_slot": (c_int32, [c_void_p, c_int32]),
     "q3kv_free_pages": (c_int32, [c_void_p, P_int32]),
+    "q3kv_slot_pages": (c_int32, [c_void_p, c_int32, P_int32, P_int32]),
+    "q3kv_fork_slot": (c_int32, [c_void_p, c_int32, c_int32, c_int64, P_int32, P_int32]),
+    "q3kv_write_pages": (c_int32, [c_void_p, c_int32, c_int64, c_int64, P_int32, P_int32, P_int32]),
+    "q3kv_trim_slot": (c_int32, [c_void_p, c_int32, c_int64, P_int32, P_int32]),
+    "q3kv_compact_pages": (c_int32, [c_void_p, c_int32, P_int32, P_int32, P_int32]),
     "q3kv_append": (c_int32, [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
                               c_int32, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_void_p]),
     "q3kv_workspace_bytes": (c_int32, [P_desc, c_int32, c_int64, c_int32, c_int32, c_int32,
@@ -143,6 +150,22 @@ PROTOTYPES = {
                                     c_void_p, c_int32, c_int32, c_int32, c_void_p, ctypes.c_float, c_void_p,
                                     ctypes.c_uint64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                     c_void_p]),
+    "q3kv_bs8_pool_bytes": (c_int32, [P_desc, ctypes.POINTER(c_size_t)]),
+    "q3kv_bs8_append": (c_int32, [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                  c_int32, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_void_p]),
+    "q3kv_bs8_workspace_bytes": (c_int32, [P_desc, c_int32, c_int64, c_int32, c_int32, ctypes.POINTER(c_size_t)]),
+    "q3kv_bs8_verify_attn": (c_int32, [c_void_p, P_desc, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                                       c_int32, c_int64, c_int32, c_int32, c_void_p, c_int32, c_void_p, c_int32,
+                                       c_void_p, c_size_t, c_void_p]),
+    "q3kv_copy_pages": (c_int32, _COPY),
+    "q3kv_fp8_copy_pages": (c_int32, _COPY),
+    "q3kv_t5k_copy_pages": (c_int32, _COPY),
+    "q3kv_bs8_copy_pages": (c_int32, _COPY),
+    "q3kv_count_tokens": (c_int32, [c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_int32,
+                                    c_int32, c_int32, c_void_p]),
+    "q3kv_process_logits": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                      c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_int32, c_void_p, c_void_p]),
 }
 
 Q3KV_NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -229,6 +229,41 @@ class Allocator:
               "q3kv_alloc_pages")
         return row
 
+    def _row(self, name: str, *args) -> np.ndarray:
+        row = np.full(self.max_pages_per_slot, -1, dtype=np.int32)
+        n = ctypes.c_int32()
+        check(getattr(self._lib, name)(self._h, *args, row.ctypes.data_as(_lib.P_int32), ctypes.byref(n)), name)
+        return row
+
+    def pages(self, slot: int) -> np.ndarray:
+        """The slot's page-table row as it is now."""
+        return self._row("q3kv_slot_pages", slot)
+
+    def fork(self, src_slot: int, dst_slot: int, n_positions: int) -> np.ndarray:
+        """dst_slot shares the pages of src_slot's first n_positions positions; its row."""
+        return self._row("q3kv_fork_slot", src_slot, dst_slot, n_positions)
+
+    def write(self, slot: int, first_position: int, n_positions: int):
+        """Pages for a write that begins at first_position, none of them shared: (row, copy); copy is None or the
+        (old page, new page, positions) that copy_pages has to move before the write."""
+        row = np.full(self.max_pages_per_slot, -1, dtype=np.int32)
+        n, copy = ctypes.c_int32(), (ctypes.c_int32 * 3)()
+        check(self._lib.q3kv_write_pages(self._h, slot, first_position, n_positions, row.ctypes.data_as(_lib.P_int32),
+                                         ctypes.byref(n), copy), "q3kv_write_pages")
+        return row, tuple(copy) if copy[0] >= 0 else None
+
+    def trim(self, slot: int, n_positions: int) -> np.ndarray:
+        """Let go of the pages behind n_positions; the row."""
+        return self._row("q3kv_trim_slot", slot, n_positions)
+
+    def compact(self, max_moves: int):
+        """Move pages to the lowest free ids: int32 arrays (src, dst) for copy_pages; rows are in pages()."""
+        src, dst = np.empty(max(max_moves, 1), np.int32), np.empty(max(max_moves, 1), np.int32)
+        n = ctypes.c_int32()
+        check(self._lib.q3kv_compact_pages(self._h, max_moves, src.ctypes.data_as(_lib.P_int32), dst.ctypes.data_as(_lib.P_int32),
+                                           ctypes.byref(n)), "q3kv_compact_pages")
+        return src[:n.value], dst[:n.value]
+
     def free_slot(self, slot: int) -> None:
         check(self._lib.q3kv_free_slot(self._h, slot), "q3kv_free_slot")
 
@@ -745,3 +780,171 @@ def accept_draft(logits: torch.Tensor, draft_probs: torch.Tensor, q_offsets: tor
                                        p[4], n, rows, max_n_q, p[5], float(temperature), p[6], int(seed) & ((1 << 64) - 1), p[7],
                                        p[8], p[9], p[10], p[11], 0 if workspace is None else workspace.nbytes, p[12])
     check(rc, "q3kv_accept_draft")
+
+
+def bs8_pool_bytes(desc: CacheDesc) -> int:
+    """q3kv_bs8_pool_bytes: bytes of a block-scaled 8-bit pool (65,600 bytes per page, layer, kv head and K or V)."""
+    n = ctypes.c_size_t()
+    check(_lib.load().q3kv_bs8_pool_bytes(ctypes.byref(desc), ctypes.byref(n)), "q3kv_bs8_pool_bytes")
+    return n.value
+
+
+def bs8_append(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, slot_len: torch.Tensor,
+               n_new: torch.Tensor, row_offsets: torch.Tensor, max_n_new: int, layer: int,
+               k: torch.Tensor, v: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_bs8_append: store k, v [rows, kv_heads, 256] as E4M3 codes with a scale per block of 16 positions and head."""
+    dev, lib = _current_device(), _lib.load()
+    n, pages, (p_pool, p_table, p_len, p_new, p_off, p_status) = _cache_pointers(
+        desc, pool, _pool_need(bs8_pool_bytes, lib, bytes(desc)), page_table, slot_len, n_new, row_offsets, status, dev)
+    if k is None or v is None:
+        _required(k=k, v=v)
+    p_k, p_v = _pointers(dev, ("k", k, None, 0), ("v", v, k.dtype if isinstance(k, torch.Tensor) else None, 0))
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != desc.num_kv_heads or shape[2] != HEAD_DIM or v.shape != shape:
+        raise ValueError(f"k and v must be [rows, {desc.num_kv_heads}, {HEAD_DIM}], got {tuple(shape)} and {tuple(v.shape)}")
+    rc = lib.q3kv_bs8_append(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_len, p_new, p_off, n, max_n_new, layer,
+                             p_k, p_v, _dtype_code(k), p_status)
+    check(rc, "q3kv_bs8_append")
+
+
+def bs8_workspace_bytes(desc: CacheDesc, num_slots: int, max_ctx_len: int, max_n_q: int, impl: int = _lib.Q3KV_IMPL_AUTO) -> int:
+    n = ctypes.c_size_t()
+    check(_lib.load().q3kv_bs8_workspace_bytes(ctypes.byref(desc), num_slots, max_ctx_len, max_n_q, impl, ctypes.byref(n)),
+          "q3kv_bs8_workspace_bytes")
+    return n.value
+
+
+def bs8_verify_attn(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                    n_q: torch.Tensor, q_offsets: torch.Tensor, max_ctx_len: int, max_n_q: int, layer: int,
+                    q: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, impl: int = _lib.Q3KV_IMPL_AUTO,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_bs8_verify_attn: out[rows, q_heads, 256] (q's dtype) for every slot's query tokens over the block-scaled cache."""
+    dev, lib = _current_device(), _lib.load()
+    n, pages, (p_pool, p_table, p_ctx, p_nq, p_off, p_status) = _cache_pointers(
+        desc, pool, _pool_need(bs8_pool_bytes, lib, bytes(desc)), page_table, ctx_len, n_q, q_offsets, status, dev)
+    if q is None or out is None or workspace is None:
+        _required(q=q, out=out, workspace=workspace)
+    p_q, p_out, p_ws = _pointers(dev, ("q", q, None, 0), ("out", out, q.dtype if isinstance(q, torch.Tensor) else None, 0),
+                                 ("workspace", workspace, None, 0))
+    heads, shape = desc.num_q_heads, q.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != HEAD_DIM:
+        raise ValueError(f"q must be [rows, {heads}, {HEAD_DIM}], got {tuple(shape)}")
+    if out.dim() != 3 or out.shape[0] < shape[0] or out.shape[1:] != shape[1:]:
+        raise ValueError(f"out must be [rows >= {shape[0]}, {heads}, {HEAD_DIM}], got {tuple(out.shape)}")
+    rc = lib.q3kv_bs8_verify_attn(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_ctx, p_nq, p_off, n, max_ctx_len,
+                                  max_n_q, layer, p_q, _dtype_code(q), p_out, impl, p_ws, workspace.nbytes, p_status)
+    check(rc, "q3kv_bs8_verify_attn")
+
+
+def copy_pages(desc: CacheDesc, pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, rows: Optional[torch.Tensor] = None,
+               dst_pool: Optional[torch.Tensor] = None, dst_num_pages: Optional[int] = None,
+               status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_copy_pages: pages src[i] to dst[i] (int32), or their first rows[i] positions, within pool or into dst_pool."""
+    _copy_pages("q3kv_copy_pages", pool_bytes, desc, pool, src, dst, rows, dst_pool, dst_num_pages, status, stream)
+
+
+def fp8_copy_pages(desc: CacheDesc, pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                   dst_pool: Optional[torch.Tensor] = None, dst_num_pages: Optional[int] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_fp8_copy_pages: copy_pages in an fp8 comparison pool."""
+    _copy_pages("q3kv_fp8_copy_pages", fp8_pool_bytes, desc, pool, src, dst, rows, dst_pool, dst_num_pages, status, stream)
+
+
+def t5k_copy_pages(desc: CacheDesc, pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                   dst_pool: Optional[torch.Tensor] = None, dst_num_pages: Optional[int] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_t5k_copy_pages: copy_pages in a turbo5k-style pool."""
+    _copy_pages("q3kv_t5k_copy_pages", t5k_pool_bytes, desc, pool, src, dst, rows, dst_pool, dst_num_pages, status, stream)
+
+
+def bs8_copy_pages(desc: CacheDesc, pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                   dst_pool: Optional[torch.Tensor] = None, dst_num_pages: Optional[int] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_bs8_copy_pages: copy_pages in a block-scaled 8-bit pool."""
+    _copy_pages("q3kv_bs8_copy_pages", bs8_pool_bytes, desc, pool, src, dst, rows, dst_pool, dst_num_pages, status, stream)
+
+
+def _copy_pages(name, pool_bytes_fn, desc, pool, src, dst, rows, dst_pool, dst_num_pages, status, stream) -> None:
+    dev, lib = _current_device(), _lib.load()
+    if pool is None or src is None or dst is None:
+        _required(pool=pool, src=src, dst=dst)
+    if (dst_pool is None) != (dst_num_pages is None):
+        raise ValueError("dst_pool and dst_num_pages come together")
+    n, i32 = src.numel(), torch.int32
+    p_pool, p_dpool, p_src, p_dst, p_rows, p_status = _pointers(
+        dev, ("pool", pool, None, 0), ("dst_pool", dst_pool, None, 0), ("src", src, i32, n), ("dst", dst, i32, n), ("rows", rows, i32, n),
+        ("status", status, i32, 1))
+    if dst.numel() != n or (rows is not None and rows.numel() != n):
+        raise ValueError(f"src, dst and rows must have one entry per page, got {n}, {dst.numel()}"
+                         + (f" and {rows.numel()}" if rows is not None else ""))
+    need = _pool_need(pool_bytes_fn, lib, bytes(desc))
+    if _nbytes(pool) < need:
+        raise ValueError(f"pool holds {_nbytes(pool)} bytes, the cache needs {need}")
+    if dst_pool is None:
+        p_dpool, pages = p_pool, desc.num_pages
+    else:
+        pages = dst_num_pages
+        if pages > 0 and _nbytes(dst_pool) < need // desc.num_pages * pages:
+            raise ValueError(f"dst_pool holds {_nbytes(dst_pool)} bytes, its pages need {need // desc.num_pages * pages}")
+    rc = getattr(lib, name)(_stream(stream), ctypes.byref(desc), p_pool, p_dpool, pages, p_src, p_dst, p_rows, n, p_status)
+    check(rc, name)
+
+
+def count_tokens(counts: torch.Tensor, vocab: int, tokens: torch.Tensor, offsets: torch.Tensor, n: torch.Tensor, max_n: int,
+                 prompt: bool = False, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_count_tokens: add tokens[offsets[b] .. + n[b]) (int32) to slot b's counts int16 [slots, stride >= vocab]."""
+    if counts is None or tokens is None or offsets is None or n is None:
+        _required(counts=counts, tokens=tokens, offsets=offsets, n=n)
+    if n.dim() != 1:
+        raise ValueError("n must be one-dimensional")
+    slots, i32 = n.numel(), torch.int32
+    p_counts, p_tok, p_off, p_n, p_status = _pointers(_current_device(), ("counts", counts, torch.int16, 0), ("tokens", tokens, i32, 0),
+                                                      ("offsets", offsets, i32, slots), ("n", n, i32, 0), ("status", status, i32, 1))
+    shape = counts.shape
+    if len(shape) != 2 or shape[0] < slots or shape[1] < vocab:
+        raise ValueError(f"counts must be [slots >= {slots}, entries >= {vocab}], got {tuple(shape)}")
+    rc = _lib.load().q3kv_count_tokens(_stream(stream), p_counts, shape[1], vocab, p_tok, tokens.numel(), p_off, p_n, slots, max_n,
+                                       1 if prompt else 0, p_status)
+    check(rc, "q3kv_count_tokens")
+
+
+def process_logits(logits: torch.Tensor, out: torch.Tensor, q_offsets: torch.Tensor, n_q: torch.Tensor, tokens: torch.Tensor,
+                   max_n_q: int, counts: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                   frequency: Optional[torch.Tensor] = None, presence: Optional[torch.Tensor] = None,
+                   bias_offsets: Optional[torch.Tensor] = None, bias_tokens: Optional[torch.Tensor] = None,
+                   bias_values: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q3kv_process_logits: penalties, biases and grammar masks on logits [rows, vocab] into out (which may be logits)."""
+    if logits is None or out is None or q_offsets is None or n_q is None or tokens is None:
+        _required(logits=logits, out=out, q_offsets=q_offsets, n_q=n_q, tokens=tokens)
+    shape = logits.shape
+    if len(shape) != 2:
+        raise ValueError(f"logits must be [rows, vocab], got {tuple(shape)}")
+    if n_q.dim() != 1:
+        raise ValueError("n_q must be one-dimensional")
+    rows, vocab = shape
+    n, i32, f32 = n_q.numel(), torch.int32, torch.float32
+    p = _pointers(_current_device(), ("logits", logits, None, 0), ("out", out, logits.dtype, 0), ("q_offsets", q_offsets, i32, n),
+                  ("n_q", n_q, i32, 0), ("tokens", tokens, i32, rows), ("counts", counts, torch.int16, 0),
+                  ("repetition", repetition, f32, n), ("frequency", frequency, f32, n), ("presence", presence, f32, n),
+                  ("bias_offsets", bias_offsets, i32, n + 1), ("bias_tokens", bias_tokens, i32, 0), ("bias_values", bias_values, f32, 0),
+                  ("mask", mask, i32, 0), ("status", status, i32, 1))
+    if out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    stride = 0
+    if counts is not None:
+        if counts.dim() != 2 or counts.shape[0] < n or counts.shape[1] < vocab:
+            raise ValueError(f"counts must be [slots >= {n}, entries >= {vocab}], got {tuple(counts.shape)}")
+        stride = counts.shape[1]
+    biases = 0
+    if bias_offsets is not None:
+        if bias_tokens is None or bias_values is None:
+            _required(bias_tokens=bias_tokens, bias_values=bias_values)
+        biases = bias_tokens.numel()
+        if bias_values.numel() != biases:
+            raise ValueError(f"bias_tokens and bias_values differ in length: {biases} and {bias_values.numel()}")
+    if mask is not None and tuple(mask.shape) != (rows, (vocab + 31) // 32):
+        raise ValueError(f"mask must be {(rows, (vocab + 31) // 32)}, got {tuple(mask.shape)}")
+    rc = _lib.load().q3kv_process_logits(_stream(stream), p[0], p[1], _dtype_code(logits), vocab, p[2], p[3], p[4], n, rows, max_n_q, p[5],
+                                         stride, p[6], p[7], p[8], p[9], p[10], p[11], biases, p[12], p[13])
+    check(rc, "q3kv_process_logits")

@@ -1,0 +1,553 @@
+// The block-scaled 8-bit cache: append, the CUDA-core leg of its verify attention, the merge and the entry points.
+//
+// Format.  A block is 16 consecutive positions of one kv head, K or V.  Its scale is 2^e with the smallest e in
+// [-64, 64] for which no |x| of the block is above 448 2^e; the codes are E4M3 of x 2^-e.  A code that is itself a
+// floating-point number gains nothing from a scale's fraction, and a power of two makes a rescaling exact but
+// for codes that fall under E4M3's smallest normal value: so a block can grow by appends.  When the rows appended
+// to a block that holds earlier rows need a larger e, the earlier codes are rewritten for it; e never falls within a
+// block (a rejected draft may leave it larger than the rows that stay need).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "q3kv_bs8.cuh"
+
+namespace q3kv {
+namespace {
+
+// ---------------------------------------------------------------- append
+// One CTA per (block, slot, kv head, K|V), a thread per row and 16 dims: it reads 32 or 64 neighbouring bytes, and a
+// warp writes four whole cores (512 bytes).  Bound: the rows read and the codes written.
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ void load16(const float* src, float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 u = reinterpret_cast<const float4*>(src)[i];
+        x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
+    }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* src, float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 u = reinterpret_cast<const uint4*>(src)[i];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    }
+}
+
+// Two floats -> two E4M3 bytes (lo in the low byte), to nearest even, magnitudes above 448 to 448.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+__device__ __forceinline__ uint4 encode16(const float (&x)[16], float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | (e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int scale_exp(float s) {       // of a stored scale, whatever its bytes hold
+    return min(kBs8MaxExp, max(-kBs8MaxExp, (int)((__float_as_uint(s) >> 23) & 0xff) - 127));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads) append_bs8_kernel(AppendArgs a) {
+    __shared__ float s_max[kAppendThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int slot = blockIdx.y, head = blockIdx.z >> 1, kv = blockIdx.z & 1;
+    const int n_new = a.n_new[slot];
+    if (n_new == 0) return;
+    const int64_t len = a.slot_len[slot], end = len + n_new;
+    const bool report = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && a.status;
+    if (n_new < 0 || n_new > a.max_n_new || len < 0) {
+        if (report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
+        return;
+    }
+    const int64_t room = (int64_t)a.max_pages_per_slot * kPageSize;
+    if (end > room && report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);      // positions behind the table are skipped
+    const int64_t block = len / kBs8Block + blockIdx.x, p0 = block * kBs8Block;
+    if (p0 >= end || p0 >= room) return;
+    const int32_t page = a.page_table[(int64_t)slot * a.max_pages_per_slot + p0 / kPageSize];
+    if (page < 0 || page >= a.num_pages) {
+        if (threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = (warp & 1) * 8 + (lane & 7), chunk = (warp >> 1) * 4 + (lane >> 3);
+    const int64_t pos = p0 + row;
+    const bool fresh = pos >= len && pos < end, kept = pos < len;
+    uint8_t* unit = a.pool + bs8_offset(a.num_layers, a.num_kv_heads, page, a.layer, head, kv);
+    const int in_page = (int)(p0 % kPageSize);
+    uint4* code = reinterpret_cast<uint4*>(unit + ((in_page + row) / 8 * 16 + chunk) * 128 + (row % 8) * 16);
+    float* scale = reinterpret_cast<float*>(unit + kBs8CodeBytes) + in_page / kBs8Block;
+
+    float x[16];
+    float top = 0.0f;
+    bool finite = true;
+    if (fresh) {
+        const T* in = static_cast<const T*>(kv == 0 ? a.k : a.v);
+        load16(in + (((int64_t)a.row_offsets[slot] + (pos - len)) * a.num_kv_heads + head) * kHeadDim + chunk * 16, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const bool ok = fabsf(x[i]) <= 3.402823466e38f;
+            finite = finite && ok;
+            top = fmaxf(top, ok ? fabsf(x[i]) : 0.0f);
+        }
+    }
+    int e = -kBs8MaxExp;
+    int old = e;
+    uint4 was = make_uint4(0, 0, 0, 0);
+    if (p0 < len) {
+        e = old = scale_exp(*scale);
+        if (kept) was = *code;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_max[warp] = top;
+    if (!__all_sync(0xffffffffu, finite) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAppendThreads / 32; ++i) top = fmaxf(top, s_max[i]);
+    // top = m 2^k with 1 <= m < 2 and 448 = 1.75 2^8; zero and subnormal values give the smallest e
+    const uint32_t u = __float_as_uint(top);
+    const int need = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    if (need > kBs8MaxExp && threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_SCALE_OVERFLOW);
+    e = min(kBs8MaxExp, max(e, need));
+    if (fresh) {
+        *code = encode16(x, pow2(-e));
+    } else if (kept && e != old) {
+        const uint32_t w[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = e4m3x2_to_f32((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+        *code = encode16(x, e - old > 2 * kBs8MaxExp - 2 ? 0.0f : pow2(old - e));
+    }
+    if (threadIdx.x == 0) *scale = pow2(e);
+}
+
+// ---------------------------------------------------------------- verify attention on CUDA cores
+// Float32 arithmetic throughout, for float32 queries.  One CTA per share; sub-tiles of 64 positions are decoded to
+// shared memory.  Bound: the FMAs of 64 rows x 64 positions x 256 dims, twice; each thread holds 4 x 4 scores and
+// 8 x 8 outputs, so that two shared 16-byte loads feed 8 (scores) or 16 (outputs) FMAs each.
+constexpr int kFmaThreads = 256;
+constexpr int kSub = 64;                  // positions per sub-tile
+constexpr int kLd = kHeadDim + 4;         // floats per row in shared memory: neighbouring rows start 4 banks apart
+constexpr int kLdP = kBs8Rows + 4;
+struct FmaSmem {
+    float q[kBs8Rows * kLd];
+    float kv[kSub * kLd];
+    float p[kSub * kLdP];                 // [position][row]
+    float m[kBs8Rows], l[kBs8Rows], f[kBs8Rows];
+    Bs8Share first;
+};
+
+__device__ __forceinline__ float ld_any(const void* p, int64_t i, int dtype) {
+    return dtype == Q3KV_F32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void st4(void* p, int64_t i, int dtype, float4 v) {
+    if (dtype == Q3KV_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
+    } else {
+        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) = *reinterpret_cast<uint2*>(h);
+    }
+}
+
+// 64 positions from p0 of a unit into shared memory as float32; positions from `valid` on become zero.
+__device__ __forceinline__ void decode_sub(const uint8_t* unit, int in_page, int valid, float* dst) {
+    const float* scales = reinterpret_cast<const float*>(unit + kBs8CodeBytes);
+    for (int i = threadIdx.x; i < kSub * 16; i += kFmaThreads) {
+        const int row = (i >> 7) * 8 + (i & 7), chunk = (i >> 3) & 15;         // memory order
+        float* to = dst + row * kLd + chunk * 16;
+        float4 o[4];
+        if (unit && row < valid) {
+            const uint4 c = *reinterpret_cast<const uint4*>(unit + (((in_page + row) >> 3) * 16 + chunk) * 128 + (row & 7) * 16);
+            const float s = scales[(in_page + row) / kBs8Block];
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 lo = e4m3x2_to_f32(w[j] & 0xffffu), hi = e4m3x2_to_f32(w[j] >> 16);
+                o[j] = make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) reinterpret_cast<float4*>(to)[j] = o[j];
+    }
+}
+
+__global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    FmaSmem& sm = *reinterpret_cast<FmaSmem*>(smem_raw);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == 0) {
+        bool bad = false;
+        const Bs8Share w = bs8_share(a, blockIdx.x, &bad);
+        if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
+        if (lane == 0) sm.first = w;
+    }
+    __syncthreads();
+    Bs8Share w = sm.first;
+    if (w.tiles == 0) return;
+    const int heads = a.num_kv_heads, qheads = heads * kGroup;
+    const int ry = tid >> 4, px = tid & 15;               // scores: rows 4 ry.., positions px + 16 j
+    const int rows8 = (tid >> 5) * 8;                     // outputs: 8 rows, dims 4 lane.. and 128 + 4 lane..
+    do {
+        const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), head = w.head(heads);
+        const int nrows = min(kBs8Rows, kGroup * (w.s.T - T0));
+        const int64_t q0 = (int64_t)a.q_offsets[w.slot] + T0;
+        __syncthreads();                                  // the last segment's outputs are read
+        for (int i = tid; i < kBs8Rows * kHeadDim; i += kFmaThreads) {
+            const int r = i >> 8, d = i & 255;
+            sm.q[r * kLd + d] = r < nrows ? ld_any(a.q, ((q0 + (r >> 3)) * qheads + head * kGroup + (r & 7)) * kHeadDim + d, a.dtype) * 0.0625f : 0.0f;
+        }
+        if (tid < kBs8Rows) {
+            sm.m[tid] = -1e30f;
+            sm.l[tid] = 0.0f;
+        }
+        float o[8][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[i][j] = 0.0f;
+        const int pos_end = min(w.s.L, (w.tile + w.tiles) * kBs8Tile);
+        for (int p0 = w.tile * kBs8Tile; p0 < pos_end; p0 += kSub) {
+            const int valid = min(kSub, w.s.L - p0);
+            const int32_t page = a.page_table[(int64_t)w.slot * a.max_pages_per_slot + p0 / kPageSize];
+            const bool good = page >= 0 && page < a.num_pages;
+            if (!good && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+            const uint8_t* unit = good ? a.pool + bs8_offset(a.num_layers, heads, page, a.layer, head, 0) : nullptr;
+            __syncthreads();                              // q is there; the last sub-tile is read
+            decode_sub(unit, p0 % kPageSize, valid, sm.kv);
+            __syncthreads();
+            float s[4][4] = {};
+            for (int d = 0; d < kHeadDim; d += 4) {
+                float4 qv[4], kv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    qv[i] = *reinterpret_cast<const float4*>(sm.q + (4 * ry + i) * kLd + d);
+                    kv[i] = *reinterpret_cast<const float4*>(sm.kv + (px + 16 * i) * kLd + d);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+                        s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+                        s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+                        s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                    }
+            }
+            // row 4 ry + i: its 64 scores are held by the 16 threads of half a warp
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * ry + i;
+                const int last = good ? w.s.L - w.s.T + T0 + (r >> 3) - p0 : -1;        // last visible position of the sub-tile
+                float top = -CUDART_INF_F;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int p = px + 16 * j;
+                    if (p > last || p >= valid) s[i][j] = -CUDART_INF_F;
+                    top = fmaxf(top, s[i][j]);
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float m0 = sm.m[r], m1 = fmaxf(m0, top);
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = expf(s[i][j] - m1);
+                    sum += p;
+                    sm.p[(px + 16 * j) * kLdP + r] = p;
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                __syncwarp();
+                if (px == 0) {
+                    const float f = expf(m0 - m1);
+                    sm.f[r] = f;
+                    sm.m[r] = m1;
+                    sm.l[r] = fmaf(sm.l[r], f, sum);
+                }
+            }
+            __syncthreads();
+            decode_sub(good ? unit + kBs8UnitBytes : nullptr, p0 % kPageSize, valid, sm.kv);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = sm.f[rows8 + i];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[i][j] *= f;
+            }
+#pragma unroll 4
+            for (int p = 0; p < kSub; ++p) {
+                const float4 p0v = *reinterpret_cast<const float4*>(sm.p + p * kLdP + rows8);
+                const float4 p1v = *reinterpret_cast<const float4*>(sm.p + p * kLdP + rows8 + 4);
+                const float4 v0 = *reinterpret_cast<const float4*>(sm.kv + p * kLd + 4 * lane);
+                const float4 v1 = *reinterpret_cast<const float4*>(sm.kv + p * kLd + 128 + 4 * lane);
+                const float pr[8] = {p0v.x, p0v.y, p0v.z, p0v.w, p1v.x, p1v.y, p1v.z, p1v.w};
+                const float vr[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[i][j] = fmaf(pr[i], vr[j], o[i][j]);
+            }
+        }
+        __syncthreads();
+        const bool whole = w.whole();
+        float* part = a.partials + ((size_t)blockIdx.x * 2 + w.part()) * kBs8PartFloats;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = rows8 + i;
+            if (r >= nrows) break;
+            const float l = sm.l[r], n = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+            const float4 lo = make_float4(o[i][0] * n, o[i][1] * n, o[i][2] * n, o[i][3] * n);
+            const float4 hi = make_float4(o[i][4] * n, o[i][5] * n, o[i][6] * n, o[i][7] * n);
+            if (whole) {
+                const int64_t at = ((q0 + (r >> 3)) * qheads + head * kGroup + (r & 7)) * kHeadDim + 4 * lane;
+                st4(a.out, at, a.dtype, lo);
+                st4(a.out, at + 128, a.dtype, hi);
+            } else {
+                *reinterpret_cast<float4*>(part + r * kHeadDim + 4 * lane) = lo;
+                *reinterpret_cast<float4*>(part + r * kHeadDim + 128 + 4 * lane) = hi;
+                if (lane == 0) *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * r) = make_float2(l != 0.0f ? sm.m[r] * 1.44269504f : -CUDART_INF_F, l);
+            }
+        }
+    } while (w.next(a));
+}
+
+// ---------------------------------------------------------------- merge
+// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partials of a cut pair; one CTA per row.
+constexpr int kMergeThreads = 256;
+
+__global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
+    __shared__ float4 s_o[kMergeThreads / 64][64];
+    __shared__ float s_l[kMergeThreads / 64], s_m[kMergeThreads / 32];
+    __shared__ int64_t s_at[2];                  // tiles before the slot, and of all slots
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = a.num_kv_heads;
+    const int slot = blockIdx.z, pair = blockIdx.y, r = blockIdx.x;
+    const Bs8Slot s = bs8_slot(a, slot, nullptr);
+    if (pair >= s.pairs(heads)) return;
+    const int T0 = pair / heads * (kBs8Rows / kGroup), head = pair % heads;
+    if (r >= min(kBs8Rows, kGroup * (s.T - T0))) return;
+    if (warp < 2) {
+        const int64_t n = bs8_tiles_before(a, warp == 0 ? slot : a.num_slots, nullptr);
+        if (lane == 0) s_at[warp] = n;
+    }
+    __syncthreads();
+    const int64_t total = s_at[1], begin = s_at[0] + (int64_t)pair * s.tiles;
+    const int c0 = bs8_cta_of(begin, total, a.ctas), c1 = bs8_cta_of(begin + s.tiles - 1, total, a.ctas);
+    if (c0 == c1) return;                        // the pair was not cut
+    const int n = c1 - c0 + 1;
+    auto part = [&](int i) { return a.partials + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kBs8PartFloats; };
+    float top = -CUDART_INF_F;
+    for (int i = tid; i < n; i += kMergeThreads) top = fmaxf(top, part(i)[kBs8Rows * kHeadDim + 2 * r]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (lane == 0) s_m[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMergeThreads / 32; ++i) top = fmaxf(top, s_m[i]);
+    if (top == -CUDART_INF_F) top = 0.0f;        // every partial is empty
+    const int col = tid & 63, group = tid >> 6;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+#pragma unroll 4
+    for (int i = group; i < n; i += kMergeThreads / 64) {
+        const float* p = part(i);
+        const float2 ml = *reinterpret_cast<const float2*>(p + kBs8Rows * kHeadDim + 2 * r);
+        const float4 v = *reinterpret_cast<const float4*>(p + r * kHeadDim + 4 * col);
+        const float f = exp2f(ml.x - top);
+        l = fmaf(f, ml.y, l);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+    }
+    s_o[group][col] = o;
+    if (col == 0) s_l[group] = l;
+    __syncthreads();
+    if (tid >= 64) return;
+    l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int g = 1; g < kMergeThreads / 64; ++g) {
+        const float4 v = s_o[g][col];
+        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+    }
+    const int64_t at = (((int64_t)a.q_offsets[slot] + T0 + (r >> 3)) * heads * kGroup + head * kGroup + (r & 7)) * kHeadDim + 4 * col;
+    st4(a.out, at, a.dtype, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+}
+
+template <typename K, typename A>
+cudaError_t launch(K kernel, const A& a, dim3 grid, int threads, size_t smem, cudaStream_t st) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// The merge's grid covers every pair that may be cut; a call whose pairs are all cut or whole alike has few idle CTAs.
+cudaError_t launch_merge_bs8(const Bs8Args& a, cudaStream_t st) {
+    const int chunks = (kGroup * a.max_n_q + kBs8Rows - 1) / kBs8Rows;
+    const dim3 grid((unsigned)(chunks > 1 ? kBs8Rows : kGroup * a.max_n_q), (unsigned)(chunks * a.num_kv_heads), (unsigned)a.num_slots);
+    return launch(merge_bs8_kernel, a, grid, kMergeThreads, 0, st);
+}
+
+int bs8_check(const q3kv_cache_desc* d, int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t impl) {
+    const int e = check_desc(d);
+    if (e != Q3KV_OK) return e;
+    if (num_slots < 0 || max_ctx_len < 0 || max_n_q < 0) return Q3KV_ERR_INVALID_ARG;
+    if (max_ctx_len > (int64_t)INT32_MAX - kPageSize) return Q3KV_ERR_INVALID_ARG;
+    if (impl < Q3KV_IMPL_AUTO || impl > Q3KV_IMPL_MMA) return Q3KV_ERR_INVALID_ARG;
+    if (num_slots > 65535 || max_n_q > kMaxNq) return Q3KV_ERR_UNSUPPORTED;
+    return Q3KV_OK;
+}
+
+size_t bs8_partials(int ctas) { return (size_t)ctas * 2 * kBs8PartFloats * sizeof(float); }
+
+}  // namespace
+
+cudaError_t launch_bs8_fma(const Bs8Args& a, cudaStream_t st) {
+    return launch(verify_bs8_fma_kernel, a, dim3((unsigned)a.ctas), kFmaThreads, sizeof(FmaSmem), st);
+}
+
+}  // namespace q3kv
+
+extern "C" {
+
+int q3kv_bs8_pool_bytes(const q3kv_cache_desc* desc, size_t* bytes) {
+    int e = q3kv::check_desc(desc);
+    if (e != Q3KV_OK) return e;
+    if (!bytes) return Q3KV_ERR_INVALID_ARG;
+    *bytes = (size_t)desc->num_pages * desc->num_layers * desc->num_kv_heads * 2 * q3kv::kBs8UnitBytes;
+    return Q3KV_OK;
+}
+
+int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_pool, const int32_t* d_page_table, int32_t max_pages_per_slot,
+                    const int32_t* d_slot_len, const int32_t* d_n_new, const int32_t* d_row_offsets, int32_t num_slots,
+                    int32_t max_n_new, int32_t layer, const void* k, const void* v, int32_t dtype, int32_t* d_status) {
+    using namespace q3kv;
+    int e = check_desc(desc);
+    if (e != Q3KV_OK) return e;
+    if (num_slots < 0 || max_n_new < 0 || max_pages_per_slot <= 0) return Q3KV_ERR_INVALID_ARG;
+    if (num_slots > 65535) return Q3KV_ERR_UNSUPPORTED;
+    if (layer < 0 || layer >= desc->num_layers) return Q3KV_ERR_INVALID_ARG;
+    if (dtype != Q3KV_F32 && dtype != Q3KV_BF16) return Q3KV_ERR_INVALID_ARG;
+    if (num_slots == 0 || max_n_new == 0) return Q3KV_OK;
+    if (!d_pool || !d_page_table || !d_slot_len || !d_n_new || !d_row_offsets || !k || !v) return Q3KV_ERR_INVALID_ARG;
+    if (!aligned16(d_pool) || !aligned16(k) || !aligned16(v)) return Q3KV_ERR_INVALID_ARG;
+    AppendArgs a{};
+    a.pool = static_cast<uint8_t*>(d_pool);
+    a.page_table = d_page_table;
+    a.max_pages_per_slot = max_pages_per_slot;
+    a.slot_len = d_slot_len;
+    a.n_new = d_n_new;
+    a.row_offsets = d_row_offsets;
+    a.num_slots = num_slots;
+    a.max_n_new = max_n_new;
+    a.num_layers = desc->num_layers;
+    a.num_kv_heads = desc->num_kv_heads;
+    a.num_pages = desc->num_pages;
+    a.layer = layer;
+    a.k = k;
+    a.v = v;
+    a.dtype = dtype;
+    a.status = d_status;
+    a.fmt = kFmtBs8;
+    // n rows from any place of a block touch at most (n - 1) / 16 + 2 blocks
+    const dim3 grid((unsigned)((max_n_new - 1) / kBs8Block + 2), (unsigned)num_slots, (unsigned)(2 * desc->num_kv_heads));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == Q3KV_F32 ? launch(append_bs8_kernel<float>, a, grid, kAppendThreads, 0, st)
+                                         : launch(append_bs8_kernel<__nv_bfloat16>, a, grid, kAppendThreads, 0, st));
+}
+
+int q3kv_bs8_workspace_bytes(const q3kv_cache_desc* desc, int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t impl,
+                             size_t* bytes) {
+    if (!bytes) return Q3KV_ERR_INVALID_ARG;
+    int ctas = 0, e = q3kv::bs8_check(desc, num_slots, max_ctx_len, max_n_q, impl);
+    if (e == Q3KV_OK) e = q3kv::device_sm_count(&ctas);
+    if (e == Q3KV_OK) *bytes = q3kv::bs8_partials(ctas);
+    return e;
+}
+
+int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* d_pool, const int32_t* d_page_table,
+                         int32_t max_pages_per_slot, const int32_t* d_ctx_len, const int32_t* d_n_q, const int32_t* d_q_offsets,
+                         int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t layer, const void* q, int32_t dtype,
+                         void* out, int32_t impl, void* d_workspace, size_t workspace_bytes, int32_t* d_status) {
+    using namespace q3kv;
+    if (max_pages_per_slot <= 0) return Q3KV_ERR_INVALID_ARG;
+    if (desc && (layer < 0 || layer >= desc->num_layers)) return Q3KV_ERR_INVALID_ARG;
+    if (dtype != Q3KV_F32 && dtype != Q3KV_BF16) return Q3KV_ERR_INVALID_ARG;
+    if (impl == Q3KV_IMPL_MMA) return Q3KV_ERR_UNSUPPORTED;
+    int e = bs8_check(desc, num_slots, max_ctx_len, max_n_q, impl);
+    if (e != Q3KV_OK) return e;
+    if (num_slots == 0 || max_n_q == 0 || max_ctx_len == 0) return Q3KV_OK;
+    if (!d_pool || !d_page_table || !d_ctx_len || !d_n_q || !d_q_offsets || !q || !out) return Q3KV_ERR_INVALID_ARG;
+    if (!aligned16(d_pool) || !aligned16(q) || !aligned16(out) || !aligned16(d_workspace)) return Q3KV_ERR_INVALID_ARG;
+    if (!d_workspace) return Q3KV_ERR_WORKSPACE_TOO_SMALL;
+    int ctas = 0;
+    e = device_sm_count(&ctas);
+    if (e != Q3KV_OK) return e;
+    if (workspace_bytes < bs8_partials(ctas)) return Q3KV_ERR_WORKSPACE_TOO_SMALL;
+    Bs8Args a{};
+    a.pool = static_cast<const uint8_t*>(d_pool);
+    a.page_table = d_page_table;
+    a.max_pages_per_slot = max_pages_per_slot;
+    a.ctx_len = d_ctx_len;
+    a.n_q = d_n_q;
+    a.q_offsets = d_q_offsets;
+    a.num_slots = num_slots;
+    a.max_ctx_len = max_ctx_len;
+    a.max_n_q = max_n_q;
+    a.num_layers = desc->num_layers;
+    a.num_kv_heads = desc->num_kv_heads;
+    a.num_pages = desc->num_pages;
+    a.layer = layer;
+    a.q = q;
+    a.out = out;
+    a.dtype = dtype;
+    a.ctas = ctas;
+    a.partials = static_cast<float*>(d_workspace);
+    a.status = d_status;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t ce = launch_bs8_fma(a, st);
+    if (ce == cudaSuccess) ce = launch_merge_bs8(a, st);
+    return cuda_status(ce);
+}
+
+}  // extern "C"

@@ -127,7 +127,29 @@ struct q3kv_allocator {
     int32_t max_pages_per_slot;
     std::vector<int32_t> free_list;              // stack; back() is handed out next
     std::vector<std::vector<int32_t>> owned;     // per-slot page ids in position order
+    std::vector<int32_t> refs;                   // slots that hold each page
 };
+
+namespace {
+
+int slot_row(const q3kv_allocator* a, int32_t slot, int32_t* row, int32_t* n_pages) {
+    const std::vector<int32_t>& mine = a->owned[slot];
+    for (int32_t i = 0; i < a->max_pages_per_slot; ++i) row[i] = (i < (int32_t)mine.size()) ? mine[i] : -1;
+    if (n_pages) *n_pages = (int32_t)mine.size();
+    return Q3KV_OK;
+}
+int32_t take_page(q3kv_allocator* a) {
+    const int32_t page = a->free_list.back();
+    a->free_list.pop_back();
+    a->refs[page] = 1;
+    return page;
+}
+// The free list's capacity is num_pages, so nothing is allocated.
+void drop_page(q3kv_allocator* a, int32_t page) {
+    if (--a->refs[page] == 0) a->free_list.push_back(page);
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -173,6 +195,7 @@ int q3kv_allocator_create(int32_t num_pages, int32_t num_slots, int32_t max_page
         a->free_list.resize(num_pages);
         for (int32_t i = 0; i < num_pages; ++i) a->free_list[i] = num_pages - 1 - i;   // page 0 first
         a->owned.resize(num_slots);
+        a->refs.resize(num_pages, 0);
         *out = a.release();
     } catch (...) {
         return Q3KV_ERR_HOST_MEMORY;
@@ -198,22 +221,115 @@ int q3kv_alloc_pages(q3kv_allocator* a, int32_t slot, int64_t n_positions, int32
             return Q3KV_ERR_HOST_MEMORY;
         }
     }
-    for (int64_t i = 0; i < extra; ++i) {
-        mine.push_back(a->free_list.back());
-        a->free_list.pop_back();
-    }
-    for (int32_t i = 0; i < a->max_pages_per_slot; ++i)
-        h_page_table_row[i] = (i < (int32_t)mine.size()) ? mine[i] : -1;
-    if (n_pages_out) *n_pages_out = (int32_t)mine.size();
-    return Q3KV_OK;
+    for (int64_t i = 0; i < extra; ++i) mine.push_back(take_page(a));
+    return slot_row(a, slot, h_page_table_row, n_pages_out);
 }
 
 int q3kv_free_slot(q3kv_allocator* a, int32_t slot) {
     if (!a) return Q3KV_ERR_INVALID_ARG;
     if (slot < 0 || slot >= a->num_slots) return Q3KV_ERR_SLOT_RANGE;
     std::vector<int32_t>& mine = a->owned[slot];
-    for (auto it = mine.rbegin(); it != mine.rend(); ++it) a->free_list.push_back(*it);
+    for (auto it = mine.rbegin(); it != mine.rend(); ++it) drop_page(a, *it);
     mine.clear();
+    return Q3KV_OK;
+}
+
+int q3kv_slot_pages(const q3kv_allocator* a, int32_t slot, int32_t* h_page_table_row, int32_t* n_pages_out) {
+    if (!a || !h_page_table_row) return Q3KV_ERR_INVALID_ARG;
+    if (slot < 0 || slot >= a->num_slots) return Q3KV_ERR_SLOT_RANGE;
+    return slot_row(a, slot, h_page_table_row, n_pages_out);
+}
+
+int q3kv_fork_slot(q3kv_allocator* a, int32_t src_slot, int32_t dst_slot, int64_t n_positions, int32_t* h_page_table_row,
+                   int32_t* n_pages_out) {
+    if (!a || !h_page_table_row || n_positions < 0 || src_slot == dst_slot) return Q3KV_ERR_INVALID_ARG;
+    if (src_slot < 0 || src_slot >= a->num_slots || dst_slot < 0 || dst_slot >= a->num_slots) return Q3KV_ERR_SLOT_RANGE;
+    const std::vector<int32_t>& from = a->owned[src_slot];
+    std::vector<int32_t>& to = a->owned[dst_slot];
+    const int64_t need = n_positions / kPageSize + (n_positions % kPageSize != 0);
+    if (need > (int64_t)from.size() || !to.empty()) return Q3KV_ERR_INVALID_ARG;
+    try {
+        to.assign(from.begin(), from.begin() + need);
+    } catch (...) {
+        return Q3KV_ERR_HOST_MEMORY;
+    }
+    for (int32_t page : to) ++a->refs[page];
+    return slot_row(a, dst_slot, h_page_table_row, n_pages_out);
+}
+
+int q3kv_write_pages(q3kv_allocator* a, int32_t slot, int64_t first_position, int64_t n_positions, int32_t* h_page_table_row,
+                     int32_t* n_pages_out, int32_t* h_copy) {
+    if (!a || !h_page_table_row || !h_copy || first_position < 0 || n_positions < 0) return Q3KV_ERR_INVALID_ARG;
+    if (slot < 0 || slot >= a->num_slots) return Q3KV_ERR_SLOT_RANGE;
+    const int64_t room = (int64_t)a->max_pages_per_slot * kPageSize;
+    if (first_position > room || n_positions > room - first_position) return Q3KV_ERR_OUT_OF_PAGES;
+    std::vector<int32_t>& mine = a->owned[slot];
+    const int64_t have = (int64_t)mine.size(), begin = first_position / kPageSize;
+    // an empty range asks for nothing
+    const int64_t end = n_positions ? (first_position + n_positions + kPageSize - 1) / kPageSize : 0;
+    int64_t fresh = std::max<int64_t>(0, end - have);
+    for (int64_t i = begin; i < std::min(end, have); ++i) fresh += a->refs[mine[i]] > 1;
+    if (fresh > (int64_t)a->free_list.size()) return Q3KV_ERR_OUT_OF_PAGES;
+    try {
+        if (end > have) mine.reserve((size_t)end);
+    } catch (...) {
+        return Q3KV_ERR_HOST_MEMORY;
+    }
+    h_copy[0] = h_copy[1] = -1;
+    h_copy[2] = 0;
+    for (int64_t i = begin; i < std::min(end, have); ++i) {
+        const int32_t old = mine[i];
+        if (a->refs[old] <= 1) continue;
+        mine[i] = take_page(a);
+        drop_page(a, old);                       // another slot holds it still
+        // only the page that the range begins inside holds positions that stay
+        if (i == begin && first_position % kPageSize) {
+            h_copy[0] = old;
+            h_copy[1] = mine[i];
+            h_copy[2] = (int32_t)(first_position % kPageSize);
+        }
+    }
+    while ((int64_t)mine.size() < end) mine.push_back(take_page(a));
+    return slot_row(a, slot, h_page_table_row, n_pages_out);
+}
+
+int q3kv_trim_slot(q3kv_allocator* a, int32_t slot, int64_t n_positions, int32_t* h_page_table_row, int32_t* n_pages_out) {
+    if (!a || !h_page_table_row || n_positions < 0) return Q3KV_ERR_INVALID_ARG;
+    if (slot < 0 || slot >= a->num_slots) return Q3KV_ERR_SLOT_RANGE;
+    std::vector<int32_t>& mine = a->owned[slot];
+    const int64_t keep = n_positions / kPageSize + (n_positions % kPageSize != 0);
+    while ((int64_t)mine.size() > keep) {
+        drop_page(a, mine.back());
+        mine.pop_back();
+    }
+    return slot_row(a, slot, h_page_table_row, n_pages_out);
+}
+
+int q3kv_compact_pages(q3kv_allocator* a, int32_t max_moves, int32_t* h_src, int32_t* h_dst, int32_t* n_moves_out) {
+    if (!a || max_moves < 0 || !n_moves_out || (max_moves > 0 && (!h_src || !h_dst))) return Q3KV_ERR_INVALID_ARG;
+    std::vector<int32_t> to;
+    try {
+        to.resize(a->num_pages);
+    } catch (...) {
+        return Q3KV_ERR_HOST_MEMORY;
+    }
+    for (int32_t i = 0; i < a->num_pages; ++i) to[i] = i;
+    int32_t n = 0;
+    for (int32_t hole = 0, last = a->num_pages - 1; n < max_moves; ++n) {
+        while (hole < last && a->refs[hole] > 0) ++hole;
+        while (hole < last && a->refs[last] == 0) --last;
+        if (hole >= last) break;
+        to[last] = hole;
+        std::swap(a->refs[hole], a->refs[last]);
+        h_src[n] = last;
+        h_dst[n] = hole;
+    }
+    for (std::vector<int32_t>& pages : a->owned)
+        for (int32_t& page : pages) page = to[page];
+    a->free_list.clear();
+    for (int32_t i = a->num_pages - 1; i >= 0; --i)
+        if (a->refs[i] == 0) a->free_list.push_back(i);
+    *n_moves_out = n;
     return Q3KV_OK;
 }
 

@@ -25,6 +25,19 @@ constexpr int kFp8RecordBytes = 256;  // fp8 E4M3 comparison format: one byte pe
 constexpr int kFmtQ3 = 0;
 constexpr int kFmtFp8 = 1;
 constexpr int kFmtT5k = 2;
+constexpr int kFmtBs8 = 3;
+
+// Block-scaled 8-bit layout: per (page, layer, kv head, K|V) a unit of 256 x 256 E4M3 codes, then 16 float32
+// scales (powers of two), one per block of 16 positions.  Codes lie in cores of 8 positions x 16 dims, 128
+// bytes each, which are tensor-core operand tiles as they stand: the code of (row, dim) is byte
+// ((row / 8) * 16 + dim / 16) * 128 + (row % 8) * 16 + dim % 16.
+constexpr int kBs8Block = 16;
+constexpr int kBs8CodeBytes = kPageSize * kHeadDim;
+constexpr int kBs8UnitBytes = kBs8CodeBytes + 4 * (kPageSize / kBs8Block);
+constexpr int kBs8MaxExp = 64;       // scales are 2^-64 .. 2^64
+__host__ __device__ inline size_t bs8_offset(int num_layers, int num_kv_heads, int64_t page, int layer, int kv_head, int kv) {
+    return (size_t)(((page * num_layers + layer) * num_kv_heads + kv_head) * 2 + kv) * kBs8UnitBytes;
+}
 
 // turbo5k layout: per (page, layer, kv head) 256 K records of 164 bytes
 // (128 bytes of low code nibbles, 32 bytes of 5th code bits, 2 fp16 scales)
