@@ -513,7 +513,7 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     if (max_pages_per_slot <= 0) return Q3KV_ERR_INVALID_ARG;
     if (desc && (layer < 0 || layer >= desc->num_layers)) return Q3KV_ERR_INVALID_ARG;
     if (dtype != Q3KV_F32 && dtype != Q3KV_BF16) return Q3KV_ERR_INVALID_ARG;
-    if (impl == Q3KV_IMPL_MMA) return Q3KV_ERR_UNSUPPORTED;
+    if (impl == Q3KV_IMPL_MMA && dtype == Q3KV_F32) return Q3KV_ERR_UNSUPPORTED;
     int e = bs8_check(desc, num_slots, max_ctx_len, max_n_q, impl);
     if (e != Q3KV_OK) return e;
     if (num_slots == 0 || max_n_q == 0 || max_ctx_len == 0) return Q3KV_OK;
@@ -545,7 +545,8 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     a.partials = static_cast<float*>(d_workspace);
     a.status = d_status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t ce = launch_bs8_fma(a, st);
+    const bool mma = impl == Q3KV_IMPL_MMA || (impl == Q3KV_IMPL_AUTO && dtype == Q3KV_BF16);
+    cudaError_t ce = mma ? launch_bs8_mma(a, st) : launch_bs8_fma(a, st);
     if (ce == cudaSuccess) ce = launch_merge_bs8(a, st);
     return cuda_status(ce);
 }

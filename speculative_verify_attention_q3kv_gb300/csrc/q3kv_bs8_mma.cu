@@ -1,0 +1,569 @@
+// Verify attention over the block-scaled 8-bit cache, tensor-core leg (bf16 queries and outputs).
+//
+// The cache's codes are the MMAs' operands as they lie in memory: a page stores them in the 8 x 16-byte cores that
+// tcgen05.mma reads, so a tile of 128 positions is one bulk copy of 32 KiB for K and one for V, and nothing is
+// decoded.  What the other operands lose in 8 bits is carried by more than one code per value:
+//   q  = 2^-k (q1 + q2)      two E4M3 codes, k per row: a bf16 value has 8 significant bits, two codes hold them all;
+//                            what is below 2^-18 of the row's largest value is rounded away
+//   p' = p1 + p2 + p3        three E5M2 codes (3 significant bits each) of the weight as fp16, relative error about 2^-11,
+//                            less than rounding the weight to bf16 would cost; E5M2 for its range (2^-16 .. 2^15):
+//                            a long context's many small weights stay above it next to a large one
+// Contractions (M = 128, float32 accumulation in TMEM):
+//   S^T[p][r | R + r] = K[p][:] . q1[r][:] | q2[r][:]   A = K codes (K-major), N = 2 R columns, K = 256 dims
+//   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions
+// with R = 16, 32 or 64 query rows (8 heads x tokens, padded).  A position is a TMEM lane, so its block's scales are two
+// numbers of one thread: the score is (S1 + S2) 2^(eK - k) log2(e) / 16, and V's scale goes into the weight's
+// exponent, p' = 2^(score + eV - m), while the row sum takes p' 2^-eV.  m is raised only when a score passes it by more
+// than 2^7 of headroom (a vote per tile), so most tiles need no maximum and no rescaling.
+//
+// Bound: the codes' bytes.  At 8 tokens a tile's 64 KiB take about 2,900 cycles of an SM's share of HBM, its 32 MMAs about
+// 1,700 and its softmax less.  One CTA per SM; warp 0 copies, warp 1 issues the MMAs, warps 2-9 are the softmax (thread =
+// position; warps 2-5 the first half of the rows, 6-9 the second).
+#include <math_constants.h>
+
+#include "q3kv_bs8.cuh"
+#include "q3kv_tcgen05.cuh"
+
+namespace q3kv {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kSoftmax = 256;                  // threads of warps 2-9
+constexpr uint32_t kTileBytes = kBs8Tile * kHeadDim;
+constexpr float kAbove = 8.0f;                 // m is set this far below the largest score: p' <= 2^8 then,
+constexpr float kRaise = 15.0f;                // and at most 2^15 until it is raised
+constexpr int kMeta = 8;                       // tiles whose scales are kept
+
+template <int R>
+struct Cfg {
+    static constexpr int kStages = R == 64 ? 4 : R == 32 ? 5 : 6;
+    static constexpr int kH = R / 2;                                   // rows per softmax thread
+    static constexpr uint32_t kS = 2 * R, kO = 4 * R;                  // TMEM columns: S buffers of 2 R, then O halves of R
+    static constexpr uint32_t kTmem = R == 64 ? 512 : R == 32 ? 256 : 128;
+};
+
+template <int R>
+struct Smem {
+    alignas(128) uint8_t kv[Cfg<R>::kStages][kTileBytes];
+    alignas(128) uint8_t q[2 * R * kHeadDim];
+    alignas(128) uint8_t p[2][3][R * kBs8Tile];
+    alignas(16) float meta[kMeta][16];         // K scales of a tile's 8 blocks, then V scales
+    alignas(16) float rs[R];                   // 2^-k of each row
+    float red[2][4][R / 2];
+    Bs8Share first;
+    int bad_page[kMeta];
+    uint32_t tmem;
+    volatile int abort;
+    unsigned long long full[Cfg<R>::kStages], empty[Cfg<R>::kStages], s_full[2], s_free[2], p_full[2], p_free[2], q_full, drained, meta_full[kMeta];
+};
+
+// Instruction descriptor, kind::f8f6f4: E4M3 A, E4M3 or E5M2 B, fp32 D, M = 128.
+__host__ __device__ constexpr uint32_t idesc8(int n, bool mn_major, bool b_e5m2) {
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((mn_major ? 1u : 0u) << 15) | ((mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t at, float* v) {
+    if constexpr (N == 8) {
+        float t[8];
+        tmem_ld8(at, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = t[i];
+    } else if constexpr (N == 16) {
+        tmem_ld16(at, v);
+    } else {
+        tmem_ld32(at, v);
+    }
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t at, const float* v) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[i + j]);
+        tmem_st8(at + i, r);
+    }
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// fp16 pair -> the pair rounded to E5M2 (the upper byte of fp16; ties away from zero), as fp16
+__device__ __forceinline__ uint32_t e5m2_of(uint32_t h) { return (h + 0x00800080u) & 0xff00ff00u; }
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return as_u32(__hsub2(as_h2(a), as_h2(b))); }
+
+// ---------------------------------------------------------------- roles
+// Bulk copies of a segment's tiles in the order of their use: K0 K1 V0 K2 V1 ... V(n-2) V(n-1).
+template <int R>
+__device__ void produce(const Bs8Args& a, Smem<R>& sm, Bs8Share w) {
+    const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
+    uint32_t cnt = 0, it = 0, issued = 0, metas = 0;
+    bool ok = true;
+    do {
+        const int32_t* table = a.page_table + (int64_t)w.slot * a.max_pages_per_slot;
+        const int last_page = (w.tile + w.tiles - 1) >> 1;
+        int window = (w.tile >> 1) - 32, ids = 0;
+        const uint8_t* prev = nullptr;
+        uint32_t prev_half = 0;
+        for (int i = 0; i <= w.tiles && ok; ++i) {
+            const int tile = w.tile + i;
+            const uint8_t* unit = nullptr;
+            if (i < w.tiles) {
+                const int pg = tile >> 1;
+                if (pg >= window + 32) {
+                    window = pg;
+                    ids = window + lane <= last_page ? table[window + lane] : 0;
+                }
+                int id = __shfl_sync(0xffffffffu, ids, pg - window);
+                const bool bad = id < 0 || id >= a.num_pages;      // the tile counts as hidden; page 0 stands in for its bytes
+                if (bad) id = 0;
+                unit = a.pool + bs8_offset(a.num_layers, heads, id, a.layer, w.head(heads), 0);
+                if (lane == 0) {
+                    const uint32_t st = cnt % Cfg<R>::kStages, half = tile & 1, slot = (it + i) % kMeta;
+                    ok = cnt < Cfg<R>::kStages || mbar_wait(&sm.empty[st], (cnt / Cfg<R>::kStages + 1) & 1, &sm.abort);
+                    if (ok) {
+                        if (bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+                        sm.bad_page[slot] = bad;
+                        mbar_arrive_expect_tx(&sm.meta_full[slot], 64);
+                        bulk_g2s(&sm.meta[slot][0], unit + kBs8CodeBytes + half * 32, 32, &sm.meta_full[slot]);
+                        bulk_g2s(&sm.meta[slot][8], unit + kBs8UnitBytes + kBs8CodeBytes + half * 32, 32, &sm.meta_full[slot]);
+                        mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
+                        bulk_g2s(sm.kv[st], unit + half * kTileBytes, kTileBytes, &sm.full[st]);
+                        issued = cnt + 1;
+                        metas = it + i + 1;
+                    }
+                }
+                ++cnt;
+            }
+            if (i > 0) {
+                if (lane == 0 && ok) {
+                    const uint32_t st = cnt % Cfg<R>::kStages;
+                    ok = cnt < Cfg<R>::kStages || mbar_wait(&sm.empty[st], (cnt / Cfg<R>::kStages + 1) & 1, &sm.abort);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
+                        bulk_g2s(sm.kv[st], prev + kBs8UnitBytes + prev_half * kTileBytes, kTileBytes, &sm.full[st]);
+                        issued = cnt + 1;
+                    }
+                }
+                ++cnt;
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            prev = unit;
+            prev_half = tile & 1;
+        }
+        it += w.tiles;
+    } while (ok && w.next(a));
+    // no copy may land after the CTA is gone, whatever stopped the others
+    if (lane == 0) {
+        for (uint32_t c = issued > Cfg<R>::kStages ? issued - Cfg<R>::kStages : 0; c < issued; ++c)
+            mbar_drain(&sm.full[c % Cfg<R>::kStages], (c / Cfg<R>::kStages) & 1);
+        for (uint32_t t = metas > kMeta ? metas - kMeta : 0; t < metas; ++t) mbar_drain(&sm.meta_full[t % kMeta], (t / kMeta) & 1);
+    }
+    __syncwarp();
+}
+
+// MMAs, by one thread.  Within a segment QK of the next tile goes before PV of this one, so the tensor pipe works while
+// the softmax does.
+template <int R>
+__device__ void issue(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
+    using C = Cfg<R>;
+    const uint32_t id_qk = idesc8(2 * R, false, false), id_pv = idesc8(R, true, true);
+    const uint64_t kdesc = make_desc(smem_u32(sm.kv[0]), 128, 2048), vdesc = make_desc(smem_u32(sm.kv[0]), 2048, 128);
+    const uint64_t qdesc = make_desc(smem_u32(sm.q), 128, 2048), pdesc = make_desc(smem_u32(sm.p[0][0]), R / 16 * 128, 128);
+    uint32_t cnt = 0, it = 0, seg = 0;
+    bool ok = true;
+    do {
+        for (int i = 0; i <= w.tiles && ok; ++i) {
+            if (i < w.tiles) {                                     // QK of tile i
+                const uint32_t t = it + i, b = t & 1, st = cnt % C::kStages;
+                if (i == 0) ok = mbar_wait(&sm.q_full, seg & 1, &sm.abort);
+                ok = ok && mbar_wait(&sm.full[st], (cnt / C::kStages) & 1, &sm.abort);
+                if (t >= 2) ok = ok && mbar_wait(&sm.s_free[b], ((t >> 1) + 1) & 1, &sm.abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ad = kdesc + st * (kTileBytes / 16);
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 32; ++k) mma8(tmem + b * C::kS, ad + k * 16, qdesc + k * 16, id_qk, k > 0);
+                mma_commit(&sm.empty[st]);
+                mma_commit(&sm.s_full[b]);
+                ++cnt;
+            }
+            if (i > 0) {                                           // PV of tile i - 1
+                const uint32_t t = it + i - 1, b = t & 1, st = cnt % C::kStages;
+                ok = mbar_wait(&sm.full[st], (cnt / C::kStages) & 1, &sm.abort) && mbar_wait(&sm.p_full[b], (t >> 1) & 1, &sm.abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ad = vdesc + st * (kTileBytes / 16), bd = pdesc + b * (3 * R * kBs8Tile / 16);
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int k = 0; k < kBs8Tile / 32; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            mma8(tmem + C::kO + h * R, ad + k * (8192 / 16) + h * (1024 / 16),
+                                 bd + part * (R * kBs8Tile / 16) + k * (4 * (R / 16) * 128 / 16), id_pv, i > 1 || part > 0 || k > 0);
+                mma_commit(&sm.empty[st]);
+                mma_commit(&sm.p_free[b]);
+                ++cnt;
+            }
+        }
+        it += w.tiles;
+        ++seg;
+    } while (ok && w.next(a));
+    mma_commit(&sm.drained);               // TMEM and the operands stay until the last MMA is done
+    mbar_drain(&sm.drained, 0);
+}
+
+// The queries of a segment as two E4M3 codes per value; a row that is not finite gets a NaN scale and comes out as NaN.
+template <int R>
+__device__ void prepare_q(const Bs8Args& a, Smem<R>& sm, const Bs8Share& w, int warp) {
+    const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
+    const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+    const int64_t q0 = (int64_t)a.q_offsets[w.slot] + T0;
+#pragma unroll 2
+    for (int r = warp; r < R; r += kSoftmax / 32) {
+        float x[8] = {};
+        if (r < nrows) load8(q + ((q0 + (r >> 3)) * heads * kGroup + w.head(heads) * kGroup + (r & 7)) * kHeadDim + 8 * lane, x);
+        float top = 0.0f;
+        bool finite = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            top = fmaxf(top, fabsf(x[i]));
+            finite = finite && fabsf(x[i]) <= 3.402823466e38f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        finite = __all_sync(0xffffffffu, finite);
+        // largest value to 128 .. 256
+        const int k = top > 0.0f && finite ? min(100, 7 - ((int)(__float_as_uint(top) >> 23) - 127)) : 0;
+        const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+        uint32_t c1[2], c2[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float y[4], d[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = x[4 * i + j] * up;
+            c1[i] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
+            uint32_t h01, h23;
+            e4m3x4_to_f16(c1[i], h01, h23);
+            const float2 f01 = __half22float2(as_h2(h01)), f23 = __half22float2(as_h2(h23));
+            d[0] = y[0] - f01.x; d[1] = y[1] - f01.y; d[2] = y[2] - f23.x; d[3] = y[3] - f23.y;
+            c2[i] = e4m3_pair(d[0], d[1]) | (e4m3_pair(d[2], d[3]) << 16);
+        }
+        uint8_t* to = sm.q + ((r >> 3) * 16 + (lane >> 1)) * 128 + (r & 7) * 16 + (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(to) = make_uint2(c1[0], c1[1]);
+        *reinterpret_cast<uint2*>(to + R * kHeadDim) = make_uint2(c2[0], c2[1]);
+        if (lane == 0) sm.rs[r] = finite ? __uint_as_float((uint32_t)(127 - k) << 23) : __int_as_float(0x7fc00000);
+    }
+}
+
+__device__ __forceinline__ int ordered(float f) {          // integers in the order of the floats
+    const int i = __float_as_int(f);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+template <int R>
+__device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
+    using C = Cfg<R>;
+    constexpr int H = C::kH;
+    const int tid = threadIdx.x - 64, lane = threadIdx.x & 31, warp = tid >> 5, heads = a.num_kv_heads;
+    const int wg = warp >> 2, quarter = (threadIdx.x >> 5) & 3;      // rows wg H .., positions 32 quarter ..: a warp reads its own TMEM lanes
+    const int p = quarter * 32 + lane, r0 = wg * H, bar = 1 + wg;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    uint32_t it = 0, vcnt = 0;             // vcnt: copies before this segment's
+    bool ok = true;
+    do {
+        const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
+        prepare_q<R>(a, sm, w, warp);
+        fence_proxy_async();
+        mbar_arrive(&sm.q_full);
+        named_sync(3, kSoftmax);           // rs is there
+        float m[H], l[H];
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+            m[c] = 0.0f;
+            l[c] = 0.0f;
+        }
+        for (int i = 0; i < w.tiles; ++i, ++it) {
+            const uint32_t b = it & 1, slot = it % kMeta;
+            const int p0 = (w.tile + i) * kBs8Tile;
+            ok = ok && mbar_wait_fast(&sm.meta_full[slot], (it / kMeta) & 1, &sm.abort);
+            const float ks = sm.meta[slot][p >> 4] * (1.44269504f / 16.0f), vs = sm.meta[slot][8 + (p >> 4)];
+            const int ev = min(kBs8MaxExp, max(-kBs8MaxExp, (int)((__float_as_uint(vs) >> 23) & 0xff) - 127));   // a block behind the context may hold anything
+            const bool hidden = sm.bad_page[slot] != 0;
+            ok = ok && mbar_wait_fast(&sm.s_full[b], (it >> 1) & 1, &sm.abort);
+            __syncwarp();
+            tc_fence_after();
+            float d[H];
+            constexpr int kHalf = H == 32 ? 16 : H;      // the second code's scores come in halves: registers
+            {
+                float s2[kHalf];
+                tmem_load<H>(lanes + b * C::kS + r0, d);
+#pragma unroll
+                for (int g = 0; g < H; g += kHalf) {
+                    tmem_load<kHalf>(lanes + b * C::kS + R + r0 + g, s2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) d[g + c] += s2[c];
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&sm.s_free[b]);
+            float top = -CUDART_INF_F;
+#pragma unroll
+            for (int c = 0; c < H; c += 4) {
+                const float4 rs = *reinterpret_cast<const float4*>(&sm.rs[r0 + c]);
+                d[c] = fmaf(d[c] * rs.x, ks, (float)ev - m[c]);
+                d[c + 1] = fmaf(d[c + 1] * rs.y, ks, (float)ev - m[c + 1]);
+                d[c + 2] = fmaf(d[c + 2] * rs.z, ks, (float)ev - m[c + 2]);
+                d[c + 3] = fmaf(d[c + 3] * rs.w, ks, (float)ev - m[c + 3]);
+            }
+            const bool tail = hidden || p0 + kBs8Tile > w.s.L - w.s.T + T0 + 1;
+            if (tail) {
+                // row r sees positions up to L - T + its token
+                const int ahead = hidden ? (1 << 20) : p0 + p - (w.s.L - w.s.T + T0);
+#pragma unroll
+                for (int c = 0; c < H; ++c)
+                    if (ahead > ((r0 + c) >> 3) || p0 + p >= w.s.L) d[c] = -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int c = 0; c < H; ++c) top = fmaxf(top, d[c]);
+            if (named_or(bar, 128, i == 0 || top > kRaise || !ok)) {
+                if (named_or(bar, 128, !ok)) {
+                    ok = false;
+                    break;
+                }
+                // new maxima of the rows over the tile's positions
+#pragma unroll
+                for (int c = 0; c < H; ++c) {
+                    const int x = __reduce_max_sync(0xffffffffu, ordered(d[c] + m[c]));
+                    if (lane == 0) sm.red[wg][quarter][c] = unordered(x);
+                }
+                named_sync(bar, 128);
+                float f[H];
+#pragma unroll
+                for (int c = 0; c < H; ++c) {
+                    const float x = fmaxf(fmaxf(sm.red[wg][0][c], sm.red[wg][1][c]), fmaxf(sm.red[wg][2][c], sm.red[wg][3][c]));
+                    // the first tile sets m; a row that sees nothing of it sees nothing of the segment's later tiles either
+                    const float now = i > 0 ? fmaxf(m[c], x - kAbove) : x > -CUDART_INF_F ? x - kAbove : 0.0f;
+                    f[c] = fast_exp2(m[c] - now);
+                    d[c] += m[c] - now;
+                    l[c] *= f[c];
+                    m[c] = now;
+                }
+                if (i > 0) {
+                    ok = mbar_wait_fast(&sm.p_free[b ^ 1], ((it - 1) >> 1) & 1, &sm.abort);      // PV of the tile before, and all earlier ones
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int g = 0; g < H; g += 8) {
+                            float o[8];
+                            tmem_load<8>(lanes + C::kO + h * R + r0 + g, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) o[c] *= f[g + c];
+                            tmem_store<8>(lanes + C::kO + h * R + r0 + g, o);
+                        }
+                    tmem_st_wait();
+                }
+            }
+            const float iv = __uint_as_float((uint32_t)(127 - ev) << 23);       // 2^-eV
+#pragma unroll
+            for (int c = 0; c < H; ++c) {
+                d[c] = fast_exp2(d[c]);
+                l[c] = fmaf(d[c], iv, l[c]);
+            }
+            if (it >= 2) ok = ok && mbar_wait_fast(&sm.p_free[b], ((it >> 1) + 1) & 1, &sm.abort);
+            uint32_t w1[H / 4], w2[H / 4], w3[H / 4];
+#pragma unroll
+            for (int c = 0; c < H / 4; ++c) {
+                const uint32_t a0 = f16_pair(d[4 * c], d[4 * c + 1]), b0 = f16_pair(d[4 * c + 2], d[4 * c + 3]);
+                const uint32_t a1 = e5m2_of(a0), b1 = e5m2_of(b0), ar = sub2(a0, a1), br = sub2(b0, b1);
+                const uint32_t a2 = e5m2_of(ar), b2 = e5m2_of(br);
+                const uint32_t a3 = sub2(ar, a2) + 0x00800080u, b3 = sub2(br, b2) + 0x00800080u;
+                w1[c] = __byte_perm(a1, b1, 0x7531);
+                w2[c] = __byte_perm(a2, b2, 0x7531);
+                w3[c] = __byte_perm(a3, b3, 0x7531);
+            }
+            uint8_t* to = sm.p[b][0] + ((p >> 3) * (R / 16) + r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
+            if constexpr (H == 8) {
+                *reinterpret_cast<uint2*>(to) = make_uint2(w1[0], w1[1]);
+                *reinterpret_cast<uint2*>(to + R * kBs8Tile) = make_uint2(w2[0], w2[1]);
+                *reinterpret_cast<uint2*>(to + 2 * R * kBs8Tile) = make_uint2(w3[0], w3[1]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < H / 16; ++c) {
+                    *reinterpret_cast<uint4*>(to + 128 * c) = make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]);
+                    *reinterpret_cast<uint4*>(to + 128 * c + R * kBs8Tile) = make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]);
+                    *reinterpret_cast<uint4*>(to + 128 * c + 2 * R * kBs8Tile) = make_uint4(w3[4 * c], w3[4 * c + 1], w3[4 * c + 2], w3[4 * c + 3]);
+                }
+            }
+            const int valid = hidden ? 0 : w.s.L - p0;
+            if (valid < kBs8Tile) {
+                // rows behind the context may hold anything, and 0 x NaN is NaN: they become zeros before PV reads them
+                const uint32_t at = vcnt + (i + 1 < w.tiles ? 2 * i + 2 : 2 * i + 1), st = at % C::kStages;
+                ok = ok && mbar_wait_fast(&sm.full[st], (at / C::kStages) & 1, &sm.abort);
+                if (p >= valid) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4*>(sm.kv[st] + ((p >> 3) * 16 + wg * 8 + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            mbar_arrive(&sm.p_full[b]);
+        }
+        vcnt += 2 * w.tiles;
+        ok = ok && mbar_wait_fast(&sm.p_free[(it - 1) & 1], ((it - 1) >> 1) & 1, &sm.abort);
+        if (named_or(3, kSoftmax, !ok)) {      // all eight warps leave together
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        // row sums over the positions
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+            if (lane == 0) sm.red[wg][quarter][c] = l[c];
+        }
+        named_sync(bar, 128);
+#pragma unroll
+        for (int c = 0; c < H; ++c) l[c] = (sm.red[wg][0][c] + sm.red[wg][1][c]) + (sm.red[wg][2][c] + sm.red[wg][3][c]);
+        const bool whole = w.whole();
+        float* part = a.partials + ((size_t)blockIdx.x * 2 + w.part()) * kBs8PartFloats;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+        const int64_t q0 = (int64_t)a.q_offsets[w.slot] + T0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float o[H];
+            tmem_load<H>(lanes + C::kO + h * R + r0, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < H; ++c) {
+                const int r = r0 + c, dim = h * 128 + p;
+                if (r >= nrows) continue;
+                if (whole)
+                    out[((q0 + (r >> 3)) * heads * kGroup + w.head(heads) * kGroup + (r & 7)) * kHeadDim + dim] =
+                        __float2bfloat16_rn(l[c] != 0.0f ? __fdividef(o[c], l[c]) : 0.0f);
+                else
+                    part[r * kHeadDim + dim] = o[c];
+            }
+        }
+        if (!whole && p < H && r0 + p < nrows) {
+            float mine = 0.0f, sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < H; ++c)
+                if (c == p) {
+                    mine = m[c];
+                    sum = l[c];
+                }
+            *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * (r0 + p)) = make_float2(sum != 0.0f ? mine : -CUDART_INF_F, sum);      // an empty partial weighs nothing
+        }
+        tc_fence_before();
+        named_sync(3, kSoftmax);           // both halves have read rs before the next segment's queries
+    } while (w.next(a));
+    if (!ok && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_TIMEOUT);
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1) verify_bs8_mma_kernel(Bs8Args a) {
+    using C = Cfg<R>;
+    extern __shared__ uint8_t raw[];
+    Smem<R>& sm = *reinterpret_cast<Smem<R>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
+    const int warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], kSoftmax);
+            mbar_init(&sm.p_full[i], kSoftmax);
+            mbar_init(&sm.p_free[i], 1);
+        }
+        mbar_init(&sm.q_full, kSoftmax);
+        mbar_init(&sm.drained, 1);
+        for (int i = 0; i < kMeta; ++i) mbar_init(&sm.meta_full[i], 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc(&sm.tmem, C::kTmem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 0) {
+        bool bad = false;
+        const Bs8Share w = bs8_share(a, blockIdx.x, &bad);
+        if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
+        if (threadIdx.x == 0) sm.first = w;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Bs8Share w = sm.first;
+    const uint32_t tmem = sm.tmem;
+    if (w.tiles > 0) {
+        if (warp == 0) {
+            produce<R>(a, sm, w);
+        } else if (warp == 1) {
+            if ((threadIdx.x & 31) == 0) issue<R>(a, sm, w, tmem);
+            __syncwarp();
+        } else {
+            softmax<R>(a, sm, w, tmem);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::kTmem);
+}
+
+template <int R>
+cudaError_t launch_r(const Bs8Args& a, cudaStream_t st) {
+    constexpr size_t smem = sizeof(Smem<R>) + 128;
+    static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+    const cudaError_t e = cudaFuncSetAttribute(verify_bs8_mma_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, verify_bs8_mma_kernel<R>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_bs8_mma(const Bs8Args& a, cudaStream_t st) {
+    const int rows = kGroup * a.max_n_q;
+    return rows <= 16 ? launch_r<16>(a, st) : rows <= 32 ? launch_r<32>(a, st) : launch_r<64>(a, st);
+}
+
+}  // namespace q3kv
