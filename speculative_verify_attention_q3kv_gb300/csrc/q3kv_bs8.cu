@@ -16,8 +16,8 @@ namespace q3kv {
 namespace {
 
 // ---------------------------------------------------------------- append
-// One CTA per (block, slot, kv head, K|V), a thread per row and 16 dims: it reads 32 or 64 neighbouring bytes, and a
-// warp writes four whole cores (512 bytes).  Bound: the rows read and the codes written.
+// One CTA per (block, slot, kv head), a thread per row and 16 dims of K and V: it reads 32 or 64 neighbouring bytes of
+// each, and a warp writes four whole cores (512 bytes).  Bound: the rows read and the codes written.
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ void load16(const float* src, float (&x)[16]) {
@@ -65,13 +65,14 @@ __device__ __forceinline__ int scale_exp(float s) {       // of a stored scale, 
 
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) append_bs8_kernel(AppendArgs a) {
-    __shared__ float s_max[kAppendThreads / 32];
+    __shared__ float s_max[2][kAppendThreads / 32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int slot = blockIdx.y, head = blockIdx.z >> 1, kv = blockIdx.z & 1;
+    const int slot = blockIdx.y, head = blockIdx.z;
     const int n_new = a.n_new[slot];
+    const int64_t len = a.slot_len[slot], first_row = a.row_offsets[slot];
     if (n_new == 0) return;
-    const int64_t len = a.slot_len[slot], end = len + n_new;
+    const int64_t end = len + n_new;
     const bool report = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && a.status;
     if (n_new < 0 || n_new > a.max_n_new || len < 0) {
         if (report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
@@ -82,64 +83,76 @@ __global__ void __launch_bounds__(kAppendThreads) append_bs8_kernel(AppendArgs a
     const int64_t block = len / kBs8Block + blockIdx.x, p0 = block * kBs8Block;
     if (p0 >= end || p0 >= room) return;
     const int32_t page = a.page_table[(int64_t)slot * a.max_pages_per_slot + p0 / kPageSize];
-    if (page < 0 || page >= a.num_pages) {
-        if (threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
-        return;
-    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = (warp & 1) * 8 + (lane & 7), chunk = (warp >> 1) * 4 + (lane >> 3);
     const int64_t pos = p0 + row;
     const bool fresh = pos >= len && pos < end, kept = pos < len;
-    uint8_t* unit = a.pool + bs8_offset(a.num_layers, a.num_kv_heads, page, a.layer, head, kv);
-    const int in_page = (int)(p0 % kPageSize);
-    uint4* code = reinterpret_cast<uint4*>(unit + ((in_page + row) / 8 * 16 + chunk) * 128 + (row % 8) * 16);
-    float* scale = reinterpret_cast<float*>(unit + kBs8CodeBytes) + in_page / kBs8Block;
-
-    float x[16];
-    float top = 0.0f;
-    bool finite = true;
+    float x[2][16];
     if (fresh) {
-        const T* in = static_cast<const T*>(kv == 0 ? a.k : a.v);
-        load16(in + (((int64_t)a.row_offsets[slot] + (pos - len)) * a.num_kv_heads + head) * kHeadDim + chunk * 16, x);
+        const int64_t at = ((first_row + (pos - len)) * a.num_kv_heads + head) * kHeadDim + chunk * 16;
+        load16(static_cast<const T*>(a.k) + at, x[0]);
+        load16(static_cast<const T*>(a.v) + at, x[1]);
+    }
+    if (page < 0 || page >= a.num_pages) {
+        if (threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
+        return;
+    }
+    uint8_t* unit = a.pool + bs8_offset(a.num_layers, a.num_kv_heads, page, a.layer, head, 0);
+    const int in_page = (int)(p0 % kPageSize);
+    uint8_t* code = unit + ((in_page + row) / 8 * 16 + chunk) * 128 + (row % 8) * 16;
+    uint8_t* scale = unit + kBs8CodeBytes + 4 * (in_page / kBs8Block);
+    int old[2] = {-kBs8MaxExp, -kBs8MaxExp};
+    uint4 was[2];
+    if (p0 < len) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const bool ok = fabsf(x[i]) <= 3.402823466e38f;
-            finite = finite && ok;
-            top = fmaxf(top, ok ? fabsf(x[i]) : 0.0f);
+        for (int kv = 0; kv < 2; ++kv) {
+            old[kv] = scale_exp(*reinterpret_cast<const float*>(scale + kv * kBs8UnitBytes));
+            if (kept) was[kv] = *reinterpret_cast<const uint4*>(code + kv * kBs8UnitBytes);
         }
     }
-    int e = -kBs8MaxExp;
-    int old = e;
-    uint4 was = make_uint4(0, 0, 0, 0);
-    if (p0 < len) {
-        e = old = scale_exp(*scale);
-        if (kept) was = *code;
-    }
+    bool finite = true;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) s_max[warp] = top;
+    for (int kv = 0; kv < 2; ++kv) {
+        float top = 0.0f;
+        if (fresh) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool ok = fabsf(x[kv][i]) <= 3.402823466e38f;
+                finite = finite && ok;
+                top = fmaxf(top, ok ? fabsf(x[kv][i]) : 0.0f);
+            }
+        }
+        // magnitudes are ordered as integers
+        const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if (lane == 0) s_max[kv][warp] = __uint_as_float(u);
+    }
     if (!__all_sync(0xffffffffu, finite) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kAppendThreads / 32; ++i) top = fmaxf(top, s_max[i]);
-    // top = m 2^k with 1 <= m < 2 and 448 = 1.75 2^8; zero and subnormal values give the smallest e
-    const uint32_t u = __float_as_uint(top);
-    const int need = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    if (need > kBs8MaxExp && threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_SCALE_OVERFLOW);
-    e = min(kBs8MaxExp, max(e, need));
-    if (fresh) {
-        *code = encode16(x, pow2(-e));
-    } else if (kept && e != old) {
-        const uint32_t w[4] = {was.x, was.y, was.z, was.w};
+    for (int kv = 0; kv < 2; ++kv) {
+        float top = s_max[kv][0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = e4m3x2_to_f32((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
+        for (int i = 1; i < kAppendThreads / 32; ++i) top = fmaxf(top, s_max[kv][i]);
+        // top = m 2^k with 1 <= m < 2 and 448 = 1.75 2^8; zero and subnormal values give the smallest e
+        const uint32_t u = __float_as_uint(top);
+        const int need = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+        if (need > kBs8MaxExp && threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_SCALE_OVERFLOW);
+        const int e = min(kBs8MaxExp, max(old[kv], need));
+        if (fresh) {
+            *reinterpret_cast<uint4*>(code + kv * kBs8UnitBytes) = encode16(x[kv], pow2(-e));
+        } else if (kept && e != old[kv]) {
+            const uint32_t w[4] = {was[kv].x, was[kv].y, was[kv].z, was[kv].w};
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = e4m3x2_to_f32((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                y[2 * i] = f.x;
+                y[2 * i + 1] = f.y;
+            }
+            *reinterpret_cast<uint4*>(code + kv * kBs8UnitBytes) = encode16(y, pow2(max(old[kv] - e, -126)));
         }
-        *code = encode16(x, e - old > 2 * kBs8MaxExp - 2 ? 0.0f : pow2(old - e));
+        if (threadIdx.x == 0) *reinterpret_cast<float*>(scale + kv * kBs8UnitBytes) = pow2(e);
     }
-    if (threadIdx.x == 0) *scale = pow2(e);
 }
 
 // ---------------------------------------------------------------- verify attention on CUDA cores
@@ -338,12 +351,14 @@ __global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) 
 }
 
 // ---------------------------------------------------------------- merge
-// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partials of a cut pair; one CTA per row.
-constexpr int kMergeThreads = 256;
+// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partials of a cut pair; one CTA per row, eight groups of
+// 64 threads with every eighth partial each.  Bound: latency.  So a group's partials are loaded together with their
+// maxima, ten at a time (80 partials of a row are under way at once), and the groups agree on M at the end.
+constexpr int kMergeGroups = 8, kMergeThreads = 64 * kMergeGroups, kMergeBatch = 10;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
-    __shared__ float4 s_o[kMergeThreads / 64][64];
-    __shared__ float s_l[kMergeThreads / 64], s_m[kMergeThreads / 32];
+    __shared__ float4 s_o[kMergeGroups][64];
+    __shared__ float2 s_ml[kMergeGroups];
     __shared__ int64_t s_at[2];                  // tiles before the slot, and of all slots
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -362,42 +377,63 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
     const int c0 = bs8_cta_of(begin, total, a.ctas), c1 = bs8_cta_of(begin + s.tiles - 1, total, a.ctas);
     if (c0 == c1) return;                        // the pair was not cut
     const int n = c1 - c0 + 1;
-    auto part = [&](int i) { return a.partials + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kBs8PartFloats; };
-    float top = -CUDART_INF_F;
-    for (int i = tid; i < n; i += kMergeThreads) top = fmaxf(top, part(i)[kBs8Rows * kHeadDim + 2 * r]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane == 0) s_m[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMergeThreads / 32; ++i) top = fmaxf(top, s_m[i]);
-    if (top == -CUDART_INF_F) top = 0.0f;        // every partial is empty
     const int col = tid & 63, group = tid >> 6;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-#pragma unroll 4
-    for (int i = group; i < n; i += kMergeThreads / 64) {
-        const float* p = part(i);
-        const float2 ml = *reinterpret_cast<const float2*>(p + kBs8Rows * kHeadDim + 2 * r);
-        const float4 v = *reinterpret_cast<const float4*>(p + r * kHeadDim + 4 * col);
-        const float f = exp2f(ml.x - top);
-        l = fmaf(f, ml.y, l);
+    float m = -CUDART_INF_F, l = 0.0f;
+    for (int i0 = group; i0 < n; i0 += kMergeGroups * kMergeBatch) {
+        float4 v[kMergeBatch];
+        float2 ml[kMergeBatch];
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+            const int i = i0 + k * kMergeGroups;
+            if (i < n) {                         // the pair's first CTA ends inside it, the others begin inside it
+                const float* p = a.partials + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kBs8PartFloats;
+                ml[k] = *reinterpret_cast<const float2*>(p + kBs8Rows * kHeadDim + 2 * r);
+                v[k] = *reinterpret_cast<const float4*>(p + r * kHeadDim + 4 * col);
+            } else {
+                ml[k] = make_float2(-CUDART_INF_F, 0.0f);
+                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) top = fmaxf(top, ml[k].x);
+        if (top == -CUDART_INF_F) continue;      // empty partials
+        const float f0 = exp2f(m - top);
+        m = top;
+        l *= f0;
+        o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+            const float f = exp2f(ml[k].x - top);
+            l = fmaf(f, ml[k].y, l);
+            o.x = fmaf(f, v[k].x, o.x);
+            o.y = fmaf(f, v[k].y, o.y);
+            o.z = fmaf(f, v[k].z, o.z);
+            o.w = fmaf(f, v[k].w, o.w);
+        }
+    }
+    s_o[group][col] = o;
+    if (col == 0) s_ml[group] = make_float2(m, l);
+    __syncthreads();
+    if (tid >= 64) return;
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int g = 0; g < kMergeGroups; ++g) top = fmaxf(top, s_ml[g].x);
+    if (top == -CUDART_INF_F) top = 0.0f;        // the row saw nothing
+    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    l = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kMergeGroups; ++g) {
+        const float f = exp2f(s_ml[g].x - top);
+        const float4 v = s_o[g][col];
+        l = fmaf(f, s_ml[g].y, l);
         o.x = fmaf(f, v.x, o.x);
         o.y = fmaf(f, v.y, o.y);
         o.z = fmaf(f, v.z, o.z);
         o.w = fmaf(f, v.w, o.w);
     }
-    s_o[group][col] = o;
-    if (col == 0) s_l[group] = l;
-    __syncthreads();
-    if (tid >= 64) return;
-    l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int g = 1; g < kMergeThreads / 64; ++g) {
-        const float4 v = s_o[g][col];
-        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
-    }
     const int64_t at = (((int64_t)a.q_offsets[slot] + T0 + (r >> 3)) * heads * kGroup + head * kGroup + (r & 7)) * kHeadDim + 4 * col;
     st4(a.out, at, a.dtype, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
@@ -490,7 +526,7 @@ int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_pool, con
     a.status = d_status;
     a.fmt = kFmtBs8;
     // n rows from any place of a block touch at most (n - 1) / 16 + 2 blocks
-    const dim3 grid((unsigned)((max_n_new - 1) / kBs8Block + 2), (unsigned)num_slots, (unsigned)(2 * desc->num_kv_heads));
+    const dim3 grid((unsigned)((max_n_new - 1) / kBs8Block + 2), (unsigned)num_slots, (unsigned)desc->num_kv_heads);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(dtype == Q3KV_F32 ? launch(append_bs8_kernel<float>, a, grid, kAppendThreads, 0, st)
                                          : launch(append_bs8_kernel<__nv_bfloat16>, a, grid, kAppendThreads, 0, st));

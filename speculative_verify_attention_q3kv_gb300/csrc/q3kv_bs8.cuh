@@ -104,12 +104,16 @@ struct Bs8Share {
 __device__ __forceinline__ Bs8Share bs8_share(const Bs8Args& a, int i, bool* bad) {
     Bs8Share w{};
     const int lane = threadIdx.x & 31;
-    const int64_t n = bs8_tiles_before(a, a.num_slots, bad);
+    Bs8Slot s = lane < a.num_slots ? bs8_slot(a, lane, bad) : Bs8Slot{0, 0, 0, 0};
+    int64_t n = s.total(a.num_kv_heads);
+    for (int b = lane + 32; b < a.num_slots; b += 32) n += bs8_slot(a, b, bad).total(a.num_kv_heads);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     const int64_t begin = (int64_t)i * n / a.ctas, end = (int64_t)(i + 1) * n / a.ctas;
     if (begin >= end) return w;
     int64_t before = 0;
     for (int b0 = 0;; b0 += 32) {                                // ends: begin < n
-        const Bs8Slot s = b0 + lane < a.num_slots ? bs8_slot(a, b0 + lane, nullptr) : Bs8Slot{0, 0, 0, 0};
+        if (b0 > 0) s = b0 + lane < a.num_slots ? bs8_slot(a, b0 + lane, nullptr) : Bs8Slot{0, 0, 0, 0};
         int64_t upto = s.total(a.num_kv_heads);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

@@ -17,8 +17,8 @@
 // than 2^7 of headroom (a vote per tile), so most tiles need no maximum and no rescaling.
 //
 // Bound: the codes' bytes.  At 8 tokens a tile's 64 KiB take about 2,900 cycles of an SM's share of HBM, its 32 MMAs about
-// 1,700 and its softmax less.  One CTA per SM; warp 0 copies, warp 1 issues the MMAs, warps 2-9 are the softmax (thread =
-// position; warps 2-5 the first half of the rows, 6-9 the second).
+// 1,700 and its softmax less.  One CTA per SM; warp 0 copies, warp 1 issues the MMAs, the others are the softmax: groups of four warps
+// with a thread per position and 8 or 16 rows.
 #include <math_constants.h>
 
 #include "q3kv_bs8.cuh"
@@ -27,8 +27,6 @@
 namespace q3kv {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kSoftmax = 256;                  // threads of warps 2-9
 constexpr uint32_t kTileBytes = kBs8Tile * kHeadDim;
 constexpr float kAbove = 8.0f;                 // m is set this far below the largest score: p' <= 2^8 then,
 constexpr float kRaise = 15.0f;                // and at most 2^15 until it is raised
@@ -37,7 +35,9 @@ constexpr int kMeta = 8;                       // tiles whose scales are kept
 template <int R>
 struct Cfg {
     static constexpr int kStages = R == 64 ? 4 : R == 32 ? 5 : 6;
-    static constexpr int kH = R / 2;                                   // rows per softmax thread
+    static constexpr int kWgs = R == 64 ? 4 : 2;                        // softmax warpgroups, each with all positions and R / kWgs rows
+    static constexpr int kH = R / kWgs;                                // rows per softmax thread
+    static constexpr int kSoftmax = 128 * kWgs, kThreads = 64 + kSoftmax;
     static constexpr uint32_t kS = 2 * R, kO = 4 * R;                  // TMEM columns: S buffers of 2 R, then O halves of R
     static constexpr uint32_t kTmem = R == 64 ? 512 : R == 32 ? 256 : 128;
 };
@@ -49,7 +49,7 @@ struct Smem {
     alignas(128) uint8_t p[2][3][R * kBs8Tile];
     alignas(16) float meta[kMeta][16];         // K scales of a tile's 8 blocks, then V scales
     alignas(16) float rs[R];                   // 2^-k of each row
-    float red[2][4][R / 2];
+    float red[Cfg<R>::kWgs][4][Cfg<R>::kH];
     Bs8Share first;
     int bad_page[kMeta];
     uint32_t tmem;
@@ -238,10 +238,17 @@ __device__ void prepare_q(const Bs8Args& a, Smem<R>& sm, const Bs8Share& w, int 
     const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
     const int64_t q0 = (int64_t)a.q_offsets[w.slot] + T0;
-#pragma unroll 2
-    for (int r = warp; r < R; r += kSoftmax / 32) {
-        float x[8] = {};
-        if (r < nrows) load8(q + ((q0 + (r >> 3)) * heads * kGroup + w.head(heads) * kGroup + (r & 7)) * kHeadDim + 8 * lane, x);
+    constexpr int kWarps = Cfg<R>::kSoftmax / 32, kEach = R / kWarps;
+    float in[kEach][8] = {};
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int r = warp + i * kWarps;
+        if (r < nrows) load8(q + ((q0 + (r >> 3)) * heads * kGroup + w.head(heads) * kGroup + (r & 7)) * kHeadDim + 8 * lane, in[i]);
+    }
+#pragma unroll
+    for (int n = 0; n < kEach; ++n) {
+        const int r = warp + n * kWarps;
+        float (&x)[8] = in[n];
         float top = 0.0f;
         bool finite = true;
 #pragma unroll
@@ -296,7 +303,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
         prepare_q<R>(a, sm, w, warp);
         fence_proxy_async();
         mbar_arrive(&sm.q_full);
-        named_sync(3, kSoftmax);           // rs is there
+        named_sync(1 + C::kWgs, C::kSoftmax);           // rs is there
         float m[H], l[H];
 #pragma unroll
         for (int c = 0; c < H; ++c) {
@@ -314,17 +321,13 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
             __syncwarp();
             tc_fence_after();
             float d[H];
-            constexpr int kHalf = H == 32 ? 16 : H;      // the second code's scores come in halves: registers
             {
-                float s2[kHalf];
+                float s2[H];
                 tmem_load<H>(lanes + b * C::kS + r0, d);
+                tmem_load<H>(lanes + b * C::kS + R + r0, s2);
+                tmem_ld_wait();
 #pragma unroll
-                for (int g = 0; g < H; g += kHalf) {
-                    tmem_load<kHalf>(lanes + b * C::kS + R + r0 + g, s2);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < kHalf; ++c) d[g + c] += s2[c];
-                }
+                for (int c = 0; c < H; ++c) d[c] += s2[c];
             }
             tc_fence_before();
             mbar_arrive(&sm.s_free[b]);
@@ -412,12 +415,9 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                 *reinterpret_cast<uint2*>(to + R * kBs8Tile) = make_uint2(w2[0], w2[1]);
                 *reinterpret_cast<uint2*>(to + 2 * R * kBs8Tile) = make_uint2(w3[0], w3[1]);
             } else {
-#pragma unroll
-                for (int c = 0; c < H / 16; ++c) {
-                    *reinterpret_cast<uint4*>(to + 128 * c) = make_uint4(w1[4 * c], w1[4 * c + 1], w1[4 * c + 2], w1[4 * c + 3]);
-                    *reinterpret_cast<uint4*>(to + 128 * c + R * kBs8Tile) = make_uint4(w2[4 * c], w2[4 * c + 1], w2[4 * c + 2], w2[4 * c + 3]);
-                    *reinterpret_cast<uint4*>(to + 128 * c + 2 * R * kBs8Tile) = make_uint4(w3[4 * c], w3[4 * c + 1], w3[4 * c + 2], w3[4 * c + 3]);
-                }
+                *reinterpret_cast<uint4*>(to) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                *reinterpret_cast<uint4*>(to + R * kBs8Tile) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+                *reinterpret_cast<uint4*>(to + 2 * R * kBs8Tile) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
             }
             const int valid = hidden ? 0 : w.s.L - p0;
             if (valid < kBs8Tile) {
@@ -426,8 +426,8 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                 ok = ok && mbar_wait_fast(&sm.full[st], (at / C::kStages) & 1, &sm.abort);
                 if (p >= valid) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4*>(sm.kv[st] + ((p >> 3) * 16 + wg * 8 + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < 16 / C::kWgs; ++c)
+                        *reinterpret_cast<uint4*>(sm.kv[st] + ((p >> 3) * 16 + wg * (16 / C::kWgs) + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
             }
             fence_proxy_async();
@@ -436,7 +436,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
         }
         vcnt += 2 * w.tiles;
         ok = ok && mbar_wait_fast(&sm.p_free[(it - 1) & 1], ((it - 1) >> 1) & 1, &sm.abort);
-        if (named_or(3, kSoftmax, !ok)) {      // all eight warps leave together
+        if (named_or(1 + C::kWgs, C::kSoftmax, !ok)) {      // all softmax warps leave together
             ok = false;
             break;
         }
@@ -482,13 +482,13 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
             *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * (r0 + p)) = make_float2(sum != 0.0f ? mine : -CUDART_INF_F, sum);      // an empty partial weighs nothing
         }
         tc_fence_before();
-        named_sync(3, kSoftmax);           // both halves have read rs before the next segment's queries
+        named_sync(1 + C::kWgs, C::kSoftmax);           // all groups have read rs before the next segment's queries
     } while (w.next(a));
     if (!ok && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_TIMEOUT);
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, 1) verify_bs8_mma_kernel(Bs8Args a) {
+__global__ void __launch_bounds__(Cfg<R>::kThreads, 1) verify_bs8_mma_kernel(Bs8Args a) {
     using C = Cfg<R>;
     extern __shared__ uint8_t raw[];
     Smem<R>& sm = *reinterpret_cast<Smem<R>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
@@ -501,11 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_bs8_mma_kernel(Bs8Args a) 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.s_free[i], kSoftmax);
-            mbar_init(&sm.p_full[i], kSoftmax);
+            mbar_init(&sm.s_free[i], C::kSoftmax);
+            mbar_init(&sm.p_full[i], C::kSoftmax);
             mbar_init(&sm.p_free[i], 1);
         }
-        mbar_init(&sm.q_full, kSoftmax);
+        mbar_init(&sm.q_full, C::kSoftmax);
         mbar_init(&sm.drained, 1);
         for (int i = 0; i < kMeta; ++i) mbar_init(&sm.meta_full[i], 1);
         sm.abort = 0;
@@ -548,7 +548,7 @@ cudaError_t launch_r(const Bs8Args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Cfg<R>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -57,8 +57,8 @@ struct alignas(16) Row8 {
     T x[kPer];
 };
 
-// Rows are loaded kBatch at a time, so that as many loads are in flight: stores to an output that
-// may be the input keep the compiler from moving later loads up.
+// A CTA takes 2,048 entries of up to kBatch rows of one slot: their logits, masks and counts are all loaded before the
+// first barrier.  Bound: bytes (logits in and out); small calls: the chain of loads lengths -> tokens -> biases.
 constexpr int kBatch = 4;
 
 template <typename T, bool VEC>
@@ -67,78 +67,101 @@ __global__ void __launch_bounds__(kThreads) process_logits_kernel(LogitArgs a) {
     __shared__ int s_tok[kMaxNq];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, slot = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, slot = blockIdx.y, j0 = blockIdx.z * kBatch;
     const int base = blockIdx.x * kChunk;
-    const bool report = blockIdx.x == 0 && tid == 0 && a.status;
-    const int w = a.n_q[slot];
-    if (w == 0) return;
-    const int r0 = a.q_offsets[slot];
-    if (w < 0 || w > a.max_n_q || r0 < 0 || r0 > a.num_rows - w) {
-        if (report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
-        return;
-    }
-    if (tid < w) {
-        const int t = a.tokens[r0 + tid];
-        s_tok[tid] = t;
-        if (blockIdx.x == 0 && (t < 0 || t >= a.vocab) && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
-    }
+    const int w = a.n_q[slot], r0 = a.q_offsets[slot];
     int b0 = 0, b1 = 0;
     if (a.bias_offsets) {
         b0 = a.bias_offsets[slot];
         b1 = a.bias_offsets[slot + 1];
-        if (b0 < 0 || b1 < b0 || b1 > a.num_biases) {
-            if (report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
-            b0 = b1 = 0;
-        }
-        if (b1 > b0)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) s_bias[tid + i * kThreads] = 0.0f;
     }
-    __syncthreads();
+    const float theta = a.repetition ? a.repetition[slot] : 1.0f;
+    const float alpha = a.frequency ? a.frequency[slot] : 0.0f, beta = a.presence ? a.presence[slot] : 0.0f;
+    // this thread's entries: 8 neighbours, or every 256th where rows are not 16-byte aligned
+    const int first = VEC ? base + tid * kPer : base + tid;
+    constexpr int kStep = VEC ? 1 : kThreads;
+    union {
+        Row8<int16_t> v;
+        int16_t x[kPer];
+    } count;
+    if (a.counts && first < a.vocab) {
+        const int16_t* c = a.counts + (int64_t)slot * a.counts_stride;
+        if (VEC) {
+            count.v = *reinterpret_cast<const Row8<int16_t>*>(c + first);   // the stride covers whole vectors
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) count.x[e] = first + e * kStep < a.vocab ? c[first + e * kStep] : (int16_t)0;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) count.x[e] = 0;
+    }
+    const bool report = blockIdx.x == 0 && blockIdx.z == 0 && a.status;
+    if (w == 0) return;
+    if (w < 0 || w > a.max_n_q || r0 < 0 || r0 > a.num_rows - w) {
+        if (report && tid == 0) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
+        return;
+    }
+    if (j0 >= w) return;
+    if (tid < w) {
+        const int t = a.tokens[r0 + tid];
+        s_tok[tid] = t;
+        if (report && (t < 0 || t >= a.vocab)) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
+    }
+    const int64_t mask_words = (a.vocab + 31) / 32;
+    const T* in = static_cast<const T*>(a.logits) + (int64_t)(r0 + j0) * a.vocab + first;
+    const int rows = min(kBatch, w - j0);
+    Row8<T> x[kBatch];
+    uint32_t allowed[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+        if (k >= rows) break;
+        const T* p = in + (int64_t)k * a.vocab;
+        if (VEC) {
+            if (first < a.vocab) x[k] = *reinterpret_cast<const Row8<T>*>(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (first + e * kStep < a.vocab) x[k].x[e] = p[e * kStep];
+        }
+        allowed[k] = ~0u;
+        if (a.mask) {
+            const uint32_t* m = reinterpret_cast<const uint32_t*>(a.mask) + (r0 + j0 + k) * mask_words;
+            if (VEC) {
+                if (first < a.vocab) allowed[k] = reinterpret_cast<const uint8_t*>(m)[first >> 3];
+            } else {
+                // a warp's entries of one step share a word: lane e holds step e's
+                const int word = (first - lane + lane * kStep) >> 5;
+                allowed[k] = lane < kPer && word < mask_words ? m[word] : 0;
+            }
+        }
+    }
+    if (b0 < 0 || b1 < b0 || b1 > a.num_biases) {
+        if (report && tid == 0) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
+        b0 = b1 = 0;
+    }
     if (b1 > b0) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) s_bias[tid + i * kThreads] = 0.0f;
+        __syncthreads();
         for (int i = b0 + tid; i < b1; i += kThreads) {
             const int t = a.bias_tokens[i];
             // ascending ids: no id twice, so the sum does not depend on an order
             if (t < 0 || t >= a.vocab || (i > b0 && a.bias_tokens[i - 1] >= t)) {
-                if (blockIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
+                if (report) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
             } else if (t >= base && t < base + kChunk) {
                 s_bias[t - base] = a.bias_values[i];
             }
         }
-        __syncthreads();
     }
+    __syncthreads();
+    if (VEC && first >= a.vocab) return;
 
-    // this thread's entries: 8 neighbours, or every 256th where rows are not 16-byte aligned
-    const int first = VEC ? base + tid * kPer : base + tid;
-    constexpr int kStep = VEC ? 1 : kThreads;
-    if (first >= a.vocab) return;
-    int count[kPer];
-    float bias[kPer];
-    if (a.counts) {
-        const int16_t* c = a.counts + (int64_t)slot * a.counts_stride;
-        if (VEC) {
-            const Row8<int16_t> v = *reinterpret_cast<const Row8<int16_t>*>(c + first);   // the stride covers whole vectors
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) count[e] = v.x[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) count[e] = first + e * kStep < a.vocab ? c[first + e * kStep] : 0;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) count[e] = 0;
-    }
-    bool prompt[kPer];
     uint32_t step[kPer];         // bit i: t_i is this entry
     bool stepping = false;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        prompt[e] = count[e] < 0;
-        count[e] &= 0x7fff;
-        step[e] = 0;
-        bias[e] = b1 > b0 ? s_bias[first - base + e * kStep] : 0.0f;
-    }
-    for (int i = 0; i < w; ++i) {
+    for (int e = 0; e < kPer; ++e) step[e] = 0;
+    for (int i = 0; i < min(w, j0 + kBatch); ++i) {
         const int d = s_tok[i] - first;
         if (VEC ? (unsigned)d < (unsigned)kPer : d >= 0 && d < kChunk && d % kThreads == 0) {
             stepping = true;
@@ -146,72 +169,38 @@ __global__ void __launch_bounds__(kThreads) process_logits_kernel(LogitArgs a) {
             for (int e = 0; e < kPer; ++e) step[e] |= (d == e * kStep ? 1u : 0u) << i;
         }
     }
-    const float theta = a.repetition ? a.repetition[slot] : 1.0f;
-    const float alpha = a.frequency ? a.frequency[slot] : 0.0f, beta = a.presence ? a.presence[slot] : 0.0f;
-    const int64_t mask_words = (a.vocab + 31) / 32;
-    const T* in = static_cast<const T*>(a.logits);
-    T* out = static_cast<T*>(a.out);
     const bool in_place = a.logits == a.out;
-
-    for (int j0 = 0; j0 < w; j0 += kBatch) {
-        Row8<T> x[kBatch];
-        uint32_t allowed[kBatch];
+    T* out = static_cast<T*>(a.out) + (int64_t)(r0 + j0) * a.vocab + first;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            if (j0 + k >= w) break;
-            const int64_t row = r0 + j0 + k;
-            const T* p = in + row * a.vocab + first;
-            if (VEC) {
-                x[k] = *reinterpret_cast<const Row8<T>*>(p);
-            } else {
+    for (int k = 0; k < kBatch; ++k) {
+        if (k >= rows) break;
+        T* p = out + (int64_t)k * a.vocab;
+        Row8<T> o;
+        bool changed = !in_place;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    if (first + e * kStep < a.vocab) x[k].x[e] = p[e * kStep];
+        for (int e = 0; e < kPer; ++e) {
+            int c = count.x[e];
+            const bool prompt = c < 0;
+            c &= 0x7fff;
+            if (stepping) c += __popc(step[e] & ((2u << (j0 + k)) - 1u));
+            float y = to_f32(x[k].x[e]);
+            if (c > 0 || prompt) {
+                y = y > 0.0f ? __fdiv_rn(y, theta) : y * theta;
+                if (c > 0) y = (y - alpha * (float)c) - beta;
             }
-            allowed[k] = 0xff;
-            if (a.mask) {
-                const uint32_t* m = reinterpret_cast<const uint32_t*>(a.mask) + row * mask_words;
-                if (VEC) {
-                    allowed[k] = reinterpret_cast<const uint8_t*>(m)[first >> 3];
-                } else {
-                    allowed[k] = 0;
-#pragma unroll
-                    for (int e = 0; e < kPer; ++e) {
-                        const int t = first + e * kStep;
-                        if (t < a.vocab) allowed[k] |= ((m[t >> 5] >> (t & 31)) & 1u) << e;
-                    }
-                }
-            }
+            if (b1 > b0) y += s_bias[first - base + e * kStep];
+            const bool allow = VEC || !a.mask ? (allowed[k] >> e) & 1u : (__shfl_sync(0xffffffffu, allowed[k], e) >> lane) & 1u;
+            if (!allow) y = -CUDART_INF_F;
+            o.x[e] = from_f32<T>(y);
+            // NaN differs from itself and is stored again
+            if (in_place) changed |= !(to_f32(o.x[e]) == to_f32(x[k].x[e]));
         }
+        if (VEC) {
+            if (changed) *reinterpret_cast<Row8<T>*>(p) = o;
+        } else {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int j = j0 + k;
-            if (j >= w) break;
-            T* p = out + (int64_t)(r0 + j) * a.vocab + first;
-            Row8<T> o;
-            bool changed = !in_place;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                int c = count[e];
-                if (stepping) c += __popc(step[e] & ((2u << j) - 1u));
-                float y = to_f32(x[k].x[e]);
-                if (c > 0 || prompt[e]) {
-                    y = y > 0.0f ? __fdiv_rn(y, theta) : y * theta;
-                    if (c > 0) y = (y - alpha * (float)c) - beta;
-                }
-                y += bias[e];
-                if (!((allowed[k] >> e) & 1u)) y = -CUDART_INF_F;
-                o.x[e] = from_f32<T>(y);
-                // NaN differs from itself and is stored again
-                if (in_place) changed |= !(to_f32(o.x[e]) == to_f32(x[k].x[e]));
-            }
-            if (VEC) {
-                if (changed) *reinterpret_cast<Row8<T>*>(p) = o;
-            } else {
-#pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                    if (first + e * kStep < a.vocab) p[e * kStep] = o.x[e];
-            }
+            for (int e = 0; e < kPer; ++e)
+                if (first + e * kStep < a.vocab) p[e * kStep] = o.x[e];
         }
     }
 }
@@ -231,18 +220,24 @@ struct CountArgs {
 
 constexpr int kCountCap = 0x7fff;
 
-// word += add in one 16-bit half, saturating in its low 15 bits; the order of additions does not matter
+__device__ __forceinline__ uint32_t* count_word(int16_t* at) {
+    return reinterpret_cast<uint32_t*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)3);
+}
+// word with add added to the 16-bit half at `shift`, saturating in its low 15 bits
+__device__ __forceinline__ uint32_t add_to(uint32_t word, int shift, int add) {
+    const uint32_t now = (uint32_t)min((int)((word >> shift) & kCountCap) + add, kCountCap);
+    return (word & ~((uint32_t)kCountCap << shift)) | (now << shift);
+}
+// the order of additions does not matter
 __device__ __forceinline__ void add_count(int16_t* at, int add) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(at);
-    uint32_t* word = reinterpret_cast<uint32_t*>(p & ~(uintptr_t)3);
-    const int shift = (p & 2) ? 16 : 0;
+    uint32_t* word = count_word(at);
+    const int shift = (reinterpret_cast<uintptr_t>(at) & 2) ? 16 : 0;
     uint32_t old = *reinterpret_cast<volatile uint32_t*>(word), seen;
     do {
         seen = old;
-        const uint32_t c = (seen >> shift) & kCountCap;
-        const uint32_t now = (uint32_t)min((int)c + add, kCountCap);
-        if (now == c) return;
-        old = atomicCAS(word, seen, (seen & ~((uint32_t)kCountCap << shift)) | (now << shift));
+        const uint32_t now = add_to(seen, shift, add);
+        if (now == seen) return;
+        old = atomicCAS(word, seen, now);
     } while (old != seen);
 }
 
@@ -284,47 +279,77 @@ __global__ void __launch_bounds__(kThreads) count_kernel(CountArgs a) {
 }
 
 // Long histories: frequent tokens would meet in the same words, so a CTA first adds up its 4,096 tokens in
-// a shared hash table (half full at most) and then adds each different token once.
-constexpr int kHistory = 4096, kTable = 8192;
+// a shared hash table (half full at most) and then adds each different token once.  Every phase is a few
+// independent accesses per thread: 4 tokens, 8 places of the table.
+constexpr int kHistory = 4096, kTable = 8192, kHistoryThreads = 1024;
 
-__global__ void __launch_bounds__(kThreads) count_history_kernel(CountArgs a) {
+__global__ void __launch_bounds__(kHistoryThreads) count_history_kernel(CountArgs a) {
     extern __shared__ int s_table[];              // [kTable] keys, then [kTable] counts
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int* keys = s_table;
+    int* sums = s_table + kTable;
+#pragma unroll
+    for (int i = 0; i < kTable / kHistoryThreads; ++i) {
+        keys[i * kHistoryThreads + threadIdx.x] = -1;
+        sums[i * kHistoryThreads + threadIdx.x] = 0;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int slot = blockIdx.y;
     int64_t begin;
     int n;
     if (!slot_range(a, slot, &begin, &n)) return;
-    const int from = blockIdx.x * kHistory, to = min(n, from + kHistory);
-    if (from >= to) return;
-    int* keys = s_table;
-    int* sums = s_table + kTable;
-    for (int i = threadIdx.x; i < kTable; i += kThreads) {
-        keys[i] = -1;
-        sums[i] = 0;
+    const int64_t from = (int64_t)blockIdx.x * kHistory;
+    if (from >= n) return;
+    int t[kHistory / kHistoryThreads];
+#pragma unroll
+    for (int k = 0; k < kHistory / kHistoryThreads; ++k) {
+        const int64_t i = from + k * kHistoryThreads + threadIdx.x;
+        t[k] = i < n ? a.tokens[begin + i] : -1;
+        if (i < n && (t[k] < 0 || t[k] >= a.vocab)) {
+            if (a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
+            t[k] = -1;
+        }
     }
     __syncthreads();
-    for (int i = from + threadIdx.x; i < to; i += kThreads) {
-        const int t = a.tokens[begin + i];
-        if (t < 0 || t >= a.vocab) {
-            if (a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
-            continue;
-        }
+#pragma unroll
+    for (int k = 0; k < kHistory / kHistoryThreads; ++k) {
+        if (t[k] < 0) continue;
         // open addressing ends: at most kHistory of kTable places are taken
-        uint32_t h = ((uint32_t)t * 2654435761u) >> 19;
-        for (int key = atomicCAS(&keys[h], -1, t); key != -1 && key != t; key = atomicCAS(&keys[h], -1, t)) h = (h + 1) & (kTable - 1);
+        uint32_t h = ((uint32_t)t[k] * 2654435761u) >> 19;
+        for (int key = atomicCAS(&keys[h], -1, t[k]); key != -1 && key != t[k]; key = atomicCAS(&keys[h], -1, t[k])) h = (h + 1) & (kTable - 1);
         atomicAdd(&sums[h], 1);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kTable; i += kThreads)
-        if (keys[i] >= 0) add_count(a.counts + (int64_t)slot * a.stride + keys[i], sums[i]);
+    int16_t* counts = a.counts + (int64_t)slot * a.stride;
+    constexpr int kPlaces = kTable / kHistoryThreads;
+    int key[kPlaces];
+    uint32_t seen[kPlaces];
+#pragma unroll
+    for (int k = 0; k < kPlaces; ++k) {
+        key[k] = keys[k * kHistoryThreads + threadIdx.x];
+        if (key[k] >= 0) seen[k] = *reinterpret_cast<volatile uint32_t*>(count_word(counts + key[k]));
+    }
+    uint32_t open = 0;                            // places whose addition has not gone through
+#pragma unroll
+    for (int k = 0; k < kPlaces; ++k)
+        if (key[k] >= 0) {
+            const int shift = (key[k] & 1) * 16;  // rows begin on whole words
+            const uint32_t now = add_to(seen[k], shift, sums[k * kHistoryThreads + threadIdx.x]);
+            if (now != seen[k] && atomicCAS(count_word(counts + key[k]), seen[k], now) != seen[k]) open |= 1u << k;
+        }
+    while (open) {
+        const int k = __ffs(open) - 1;
+        open &= open - 1;
+        const int place = k * kHistoryThreads + threadIdx.x;
+        add_count(counts + keys[place], sums[place]);
+    }
 }
 
 template <typename K, typename A>
-cudaError_t launch(K kernel, const A& a, dim3 grid, size_t smem, cudaStream_t st) {
+cudaError_t launch(K kernel, const A& a, dim3 grid, size_t smem, cudaStream_t st, int threads = kThreads) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -359,7 +384,8 @@ int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_stride, in
         constexpr size_t smem = 2 * kTable * sizeof(int);
         cudaError_t ce = cudaFuncSetAttribute(count_history_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (ce != cudaSuccess) return cuda_status(ce);
-        return cuda_status(launch(count_history_kernel, a, dim3((unsigned)(((int64_t)max_n + kHistory - 1) / kHistory), num_slots), smem, st));
+        return cuda_status(launch(count_history_kernel, a, dim3((unsigned)(((int64_t)max_n + kHistory - 1) / kHistory), num_slots), smem, st,
+                                  kHistoryThreads));
     }
     const dim3 grid((unsigned)(((int64_t)max_n + kThreads - 1) / kThreads), (unsigned)num_slots);
     return cuda_status(prompt ? launch(count_kernel<true>, a, grid, 0, st) : launch(count_kernel<false>, a, grid, 0, st));
@@ -408,7 +434,7 @@ int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dty
     a.num_biases = num_biases;
     a.mask = d_mask;
     a.status = d_status;
-    const dim3 grid((unsigned)(((int64_t)vocab + kChunk - 1) / kChunk), (unsigned)num_slots);
+    const dim3 grid((unsigned)(((int64_t)vocab + kChunk - 1) / kChunk), (unsigned)num_slots, (unsigned)((max_n_q + kBatch - 1) / kBatch));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     // rows start on 16 bytes and end with a whole group of 8 entries
     const bool vec = vocab % 8 == 0;
