@@ -5,9 +5,9 @@
 // decoded.  What the other operands lose in 8 bits is carried by more than one code per value:
 //   q  = 2^-k (q1 + q2)      two E4M3 codes, k per row: a bf16 value has 8 significant bits, two codes hold them all;
 //                            what is below 2^-18 of the row's largest value is rounded away
-//   p' = p1 + p2 + p3        three E5M2 codes (3 significant bits each) of the weight as fp16, relative error about 2^-11,
-//                            less than rounding the weight to bf16 would cost; E5M2 for its range (2^-16 .. 2^15):
-//                            a long context's many small weights stay above it next to a large one
+//   p' = p1 + p2 + p3        three E5M2 codes (3 significant bits each) of the weight as fp16: at most 2^-9 off, as if
+//                            the weight were rounded to bf16; E5M2 for its range (2^-16 .. 2^15): a long context's
+//                            many small weights stay above it next to a large one
 // Contractions (M = 128, float32 accumulation in TMEM):
 //   S^T[p][r | R + r] = K[p][:] . q1[r][:] | q2[r][:]   A = K codes (K-major), N = 2 R columns, K = 256 dims
 //   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions
@@ -48,7 +48,7 @@ struct Smem {
     alignas(128) uint8_t q[2 * R * kHeadDim];
     alignas(128) uint8_t p[2][3][R * kBs8Tile];
     alignas(16) float meta[kMeta][16];         // K scales of a tile's 8 blocks, then V scales
-    alignas(16) float rs[R];                   // 2^-k of each row
+    alignas(16) float rs[R], m[R], dm[R];      // of each row: 2^-k, the subtracted maximum, its last change
     float red[Cfg<R>::kWgs][4][Cfg<R>::kH];
     Bs8Share first;
     int bad_page[kMeta];
@@ -105,8 +105,6 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// fp16 pair -> the pair rounded to E5M2 (the upper byte of fp16; ties away from zero), as fp16
-__device__ __forceinline__ uint32_t e5m2_of(uint32_t h) { return (h + 0x00800080u) & 0xff00ff00u; }
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return as_u32(__hsub2(as_h2(a), as_h2(b))); }
 
 // ---------------------------------------------------------------- roles
@@ -288,10 +286,35 @@ __device__ __forceinline__ int ordered(float f) {          // integers in the or
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
+// Pairs of float32 in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 template <int R>
 __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
     using C = Cfg<R>;
-    constexpr int H = C::kH;
+    constexpr int H = C::kH, kAll = 1 + C::kWgs;                     // kAll: barrier of all softmax warps
     const int tid = threadIdx.x - 64, lane = threadIdx.x & 31, warp = tid >> 5, heads = a.num_kv_heads;
     const int wg = warp >> 2, quarter = (threadIdx.x >> 5) & 3;      // rows wg H .., positions 32 quarter ..: a warp reads its own TMEM lanes
     const int p = quarter * 32 + lane, r0 = wg * H, bar = 1 + wg;
@@ -299,57 +322,54 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
     uint32_t it = 0, vcnt = 0;             // vcnt: copies before this segment's
     bool ok = true;
     do {
-        const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
         prepare_q<R>(a, sm, w, warp);
+        if (tid < R) sm.m[tid] = 0.0f;
         fence_proxy_async();
         mbar_arrive(&sm.q_full);
-        named_sync(1 + C::kWgs, C::kSoftmax);           // rs is there
-        float m[H], l[H];
+        named_sync(kAll, C::kSoftmax);     // rs and m are there
+        float2 l[H / 2];
 #pragma unroll
-        for (int c = 0; c < H; ++c) {
-            m[c] = 0.0f;
-            l[c] = 0.0f;
-        }
+        for (int c = 0; c < H / 2; ++c) l[c] = both(0.0f);
+        const int seen = w.s.L - w.s.T + w.chunk(heads) * (kBs8Rows / kGroup);      // last position that the chunk's first token sees
         for (int i = 0; i < w.tiles; ++i, ++it) {
             const uint32_t b = it & 1, slot = it % kMeta;
             const int p0 = (w.tile + i) * kBs8Tile;
             ok = ok && mbar_wait_fast(&sm.meta_full[slot], (it / kMeta) & 1, &sm.abort);
-            const float ks = sm.meta[slot][p >> 4] * (1.44269504f / 16.0f), vs = sm.meta[slot][8 + (p >> 4)];
-            const int ev = min(kBs8MaxExp, max(-kBs8MaxExp, (int)((__float_as_uint(vs) >> 23) & 0xff) - 127));   // a block behind the context may hold anything
+            const float ks = sm.meta[slot][p >> 4] * (1.44269504f / 16.0f);
+            // a block behind the context may hold anything
+            const int ev = min(kBs8MaxExp, max(-kBs8MaxExp, (int)((__float_as_uint(sm.meta[slot][8 + (p >> 4)]) >> 23) & 0xff) - 127));
             const bool hidden = sm.bad_page[slot] != 0;
             ok = ok && mbar_wait_fast(&sm.s_full[b], (it >> 1) & 1, &sm.abort);
             __syncwarp();
             tc_fence_after();
             float d[H];
+            float2* d2 = reinterpret_cast<float2*>(d);
             {
                 float s2[H];
                 tmem_load<H>(lanes + b * C::kS + r0, d);
                 tmem_load<H>(lanes + b * C::kS + R + r0, s2);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < H; ++c) d[c] += s2[c];
+                for (int c = 0; c < H / 2; ++c) d2[c] = add2(d2[c], reinterpret_cast<float2*>(s2)[c]);
             }
             tc_fence_before();
             mbar_arrive(&sm.s_free[b]);
-            float top = -CUDART_INF_F;
 #pragma unroll
             for (int c = 0; c < H; c += 4) {
-                const float4 rs = *reinterpret_cast<const float4*>(&sm.rs[r0 + c]);
-                d[c] = fmaf(d[c] * rs.x, ks, (float)ev - m[c]);
-                d[c + 1] = fmaf(d[c + 1] * rs.y, ks, (float)ev - m[c + 1]);
-                d[c + 2] = fmaf(d[c + 2] * rs.z, ks, (float)ev - m[c + 2]);
-                d[c + 3] = fmaf(d[c + 3] * rs.w, ks, (float)ev - m[c + 3]);
+                const float4 rs = *reinterpret_cast<const float4*>(&sm.rs[r0 + c]), m = *reinterpret_cast<const float4*>(&sm.m[r0 + c]);
+                d2[c / 2] = fma2(mul2(d2[c / 2], make_float2(rs.x, rs.y)), both(ks), add2(both((float)ev), make_float2(-m.x, -m.y)));
+                d2[c / 2 + 1] = fma2(mul2(d2[c / 2 + 1], make_float2(rs.z, rs.w)), both(ks), add2(both((float)ev), make_float2(-m.z, -m.w)));
             }
-            const bool tail = hidden || p0 + kBs8Tile > w.s.L - w.s.T + T0 + 1;
-            if (tail) {
+            if (hidden || p0 + kBs8Tile > seen + 1) {
                 // row r sees positions up to L - T + its token
-                const int ahead = hidden ? (1 << 20) : p0 + p - (w.s.L - w.s.T + T0);
+                const int ahead = hidden ? (1 << 20) : p0 + p - seen;
 #pragma unroll
                 for (int c = 0; c < H; ++c)
                     if (ahead > ((r0 + c) >> 3) || p0 + p >= w.s.L) d[c] = -CUDART_INF_F;
             }
+            float top = d[0];
 #pragma unroll
-            for (int c = 0; c < H; ++c) top = fmaxf(top, d[c]);
+            for (int c = 1; c < H; ++c) top = fmaxf(top, d[c]);
             if (named_or(bar, 128, i == 0 || top > kRaise || !ok)) {
                 if (named_or(bar, 128, !ok)) {
                     ok = false;
@@ -358,57 +378,59 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                 // new maxima of the rows over the tile's positions
 #pragma unroll
                 for (int c = 0; c < H; ++c) {
-                    const int x = __reduce_max_sync(0xffffffffu, ordered(d[c] + m[c]));
+                    const int x = __reduce_max_sync(0xffffffffu, ordered(d[c] + sm.m[r0 + c]));
                     if (lane == 0) sm.red[wg][quarter][c] = unordered(x);
                 }
                 named_sync(bar, 128);
-                float f[H];
-#pragma unroll
-                for (int c = 0; c < H; ++c) {
-                    const float x = fmaxf(fmaxf(sm.red[wg][0][c], sm.red[wg][1][c]), fmaxf(sm.red[wg][2][c], sm.red[wg][3][c]));
+                if (p < H) {
+                    const float x = fmaxf(fmaxf(sm.red[wg][0][p], sm.red[wg][1][p]), fmaxf(sm.red[wg][2][p], sm.red[wg][3][p]));
+                    const float m = sm.m[r0 + p];
                     // the first tile sets m; a row that sees nothing of it sees nothing of the segment's later tiles either
-                    const float now = i > 0 ? fmaxf(m[c], x - kAbove) : x > -CUDART_INF_F ? x - kAbove : 0.0f;
-                    f[c] = fast_exp2(m[c] - now);
-                    d[c] += m[c] - now;
-                    l[c] *= f[c];
-                    m[c] = now;
+                    const float now = i > 0 ? fmaxf(m, x - kAbove) : x > -CUDART_INF_F ? x - kAbove : 0.0f;
+                    sm.m[r0 + p] = now;
+                    sm.dm[r0 + p] = m - now;
+                }
+                named_sync(bar, 128);
+#pragma unroll
+                for (int c = 0; c < H / 2; ++c) {
+                    const float2 dm = *reinterpret_cast<const float2*>(&sm.dm[r0 + 2 * c]);
+                    d2[c] = add2(d2[c], dm);
+                    if (i > 0) l[c] = mul2(l[c], make_float2(fast_exp2(dm.x), fast_exp2(dm.y)));
                 }
                 if (i > 0) {
                     ok = mbar_wait_fast(&sm.p_free[b ^ 1], ((it - 1) >> 1) & 1, &sm.abort);      // PV of the tile before, and all earlier ones
                     __syncwarp();
                     tc_fence_after();
+#pragma unroll 1
+                    for (int g = 0; g < 2 * H; g += 8) {
+                        const uint32_t at = lanes + C::kO + (g / H) * R + r0 + g % H;
+                        float o[8];
+                        tmem_load<8>(at, o);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int g = 0; g < H; g += 8) {
-                            float o[8];
-                            tmem_load<8>(lanes + C::kO + h * R + r0 + g, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) o[c] *= f[g + c];
-                            tmem_store<8>(lanes + C::kO + h * R + r0 + g, o);
-                        }
+                        for (int c = 0; c < 8; ++c) o[c] *= fast_exp2(sm.dm[r0 + g % H + c]);
+                        tmem_store<8>(at, o);
+                    }
                     tmem_st_wait();
                 }
             }
-            const float iv = __uint_as_float((uint32_t)(127 - ev) << 23);       // 2^-eV
-#pragma unroll
-            for (int c = 0; c < H; ++c) {
-                d[c] = fast_exp2(d[c]);
-                l[c] = fmaf(d[c], iv, l[c]);
-            }
-            if (it >= 2) ok = ok && mbar_wait_fast(&sm.p_free[b], ((it >> 1) + 1) & 1, &sm.abort);
+            const float2 iv = both(__uint_as_float((uint32_t)(127 - ev) << 23));       // 2^-eV
             uint32_t w1[H / 4], w2[H / 4], w3[H / 4];
 #pragma unroll
             for (int c = 0; c < H / 4; ++c) {
-                const uint32_t a0 = f16_pair(d[4 * c], d[4 * c + 1]), b0 = f16_pair(d[4 * c + 2], d[4 * c + 3]);
-                const uint32_t a1 = e5m2_of(a0), b1 = e5m2_of(b0), ar = sub2(a0, a1), br = sub2(b0, b1);
-                const uint32_t a2 = e5m2_of(ar), b2 = e5m2_of(br);
-                const uint32_t a3 = sub2(ar, a2) + 0x00800080u, b3 = sub2(br, b2) + 0x00800080u;
-                w1[c] = __byte_perm(a1, b1, 0x7531);
-                w2[c] = __byte_perm(a2, b2, 0x7531);
+                const float2 x = make_float2(fast_exp2(d[4 * c]), fast_exp2(d[4 * c + 1]));
+                const float2 y = make_float2(fast_exp2(d[4 * c + 2]), fast_exp2(d[4 * c + 3]));
+                l[2 * c] = fma2(x, iv, l[2 * c]);
+                l[2 * c + 1] = fma2(y, iv, l[2 * c + 1]);
+                // E5M2 is the upper byte of fp16: the first two codes are cut off, the third is rounded (half a step: 0x80)
+                const uint32_t a0 = f16_pair(x.x, x.y), b0 = f16_pair(y.x, y.y);
+                const uint32_t ar = sub2(a0, a0 & 0xff00ff00u), br = sub2(b0, b0 & 0xff00ff00u);
+                const uint32_t a3 = sub2(ar, ar & 0xff00ff00u) + 0x00800080u, b3 = sub2(br, br & 0xff00ff00u) + 0x00800080u;
+                w1[c] = __byte_perm(a0, b0, 0x7531);
+                w2[c] = __byte_perm(ar, br, 0x7531);
                 w3[c] = __byte_perm(a3, b3, 0x7531);
             }
+            if (it >= 2) ok = ok && mbar_wait_fast(&sm.p_free[b], ((it >> 1) + 1) & 1, &sm.abort);
             uint8_t* to = sm.p[b][0] + ((p >> 3) * (R / 16) + r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
             if constexpr (H == 8) {
                 *reinterpret_cast<uint2*>(to) = make_uint2(w1[0], w1[1]);
@@ -436,53 +458,51 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
         }
         vcnt += 2 * w.tiles;
         ok = ok && mbar_wait_fast(&sm.p_free[(it - 1) & 1], ((it - 1) >> 1) & 1, &sm.abort);
-        if (named_or(1 + C::kWgs, C::kSoftmax, !ok)) {      // all softmax warps leave together
+        if (named_or(kAll, C::kSoftmax, !ok)) {      // all softmax warps leave together
             ok = false;
             break;
         }
         tc_fence_after();
         // row sums over the positions
 #pragma unroll
-        for (int c = 0; c < H; ++c) {
+        for (int c = 0; c < H / 2; ++c) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
-            if (lane == 0) sm.red[wg][quarter][c] = l[c];
+            for (int o = 16; o > 0; o >>= 1)
+                l[c] = add2(l[c], make_float2(__shfl_xor_sync(0xffffffffu, l[c].x, o), __shfl_xor_sync(0xffffffffu, l[c].y, o)));
+            if (lane == 0) *reinterpret_cast<float2*>(&sm.red[wg][quarter][2 * c]) = l[c];
         }
         named_sync(bar, 128);
-#pragma unroll
-        for (int c = 0; c < H; ++c) l[c] = (sm.red[wg][0][c] + sm.red[wg][1][c]) + (sm.red[wg][2][c] + sm.red[wg][3][c]);
+        const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
         const bool whole = w.whole();
         float* part = a.partials + ((size_t)blockIdx.x * 2 + w.part()) * kBs8PartFloats;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-        const int64_t q0 = (int64_t)a.q_offsets[w.slot] + T0;
-#pragma unroll
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                             (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim;
+        auto sum = [&](int c) { return (sm.red[wg][0][c] + sm.red[wg][1][c]) + (sm.red[wg][2][c] + sm.red[wg][3][c]); };
+        if (!whole && p < H && r0 + p < nrows) {
+            const float mine = sum(p);
+            *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * (r0 + p)) =
+                make_float2(mine != 0.0f ? sm.m[r0 + p] : -CUDART_INF_F, mine);      // an empty partial weighs nothing
+        }
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             float o[H];
             tmem_load<H>(lanes + C::kO + h * R + r0, o);
             tmem_ld_wait();
+            const int dim = h * 128 + p;
 #pragma unroll
             for (int c = 0; c < H; ++c) {
-                const int r = r0 + c, dim = h * 128 + p;
+                const int r = r0 + c;
                 if (r >= nrows) continue;
-                if (whole)
-                    out[((q0 + (r >> 3)) * heads * kGroup + w.head(heads) * kGroup + (r & 7)) * kHeadDim + dim] =
-                        __float2bfloat16_rn(l[c] != 0.0f ? __fdividef(o[c], l[c]) : 0.0f);
-                else
+                if (whole) {
+                    const float n = sum(c);
+                    out[((int64_t)(r >> 3) * heads * kGroup + (r & 7)) * kHeadDim + dim] = __float2bfloat16_rn(n != 0.0f ? __fdividef(o[c], n) : 0.0f);
+                } else {
                     part[r * kHeadDim + dim] = o[c];
+                }
             }
         }
-        if (!whole && p < H && r0 + p < nrows) {
-            float mine = 0.0f, sum = 0.0f;
-#pragma unroll
-            for (int c = 0; c < H; ++c)
-                if (c == p) {
-                    mine = m[c];
-                    sum = l[c];
-                }
-            *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * (r0 + p)) = make_float2(sum != 0.0f ? mine : -CUDART_INF_F, sum);      // an empty partial weighs nothing
-        }
         tc_fence_before();
-        named_sync(1 + C::kWgs, C::kSoftmax);           // all groups have read rs before the next segment's queries
+        named_sync(kAll, C::kSoftmax);     // all groups are done with rs, m and red before the next segment's queries
     } while (w.next(a));
     if (!ok && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_TIMEOUT);
 }
