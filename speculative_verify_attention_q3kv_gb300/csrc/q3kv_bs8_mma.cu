@@ -17,8 +17,8 @@
 // than 2^7 of headroom (a vote per tile), so most tiles need no maximum and no rescaling.
 //
 // Bound: the codes' bytes.  At 8 tokens a tile's 64 KiB take about 2,900 cycles of an SM's share of HBM, its 32 MMAs about
-// 1,700 and its softmax less.  One CTA per SM; warp 0 copies, warp 1 issues the MMAs, the others are the softmax: groups of four warps
-// with a thread per position and 8 or 16 rows.
+// 1,700 and its softmax less.  One CTA per SM; warp 0 copies, warps 1-3 issue the MMAs, the others are the softmax: groups of
+// four warps with a thread per position and 8 or 16 rows.
 #include <math_constants.h>
 
 #include "q3kv_bs8.cuh"
@@ -34,27 +34,28 @@ constexpr int kMeta = 8;                       // tiles whose scales are kept
 
 template <int R>
 struct Cfg {
-    static constexpr int kStages = R == 64 ? 4 : R == 32 ? 5 : 6;
+    static constexpr int kK = R == 64 ? 2 : 3, kV = 3;                 // tiles of K and of V in shared memory: V waits for the softmax
     static constexpr int kWgs = R == 64 ? 4 : 2;                        // softmax warpgroups, each with all positions and R / kWgs rows
     static constexpr int kH = R / kWgs;                                // rows per softmax thread
-    static constexpr int kSoftmax = 128 * kWgs, kThreads = 64 + kSoftmax;
+    static constexpr int kSoftmax = 128 * kWgs, kThreads = 128 + kSoftmax;
     static constexpr uint32_t kS = 2 * R, kO = 4 * R;                  // TMEM columns: S buffers of 2 R, then O halves of R
     static constexpr uint32_t kTmem = R == 64 ? 512 : R == 32 ? 256 : 128;
 };
 
 template <int R>
 struct Smem {
-    alignas(128) uint8_t kv[Cfg<R>::kStages][kTileBytes];
+    alignas(128) uint8_t k[Cfg<R>::kK][kTileBytes];
+    alignas(128) uint8_t v[Cfg<R>::kV][kTileBytes];
     alignas(128) uint8_t q[2 * R * kHeadDim];
-    alignas(128) uint8_t p[2][3][R * kBs8Tile];
+    alignas(128) uint8_t p[3][R * kBs8Tile];
     alignas(16) float meta[kMeta][16];         // K scales of a tile's 8 blocks, then V scales
-    alignas(16) float rs[R], m[R], dm[R];      // of each row: 2^-k, the subtracted maximum, its last change
+    alignas(16) float rs[R], m[R], dm[R];      // of each row: 2^-k, the maximum negated, its last change
     float red[Cfg<R>::kWgs][4][Cfg<R>::kH];
     Bs8Share first;
     int bad_page[kMeta];
     uint32_t tmem;
     volatile int abort;
-    unsigned long long full[Cfg<R>::kStages], empty[Cfg<R>::kStages], s_full[2], s_free[2], p_full[2], p_free[2], q_full, drained, meta_full[kMeta];
+    unsigned long long k_full[Cfg<R>::kK], k_free[Cfg<R>::kK], v_full[Cfg<R>::kV], v_free[Cfg<R>::kV], s_full[2], s_free[2], p_full, p_free, q_full, drained, meta_full[kMeta];
 };
 
 // Instruction descriptor, kind::f8f6f4: E4M3 A, E4M3 or E5M2 B, fp32 D, M = 128.
@@ -108,20 +109,22 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return as_u32(__hsub2(as_h2(a), as_h2(b))); }
 
 // ---------------------------------------------------------------- roles
+// A barrier is waited for by parity, so whoever waits for one has to see each of its phases: K and V have rings of their own.
+//
 // Bulk copies of a segment's tiles in the order of their use: K0 K1 V0 K2 V1 ... V(n-2) V(n-1).
 template <int R>
 __device__ void produce(const Bs8Args& a, Smem<R>& sm, Bs8Share w) {
+    using C = Cfg<R>;
     const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
-    uint32_t cnt = 0, it = 0, issued = 0, metas = 0;
+    uint32_t it = 0, ks = 0, vs = 0;       // tiles before the segment; copies of K and of V so far
     bool ok = true;
     do {
         const int32_t* table = a.page_table + (int64_t)w.slot * a.max_pages_per_slot;
         const int last_page = (w.tile + w.tiles - 1) >> 1;
         int window = (w.tile >> 1) - 32, ids = 0;
         const uint8_t* prev = nullptr;
-        uint32_t prev_half = 0;
         for (int i = 0; i <= w.tiles && ok; ++i) {
-            const int tile = w.tile + i;
+            const int tile = w.tile + i, half = tile & 1;
             const uint8_t* unit = nullptr;
             if (i < w.tiles) {
                 const int pg = tile >> 1;
@@ -134,99 +137,99 @@ __device__ void produce(const Bs8Args& a, Smem<R>& sm, Bs8Share w) {
                 if (bad) id = 0;
                 unit = a.pool + bs8_offset(a.num_layers, heads, id, a.layer, w.head(heads), 0);
                 if (lane == 0) {
-                    const uint32_t st = cnt % Cfg<R>::kStages, half = tile & 1, slot = (it + i) % kMeta;
-                    ok = cnt < Cfg<R>::kStages || mbar_wait(&sm.empty[st], (cnt / Cfg<R>::kStages + 1) & 1, &sm.abort);
+                    const uint32_t t = it + i, st = t % C::kK, slot = t % kMeta;
+                    ok = t < C::kK || mbar_wait(&sm.k_free[st], (t / C::kK + 1) & 1, &sm.abort);
                     if (ok) {
                         if (bad && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
                         sm.bad_page[slot] = bad;
                         mbar_arrive_expect_tx(&sm.meta_full[slot], 64);
                         bulk_g2s(&sm.meta[slot][0], unit + kBs8CodeBytes + half * 32, 32, &sm.meta_full[slot]);
                         bulk_g2s(&sm.meta[slot][8], unit + kBs8UnitBytes + kBs8CodeBytes + half * 32, 32, &sm.meta_full[slot]);
-                        mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
-                        bulk_g2s(sm.kv[st], unit + half * kTileBytes, kTileBytes, &sm.full[st]);
-                        issued = cnt + 1;
-                        metas = it + i + 1;
+                        mbar_arrive_expect_tx(&sm.k_full[st], kTileBytes);
+                        bulk_g2s(sm.k[st], unit + half * kTileBytes, kTileBytes, &sm.k_full[st]);
+                        ks = t + 1;
                     }
                 }
-                ++cnt;
+                unit += kBs8UnitBytes + half * kTileBytes;         // V of the same tile
             }
-            if (i > 0) {
-                if (lane == 0 && ok) {
-                    const uint32_t st = cnt % Cfg<R>::kStages;
-                    ok = cnt < Cfg<R>::kStages || mbar_wait(&sm.empty[st], (cnt / Cfg<R>::kStages + 1) & 1, &sm.abort);
-                    if (ok) {
-                        mbar_arrive_expect_tx(&sm.full[st], kTileBytes);
-                        bulk_g2s(sm.kv[st], prev + kBs8UnitBytes + prev_half * kTileBytes, kTileBytes, &sm.full[st]);
-                        issued = cnt + 1;
-                    }
+            if (i > 0 && lane == 0 && ok) {
+                const uint32_t t = it + i - 1, st = t % C::kV;
+                ok = t < C::kV || mbar_wait(&sm.v_free[st], (t / C::kV + 1) & 1, &sm.abort);
+                if (ok) {
+                    mbar_arrive_expect_tx(&sm.v_full[st], kTileBytes);
+                    bulk_g2s(sm.v[st], prev, kTileBytes, &sm.v_full[st]);
+                    vs = t + 1;
                 }
-                ++cnt;
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             prev = unit;
-            prev_half = tile & 1;
         }
         it += w.tiles;
     } while (ok && w.next(a));
     // no copy may land after the CTA is gone, whatever stopped the others
     if (lane == 0) {
-        for (uint32_t c = issued > Cfg<R>::kStages ? issued - Cfg<R>::kStages : 0; c < issued; ++c)
-            mbar_drain(&sm.full[c % Cfg<R>::kStages], (c / Cfg<R>::kStages) & 1);
-        for (uint32_t t = metas > kMeta ? metas - kMeta : 0; t < metas; ++t) mbar_drain(&sm.meta_full[t % kMeta], (t / kMeta) & 1);
+        for (uint32_t t = ks > C::kK ? ks - C::kK : 0; t < ks; ++t) mbar_drain(&sm.k_full[t % C::kK], (t / C::kK) & 1);
+        for (uint32_t t = vs > C::kV ? vs - C::kV : 0; t < vs; ++t) mbar_drain(&sm.v_full[t % C::kV], (t / C::kV) & 1);
+        for (uint32_t t = ks > kMeta ? ks - kMeta : 0; t < ks; ++t) mbar_drain(&sm.meta_full[t % kMeta], (t / kMeta) & 1);
     }
     __syncwarp();
 }
 
-// MMAs, by one thread.  Within a segment QK of the next tile goes before PV of this one, so the tensor pipe works while
-// the softmax does.
+// MMAs, by one thread of each of three warps: QK, and PV into the two halves of O.  A thread needs about 100 cycles to
+// form the descriptors of an MMA and issue it, twice what the tensor pipe takes for one, so one thread would bound a tile
+// (32 MMAs).  Each waits for its own operands only: QK of later tiles runs while the softmax works on this one.
 template <int R>
-__device__ void issue(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
+__device__ void issue_qk(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
     using C = Cfg<R>;
-    const uint32_t id_qk = idesc8(2 * R, false, false), id_pv = idesc8(R, true, true);
-    const uint64_t kdesc = make_desc(smem_u32(sm.kv[0]), 128, 2048), vdesc = make_desc(smem_u32(sm.kv[0]), 2048, 128);
-    const uint64_t qdesc = make_desc(smem_u32(sm.q), 128, 2048), pdesc = make_desc(smem_u32(sm.p[0][0]), R / 16 * 128, 128);
-    uint32_t cnt = 0, it = 0, seg = 0;
+    const uint64_t kdesc = make_desc(smem_u32(sm.k[0]), 128, 2048), qdesc = make_desc(smem_u32(sm.q), 128, 2048);
+    uint32_t it = 0, seg = 0;
     bool ok = true;
     do {
-        for (int i = 0; i <= w.tiles && ok; ++i) {
-            if (i < w.tiles) {                                     // QK of tile i
-                const uint32_t t = it + i, b = t & 1, st = cnt % C::kStages;
-                if (i == 0) ok = mbar_wait(&sm.q_full, seg & 1, &sm.abort);
-                ok = ok && mbar_wait(&sm.full[st], (cnt / C::kStages) & 1, &sm.abort);
-                if (t >= 2) ok = ok && mbar_wait(&sm.s_free[b], ((t >> 1) + 1) & 1, &sm.abort);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t ad = kdesc + st * (kTileBytes / 16);
+        ok = mbar_wait(&sm.q_full, seg & 1, &sm.abort);
+        for (int i = 0; i < w.tiles && ok; ++i) {
+            const uint32_t t = it + i, b = t & 1, st = t % C::kK;
+            ok = mbar_wait(&sm.k_full[st], (t / C::kK) & 1, &sm.abort);
+            if (t >= 2) ok = ok && mbar_wait(&sm.s_free[b], ((t >> 1) + 1) & 1, &sm.abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = kdesc + st * (kTileBytes / 16);
 #pragma unroll
-                for (int k = 0; k < kHeadDim / 32; ++k) mma8(tmem + b * C::kS, ad + k * 16, qdesc + k * 16, id_qk, k > 0);
-                mma_commit(&sm.empty[st]);
-                mma_commit(&sm.s_full[b]);
-                ++cnt;
-            }
-            if (i > 0) {                                           // PV of tile i - 1
-                const uint32_t t = it + i - 1, b = t & 1, st = cnt % C::kStages;
-                ok = mbar_wait(&sm.full[st], (cnt / C::kStages) & 1, &sm.abort) && mbar_wait(&sm.p_full[b], (t >> 1) & 1, &sm.abort);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t ad = vdesc + st * (kTileBytes / 16), bd = pdesc + b * (3 * R * kBs8Tile / 16);
-#pragma unroll
-                for (int part = 0; part < 3; ++part)
-#pragma unroll
-                    for (int k = 0; k < kBs8Tile / 32; ++k)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            mma8(tmem + C::kO + h * R, ad + k * (8192 / 16) + h * (1024 / 16),
-                                 bd + part * (R * kBs8Tile / 16) + k * (4 * (R / 16) * 128 / 16), id_pv, i > 1 || part > 0 || k > 0);
-                mma_commit(&sm.empty[st]);
-                mma_commit(&sm.p_free[b]);
-                ++cnt;
-            }
+            for (int k = 0; k < kHeadDim / 32; ++k) mma8(tmem + b * C::kS, ad + k * 16, qdesc + k * 16, idesc8(2 * R, false, false), k > 0);
+            mma_commit(&sm.k_free[st]);
+            mma_commit(&sm.s_full[b]);
         }
         it += w.tiles;
         ++seg;
     } while (ok && w.next(a));
-    mma_commit(&sm.drained);               // TMEM and the operands stay until the last MMA is done
-    mbar_drain(&sm.drained, 0);
+    mma_commit(&sm.drained);
+}
+
+template <int R>
+__device__ void issue_pv(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem, int half) {
+    using C = Cfg<R>;
+    const uint64_t vdesc = make_desc(smem_u32(sm.v[0]) + half * 1024, 2048, 128), pdesc = make_desc(smem_u32(sm.p[0]), R / 16 * 128, 128);
+    const uint32_t o = tmem + C::kO + half * R;
+    uint32_t it = 0;
+    bool ok = true;
+    do {
+        for (int i = 0; i < w.tiles && ok; ++i) {
+            const uint32_t t = it + i, st = t % C::kV;
+            ok = mbar_wait(&sm.v_full[st], (t / C::kV) & 1, &sm.abort) && mbar_wait(&sm.p_full, t & 1, &sm.abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = vdesc + st * (kTileBytes / 16);
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int k = 0; k < kBs8Tile / 32; ++k)
+                    mma8(o, ad + k * (8192 / 16), pdesc + part * (R * kBs8Tile / 16) + k * (4 * (R / 16) * 128 / 16), idesc8(R, true, true),
+                         i > 0 || part > 0 || k > 0);
+            mma_commit(&sm.v_free[st]);
+            mma_commit(&sm.p_free);
+        }
+        it += w.tiles;
+    } while (ok && w.next(a));
+    mma_commit(&sm.drained);
 }
 
 // The queries of a segment as two E4M3 codes per value; a row that is not finite gets a NaN scale and comes out as NaN.
@@ -286,6 +289,12 @@ __device__ __forceinline__ int ordered(float f) {          // integers in the or
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
+// One arrival per warp.
+__device__ __forceinline__ void warp_arrive(unsigned long long* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // Pairs of float32 in one instruction.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 r;
@@ -315,17 +324,17 @@ template <int R>
 __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
     using C = Cfg<R>;
     constexpr int H = C::kH, kAll = 1 + C::kWgs;                     // kAll: barrier of all softmax warps
-    const int tid = threadIdx.x - 64, lane = threadIdx.x & 31, warp = tid >> 5, heads = a.num_kv_heads;
+    const int tid = threadIdx.x - 128, lane = threadIdx.x & 31, warp = tid >> 5, heads = a.num_kv_heads;
     const int wg = warp >> 2, quarter = (threadIdx.x >> 5) & 3;      // rows wg H .., positions 32 quarter ..: a warp reads its own TMEM lanes
     const int p = quarter * 32 + lane, r0 = wg * H, bar = 1 + wg;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    uint32_t it = 0, vcnt = 0;             // vcnt: copies before this segment's
+    uint32_t it = 0;
     bool ok = true;
     do {
         prepare_q<R>(a, sm, w, warp);
         if (tid < R) sm.m[tid] = 0.0f;
         fence_proxy_async();
-        mbar_arrive(&sm.q_full);
+        warp_arrive(&sm.q_full);
         named_sync(kAll, C::kSoftmax);     // rs and m are there
         float2 l[H / 2];
 #pragma unroll
@@ -353,12 +362,12 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                 for (int c = 0; c < H / 2; ++c) d2[c] = add2(d2[c], reinterpret_cast<float2*>(s2)[c]);
             }
             tc_fence_before();
-            mbar_arrive(&sm.s_free[b]);
+            warp_arrive(&sm.s_free[b]);
 #pragma unroll
             for (int c = 0; c < H; c += 4) {
                 const float4 rs = *reinterpret_cast<const float4*>(&sm.rs[r0 + c]), m = *reinterpret_cast<const float4*>(&sm.m[r0 + c]);
-                d2[c / 2] = fma2(mul2(d2[c / 2], make_float2(rs.x, rs.y)), both(ks), add2(both((float)ev), make_float2(-m.x, -m.y)));
-                d2[c / 2 + 1] = fma2(mul2(d2[c / 2 + 1], make_float2(rs.z, rs.w)), both(ks), add2(both((float)ev), make_float2(-m.z, -m.w)));
+                d2[c / 2] = fma2(mul2(d2[c / 2], make_float2(rs.x, rs.y)), both(ks), add2(both((float)ev), make_float2(m.x, m.y)));
+                d2[c / 2 + 1] = fma2(mul2(d2[c / 2 + 1], make_float2(rs.z, rs.w)), both(ks), add2(both((float)ev), make_float2(m.z, m.w)));
             }
             if (hidden || p0 + kBs8Tile > seen + 1) {
                 // row r sees positions up to L - T + its token
@@ -378,16 +387,16 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                 // new maxima of the rows over the tile's positions
 #pragma unroll
                 for (int c = 0; c < H; ++c) {
-                    const int x = __reduce_max_sync(0xffffffffu, ordered(d[c] + sm.m[r0 + c]));
+                    const int x = __reduce_max_sync(0xffffffffu, ordered(d[c] - sm.m[r0 + c]));
                     if (lane == 0) sm.red[wg][quarter][c] = unordered(x);
                 }
                 named_sync(bar, 128);
                 if (p < H) {
                     const float x = fmaxf(fmaxf(sm.red[wg][0][p], sm.red[wg][1][p]), fmaxf(sm.red[wg][2][p], sm.red[wg][3][p]));
-                    const float m = sm.m[r0 + p];
+                    const float m = -sm.m[r0 + p];
                     // the first tile sets m; a row that sees nothing of it sees nothing of the segment's later tiles either
                     const float now = i > 0 ? fmaxf(m, x - kAbove) : x > -CUDART_INF_F ? x - kAbove : 0.0f;
-                    sm.m[r0 + p] = now;
+                    sm.m[r0 + p] = -now;
                     sm.dm[r0 + p] = m - now;
                 }
                 named_sync(bar, 128);
@@ -398,7 +407,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                     if (i > 0) l[c] = mul2(l[c], make_float2(fast_exp2(dm.x), fast_exp2(dm.y)));
                 }
                 if (i > 0) {
-                    ok = mbar_wait_fast(&sm.p_free[b ^ 1], ((it - 1) >> 1) & 1, &sm.abort);      // PV of the tile before, and all earlier ones
+                    ok = mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);      // PV of the tile before, and all earlier ones
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -430,8 +439,8 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                 w2[c] = __byte_perm(ar, br, 0x7531);
                 w3[c] = __byte_perm(a3, b3, 0x7531);
             }
-            if (it >= 2) ok = ok && mbar_wait_fast(&sm.p_free[b], ((it >> 1) + 1) & 1, &sm.abort);
-            uint8_t* to = sm.p[b][0] + ((p >> 3) * (R / 16) + r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
+            if (it > 0) ok = ok && mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);
+            uint8_t* to = sm.p[0] + ((p >> 3) * (R / 16) + r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
             if constexpr (H == 8) {
                 *reinterpret_cast<uint2*>(to) = make_uint2(w1[0], w1[1]);
                 *reinterpret_cast<uint2*>(to + R * kBs8Tile) = make_uint2(w2[0], w2[1]);
@@ -444,20 +453,19 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
             const int valid = hidden ? 0 : w.s.L - p0;
             if (valid < kBs8Tile) {
                 // rows behind the context may hold anything, and 0 x NaN is NaN: they become zeros before PV reads them
-                const uint32_t at = vcnt + (i + 1 < w.tiles ? 2 * i + 2 : 2 * i + 1), st = at % C::kStages;
-                ok = ok && mbar_wait_fast(&sm.full[st], (at / C::kStages) & 1, &sm.abort);
+                const uint32_t st = it % C::kV;
+                ok = ok && mbar_wait_fast(&sm.v_full[st], (it / C::kV) & 1, &sm.abort);      // PV(it - 1) has seen the phase before
                 if (p >= valid) {
 #pragma unroll
                     for (int c = 0; c < 16 / C::kWgs; ++c)
-                        *reinterpret_cast<uint4*>(sm.kv[st] + ((p >> 3) * 16 + wg * (16 / C::kWgs) + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(sm.v[st] + ((p >> 3) * 16 + wg * (16 / C::kWgs) + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
             }
             fence_proxy_async();
             tc_fence_before();
-            mbar_arrive(&sm.p_full[b]);
+            warp_arrive(&sm.p_full);
         }
-        vcnt += 2 * w.tiles;
-        ok = ok && mbar_wait_fast(&sm.p_free[(it - 1) & 1], ((it - 1) >> 1) & 1, &sm.abort);
+        ok = ok && mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);
         if (named_or(kAll, C::kSoftmax, !ok)) {      // all softmax warps leave together
             ok = false;
             break;
@@ -481,7 +489,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
         if (!whole && p < H && r0 + p < nrows) {
             const float mine = sum(p);
             *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * (r0 + p)) =
-                make_float2(mine != 0.0f ? sm.m[r0 + p] : -CUDART_INF_F, mine);      // an empty partial weighs nothing
+                make_float2(mine != 0.0f ? -sm.m[r0 + p] : -CUDART_INF_F, mine);      // an empty partial weighs nothing
         }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -515,18 +523,22 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1) verify_bs8_mma_kernel(Bs8
     const int warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 32) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], 1);
+        for (int i = 0; i < C::kK; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_free[i], 1);
+        }
+        for (int i = 0; i < C::kV; ++i) {
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_free[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.s_free[i], C::kSoftmax);
-            mbar_init(&sm.p_full[i], C::kSoftmax);
-            mbar_init(&sm.p_free[i], 1);
+            mbar_init(&sm.s_free[i], C::kSoftmax / 32);
         }
-        mbar_init(&sm.q_full, C::kSoftmax);
-        mbar_init(&sm.drained, 1);
+        mbar_init(&sm.p_full, C::kSoftmax / 32);
+        mbar_init(&sm.p_free, 2);
+        mbar_init(&sm.q_full, C::kSoftmax / 32);
+        mbar_init(&sm.drained, 3);
         for (int i = 0; i < kMeta; ++i) mbar_init(&sm.meta_full[i], 1);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -547,8 +559,12 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1) verify_bs8_mma_kernel(Bs8
     if (w.tiles > 0) {
         if (warp == 0) {
             produce<R>(a, sm, w);
-        } else if (warp == 1) {
-            if ((threadIdx.x & 31) == 0) issue<R>(a, sm, w, tmem);
+        } else if (warp < 4) {
+            if ((threadIdx.x & 31) == 0) {
+                if (warp == 1) issue_qk<R>(a, sm, w, tmem);
+                else issue_pv<R>(a, sm, w, tmem, warp - 2);
+                mbar_drain(&sm.drained, 0);        // TMEM and the operands stay until the last MMA is done
+            }
             __syncwarp();
         } else {
             softmax<R>(a, sm, w, tmem);
