@@ -235,59 +235,69 @@ __device__ void issue_pv(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tme
 // The queries of a segment as two E4M3 codes per value; a row that is not finite gets a NaN scale and comes out as NaN.
 template <int R>
 __device__ void prepare_q(const Bs8Args& a, Smem<R>& sm, const Bs8Share& w, int warp) {
+    constexpr int kWarps = Cfg<R>::kSoftmax / 32, kEach = R / kWarps;
     const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
     const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    const int64_t q0 = (int64_t)a.q_offsets[w.slot] + T0;
-    constexpr int kWarps = Cfg<R>::kSoftmax / 32, kEach = R / kWarps;
-    float in[kEach][8] = {};
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                             (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim + 8 * lane;
+    uint4 in[kEach];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int r = warp + i * kWarps;
-        if (r < nrows) load8(q + ((q0 + (r >> 3)) * heads * kGroup + w.head(heads) * kGroup + (r & 7)) * kHeadDim + 8 * lane, in[i]);
+    for (int i = 0; i < kEach; ++i) {            // padding rows load the last row
+        const int r = min(warp + i * kWarps, nrows - 1);
+        in[i] = *reinterpret_cast<const uint4*>(q + ((int64_t)(r >> 3) * heads * kGroup + (r & 7)) * kHeadDim);
     }
 #pragma unroll
     for (int n = 0; n < kEach; ++n) {
         const int r = warp + n * kWarps;
-        float (&x)[8] = in[n];
-        float top = 0.0f;
-        bool finite = true;
+        const uint32_t in4[4] = {in[n].x, in[n].y, in[n].z, in[n].w};
+        // magnitudes are ordered as integers, and what is not finite comes last
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            top = fmaxf(top, fabsf(x[i]));
-            finite = finite && fabsf(x[i]) <= 3.402823466e38f;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        finite = __all_sync(0xffffffffu, finite);
+        for (int i = 0; i < 4; ++i) top = max(top, max(in4[i] & 0x7fffu, (in4[i] >> 16) & 0x7fffu));
+        top = __reduce_max_sync(0xffffffffu, top);
+        const bool finite = top < 0x7f80u, zero = top == 0 || r >= nrows;
         // largest value to 128 .. 256
-        const int k = top > 0.0f && finite ? min(100, 7 - ((int)(__float_as_uint(top) >> 23) - 127)) : 0;
-        const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+        const int k = zero || !finite ? 0 : min(100, 7 - ((int)(top >> 7) - 127));
+        const float up = zero ? 0.0f : __uint_as_float((uint32_t)(k + 127) << 23);
         uint32_t c1[2], c2[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float y[4], d[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = x[4 * i + j] * up;
-            c1[i] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
+            const float2 y0 = make_float2(__uint_as_float(in4[2 * i] << 16) * up, __uint_as_float(in4[2 * i] & 0xffff0000u) * up);
+            const float2 y1 = make_float2(__uint_as_float(in4[2 * i + 1] << 16) * up, __uint_as_float(in4[2 * i + 1] & 0xffff0000u) * up);
+            c1[i] = e4m3_pair(y0.x, y0.y) | (e4m3_pair(y1.x, y1.y) << 16);
             uint32_t h01, h23;
             e4m3x4_to_f16(c1[i], h01, h23);
-            const float2 f01 = __half22float2(as_h2(h01)), f23 = __half22float2(as_h2(h23));
-            d[0] = y[0] - f01.x; d[1] = y[1] - f01.y; d[2] = y[2] - f23.x; d[3] = y[3] - f23.y;
-            c2[i] = e4m3_pair(d[0], d[1]) | (e4m3_pair(d[2], d[3]) << 16);
+            const float2 f0 = __half22float2(as_h2(h01)), f1 = __half22float2(as_h2(h23));
+            c2[i] = e4m3_pair(y0.x - f0.x, y0.y - f0.y) | (e4m3_pair(y1.x - f1.x, y1.y - f1.y) << 16);
         }
         uint8_t* to = sm.q + ((r >> 3) * 16 + (lane >> 1)) * 128 + (r & 7) * 16 + (lane & 1) * 8;
         *reinterpret_cast<uint2*>(to) = make_uint2(c1[0], c1[1]);
         *reinterpret_cast<uint2*>(to + R * kHeadDim) = make_uint2(c2[0], c2[1]);
-        if (lane == 0) sm.rs[r] = finite ? __uint_as_float((uint32_t)(127 - k) << 23) : __int_as_float(0x7fc00000);
+        if (lane == 0) sm.rs[r] = finite || r >= nrows ? __uint_as_float((uint32_t)(127 - k) << 23) : __int_as_float(0x7fc00000);
     }
 }
 
-__device__ __forceinline__ int ordered(float f) {          // integers in the order of the floats
-    const int i = __float_as_int(f);
-    return i ^ ((i >> 31) & 0x7fffffff);
+// Each of H values reduced over the warp, value (lane / (32 / H)) for each lane: halves are exchanged until one is left.
+template <int H, typename Op>
+__device__ __forceinline__ float reduce_rows(const float (&in)[H], Op op) {
+    const int lane = threadIdx.x & 31;
+    float v[H];
+#pragma unroll
+    for (int c = 0; c < H; ++c) v[c] = in[c];
+    int mask = 16;
+#pragma unroll
+    for (int n = H / 2; n > 0; n >>= 1, mask >>= 1) {
+        const bool upper = lane & mask;
+#pragma unroll
+        for (int c = 0; c < n; ++c) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? v[c] : v[c + n], mask);
+            v[c] = op(upper ? v[c + n] : v[c], other);
+        }
+    }
+#pragma unroll
+    for (; mask > 0; mask >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], mask));
+    return v[0];
 }
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 // One arrival per warp.
 __device__ __forceinline__ void warp_arrive(unsigned long long* bar) {
@@ -385,10 +395,12 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                     break;
                 }
                 // new maxima of the rows over the tile's positions
+                {
+                    float t[H];
 #pragma unroll
-                for (int c = 0; c < H; ++c) {
-                    const int x = __reduce_max_sync(0xffffffffu, ordered(d[c] - sm.m[r0 + c]));
-                    if (lane == 0) sm.red[wg][quarter][c] = unordered(x);
+                    for (int c = 0; c < H; ++c) t[c] = d[c] - sm.m[r0 + c];
+                    const float x = reduce_rows<H>(t, [](float u, float v) { return fmaxf(u, v); });
+                    if (lane % (32 / H) == 0) sm.red[wg][quarter][lane / (32 / H)] = x;
                 }
                 named_sync(bar, 128);
                 if (p < H) {
@@ -472,12 +484,9 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
         }
         tc_fence_after();
         // row sums over the positions
-#pragma unroll
-        for (int c = 0; c < H / 2; ++c) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                l[c] = add2(l[c], make_float2(__shfl_xor_sync(0xffffffffu, l[c].x, o), __shfl_xor_sync(0xffffffffu, l[c].y, o)));
-            if (lane == 0) *reinterpret_cast<float2*>(&sm.red[wg][quarter][2 * c]) = l[c];
+        {
+            const float x = reduce_rows<H>(reinterpret_cast<float (&)[H]>(l), [](float u, float v) { return u + v; });
+            if (lane % (32 / H) == 0) sm.red[wg][quarter][lane / (32 / H)] = x;
         }
         named_sync(bar, 128);
         const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
@@ -485,27 +494,33 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
         float* part = a.partials + ((size_t)blockIdx.x * 2 + w.part()) * kBs8PartFloats;
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                              (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim;
-        auto sum = [&](int c) { return (sm.red[wg][0][c] + sm.red[wg][1][c]) + (sm.red[wg][2][c] + sm.red[wg][3][c]); };
-        if (!whole && p < H && r0 + p < nrows) {
-            const float mine = sum(p);
-            *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * (r0 + p)) =
-                make_float2(mine != 0.0f ? -sm.m[r0 + p] : -CUDART_INF_F, mine);      // an empty partial weighs nothing
+        if (p < H) {                       // one thread per row; then all read their rows' factors
+            const float mine = (sm.red[wg][0][p] + sm.red[wg][1][p]) + (sm.red[wg][2][p] + sm.red[wg][3][p]);
+            if (!whole && r0 + p < nrows)
+                *reinterpret_cast<float2*>(part + kBs8Rows * kHeadDim + 2 * (r0 + p)) =
+                    make_float2(mine != 0.0f ? -sm.m[r0 + p] : -CUDART_INF_F, mine);      // an empty partial weighs nothing
+            sm.dm[r0 + p] = mine != 0.0f ? __fdividef(1.0f, mine) : 0.0f;
         }
-#pragma unroll 1
+        named_sync(bar, 128);
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
             float o[H];
             tmem_load<H>(lanes + C::kO + h * R + r0, o);
             tmem_ld_wait();
-            const int dim = h * 128 + p;
+            if (whole) {
+                __nv_bfloat16* to = out + ((int64_t)(r0 >> 3) * heads * kGroup) * kHeadDim + h * 128 + p;
 #pragma unroll
-            for (int c = 0; c < H; ++c) {
-                const int r = r0 + c;
-                if (r >= nrows) continue;
-                if (whole) {
-                    const float n = sum(c);
-                    out[((int64_t)(r >> 3) * heads * kGroup + (r & 7)) * kHeadDim + dim] = __float2bfloat16_rn(n != 0.0f ? __fdividef(o[c], n) : 0.0f);
+                for (int c = 0; c < H; ++c)
+                    if (r0 + c < nrows) to[((int64_t)(c >> 3) * heads * kGroup + (c & 7)) * kHeadDim] = __float2bfloat16_rn(o[c] * sm.dm[r0 + c]);
+            } else {
+                float* to = part + r0 * kHeadDim + h * 128 + p;
+                if (r0 + H <= nrows) {
+#pragma unroll
+                    for (int c = 0; c < H; ++c) to[c * kHeadDim] = o[c];
                 } else {
-                    part[r * kHeadDim + dim] = o[c];
+#pragma unroll
+                    for (int c = 0; c < H; ++c)
+                        if (r0 + c < nrows) to[c * kHeadDim] = o[c];
                 }
             }
         }
