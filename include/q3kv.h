@@ -716,8 +716,8 @@ Q3KV_API int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_
 
 /* Verify attention over it, with q3kv_verify_attn's arguments and masks but for:
  *   out     of q's dtype (float32 or bf16), same indexing as q
- *   impl    Q3KV_IMPL_AUTO: the tensor-core leg for bf16, the CUDA-core leg (float32 arithmetic)
- *           for float32; Q3KV_IMPL_MMA with float32 is Q3KV_ERR_UNSUPPORTED
+ *   impl    Q3KV_IMPL_AUTO = Q3KV_IMPL_MMA: the tensor-core leg; Q3KV_IMPL_FMA: the CUDA-core leg
+ *           (float32 arithmetic)
  *   d_workspace   at least q3kv_bs8_workspace_bytes(...) bytes, 16-byte aligned, no initial
  *           contents needed; its size is the same for every call on a device.  Calls that share
  *           one must not overlap on the GPU.

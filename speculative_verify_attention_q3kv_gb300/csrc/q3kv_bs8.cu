@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_bs8_kernel(AppendArgs a
 }
 
 // ---------------------------------------------------------------- verify attention on CUDA cores
-// Float32 arithmetic throughout, for float32 queries.  One CTA per share; sub-tiles of 64 positions are decoded to
+// The reference leg: float32 arithmetic throughout.  One CTA per share; sub-tiles of 64 positions are decoded to
 // shared memory.  Bound: the FMAs of 64 rows x 64 positions x 256 dims, twice; each thread holds 4 x 4 scores and
 // 8 x 8 outputs, so that two shared 16-byte loads feed 8 (scores) or 16 (outputs) FMAs each.
 constexpr int kFmaThreads = 256;
@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
     const int slot = blockIdx.z, pair = blockIdx.y, r = blockIdx.x;
     const Bs8Slot s = bs8_slot(a, slot, nullptr);
     if (pair >= s.pairs(heads)) return;
-    const int T0 = pair / heads * (kBs8Rows / kGroup), head = pair % heads;
-    if (r >= min(kBs8Rows, kGroup * (s.T - T0))) return;
+    const int T0 = pair / heads * (a.rows / kGroup), head = pair % heads;
+    if (r >= min(a.rows, kGroup * (s.T - T0))) return;
     if (warp < 2) {
         const int64_t n = bs8_tiles_before(a, warp == 0 ? slot : a.num_slots, nullptr);
         if (lane == 0) s_at[warp] = n;
@@ -459,8 +459,8 @@ cudaError_t launch(K kernel, const A& a, dim3 grid, int threads, size_t smem, cu
 
 // The merge's grid covers every pair that may be cut; a call whose pairs are all cut or whole alike has few idle CTAs.
 cudaError_t launch_merge_bs8(const Bs8Args& a, cudaStream_t st) {
-    const int chunks = (kGroup * a.max_n_q + kBs8Rows - 1) / kBs8Rows;
-    const dim3 grid((unsigned)(chunks > 1 ? kBs8Rows : kGroup * a.max_n_q), (unsigned)(chunks * a.num_kv_heads), (unsigned)a.num_slots);
+    const int chunks = (kGroup * a.max_n_q + a.rows - 1) / a.rows;
+    const dim3 grid((unsigned)(chunks > 1 ? a.rows : kGroup * a.max_n_q), (unsigned)(chunks * a.num_kv_heads), (unsigned)a.num_slots);
     return launch(merge_bs8_kernel, a, grid, kMergeThreads, 0, st);
 }
 
@@ -549,7 +549,6 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     if (max_pages_per_slot <= 0) return Q3KV_ERR_INVALID_ARG;
     if (desc && (layer < 0 || layer >= desc->num_layers)) return Q3KV_ERR_INVALID_ARG;
     if (dtype != Q3KV_F32 && dtype != Q3KV_BF16) return Q3KV_ERR_INVALID_ARG;
-    if (impl == Q3KV_IMPL_MMA && dtype == Q3KV_F32) return Q3KV_ERR_UNSUPPORTED;
     int e = bs8_check(desc, num_slots, max_ctx_len, max_n_q, impl);
     if (e != Q3KV_OK) return e;
     if (num_slots == 0 || max_n_q == 0 || max_ctx_len == 0) return Q3KV_OK;
@@ -581,7 +580,8 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     a.partials = static_cast<float*>(d_workspace);
     a.status = d_status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool mma = impl == Q3KV_IMPL_MMA || (impl == Q3KV_IMPL_AUTO && dtype == Q3KV_BF16);
+    const bool mma = impl != Q3KV_IMPL_FMA;
+    a.rows = mma ? bs8_mma_rows(dtype) : kBs8Rows;
     cudaError_t ce = mma ? launch_bs8_mma(a, st) : launch_bs8_fma(a, st);
     if (ce == cudaSuccess) ce = launch_merge_bs8(a, st);
     return cuda_status(ce);

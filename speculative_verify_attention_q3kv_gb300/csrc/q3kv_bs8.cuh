@@ -1,6 +1,6 @@
 // Verify attention over the block-scaled 8-bit cache: what both legs and the merge share.
 //
-// Work is cut into tiles of 128 positions of one (slot, row chunk of 64, kv head) pair.  All tiles of a call,
+// Work is cut into tiles of 128 positions of one (slot, row chunk, kv head) pair.  All tiles of a call,
 // pair after pair, are shared out evenly: CTA i of G takes tiles [i n / G, (i + 1) n / G).  A pair inside one
 // CTA's share goes straight to the output; of a pair that is cut, each CTA writes a partial (unnormalised
 // output, maximum, sum), of which it has at most two: the pair its share begins inside, and the pair it ends
@@ -13,7 +13,7 @@
 namespace q3kv {
 
 constexpr int kBs8Tile = 128;
-constexpr int kBs8Rows = 64;                 // query rows per chunk: 8 tokens of 8 heads
+constexpr int kBs8Rows = 64;                 // query rows per chunk at most: 8 tokens of 8 heads
 constexpr size_t kBs8PartFloats = (size_t)kBs8Rows * (kHeadDim + 2);     // per partial: outputs, then (maximum, sum) per row
 
 struct Bs8Args {
@@ -33,6 +33,7 @@ struct Bs8Args {
     const void* q;
     void* out;
     int32_t dtype;               // of q and out
+    int32_t rows;                // query rows per chunk
     int32_t ctas;                // G
     float* partials;             // [G][2][kBs8PartFloats]
     int32_t* status;
@@ -40,6 +41,7 @@ struct Bs8Args {
 
 cudaError_t launch_bs8_fma(const Bs8Args& a, cudaStream_t stream);
 cudaError_t launch_bs8_mma(const Bs8Args& a, cudaStream_t stream);
+int bs8_mma_rows(int dtype);                 // the tensor-core leg's chunk
 
 // Lengths of one slot; tiles and chunks are 0 for a slot with nothing to do or with lengths the call does not allow.
 struct Bs8Slot {
@@ -54,7 +56,7 @@ __device__ __forceinline__ Bs8Slot bs8_slot(const Bs8Args& a, int b, bool* bad) 
                     a.q_offsets[b] >= 0;
     if (ok) {
         s.tiles = (s.L + kBs8Tile - 1) / kBs8Tile;
-        s.chunks = (kGroup * s.T + kBs8Rows - 1) / kBs8Rows;
+        s.chunks = (kGroup * s.T + a.rows - 1) / a.rows;
     } else if (bad && s.T != 0) {
         *bad = true;
     }

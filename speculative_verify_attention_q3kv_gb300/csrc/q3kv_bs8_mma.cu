@@ -21,6 +21,8 @@
 // four warps with a thread per position and 8 or 16 rows.
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "q3kv_bs8.cuh"
 #include "q3kv_tcgen05.cuh"
 
@@ -30,32 +32,35 @@ namespace {
 constexpr uint32_t kTileBytes = kBs8Tile * kHeadDim;
 constexpr float kAbove = 8.0f;                 // m is set this far below the largest score: p' <= 2^8 then,
 constexpr float kRaise = 15.0f;                // and at most 2^15 until it is raised
+constexpr float kQStep = 4096.0f;             // between the two groups of a float32 query's codes
 constexpr int kMeta = 8;                       // tiles whose scales are kept
 
-template <int R>
+template <int R, bool F32>
 struct Cfg {
-    static constexpr int kK = R == 64 ? 2 : 3, kV = 3;                 // tiles of K and of V in shared memory: V waits for the softmax
     static constexpr int kWgs = R == 64 ? 4 : 2;                        // softmax warpgroups, each with all positions and R / kWgs rows
     static constexpr int kH = R / kWgs;                                // rows per softmax thread
     static constexpr int kSoftmax = 128 * kWgs, kThreads = 128 + kSoftmax;
-    static constexpr uint32_t kS = 2 * R, kO = 4 * R;                  // TMEM columns: S buffers of 2 R, then O halves of R
-    static constexpr uint32_t kTmem = R == 64 ? 512 : R == 32 ? 256 : 128;
+    static constexpr int kQ = F32 ? 6 : 2, kP = F32 ? 6 : 3;            // codes per query value and per weight
+    static constexpr int kK = R == 64 || F32 ? 2 : 3, kV = F32 && R == 32 ? 2 : 3;   // tiles in shared memory; V waits for the softmax
+    static constexpr uint32_t kS = kQ * R, kO = 2 * kS;                // TMEM columns: two S buffers, then O halves of R
+    static constexpr uint32_t kUsed = kO + 2 * R, kTmem = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
+    static_assert(kUsed <= 512 && kS <= 256, "TMEM and the MMA's N");
 };
 
-template <int R>
+template <int R, bool F32>
 struct Smem {
-    alignas(128) uint8_t k[Cfg<R>::kK][kTileBytes];
-    alignas(128) uint8_t v[Cfg<R>::kV][kTileBytes];
-    alignas(128) uint8_t q[2 * R * kHeadDim];
-    alignas(128) uint8_t p[3][R * kBs8Tile];
+    alignas(128) uint8_t k[Cfg<R, F32>::kK][kTileBytes];
+    alignas(128) uint8_t v[Cfg<R, F32>::kV][kTileBytes];
+    alignas(128) uint8_t q[Cfg<R, F32>::kQ * R * kHeadDim];
+    alignas(128) uint8_t p[Cfg<R, F32>::kP][R * kBs8Tile];
     alignas(16) float meta[kMeta][16];         // K scales of a tile's 8 blocks, then V scales
     alignas(16) float rs[R], m[R], dm[R];      // of each row: 2^-k, the maximum negated, its last change
-    float red[Cfg<R>::kWgs][4][Cfg<R>::kH];
+    float red[Cfg<R, F32>::kWgs][4][Cfg<R, F32>::kH];
     Bs8Share first;
     int bad_page[kMeta];
     uint32_t tmem;
     volatile int abort;
-    unsigned long long k_full[Cfg<R>::kK], k_free[Cfg<R>::kK], v_full[Cfg<R>::kV], v_free[Cfg<R>::kV], s_full[2], s_free[2], p_full, p_free, q_full, drained, meta_full[kMeta];
+    unsigned long long k_full[Cfg<R, F32>::kK], k_free[Cfg<R, F32>::kK], v_full[Cfg<R, F32>::kV], v_free[Cfg<R, F32>::kV], s_full[2], s_free[2], p_full, p_free, q_full, drained, meta_full[kMeta];
 };
 
 // Instruction descriptor, kind::f8f6f4: E4M3 A, E4M3 or E5M2 B, fp32 D, M = 128.
@@ -112,9 +117,9 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return as_u32
 // A barrier is waited for by parity, so whoever waits for one has to see each of its phases: K and V have rings of their own.
 //
 // Bulk copies of a segment's tiles in the order of their use: K0 K1 V0 K2 V1 ... V(n-2) V(n-1).
-template <int R>
-__device__ void produce(const Bs8Args& a, Smem<R>& sm, Bs8Share w) {
-    using C = Cfg<R>;
+template <int R, bool F32>
+__device__ void produce(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w) {
+    using C = Cfg<R, F32>;
     const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
     uint32_t it = 0, ks = 0, vs = 0;       // tiles before the segment; copies of K and of V so far
     bool ok = true;
@@ -178,9 +183,9 @@ __device__ void produce(const Bs8Args& a, Smem<R>& sm, Bs8Share w) {
 // MMAs, by one thread of each of three warps: QK, and PV into the two halves of O.  A thread needs about 100 cycles to
 // form the descriptors of an MMA and issue it, twice what the tensor pipe takes for one, so one thread would bound a tile
 // (32 MMAs).  Each waits for its own operands only: QK of later tiles runs while the softmax works on this one.
-template <int R>
-__device__ void issue_qk(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
-    using C = Cfg<R>;
+template <int R, bool F32>
+__device__ void issue_qk(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t tmem) {
+    using C = Cfg<R, F32>;
     const uint64_t kdesc = make_desc(smem_u32(sm.k[0]), 128, 2048), qdesc = make_desc(smem_u32(sm.q), 128, 2048);
     uint32_t it = 0, seg = 0;
     bool ok = true;
@@ -194,7 +199,7 @@ __device__ void issue_qk(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tme
             tc_fence_after();
             const uint64_t ad = kdesc + st * (kTileBytes / 16);
 #pragma unroll
-            for (int k = 0; k < kHeadDim / 32; ++k) mma8(tmem + b * C::kS, ad + k * 16, qdesc + k * 16, idesc8(2 * R, false, false), k > 0);
+            for (int k = 0; k < kHeadDim / 32; ++k) mma8(tmem + b * C::kS, ad + k * 16, qdesc + k * 16, idesc8(C::kS, false, false), k > 0);
             mma_commit(&sm.k_free[st]);
             mma_commit(&sm.s_full[b]);
         }
@@ -204,9 +209,9 @@ __device__ void issue_qk(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tme
     mma_commit(&sm.drained);
 }
 
-template <int R>
-__device__ void issue_pv(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem, int half) {
-    using C = Cfg<R>;
+template <int R, bool F32>
+__device__ void issue_pv(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t tmem, int half) {
+    using C = Cfg<R, F32>;
     const uint64_t vdesc = make_desc(smem_u32(sm.v[0]) + half * 1024, 2048, 128), pdesc = make_desc(smem_u32(sm.p[0]), R / 16 * 128, 128);
     const uint32_t o = tmem + C::kO + half * R;
     uint32_t it = 0;
@@ -219,11 +224,11 @@ __device__ void issue_pv(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tme
             tc_fence_after();
             const uint64_t ad = vdesc + st * (kTileBytes / 16);
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
+            for (int part = 0; part < C::kP; ++part)
 #pragma unroll
                 for (int k = 0; k < kBs8Tile / 32; ++k)
                     mma8(o, ad + k * (8192 / 16), pdesc + part * (R * kBs8Tile / 16) + k * (4 * (R / 16) * 128 / 16), idesc8(R, true, true),
-                         i > 0 || part > 0 || k > 0);
+                         (!F32 && i > 0) || part > 0 || k > 0);
             mma_commit(&sm.v_free[st]);
             mma_commit(&sm.p_free);
         }
@@ -232,47 +237,70 @@ __device__ void issue_pv(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tme
     mma_commit(&sm.drained);
 }
 
-// The queries of a segment as two E4M3 codes per value; a row that is not finite gets a NaN scale and comes out as NaN.
-template <int R>
-__device__ void prepare_q(const Bs8Args& a, Smem<R>& sm, const Bs8Share& w, int warp) {
-    constexpr int kWarps = Cfg<R>::kSoftmax / 32, kEach = R / kWarps;
+// The queries of a segment as codes; a row that is not finite gets a NaN scale and comes out as NaN.
+template <int R, bool F32>
+__device__ void prepare_q(const Bs8Args& a, Smem<R, F32>& sm, const Bs8Share& w, int warp) {
+    using C = Cfg<R, F32>;
+    using T = std::conditional_t<F32, float, __nv_bfloat16>;
+    constexpr int kWarps = C::kSoftmax / 32, kEach = R / kWarps, kVecs = F32 ? 2 : 1;
     const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
-    const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                             (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim + 8 * lane;
-    uint4 in[kEach];
+    const int T0 = w.chunk(heads) * (a.rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
+    const T* q = static_cast<const T*>(a.q) + (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim + 8 * lane;
+    uint4 in[kEach][kVecs];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {            // padding rows load the last row
         const int r = min(warp + i * kWarps, nrows - 1);
-        in[i] = *reinterpret_cast<const uint4*>(q + ((int64_t)(r >> 3) * heads * kGroup + (r & 7)) * kHeadDim);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            in[i][v] = reinterpret_cast<const uint4*>(q + ((int64_t)(r >> 3) * heads * kGroup + (r & 7)) * kHeadDim)[v];
     }
 #pragma unroll
     for (int n = 0; n < kEach; ++n) {
         const int r = warp + n * kWarps;
-        const uint32_t in4[4] = {in[n].x, in[n].y, in[n].z, in[n].w};
+        uint32_t x[8];                           // float32 bits
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) {
+                const uint4 u = in[n][i >> 1];
+                x[2 * i] = (i & 1) ? u.z : u.x;
+                x[2 * i + 1] = (i & 1) ? u.w : u.y;
+            } else {
+                const uint32_t u = i == 0 ? in[n][0].x : i == 1 ? in[n][0].y : i == 2 ? in[n][0].z : in[n][0].w;
+                x[2 * i] = u << 16;
+                x[2 * i + 1] = u & 0xffff0000u;
+            }
+        }
         // magnitudes are ordered as integers, and what is not finite comes last
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(in4[i] & 0x7fffu, (in4[i] >> 16) & 0x7fffu));
+        for (int i = 0; i < 8; ++i) top = max(top, x[i] & 0x7fffffffu);
         top = __reduce_max_sync(0xffffffffu, top);
-        const bool finite = top < 0x7f80u, zero = top == 0 || r >= nrows;
+        const bool finite = top < 0x7f800000u, zero = top == 0 || r >= nrows;
         // largest value to 128 .. 256
-        const int k = zero || !finite ? 0 : min(100, 7 - ((int)(top >> 7) - 127));
+        const int k = zero || !finite ? 0 : min(100, 7 - ((int)(top >> 23) - 127));
         const float up = zero ? 0.0f : __uint_as_float((uint32_t)(k + 127) << 23);
-        uint32_t c1[2], c2[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 y0 = make_float2(__uint_as_float(in4[2 * i] << 16) * up, __uint_as_float(in4[2 * i] & 0xffff0000u) * up);
-            const float2 y1 = make_float2(__uint_as_float(in4[2 * i + 1] << 16) * up, __uint_as_float(in4[2 * i + 1] & 0xffff0000u) * up);
-            c1[i] = e4m3_pair(y0.x, y0.y) | (e4m3_pair(y1.x, y1.y) << 16);
-            uint32_t h01, h23;
-            e4m3x4_to_f16(c1[i], h01, h23);
-            const float2 f0 = __half22float2(as_h2(h01)), f1 = __half22float2(as_h2(h23));
-            c2[i] = e4m3_pair(y0.x - f0.x, y0.y - f0.y) | (e4m3_pair(y1.x - f1.x, y1.y - f1.y) << 16);
-        }
         uint8_t* to = sm.q + ((r >> 3) * 16 + (lane >> 1)) * 128 + (r & 7) * 16 + (lane & 1) * 8;
-        *reinterpret_cast<uint2*>(to) = make_uint2(c1[0], c1[1]);
-        *reinterpret_cast<uint2*>(to + R * kHeadDim) = make_uint2(c2[0], c2[1]);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(x[i]) * up;
+#pragma unroll
+        for (int c = 0; c < C::kQ; ++c) {
+            uint32_t code[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                code[i] = e4m3_pair(y[4 * i], y[4 * i + 1]) | (e4m3_pair(y[4 * i + 2], y[4 * i + 3]) << 16);
+                if (c + 1 == C::kQ) continue;
+                uint32_t h01, h23;
+                e4m3x4_to_f16(code[i], h01, h23);
+                const float2 f0 = __half22float2(as_h2(h01)), f1 = __half22float2(as_h2(h23));
+                const float rest = F32 && c == 2 ? kQStep : 1.0f;      // the second three codes carry 12 bits less
+                y[4 * i] = (y[4 * i] - f0.x) * rest;
+                y[4 * i + 1] = (y[4 * i + 1] - f0.y) * rest;
+                y[4 * i + 2] = (y[4 * i + 2] - f1.x) * rest;
+                y[4 * i + 3] = (y[4 * i + 3] - f1.y) * rest;
+            }
+            *reinterpret_cast<uint2*>(to + c * R * kHeadDim) = make_uint2(code[0], code[1]);
+        }
         if (lane == 0) sm.rs[r] = finite || r >= nrows ? __uint_as_float((uint32_t)(127 - k) << 23) : __int_as_float(0x7fc00000);
     }
 }
@@ -330,9 +358,34 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-template <int R>
-__device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem) {
-    using C = Cfg<R>;
+// Two floats -> two E5M2 bytes (lo in the low byte); and minus the values of two such bytes.
+__device__ __forceinline__ uint32_t e5m2_pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 e5m2_negative(uint32_t two) {
+    return __half22float2(as_h2(__byte_perm(two, 0, 0x1404) ^ 0x80008000u));
+}
+
+// Float32 outputs leave TMEM after every tile: its accumulators need not round to nearest, and a long context's many
+// additions would show that.
+template <int R, bool F32>
+__device__ __forceinline__ void drain(uint32_t lanes, int r0, float* acc) {
+    using C = Cfg<R, F32>;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float o[C::kH];
+        tmem_load<C::kH>(lanes + C::kO + h * R + r0, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < C::kH; ++c) acc[h * C::kH + c] += o[c];
+    }
+}
+
+template <int R, bool F32>
+__device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t tmem) {
+    using C = Cfg<R, F32>;
     constexpr int H = C::kH, kAll = 1 + C::kWgs;                     // kAll: barrier of all softmax warps
     const int tid = threadIdx.x - 128, lane = threadIdx.x & 31, warp = tid >> 5, heads = a.num_kv_heads;
     const int wg = warp >> 2, quarter = (threadIdx.x >> 5) & 3;      // rows wg H .., positions 32 quarter ..: a warp reads its own TMEM lanes
@@ -341,7 +394,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
     uint32_t it = 0;
     bool ok = true;
     do {
-        prepare_q<R>(a, sm, w, warp);
+        prepare_q<R, F32>(a, sm, w, warp);
         if (tid < R) sm.m[tid] = 0.0f;
         fence_proxy_async();
         warp_arrive(&sm.q_full);
@@ -349,7 +402,12 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
         float2 l[H / 2];
 #pragma unroll
         for (int c = 0; c < H / 2; ++c) l[c] = both(0.0f);
-        const int seen = w.s.L - w.s.T + w.chunk(heads) * (kBs8Rows / kGroup);      // last position that the chunk's first token sees
+        float acc[F32 ? 2 * H : 1];        // float32: outputs so far
+        if constexpr (F32) {
+#pragma unroll
+            for (int c = 0; c < 2 * H; ++c) acc[c] = 0.0f;
+        }
+        const int seen = w.s.L - w.s.T + w.chunk(heads) * (a.rows / kGroup);      // last position that the chunk's first token sees
         for (int i = 0; i < w.tiles; ++i, ++it) {
             const uint32_t b = it & 1, slot = it % kMeta;
             const int p0 = (w.tile + i) * kBs8Tile;
@@ -364,12 +422,18 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
             float d[H];
             float2* d2 = reinterpret_cast<float2*>(d);
             {
+                // the codes' scores, smallest first
                 float s2[H];
-                tmem_load<H>(lanes + b * C::kS + r0, d);
-                tmem_load<H>(lanes + b * C::kS + R + r0, s2);
-                tmem_ld_wait();
+                tmem_load<H>(lanes + b * C::kS + (C::kQ - 1) * R + r0, d);
 #pragma unroll
-                for (int c = 0; c < H / 2; ++c) d2[c] = add2(d2[c], reinterpret_cast<float2*>(s2)[c]);
+                for (int q = C::kQ - 2; q >= 0; --q) {
+                    tmem_load<H>(lanes + b * C::kS + q * R + r0, s2);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < H / 2; ++c)
+                        d2[c] = F32 && q == 2 ? fma2(d2[c], both(1.0f / kQStep), reinterpret_cast<float2*>(s2)[c])
+                                              : add2(d2[c], reinterpret_cast<float2*>(s2)[c]);
+                }
             }
             tc_fence_before();
             warp_arrive(&sm.s_free[b]);
@@ -389,7 +453,8 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
             float top = d[0];
 #pragma unroll
             for (int c = 1; c < H; ++c) top = fmaxf(top, d[c]);
-            if (named_or(bar, 128, i == 0 || top > kRaise || !ok)) {
+            const bool raise = named_or(bar, 128, i == 0 || top > kRaise || !ok);
+            if (raise) {
                 if (named_or(bar, 128, !ok)) {
                     ok = false;
                     break;
@@ -418,7 +483,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                     d2[c] = add2(d2[c], dm);
                     if (i > 0) l[c] = mul2(l[c], make_float2(fast_exp2(dm.x), fast_exp2(dm.y)));
                 }
-                if (i > 0) {
+                if (!F32 && i > 0) {
                     ok = mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);      // PV of the tile before, and all earlier ones
                     __syncwarp();
                     tc_fence_after();
@@ -436,31 +501,46 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
                 }
             }
             const float2 iv = both(__uint_as_float((uint32_t)(127 - ev) << 23));       // 2^-eV
-            uint32_t w1[H / 4], w2[H / 4], w3[H / 4];
+            uint32_t code[C::kP][H / 4];
 #pragma unroll
             for (int c = 0; c < H / 4; ++c) {
-                const float2 x = make_float2(fast_exp2(d[4 * c]), fast_exp2(d[4 * c + 1]));
-                const float2 y = make_float2(fast_exp2(d[4 * c + 2]), fast_exp2(d[4 * c + 3]));
+                float2 x = make_float2(fast_exp2(d[4 * c]), fast_exp2(d[4 * c + 1]));
+                float2 y = make_float2(fast_exp2(d[4 * c + 2]), fast_exp2(d[4 * c + 3]));
                 l[2 * c] = fma2(x, iv, l[2 * c]);
                 l[2 * c + 1] = fma2(y, iv, l[2 * c + 1]);
-                // E5M2 is the upper byte of fp16: the first two codes are cut off, the third is rounded (half a step: 0x80)
-                const uint32_t a0 = f16_pair(x.x, x.y), b0 = f16_pair(y.x, y.y);
-                const uint32_t ar = sub2(a0, a0 & 0xff00ff00u), br = sub2(b0, b0 & 0xff00ff00u);
-                const uint32_t a3 = sub2(ar, ar & 0xff00ff00u) + 0x00800080u, b3 = sub2(br, br & 0xff00ff00u) + 0x00800080u;
-                w1[c] = __byte_perm(a0, b0, 0x7531);
-                w2[c] = __byte_perm(ar, br, 0x7531);
-                w3[c] = __byte_perm(a3, b3, 0x7531);
+                if constexpr (F32) {
+#pragma unroll
+                    for (int n = 0; n < C::kP; ++n) {
+                        code[n][c] = e5m2_pair(x.x, x.y) | (e5m2_pair(y.x, y.y) << 16);
+                        if (n + 1 == C::kP) break;
+                        x = add2(x, e5m2_negative(code[n][c]));
+                        y = add2(y, e5m2_negative(code[n][c] >> 16));
+                    }
+                } else {
+                    // E5M2 is the upper byte of fp16: the first two codes are cut off, the third is rounded (half a step: 0x80)
+                    const uint32_t a0 = f16_pair(x.x, x.y), b0 = f16_pair(y.x, y.y);
+                    const uint32_t ar = sub2(a0, a0 & 0xff00ff00u), br = sub2(b0, b0 & 0xff00ff00u);
+                    const uint32_t a3 = sub2(ar, ar & 0xff00ff00u) + 0x00800080u, b3 = sub2(br, br & 0xff00ff00u) + 0x00800080u;
+                    code[0][c] = __byte_perm(a0, b0, 0x7531);
+                    code[1][c] = __byte_perm(ar, br, 0x7531);
+                    code[2][c] = __byte_perm(a3, b3, 0x7531);
+                }
             }
             if (it > 0) ok = ok && mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);
+            if constexpr (F32) {
+                __syncwarp();
+                tc_fence_after();
+                if (i > 0) drain<R, F32>(lanes, r0, acc);
+                if (raise) {
+#pragma unroll
+                    for (int c = 0; c < 2 * H; ++c) acc[c] *= fast_exp2(sm.dm[r0 + c % H]);
+                }
+            }
             uint8_t* to = sm.p[0] + ((p >> 3) * (R / 16) + r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
-            if constexpr (H == 8) {
-                *reinterpret_cast<uint2*>(to) = make_uint2(w1[0], w1[1]);
-                *reinterpret_cast<uint2*>(to + R * kBs8Tile) = make_uint2(w2[0], w2[1]);
-                *reinterpret_cast<uint2*>(to + 2 * R * kBs8Tile) = make_uint2(w3[0], w3[1]);
-            } else {
-                *reinterpret_cast<uint4*>(to) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-                *reinterpret_cast<uint4*>(to + R * kBs8Tile) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-                *reinterpret_cast<uint4*>(to + 2 * R * kBs8Tile) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+#pragma unroll
+            for (int n = 0; n < C::kP; ++n) {
+                if constexpr (H == 8) *reinterpret_cast<uint2*>(to + n * R * kBs8Tile) = make_uint2(code[n][0], code[n][1]);
+                else *reinterpret_cast<uint4*>(to + n * R * kBs8Tile) = make_uint4(code[n][0], code[n][1], code[n][2], code[n][3]);
             }
             const int valid = hidden ? 0 : w.s.L - p0;
             if (valid < kBs8Tile) {
@@ -483,17 +563,18 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
             break;
         }
         tc_fence_after();
+        if constexpr (F32) drain<R, F32>(lanes, r0, acc);
         // row sums over the positions
         {
             const float x = reduce_rows<H>(reinterpret_cast<float (&)[H]>(l), [](float u, float v) { return u + v; });
             if (lane % (32 / H) == 0) sm.red[wg][quarter][lane / (32 / H)] = x;
         }
         named_sync(bar, 128);
-        const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
+        const int T0 = w.chunk(heads) * (a.rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
         const bool whole = w.whole();
         float* part = a.partials + ((size_t)blockIdx.x * 2 + w.part()) * kBs8PartFloats;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                             (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim;
+        using T = std::conditional_t<F32, float, __nv_bfloat16>;
+        T* out = static_cast<T*>(a.out) + (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim;
         if (p < H) {                       // one thread per row; then all read their rows' factors
             const float mine = (sm.red[wg][0][p] + sm.red[wg][1][p]) + (sm.red[wg][2][p] + sm.red[wg][3][p]);
             if (!whole && r0 + p < nrows)
@@ -505,13 +586,18 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float o[H];
-            tmem_load<H>(lanes + C::kO + h * R + r0, o);
-            tmem_ld_wait();
+            if constexpr (F32) {
+#pragma unroll
+                for (int c = 0; c < H; ++c) o[c] = acc[h * H + c];
+            } else {
+                tmem_load<H>(lanes + C::kO + h * R + r0, o);
+                tmem_ld_wait();
+            }
             if (whole) {
-                __nv_bfloat16* to = out + ((int64_t)(r0 >> 3) * heads * kGroup) * kHeadDim + h * 128 + p;
+                T* to = out + ((int64_t)(r0 >> 3) * heads * kGroup) * kHeadDim + h * 128 + p;
 #pragma unroll
                 for (int c = 0; c < H; ++c)
-                    if (r0 + c < nrows) to[((int64_t)(c >> 3) * heads * kGroup + (c & 7)) * kHeadDim] = __float2bfloat16_rn(o[c] * sm.dm[r0 + c]);
+                    if (r0 + c < nrows) to[((int64_t)(c >> 3) * heads * kGroup + (c & 7)) * kHeadDim] = (T)(o[c] * sm.dm[r0 + c]);
             } else {
                 float* to = part + r0 * kHeadDim + h * 128 + p;
                 if (r0 + H <= nrows) {
@@ -530,11 +616,11 @@ __device__ void softmax(const Bs8Args& a, Smem<R>& sm, Bs8Share w, uint32_t tmem
     if (!ok && tid == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_TIMEOUT);
 }
 
-template <int R>
-__global__ void __launch_bounds__(Cfg<R>::kThreads, 1) verify_bs8_mma_kernel(Bs8Args a) {
-    using C = Cfg<R>;
+template <int R, bool F32>
+__global__ void __launch_bounds__(Cfg<R, F32>::kThreads, 1) verify_bs8_mma_kernel(Bs8Args a) {
+    using C = Cfg<R, F32>;
     extern __shared__ uint8_t raw[];
-    Smem<R>& sm = *reinterpret_cast<Smem<R>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
+    Smem<R, F32>& sm = *reinterpret_cast<Smem<R, F32>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
     const int warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 32) {
@@ -573,16 +659,16 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1) verify_bs8_mma_kernel(Bs8
     const uint32_t tmem = sm.tmem;
     if (w.tiles > 0) {
         if (warp == 0) {
-            produce<R>(a, sm, w);
+            produce<R, F32>(a, sm, w);
         } else if (warp < 4) {
             if ((threadIdx.x & 31) == 0) {
-                if (warp == 1) issue_qk<R>(a, sm, w, tmem);
-                else issue_pv<R>(a, sm, w, tmem, warp - 2);
+                if (warp == 1) issue_qk<R, F32>(a, sm, w, tmem);
+                else issue_pv<R, F32>(a, sm, w, tmem, warp - 2);
                 mbar_drain(&sm.drained, 0);        // TMEM and the operands stay until the last MMA is done
             }
             __syncwarp();
         } else {
-            softmax<R>(a, sm, w, tmem);
+            softmax<R, F32>(a, sm, w, tmem);
         }
     }
     tc_fence_before();
@@ -591,15 +677,15 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, 1) verify_bs8_mma_kernel(Bs8
     if (warp == 1) tmem_dealloc(tmem, C::kTmem);
 }
 
-template <int R>
+template <int R, bool F32>
 cudaError_t launch_r(const Bs8Args& a, cudaStream_t st) {
-    constexpr size_t smem = sizeof(Smem<R>) + 128;
+    constexpr size_t smem = sizeof(Smem<R, F32>) + 128;
     static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-    const cudaError_t e = cudaFuncSetAttribute(verify_bs8_mma_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(verify_bs8_mma_kernel<R, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.ctas);
-    cfg.blockDim = dim3(Cfg<R>::kThreads);
+    cfg.blockDim = dim3(Cfg<R, F32>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -607,14 +693,17 @@ cudaError_t launch_r(const Bs8Args& a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_bs8_mma_kernel<R>, a);
+    return cudaLaunchKernelEx(&cfg, verify_bs8_mma_kernel<R, F32>, a);
 }
 
 }  // namespace
 
+int bs8_mma_rows(int dtype) { return dtype == Q3KV_F32 ? 32 : kBs8Rows; }
+
 cudaError_t launch_bs8_mma(const Bs8Args& a, cudaStream_t st) {
     const int rows = kGroup * a.max_n_q;
-    return rows <= 16 ? launch_r<16>(a, st) : rows <= 32 ? launch_r<32>(a, st) : launch_r<64>(a, st);
+    if (a.dtype == Q3KV_F32) return rows <= 16 ? launch_r<16, true>(a, st) : launch_r<32, true>(a, st);
+    return rows <= 16 ? launch_r<16, false>(a, st) : rows <= 32 ? launch_r<32, false>(a, st) : launch_r<64, false>(a, st);
 }
 
 }  // namespace q3kv
