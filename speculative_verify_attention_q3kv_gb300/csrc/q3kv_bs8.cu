@@ -211,8 +211,8 @@ __device__ __forceinline__ void decode_sub(const uint8_t* unit, int in_page, int
 __global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     FmaSmem& sm = *reinterpret_cast<FmaSmem*>(smem_raw);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // after the wait: the merge reads the lengths before its own
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (warp == 0) {
         bool bad = false;
@@ -360,22 +360,26 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
     __shared__ float4 s_o[kMergeGroups][64];
     __shared__ float2 s_ml[kMergeGroups];
     __shared__ int64_t s_at[2];                  // tiles before the slot, and of all slots
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The lengths were complete before the verify kernel let this one start; its partials are after the wait.  Every CTA
+    // waits, also one without work: whoever follows this kernel goes by its end.
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = a.num_kv_heads;
     const int slot = blockIdx.z, pair = blockIdx.y, r = blockIdx.x;
     const Bs8Slot s = bs8_slot(a, slot, nullptr);
-    if (pair >= s.pairs(heads)) return;
     const int T0 = pair / heads * (a.rows / kGroup), head = pair % heads;
-    if (r >= min(a.rows, kGroup * (s.T - T0))) return;
     if (warp < 2) {
         const int64_t n = bs8_tiles_before(a, warp == 0 ? slot : a.num_slots, nullptr);
         if (lane == 0) s_at[warp] = n;
     }
     __syncthreads();
-    const int64_t total = s_at[1], begin = s_at[0] + (int64_t)pair * s.tiles;
-    const int c0 = bs8_cta_of(begin, total, a.ctas), c1 = bs8_cta_of(begin + s.tiles - 1, total, a.ctas);
-    if (c0 == c1) return;                        // the pair was not cut
+    int c0 = 0, c1 = 0;
+    if (pair < s.pairs(heads) && r < min(a.rows, kGroup * (s.T - T0))) {
+        const int64_t total = s_at[1], begin = s_at[0] + (int64_t)pair * s.tiles;
+        c0 = bs8_cta_of(begin, total, a.ctas);
+        c1 = bs8_cta_of(begin + s.tiles - 1, total, a.ctas);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (c0 == c1) return;                        // nothing here, or the pair was not cut
     const int n = c1 - c0 + 1;
     const int col = tid & 63, group = tid >> 6;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

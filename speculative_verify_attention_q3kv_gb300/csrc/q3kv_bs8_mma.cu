@@ -246,26 +246,29 @@ __device__ void prepare_q(const Bs8Args& a, Smem<R, F32>& sm, const Bs8Share& w,
     const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
     const int T0 = w.chunk(heads) * (a.rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
     const T* q = static_cast<const T*>(a.q) + (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim + 8 * lane;
-    uint4 in[kEach][kVecs];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {            // padding rows load the last row
-        const int r = min(warp + i * kWarps, nrows - 1);
+    auto load = [&](int n, uint4 (&to)[kVecs]) {       // padding rows load the last row
+        const int r = min(warp + n * kWarps, nrows - 1);
 #pragma unroll
         for (int v = 0; v < kVecs; ++v)
-            in[i][v] = reinterpret_cast<const uint4*>(q + ((int64_t)(r >> 3) * heads * kGroup + (r & 7)) * kHeadDim)[v];
-    }
-#pragma unroll
+            to[v] = reinterpret_cast<const uint4*>(q + ((int64_t)(r >> 3) * heads * kGroup + (r & 7)) * kHeadDim)[v];
+    };
+    uint4 in[kVecs], next[kVecs], third[kVecs];
+    load(0, in);
+    load(1, next);
+    // rolled, two rows ahead: code that runs once costs its fetch
+#pragma unroll 1
     for (int n = 0; n < kEach; ++n) {
         const int r = warp + n * kWarps;
+        load(n + 2, third);
         uint32_t x[8];                           // float32 bits
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (F32) {
-                const uint4 u = in[n][i >> 1];
+                const uint4 u = in[F32 ? i >> 1 : 0];
                 x[2 * i] = (i & 1) ? u.z : u.x;
                 x[2 * i + 1] = (i & 1) ? u.w : u.y;
             } else {
-                const uint32_t u = i == 0 ? in[n][0].x : i == 1 ? in[n][0].y : i == 2 ? in[n][0].z : in[n][0].w;
+                const uint32_t u = i == 0 ? in[0].x : i == 1 ? in[0].y : i == 2 ? in[0].z : in[0].w;
                 x[2 * i] = u << 16;
                 x[2 * i + 1] = u & 0xffff0000u;
             }
@@ -302,6 +305,11 @@ __device__ void prepare_q(const Bs8Args& a, Smem<R, F32>& sm, const Bs8Share& w,
             *reinterpret_cast<uint2*>(to + c * R * kHeadDim) = make_uint2(code[0], code[1]);
         }
         if (lane == 0) sm.rs[r] = finite || r >= nrows ? __uint_as_float((uint32_t)(127 - k) << 23) : __int_as_float(0x7fc00000);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            in[v] = next[v];
+            next[v] = third[v];
+        }
     }
 }
 
@@ -622,7 +630,6 @@ __global__ void __launch_bounds__(Cfg<R, F32>::kThreads, 1) verify_bs8_mma_kerne
     extern __shared__ uint8_t raw[];
     Smem<R, F32>& sm = *reinterpret_cast<Smem<R, F32>*>((reinterpret_cast<uintptr_t>(raw) + 127) & ~(uintptr_t)127);
     const int warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 32) {
         for (int i = 0; i < C::kK; ++i) {
             mbar_init(&sm.k_full[i], 1);
@@ -646,6 +653,8 @@ __global__ void __launch_bounds__(Cfg<R, F32>::kThreads, 1) verify_bs8_mma_kerne
     }
     if (warp == 1) tmem_alloc(&sm.tmem, C::kTmem);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // only now: the merge reads the lengths before its own wait, and whoever writes them is done here
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
         bool bad = false;
         const Bs8Share w = bs8_share(a, blockIdx.x, &bad);
