@@ -20,25 +20,39 @@ namespace {
 // each, and a warp writes four whole cores (512 bytes).  Bound: the rows read and the codes written.
 constexpr int kAppendThreads = 256;
 
-__device__ __forceinline__ void load16(const float* src, float (&x)[16]) {
+// Sixteen values as they lie in memory: fewer registers than float32 (bf16) while they wait for the block's maximum.
+template <typename T>
+struct Raw16 {
+    static constexpr int kWords = (int)sizeof(T) * 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 u = reinterpret_cast<const float4*>(src)[i];
-        x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
-    }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* src, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 u = reinterpret_cast<const uint4*>(src)[i];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+            w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
         }
     }
-}
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    // largest finite magnitude, as float32 bits (which are in the magnitudes' order)
+    __device__ __forceinline__ uint32_t top(bool* finite) const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(at(i)) & 0x7fffffffu);
+        if (m >= 0x7f800000u) {
+            *finite = false;
+            m = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t u = __float_as_uint(at(i)) & 0x7fffffffu;
+                m = max(m, u < 0x7f800000u ? u : 0u);
+            }
+        }
+        return m;
+    }
+};
 
 // Two floats -> two E4M3 bytes (lo in the low byte), to nearest even, magnitudes above 448 to 448.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -51,11 +65,12 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
-__device__ __forceinline__ uint4 encode16(const float (&x)[16], float inv) {
+template <typename At>
+__device__ __forceinline__ uint4 encode16(At x, float inv) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) | (e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+        w[i] = e4m3x2(x(4 * i) * inv, x(4 * i + 1) * inv) | (e4m3x2(x(4 * i + 2) * inv, x(4 * i + 3) * inv) << 16);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -64,8 +79,8 @@ __device__ __forceinline__ int scale_exp(float s) {       // of a stored scale, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) append_bs8_kernel(AppendArgs a) {
-    __shared__ float s_max[2][kAppendThreads / 32];
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 6 : 4) append_bs8_kernel(AppendArgs a) {
+    __shared__ uint32_t s_max[2][kAppendThreads / 32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int slot = blockIdx.y, head = blockIdx.z;
@@ -87,11 +102,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_bs8_kernel(AppendArgs a
     const int row = (warp & 1) * 8 + (lane & 7), chunk = (warp >> 1) * 4 + (lane >> 3);
     const int64_t pos = p0 + row;
     const bool fresh = pos >= len && pos < end, kept = pos < len;
-    float x[2][16];
+    Raw16<T> x[2];
     if (fresh) {
         const int64_t at = ((first_row + (pos - len)) * a.num_kv_heads + head) * kHeadDim + chunk * 16;
-        load16(static_cast<const T*>(a.k) + at, x[0]);
-        load16(static_cast<const T*>(a.v) + at, x[1]);
+        x[0].load(static_cast<const T*>(a.k) + at);
+        x[1].load(static_cast<const T*>(a.v) + at);
     }
     if (page < 0 || page >= a.num_pages) {
         if (threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_PAGE);
@@ -113,43 +128,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_bs8_kernel(AppendArgs a
     bool finite = true;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        float top = 0.0f;
-        if (fresh) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool ok = fabsf(x[kv][i]) <= 3.402823466e38f;
-                finite = finite && ok;
-                top = fmaxf(top, ok ? fabsf(x[kv][i]) : 0.0f);
-            }
-        }
-        // magnitudes are ordered as integers
-        const uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        if (lane == 0) s_max[kv][warp] = __uint_as_float(u);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, fresh ? x[kv].top(&finite) : 0u);
+        if (lane == 0) s_max[kv][warp] = top;
     }
     if (!__all_sync(0xffffffffu, finite) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
     __syncthreads();
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        float top = s_max[kv][0];
+        uint32_t u = s_max[kv][0];
 #pragma unroll
-        for (int i = 1; i < kAppendThreads / 32; ++i) top = fmaxf(top, s_max[kv][i]);
+        for (int i = 1; i < kAppendThreads / 32; ++i) u = max(u, s_max[kv][i]);
         // top = m 2^k with 1 <= m < 2 and 448 = 1.75 2^8; zero and subnormal values give the smallest e
-        const uint32_t u = __float_as_uint(top);
         const int need = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
         if (need > kBs8MaxExp && threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_SCALE_OVERFLOW);
         const int e = min(kBs8MaxExp, max(old[kv], need));
         if (fresh) {
-            *reinterpret_cast<uint4*>(code + kv * kBs8UnitBytes) = encode16(x[kv], pow2(-e));
+            *reinterpret_cast<uint4*>(code + kv * kBs8UnitBytes) = encode16([&](int i) { return x[kv].at(i); }, pow2(-e));
         } else if (kept && e != old[kv]) {
             const uint32_t w[4] = {was[kv].x, was[kv].y, was[kv].z, was[kv].w};
-            float y[16];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = e4m3x2_to_f32((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-                y[2 * i] = f.x;
-                y[2 * i + 1] = f.y;
-            }
-            *reinterpret_cast<uint4*>(code + kv * kBs8UnitBytes) = encode16(y, pow2(max(old[kv] - e, -126)));
+            *reinterpret_cast<uint4*>(code + kv * kBs8UnitBytes) = encode16([&](int i) {
+                const float2 f = e4m3x2_to_f32((w[i >> 2] >> (16 * ((i >> 1) & 1))) & 0xffffu);
+                return (i & 1) ? f.y : f.x;
+            }, pow2(max(old[kv] - e, -126)));
         }
         if (threadIdx.x == 0) *reinterpret_cast<float*>(scale + kv * kBs8UnitBytes) = pow2(e);
     }

@@ -57,12 +57,57 @@ struct alignas(16) Row8 {
     T x[kPer];
 };
 
-// A CTA takes 2,048 entries of up to kBatch rows of one slot: their logits, masks and counts are all loaded before the
-// first barrier.  Bound: bytes (logits in and out); small calls: the chain of loads lengths -> tokens -> biases.
+// A CTA takes 2,048 entries of up to kBatch rows of one slot.  Bound: bytes (logits in and out), which asks for many in
+// flight: the rows come by asynchronous 16-byte copies into shared memory (an SM has up to 160 KiB under way, where rows
+// held in registers allowed 48 to 96), whole vectors also where a row does not start on one.  An entry's penalty
+// alpha c + beta [c > 0] - bias is the same in all rows but where the step's own tokens count, so a row costs five
+// instructions per entry, and a warp none of whose entries is seen or biased (most are, away from the frequent tokens)
+// only applies the mask.  Small calls are bound by the chain lengths -> rows and tokens -> biases.
 constexpr int kBatch = 4;
+template <typename T>
+constexpr int kRowBytes = kChunk * (int)sizeof(T) + 16;
+
+// 16 bytes to shared memory, of which the first `bytes` are read and the rest becomes zero.
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// 8 entries with the ones whose bit is 0 set to -inf
+__device__ __forceinline__ void apply_mask(Row8<float>& o, uint32_t allowed) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+        if (!((allowed >> e) & 1u)) o.x[e] = -CUDART_INF_F;
+}
+// Each byte of the result: the sign of one of x's bytes, in all its bits.
+template <uint32_t SELECT>
+__device__ __forceinline__ uint32_t spread(uint32_t x) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(x), "n"(SELECT));
+    return r;
+}
+__device__ __forceinline__ void apply_mask(Row8<__nv_bfloat16>& o, uint32_t allowed) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 4) {
+        // bits e .. e + 3 to the sign bits of four bytes, which the permutations then repeat over two bytes each
+        const uint32_t signs = (((allowed >> e) & 15u) * 0x00204081u & 0x01010101u) << 7;
+        const uint32_t low = spread<0x9988>(signs), high = spread<0xbbaa>(signs);
+        w[e / 2] = (w[e / 2] & low) | (0xff80ff80u & ~low);
+        w[e / 2 + 1] = (w[e / 2 + 1] & high) | (0xff80ff80u & ~high);
+    }
+}
+template <typename T>
+__device__ __forceinline__ bool same_bits(const Row8<T>& a, const Row8<T>& b) {
+    const uint32_t *x = reinterpret_cast<const uint32_t*>(&a), *y = reinterpret_cast<const uint32_t*>(&b);
+    uint32_t d = 0;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) * kPer / 4; ++i) d |= x[i] ^ y[i];
+    return d == 0;
+}
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) process_logits_kernel(LogitArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logits_kernel(LogitArgs a) {
+    extern __shared__ __align__(16) uint8_t s_rows[];       // [kBatch][kRowBytes]
     __shared__ float s_bias[kChunk];
     __shared__ int s_tok[kMaxNq];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -80,14 +125,11 @@ __global__ void __launch_bounds__(kThreads) process_logits_kernel(LogitArgs a) {
     // this thread's entries: 8 neighbours, or every 256th where rows are not 16-byte aligned
     const int first = VEC ? base + tid * kPer : base + tid;
     constexpr int kStep = VEC ? 1 : kThreads;
-    union {
-        Row8<int16_t> v;
-        int16_t x[kPer];
-    } count;
+    Row8<int16_t> count;
     if (a.counts && first < a.vocab) {
         const int16_t* c = a.counts + (int64_t)slot * a.counts_stride;
         if (VEC) {
-            count.v = *reinterpret_cast<const Row8<int16_t>*>(c + first);   // the stride covers whole vectors
+            count = *reinterpret_cast<const Row8<int16_t>*>(c + first);   // the stride covers whole vectors
         } else {
 #pragma unroll
             for (int e = 0; e < kPer; ++e) count.x[e] = first + e * kStep < a.vocab ? c[first + e * kStep] : (int16_t)0;
@@ -103,43 +145,51 @@ __global__ void __launch_bounds__(kThreads) process_logits_kernel(LogitArgs a) {
         return;
     }
     if (j0 >= w) return;
+    const int rows = min(kBatch, w - j0);
+    const int64_t begin = ((int64_t)(r0 + j0) * a.vocab + base) * (int)sizeof(T);      // byte of the first row's first entry
+    const int64_t row_bytes = (int64_t)a.vocab * (int)sizeof(T);
+    const uint8_t* in = static_cast<const uint8_t*>(a.logits) + begin;
+    uint8_t* to = s_rows + tid * 16;
+    const int bytes = min(kChunk, a.vocab - base) * (int)sizeof(T);
+#pragma unroll 1
+    for (int k = 0; k < rows; ++k, in += row_bytes, to += kRowBytes<T>) {
+        const int shift = VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(in) & 15);       // the buffer begins on 16 bytes
+        const uint8_t* from = in - shift;
+        const int left = bytes + shift;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const int at = (tid + i * kThreads) * 16;
+            if (at < left) copy16(to + i * kThreads * 16, from + at, min(16, left - at));
+        }
+        if (!VEC && tid == 0 && left > kChunk * (int)sizeof(T))
+            copy16(s_rows + k * kRowBytes<T> + kChunk * sizeof(T), from + kChunk * sizeof(T), left - kChunk * (int)sizeof(T));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int64_t mask_bytes = (a.vocab + 31) / 32 * 4;
+    uint32_t allowed[kBatch];
+    {
+        const uint8_t* m = reinterpret_cast<const uint8_t*>(a.mask) + (r0 + j0) * mask_bytes;
+        // a warp's entries of one step share a word where rows are not aligned: lane e holds step e's
+        const int word = (first - lane + lane * kStep) >> 5;
+        const bool own = a.mask && (VEC ? first < a.vocab : lane < kPer && word * 4 < mask_bytes);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k, m += mask_bytes) {
+            allowed[k] = VEC ? 0xffu : 0u;
+            if (own && k < rows) allowed[k] = VEC ? m[first >> 3] : reinterpret_cast<const uint32_t*>(m)[word];
+        }
+    }
+    bool near = false;                   // a token of the step is in the chunk
     if (tid < w) {
         const int t = a.tokens[r0 + tid];
         s_tok[tid] = t;
         if (report && (t < 0 || t >= a.vocab)) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
-    }
-    const int64_t mask_words = (a.vocab + 31) / 32;
-    const T* in = static_cast<const T*>(a.logits) + (int64_t)(r0 + j0) * a.vocab + first;
-    const int rows = min(kBatch, w - j0);
-    Row8<T> x[kBatch];
-    uint32_t allowed[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-        if (k >= rows) break;
-        const T* p = in + (int64_t)k * a.vocab;
-        if (VEC) {
-            if (first < a.vocab) x[k] = *reinterpret_cast<const Row8<T>*>(p);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e)
-                if (first + e * kStep < a.vocab) x[k].x[e] = p[e * kStep];
-        }
-        allowed[k] = ~0u;
-        if (a.mask) {
-            const uint32_t* m = reinterpret_cast<const uint32_t*>(a.mask) + (r0 + j0 + k) * mask_words;
-            if (VEC) {
-                if (first < a.vocab) allowed[k] = reinterpret_cast<const uint8_t*>(m)[first >> 3];
-            } else {
-                // a warp's entries of one step share a word: lane e holds step e's
-                const int word = (first - lane + lane * kStep) >> 5;
-                allowed[k] = lane < kPer && word < mask_words ? m[word] : 0;
-            }
-        }
+        near = t >= base && t < min(base + kChunk, a.vocab) && tid < j0 + kBatch;
     }
     if (b0 < 0 || b1 < b0 || b1 > a.num_biases) {
         if (report && tid == 0) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
         b0 = b1 = 0;
     }
+    bool biased = false;                 // a bias is
     if (b1 > b0) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) s_bias[tid + i * kThreads] = 0.0f;
@@ -151,53 +201,93 @@ __global__ void __launch_bounds__(kThreads) process_logits_kernel(LogitArgs a) {
                 if (report) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
             } else if (t >= base && t < base + kChunk) {
                 s_bias[t - base] = a.bias_values[i];
+                biased = true;
             }
         }
+        biased = __syncthreads_or(biased);
     }
-    __syncthreads();
-    if (VEC && first >= a.vocab) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    near = __syncthreads_or(near);
 
-    uint32_t step[kPer];         // bit i: t_i is this entry
-    bool stepping = false;
+    // what this thread's entries lose in every row, and where the step's tokens add to it
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(&count);
+    uint32_t seen = 0, marks = 0;        // bit e: entry e is seen in every row; it changes in some
+    if (words[0] | words[1] | words[2] | words[3])
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) step[e] = 0;
-    for (int i = 0; i < min(w, j0 + kBatch); ++i) {
-        const int d = s_tok[i] - first;
-        if (VEC ? (unsigned)d < (unsigned)kPer : d >= 0 && d < kChunk && d % kThreads == 0) {
-            stepping = true;
+        for (int e = 0; e < kPer; ++e) seen |= (count.x[e] != 0 ? 1u : 0u) << e;
+    marks = seen;
+    if (biased)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) step[e] |= (d == e * kStep ? 1u : 0u) << i;
+        for (int e = 0; e < kPer; ++e) marks |= (s_bias[first - base + e * kStep] != 0.0f ? 1u : 0u) << e;
+    uint32_t step[kPer / 2] = {0, 0, 0, 0};                 // 16 bits per entry, bit i set where t_i is the entry
+    if (near)
+        for (int i = 0; i < min(w, j0 + kBatch); ++i) {
+            const int d = s_tok[i] - first;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (d == e * kStep) {
+                    step[e / 2] |= 1u << (i + 16 * (e & 1));
+                    marks |= 1u << e;
+                }
+        }
+    const uint32_t changing = __reduce_or_sync(0xffffffffu, marks);     // the warp skips the other entries
+    float less[kPer];
+    float inverse = 1.0f;
+    if (changing) {
+        inverse = __fdiv_rn(1.0f, theta);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int c = count.x[e] & 0x7fff;
+            less[e] = c > 0 ? fmaf(alpha, (float)c, beta) : 0.0f;
+            if (biased) less[e] -= s_bias[first - base + e * kStep];
         }
     }
     const bool in_place = a.logits == a.out;
-    T* out = static_cast<T*>(a.out) + (int64_t)(r0 + j0) * a.vocab + first;
+    const uint8_t* row = s_rows;
+    uint8_t* out = static_cast<uint8_t*>(a.out) + begin;
+#pragma unroll 1
+    for (int k = 0; k < rows; ++k, row += kRowBytes<T>, out += row_bytes) {
+        Row8<T> x, o;
+        if (VEC) {
+            x = reinterpret_cast<const Row8<T>*>(row)[tid];
+        } else {
+            const T* p = reinterpret_cast<const T*>(row + (reinterpret_cast<uintptr_t>(out) & 15)) + tid;      // in and out are aligned alike
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-        if (k >= rows) break;
-        T* p = out + (int64_t)k * a.vocab;
-        Row8<T> o;
-        bool changed = !in_place;
+            for (int e = 0; e < kPer; ++e) x.x[e] = p[e * kStep];        // anything behind the end
+        }
+        o = x;
+        if (changing) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            int c = count.x[e];
-            const bool prompt = c < 0;
-            c &= 0x7fff;
-            if (stepping) c += __popc(step[e] & ((2u << (j0 + k)) - 1u));
-            float y = to_f32(x[k].x[e]);
-            if (c > 0 || prompt) {
-                y = y > 0.0f ? __fdiv_rn(y, theta) : y * theta;
-                if (c > 0) y = (y - alpha * (float)c) - beta;
+            for (int e = 0; e < kPer; ++e) {
+                if (!((changing >> e) & 1u)) continue;
+                float y = to_f32(x.x[e]), s = less[e];
+                bool known = (seen >> e) & 1u;
+                if (near) {
+                    const int more = __popc(step[e / 2] & (((2u << (j0 + k)) - 1u) << (16 * (e & 1))));
+                    if (more) {
+                        s += (count.x[e] & 0x7fff) > 0 ? alpha * (float)more : fmaf(alpha, (float)more, beta);
+                        known = true;
+                    }
+                }
+                y = known ? y * (y > 0.0f ? inverse : theta) : y;
+                o.x[e] = from_f32<T>(y - s);
             }
-            if (b1 > b0) y += s_bias[first - base + e * kStep];
-            const bool allow = VEC || !a.mask ? (allowed[k] >> e) & 1u : (__shfl_sync(0xffffffffu, allowed[k], e) >> lane) & 1u;
-            if (!allow) y = -CUDART_INF_F;
-            o.x[e] = from_f32<T>(y);
-            // NaN differs from itself and is stored again
-            if (in_place) changed |= !(to_f32(o.x[e]) == to_f32(x[k].x[e]));
+        }
+        if (a.mask) {
+            uint32_t mine = allowed[0];
+            if (!VEC) {
+                mine = 0;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) mine |= ((__shfl_sync(0xffffffffu, allowed[0], e) >> lane) & 1u) << e;
+            }
+            apply_mask(o, mine);
+#pragma unroll
+            for (int i = 0; i + 1 < kBatch; ++i) allowed[i] = allowed[i + 1];
         }
         if (VEC) {
-            if (changed) *reinterpret_cast<Row8<T>*>(p) = o;
+            if (first < a.vocab && (!in_place || !same_bits(o, x))) reinterpret_cast<Row8<T>*>(out)[tid] = o;
         } else {
+            T* p = reinterpret_cast<T*>(out) + tid;
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
                 if (first + e * kStep < a.vocab) p[e * kStep] = o.x[e];
@@ -225,7 +315,7 @@ __device__ __forceinline__ uint32_t* count_word(int16_t* at) {
 }
 // word with add added to the 16-bit half at `shift`, saturating in its low 15 bits
 __device__ __forceinline__ uint32_t add_to(uint32_t word, int shift, int add) {
-    const uint32_t now = (uint32_t)min((int)((word >> shift) & kCountCap) + add, kCountCap);
+    const uint32_t now = min(((word >> shift) & kCountCap) + (uint32_t)add, (uint32_t)kCountCap);
     return (word & ~((uint32_t)kCountCap << shift)) | (now << shift);
 }
 // the order of additions does not matter
@@ -248,6 +338,8 @@ __device__ __forceinline__ bool slot_range(const CountArgs& a, int slot, int64_t
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
     return false;
 }
+
+constexpr int kFew = 64;      // tokens per slot up to which every token has a thread of its own
 
 // Few tokens per slot, or marks of a prompt (a mark that is there already costs no atomic): a thread per
 // token; equal tokens of a warp are added once.
@@ -278,71 +370,50 @@ __global__ void __launch_bounds__(kThreads) count_kernel(CountArgs a) {
     if (t >= 0 && (threadIdx.x & 31) == __ffs(same) - 1) add_count(at, __popc(same));
 }
 
-// Long histories: frequent tokens would meet in the same words, so a CTA first adds up its 4,096 tokens in
-// a shared hash table (half full at most) and then adds each different token once.  Every phase is a few
-// independent accesses per thread: 4 tokens, 8 places of the table.
-constexpr int kHistory = 4096, kTable = 8192, kHistoryThreads = 1024;
+// Long histories: frequent tokens of many threads would meet in the same words.  So a CTA owns 16,384 vocabulary entries
+// of a slot, reads all of the slot's tokens (they come from L2 for all but the first CTA), counts its own in shared
+// memory and adds each entry once: no atomics in global memory, no order.
+constexpr int kRange = 16384, kHistoryThreads = 1024, kAhead = 16;
 
 __global__ void __launch_bounds__(kHistoryThreads) count_history_kernel(CountArgs a) {
-    extern __shared__ int s_table[];              // [kTable] keys, then [kTable] counts
+    extern __shared__ __align__(16) int s_count[];              // [kRange]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int* keys = s_table;
-    int* sums = s_table + kTable;
-#pragma unroll
-    for (int i = 0; i < kTable / kHistoryThreads; ++i) {
-        keys[i * kHistoryThreads + threadIdx.x] = -1;
-        sums[i * kHistoryThreads + threadIdx.x] = 0;
-    }
+    for (int i = threadIdx.x; i < kRange / 4; i += kHistoryThreads) reinterpret_cast<int4*>(s_count)[i] = make_int4(0, 0, 0, 0);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int slot = blockIdx.y;
+    const int slot = blockIdx.y, base = blockIdx.x * kRange;
     int64_t begin;
     int n;
-    if (!slot_range(a, slot, &begin, &n)) return;
-    const int64_t from = (int64_t)blockIdx.x * kHistory;
-    if (from >= n) return;
-    int t[kHistory / kHistoryThreads];
+    if (!slot_range(a, slot, &begin, &n) || n == 0) return;
+    __syncthreads();
+    const int32_t* tokens = a.tokens + begin;
+    bool bad = false;
+    for (int64_t i0 = threadIdx.x; i0 < n; i0 += kAhead * kHistoryThreads) {
+        int t[kAhead];
 #pragma unroll
-    for (int k = 0; k < kHistory / kHistoryThreads; ++k) {
-        const int64_t i = from + k * kHistoryThreads + threadIdx.x;
-        t[k] = i < n ? a.tokens[begin + i] : -1;
-        if (i < n && (t[k] < 0 || t[k] >= a.vocab)) {
-            if (a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
-            t[k] = -1;
+        for (int k = 0; k < kAhead; ++k) t[k] = i0 + k * kHistoryThreads < n ? tokens[i0 + k * kHistoryThreads] : base;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i0 + k * kHistoryThreads >= n) break;
+            bad |= t[k] < 0 || t[k] >= a.vocab;
+            if (t[k] >= base && t[k] < min(base + kRange, a.vocab)) atomicAdd(&s_count[t[k] - base], 1);
         }
     }
+    if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
     __syncthreads();
+    // two entries per word; the stride is even, so a word of this slot is this CTA's alone
+    uint32_t* words = reinterpret_cast<uint32_t*>(a.counts + (int64_t)slot * a.stride + base);
+    constexpr int kWords = kRange / 2 / kHistoryThreads;
+    uint32_t was[kWords];
+    int2 add[kWords];
 #pragma unroll
-    for (int k = 0; k < kHistory / kHistoryThreads; ++k) {
-        if (t[k] < 0) continue;
-        // open addressing ends: at most kHistory of kTable places are taken
-        uint32_t h = ((uint32_t)t[k] * 2654435761u) >> 19;
-        for (int key = atomicCAS(&keys[h], -1, t[k]); key != -1 && key != t[k]; key = atomicCAS(&keys[h], -1, t[k])) h = (h + 1) & (kTable - 1);
-        atomicAdd(&sums[h], 1);
+    for (int k = 0; k < kWords; ++k) {
+        const int i = k * kHistoryThreads + threadIdx.x;
+        add[k] = reinterpret_cast<const int2*>(s_count)[i];
+        if (add[k].x | add[k].y) was[k] = words[i];
     }
-    __syncthreads();
-    int16_t* counts = a.counts + (int64_t)slot * a.stride;
-    constexpr int kPlaces = kTable / kHistoryThreads;
-    int key[kPlaces];
-    uint32_t seen[kPlaces];
 #pragma unroll
-    for (int k = 0; k < kPlaces; ++k) {
-        key[k] = keys[k * kHistoryThreads + threadIdx.x];
-        if (key[k] >= 0) seen[k] = *reinterpret_cast<volatile uint32_t*>(count_word(counts + key[k]));
-    }
-    uint32_t open = 0;                            // places whose addition has not gone through
-#pragma unroll
-    for (int k = 0; k < kPlaces; ++k)
-        if (key[k] >= 0) {
-            const int shift = (key[k] & 1) * 16;  // rows begin on whole words
-            const uint32_t now = add_to(seen[k], shift, sums[k * kHistoryThreads + threadIdx.x]);
-            if (now != seen[k] && atomicCAS(count_word(counts + key[k]), seen[k], now) != seen[k]) open |= 1u << k;
-        }
-    while (open) {
-        const int k = __ffs(open) - 1;
-        open &= open - 1;
-        const int place = k * kHistoryThreads + threadIdx.x;
-        add_count(counts + keys[place], sums[place]);
-    }
+    for (int k = 0; k < kWords; ++k)
+        if (add[k].x | add[k].y) words[k * kHistoryThreads + threadIdx.x] = add_to(add_to(was[k], 0, add[k].x), 16, add[k].y);
 }
 
 template <typename K, typename A>
@@ -380,11 +451,11 @@ int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_stride, in
         return Q3KV_ERR_INVALID_ARG;
     CountArgs a{d_counts, counts_stride, vocab, d_tokens, num_tokens, d_offsets, d_n, max_n, d_status};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!prompt && max_n > kThreads) {
-        constexpr size_t smem = 2 * kTable * sizeof(int);
+    if (!prompt && max_n > kFew) {
+        constexpr size_t smem = kRange * sizeof(int);
         cudaError_t ce = cudaFuncSetAttribute(count_history_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (ce != cudaSuccess) return cuda_status(ce);
-        return cuda_status(launch(count_history_kernel, a, dim3((unsigned)(((int64_t)max_n + kHistory - 1) / kHistory), num_slots), smem, st,
+        return cuda_status(launch(count_history_kernel, a, dim3((unsigned)(((int64_t)vocab + kRange - 1) / kRange), num_slots), smem, st,
                                   kHistoryThreads));
     }
     const dim3 grid((unsigned)(((int64_t)max_n + kThreads - 1) / kThreads), (unsigned)num_slots);
@@ -439,9 +510,10 @@ int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dty
     // rows start on 16 bytes and end with a whole group of 8 entries
     const bool vec = vocab % 8 == 0;
     if (dtype == Q3KV_F32)
-        return cuda_status(vec ? launch(process_logits_kernel<float, true>, a, grid, 0, st) : launch(process_logits_kernel<float, false>, a, grid, 0, st));
-    return cuda_status(vec ? launch(process_logits_kernel<__nv_bfloat16, true>, a, grid, 0, st)
-                           : launch(process_logits_kernel<__nv_bfloat16, false>, a, grid, 0, st));
+        return cuda_status(launch(vec ? process_logits_kernel<float, true> : process_logits_kernel<float, false>, a, grid,
+                                  kBatch * kRowBytes<float>, st));
+    return cuda_status(launch(vec ? process_logits_kernel<__nv_bfloat16, true> : process_logits_kernel<__nv_bfloat16, false>, a, grid,
+                              kBatch * kRowBytes<__nv_bfloat16>, st));
 }
 
 }  // extern "C"
