@@ -39,8 +39,14 @@ struct Raw16 {
     // largest finite magnitude, as float32 bits (which are in the magnitudes' order)
     __device__ __forceinline__ uint32_t top(bool* finite) const {
         uint32_t m = 0;
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(at(i)) & 0x7fffffffu);
+            for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7fffffffu);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);       // two values at a time
+            m = max(m & 0xffff0000u, m << 16);
+        }
         if (m >= 0x7f800000u) {
             *finite = false;
             m = 0;
@@ -65,12 +71,21 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t two) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
+__device__ __forceinline__ float2 times(float a, float b, float f) {       // both products in one instruction
+    float2 x = make_float2(a, b), y = make_float2(f, f), r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(x)), "l"(reinterpret_cast<unsigned long long&>(y)));
+    return r;
+}
 template <typename At>
 __device__ __forceinline__ uint4 encode16(At x, float inv) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = e4m3x2(x(4 * i) * inv, x(4 * i + 1) * inv) | (e4m3x2(x(4 * i + 2) * inv, x(4 * i + 3) * inv) << 16);
+    for (int i = 0; i < 4; ++i) {
+        const float2 lo = times(x(4 * i), x(4 * i + 1), inv), hi = times(x(4 * i + 2), x(4 * i + 3), inv);
+        w[i] = __byte_perm(e4m3x2(lo.x, lo.y), e4m3x2(hi.x, hi.y), 0x5410);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -84,27 +99,26 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 6 : 4) append
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int slot = blockIdx.y, head = blockIdx.z;
-    const int n_new = a.n_new[slot];
-    const int64_t len = a.slot_len[slot], first_row = a.row_offsets[slot];
+    const int n_new = a.n_new[slot], len = a.slot_len[slot], first_row = a.row_offsets[slot];
     if (n_new == 0) return;
-    const int64_t end = len + n_new;
     const bool report = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && a.status;
     if (n_new < 0 || n_new > a.max_n_new || len < 0) {
         if (report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
         return;
     }
-    const int64_t room = (int64_t)a.max_pages_per_slot * kPageSize;
-    if (end > room && report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);      // positions behind the table are skipped
-    const int64_t block = len / kBs8Block + blockIdx.x, p0 = block * kBs8Block;
-    if (p0 >= end || p0 >= room) return;
+    // positions as unsigned 32-bit numbers; those behind the table are skipped
+    const uint32_t room = (uint32_t)min((int64_t)a.max_pages_per_slot * kPageSize, (int64_t)INT32_MAX + 1), want = (uint32_t)len + (uint32_t)n_new;
+    if (want > room && report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
+    const uint32_t end = min(want, room), p0 = ((uint32_t)len / kBs8Block + blockIdx.x) * kBs8Block;
+    if (p0 >= end) return;
     const int32_t page = a.page_table[(int64_t)slot * a.max_pages_per_slot + p0 / kPageSize];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = (warp & 1) * 8 + (lane & 7), chunk = (warp >> 1) * 4 + (lane >> 3);
-    const int64_t pos = p0 + row;
-    const bool fresh = pos >= len && pos < end, kept = pos < len;
+    const uint32_t row = (warp & 1) * 8 + (lane & 7), chunk = (warp >> 1) * 4 + (lane >> 3);
+    const uint32_t pos = p0 + row;
+    const bool kept = pos < (uint32_t)len, fresh = !kept && pos < end;
     Raw16<T> x[2];
     if (fresh) {
-        const int64_t at = ((first_row + (pos - len)) * a.num_kv_heads + head) * kHeadDim + chunk * 16;
+        const int64_t at = ((int64_t)(first_row + (int)(pos - (uint32_t)len)) * a.num_kv_heads + head) * kHeadDim + chunk * 16;
         x[0].load(static_cast<const T*>(a.k) + at);
         x[1].load(static_cast<const T*>(a.v) + at);
     }
@@ -113,12 +127,12 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 6 : 4) append
         return;
     }
     uint8_t* unit = a.pool + bs8_offset(a.num_layers, a.num_kv_heads, page, a.layer, head, 0);
-    const int in_page = (int)(p0 % kPageSize);
+    const uint32_t in_page = p0 % kPageSize;
     uint8_t* code = unit + ((in_page + row) / 8 * 16 + chunk) * 128 + (row % 8) * 16;
     uint8_t* scale = unit + kBs8CodeBytes + 4 * (in_page / kBs8Block);
     int old[2] = {-kBs8MaxExp, -kBs8MaxExp};
     uint4 was[2];
-    if (p0 < len) {
+    if (p0 < (uint32_t)len) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
             old[kv] = scale_exp(*reinterpret_cast<const float*>(scale + kv * kBs8UnitBytes));
