@@ -724,7 +724,8 @@ Q3KV_API int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_
  * A slot with T_b > L_b, L_b above max_ctx_len or beyond its page table, T_b above max_n_q or a
  * negative offset sets Q3KV_STATUS_BAD_LENGTH and its rows are left as they were.  Positions of
  * a page out of range count as hidden (Q3KV_STATUS_BAD_PAGE); a row that sees nothing is 0.  A
- * query row that is not finite gives NaN. */
+ * query row that is not finite gives NaN; scores have to stay within float32.  out must not
+ * overlap any other operand, nor may the workspace. */
 Q3KV_API int q3kv_bs8_workspace_bytes(const q3kv_cache_desc* desc, int32_t num_slots, int64_t max_ctx_len,
                      int32_t max_n_q, int32_t impl, size_t* bytes);
 Q3KV_API int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* d_pool,
@@ -741,7 +742,8 @@ Q3KV_API int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, con
  * that begins before d_rows[i] is copied).
  *   desc            the cache's shape; num_pages of the source pool
  *   d_dst_pool, dst_num_pages   may be the source pool (dst_num_pages = desc->num_pages);
- *                   pools that overlap otherwise are refused
+ *                   pools that overlap otherwise are refused, and
+ *                   so are lists within the destination pool
  *   n               at most 4096 (Q3KV_ERR_UNSUPPORTED above)
  * All pairs are copied as if at once.  A pair with a page out of range, or whose destination is
  * another pair's destination or (in one pool) source, sets Q3KV_STATUS_BAD_PAGE and is skipped; a row count
@@ -781,6 +783,7 @@ Q3KV_API int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_s
  * it comes after the step's tokens t_0 .. t_j (d_tokens, same indexing), which d_counts does not
  * hold yet.  With c = count + #{i <= j : t_i = x}, in float32, for every token x of the row:
  *   y = l;  if c > 0 or the prompt holds x:  y = y > 0 ? y / repetition : y * repetition
+ *     (the quotient as the product with 1 / repetition)
  *   if c > 0:  y = y - frequency c - presence
  *   y = y + bias(x);  where the row's mask bit is 0:  y = -inf
  * and out = y rounded to the logits' dtype (f32 or bf16).

@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
     int c0 = 0, c1 = 0;
     if (pair < s.pairs(heads) && r < min(a.rows, kGroup * (s.T - T0))) {
         const int64_t total = s_at[1], begin = s_at[0] + (int64_t)pair * s.tiles;
-        c0 = bs8_cta_of(begin, total, a.ctas);
-        c1 = bs8_cta_of(begin + s.tiles - 1, total, a.ctas);
+        c0 = bs8_cta_of(begin, total, bs8_ctas(a, total));
+        c1 = bs8_cta_of(begin + s.tiles - 1, total, bs8_ctas(a, total));
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

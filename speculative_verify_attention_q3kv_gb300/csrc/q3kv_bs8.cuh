@@ -1,7 +1,7 @@
 // Verify attention over the block-scaled 8-bit cache: what both legs and the merge share.
 //
 // Work is cut into tiles of 128 positions of one (slot, row chunk, kv head) pair.  All tiles of a call,
-// pair after pair, are shared out evenly: CTA i of G takes tiles [i n / G, (i + 1) n / G).  A pair inside one
+// pair after pair, are shared out evenly: of G = min(CTAs, tiles), CTA i takes tiles [i n / G, (i + 1) n / G), one at least.  A pair inside one
 // CTA's share goes straight to the output; of a pair that is cut, each CTA writes a partial (unnormalised
 // output, maximum, sum), of which it has at most two: the pair its share begins inside, and the pair it ends
 // inside.  So the workspace depends on the GPU alone, a ragged batch keeps every SM busy to the last tile, and
@@ -77,7 +77,8 @@ __device__ __forceinline__ int64_t bs8_muldiv(int64_t a, int b, int64_t c) {
     if (a * b < (1ll << 32) && c < (1ll << 32)) return (uint32_t)(a * b) / (uint32_t)c;
     return a * b / c;
 }
-// First tile of CTA i's share of n, and the CTA that owns tile t.
+// CTAs that have a share; first tile of CTA i's share of n, and the CTA that owns tile t.
+__device__ __forceinline__ int bs8_ctas(const Bs8Args& a, int64_t n) { return (int)min((int64_t)a.ctas, n); }
 __device__ __forceinline__ int64_t bs8_begin(int i, int64_t n, int G) { return bs8_muldiv(n, i, G); }
 __device__ __forceinline__ int bs8_cta_of(int64_t t, int64_t n, int G) {
     const int64_t x = (t + 1) * G - 1;
@@ -120,8 +121,9 @@ __device__ __forceinline__ Bs8Share bs8_share(const Bs8Args& a, int i, bool* bad
     for (int b = lane + 32; b < a.num_slots; b += 32) n += bs8_slot(a, b, bad).total(a.num_kv_heads);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    const int64_t begin = bs8_begin(i, n, a.ctas), end = bs8_begin(i + 1, n, a.ctas);
-    if (begin >= end) return w;
+    const int G = bs8_ctas(a, n);
+    if (i >= G) return w;
+    const int64_t begin = bs8_begin(i, n, G), end = bs8_begin(i + 1, n, G);
     int64_t before = 0;
     for (int b0 = 0;; b0 += 32) {                                // ends: begin < n
         if (b0 > 0) s = b0 + lane < a.num_slots ? bs8_slot(a, b0 + lane, nullptr) : Bs8Slot{0, 0, 0, 0};

@@ -129,6 +129,10 @@ int copy_impl(int fmt, void* stream, const q3kv_cache_desc* desc, const void* d_
     const int64_t src_bytes = (int64_t)(page * desc->num_pages), dst_bytes = (int64_t)(page * dst_num_pages);
     if (d_src_pool == d_dst_pool ? dst_num_pages != desc->num_pages : overlap(d_src_pool, src_bytes, d_dst_pool, dst_bytes))
         return Q3KV_ERR_INVALID_ARG;
+    const int64_t list = 4 * (int64_t)n;
+    if (overlap(d_dst_pool, dst_bytes, d_src, list) || overlap(d_dst_pool, dst_bytes, d_dst, list) ||
+        (d_rows && overlap(d_dst_pool, dst_bytes, d_rows, list)) || (d_status && overlap(d_dst_pool, dst_bytes, d_status, 4)))
+        return Q3KV_ERR_INVALID_ARG;
     CopyArgs a{};
     a.src_pool = static_cast<const uint8_t*>(d_src_pool);
     a.dst_pool = static_cast<uint8_t*>(d_dst_pool);
