@@ -184,11 +184,10 @@ def _pool_need(pool_bytes_fn, lib, desc_bytes: bytes) -> int:
     return pool_bytes_fn(CacheDesc.from_buffer_copy(desc_bytes))
 
 
-def _refuse_overlap(out_name: str, out: torch.Tensor, **others) -> None:
-    """Refuse an output that shares bytes with another operand of the call."""
-    start, end = out.data_ptr(), out.data_ptr() + out.nbytes
-    for name, t in others.items():
-        if t is not None and t.nbytes and start < t.data_ptr() + t.nbytes and t.data_ptr() < end:
+def _refuse_overlap(out_name: str, start: int, nbytes: int, *others) -> None:
+    """Refuse an output that shares bytes with another operand (name, pointer, bytes) of the call."""
+    for name, at, n in others:
+        if start < at + n and at < start + nbytes:
             raise ValueError(f"{out_name} overlaps {name}")
 
 
@@ -810,7 +809,8 @@ def bs8_append(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tensor, sl
     shape = k.shape
     if len(shape) != 3 or shape[1] != desc.num_kv_heads or shape[2] != HEAD_DIM or v.shape != shape:
         raise ValueError(f"k and v must be [rows, {desc.num_kv_heads}, {HEAD_DIM}], got {tuple(shape)} and {tuple(v.shape)}")
-    _refuse_overlap("pool", pool, k=k, v=v, page_table=page_table, slot_len=slot_len, n_new=n_new, row_offsets=row_offsets)
+    size = k.nbytes
+    _refuse_overlap("pool", p_pool, pool.nbytes, ("k", p_k, size), ("v", p_v, size))
     rc = lib.q3kv_bs8_append(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_len, p_new, p_off, n, max_n_new, layer,
                              p_k, p_v, _dtype_code(k), p_status)
     check(rc, "q3kv_bs8_append")
@@ -840,10 +840,11 @@ def bs8_verify_attn(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tenso
         raise ValueError(f"q must be [rows, {heads}, {HEAD_DIM}], got {tuple(shape)}")
     if out.dim() != 3 or out.shape[0] < shape[0] or out.shape[1:] != shape[1:]:
         raise ValueError(f"out must be [rows >= {shape[0]}, {heads}, {HEAD_DIM}], got {tuple(out.shape)}")
-    _refuse_overlap("out", out, q=q, pool=pool, workspace=workspace, page_table=page_table, ctx_len=ctx_len, n_q=n_q, q_offsets=q_offsets)
-    _refuse_overlap("workspace", workspace, q=q, pool=pool, page_table=page_table, ctx_len=ctx_len, n_q=n_q, q_offsets=q_offsets)
+    reads, ws_bytes = (("q", p_q, q.nbytes), ("the pool", p_pool, pool.nbytes)), workspace.nbytes
+    _refuse_overlap("out", p_out, out.nbytes, *reads, ("the workspace", p_ws, ws_bytes))
+    _refuse_overlap("workspace", p_ws, ws_bytes, *reads)
     rc = lib.q3kv_bs8_verify_attn(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_ctx, p_nq, p_off, n, max_ctx_len,
-                                  max_n_q, layer, p_q, _dtype_code(q), p_out, impl, p_ws, workspace.nbytes, p_status)
+                                  max_n_q, layer, p_q, _dtype_code(q), p_out, impl, p_ws, ws_bytes, p_status)
     check(rc, "q3kv_bs8_verify_attn")
 
 

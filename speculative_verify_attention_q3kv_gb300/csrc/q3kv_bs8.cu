@@ -458,10 +458,6 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
 
 template <typename K, typename A>
 cudaError_t launch(K kernel, const A& a, dim3 grid, int threads, size_t smem, cudaStream_t st) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -497,6 +493,9 @@ size_t bs8_partials(int ctas) { return (size_t)ctas * 2 * kBs8PartFloats * sizeo
 }  // namespace
 
 cudaError_t launch_bs8_fma(const Bs8Args& a, cudaStream_t st) {
+    static std::atomic<bool> allowed[kMaxDevices];
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(verify_bs8_fma_kernel), sizeof(FmaSmem), allowed);
+    if (e != cudaSuccess) return e;
     return launch(verify_bs8_fma_kernel, a, dim3((unsigned)a.ctas), kFmaThreads, sizeof(FmaSmem), st);
 }
 

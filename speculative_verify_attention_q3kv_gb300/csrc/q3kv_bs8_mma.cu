@@ -690,7 +690,8 @@ template <int R, bool F32>
 cudaError_t launch_r(const Bs8Args& a, cudaStream_t st) {
     constexpr size_t smem = sizeof(Smem<R, F32>) + 128;
     static_assert(smem <= 227 * 1024, "shared memory of one CTA");
-    const cudaError_t e = cudaFuncSetAttribute(verify_bs8_mma_kernel<R, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> allowed[kMaxDevices];
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(verify_bs8_mma_kernel<R, F32>), smem, allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.ctas);

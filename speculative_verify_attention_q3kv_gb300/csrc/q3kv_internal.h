@@ -1,6 +1,7 @@
 // Internal declarations shared by the host entry points and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <stddef.h>
@@ -183,6 +184,16 @@ constexpr size_t kAcceptPartialBytes = 24;   // largest per-chunk record (sample
 int check_desc(const q3kv_cache_desc* d);
 int cuda_status(cudaError_t e);
 int device_sm_count(int* sms);
+// Once per kernel and device: allow a kernel `smem` bytes of dynamic shared memory (done: a flag per device of that kernel).
+constexpr int kMaxDevices = 64;
+inline cudaError_t allow_smem(const void* kernel, size_t smem, std::atomic<bool> (&done)[kMaxDevices]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
 // [a, a + an) and [b, b + bn) bytes share one
 inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);

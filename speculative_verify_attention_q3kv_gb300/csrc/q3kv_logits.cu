@@ -453,7 +453,8 @@ int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_stride, in
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!prompt && max_n > kFew) {
         constexpr size_t smem = kRange * sizeof(int);
-        cudaError_t ce = cudaFuncSetAttribute(count_history_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<bool> allowed[kMaxDevices];
+        cudaError_t ce = allow_smem(reinterpret_cast<const void*>(count_history_kernel), smem, allowed);
         if (ce != cudaSuccess) return cuda_status(ce);
         return cuda_status(launch(count_history_kernel, a, dim3((unsigned)(((int64_t)vocab + kRange - 1) / kRange), num_slots), smem, st,
                                   kHistoryThreads));
