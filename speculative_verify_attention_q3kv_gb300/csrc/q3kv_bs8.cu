@@ -365,19 +365,23 @@ __global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) 
 }
 
 // ---------------------------------------------------------------- merge
-// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partials of a cut pair; one CTA per row, eight groups of
-// 64 threads with every eighth partial each.  Bound: latency.  So a group's partials are loaded together with their
-// maxima, ten at a time (80 partials of a row are under way at once), and the groups agree on M at the end.
-constexpr int kMergeGroups = 8, kMergeThreads = 64 * kMergeGroups, kMergeBatch = 10;
+// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over the partials of a cut pair.  A group of 64 threads loads its
+// partials of a row together with their maxima, ten at a time, and groups that share a row agree on M at the end.
+// Bound: latency.  Few rows (one slot): eight groups per row and one row per CTA, so that 80 partials of a row are under
+// way at once; many rows, which then have few partials each: a group per row, four rows per CTA, so that few CTAs come and
+// go (1,280 rows of 5 slots: 19 us with a CTA each, 5 so; 128 rows of 76 partials: 6 us with a CTA each).
+constexpr int kMergeBatch = 10;
 
-__global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
-    __shared__ float4 s_o[kMergeGroups][64];
-    __shared__ float2 s_ml[kMergeGroups];
+template <int GROUPS, int ROWS>          // groups per row, rows per CTA
+__global__ void __launch_bounds__(64 * GROUPS * ROWS) merge_bs8_kernel(Bs8Args a) {
+    __shared__ float4 s_o[GROUPS][64];
+    __shared__ float2 s_ml[GROUPS];
     __shared__ int64_t s_at[2];                  // tiles before the slot, and of all slots
     // The lengths were complete before the verify kernel let this one start; its partials are after the wait.  Every CTA
     // waits, also one without work: whoever follows this kernel goes by its end.
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = a.num_kv_heads;
-    const int slot = blockIdx.z, pair = blockIdx.y, r = blockIdx.x;
+    const int col = tid & 63, group = (tid >> 6) % GROUPS;
+    const int slot = blockIdx.z, pair = blockIdx.y, r = blockIdx.x * ROWS + (tid >> 6) / GROUPS;
     const Bs8Slot s = bs8_slot(a, slot, nullptr);
     const int T0 = pair / heads * (a.rows / kGroup), head = pair % heads;
     if (warp < 2) {
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
     }
     __syncthreads();
     int c0 = 0, c1 = 0;
-    if (pair < s.pairs(heads) && r < min(a.rows, kGroup * (s.T - T0))) {
+    if (pair < s.pairs(heads)) {
         const int64_t total = s_at[1], begin = s_at[0] + (int64_t)pair * s.tiles;
         c0 = bs8_cta_of(begin, total, bs8_ctas(a, total));
         c1 = bs8_cta_of(begin + s.tiles - 1, total, bs8_ctas(a, total));
@@ -394,16 +398,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (c0 == c1) return;                        // nothing here, or the pair was not cut
+    if (r >= min(a.rows, kGroup * (s.T - T0))) return;       // a CTA of several rows has no barrier from here on
     const int n = c1 - c0 + 1;
-    const int col = tid & 63, group = tid >> 6;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float m = -CUDART_INF_F, l = 0.0f;
-    for (int i0 = group; i0 < n; i0 += kMergeGroups * kMergeBatch) {
+    for (int i0 = group; i0 < n; i0 += GROUPS * kMergeBatch) {
         float4 v[kMergeBatch];
         float2 ml[kMergeBatch];
 #pragma unroll
         for (int k = 0; k < kMergeBatch; ++k) {
-            const int i = i0 + k * kMergeGroups;
+            const int i = i0 + k * GROUPS;
             if (i < n) {                         // the pair's first CTA ends inside it, the others begin inside it
                 const float* p = a.partials + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kBs8PartFloats;
                 ml[k] = *reinterpret_cast<const float2*>(p + kBs8Rows * kHeadDim + 2 * r);
@@ -431,25 +435,27 @@ __global__ void __launch_bounds__(kMergeThreads) merge_bs8_kernel(Bs8Args a) {
             o.w = fmaf(f, v[k].w, o.w);
         }
     }
-    s_o[group][col] = o;
-    if (col == 0) s_ml[group] = make_float2(m, l);
-    __syncthreads();
-    if (tid >= 64) return;
-    float top = -CUDART_INF_F;
+    if constexpr (GROUPS > 1) {
+        s_o[group][col] = o;
+        if (col == 0) s_ml[group] = make_float2(m, l);
+        __syncthreads();
+        if (tid >= 64) return;
+        float top = -CUDART_INF_F;
 #pragma unroll
-    for (int g = 0; g < kMergeGroups; ++g) top = fmaxf(top, s_ml[g].x);
-    if (top == -CUDART_INF_F) top = 0.0f;        // the row saw nothing
-    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    l = 0.0f;
+        for (int g = 0; g < GROUPS; ++g) top = fmaxf(top, s_ml[g].x);
+        if (top == -CUDART_INF_F) top = 0.0f;    // the row saw nothing
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        l = 0.0f;
 #pragma unroll
-    for (int g = 0; g < kMergeGroups; ++g) {
-        const float f = exp2f(s_ml[g].x - top);
-        const float4 v = s_o[g][col];
-        l = fmaf(f, s_ml[g].y, l);
-        o.x = fmaf(f, v.x, o.x);
-        o.y = fmaf(f, v.y, o.y);
-        o.z = fmaf(f, v.z, o.z);
-        o.w = fmaf(f, v.w, o.w);
+        for (int g = 0; g < GROUPS; ++g) {
+            const float f = exp2f(s_ml[g].x - top);
+            const float4 v = s_o[g][col];
+            l = fmaf(f, s_ml[g].y, l);
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
     }
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     const int64_t at = (((int64_t)a.q_offsets[slot] + T0 + (r >> 3)) * heads * kGroup + head * kGroup + (r & 7)) * kHeadDim + 4 * col;
@@ -471,11 +477,13 @@ cudaError_t launch(K kernel, const A& a, dim3 grid, int threads, size_t smem, cu
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-// The merge's grid covers every pair that may be cut; a call whose pairs are all cut or whole alike has few idle CTAs.
+// The merge's grid covers every pair that may be cut.
 cudaError_t launch_merge_bs8(const Bs8Args& a, cudaStream_t st) {
-    const int chunks = (kGroup * a.max_n_q + a.rows - 1) / a.rows;
-    const dim3 grid((unsigned)(chunks > 1 ? a.rows : kGroup * a.max_n_q), (unsigned)(chunks * a.num_kv_heads), (unsigned)a.num_slots);
-    return launch(merge_bs8_kernel, a, grid, kMergeThreads, 0, st);
+    const int chunks = (kGroup * a.max_n_q + a.rows - 1) / a.rows, pairs = chunks * a.num_kv_heads;
+    const int rows = chunks > 1 ? a.rows : kGroup * a.max_n_q;
+    if ((int64_t)rows * pairs * a.num_slots > 2 * a.ctas)
+        return launch(merge_bs8_kernel<1, 4>, a, dim3((unsigned)((rows + 3) / 4), (unsigned)pairs, (unsigned)a.num_slots), 256, 0, st);
+    return launch(merge_bs8_kernel<8, 1>, a, dim3((unsigned)rows, (unsigned)pairs, (unsigned)a.num_slots), 512, 0, st);
 }
 
 int bs8_check(const q3kv_cache_desc* d, int32_t num_slots, int64_t max_ctx_len, int32_t max_n_q, int32_t impl) {
