@@ -376,7 +376,7 @@ template <int GROUPS, int ROWS>          // groups per row, rows per CTA
 __global__ void __launch_bounds__(64 * GROUPS * ROWS) merge_bs8_kernel(Bs8Args a) {
     __shared__ float4 s_o[GROUPS][64];
     __shared__ float2 s_ml[GROUPS];
-    __shared__ int64_t s_at[2];                  // tiles before the slot, and of all slots
+    __shared__ uint64_t s_at[2];                 // tiles before the slot, and of all slots
     // The lengths were complete before the verify kernel let this one start; its partials are after the wait.  Every CTA
     // waits, also one without work: whoever follows this kernel goes by its end.
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = a.num_kv_heads;
@@ -385,15 +385,23 @@ __global__ void __launch_bounds__(64 * GROUPS * ROWS) merge_bs8_kernel(Bs8Args a
     const Bs8Slot s = bs8_slot(a, slot, nullptr);
     const int T0 = pair / heads * (a.rows / kGroup), head = pair % heads;
     if (warp < 2) {
-        const int64_t n = bs8_tiles_before(a, warp == 0 ? slot : a.num_slots, nullptr);
+        const int upto = warp == 0 ? slot : a.num_slots;
+        const uint64_t n = a.narrow ? bs8_tiles_before<uint32_t>(a, upto, nullptr) : bs8_tiles_before<uint64_t>(a, upto, nullptr);
         if (lane == 0) s_at[warp] = n;
     }
     __syncthreads();
     int c0 = 0, c1 = 0;
     if (pair < s.pairs(heads)) {
-        const int64_t total = s_at[1], begin = s_at[0] + (int64_t)pair * s.tiles;
-        c0 = bs8_cta_of(begin, total, bs8_ctas(a, total));
-        c1 = bs8_cta_of(begin + s.tiles - 1, total, bs8_ctas(a, total));
+        const uint64_t total = s_at[1], begin = s_at[0] + (uint64_t)pair * s.tiles, last = begin + s.tiles - 1;
+        if (a.narrow) {
+            const uint32_t n = (uint32_t)total, G = bs8_ctas(a, n);
+            c0 = bs8_cta_of((uint32_t)begin, n, G);
+            c1 = bs8_cta_of((uint32_t)last, n, G);
+        } else {
+            const uint64_t G = bs8_ctas(a, total);
+            c0 = bs8_cta_of(begin, total, G);
+            c1 = bs8_cta_of(last, total, G);
+        }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -603,10 +611,13 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     a.dtype = dtype;
     a.ctas = ctas;
     a.partials = static_cast<float*>(d_workspace);
-    a.status = d_status;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool mma = impl != Q3KV_IMPL_FMA;
     a.rows = mma ? bs8_mma_rows(dtype) : kBs8Rows;
+    const double most = (double)num_slots * ((max_ctx_len + kBs8Tile - 1) / kBs8Tile) * desc->num_kv_heads *
+                        ((kGroup * max_n_q + a.rows - 1) / a.rows) * ctas;
+    a.narrow = most < 4.0e9;
+    a.status = d_status;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t ce = mma ? launch_bs8_mma(a, st) : launch_bs8_fma(a, st);
     if (ce == cudaSuccess) ce = launch_merge_bs8(a, st);
     return cuda_status(ce);

@@ -34,7 +34,8 @@ struct Bs8Args {
     void* out;
     int32_t dtype;               // of q and out
     int32_t rows;                // query rows per chunk
-    int32_t ctas;                // G
+    int32_t ctas;                // G at most
+    int32_t narrow;              // tiles x CTAs of the whole call fit 32 bits
     float* partials;             // [G][2][kBs8PartFloats]
     int32_t* status;
 };
@@ -47,7 +48,6 @@ int bs8_mma_rows(int dtype);                 // the tensor-core leg's chunk
 struct Bs8Slot {
     int L, T, tiles, chunks;
     __device__ __forceinline__ int pairs(int heads) const { return chunks * heads; }
-    __device__ __forceinline__ int64_t total(int heads) const { return (int64_t)tiles * chunks * heads; }
 };
 
 __device__ __forceinline__ Bs8Slot bs8_slot(const Bs8Args& a, int b, bool* bad) {
@@ -63,27 +63,32 @@ __device__ __forceinline__ Bs8Slot bs8_slot(const Bs8Args& a, int b, bool* bad) 
     return s;
 }
 
-// Tiles of slots [0, b) by a warp; every lane gets it.
-__device__ __forceinline__ int64_t bs8_tiles_before(const Bs8Args& a, int b, bool* bad) {
-    int64_t n = 0;
-    for (int i = threadIdx.x & 31; i < b; i += 32) n += bs8_slot(a, i, bad).total(a.num_kv_heads);
+// All of a call's tiles are counted in type N: 32 bits where the host has seen that tiles x CTAs fit (a fifth of the
+// 64-bit steps' time), 64 otherwise.
+__device__ __forceinline__ uint32_t bs8_warp_sum(uint32_t v) { return __reduce_add_sync(0xffffffffu, v); }
+__device__ __forceinline__ uint64_t bs8_warp_sum(uint64_t v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <typename N>
+__device__ __forceinline__ N bs8_total(const Bs8Slot& s, int heads) { return (N)s.tiles * (N)(s.chunks * heads); }
+
+// Tiles of slots [0, b) by a warp; every lane gets it.
+template <typename N>
+__device__ __forceinline__ N bs8_tiles_before(const Bs8Args& a, int b, bool* bad) {
+    N n = 0;
+    for (int i = threadIdx.x & 31; i < b; i += 32) n += bs8_total<N>(bs8_slot(a, i, bad), a.num_kv_heads);
+    return bs8_warp_sum(n);
 }
 
-// a b / c for a <= 2^40, b and c below 2^31: in 32 bits, which takes a tenth of the time, where the numbers allow it.
-__device__ __forceinline__ int64_t bs8_muldiv(int64_t a, int b, int64_t c) {
-    if (a * b < (1ll << 32) && c < (1ll << 32)) return (uint32_t)(a * b) / (uint32_t)c;
-    return a * b / c;
-}
-// CTAs that have a share; first tile of CTA i's share of n, and the CTA that owns tile t.
-__device__ __forceinline__ int bs8_ctas(const Bs8Args& a, int64_t n) { return (int)min((int64_t)a.ctas, n); }
-__device__ __forceinline__ int64_t bs8_begin(int i, int64_t n, int G) { return bs8_muldiv(n, i, G); }
-__device__ __forceinline__ int bs8_cta_of(int64_t t, int64_t n, int G) {
-    const int64_t x = (t + 1) * G - 1;
-    return (int)(x < (1ll << 32) && n < (1ll << 32) ? (uint32_t)x / (uint32_t)n : x / n);
-}
+// CTAs that have a share of n tiles; first tile of CTA i's share, and the CTA that owns tile t.
+template <typename N>
+__device__ __forceinline__ N bs8_ctas(const Bs8Args& a, N n) { return min((N)a.ctas, n); }
+template <typename N>
+__device__ __forceinline__ N bs8_begin(N i, N n, N G) { return i * n / G; }
+template <typename N>
+__device__ __forceinline__ int bs8_cta_of(N t, N n, N G) { return (int)(((t + 1) * G - 1) / n); }
 
 // One CTA's share as a sequence of segments, each within one pair.
 struct Bs8Share {
@@ -113,24 +118,24 @@ struct Bs8Share {
 };
 
 // By one warp: the first segment of CTA i; tiles = 0 if its share is empty.
-__device__ __forceinline__ Bs8Share bs8_share(const Bs8Args& a, int i, bool* bad) {
+template <typename N>
+__device__ __forceinline__ Bs8Share bs8_share_in(const Bs8Args& a, int i, bool* bad) {
     Bs8Share w{};
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
     Bs8Slot s = lane < a.num_slots ? bs8_slot(a, lane, bad) : Bs8Slot{0, 0, 0, 0};
-    int64_t n = s.total(a.num_kv_heads);
-    for (int b = lane + 32; b < a.num_slots; b += 32) n += bs8_slot(a, b, bad).total(a.num_kv_heads);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    const int G = bs8_ctas(a, n);
-    if (i >= G) return w;
-    const int64_t begin = bs8_begin(i, n, G), end = bs8_begin(i + 1, n, G);
-    int64_t before = 0;
+    N n = bs8_total<N>(s, heads);
+    for (int b = lane + 32; b < a.num_slots; b += 32) n += bs8_total<N>(bs8_slot(a, b, bad), heads);
+    n = bs8_warp_sum(n);
+    const N G = bs8_ctas(a, n);
+    if ((N)i >= G) return w;
+    const N begin = bs8_begin<N>(i, n, G), end = bs8_begin<N>(i + 1, n, G);
+    N before = 0;
     for (int b0 = 0;; b0 += 32) {                                // ends: begin < n
         if (b0 > 0) s = b0 + lane < a.num_slots ? bs8_slot(a, b0 + lane, nullptr) : Bs8Slot{0, 0, 0, 0};
-        int64_t upto = s.total(a.num_kv_heads);
+        N upto = bs8_total<N>(s, heads);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            const N v = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += v;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, before + upto > begin);
@@ -141,15 +146,18 @@ __device__ __forceinline__ Bs8Share bs8_share(const Bs8Args& a, int i, bool* bad
             w.s.T = __shfl_sync(0xffffffffu, s.T, l);
             w.s.tiles = __shfl_sync(0xffffffffu, s.tiles, l);
             w.s.chunks = __shfl_sync(0xffffffffu, s.chunks, l);
-            const int64_t in = begin - (before + __shfl_sync(0xffffffffu, upto, l) - w.s.total(a.num_kv_heads));
-            w.pair = (int)bs8_muldiv(in, 1, w.s.tiles);
-            w.tile = (int)(in - (int64_t)w.pair * w.s.tiles);
-            w.tiles = (int)min((int64_t)(w.s.tiles - w.tile), end - begin);
-            w.left = end - begin - w.tiles;
+            const N in = begin - (before + __shfl_sync(0xffffffffu, upto, l) - bs8_total<N>(w.s, heads));
+            w.pair = (int)(in / (N)w.s.tiles);
+            w.tile = (int)(in - (N)w.pair * (N)w.s.tiles);
+            w.tiles = (int)min((N)(w.s.tiles - w.tile), end - begin);
+            w.left = (int64_t)(end - begin) - w.tiles;
             return w;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);
     }
+}
+__device__ __forceinline__ Bs8Share bs8_share(const Bs8Args& a, int i, bool* bad) {
+    return a.narrow ? bs8_share_in<uint32_t>(a, i, bad) : bs8_share_in<uint64_t>(a, i, bad);
 }
 
 }  // namespace q3kv
