@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) 
     do {
         const int T0 = w.chunk(heads) * (kBs8Rows / kGroup), head = w.head(heads);
         const int nrows = min(kBs8Rows, kGroup * (w.s.T - T0));
-        const int64_t q0 = (int64_t)a.q_offsets[w.slot] + T0;
+        const int64_t q0 = (int64_t)w.s.q0 + T0;
         __syncthreads();                                  // the last segment's outputs are read
         for (int i = tid; i < kBs8Rows * kHeadDim; i += kFmaThreads) {
             const int r = i >> 8, d = i & 255;
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(64 * GROUPS * ROWS) merge_bs8_kernel(Bs8Args a
         }
     }
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    const int64_t at = (((int64_t)a.q_offsets[slot] + T0 + (r >> 3)) * heads * kGroup + head * kGroup + (r & 7)) * kHeadDim + 4 * col;
+    const int64_t at = (((int64_t)s.q0 + T0 + (r >> 3)) * heads * kGroup + head * kGroup + (r & 7)) * kHeadDim + 4 * col;
     st4(a.out, at, a.dtype, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 

@@ -46,14 +46,14 @@ int bs8_mma_rows(int dtype);                 // the tensor-core leg's chunk
 
 // Lengths of one slot; tiles and chunks are 0 for a slot with nothing to do or with lengths the call does not allow.
 struct Bs8Slot {
-    int L, T, tiles, chunks;
+    int L, T, q0, tiles, chunks;             // q0: row of its first query token
     __device__ __forceinline__ int pairs(int heads) const { return chunks * heads; }
 };
 
 __device__ __forceinline__ Bs8Slot bs8_slot(const Bs8Args& a, int b, bool* bad) {
-    Bs8Slot s{a.ctx_len[b], a.n_q[b], 0, 0};
-    const bool ok = s.T > 0 && s.T <= a.max_n_q && s.T <= s.L && s.L <= a.max_ctx_len && s.L <= (int64_t)a.max_pages_per_slot * kPageSize &&
-                    a.q_offsets[b] >= 0;
+    Bs8Slot s{a.ctx_len[b], a.n_q[b], a.q_offsets[b], 0, 0};      // three loads at once
+    const bool ok = (s.T > 0) & (s.T <= a.max_n_q) & (s.T <= s.L) & (s.L <= a.max_ctx_len) & (s.q0 >= 0) &
+                    (s.L <= (int64_t)a.max_pages_per_slot * kPageSize);
     if (ok) {
         s.tiles = (s.L + kBs8Tile - 1) / kBs8Tile;
         s.chunks = (kGroup * s.T + a.rows - 1) / a.rows;
@@ -122,7 +122,7 @@ template <typename N>
 __device__ __forceinline__ Bs8Share bs8_share_in(const Bs8Args& a, int i, bool* bad) {
     Bs8Share w{};
     const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
-    Bs8Slot s = lane < a.num_slots ? bs8_slot(a, lane, bad) : Bs8Slot{0, 0, 0, 0};
+    Bs8Slot s = lane < a.num_slots ? bs8_slot(a, lane, bad) : Bs8Slot{0, 0, 0, 0, 0};
     N n = bs8_total<N>(s, heads);
     for (int b = lane + 32; b < a.num_slots; b += 32) n += bs8_total<N>(bs8_slot(a, b, bad), heads);
     n = bs8_warp_sum(n);
@@ -131,7 +131,7 @@ __device__ __forceinline__ Bs8Share bs8_share_in(const Bs8Args& a, int i, bool* 
     const N begin = bs8_begin<N>(i, n, G), end = bs8_begin<N>(i + 1, n, G);
     N before = 0;
     for (int b0 = 0;; b0 += 32) {                                // ends: begin < n
-        if (b0 > 0) s = b0 + lane < a.num_slots ? bs8_slot(a, b0 + lane, nullptr) : Bs8Slot{0, 0, 0, 0};
+        if (b0 > 0) s = b0 + lane < a.num_slots ? bs8_slot(a, b0 + lane, nullptr) : Bs8Slot{0, 0, 0, 0, 0};
         N upto = bs8_total<N>(s, heads);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -144,6 +144,7 @@ __device__ __forceinline__ Bs8Share bs8_share_in(const Bs8Args& a, int i, bool* 
             w.slot = b0 + l;
             w.s.L = __shfl_sync(0xffffffffu, s.L, l);
             w.s.T = __shfl_sync(0xffffffffu, s.T, l);
+            w.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
             w.s.tiles = __shfl_sync(0xffffffffu, s.tiles, l);
             w.s.chunks = __shfl_sync(0xffffffffu, s.chunks, l);
             const N in = begin - (before + __shfl_sync(0xffffffffu, upto, l) - bs8_total<N>(w.s, heads));

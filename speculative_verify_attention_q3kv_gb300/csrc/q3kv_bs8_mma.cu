@@ -11,7 +11,7 @@
 // Contractions (M = 128, float32 accumulation in TMEM):
 //   S^T[p][r | R + r] = K[p][:] . q1[r][:] | q2[r][:]   A = K codes (K-major), N = 2 R columns, K = 256 dims
 //   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions
-// with R = 16, 32 or 64 query rows (8 heads x tokens, padded).  A position is a TMEM lane, so its block's scales are two
+// with R = 16, 32, 48 or 64 query rows (8 heads x tokens, padded).  A position is a TMEM lane, so its block's scales are two
 // numbers of one thread: the score is (S1 + S2) 2^(eK - k) log2(e) / 16, and V's scale goes into the weight's
 // exponent, p' = 2^(score + eV - m), while the row sum takes p' 2^-eV.  m is raised only when a score passes it by more
 // than 2^7 of headroom (a vote per tile), so most tiles need no maximum and no rescaling.
@@ -37,11 +37,11 @@ constexpr int kMeta = 8;                       // tiles whose scales are kept
 
 template <int R, bool F32>
 struct Cfg {
-    static constexpr int kWgs = R == 64 ? 4 : 2;                        // softmax warpgroups, each with all positions and R / kWgs rows
+    static constexpr int kWgs = R > 32 ? R / 16 : 2;                        // softmax warpgroups, each with all positions and R / kWgs rows
     static constexpr int kH = R / kWgs;                                // rows per softmax thread
     static constexpr int kSoftmax = 128 * kWgs, kThreads = 128 + kSoftmax;
     static constexpr int kQ = F32 ? 6 : 2, kP = F32 ? 6 : 3;            // codes per query value and per weight
-    static constexpr int kK = R == 64 || F32 ? 2 : 3, kV = F32 && R == 32 ? 2 : 3;   // tiles in shared memory; V waits for the softmax
+    static constexpr int kK = R > 32 || F32 ? 2 : 3, kV = F32 && R == 32 ? 2 : 3;   // tiles in shared memory; V waits for the softmax
     static constexpr uint32_t kS = kQ * R, kO = 2 * kS;                // TMEM columns: two S buffers, then O halves of R
     static constexpr uint32_t kUsed = kO + 2 * R, kTmem = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
     static_assert(kUsed <= 512 && kS <= 256, "TMEM and the MMA's N");
@@ -245,7 +245,7 @@ __device__ void prepare_q(const Bs8Args& a, Smem<R, F32>& sm, const Bs8Share& w,
     constexpr int kWarps = C::kSoftmax / 32, kEach = R / kWarps, kVecs = F32 ? 2 : 1;
     const int lane = threadIdx.x & 31, heads = a.num_kv_heads;
     const int T0 = w.chunk(heads) * (a.rows / kGroup), nrows = min(R, kGroup * (w.s.T - T0));
-    const T* q = static_cast<const T*>(a.q) + (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim + 8 * lane;
+    const T* q = static_cast<const T*>(a.q) + (((int64_t)w.s.q0 + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim + 8 * lane;
     auto load = [&](int n, uint4 (&to)[kVecs]) {       // padding rows load the last row
         const int r = min(warp + n * kWarps, nrows - 1);
 #pragma unroll
@@ -556,9 +556,8 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                 const uint32_t st = it % C::kV;
                 ok = ok && mbar_wait_fast(&sm.v_full[st], (it / C::kV) & 1, &sm.abort);      // PV(it - 1) has seen the phase before
                 if (p >= valid) {
-#pragma unroll
-                    for (int c = 0; c < 16 / C::kWgs; ++c)
-                        *reinterpret_cast<uint4*>(sm.v[st] + ((p >> 3) * 16 + wg * (16 / C::kWgs) + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int c = wg; c < kHeadDim / 16; c += C::kWgs)
+                        *reinterpret_cast<uint4*>(sm.v[st] + ((p >> 3) * 16 + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
             }
             fence_proxy_async();
@@ -582,7 +581,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
         const bool whole = w.whole();
         float* part = a.partials + ((size_t)blockIdx.x * 2 + w.part()) * kBs8PartFloats;
         using T = std::conditional_t<F32, float, __nv_bfloat16>;
-        T* out = static_cast<T*>(a.out) + (((int64_t)a.q_offsets[w.slot] + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim;
+        T* out = static_cast<T*>(a.out) + (((int64_t)w.s.q0 + T0) * heads * kGroup + w.head(heads) * kGroup) * kHeadDim;
         if (p < H) {                       // one thread per row; then all read their rows' factors
             const float mine = (sm.red[wg][0][p] + sm.red[wg][1][p]) + (sm.red[wg][2][p] + sm.red[wg][3][p]);
             if (!whole && r0 + p < nrows)
@@ -713,7 +712,8 @@ int bs8_mma_rows(int dtype) { return dtype == Q3KV_F32 ? 32 : kBs8Rows; }
 cudaError_t launch_bs8_mma(const Bs8Args& a, cudaStream_t st) {
     const int rows = kGroup * a.max_n_q;
     if (a.dtype == Q3KV_F32) return rows <= 16 ? launch_r<16, true>(a, st) : launch_r<32, true>(a, st);
-    return rows <= 16 ? launch_r<16, false>(a, st) : rows <= 32 ? launch_r<32, false>(a, st) : launch_r<64, false>(a, st);
+    if (rows <= 32) return rows <= 16 ? launch_r<16, false>(a, st) : launch_r<32, false>(a, st);
+    return rows <= 48 ? launch_r<48, false>(a, st) : launch_r<64, false>(a, st);
 }
 
 }  // namespace q3kv
