@@ -612,7 +612,7 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     a.ctas = ctas;
     a.partials = static_cast<float*>(d_workspace);
     const bool mma = impl != Q3KV_IMPL_FMA;
-    a.rows = mma ? bs8_mma_rows(dtype) : kBs8Rows;
+    a.rows = mma ? bs8_mma_rows(dtype, max_n_q) : kBs8Rows;
     const double most = (double)num_slots * ((max_ctx_len + kBs8Tile - 1) / kBs8Tile) * desc->num_kv_heads *
                         ((kGroup * max_n_q + a.rows - 1) / a.rows) * ctas;
     a.narrow = most < 4.0e9;

@@ -42,7 +42,7 @@ struct Bs8Args {
 
 cudaError_t launch_bs8_fma(const Bs8Args& a, cudaStream_t stream);
 cudaError_t launch_bs8_mma(const Bs8Args& a, cudaStream_t stream);
-int bs8_mma_rows(int dtype);                 // the tensor-core leg's chunk
+int bs8_mma_rows(int dtype, int max_n_q);                 // the tensor-core leg's chunk
 
 // Lengths of one slot; tiles and chunks are 0 for a slot with nothing to do or with lengths the call does not allow.
 struct Bs8Slot {

@@ -707,13 +707,17 @@ cudaError_t launch_r(const Bs8Args& a, cudaStream_t st) {
 
 }  // namespace
 
-int bs8_mma_rows(int dtype) { return dtype == Q3KV_F32 ? 32 : kBs8Rows; }
+// More than 64 rows are two chunks alike, so that 9 to 12 tokens take 48 rows each instead of 64 and a rest.
+int bs8_mma_rows(int dtype, int max_n_q) {
+    if (dtype == Q3KV_F32) return 32;
+    return kGroup * max_n_q > kBs8Rows && kGroup * max_n_q <= 96 ? 48 : kBs8Rows;
+}
 
 cudaError_t launch_bs8_mma(const Bs8Args& a, cudaStream_t st) {
     const int rows = kGroup * a.max_n_q;
     if (a.dtype == Q3KV_F32) return rows <= 16 ? launch_r<16, true>(a, st) : launch_r<32, true>(a, st);
     if (rows <= 32) return rows <= 16 ? launch_r<16, false>(a, st) : launch_r<32, false>(a, st);
-    return rows <= 48 ? launch_r<48, false>(a, st) : launch_r<64, false>(a, st);
+    return rows <= 48 || a.rows == 48 ? launch_r<48, false>(a, st) : launch_r<64, false>(a, st);
 }
 
 }  // namespace q3kv
