@@ -936,10 +936,10 @@ def process_logits(logits: torch.Tensor, out: torch.Tensor, q_offsets: torch.Ten
         raise ValueError("n_q must be one-dimensional")
     rows, vocab = shape
     n, i32, f32 = n_q.numel(), torch.int32, torch.float32
-    p = _pointers(_current_device(), ("logits", logits, None, 0), ("out", out, logits.dtype, 0), ("q_offsets", q_offsets, i32, n),
+    dev = _current_device()
+    p = _pointers(dev, ("logits", logits, None, 0), ("out", out, logits.dtype, 0), ("q_offsets", q_offsets, i32, n),
                   ("n_q", n_q, i32, 0), ("tokens", tokens, i32, rows), ("counts", counts, torch.int16, 0),
                   ("repetition", repetition, f32, n), ("frequency", frequency, f32, n), ("presence", presence, f32, n),
-                  ("bias_offsets", bias_offsets, i32, n + 1), ("bias_tokens", bias_tokens, i32, 0), ("bias_values", bias_values, f32, 0),
                   ("mask", mask, i32, 0), ("status", status, i32, 1))
     if out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
@@ -948,15 +948,16 @@ def process_logits(logits: torch.Tensor, out: torch.Tensor, q_offsets: torch.Ten
         if counts.dim() != 2 or counts.shape[0] < n or counts.shape[1] < vocab:
             raise ValueError(f"counts must be [slots >= {n}, entries >= {vocab}], got {tuple(counts.shape)}")
         stride = counts.shape[1]
-    biases = 0
+    biases, b = 0, (None, None, None)
     if bias_offsets is not None:
         if bias_tokens is None or bias_values is None:
             _required(bias_tokens=bias_tokens, bias_values=bias_values)
+        b = _pointers(dev, ("bias_offsets", bias_offsets, i32, n + 1), ("bias_tokens", bias_tokens, i32, 0), ("bias_values", bias_values, f32, 0))
         biases = bias_tokens.numel()
         if bias_values.numel() != biases:
             raise ValueError(f"bias_tokens and bias_values differ in length: {biases} and {bias_values.numel()}")
-    if mask is not None and tuple(mask.shape) != (rows, (vocab + 31) // 32):
+    if mask is not None and mask.shape != (rows, (vocab + 31) // 32):
         raise ValueError(f"mask must be {(rows, (vocab + 31) // 32)}, got {tuple(mask.shape)}")
     rc = _lib.load().q3kv_process_logits(_stream(stream), p[0], p[1], _dtype_code(logits), vocab, p[2], p[3], p[4], n, rows, max_n_q, p[5],
-                                         stride, p[6], p[7], p[8], p[9], p[10], p[11], biases, p[12], p[13])
+                                         stride, p[6], p[7], p[8], b[0], b[1], b[2], biases, p[9], p[10])
     check(rc, "q3kv_process_logits")

@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <algorithm>
+
 #include "q3kv_internal.h"
 
 namespace q3kv {
@@ -57,13 +59,16 @@ struct alignas(16) Row8 {
     T x[kPer];
 };
 
-// A CTA takes 2,048 entries of up to kBatch rows of one slot.  Bound: bytes (logits in and out), which asks for many in
-// flight: the rows come by asynchronous 16-byte copies into shared memory (an SM has up to 160 KiB under way, where rows
-// held in registers allowed 48 to 96), whole vectors also where a row does not start on one.  An entry's penalty
-// alpha c + beta [c > 0] - bias is the same in all rows but where the step's own tokens count, so a row costs five
-// instructions per entry, and a warp none of whose entries is seen or biased (most are, away from the frequent tokens)
-// only applies the mask.  Small calls are bound by the chain lengths -> rows and tokens -> biases.
-constexpr int kBatch = 4;
+// A CTA takes 2,048 entries of a slot's rows, or of a part of them where the CTAs would be few, one row after the other.
+// Bound: bytes (logits in and out) and, close behind, issue slots.  So the rows come by asynchronous 16-byte copies into a
+// ring of two groups of rows, whole vectors also where a row does not start on one, and no registers hold them; an entry's penalty
+// alpha c + beta [c > 0] - bias is worked out once for all rows but where the step's own tokens count; and a warp
+// looks only at those of its eight steps in which some lane's entry changes (most entries are not seen, away from the
+// frequent tokens): the others only take the mask.
+template <typename T>
+constexpr int kGroupRows = 8 / (int)sizeof(T);      // copied together, while the group before is worked on
+template <typename T>
+constexpr int kRing = 2 * kGroupRows<T>;
 template <typename T>
 constexpr int kRowBytes = kChunk * (int)sizeof(T) + 16;
 
@@ -106,13 +111,13 @@ __device__ __forceinline__ bool same_bits(const Row8<T>& a, const Row8<T>& b) {
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logits_kernel(LogitArgs a) {
-    extern __shared__ __align__(16) uint8_t s_rows[];       // [kBatch][kRowBytes]
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logits_kernel(LogitArgs a, int per) {
+    extern __shared__ __align__(16) uint8_t s_rows[];       // [kRing][kRowBytes]
     __shared__ float s_bias[kChunk];
     __shared__ int s_tok[kMaxNq];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, slot = blockIdx.y, j0 = blockIdx.z * kBatch;
+    const int tid = threadIdx.x, lane = tid & 31, slot = blockIdx.y;
     const int base = blockIdx.x * kChunk;
     const int w = a.n_q[slot], r0 = a.q_offsets[slot];
     int b0 = 0, b1 = 0;
@@ -144,46 +149,47 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
         if (report && tid == 0) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
         return;
     }
-    if (j0 >= w) return;
-    const int rows = min(kBatch, w - j0);
+    const int j0 = blockIdx.z * per, j1 = min(w, j0 + per);      // rows of this CTA
+    if (j0 >= j1) return;
     const int64_t begin = ((int64_t)(r0 + j0) * a.vocab + base) * (int)sizeof(T);      // byte of the first row's first entry
     const int64_t row_bytes = (int64_t)a.vocab * (int)sizeof(T);
-    const uint8_t* in = static_cast<const uint8_t*>(a.logits) + begin;
-    uint8_t* to = s_rows + tid * 16;
     const int bytes = min(kChunk, a.vocab - base) * (int)sizeof(T);
+    const uint8_t* in = static_cast<const uint8_t*>(a.logits) + begin;      // the next row to be copied
+    int ahead = j0;
+    auto copy_group = [&]() {                                      // empty behind the last row
 #pragma unroll 1
-    for (int k = 0; k < rows; ++k, in += row_bytes, to += kRowBytes<T>) {
-        const int shift = VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(in) & 15);       // the buffer begins on 16 bytes
-        const uint8_t* from = in - shift;
-        const int left = bytes + shift;
+        for (const int end = min(j1, ahead + kGroupRows<T>); ahead < end; ++ahead) {
+            uint8_t* to = s_rows + (ahead - j0) % kRing<T> * kRowBytes<T>;
+            if (VEC) {                                             // each thread its own entries
+                constexpr int kOwn = kPer * (int)sizeof(T);
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            const int at = (tid + i * kThreads) * 16;
-            if (at < left) copy16(to + i * kThreads * 16, from + at, min(16, left - at));
+                for (int i = 0; i < kOwn; i += 16)
+                    if (first < a.vocab) copy16(to + tid * kOwn + i, in + tid * kOwn + i, 16);
+            } else {
+                const int shift = (int)(reinterpret_cast<uintptr_t>(in) & 15);       // the buffer begins on 16 bytes
+                for (int at = tid * 16; at < bytes + shift; at += kThreads * 16) copy16(to + at, in - shift + at, min(16, bytes + shift - at));
+            }
+            in += row_bytes;
         }
-        if (!VEC && tid == 0 && left > kChunk * (int)sizeof(T))
-            copy16(s_rows + k * kRowBytes<T> + kChunk * sizeof(T), from + kChunk * sizeof(T), left - kChunk * (int)sizeof(T));
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    copy_group();
+    // masks: this thread's byte, or, as a warp's entries of one step share a word where rows are not aligned, step `lane`'s word
     const int64_t mask_bytes = (a.vocab + 31) / 32 * 4;
-    uint32_t allowed[kBatch];
-    {
-        const uint8_t* m = reinterpret_cast<const uint8_t*>(a.mask) + (r0 + j0) * mask_bytes;
-        // a warp's entries of one step share a word where rows are not aligned: lane e holds step e's
-        const int word = (first - lane + lane * kStep) >> 5;
-        const bool own = a.mask && (VEC ? first < a.vocab : lane < kPer && word * 4 < mask_bytes);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k, m += mask_bytes) {
-            allowed[k] = VEC ? 0xffu : 0u;
-            if (own && k < rows) allowed[k] = VEC ? m[first >> 3] : reinterpret_cast<const uint32_t*>(m)[word];
-        }
-    }
+    const int word = (first - lane + lane * kStep) >> 5;
+    const bool own = a.mask && (VEC ? first < a.vocab : lane < kPer && word * 4 < mask_bytes);
+    const uint8_t* mask = reinterpret_cast<const uint8_t*>(a.mask) + (r0 + j0) * mask_bytes;
+    auto load_mask = [&](int j) -> uint32_t {
+        if (!own || j >= j1) return VEC ? 0xffu : 0u;
+        return VEC ? mask[first >> 3] : reinterpret_cast<const uint32_t*>(mask)[word];
+    };
+    uint32_t allowed = load_mask(j0);
     bool near = false;                   // a token of the step is in the chunk
     if (tid < w) {
         const int t = a.tokens[r0 + tid];
         s_tok[tid] = t;
         if (report && (t < 0 || t >= a.vocab)) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
-        near = t >= base && t < min(base + kChunk, a.vocab) && tid < j0 + kBatch;
+        near = t >= base && t < min(base + kChunk, a.vocab) && tid < j1;
     }
     if (b0 < 0 || b1 < b0 || b1 > a.num_biases) {
         if (report && tid == 0) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
@@ -206,7 +212,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
         }
         biased = __syncthreads_or(biased);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     near = __syncthreads_or(near);
 
     // what this thread's entries lose in every row, and where the step's tokens add to it
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
         for (int e = 0; e < kPer; ++e) marks |= (s_bias[first - base + e * kStep] != 0.0f ? 1u : 0u) << e;
     uint32_t step[kPer / 2] = {0, 0, 0, 0};                 // 16 bits per entry, bit i set where t_i is the entry
     if (near)
-        for (int i = 0; i < min(w, j0 + kBatch); ++i) {
+        for (int i = 0; i < j1; ++i) {
             const int d = s_tok[i] - first;
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
@@ -243,10 +248,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
         }
     }
     const bool in_place = a.logits == a.out;
-    const uint8_t* row = s_rows;
+    const int valid = (a.vocab - first + kStep - 1) / kStep;      // this thread's entries that exist (not VEC)
     uint8_t* out = static_cast<uint8_t*>(a.out) + begin;
 #pragma unroll 1
-    for (int k = 0; k < rows; ++k, row += kRowBytes<T>, out += row_bytes) {
+    for (int j = j0; j < j1; ++j, out += row_bytes) {
+        if ((j - j0) % kGroupRows<T> == 0) {
+            if (!VEC) __syncthreads();   // all are done with the group before, whose place the next one takes
+            copy_group();
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            if (!VEC) __syncthreads();   // others' copies have landed too
+        }
+        mask += mask_bytes;
+        const uint32_t next = load_mask(j + 1);
+        const uint8_t* row = s_rows + (j - j0) % kRing<T> * kRowBytes<T>;
         Row8<T> x, o;
         if (VEC) {
             x = reinterpret_cast<const Row8<T>*>(row)[tid];
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
                 float y = to_f32(x.x[e]), s = less[e];
                 bool known = (seen >> e) & 1u;
                 if (near) {
-                    const int more = __popc(step[e / 2] & (((2u << (j0 + k)) - 1u) << (16 * (e & 1))));
+                    const int more = __popc(step[e / 2] & (((2u << j) - 1u) << (16 * (e & 1))));
                     if (more) {
                         s += (count.x[e] & 0x7fff) > 0 ? alpha * (float)more : fmaf(alpha, (float)more, beta);
                         known = true;
@@ -274,23 +288,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
             }
         }
         if (a.mask) {
-            uint32_t mine = allowed[0];
-            if (!VEC) {
-                mine = 0;
+            if (VEC) {
+                apply_mask(o, allowed);
+            } else {
+                const uint32_t bit = 1u << lane;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) mine |= ((__shfl_sync(0xffffffffu, allowed[0], e) >> lane) & 1u) << e;
+                for (int e = 0; e < kPer; ++e)
+                    if (!(__shfl_sync(0xffffffffu, allowed, e) & bit)) o.x[e] = from_f32<T>(-CUDART_INF_F);
             }
-            apply_mask(o, mine);
-#pragma unroll
-            for (int i = 0; i + 1 < kBatch; ++i) allowed[i] = allowed[i + 1];
         }
+        allowed = next;
         if (VEC) {
             if (first < a.vocab && (!in_place || !same_bits(o, x))) reinterpret_cast<Row8<T>*>(out)[tid] = o;
         } else {
             T* p = reinterpret_cast<T*>(out) + tid;
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
-                if (first + e * kStep < a.vocab) p[e * kStep] = o.x[e];
+                if (e < valid) p[e * kStep] = o.x[e];
         }
     }
 }
@@ -416,8 +430,8 @@ __global__ void __launch_bounds__(kHistoryThreads) count_history_kernel(CountArg
         if (add[k].x | add[k].y) words[k * kHistoryThreads + threadIdx.x] = add_to(add_to(was[k], 0, add[k].x), 16, add[k].y);
 }
 
-template <typename K, typename A>
-cudaError_t launch(K kernel, const A& a, dim3 grid, size_t smem, cudaStream_t st, int threads = kThreads) {
+template <typename K, typename A, typename... More>
+cudaError_t launch(K kernel, const A& a, dim3 grid, size_t smem, cudaStream_t st, int threads = kThreads, More... more) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -428,7 +442,7 @@ cudaError_t launch(K kernel, const A& a, dim3 grid, size_t smem, cudaStream_t st
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, more...);
 }
 
 }  // namespace
@@ -506,15 +520,22 @@ int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dty
     a.num_biases = num_biases;
     a.mask = d_mask;
     a.status = d_status;
-    const dim3 grid((unsigned)(((int64_t)vocab + kChunk - 1) / kChunk), (unsigned)num_slots, (unsigned)((max_n_q + kBatch - 1) / kBatch));
+    int sms = 0;
+    const int e = device_sm_count(&sms);
+    if (e != Q3KV_OK) return e;
+    // a slot's rows go to one CTA per chunk where that gives every SM eight CTAs, else to several (8 slots x 16 float32:
+    // 18.7 us with four per SM, 19.8 with eight, 21.0 with twelve; 1 x 6: 4.8, 4.2, 4.3)
+    const int64_t chunks = ((int64_t)vocab + kChunk - 1) / kChunk, few = chunks * num_slots;
+    const int parts = (int)std::min<int64_t>(max_n_q, std::max<int64_t>(1, (8 * (int64_t)sms + few / 2) / few)), per = (max_n_q + parts - 1) / parts;
+    const dim3 grid((unsigned)chunks, (unsigned)num_slots, (unsigned)((max_n_q + per - 1) / per));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     // rows start on 16 bytes and end with a whole group of 8 entries
     const bool vec = vocab % 8 == 0;
     if (dtype == Q3KV_F32)
         return cuda_status(launch(vec ? process_logits_kernel<float, true> : process_logits_kernel<float, false>, a, grid,
-                                  kBatch * kRowBytes<float>, st));
+                                  kRing<float> * kRowBytes<float>, st, kThreads, per));
     return cuda_status(launch(vec ? process_logits_kernel<__nv_bfloat16, true> : process_logits_kernel<__nv_bfloat16, false>, a, grid,
-                              kBatch * kRowBytes<__nv_bfloat16>, st));
+                              kRing<__nv_bfloat16> * kRowBytes<__nv_bfloat16>, st, kThreads, per));
 }
 
 }  // extern "C"
