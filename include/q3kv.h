@@ -706,7 +706,9 @@ Q3KV_API int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, 
  *   ((r/8)*16 + d/16)*128 + (r%8)*16 + d%16,
  * and the 16 blocks' scales are float32 at byte 65536 + 4*(r/16).  16-byte aligned.
  * Arguments, status bits and errors of q3kv_bs8_append are those of q3kv_append
- * (SCALE_OVERFLOW: a finite value above 448 2^64, which saturates). */
+ * (SCALE_OVERFLOW: a finite value above 448 2^64, which saturates; BAD_LENGTH: also a negative row
+ * offset).  A NaN in K is a NaN code; one in V is a zero there and a NaN code in K at the same position
+ * and dim, so that queries that see the position come out as NaN and no others do. */
 Q3KV_API int q3kv_bs8_pool_bytes(const q3kv_cache_desc* desc, size_t* bytes);
 Q3KV_API int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_pool,
                      const int32_t* d_page_table, int32_t max_pages_per_slot,
@@ -768,7 +770,7 @@ Q3KV_API int q3kv_bs8_copy_pages(void* stream, const q3kv_cache_desc* desc, cons
  * d_counts int16 [num_slots, counts_stride], one word per vocabulary entry and slot: bits 0..14
  * how often the token was generated (stays at 32767), bit 15 set if the prompt holds it.  A new
  * slot's words are zeroed by the caller.  counts_stride: entries per slot, a multiple of 8, at
- * least vocab; d_counts 16-byte aligned.
+ * least vocab (at most 2^28); d_counts 16-byte aligned.
  *
  * q3kv_count_tokens adds slot b's tokens d_tokens[d_offsets[b] .. + d_n[b]) (prompt = 0: one per
  * occurrence; 1: marks them as the prompt's).  d_tokens holds num_tokens; max_n bounds d_n[b].

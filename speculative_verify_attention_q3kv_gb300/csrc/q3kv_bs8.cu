@@ -6,6 +6,9 @@
 // for codes that fall under E4M3's smallest normal value: so a block can grow by appends.  When the rows appended
 // to a block that holds earlier rows need a larger e, the earlier codes are rewritten for it; e never falls within a
 // block (a rejected draft may leave it larger than the rows that stay need).
+//
+// A NaN in V would reach rows that do not see its position (0 x NaN is NaN in the product with the weights), one in K
+// only rows that do.  So a V NaN is stored as a zero there and a NaN in K's code of the same position and dim.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -35,6 +38,22 @@ struct Raw16 {
     __device__ __forceinline__ float at(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    // NaNs become zeros here and NaNs in k
+    __device__ __forceinline__ void nan_to(Raw16& k) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = at(i);
+            if (v == v) continue;
+            if constexpr (sizeof(T) == 4) {
+                k.w[i] = 0x7fc00000u;
+                w[i] = 0u;
+            } else {
+                const uint32_t half = (i & 1) ? 0xffff0000u : 0x0000ffffu;
+                k.w[i >> 1] = (k.w[i >> 1] & ~half) | (0x7fc07fc0u & half);
+                w[i >> 1] &= ~half;
+            }
+        }
     }
     // largest finite magnitude, as float32 bits (which are in the magnitudes' order)
     __device__ __forceinline__ uint32_t top(bool* finite) const {
@@ -102,7 +121,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 6 : 4) append
     const int n_new = a.n_new[slot], len = a.slot_len[slot], first_row = a.row_offsets[slot];
     if (n_new == 0) return;
     const bool report = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && a.status;
-    if (n_new < 0 || n_new > a.max_n_new || len < 0) {
+    if (n_new < 0 || n_new > a.max_n_new || len < 0 || first_row < 0) {
         if (report) atomicOr(a.status, Q3KV_STATUS_BAD_LENGTH);
         return;
     }
@@ -145,6 +164,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 6 : 4) append
         const uint32_t top = __reduce_max_sync(0xffffffffu, fresh ? x[kv].top(&finite) : 0u);
         if (lane == 0) s_max[kv][warp] = top;
     }
+    if (!finite) x[1].nan_to(x[0]);
     if (!__all_sync(0xffffffffu, finite) && lane == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_NONFINITE_INPUT);
     __syncthreads();
 #pragma unroll

@@ -19,6 +19,7 @@
 namespace q3kv {
 namespace {
 
+constexpr int kMaxVocab = 1 << 28;            // entries' indexes, and those of the vectors behind the last, fit 32 bits
 constexpr int kThreads = 256;
 constexpr int kPer = 8;                       // entries per thread
 constexpr int kChunk = kThreads * kPer;       // vocabulary entries per CTA
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(kThreads) count_kernel(CountArgs a) {
     int64_t begin;
     int n;
     if (!slot_range(a, slot, &begin, &n)) return;
-    const int i = blockIdx.x * kThreads + threadIdx.x;
-    if ((int)(blockIdx.x * kThreads + (threadIdx.x & ~31)) >= n) return;      // whole warps leave
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i - (threadIdx.x & 31) >= n) return;      // whole warps leave
     int t = i < n ? a.tokens[begin + i] : -1;
     if (i < n && (t < 0 || t >= a.vocab)) {
         if (a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
@@ -456,7 +457,7 @@ int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_stride, in
     using namespace q3kv;
     if (vocab <= 0 || num_tokens < 0 || num_slots < 0 || max_n < 0 || (prompt != 0 && prompt != 1)) return Q3KV_ERR_INVALID_ARG;
     if (counts_stride < vocab || counts_stride % 8 != 0) return Q3KV_ERR_INVALID_ARG;
-    if (num_slots > 65535) return Q3KV_ERR_UNSUPPORTED;
+    if (num_slots > 65535 || vocab > kMaxVocab) return Q3KV_ERR_UNSUPPORTED;
     if (num_slots == 0 || max_n == 0 || num_tokens == 0) return Q3KV_OK;
     if (!d_counts || !d_tokens || !d_offsets || !d_n || !aligned16(d_counts)) return Q3KV_ERR_INVALID_ARG;
     const int64_t bytes = (int64_t)num_slots * counts_stride * 2;
@@ -485,7 +486,7 @@ int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dty
     using namespace q3kv;
     if (dtype != Q3KV_F32 && dtype != Q3KV_BF16) return Q3KV_ERR_INVALID_ARG;
     if (vocab <= 0 || num_slots < 0 || num_rows < 0 || max_n_q < 0 || num_biases < 0) return Q3KV_ERR_INVALID_ARG;
-    if (max_n_q > kMaxNq || num_slots > 65535) return Q3KV_ERR_UNSUPPORTED;
+    if (max_n_q > kMaxNq || num_slots > 65535 || vocab > kMaxVocab) return Q3KV_ERR_UNSUPPORTED;
     if (d_counts && (counts_stride < vocab || counts_stride % 8 != 0)) return Q3KV_ERR_INVALID_ARG;
     if (num_slots == 0 || num_rows == 0 || max_n_q == 0) return Q3KV_OK;
     if (!logits || !out || !d_q_offsets || !d_n_q || !d_tokens) return Q3KV_ERR_INVALID_ARG;

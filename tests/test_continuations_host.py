@@ -215,7 +215,7 @@ def test_count_tokens_refusals(lib):
                dict(n_tok=-1), dict(off=None), dict(n=None), dict(slots=-1), dict(most=-1), dict(prompt=2), dict(prompt=-1),
                dict(tokens=(1 << 30) + 400), dict(tokens=(1 << 30) - 196), dict(off=1 << 30), dict(n=(1 << 30) + 412), dict(status=1 << 30)):
         assert call(**kw) == INVALID, kw
-    assert call(slots=65536) == UNSUPPORTED
+    assert call(slots=65536) == UNSUPPORTED and call(vocab=(1 << 28) + 1, stride=(1 << 28) + 8) == UNSUPPORTED
 
 
 def test_process_logits_refusals(lib):
@@ -235,7 +235,7 @@ def test_process_logits_refusals(lib):
                dict(tok=inside), dict(counts=inside), dict(rep=inside), dict(fre=inside), dict(pre=inside), dict(boff=inside), dict(btok=inside),
                dict(bval=inside), dict(mask=inside), dict(status=inside)):
         assert call(**kw) == INVALID, kw
-    for kw in (dict(max_nq=17), dict(slots=65536)):
+    for kw in (dict(max_nq=17), dict(slots=65536), dict(vocab=(1 << 28) + 1, counts=None)):
         assert call(**kw) == UNSUPPORTED, kw
 
 

@@ -121,6 +121,29 @@ def test_values_that_are_not_finite_and_scales_that_overflow():
         assert int(cache.status) == bits, bad
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_nan_in_v_reaches_those_who_see_it_and_no_others(dtype):
+    L, T = [300], [6]
+    cache = Bs8Cache(L, kv=1)
+    rng = np.random.default_rng(40)
+    k, v = (rng.standard_normal((300, 1, 256)).astype(np.float32) for _ in range(2))
+    q = queries(6, 1, 41, dtype)
+    cache.append([0], [k], [v], dtype=dtype)
+    clean = {impl: cache.verify(L, T, q, impl=impl) for impl in (FMA, MMA)}
+    for d, bad in ((7, np.nan), (8, np.nan), (200, -np.nan)):
+        v2 = v.copy()
+        v2[297, 0, d], v2[298, 0, 0] = bad, np.inf       # the fourth draft's; an infinity saturates
+        cache.append([0], [k], [v2], dtype=dtype)
+        codes_k, _ = cache.raw(0, 300, 0, 0, 0)
+        codes_v, _ = cache.raw(0, 300, 0, 0, 1)
+        assert np.array_equal(np.argwhere((codes_k & 0x7F) == 0x7F), [[297, d]]) and codes_v[297, d] & 0x7F == 0 and codes_v[298, 0] == 0x7E
+        assert not np.any((codes_v & 0x7F) == 0x7F)
+        for impl in (FMA, MMA):
+            out = cache.verify(L, T, q, impl=impl)
+            assert torch.equal(out[:3], clean[impl][:3]) and bool(torch.isnan(out[3:]).all())
+    assert int(cache.status) == 1
+
+
 def test_append_status_words():
     x = np.zeros((1, 5, 1, 256), np.float32)
 
@@ -139,6 +162,10 @@ def test_append_status_words():
     assert run(-1, 5) == (8, False) and run(0, 5, most=4) == (8, False)
     assert run(250, 10) == (8, True)                  # what fits the table is stored
     assert run(256, 3) == (8, False) and run(2 ** 31 - 2, 5) == (8, False)
+    cache = Bs8Cache([256], kv=1)
+    rows = torch.ones((4, 1, 256), device="cuda")
+    api.bs8_append(cache.desc, cache.pool, cache.page_table, i32([0]), i32([2]), i32([-1, 1]), 2, 0, rows, rows, cache.status)
+    assert int(cache.status) == 8 and bool((cache.pool == 0xFF).all())
 
 
 # ------------------------------------------------------------------ verify
@@ -377,6 +404,20 @@ def test_units_beyond_32_bit_offsets():
     for dtype, kind in ((torch.bfloat16, "bf16"), (torch.float32, "f32")):
         q = queries(5, 4, 31, dtype)
         check(cache.verify([600], [5], q, layer=15), q, cache, [600], [5], kind, layer=15)
+
+
+@pytest.mark.parametrize("dtype,impl", [(torch.bfloat16, 0), (torch.float32, 0), (torch.float32, FMA)])
+def test_bounds_beyond_32_bit_tile_counts(dtype, impl):
+    """The largest max_ctx_len: tiles x CTAs no longer fit 32 bits by the host's bound, the results are the same bits."""
+    rng = np.random.default_rng(42)
+    L = rng.integers(10, 900, 40).tolist()
+    T = rng.integers(0, 10, 40).tolist()
+    cache = Bs8Cache(L, kv=2)
+    cache.fill(L, seed=43)
+    q = queries(sum(T), 2, 44, dtype)
+    a = cache.verify(L, T, q, impl=impl)
+    b = cache.verify(L, T, q, impl=impl, max_ctx=2 ** 31 - 300)
+    assert torch.equal(a, b) and int(cache.status) == 0
 
 
 def test_the_longest_share():
