@@ -1,4 +1,8 @@
 """The operators of many continuations of one context, run together as a serving loop would."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -116,3 +120,53 @@ def test_forked_continuations(dtype, kind):
     for b in range(slots):
         alloc.free_slot(b)
     assert alloc.free_pages() == 24
+
+
+_FIRST_CALLS = """
+import torch
+from speculative_verify_attention_q3kv_gb300 import api
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+desc = api.make_desc(1, 2, 8)
+pool = torch.zeros(api.bs8_pool_bytes(desc), dtype=torch.uint8, device="cuda")
+table, ctx, n, off, at = i32(0, 1, 2, 3)[None], i32(900), i32(3), i32(0, 3), i32(897)
+gen = torch.Generator(device="cuda").manual_seed(0)
+k0, v0 = (torch.randn(897, 2, 256, generator=gen, device="cuda") for _ in range(2))
+k, v = (torch.randn(3, 2, 256, generator=gen, device="cuda") for _ in range(2))
+q = torch.randn(3, 16, 256, generator=gen, device="cuda")
+outs = [torch.zeros(3, 16, 256, device="cuda", dtype=d) for d in (torch.float32, torch.float32, torch.bfloat16)]
+ws = torch.zeros(api.bs8_workspace_bytes(desc, 1, 900, 3), dtype=torch.uint8, device="cuda")
+logits, done = torch.randn(3, 5001, generator=gen, device="cuda"), torch.zeros(3, 5001, device="cuda")
+counts, tok, st = torch.zeros(1, 5008, dtype=torch.int16, device="cuda"), i32(5, 6, 7), i32(0)
+history, zero, many, theta = torch.randint(0, 5001, (2000,), generator=gen, dtype=torch.int32, device="cuda"), i32(0), i32(2000), torch.full((1,), 1.5, device="cuda")
+qb = q.bfloat16()
+def step():
+    counts.zero_()
+    api.bs8_append(desc, pool, table, i32_zero, len0, off0, 897, 0, k0, v0, st)
+    api.bs8_append(desc, pool, table, at, n, off, 3, 0, k, v, st)
+    api.bs8_verify_attn(desc, pool, table, ctx, n, off, 900, 3, 0, q, outs[0], ws, status=st)
+    api.bs8_verify_attn(desc, pool, table, ctx, n, off, 900, 3, 0, q, outs[1], ws, impl=1, status=st)
+    api.bs8_verify_attn(desc, pool, table, ctx, n, off, 900, 3, 0, qb, outs[2], ws, status=st)
+    api.bs8_copy_pages(desc, pool, src, dst, status=st)
+    api.count_tokens(counts, 5001, history, zero, many, 2000, status=st)
+    api.count_tokens(counts, 5001, tok, off, n, 3, status=st)
+    api.process_logits(logits, done, off, n, tok, 3, counts=counts, repetition=theta, status=st)
+i32_zero, len0, off0, src, dst = i32(0), i32(897), i32(0, 897), i32(0, 1), i32(6, 7)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (*outs, pool, counts, done, st)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (*outs, pool, counts, done, st)))
+assert st.item() == 0 and int((counts & 0x7fff).sum()) == 2003 and float((outs[0] - outs[1]).abs().max()) < 1e-3
+print("captured")
+"""
+
+
+def test_the_first_calls_of_a_process_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], capture_output=True, text=True, timeout=240, cwd=root)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

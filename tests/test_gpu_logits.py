@@ -31,7 +31,7 @@ def _stride(vocab):
 # ------------------------------------------------------------------ counts
 @pytest.mark.parametrize("prompt", [False, True])
 @pytest.mark.parametrize("n,vocab", [([0, 1, 5, 16], 1000), ([64, 63, 0, 7], 40), ([65, 3, 0, 1, 300], 2000), ([5000, 1, 70], 50021),
-                                     ([20000], 16385), ([1], 1), ([100], 1)])
+                                     ([20000], 16385), ([1], 1), ([100], 1), ([200000], 3001), ([70001, 30000], 20011)])
 def test_counts(n, vocab, prompt):
     rng = np.random.default_rng(len(n))
     slots = len(n)
