@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) 
 // partials of a row together with their maxima, ten at a time, and groups that share a row agree on M at the end.
 // Bound: latency.  Few rows (one slot): eight groups per row and one row per CTA, so that 80 partials of a row are under
 // way at once; many rows, which then have few partials each: a group per row, four rows per CTA, so that few CTAs come and
-// go (1,280 rows of 5 slots: 19 us with a CTA each, 5 so; 128 rows of 76 partials: 6 us with a CTA each).
+// go (1,280 rows of 5 slots: 19 us with a CTA each, 7 so; 128 rows of 76 partials: 6 us with a CTA each).
 constexpr int kMergeBatch = 10;
 
 template <int GROUPS, int ROWS>          // groups per row, rows per CTA

@@ -10,14 +10,16 @@
 //                            many small weights stay above it next to a large one
 // Contractions (M = 128, float32 accumulation in TMEM):
 //   S^T[p][r | R + r] = K[p][:] . q1[r][:] | q2[r][:]   A = K codes (K-major), N = 2 R columns, K = 256 dims
-//   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions
+//   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions,
+//                                                        two or three codes side by side in the columns, summed at the end
 // with R = 16, 32, 48 or 64 query rows (8 heads x tokens, padded).  A position is a TMEM lane, so its block's scales are two
 // numbers of one thread: the score is (S1 + S2) 2^(eK - k) log2(e) / 16, and V's scale goes into the weight's
 // exponent, p' = 2^(score + eV - m), while the row sum takes p' 2^-eV.  m is raised only when a score passes it by more
 // than 2^7 of headroom (a vote per tile), so most tiles need no maximum and no rescaling.
 //
-// Bound: the codes' bytes.  At 8 tokens a tile's 64 KiB take about 2,900 cycles of an SM's share of HBM, its 32 MMAs about
-// 1,700 and its softmax less.  One CTA per SM; warp 0 copies, warps 1-3 issue the MMAs, the others are the softmax: groups of
+// Bound: the codes' bytes.  At 8 tokens a tile's 64 KiB take about 2,900 cycles of an SM's share of HBM (655,360 positions
+// of 2 heads: 111 us, 6,070 GB/s; 1 token 103 us, 6,500 GB/s); its 24 MMAs and its softmax, which overlap, less.  9 to 16
+// tokens are two chunks of rows and take twice that (165 and 208 us).  One CTA per SM; warp 0 copies, warps 1-3 issue the MMAs, the others are the softmax: groups of
 // four warps with a thread per position and 8 or 16 rows.
 #include <math_constants.h>
 
@@ -37,13 +39,22 @@ constexpr int kMeta = 8;                       // tiles whose scales are kept
 
 template <int R, bool F32>
 struct Cfg {
-    static constexpr int kWgs = R > 32 ? R / 16 : 2;                        // softmax warpgroups, each with all positions and R / kWgs rows
-    static constexpr int kH = R / kWgs;                                // rows per softmax thread
+    // Rows per softmax thread; a warpgroup has all positions.  More warps hide more of each other's latency (32,768 positions,
+    // 16 -> 8 rows: 4 tokens 16.2 -> 15.1 us, 6 tokens 17.2 -> 16.6); 8 rows of 64 would be more threads than a CTA has,
+    // and 4 rows of 16 gain nothing (14.0, 14.3).
+    static constexpr int kH = R > 48 ? 16 : 8, kWgs = R / kH;
     static constexpr int kSoftmax = 128 * kWgs, kThreads = 128 + kSoftmax;
     static constexpr int kQ = F32 ? 6 : 2, kP = F32 ? 6 : 3;            // codes per query value and per weight
-    static constexpr int kK = R > 32 || F32 ? 2 : 3, kV = F32 && R == 32 ? 2 : 3;   // tiles in shared memory; V waits for the softmax
-    static constexpr uint32_t kS = kQ * R, kO = 2 * kS;                // TMEM columns: two S buffers, then O halves of R
-    static constexpr uint32_t kUsed = kO + 2 * R, kTmem = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
+    // Weight codes side by side in the columns of a PV MMA, as many as TMEM has room for: an MMA of few columns takes as
+    // long as one of 64 (32,768 x 1: 14.4 -> 13.9 us; float32 5 slots x 16: 26.8 -> 25.4).
+    static constexpr int kBeside = F32 ? (R == 16 ? 6 : 2) : R > 48 ? 2 : 3;
+    // Weight buffers: PV of a tile runs during the next tile's softmax (655,360 x 8: 117 -> 111 us).  Float32 waits for each
+    // tile's outputs anyway.
+    static constexpr int kPBufs = F32 ? 1 : 2;
+    // tiles in shared memory, as many as the queries and weights leave room for; V waits for the softmax
+    static constexpr int kK = R > 16 || F32 ? 2 : 3, kV = R > 48 || (F32 && R == 32) ? 2 : 3;
+    static constexpr uint32_t kS = kQ * R, kO = 2 * kS;                // TMEM columns: two S buffers, then O halves of kBeside R
+    static constexpr uint32_t kUsed = kO + 2 * kBeside * R, kTmem = kUsed > 256 ? 512 : kUsed > 128 ? 256 : 128;
     static_assert(kUsed <= 512 && kS <= 256, "TMEM and the MMA's N");
 };
 
@@ -52,7 +63,7 @@ struct Smem {
     alignas(128) uint8_t k[Cfg<R, F32>::kK][kTileBytes];
     alignas(128) uint8_t v[Cfg<R, F32>::kV][kTileBytes];
     alignas(128) uint8_t q[Cfg<R, F32>::kQ * R * kHeadDim];
-    alignas(128) uint8_t p[Cfg<R, F32>::kP][R * kBs8Tile];
+    alignas(128) uint8_t p[Cfg<R, F32>::kPBufs][Cfg<R, F32>::kP * R * kBs8Tile];
     alignas(16) float meta[kMeta][16];         // K scales of a tile's 8 blocks, then V scales
     alignas(16) float rs[R], m[R], dm[R];      // of each row: 2^-k, the maximum negated, its last change
     float red[Cfg<R, F32>::kWgs][4][Cfg<R, F32>::kH];
@@ -60,7 +71,7 @@ struct Smem {
     int bad_page[kMeta];
     uint32_t tmem;
     volatile int abort;
-    unsigned long long k_full[Cfg<R, F32>::kK], k_free[Cfg<R, F32>::kK], v_full[Cfg<R, F32>::kV], v_free[Cfg<R, F32>::kV], s_full[2], s_free[2], p_full, p_free, q_full, drained, meta_full[kMeta];
+    unsigned long long k_full[Cfg<R, F32>::kK], k_free[Cfg<R, F32>::kK], v_full[Cfg<R, F32>::kV], v_free[Cfg<R, F32>::kV], s_full[2], s_free[2], p_full[2], p_free[2], q_full, drained, meta_full[kMeta];
 };
 
 // Instruction descriptor, kind::f8f6f4: E4M3 A, E4M3 or E5M2 B, fp32 D, M = 128.
@@ -182,7 +193,7 @@ __device__ void produce(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w) {
 
 // MMAs, by one thread of each of three warps: QK, and PV into the two halves of O.  A thread needs about 100 cycles to
 // form the descriptors of an MMA and issue it, twice what the tensor pipe takes for one, so one thread would bound a tile
-// (32 MMAs).  Each waits for its own operands only: QK of later tiles runs while the softmax works on this one.
+// (24 MMAs at 8 tokens).  Each waits for its own operands only: QK of later tiles runs while the softmax works on this one.
 template <int R, bool F32>
 __device__ void issue_qk(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t tmem) {
     using C = Cfg<R, F32>;
@@ -212,25 +223,29 @@ __device__ void issue_qk(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_
 template <int R, bool F32>
 __device__ void issue_pv(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t tmem, int half) {
     using C = Cfg<R, F32>;
-    const uint64_t vdesc = make_desc(smem_u32(sm.v[0]) + half * 1024, 2048, 128), pdesc = make_desc(smem_u32(sm.p[0]), R / 16 * 128, 128);
-    const uint32_t o = tmem + C::kO + half * R;
+    const uint64_t vdesc = make_desc(smem_u32(sm.v[0]) + half * 1024, 2048, 128), pdesc = make_desc(smem_u32(sm.p[0]), C::kBeside * R / 16 * 128, 128);
+    const uint64_t pdesc1 = make_desc(smem_u32(sm.p[0]), R / 16 * 128, 128);         // of a last code alone
+    const uint32_t o = tmem + C::kO + half * C::kBeside * R;
     uint32_t it = 0;
     bool ok = true;
     do {
         for (int i = 0; i < w.tiles && ok; ++i) {
-            const uint32_t t = it + i, st = t % C::kV;
-            ok = mbar_wait(&sm.v_full[st], (t / C::kV) & 1, &sm.abort) && mbar_wait(&sm.p_full, t & 1, &sm.abort);
+            const uint32_t t = it + i, st = t % C::kV, pb = t % C::kPBufs;
+            ok = mbar_wait(&sm.v_full[st], (t / C::kV) & 1, &sm.abort) && mbar_wait(&sm.p_full[pb], (t / C::kPBufs) & 1, &sm.abort);
             if (!ok) break;
             tc_fence_after();
             const uint64_t ad = vdesc + st * (kTileBytes / 16);
 #pragma unroll
-            for (int part = 0; part < C::kP; ++part)
+            for (int part = 0; part < C::kP; part += C::kBeside) {
+                const int wide = min(C::kBeside, C::kP - part);
 #pragma unroll
                 for (int k = 0; k < kBs8Tile / 32; ++k)
-                    mma8(o, ad + k * (8192 / 16), pdesc + part * (R * kBs8Tile / 16) + k * (4 * (R / 16) * 128 / 16), idesc8(R, true, true),
-                         (!F32 && i > 0) || part > 0 || k > 0);
+                    mma8(o, ad + k * (8192 / 16),
+                         (wide == 1 ? pdesc1 : pdesc) + (pb * C::kP + part) * (R * kBs8Tile / 16) + k * (4 * (wide * R / 16) * 128 / 16),
+                         idesc8(wide * R, true, true), (!F32 && i > 0) || part > 0 || k > 0);
+            }
             mma_commit(&sm.v_free[st]);
-            mma_commit(&sm.p_free);
+            mma_commit(&sm.p_free[pb]);
         }
         it += w.tiles;
     } while (ok && w.next(a));
@@ -376,6 +391,22 @@ __device__ __forceinline__ float2 e5m2_negative(uint32_t two) {
     return __half22float2(as_h2(__byte_perm(two, 0, 0x1404) ^ 0x80008000u));
 }
 
+// A thread's rows of one half of O: the sums of the codes beside each other, smallest first.
+template <int R, bool F32>
+__device__ __forceinline__ void outputs(uint32_t lanes, int r0, int half, float* o) {
+    using C = Cfg<R, F32>;
+    float part[C::kBeside][C::kH];
+#pragma unroll
+    for (int n = 0; n < C::kBeside; ++n) tmem_load<C::kH>(lanes + C::kO + (half * C::kBeside + n) * R + r0, part[n]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < C::kH; ++c) {
+        o[c] = part[C::kBeside - 1][c];
+#pragma unroll
+        for (int n = C::kBeside - 2; n >= 0; --n) o[c] += part[n][c];
+    }
+}
+
 // Float32 outputs leave TMEM after every tile: its accumulators need not round to nearest, and a long context's many
 // additions would show that.
 template <int R, bool F32>
@@ -384,8 +415,7 @@ __device__ __forceinline__ void drain(uint32_t lanes, int r0, float* acc) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float o[C::kH];
-        tmem_load<C::kH>(lanes + C::kO + h * R + r0, o);
-        tmem_ld_wait();
+        outputs<R, F32>(lanes, r0, h, o);
 #pragma unroll
         for (int c = 0; c < C::kH; ++c) acc[h * C::kH + c] += o[c];
     }
@@ -401,6 +431,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t it = 0;
     bool ok = true;
+    const auto wait_pv = [&](uint32_t t) { return mbar_wait_fast(&sm.p_free[t % C::kPBufs], (t / C::kPBufs) & 1, &sm.abort); };
     do {
         prepare_q<R, F32>(a, sm, w, warp);
         if (tid < R) sm.m[tid] = 0.0f;
@@ -492,11 +523,11 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                     if (i > 0) l[c] = mul2(l[c], make_float2(fast_exp2(dm.x), fast_exp2(dm.y)));
                 }
                 if (!F32 && i > 0) {
-                    ok = mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);      // PV of the tile before, and all earlier ones
+                    ok = wait_pv(it - 1);      // PV of the tile before, and all earlier ones
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int g = 0; g < 2 * H; g += 8) {
+                    for (int g = 0; g < 2 * C::kBeside * H; g += 8) {
                         const uint32_t at = lanes + C::kO + (g / H) * R + r0 + g % H;
                         float o[8];
                         tmem_load<8>(at, o);
@@ -534,7 +565,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                     code[2][c] = __byte_perm(a3, b3, 0x7531);
                 }
             }
-            if (it > 0) ok = ok && mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);
+            if (it >= C::kPBufs) ok = ok && wait_pv(it - C::kPBufs);
             if constexpr (F32) {
                 __syncwarp();
                 tc_fence_after();
@@ -544,17 +575,19 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                     for (int c = 0; c < 2 * H; ++c) acc[c] *= fast_exp2(sm.dm[r0 + c % H]);
                 }
             }
-            uint8_t* to = sm.p[0] + ((p >> 3) * (R / 16) + r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
+            uint8_t* pb = sm.p[it % C::kPBufs] + (r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
 #pragma unroll
             for (int n = 0; n < C::kP; ++n) {
-                if constexpr (H == 8) *reinterpret_cast<uint2*>(to + n * R * kBs8Tile) = make_uint2(code[n][0], code[n][1]);
-                else *reinterpret_cast<uint4*>(to + n * R * kBs8Tile) = make_uint4(code[n][0], code[n][1], code[n][2], code[n][3]);
+                const int part = n / C::kBeside * C::kBeside, wide = min(C::kBeside, C::kP - part);
+                uint8_t* to = pb + part * R * kBs8Tile + (n - part) * (R / 16 * 128) + (p >> 3) * (wide * R / 16 * 128);
+                if constexpr (H == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[n][0], code[n][1]);
+                else *reinterpret_cast<uint4*>(to) = make_uint4(code[n][0], code[n][1], code[n][2], code[n][3]);
             }
             const int valid = hidden ? 0 : w.s.L - p0;
             if (valid < kBs8Tile) {
                 // rows behind the context may hold anything, and 0 x NaN is NaN: they become zeros before PV reads them
                 const uint32_t st = it % C::kV;
-                ok = ok && mbar_wait_fast(&sm.v_full[st], (it / C::kV) & 1, &sm.abort);      // PV(it - 1) has seen the phase before
+                ok = ok && mbar_wait_fast(&sm.v_full[st], (it / C::kV) & 1, &sm.abort);      // PV of the tile kV before is done
                 if (p >= valid) {
                     for (int c = wg; c < kHeadDim / 16; c += C::kWgs)
                         *reinterpret_cast<uint4*>(sm.v[st] + ((p >> 3) * 16 + c) * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -562,9 +595,9 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
             }
             fence_proxy_async();
             tc_fence_before();
-            warp_arrive(&sm.p_full);
+            warp_arrive(&sm.p_full[it % C::kPBufs]);
         }
-        ok = ok && mbar_wait_fast(&sm.p_free, (it - 1) & 1, &sm.abort);
+        ok = ok && wait_pv(it - 1);
         if (named_or(kAll, C::kSoftmax, !ok)) {      // all softmax warps leave together
             ok = false;
             break;
@@ -597,8 +630,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
 #pragma unroll
                 for (int c = 0; c < H; ++c) o[c] = acc[h * H + c];
             } else {
-                tmem_load<H>(lanes + C::kO + h * R + r0, o);
-                tmem_ld_wait();
+                outputs<R, F32>(lanes, r0, h, o);
             }
             if (whole) {
                 T* to = out + ((int64_t)(r0 >> 3) * heads * kGroup) * kHeadDim + h * 128 + p;
@@ -642,8 +674,10 @@ __global__ void __launch_bounds__(Cfg<R, F32>::kThreads, 1) verify_bs8_mma_kerne
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_free[i], C::kSoftmax / 32);
         }
-        mbar_init(&sm.p_full, C::kSoftmax / 32);
-        mbar_init(&sm.p_free, 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.p_full[i], C::kSoftmax / 32);
+            mbar_init(&sm.p_free[i], 2);
+        }
         mbar_init(&sm.q_full, C::kSoftmax / 32);
         mbar_init(&sm.drained, 3);
         for (int i = 0; i < kMeta; ++i) mbar_init(&sm.meta_full[i], 1);
