@@ -388,12 +388,15 @@ __global__ void __launch_bounds__(kThreads) count_kernel(CountArgs a) {
 
 // Long histories: frequent tokens of many threads would meet in the same words.  So a CTA owns 16,384 vocabulary entries
 // of a slot, reads all of the slot's tokens (they come from L2 for all but the first CTA), counts its own in shared
-// memory and adds each entry once: no atomics in global memory, no order.  Where slots are few, a cluster of up to eight
-// CTAs shares a range's tokens, and each adds up its part of the entries from the shared memory of all (1 x 524,288: 67 us
-// with one CTA per range, 35 with eight that add by compare-and-swap in global memory, 23 so).
-constexpr int kRange = 16384, kHistoryThreads = 1024, kAhead = 16;
+// memory and adds each entry once: no atomics in global memory, no order.  Where slots are few, a cluster of up to four
+// CTAs shares a range's tokens, and each adds up its part of the entries from the shared memory of all (1 x 524,288: 13.5 us
+// with four CTAs, 15.8 with eight, whose cluster takes 5 us more to start).
+// Bound: issue slots, one token costs each range's CTA about seven instructions (8 x 65,536 of 248,320 entries: 8.2 us, 11.7
+// with a check of the end at every token).
+constexpr int kRange = 16384, kHistoryThreads = 1024;
+constexpr unsigned kMaxParts = 4;
 
-template <bool CLUSTER>
+template <int kAhead, bool CLUSTER>      // loads under way per thread
 __global__ void __launch_bounds__(kHistoryThreads) count_history_kernel(CountArgs a) {
     extern __shared__ __align__(16) int s_count[];              // [kRange]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -404,21 +407,34 @@ __global__ void __launch_bounds__(kHistoryThreads) count_history_kernel(CountArg
     int n;
     if (!slot_range(a, slot, &begin, &n) || n == 0) return;
     __syncthreads();
-    const int32_t* tokens = a.tokens + begin;
-    const int64_t part = (n + gridDim.z - 1) / gridDim.z, last = min((int64_t)n, (blockIdx.z + 1) * part);
-    bool bad = false;
-    for (int64_t i0 = blockIdx.z * part + threadIdx.x; i0 < last; i0 += kAhead * kHistoryThreads) {
-        int t[kAhead];
+    // this CTA's part of the tokens: whole rounds of kAhead loads per thread, then single ones
+    const int64_t part = ((int64_t)n + gridDim.z - 1) / gridDim.z, first = min((int64_t)n, blockIdx.z * part);
+    const int mine = (int)min(n - first, part);
+    const int32_t* tokens = a.tokens + begin + first + threadIdx.x;
+    const uint32_t entries = min(kRange, a.vocab - base);
+    uint32_t largest = 0;                        // a negative token is a large number
+    const auto add_one = [&](uint32_t t) {
+        largest = max(largest, t);
+        const uint32_t at = t - base;
+        if (at < entries) atomicAdd(&s_count[at], 1);
+    };
+    int left = mine;
+    for (; left >= kAhead * kHistoryThreads; left -= kAhead * kHistoryThreads, tokens += kAhead * kHistoryThreads) {
+        uint32_t t[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) t[k] = i0 + k * kHistoryThreads < last ? tokens[i0 + k * kHistoryThreads] : base;
+        for (int k = 0; k < kAhead; ++k) t[k] = tokens[k * kHistoryThreads];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (i0 + k * kHistoryThreads >= last) break;
-            bad |= t[k] < 0 || t[k] >= a.vocab;
-            if (t[k] >= base && t[k] < min(base + kRange, a.vocab)) atomicAdd(&s_count[t[k] - base], 1);
-        }
+        for (int k = 0; k < kAhead; ++k) add_one(t[k]);
     }
-    if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
+    left -= threadIdx.x;
+    uint32_t t[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (k * kHistoryThreads < left) t[k] = tokens[k * kHistoryThreads];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (k * kHistoryThreads < left) add_one(t[k]);
+    if (largest >= (uint32_t)a.vocab && blockIdx.x == 0 && a.status) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
     const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();      // the CTAs along z
     if (CLUSTER) cluster.sync();
     else __syncthreads();
@@ -435,12 +451,12 @@ __global__ void __launch_bounds__(kHistoryThreads) count_history_kernel(CountArg
         if (!CLUSTER) {
             add[k] = reinterpret_cast<const int2*>(s_count)[i];
         } else if (i < share) {
-            int2 c[8];
+            int2 c[kMaxParts];
 #pragma unroll
-            for (unsigned r = 0; r < 8; ++r)
+            for (unsigned r = 0; r < kMaxParts; ++r)
                 c[r] = r < gridDim.z ? reinterpret_cast<const int2*>(cluster.map_shared_rank(s_count, r))[from + i] : make_int2(0, 0);
 #pragma unroll
-            for (unsigned r = 0; r < 8; ++r) {
+            for (unsigned r = 0; r < kMaxParts; ++r) {
                 add[k].x += c[r].x;
                 add[k].y += c[r].y;
             }
@@ -490,18 +506,14 @@ int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_stride, in
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!prompt && max_n > kFew) {
         constexpr size_t smem = kRange * sizeof(int);
-        static std::atomic<bool> allowed[2][kMaxDevices];
-        cudaError_t ce = allow_smem(reinterpret_cast<const void*>(count_history_kernel<false>), smem, allowed[0]);
-        if (ce == cudaSuccess) ce = allow_smem(reinterpret_cast<const void*>(count_history_kernel<true>), smem, allowed[1]);
-        if (ce != cudaSuccess) return cuda_status(ce);
         int sms = 0;
         const int e = device_sm_count(&sms);
         if (e != Q3KV_OK) return e;
         const int64_t ranges = ((int64_t)vocab + kRange - 1) / kRange;
-        // clusters while each CTA has an SM and 32,768 tokens at least: a cluster costs about 5 us of its own (1 x 65,536: 12 us
-        // with eight CTAs per range, 11 with one)
+        // clusters while each CTA has an SM and 16,384 tokens at least (1 x 65,536: 8.0 us with one CTA per range, 7.4 with two,
+        // 6.2 with four; 1 x 32,768: 5.9 with one, 6.2 with two)
         unsigned parts = 1;
-        while (parts < 8 && 2 * parts * ranges * num_slots <= sms && max_n / (2 * (int)parts) >= 32768) parts *= 2;
+        while (parts < kMaxParts && 2 * parts * ranges * num_slots <= sms && max_n / (2 * (int)parts) >= 16384) parts *= 2;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)ranges, (unsigned)num_slots, parts);
         cfg.blockDim = dim3(kHistoryThreads);
@@ -516,7 +528,14 @@ int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_stride, in
         attr[1].val.clusterDim.z = parts;
         cfg.attrs = attr;
         cfg.numAttrs = parts > 1 ? 2 : 1;
-        return cuda_status(cudaLaunchKernelEx(&cfg, parts > 1 ? count_history_kernel<true> : count_history_kernel<false>, a));
+        // 16 loads a thread let one CTA onto an SM, 8 two of them (8 x 65,536: 8.2 us with 16, 10.9 with 8; 32 x 4,096: 12.3 with
+        // 16, 7.7 with 8)
+        const int kind = parts > 1 ? 2 : ranges * num_slots > sms ? 1 : 0;
+        static constexpr void (*kernels[3])(CountArgs) = {count_history_kernel<16, false>, count_history_kernel<8, false>,
+                                                          count_history_kernel<16, true>};
+        static std::atomic<bool> allowed[3][kMaxDevices];
+        const cudaError_t ce = allow_smem(reinterpret_cast<const void*>(kernels[kind]), smem, allowed[kind]);
+        return cuda_status(ce != cudaSuccess ? ce : cudaLaunchKernelEx(&cfg, kernels[kind], a));
     }
     const dim3 grid((unsigned)(((int64_t)max_n + kThreads - 1) / kThreads), (unsigned)num_slots);
     return cuda_status(prompt ? launch(count_kernel<true>, a, grid, 0, st) : launch(count_kernel<false>, a, grid, 0, st));

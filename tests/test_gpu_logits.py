@@ -46,6 +46,22 @@ def test_counts(n, vocab, prompt):
     assert np.array_equal(got.cpu().numpy(), want) and int(status) == 0
 
 
+@pytest.mark.parametrize("slots", [6, 200])
+def test_counts_at_the_ends_of_rounds(slots):
+    # a CTA loads rounds of 8 or 16 times 1,024 tokens, by how many CTAs there are, then single ones; parts of 1, 2 and 4 CTAs
+    rng = np.random.default_rng(slots)
+    vocab = 16390
+    for most in (8193, 16385, 32769, 65537, 65540):
+        n = [most - rng.integers(0, 3) if b % 6 < 3 else [0, 1, most // 2][b % 3] for b in range(min(slots, 6))] + [most % 8192 + 1] * (slots - 6)
+        tokens = rng.integers(0, vocab, most).astype(np.int32)
+        counts = np.zeros((slots, _stride(vocab)), np.int16)
+        for b in range(slots):
+            counts[b, :vocab] = np.bincount(tokens[:n[b]], minlength=vocab)
+        got, status = torch.zeros(counts.shape, dtype=torch.int16, device="cuda"), i32([0])
+        api.count_tokens(got, vocab, i32(tokens), i32([0] * slots), i32(n), most, status=status)
+        assert np.array_equal(got.cpu().numpy(), counts) and int(status) == 0
+
+
 @pytest.mark.parametrize("n", [30, 3000])
 def test_counts_saturate_and_leave_their_neighbours(n):
     for start in (32767, 32766, 32767 - n + 1, 0):
