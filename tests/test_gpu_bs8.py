@@ -49,6 +49,28 @@ def test_appends_of_one_slot(steps, dtype):
     assert int(cache.status) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_on_16_bytes_only(dtype):
+    # rows are read in pieces of 32 bytes where both tensors begin on 32, of 16 elsewhere
+    n, step = 300, 16 // dtype.itemsize
+    rng = np.random.default_rng(16)
+    x = [torch.from_numpy(rng.standard_normal((n, 2, 256)).astype(np.float32)).cuda().to(dtype) for _ in range(2)]
+    pools = []
+    for shift_k, shift_v in ((0, 0), (1, 0), (0, 1), (1, 1)):
+        cache = Bs8Cache([n])
+        rows = []
+        for t, shift in zip(x, (shift_k, shift_v)):
+            room = torch.zeros(t.numel() + step, dtype=dtype, device="cuda")
+            at = room[shift * step:shift * step + t.numel()].view(n, 2, 256)
+            at.copy_(t)
+            assert at.data_ptr() % 32 == 16 * shift
+            rows.append(at)
+        api.bs8_append(cache.desc, cache.pool, cache.page_table, i32([0]), i32([n]), i32([0]), n, 0, *rows, cache.status)
+        assert int(cache.status) == 0
+        pools.append(cache.pool)
+    assert all(torch.equal(p, pools[0]) for p in pools)
+
+
 def test_ragged_appends_leave_everything_else():
     rng = np.random.default_rng(5)
     starts, n = [0, 250, 16, 511, 7], [40, 20, 0, 2, 300]
