@@ -24,6 +24,7 @@ constexpr int kMaxVocab = 1 << 28;            // entries' indexes, and those of 
 constexpr int kThreads = 256;
 constexpr int kPer = 8;                       // entries per thread
 constexpr int kChunk = kThreads * kPer;       // vocabulary entries per CTA
+constexpr int kBiasAhead = 2;
 
 struct LogitArgs {
     const void* logits;
@@ -63,14 +64,12 @@ struct alignas(16) Row8 {
 
 // A CTA takes 2,048 entries of a slot's rows, or of a part of them where the CTAs would be few, one row after the other.
 // Bound: bytes (logits in and out) and, close behind, issue slots.  So the rows come by asynchronous 16-byte copies into a
-// ring of two groups of rows, whole vectors also where a row does not start on one, and no registers hold them; an entry's penalty
+// ring of two, whole vectors also where a row does not start on one, and no registers hold them (longer rings and rows in
+// groups cost more in CTAs per SM than they hide: 8 slots x 16 float32 17.0 us, three rows 17.5, two groups of two 18.6); an entry's penalty
 // alpha c + beta [c > 0] - bias is worked out once for all rows but where the step's own tokens count; and a warp
 // looks only at those of its eight steps in which some lane's entry changes (most entries are not seen, away from the
 // frequent tokens): the others only take the mask.
-template <typename T>
-constexpr int kGroupRows = 8 / (int)sizeof(T);      // copied together, while the group before is worked on
-template <typename T>
-constexpr int kRing = 2 * kGroupRows<T>;
+constexpr int kRing = 2;                      // rows
 template <typename T>
 constexpr int kRowBytes = kChunk * (int)sizeof(T) + 16;
 
@@ -113,7 +112,7 @@ __device__ __forceinline__ bool same_bits(const Row8<T>& a, const Row8<T>& b) {
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logits_kernel(LogitArgs a, int per) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) process_logits_kernel(LogitArgs a, int per) {
     extern __shared__ __align__(16) uint8_t s_rows[];       // [kRing][kRowBytes]
     __shared__ float s_bias[kChunk];
     __shared__ int s_tok[kMaxNq];
@@ -158,10 +157,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
     const int bytes = min(kChunk, a.vocab - base) * (int)sizeof(T);
     const uint8_t* in = static_cast<const uint8_t*>(a.logits) + begin;      // the next row to be copied
     int ahead = j0;
-    auto copy_group = [&]() {                                      // empty behind the last row
-#pragma unroll 1
-        for (const int end = min(j1, ahead + kGroupRows<T>); ahead < end; ++ahead) {
-            uint8_t* to = s_rows + (ahead - j0) % kRing<T> * kRowBytes<T>;
+    auto copy_row = [&]() {                                        // empty behind the last row
+        if (ahead < j1) {
+            uint8_t* to = s_rows + (ahead - j0) % kRing * kRowBytes<T>;
             if (VEC) {                                             // each thread its own entries
                 constexpr int kOwn = kPer * (int)sizeof(T);
 #pragma unroll
@@ -172,10 +170,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
                 for (int at = tid * 16; at < bytes + shift; at += kThreads * 16) copy16(to + at, in - shift + at, min(16, bytes + shift - at));
             }
             in += row_bytes;
+            ++ahead;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    copy_group();
+    copy_row();
     // masks: this thread's byte, or, as a warp's entries of one step share a word where rows are not aligned, step `lane`'s word
     const int64_t mask_bytes = (a.vocab + 31) / 32 * 4;
     const int word = (first - lane + lane * kStep) >> 5;
@@ -202,14 +201,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
 #pragma unroll
         for (int i = 0; i < kPer; ++i) s_bias[tid + i * kThreads] = 0.0f;
         __syncthreads();
-        for (int i = b0 + tid; i < b1; i += kThreads) {
-            const int t = a.bias_tokens[i];
-            // ascending ids: no id twice, so the sum does not depend on an order
-            if (t < 0 || t >= a.vocab || (i > b0 && a.bias_tokens[i - 1] >= t)) {
-                if (report) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
-            } else if (t >= base && t < base + kChunk) {
-                s_bias[t - base] = a.bias_values[i];
-                biased = true;
+        for (int i0 = b0 + tid; i0 < b1; i0 += kBiasAhead * kThreads) {
+            int t[kBiasAhead], before[kBiasAhead];
+            float value[kBiasAhead];
+#pragma unroll
+            for (int k = 0; k < kBiasAhead; ++k) {             // all loads at once, also of values that are not needed
+                const int i = i0 + k * kThreads;
+                t[k] = i < b1 ? a.bias_tokens[i] : 0;
+                before[k] = i < b1 && i > b0 ? a.bias_tokens[i - 1] : -1;
+                value[k] = i < b1 ? a.bias_values[i] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kBiasAhead; ++k) {
+                if (i0 + k * kThreads >= b1) break;
+                // ascending ids: no id twice, so the sum does not depend on an order
+                if (t[k] < 0 || t[k] >= a.vocab || before[k] >= t[k]) {
+                    if (report) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
+                } else if (t[k] >= base && t[k] < base + kChunk) {
+                    s_bias[t[k] - base] = value[k];
+                    biased = true;
+                }
             }
         }
         biased = __syncthreads_or(biased);
@@ -254,15 +265,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) process_logi
     uint8_t* out = static_cast<uint8_t*>(a.out) + begin;
 #pragma unroll 1
     for (int j = j0; j < j1; ++j, out += row_bytes) {
-        if ((j - j0) % kGroupRows<T> == 0) {
-            if (!VEC) __syncthreads();   // all are done with the group before, whose place the next one takes
-            copy_group();
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            if (!VEC) __syncthreads();   // others' copies have landed too
-        }
+        if (!VEC) __syncthreads();       // all are done with the row before, whose place the next one takes
+        copy_row();
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (!VEC) __syncthreads();       // others' copies have landed too
         mask += mask_bytes;
         const uint32_t next = load_mask(j + 1);
-        const uint8_t* row = s_rows + (j - j0) % kRing<T> * kRowBytes<T>;
+        const uint8_t* row = s_rows + (j - j0) % kRing * kRowBytes<T>;
         Row8<T> x, o;
         if (VEC) {
             x = reinterpret_cast<const Row8<T>*>(row)[tid];
@@ -597,9 +606,9 @@ int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dty
     const bool vec = vocab % 8 == 0;
     if (dtype == Q3KV_F32)
         return cuda_status(launch(vec ? process_logits_kernel<float, true> : process_logits_kernel<float, false>, a, grid,
-                                  kRing<float> * kRowBytes<float>, st, kThreads, per));
+                                  kRing * kRowBytes<float>, st, kThreads, per));
     return cuda_status(launch(vec ? process_logits_kernel<__nv_bfloat16, true> : process_logits_kernel<__nv_bfloat16, false>, a, grid,
-                              kRing<__nv_bfloat16> * kRowBytes<__nv_bfloat16>, st, kThreads, per));
+                              kRing * kRowBytes<__nv_bfloat16>, st, kThreads, per));
 }
 
 }  // extern "C"
