@@ -14,6 +14,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "q3kv_internal.h"
 
@@ -65,7 +66,8 @@ struct alignas(16) Row8 {
 // A CTA takes 2,048 entries of a slot's rows, or of a part of them where the CTAs would be few, one row after the other.
 // Bound: bytes (logits in and out) and, close behind, issue slots.  So the rows come by asynchronous 16-byte copies into a
 // ring of two, whole vectors also where a row does not start on one, and no registers hold them (longer rings and rows in
-// groups cost more in CTAs per SM than they hide: 8 slots x 16 float32 17.0 us, three rows 17.5, two groups of two 18.6); an entry's penalty
+// groups cost more in CTAs per SM than they hide: 8 slots x 16 float32 17.0 us, three rows 17.5, two groups of two 18.6; with
+// four CTAs per SM instead of five 18.7); an entry's penalty
 // alpha c + beta [c > 0] - bias is worked out once for all rows but where the step's own tokens count; and a warp
 // looks only at those of its eight steps in which some lane's entry changes (most entries are not seen, away from the
 // frequent tokens): the others only take the mask.
@@ -102,17 +104,10 @@ __device__ __forceinline__ void apply_mask(Row8<__nv_bfloat16>& o, uint32_t allo
         w[e / 2 + 1] = (w[e / 2 + 1] & high) | (0xff80ff80u & ~high);
     }
 }
-template <typename T>
-__device__ __forceinline__ bool same_bits(const Row8<T>& a, const Row8<T>& b) {
-    const uint32_t *x = reinterpret_cast<const uint32_t*>(&a), *y = reinterpret_cast<const uint32_t*>(&b);
-    uint32_t d = 0;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) * kPer / 4; ++i) d |= x[i] ^ y[i];
-    return d == 0;
-}
+__device__ __forceinline__ bool same_bits(uint4 a, uint4 b) { return ((a.x ^ b.x) | (a.y ^ b.y) | (a.z ^ b.z) | (a.w ^ b.w)) == 0; }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) process_logits_kernel(LogitArgs a, int per) {
+__global__ void __launch_bounds__(kThreads, 5) process_logits_kernel(LogitArgs a, int per) {
     extern __shared__ __align__(16) uint8_t s_rows[];       // [kRing][kRowBytes]
     __shared__ float s_bias[kChunk];
     __shared__ int s_tok[kMaxNq];
@@ -128,21 +123,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) 
     }
     const float theta = a.repetition ? a.repetition[slot] : 1.0f;
     const float alpha = a.frequency ? a.frequency[slot] : 0.0f, beta = a.presence ? a.presence[slot] : 0.0f;
-    // this thread's entries: 8 neighbours, or every 256th where rows are not 16-byte aligned
-    const int first = VEC ? base + tid * kPer : base + tid;
-    constexpr int kStep = VEC ? 1 : kThreads;
+    // this thread's entries: vectors of 16 bytes, neighbours in neighbouring threads, or single ones where rows are not aligned
+    constexpr int kVec = VEC ? 16 / (int)sizeof(T) : 1, kVecs = kPer / kVec, kNext = kThreads * kVec;
+    const int first = base + tid * kVec;
+    const auto off = [](int e) { return e / kVec * kNext + e % kVec; };
     Row8<int16_t> count;
-    if (a.counts && first < a.vocab) {
-        const int16_t* c = a.counts + (int64_t)slot * a.counts_stride;
-        if (VEC) {
-            count = *reinterpret_cast<const Row8<int16_t>*>(c + first);   // the stride covers whole vectors
-        } else {
+    {
+        const int16_t* c = a.counts + (int64_t)slot * a.counts_stride + first;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) count.x[e] = first + e * kStep < a.vocab ? c[first + e * kStep] : (int16_t)0;
+        for (int v = 0; v < kVecs; ++v) {                      // the stride covers whole vectors
+            using V = std::conditional_t<kVec == 8, uint4, std::conditional_t<kVec == 4, uint2, int16_t>>;
+            reinterpret_cast<V*>(&count)[v] = a.counts && first + v * kNext < a.vocab ? *reinterpret_cast<const V*>(c + v * kNext) : V{};
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) count.x[e] = 0;
     }
     const bool report = blockIdx.x == 0 && blockIdx.z == 0 && a.status;
     if (w == 0) return;
@@ -161,10 +153,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) 
         if (ahead < j1) {
             uint8_t* to = s_rows + (ahead - j0) % kRing * kRowBytes<T>;
             if (VEC) {                                             // each thread its own entries
-                constexpr int kOwn = kPer * (int)sizeof(T);
 #pragma unroll
-                for (int i = 0; i < kOwn; i += 16)
-                    if (first < a.vocab) copy16(to + tid * kOwn + i, in + tid * kOwn + i, 16);
+                for (int v = 0; v < kVecs; ++v)
+                    if (first + v * kNext < a.vocab) copy16(to + (v * kThreads + tid) * 16, in + (v * kThreads + tid) * 16, 16);
             } else {
                 const int shift = (int)(reinterpret_cast<uintptr_t>(in) & 15);       // the buffer begins on 16 bytes
                 for (int at = tid * 16; at < bytes + shift; at += kThreads * 16) copy16(to + at, in - shift + at, min(16, bytes + shift - at));
@@ -175,14 +166,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) 
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     copy_row();
-    // masks: this thread's byte, or, as a warp's entries of one step share a word where rows are not aligned, step `lane`'s word
+    // masks: this thread's bits, or, as a warp's entries of one step share a word where rows are not aligned, step `lane`'s word
     const int64_t mask_bytes = (a.vocab + 31) / 32 * 4;
-    const int word = (first - lane + lane * kStep) >> 5;
+    const int word = (first - lane + lane * kNext) >> 5;
     const bool own = a.mask && (VEC ? first < a.vocab : lane < kPer && word * 4 < mask_bytes);
     const uint8_t* mask = reinterpret_cast<const uint8_t*>(a.mask) + (r0 + j0) * mask_bytes;
     auto load_mask = [&](int j) -> uint32_t {
         if (!own || j >= j1) return VEC ? 0xffu : 0u;
-        return VEC ? mask[first >> 3] : reinterpret_cast<const uint32_t*>(mask)[word];
+        if (!VEC) return reinterpret_cast<const uint32_t*>(mask)[word];
+        uint32_t bits = mask[first >> 3];
+        if (kVecs == 2) {                                          // a half of each of two bytes
+            const uint32_t more = first + kNext < a.vocab ? mask[(first + kNext) >> 3] : 0u;
+            bits = (bits >> (first & 4) & 15u) | (more >> (first & 4) & 15u) << 4;
+        }
+        return bits;
     };
     uint32_t allowed = load_mask(j0);
     bool near = false;                   // a token of the step is in the chunk
@@ -236,14 +233,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) 
     marks = seen;
     if (biased)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) marks |= (s_bias[first - base + e * kStep] != 0.0f ? 1u : 0u) << e;
+        for (int e = 0; e < kPer; ++e) marks |= (s_bias[first - base + off(e)] != 0.0f ? 1u : 0u) << e;
     uint32_t step[kPer / 2] = {0, 0, 0, 0};                 // 16 bits per entry, bit i set where t_i is the entry
     if (near)
         for (int i = 0; i < j1; ++i) {
             const int d = s_tok[i] - first;
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
-                if (d == e * kStep) {
+                if (d == off(e)) {
                     step[e / 2] |= 1u << (i + 16 * (e & 1));
                     marks |= 1u << e;
                 }
@@ -257,11 +254,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) 
         for (int e = 0; e < kPer; ++e) {
             const int c = count.x[e] & 0x7fff;
             less[e] = c > 0 ? fmaf(alpha, (float)c, beta) : 0.0f;
-            if (biased) less[e] -= s_bias[first - base + e * kStep];
+            if (biased) less[e] -= s_bias[first - base + off(e)];
         }
     }
     const bool in_place = a.logits == a.out;
-    const int valid = (a.vocab - first + kStep - 1) / kStep;      // this thread's entries that exist (not VEC)
+    const int valid = (a.vocab - first + kNext - 1) / kNext;      // this thread's vectors that exist
     uint8_t* out = static_cast<uint8_t*>(a.out) + begin;
 #pragma unroll 1
     for (int j = j0; j < j1; ++j, out += row_bytes) {
@@ -274,11 +271,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) 
         const uint8_t* row = s_rows + (j - j0) % kRing * kRowBytes<T>;
         Row8<T> x, o;
         if (VEC) {
-            x = reinterpret_cast<const Row8<T>*>(row)[tid];
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) reinterpret_cast<uint4*>(&x)[v] = reinterpret_cast<const uint4*>(row)[v * kThreads + tid];
         } else {
             const T* p = reinterpret_cast<const T*>(row + (reinterpret_cast<uintptr_t>(out) & 15)) + tid;      // in and out are aligned alike
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) x.x[e] = p[e * kStep];        // anything behind the end
+            for (int e = 0; e < kPer; ++e) x.x[e] = p[e * kThreads];     // anything behind the end
         }
         o = x;
         if (changing) {
@@ -310,12 +308,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : (VEC ? 4 : 5)) 
         }
         allowed = next;
         if (VEC) {
-            if (first < a.vocab && (!in_place || !same_bits(o, x))) reinterpret_cast<Row8<T>*>(out)[tid] = o;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const uint4 to = reinterpret_cast<const uint4*>(&o)[v];
+                if (v < valid && (!in_place || !same_bits(to, reinterpret_cast<const uint4*>(&x)[v])))
+                    reinterpret_cast<uint4*>(out)[v * kThreads + tid] = to;
+            }
         } else {
             T* p = reinterpret_cast<T*>(out) + tid;
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
-                if (e < valid) p[e * kStep] = o.x[e];
+                if (e < valid) p[e * kThreads] = o.x[e];
         }
     }
 }
@@ -597,7 +600,7 @@ int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dty
     const int e = device_sm_count(&sms);
     if (e != Q3KV_OK) return e;
     // a slot's rows go to one CTA per chunk where that gives every SM eight CTAs, else to several (8 slots x 16 float32:
-    // 18.7 us with four per SM, 19.8 with eight, 21.0 with twelve; 1 x 6: 4.8, 4.2, 4.3)
+    // 20.0 us with five per SM, 17.0 with eight, 19.0 with ten)
     const int64_t chunks = ((int64_t)vocab + kChunk - 1) / kChunk, few = chunks * num_slots;
     const int parts = (int)std::min<int64_t>(max_n_q, std::max<int64_t>(1, (8 * (int64_t)sms + few / 2) / few)), per = (max_n_q + parts - 1) / parts;
     const dim3 grid((unsigned)chunks, (unsigned)num_slots, (unsigned)((max_n_q + per - 1) / per));
