@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kThreads) count_kernel(CountArgs a) {
 // memory and adds each entry once: no atomics in global memory, no order.  Where slots are few, a cluster of up to four
 // CTAs shares a range's tokens, and each adds up its part of the entries from the shared memory of all (1 x 524,288: 13.5 us
 // with four CTAs, 15.8 with eight, whose cluster takes 5 us more to start).
-// Bound: issue slots, one token costs each range's CTA about seven instructions (8 x 65,536 of 248,320 entries: 8.2 us, 11.7
-// with a check of the end at every token).
+// Bound: the rounds' latency and issue slots; a token costs each range's CTA about seven instructions (8 x 65,536 of 248,320
+// entries: 8.2 us, 11.7 with a check of the end at every token).
 constexpr int kRange = 16384, kHistoryThreads = 1024;
 constexpr unsigned kMaxParts = 4;
 
