@@ -35,6 +35,7 @@ constexpr uint32_t kTileBytes = kBs8Tile * kHeadDim;
 constexpr float kAbove = 8.0f;                 // m is set this far below the largest score: p' <= 2^8 then,
 constexpr float kRaise = 15.0f;                // and at most 2^15 until it is raised
 constexpr float kQStep = 4096.0f;             // between the two groups of a float32 query's codes
+constexpr float kPStep = 2048.0f;             // and of a float32 weight's: what three codes leave of 2^15 is 2^4 at most
 constexpr int kMeta = 8;                       // tiles whose scales are kept
 
 template <int R, bool F32>
@@ -48,6 +49,11 @@ struct Cfg {
     // Weight codes side by side in the columns of a PV MMA, as many as TMEM has room for: an MMA of few columns takes as
     // long as one of 64 (32,768 x 1: 14.4 -> 13.9 us; float32 5 slots x 16: 26.8 -> 25.4).
     static constexpr int kBeside = F32 ? (R == 16 ? 6 : 2) : R > 48 ? 2 : 3;
+    static constexpr int kParts = (kP + kBeside - 1) / kBeside;        // MMAs that share their columns
+    // Code n of a weight is code `column` of part `part`.  Float32's second three codes have columns of their own.
+    __host__ __device__ static constexpr int part(int n) { return F32 ? n % kParts : n / kBeside; }
+    __host__ __device__ static constexpr int column(int n) { return F32 ? n / kParts : n % kBeside; }
+    __host__ __device__ static constexpr int wide(int part) { return F32 || (part + 1) * kBeside <= kP ? kBeside : kP - part * kBeside; }
     // Weight buffers: PV of a tile runs during the next tile's softmax (655,360 x 8: 117 -> 111 us).  Float32 waits for each
     // tile's outputs anyway.
     static constexpr int kPBufs = F32 ? 1 : 2;
@@ -236,12 +242,12 @@ __device__ void issue_pv(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_
             tc_fence_after();
             const uint64_t ad = vdesc + st * (kTileBytes / 16);
 #pragma unroll
-            for (int part = 0; part < C::kP; part += C::kBeside) {
-                const int wide = min(C::kBeside, C::kP - part);
+            for (int part = 0; part < C::kParts; ++part) {
+                const int wide = C::wide(part);
 #pragma unroll
                 for (int k = 0; k < kBs8Tile / 32; ++k)
                     mma8(o, ad + k * (8192 / 16),
-                         (wide == 1 ? pdesc1 : pdesc) + (pb * C::kP + part) * (R * kBs8Tile / 16) + k * (4 * (wide * R / 16) * 128 / 16),
+                         (wide == 1 ? pdesc1 : pdesc) + (pb * C::kP + part * C::kBeside) * (R * kBs8Tile / 16) + k * (4 * (wide * R / 16) * 128 / 16),
                          idesc8(wide * R, true, true), (!F32 && i > 0) || part > 0 || k > 0);
             }
             mma_commit(&sm.v_free[st]);
@@ -403,7 +409,7 @@ __device__ __forceinline__ void outputs(uint32_t lanes, int r0, int half, float*
     for (int c = 0; c < C::kH; ++c) {
         o[c] = part[C::kBeside - 1][c];
 #pragma unroll
-        for (int n = C::kBeside - 2; n >= 0; --n) o[c] += part[n][c];
+        for (int n = C::kBeside - 2; n >= 0; --n) o[c] = F32 && n == C::kBeside / 2 - 1 ? fmaf(o[c], 1.0f / kPStep, part[n][c]) : o[c] + part[n][c];
     }
 }
 
@@ -554,6 +560,10 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                         if (n + 1 == C::kP) break;
                         x = add2(x, e5m2_negative(code[n][c]));
                         y = add2(y, e5m2_negative(code[n][c] >> 16));
+                        if (n == 2) {                // exact; without it a weight below 2^-25 of the largest would be gone
+                            x = mul2(x, both(kPStep));
+                            y = mul2(y, both(kPStep));
+                        }
                     }
                 } else {
                     // E5M2 is the upper byte of fp16: the first two codes are cut off, the third is rounded (half a step: 0x80)
@@ -578,8 +588,8 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
             uint8_t* pb = sm.p[it % C::kPBufs] + (r0 / 16) * 128 + (p & 7) * 16 + (r0 & 15);
 #pragma unroll
             for (int n = 0; n < C::kP; ++n) {
-                const int part = n / C::kBeside * C::kBeside, wide = min(C::kBeside, C::kP - part);
-                uint8_t* to = pb + part * R * kBs8Tile + (n - part) * (R / 16 * 128) + (p >> 3) * (wide * R / 16 * 128);
+                const int part = C::part(n);
+                uint8_t* to = pb + part * C::kBeside * R * kBs8Tile + C::column(n) * (R / 16 * 128) + (p >> 3) * (C::wide(part) * R / 16 * 128);
                 if constexpr (H == 8) *reinterpret_cast<uint2*>(to) = make_uint2(code[n][0], code[n][1]);
                 else *reinterpret_cast<uint4*>(to) = make_uint4(code[n][0], code[n][1], code[n][2], code[n][3]);
             }

@@ -269,6 +269,23 @@ def test_verify_of_uneven_caches(shape, kind, dtype, impl):
     check(cache.verify(L, T, q, impl=impl), q, cache, L, T, kind)
 
 
+@pytest.mark.parametrize("T", [2, 4])
+@pytest.mark.parametrize("kind,dtype,impl", KINDS[:3])
+def test_one_large_weight_and_many_equal_small_ones(kind, dtype, impl, T):
+    """Half of the weight on one early key, the rest shared out evenly: what one weight's codes lose is lost by all.  More
+    slots than CTAs, which share their pages, so that a CTA goes through a whole context."""
+    L, slots = 20000, 160
+    one = Bs8Cache([L], kv=1)
+    one.fill([L], seed=21, shape=lambda k, v, b: (np.where(np.arange(L)[:, None, None] == 3, np.log(L) / 16, 0.0 * k).astype(np.float32), v + 1.0))
+    q = (1.0 + 0.05 * queries(T, 1, 22, torch.float32)).to(dtype)
+    out = torch.full((slots * T, 8, 256), 77.0, dtype=dtype, device="cuda")
+    api.bs8_verify_attn(one.desc, one.pool, one.page_table.repeat(slots, 1), i32([L] * slots), i32([T] * slots), offsets([T] * slots), L, T,
+                        0, q.repeat(slots, 1, 1), out, one.workspace([L], [T], slots), impl, one.status)
+    assert int(one.status) == 0
+    for b in (0, 1, 77, slots - 1):
+        check(out[b * T:b * T + T], q, one, [L], [T], kind)
+
+
 @pytest.mark.parametrize("kind,dtype,impl", KINDS[:3])
 def test_rows_of_very_different_sizes(kind, dtype, impl):
     """Each row has a scale of its own: 2^-40 .. 2^3, and a row of zeros."""
