@@ -726,8 +726,9 @@ Q3KV_API int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_
  * A slot with T_b > L_b, L_b above max_ctx_len or beyond its page table, T_b above max_n_q or a
  * negative offset sets Q3KV_STATUS_BAD_LENGTH and its rows are left as they were.  Positions of
  * a page out of range count as hidden (Q3KV_STATUS_BAD_PAGE); a row that sees nothing is 0.  A
- * query row that is not finite gives NaN; scores have to stay within float32.  Neither out nor the
- * workspace may overlap another operand. */
+ * query row that is not finite gives NaN; scores have to stay within float32.  The tensor-core leg
+ * keeps weights times V's block scales in float32: V blocks of a context whose scales lie more than
+ * 2^90 apart may lose weights.  Neither out nor the workspace may overlap another operand. */
 Q3KV_API int q3kv_bs8_workspace_bytes(const q3kv_cache_desc* desc, int32_t num_slots, int64_t max_ctx_len,
                      int32_t max_n_q, int32_t impl, size_t* bytes);
 Q3KV_API int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* d_pool,

@@ -6,8 +6,9 @@
 //   q  = 2^-k (q1 + q2)      two E4M3 codes, k per row: a bf16 value has 8 significant bits, two codes hold them all;
 //                            what is below 2^-18 of the row's largest value is rounded away
 //   p' = p1 + p2 + p3        three E5M2 codes (3 significant bits each) of the weight as fp16: at most 2^-9 off, as if
-//                            the weight were rounded to bf16; E5M2 for its range (2^-16 .. 2^15): a long context's
-//                            many small weights stay above it next to a large one
+//                            the weight were rounded to bf16; E5M2 for its range (2^-16 .. 2^15), and the last code
+//                            times 2^5: a long context's many small weights are not lost next to a large one, and where
+//                            they are equal, and so is what they lose, their sum is right
 // Contractions (M = 128, float32 accumulation in TMEM):
 //   S^T[p][r | R + r] = K[p][:] . q1[r][:] | q2[r][:]   A = K codes (K-major), N = 2 R columns, K = 256 dims
 //   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions,
@@ -18,7 +19,7 @@
 // than 2^7 of headroom (a vote per tile), so most tiles need no maximum and no rescaling.
 //
 // Bound: the codes' bytes.  At 8 tokens a tile's 64 KiB take about 2,900 cycles of an SM's share of HBM (655,360 positions
-// of 2 heads: 111 us, 6,070 GB/s; 1 token 103 us, 6,500 GB/s); its 24 MMAs and its softmax, which overlap, less.  9 to 16
+// of 2 heads: 112 us, 6,000 GB/s; 1 token 103 us, 6,500 GB/s); its 24 MMAs and its softmax, which overlap, less.  9 to 16
 // tokens are two chunks of rows and take twice that (165 and 208 us).  One CTA per SM; warp 0 copies, warps 1-3 issue the MMAs, the others are the softmax: groups of
 // four warps with a thread per position and 8 or 16 rows.
 #include <math_constants.h>
@@ -36,6 +37,7 @@ constexpr float kAbove = 8.0f;                 // m is set this far below the la
 constexpr float kRaise = 15.0f;                // and at most 2^15 until it is raised
 constexpr float kQStep = 4096.0f;             // between the two groups of a float32 query's codes
 constexpr float kPStep = 2048.0f;             // and of a float32 weight's: what three codes leave of 2^15 is 2^4 at most
+constexpr float kPLast = 32.0f;               // before a bf16 weight's last code: what two leave of 2^15 is under 2^10
 constexpr int kMeta = 8;                       // tiles whose scales are kept
 
 template <int R, bool F32>
@@ -50,9 +52,10 @@ struct Cfg {
     // long as one of 64 (32,768 x 1: 14.4 -> 13.9 us; float32 5 slots x 16: 26.8 -> 25.4).
     static constexpr int kBeside = F32 ? (R == 16 ? 6 : 2) : R > 48 ? 2 : 3;
     static constexpr int kParts = (kP + kBeside - 1) / kBeside;        // MMAs that share their columns
-    // Code n of a weight is code `column` of part `part`.  Float32's second three codes have columns of their own.
-    __host__ __device__ static constexpr int part(int n) { return F32 ? n % kParts : n / kBeside; }
-    __host__ __device__ static constexpr int column(int n) { return F32 ? n / kParts : n % kBeside; }
+    // Code n of a weight is code `column` of part `part`.  Codes that are scaled up (float32's second three, bf16's last)
+    // have columns of their own: of two columns the second.
+    __host__ __device__ static constexpr int part(int n) { return F32 ? n % kParts : kBeside == 2 && n == 1 ? 1 : 0; }
+    __host__ __device__ static constexpr int column(int n) { return F32 ? n / kParts : kBeside == 2 ? n / 2 : n; }
     __host__ __device__ static constexpr int wide(int part) { return F32 || (part + 1) * kBeside <= kP ? kBeside : kP - part * kBeside; }
     // Weight buffers: PV of a tile runs during the next tile's softmax (655,360 x 8: 117 -> 111 us).  Float32 waits for each
     // tile's outputs anyway.
@@ -128,6 +131,7 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t last2(uint32_t a) { return as_u32(__hmul2(as_h2(a), __float2half2_rn(kPLast))); }
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) { return as_u32(__hsub2(as_h2(a), as_h2(b))); }
 
 // ---------------------------------------------------------------- roles
@@ -407,9 +411,11 @@ __device__ __forceinline__ void outputs(uint32_t lanes, int r0, int half, float*
     tmem_ld_wait();
 #pragma unroll
     for (int c = 0; c < C::kH; ++c) {
+        constexpr int kScaled = F32 ? C::kBeside / 2 : 1;        // columns
         o[c] = part[C::kBeside - 1][c];
 #pragma unroll
-        for (int n = C::kBeside - 2; n >= 0; --n) o[c] = F32 && n == C::kBeside / 2 - 1 ? fmaf(o[c], 1.0f / kPStep, part[n][c]) : o[c] + part[n][c];
+        for (int n = C::kBeside - 2; n >= 0; --n)
+            o[c] = n == C::kBeside - kScaled - 1 ? fmaf(o[c], 1.0f / (F32 ? kPStep : kPLast), part[n][c]) : o[c] + part[n][c];
     }
 }
 
@@ -566,10 +572,11 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                         }
                     }
                 } else {
-                    // E5M2 is the upper byte of fp16: the first two codes are cut off, the third is rounded (half a step: 0x80)
+                    // E5M2 is the upper byte of fp16: the first two codes are cut off, the third, times 2^5, is rounded (half
+                    // a step: 0x80)
                     const uint32_t a0 = f16_pair(x.x, x.y), b0 = f16_pair(y.x, y.y);
                     const uint32_t ar = sub2(a0, a0 & 0xff00ff00u), br = sub2(b0, b0 & 0xff00ff00u);
-                    const uint32_t a3 = sub2(ar, ar & 0xff00ff00u) + 0x00800080u, b3 = sub2(br, br & 0xff00ff00u) + 0x00800080u;
+                    const uint32_t a3 = last2(sub2(ar, ar & 0xff00ff00u)) + 0x00800080u, b3 = last2(sub2(br, br & 0xff00ff00u)) + 0x00800080u;
                     code[0][c] = __byte_perm(a0, b0, 0x7531);
                     code[1][c] = __byte_perm(ar, br, 0x7531);
                     code[2][c] = __byte_perm(a3, b3, 0x7531);

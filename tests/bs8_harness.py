@@ -108,8 +108,8 @@ def reference(q, k, v, n_ctx, kind, hidden=None):
     - bf16 queries: codes below 2^-17 of the row's largest value are rounded away, 2^-18 max|q| sum |k_d| / 16 at most;
     - bf16's weights in three codes: 2^-9 and the rounding to fp16 before them, 2^-11 (half of fp16's step);
       float32's in six: 2^-23;
-    - a code's smallest step: half of 2^-16 (bf16) or 2^-27 (float32) against largest weights of 2^8 or more, 2^-25 or 2^-36
-      per position;
+    - a code's smallest step against largest weights of 2^8 or more: half of 2^-21 (bf16; half of fp16's 2^-24 before) or of
+      2^-27 (float32), 2^-29 in all or 2^-36 per position;
     - sums in float32 over the tiles of one CTA and the partials, and the row sum: 2^-16;
     and the output's own rounding, half a step: 2^-8 (bf16) or 2^-24 of the value.
     """
@@ -137,7 +137,7 @@ def reference(q, k, v, n_ctx, kind, hidden=None):
             visible = np.where(mask, 0.0, np.abs(K).sum(axis=1)[None, :]).max(axis=1, keepdims=True)
             e = e + 2.0 ** -18 * np.abs(q[:, h]).max(axis=1, keepdims=True) * visible / 16.0
         c = {"bf16": 2.0 ** -9 + 2.0 ** -11, "f32": 2.0 ** -23, "fma": 0.0}[kind] + 2.0 * e + 2.0 ** -16
-        floor = L * {"bf16": 2.0 ** -25, "f32": 2.0 ** -36, "fma": 0.0}[kind] * np.abs(V).max()
+        floor = L * {"bf16": 2.0 ** -29, "f32": 2.0 ** -36, "fma": 0.0}[kind] * np.abs(V).max()
         tol[:, h] = c * A + floor + 2.0 ** -24 * np.abs(out[:, h])
         out[empty, h] = 0.0
     return out, tol
