@@ -791,7 +791,7 @@ Q3KV_API int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_s
  *   y = y + bias(x);  where the row's mask bit is 0:  y = -inf
  * and out = y rounded to the logits' dtype (f32 or bf16).
  *   out            [num_rows, vocab]; may be logits itself (then rows change in place), must not overlap
- *                  any other operand.  Rows of no slot are left as they were.
+ *                  any other operand.  Rows of no slot are left as they were; two slots share none.
  *   d_counts       or NULL: only the step's tokens count
  *   d_repetition, d_frequency, d_presence   float [num_slots], each or NULL (1, 0, 0)
  *   d_bias_offsets int32 [num_slots + 1] or NULL; slot b's biases are entries
