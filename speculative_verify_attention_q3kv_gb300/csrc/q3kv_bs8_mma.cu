@@ -5,10 +5,11 @@
 // decoded.  What the other operands lose in 8 bits is carried by more than one code per value:
 //   q  = 2^-k (q1 + q2)      two E4M3 codes, k per row: a bf16 value has 8 significant bits, two codes hold them all;
 //                            what is below 2^-18 of the row's largest value is rounded away
-//   p' = p1 + p2 + p3        three E5M2 codes (3 significant bits each) of the weight as fp16: at most 2^-9 off, as if
-//                            the weight were rounded to bf16; E5M2 for its range (2^-16 .. 2^15), and the last code
-//                            times 2^5: a long context's many small weights are not lost next to a large one, and where
-//                            they are equal, and so is what they lose, their sum is right
+//   p' = p1 + p2 + p3        three E5M2 codes (3 significant bits each, every one rounded to nearest, so that signs add a
+//                            bit to the second and third) hold the weight as fp16 exactly from 2^-10 on: 11 bits, at most
+//                            2^-11 off; E5M2 for its range (2^-16 .. 2^15), and the last code times 2^7: a long context's
+//                            many small weights are not lost next to a large one, and where they are equal, and so is
+//                            what they lose, their sum is right
 // Contractions (M = 128, float32 accumulation in TMEM):
 //   S^T[p][r | R + r] = K[p][:] . q1[r][:] | q2[r][:]   A = K codes (K-major), N = 2 R columns, K = 256 dims
 //   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions,
@@ -37,7 +38,7 @@ constexpr float kAbove = 8.0f;                 // m is set this far below the la
 constexpr float kRaise = 15.0f;                // and at most 2^15 until it is raised
 constexpr float kQStep = 4096.0f;             // between the two groups of a float32 query's codes
 constexpr float kPStep = 2048.0f;             // and of a float32 weight's: what three codes leave of 2^15 is 2^4 at most
-constexpr float kPLast = 32.0f;               // before a bf16 weight's last code: what two leave of 2^15 is under 2^10
+constexpr float kPLast = 128.0f;              // before a bf16 weight's last code: what two leave of 2^15 is 2^8 at most
 constexpr int kMeta = 8;                       // tiles whose scales are kept
 
 template <int R, bool F32>
@@ -572,14 +573,15 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                         }
                     }
                 } else {
-                    // E5M2 is the upper byte of fp16: the first two codes are cut off, the third, times 2^5, is rounded (half
-                    // a step: 0x80)
-                    const uint32_t a0 = f16_pair(x.x, x.y), b0 = f16_pair(y.x, y.y);
-                    const uint32_t ar = sub2(a0, a0 & 0xff00ff00u), br = sub2(b0, b0 & 0xff00ff00u);
-                    const uint32_t a3 = last2(sub2(ar, ar & 0xff00ff00u)) + 0x00800080u, b3 = last2(sub2(br, br & 0xff00ff00u)) + 0x00800080u;
+                    // E5M2 is the upper byte of fp16, and half a step of it is 0x80, whatever the sign.  (A NaN's codes become
+                    // zeros: the row sum keeps it.)
+                    constexpr uint32_t kHalf = 0x00800080u, kByte = 0xff00ff00u;
+                    const uint32_t lo = f16_pair(x.x, x.y), hi = f16_pair(y.x, y.y), a0 = lo + kHalf, b0 = hi + kHalf;
+                    const uint32_t ar = sub2(lo, a0 & kByte), br = sub2(hi, b0 & kByte), a1 = ar + kHalf, b1 = br + kHalf;
+                    const uint32_t a2 = last2(sub2(ar, a1 & kByte)) + kHalf, b2 = last2(sub2(br, b1 & kByte)) + kHalf;
                     code[0][c] = __byte_perm(a0, b0, 0x7531);
-                    code[1][c] = __byte_perm(ar, br, 0x7531);
-                    code[2][c] = __byte_perm(a3, b3, 0x7531);
+                    code[1][c] = __byte_perm(a1, b1, 0x7531);
+                    code[2][c] = __byte_perm(a2, b2, 0x7531);
                 }
             }
             if (it >= C::kPBufs) ok = ok && wait_pv(it - C::kPBufs);
