@@ -589,7 +589,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                 __syncwarp();
                 tc_fence_after();
                 if (i > 0) drain<R, F32>(lanes, r0, acc);
-                if (raise) {
+                if (raise && i > 0) {            // the first tile has nothing to scale, and its factor may be infinite
 #pragma unroll
                     for (int c = 0; c < 2 * H; ++c) acc[c] *= fast_exp2(sm.dm[r0 + c % H]);
                 }
