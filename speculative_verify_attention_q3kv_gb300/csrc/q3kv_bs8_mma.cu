@@ -460,6 +460,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
             for (int c = 0; c < 2 * H; ++c) acc[c] = 0.0f;
         }
         const int seen = w.s.L - w.s.T + w.chunk(heads) * (a.rows / kGroup);      // last position that the chunk's first token sees
+        bool fresh = true;                 // no tile of the segment has shown a position yet: pages out of range hide theirs
         for (int i = 0; i < w.tiles; ++i, ++it) {
             const uint32_t b = it & 1, slot = it % kMeta;
             const int p0 = (w.tile + i) * kBs8Tile;
@@ -505,7 +506,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
             float top = d[0];
 #pragma unroll
             for (int c = 1; c < H; ++c) top = fmaxf(top, d[c]);
-            const bool raise = named_or(bar, 128, i == 0 || top > kRaise || !ok);
+            const bool raise = named_or(bar, 128, fresh || top > kRaise || !ok);
             if (raise) {
                 if (named_or(bar, 128, !ok)) {
                     ok = false;
@@ -523,8 +524,8 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                 if (p < H) {
                     const float x = fmaxf(fmaxf(sm.red[wg][0][p], sm.red[wg][1][p]), fmaxf(sm.red[wg][2][p], sm.red[wg][3][p]));
                     const float m = -sm.m[r0 + p];
-                    // the first tile sets m; a row that sees nothing of it sees nothing of the segment's later tiles either
-                    const float now = i > 0 ? fmaxf(m, x - kAbove) : x > -CUDART_INF_F ? x - kAbove : 0.0f;
+                    // the first visible tile sets m; a row that sees nothing of it sees nothing of the segment's later tiles
+                    const float now = !fresh ? fmaxf(m, x - kAbove) : x > -CUDART_INF_F ? x - kAbove : 0.0f;
                     sm.m[r0 + p] = -now;
                     sm.dm[r0 + p] = m - now;
                 }
@@ -533,9 +534,9 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                 for (int c = 0; c < H / 2; ++c) {
                     const float2 dm = *reinterpret_cast<const float2*>(&sm.dm[r0 + 2 * c]);
                     d2[c] = add2(d2[c], dm);
-                    if (i > 0) l[c] = mul2(l[c], make_float2(fast_exp2(dm.x), fast_exp2(dm.y)));
+                    if (!fresh) l[c] = mul2(l[c], make_float2(fast_exp2(dm.x), fast_exp2(dm.y)));
                 }
-                if (!F32 && i > 0) {
+                if (!F32 && !fresh) {
                     ok = wait_pv(it - 1);      // PV of the tile before, and all earlier ones
                     __syncwarp();
                     tc_fence_after();
@@ -589,7 +590,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                 __syncwarp();
                 tc_fence_after();
                 if (i > 0) drain<R, F32>(lanes, r0, acc);
-                if (raise && i > 0) {            // the first tile has nothing to scale, and its factor may be infinite
+                if (raise && !fresh) {           // before, there is nothing to scale, and the factor may be infinite
 #pragma unroll
                     for (int c = 0; c < 2 * H; ++c) acc[c] *= fast_exp2(sm.dm[r0 + c % H]);
                 }
@@ -615,6 +616,7 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
             fence_proxy_async();
             tc_fence_before();
             warp_arrive(&sm.p_full[it % C::kPBufs]);
+            fresh = fresh && hidden;
         }
         ok = ok && wait_pv(it - 1);
         if (named_or(kAll, C::kSoftmax, !ok)) {      // all softmax warps leave together

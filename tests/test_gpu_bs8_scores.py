@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from bs8_harness import Bs8Cache, check, i32, offsets, queries
-from speculative_verify_attention_q3kv_gb300 import api
+from speculative_verify_attention_q3kv_gb300 import _lib, api
 from test_gpu_bs8 import KINDS
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +79,30 @@ def test_zero_values_in_front_of_the_others(kind, dtype, impl):
     q = (1.0 + 0.05 * queries(T, 1, 55, torch.float32)).to(dtype)
     _check_some(_shared(cache, L, T, q, impl), q, cache, L, T, kind)
     check(cache.verify([L], [T], q, impl=impl), q, cache, [L], [T], kind)
+
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("score,v_scale", [(-14.0, 1.0), (0.0, 1e-5), (-90.0, 1.0), (40.0, 1.0)])
+@pytest.mark.parametrize("kind,dtype,impl", KINDS[:3])
+def test_pages_out_of_range_in_front_of_a_share(kind, dtype, impl, score, v_scale, T):
+    """The first page and one further back are hidden; the visible tiles behind them count as if those were not there."""
+    L = 1100
+    cache = Bs8Cache([L], kv=1)
+    cache.fill([L], seed=56, shape=_at_score(score, v_scale, spread=0.5 / max(1.0, abs(score)) if score else 0.0))
+    q = (1.0 + 0.05 * queries(T, 1, 57, torch.float32)).to(dtype)
+    hidden = np.zeros(L, bool)
+    hidden[:256] = hidden[768:1024] = True
+    cache.page_table[0, 0], cache.page_table[0, 3] = -1, cache.num_pages
+    out = _shared(cache, L, T, q, impl)
+    assert int(cache.status) == _lib.Q3KV_STATUS_BAD_PAGE
+    _check_some(out, q, cache, L, T, kind, [hidden])
+
+
+@pytest.mark.parametrize("kind,dtype,impl", KINDS[:3])
+def test_only_the_last_page_is_in_range(kind, dtype, impl):
+    L, T = 1100, 5
+    cache = Bs8Cache([L], kv=1)
+    cache.fill([L], seed=58, shape=_at_score(-20.0))
+    q = (1.0 + 0.05 * queries(T, 1, 59, torch.float32)).to(dtype)
+    cache.page_table[0, :4] = -1
+    _check_some(_shared(cache, L, T, q, impl), q, cache, L, T, kind, [np.arange(L) < 1024])
