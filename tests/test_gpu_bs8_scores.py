@@ -8,7 +8,7 @@ import torch
 
 from bs8_harness import Bs8Cache, check, i32, offsets, queries
 from speculative_verify_attention_q3kv_gb300 import _lib, api
-from test_gpu_bs8 import KINDS
+from test_gpu_bs8 import KINDS, _late, _quiet, _rising, _scales
 
 pytestmark = pytest.mark.gpu
 SLOTS = 160
@@ -106,3 +106,18 @@ def test_only_the_last_page_is_in_range(kind, dtype, impl):
     q = (1.0 + 0.05 * queries(T, 1, 59, torch.float32)).to(dtype)
     cache.page_table[0, :4] = -1
     _check_some(_shared(cache, L, T, q, impl), q, cache, L, T, kind, [np.arange(L) < 1024])
+
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("shape,scale", [(_rising, 1.5), (_rising, 6.0), (_late, 1.5), (_scales, 1.5), (_quiet, 1.5)])
+@pytest.mark.parametrize("kind,dtype,impl", KINDS[:3])
+def test_uneven_caches_in_long_shares(shape, scale, kind, dtype, impl, T):
+    """The running maximum is raised within a share, several times where keys rise (scores to over 100)."""
+    L = 1500
+    cache = Bs8Cache([L], kv=1)
+    cache.fill([L], seed=60, shape=shape)
+    q = queries(T, 1, 61, dtype, scale)
+    if shape is _quiet:
+        q = q.float().abs().to(dtype)
+    _check_some(_shared(cache, L, T, q, impl), q, cache, L, T, kind)
+    assert int(cache.status) == 0
