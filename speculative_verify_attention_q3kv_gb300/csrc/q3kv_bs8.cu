@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) 
         __syncthreads();                                  // the last segment's outputs are read
         for (int i = tid; i < kBs8Rows * kHeadDim; i += kFmaThreads) {
             const int r = i >> 8, d = i & 255;
-            sm.q[r * kLd + d] = r < nrows ? ld_any(a.q, ((q0 + (r >> 3)) * qheads + head * kGroup + (r & 7)) * kHeadDim + d, a.dtype) * 0.0625f : 0.0f;
+            const float x = r < nrows ? ld_any(a.q, ((q0 + (r >> 3)) * qheads + head * kGroup + (r & 7)) * kHeadDim + d, a.dtype) : 0.0f;
+            // an infinity as a NaN: against keys of one sign it would hide every position (all scores -inf)
+            sm.q[r * kLd + d] = isinf(x) ? CUDART_NAN_F : x * 0.0625f;
         }
         if (tid < kBs8Rows) {
             sm.m[tid] = -1e30f;

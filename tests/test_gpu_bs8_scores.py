@@ -121,3 +121,20 @@ def test_uneven_caches_in_long_shares(shape, scale, kind, dtype, impl, T):
         q = q.float().abs().to(dtype)
     _check_some(_shared(cache, L, T, q, impl), q, cache, L, T, kind)
     assert int(cache.status) == 0
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("inf", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("kind,dtype,impl", KINDS)
+def test_infinite_queries_whatever_the_scores_sign(kind, dtype, impl, inf, sign):
+    """An infinity against keys of one sign makes every score the same infinity, minus infinity too: the row is NaN."""
+    L, T = [300], [2]
+    cache = Bs8Cache(L, kv=1)
+    cache.fill(L, seed=62, shape=lambda k, v, b: (sign * (0.5 + np.abs(k)), v))
+    q = queries(2, 1, 63, dtype)
+    clean = cache.verify(L, T, q, impl=impl)
+    q[1, 4, 30] = inf
+    out = cache.verify(L, T, q, impl=impl)
+    bad = torch.zeros((2, 8), dtype=torch.bool, device="cuda")
+    bad[1, 4] = True
+    assert bool(torch.isnan(out[bad]).all()) and torch.equal(out[~bad], clean[~bad])
