@@ -3,8 +3,8 @@
 // The cache's codes are the MMAs' operands as they lie in memory: a page stores them in the 8 x 16-byte cores that
 // tcgen05.mma reads, so a tile of 128 positions is one bulk copy of 32 KiB for K and one for V, and nothing is
 // decoded.  What the other operands lose in 8 bits is carried by more than one code per value:
-//   q  = 2^-k (q1 + q2)      two E4M3 codes, k per row: a bf16 value has 8 significant bits, two codes hold them all;
-//                            what is below 2^-18 of the row's largest value is rounded away
+//   q  = 2^-k (q1 + q2)      two E4M3 codes, k per row, the second times 2^5: a bf16 value has 8 significant bits, and two
+//                            codes hold them all from 2^-14 of the row's largest value on; below, the half step is 2^-22 of it at most
 //   p' = p1 + p2 + p3        three E5M2 codes (3 significant bits each, every one rounded to nearest, so that signs add a
 //                            bit to the second and third) hold the weight as fp16 exactly from 2^-10 on: 11 bits, at most
 //                            2^-11 off; E5M2 for its range (2^-16 .. 2^15), and the last code times 2^7: a long context's
@@ -15,7 +15,7 @@
 //   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions,
 //                                                        two or three codes side by side in the columns, summed at the end
 // with R = 16, 32, 48 or 64 query rows (8 heads x tokens, padded).  A position is a TMEM lane, so its block's scales are two
-// numbers of one thread: the score is (S1 + S2) 2^(eK - k) log2(e) / 16, and V's scale goes into the weight's
+// numbers of one thread: the score is (S1 + 2^-5 S2) 2^(eK - k) log2(e) / 16, and V's scale goes into the weight's
 // exponent, p' = 2^(score + eV - m), while the row sum takes p' 2^-eV.  m is raised only when a score passes it by more
 // than 2^7 of headroom (a vote per tile), so most tiles need no maximum and no rescaling.
 //
@@ -36,6 +36,7 @@ namespace {
 constexpr uint32_t kTileBytes = kBs8Tile * kHeadDim;
 constexpr float kAbove = 8.0f;                 // m is set this far below the largest score: p' <= 2^8 then,
 constexpr float kRaise = 15.0f;                // and at most 2^15 until it is raised
+constexpr float kQLast = 32.0f;               // before a bf16 query's second code: what one leaves of 2^8 is 2^3 at most
 constexpr float kQStep = 4096.0f;             // between the two groups of a float32 query's codes
 constexpr float kPStep = 2048.0f;             // and of a float32 weight's: what three codes leave of 2^15 is 2^4 at most
 constexpr float kPLast = 128.0f;              // before a bf16 weight's last code: what two leave of 2^15 is 2^8 at most
@@ -322,7 +323,7 @@ __device__ void prepare_q(const Bs8Args& a, Smem<R, F32>& sm, const Bs8Share& w,
                 uint32_t h01, h23;
                 e4m3x4_to_f16(code[i], h01, h23);
                 const float2 f0 = __half22float2(as_h2(h01)), f1 = __half22float2(as_h2(h23));
-                const float rest = F32 && c == 2 ? kQStep : 1.0f;      // the second three codes carry 12 bits less
+                const float rest = !F32 ? kQLast : c == 2 ? kQStep : 1.0f;      // float32: the second three codes carry 12 bits less
                 y[4 * i] = (y[4 * i] - f0.x) * rest;
                 y[4 * i + 1] = (y[4 * i + 1] - f0.y) * rest;
                 y[4 * i + 2] = (y[4 * i + 2] - f1.x) * rest;
@@ -484,8 +485,8 @@ __device__ void softmax(const Bs8Args& a, Smem<R, F32>& sm, Bs8Share w, uint32_t
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < H / 2; ++c)
-                        d2[c] = F32 && q == 2 ? fma2(d2[c], both(1.0f / kQStep), reinterpret_cast<float2*>(s2)[c])
-                                              : add2(d2[c], reinterpret_cast<float2*>(s2)[c]);
+                        d2[c] = !F32 || q == 2 ? fma2(d2[c], both(1.0f / (F32 ? kQStep : kQLast)), reinterpret_cast<float2*>(s2)[c])
+                                               : add2(d2[c], reinterpret_cast<float2*>(s2)[c]);
                 }
             }
             tc_fence_before();

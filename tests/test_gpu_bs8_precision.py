@@ -59,3 +59,20 @@ def test_weights_hold_eleven_bits(T):
     q[:, :, 0] = 16.0 * (0.25 + 0.75 * torch.rand((16 * T, 8), generator=gen, device="cuda"))
     q = q.to(torch.bfloat16)
     _within(*_second_of_two(T, (8.0 * one, 4.0 * one), -64.0 * one, q, 70), 2.0 ** -11 + 2.0 ** -17)
+
+
+@pytest.mark.parametrize("T", [1, 4, 6, 8])
+def test_queries_next_to_a_large_value(T):
+    """One value of a query row is 2^10.5 to 2^11.5 times the others, at a dim where the keys are zero: the others count with all of
+    their 8 bits (two codes hold them down to 2^-14 of the largest value).
+
+    All small values of a row are alike, so that what one loses all lose.  The scores are off by 2^-22 times the sum of their
+    products' magnitudes and by 2^-22 (|s| + max |s|), all of them 10 at most: 2^-16 in all, for weight and row sum.  The weight is
+    rounded to fp16 as above."""
+    many = np.ones(256, np.float32)
+    many[0] = 0.0
+    gen = torch.Generator(device="cuda").manual_seed(73)
+    q = (2.0 ** -11.5 * (1.0 + torch.rand((16 * T, 8, 1), generator=gen, device="cuda"))).expand(-1, -1, 256).clone()
+    q[:, :, 0] = 1.0
+    q = q.to(torch.bfloat16)
+    _within(*_second_of_two(T, (896.0 * many, 448.0 * many), -896.0 * many, q, 72), 2.0 ** -11 + 2.0 ** -16)
