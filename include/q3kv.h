@@ -802,7 +802,7 @@ Q3KV_API int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_s
  * A slot whose rows are not within num_rows, or a range of biases outside num_biases, sets
  * Q3KV_STATUS_BAD_LENGTH (the slot, or its biases, are skipped).  A step token or a bias token
  * outside [0, vocab), or a bias token not above the one before it, sets Q3KV_STATUS_BAD_TOKEN
- * and is skipped. */
+ * and is skipped; of several biases that are then left for one token the last counts. */
 Q3KV_API int q3kv_process_logits(void* stream, const void* logits, void* out, int32_t dtype, int32_t vocab,
                      const int32_t* d_q_offsets, const int32_t* d_n_q, const int32_t* d_tokens,
                      int32_t num_slots, int32_t num_rows, int32_t max_n_q,

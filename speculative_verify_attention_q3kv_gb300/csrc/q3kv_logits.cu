@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 5) process_logits_kernel(LogitArgs a
     extern __shared__ __align__(16) uint8_t s_rows[];       // [kRing][kRowBytes]
     __shared__ float s_bias[kChunk];
     __shared__ int s_tok[kMaxNq];
+    __shared__ int s_unsorted;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, slot = blockIdx.y;
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 5) process_logits_kernel(LogitArgs a
     }
     bool biased = false;                 // a bias is
     if (b1 > b0) {
+        if (tid == 0) s_unsorted = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) s_bias[tid + i * kThreads] = 0.0f;
         __syncthreads();
@@ -211,8 +213,9 @@ __global__ void __launch_bounds__(kThreads, 5) process_logits_kernel(LogitArgs a
 #pragma unroll
             for (int k = 0; k < kBiasAhead; ++k) {
                 if (i0 + k * kThreads >= b1) break;
-                // ascending ids: no id twice, so the sum does not depend on an order
+                // ascending ids: no id twice, so no order of the stores
                 if (t[k] < 0 || t[k] >= a.vocab || before[k] >= t[k]) {
+                    s_unsorted = 1;
                     if (report) atomicOr(a.status, Q3KV_STATUS_BAD_TOKEN);
                 } else if (t[k] >= base && t[k] < base + kChunk) {
                     s_bias[t[k] - base] = value[k];
@@ -221,6 +224,18 @@ __global__ void __launch_bounds__(kThreads, 5) process_logits_kernel(LogitArgs a
             }
         }
         biased = __syncthreads_or(biased);
+        // Where the ids do not ascend throughout, one may be left twice (5, 3, 5): the list once more, by one warp and in order,
+        // so that the last entry stays.
+        if (s_unsorted && biased && tid < 32) {
+            for (int i0 = b0; i0 < b1; i0 += 32) {
+                const int i = i0 + tid;
+                const int t = i < b1 ? a.bias_tokens[i] : -1, before = i > b0 && i < b1 ? a.bias_tokens[i - 1] : -1;
+                const bool mine = t >= base && t < min(base + kChunk, a.vocab) && before < t;
+                const uint32_t same = __match_any_sync(0xffffffffu, mine ? t : -1);
+                if (mine && tid == 31 - __clz(same)) s_bias[t - base] = a.bias_values[i];
+                __syncwarp();
+            }
+        }
     }
     near = __syncthreads_or(near);
 

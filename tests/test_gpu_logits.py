@@ -334,3 +334,20 @@ def test_logits_on_another_stream_and_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         c.check(out)
+
+
+@pytest.mark.parametrize("n", [3, 70, 700])
+def test_biases_out_of_order_do_not_depend_on_one(n):
+    """5, 3, 5, 3, ...: every 3 is not above the 5 before it and is skipped; of the entries left for one token the last counts."""
+    toks = np.array([5, 3] * n)[:2 * n - 1]
+    # and tokens of another chunk, ascending but for one that comes again later
+    toks = np.concatenate([toks, [2050, 2060, 2055, 2060, 4000]])
+    vals = np.arange(1, len(toks) + 1, dtype=np.float32)
+    x = torch.zeros((2, 4096), device="cuda")
+    want = torch.zeros((2, 4096))
+    want[:, 5], want[:, 2050], want[:, 2060], want[:, 4000] = float(vals[2 * n - 2]), float(vals[-5]), float(vals[-2]), float(vals[-1])
+    for _ in range(20):
+        out, status = torch.full_like(x, 77.0), i32([0])
+        api.process_logits(x, out, i32([0]), i32([2]), i32([0, 0]), 2, bias_offsets=i32([0, len(toks)]), bias_tokens=i32(toks),
+                           bias_values=torch.from_numpy(vals).cuda(), status=status)
+        assert torch.equal(out.cpu(), want) and int(status) == _lib.Q3KV_STATUS_BAD_TOKEN
