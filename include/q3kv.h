@@ -707,7 +707,8 @@ Q3KV_API int q3kv_accept_draft(void* stream, const void* logits, int32_t dtype, 
  * and the 16 blocks' scales are float32 at byte 65536 + 4*(r/16).  16-byte aligned.
  * Arguments, status bits and errors of q3kv_bs8_append are those of q3kv_append
  * (SCALE_OVERFLOW: a finite value above 448 2^64, which saturates; BAD_LENGTH: also a negative row
- * offset).  A NaN in K is a NaN code; one in V is a zero there and a NaN code in K at the same position
+ * offset).  The pool must not overlap another operand (Q3KV_ERR_INVALID_ARG where the call can see it: not the
+ * ends of k and v).  A NaN in K is a NaN code; one in V is a zero there and a NaN code in K at the same position
  * and dim, so that queries that see the position come out as NaN and no others do. */
 Q3KV_API int q3kv_bs8_pool_bytes(const q3kv_cache_desc* desc, size_t* bytes);
 Q3KV_API int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_pool,
@@ -728,7 +729,8 @@ Q3KV_API int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_
  * a page out of range count as hidden (Q3KV_STATUS_BAD_PAGE); a row that sees nothing is 0.  A
  * query row that is not finite gives NaN; scores have to stay within float32.  The tensor-core leg
  * keeps weights times V's block scales in float32: V blocks of a context whose scales lie more than
- * 2^90 apart may lose weights.  Neither out nor the workspace may overlap another operand. */
+ * 2^90 apart may lose weights.  Neither out nor the workspace may overlap another operand
+ * (Q3KV_ERR_INVALID_ARG where the call can see it: not the ends of q and out). */
 Q3KV_API int q3kv_bs8_workspace_bytes(const q3kv_cache_desc* desc, int32_t num_slots, int64_t max_ctx_len,
                      int32_t max_n_q, int32_t impl, size_t* bytes);
 Q3KV_API int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* d_pool,

@@ -841,7 +841,10 @@ def bs8_verify_attn(desc: CacheDesc, pool: torch.Tensor, page_table: torch.Tenso
     if out.dim() != 3 or out.shape[0] < shape[0] or out.shape[1:] != shape[1:]:
         raise ValueError(f"out must be [rows >= {shape[0]}, {heads}, {HEAD_DIM}], got {tuple(out.shape)}")
     reads, ws_bytes = (("q", p_q, q.nbytes), ("the pool", p_pool, pool.nbytes)), workspace.nbytes
-    _refuse_overlap("out", p_out, out.nbytes, *reads, ("the workspace", p_ws, ws_bytes))
+    # the library itself holds the workspace against the page table and the lists; only the binding knows where out ends
+    _refuse_overlap("out", p_out, out.nbytes, *reads, ("the workspace", p_ws, ws_bytes), ("the page table", p_table, 4 * n * pages),
+                    ("the lengths", p_ctx, 4 * n), ("the token counts", p_nq, 4 * n), ("the offsets", p_off, 4 * n),
+                    ("the status", p_status or 0, 4 if p_status else 0))
     _refuse_overlap("workspace", p_ws, ws_bytes, *reads)
     rc = lib.q3kv_bs8_verify_attn(_stream(stream), ctypes.byref(desc), p_pool, p_table, pages, p_ctx, p_nq, p_off, n, max_ctx_len,
                                   max_n_q, layer, p_q, _dtype_code(q), p_out, impl, p_ws, ws_bytes, p_status)

@@ -537,6 +537,16 @@ int bs8_check(const q3kv_cache_desc* d, int32_t num_slots, int64_t max_ctx_len, 
     return Q3KV_OK;
 }
 
+// A buffer that a call writes shares a byte with its page table, its lists or its status.
+bool over_lists(const void* buffer, int64_t bytes, const int32_t* table, int32_t pages_per_slot, const int32_t* lengths, const int32_t* counts,
+                const int32_t* offsets, int32_t num_slots, const int32_t* status) {
+    const int64_t list = 4 * (int64_t)num_slots;
+    return overlap(buffer, bytes, table, list * pages_per_slot) || overlap(buffer, bytes, lengths, list) || overlap(buffer, bytes, counts, list) ||
+           overlap(buffer, bytes, offsets, list) || (status && overlap(buffer, bytes, status, 4));
+}
+
+size_t bs8_pool_size(const q3kv_cache_desc* d) { return (size_t)d->num_pages * d->num_layers * d->num_kv_heads * 2 * kBs8UnitBytes; }
+
 size_t bs8_partials(int ctas) { return (size_t)ctas * 2 * kBs8PartFloats * sizeof(float); }
 
 }  // namespace
@@ -556,7 +566,7 @@ int q3kv_bs8_pool_bytes(const q3kv_cache_desc* desc, size_t* bytes) {
     int e = q3kv::check_desc(desc);
     if (e != Q3KV_OK) return e;
     if (!bytes) return Q3KV_ERR_INVALID_ARG;
-    *bytes = (size_t)desc->num_pages * desc->num_layers * desc->num_kv_heads * 2 * q3kv::kBs8UnitBytes;
+    *bytes = q3kv::bs8_pool_size(desc);
     return Q3KV_OK;
 }
 
@@ -573,6 +583,10 @@ int q3kv_bs8_append(void* stream, const q3kv_cache_desc* desc, void* d_pool, con
     if (num_slots == 0 || max_n_new == 0) return Q3KV_OK;
     if (!d_pool || !d_page_table || !d_slot_len || !d_n_new || !d_row_offsets || !k || !v) return Q3KV_ERR_INVALID_ARG;
     if (!aligned16(d_pool) || !aligned16(k) || !aligned16(v)) return Q3KV_ERR_INVALID_ARG;
+    const int64_t pool_bytes = (int64_t)bs8_pool_size(desc);          // of k and v the call knows where they begin
+    if (over_lists(d_pool, pool_bytes, d_page_table, max_pages_per_slot, d_slot_len, d_n_new, d_row_offsets, num_slots, d_status) ||
+        overlap(d_pool, pool_bytes, k, 16) || overlap(d_pool, pool_bytes, v, 16))
+        return Q3KV_ERR_INVALID_ARG;
     AppendArgs a{};
     a.pool = static_cast<uint8_t*>(d_pool);
     a.page_table = d_page_table;
@@ -621,6 +635,12 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     if (!d_pool || !d_page_table || !d_ctx_len || !d_n_q || !d_q_offsets || !q || !out) return Q3KV_ERR_INVALID_ARG;
     if (!aligned16(d_pool) || !aligned16(q) || !aligned16(out) || !aligned16(d_workspace)) return Q3KV_ERR_INVALID_ARG;
     if (!d_workspace) return Q3KV_ERR_WORKSPACE_TOO_SMALL;
+    const int64_t ws_bytes = (int64_t)workspace_bytes;                // of q and out the call knows where they begin
+    if (over_lists(d_workspace, ws_bytes, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q, d_q_offsets, num_slots, d_status) ||
+        over_lists(out, 16, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q, d_q_offsets, num_slots, d_status) ||
+        overlap(d_workspace, ws_bytes, d_pool, (int64_t)bs8_pool_size(desc)) || overlap(out, 16, d_pool, (int64_t)bs8_pool_size(desc)) ||
+        overlap(d_workspace, ws_bytes, q, 16) || overlap(d_workspace, ws_bytes, out, 16))
+        return Q3KV_ERR_INVALID_ARG;
     int ctas = 0;
     e = device_sm_count(&ctas);
     if (e != Q3KV_OK) return e;

@@ -344,3 +344,43 @@ def test_count_and_logits_binding(fake):
                  (lg.view(-1), lg.view(-1), off, n, tok), (lg, None, off, n, tok), (lg.t(), lg.t(), off, n, tok)):
         with pytest.raises((ValueError, TypeError)):
             api.process_logits(*args, 5)
+
+
+def test_bs8_outputs_over_lists_are_refused(lib):
+    """What a call writes may not be what it, or its merge, still reads: lengths that change under it would send rows anywhere."""
+    pool, ws, out, lists = 1 << 30, 2 << 30, 3 << 30, [1 << 20, 2 << 20, 3 << 20, 4 << 20]
+    size, n = 10 * 3 * 2 * 2 * 65600, 1 << 20
+    append = dict(table=lists[0], ln=lists[1], new=lists[2], off=lists[3], k=5 << 20, v=6 << 20, status=7 << 20)
+    inside = (pool, pool + size - 4, pool - 4)
+    for name in append:
+        for at in (pool, pool + size - 16) if name in "kv" else inside if name in ("table", "ln", "new", "off") else inside[:2]:
+            a = dict(append, **{name: at})
+            assert lib.q3kv_bs8_append(None, _ref(_desc()), pool, a["table"], 4, a["ln"], a["new"], a["off"], 2, 3, 0, a["k"], a["v"], 1,
+                                       a["status"]) == INVALID, (name, at)
+    verify = dict(pool=pool, table=lists[0], ctx=lists[1], nq=lists[2], off=lists[3], q=5 << 20, out=out, ws=ws, status=7 << 20)
+
+    def call(**kw):
+        a = dict(verify, **kw)
+        return lib.q3kv_bs8_verify_attn(None, _ref(_desc()), a["pool"], a["table"], 4, a["ctx"], a["nq"], a["off"], 2, 1000, 4, 0, a["q"], 1,
+                                        a["out"], 0, a["ws"], n, a["status"])
+
+    for name in ("table", "ctx", "nq", "off", "status"):
+        for at in (ws, ws + n - 4, out, out + 12):
+            assert call(**{name: at}) == INVALID, (name, at)
+    for kw in (dict(ws=pool), dict(ws=pool + size - 16), dict(out=pool), dict(out=pool + size - 16), dict(q=ws), dict(out=ws + n - 16), dict(ws=pool - n + 16)):
+        assert call(**kw) == INVALID, kw
+
+
+def test_bs8_binding_refuses_outputs_over_lists(fake):
+    words = torch.zeros(40000, dtype=i32)
+    out = words[:4 * 16 * 256].view(torch.float32).view(4, 16, 256)
+    t = _verify_args(out=out)
+    call = lambda t, status=None: api.bs8_verify_attn(t["desc"], t["pool"], t["table"], t["ctx"], t["nq"], t["off"], 100, 4, 0, t["q"], t["out"],  # noqa: E731
+                                                      t["ws"], status=status)
+    call(t, status=torch.zeros(1, dtype=i32))
+    for kw in (dict(table=words[100:106].view(2, 3)), dict(ctx=words[:2]), dict(nq=words[16380:16382]), dict(off=words[16383:16386])):
+        with pytest.raises(ValueError, match="out overlaps"):
+            call(dict(t, **kw))
+    with pytest.raises(ValueError, match="out overlaps the status"):
+        call(t, status=words[7:8])
+    call(dict(t, off=words[16384:16387]))
