@@ -208,6 +208,9 @@ constexpr int kFmaThreads = 256;
 constexpr int kSub = 64;                  // positions per sub-tile
 constexpr int kLd = kHeadDim + 4;         // floats per row in shared memory: neighbouring rows start 4 banks apart
 constexpr int kLdP = kBs8Rows + 4;
+// A row's maximum before its first position: finite, and times log2(e) too, so that a row that sees nothing takes no difference
+// of infinities and a row of NaNs is no empty partial.
+constexpr float kLowest = -2.35e38f;
 struct FmaSmem {
     float q[kBs8Rows * kLd];
     float kv[kSub * kLd];
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kFmaThreads) verify_bs8_fma_kernel(Bs8Args a) 
             sm.q[r * kLd + d] = isinf(x) ? CUDART_NAN_F : x * 0.0625f;
         }
         if (tid < kBs8Rows) {
-            sm.m[tid] = -1e30f;
+            sm.m[tid] = kLowest;
             sm.l[tid] = 0.0f;
         }
         float o[8][8];

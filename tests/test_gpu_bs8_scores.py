@@ -138,3 +138,16 @@ def test_infinite_queries_whatever_the_scores_sign(kind, dtype, impl, inf, sign)
     bad = torch.zeros((2, 8), dtype=torch.bool, device="cuda")
     bad[1, 4] = True
     assert bool(torch.isnan(out[bad]).all()) and torch.equal(out[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("score", [-1e36, 1e36])
+@pytest.mark.parametrize("kind,dtype,impl", KINDS)
+def test_scores_near_the_ends_of_float32(kind, dtype, impl, score):
+    """One position has all of the weight whatever its score: its V, off by the roundings of the weight (2^-11 as fp16), of the quotient
+    and of the output."""
+    cache = Bs8Cache([1], kv=1)
+    cache.fill([1], seed=64, shape=lambda k, v, b: (np.full_like(k, score / 1e18 / 16), v))
+    q = torch.full((1, 8, 256), 1e18, device="cuda").to(dtype)
+    got = cache.verify([1], [1], q, impl=impl).double().cpu().numpy()
+    v = cache.values(0, 1)[1][0, 0]
+    assert np.all(np.abs(got - v) <= (2.0 ** -11 + 2.0 ** -8 + 2.0 ** -18) * np.abs(v))
