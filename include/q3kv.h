@@ -788,7 +788,7 @@ Q3KV_API int q3kv_count_tokens(void* stream, int16_t* d_counts, int64_t counts_s
  * it comes after the step's tokens t_0 .. t_j (d_tokens, same indexing), which d_counts does not
  * hold yet.  With c = count + #{i <= j : t_i = x}, in float32, for every token x of the row:
  *   y = l;  if c > 0 or the prompt holds x:  y = y > 0 ? y / repetition : y * repetition
- *     (the quotient as the product with 1 / repetition)
+ *     (the quotient as the product with 1 / repetition, which has to be a normal number)
  *   if c > 0:  y = y - frequency c - presence
  *   y = y + bias(x);  where the row's mask bit is 0:  y = -inf
  * and out = y rounded to the logits' dtype (f32 or bf16).

@@ -1,4 +1,4 @@
-// Verify attention over the block-scaled 8-bit cache, tensor-core leg (bf16 queries and outputs).
+// Verify attention over the block-scaled 8-bit cache, tensor-core leg (bf16 or float32 queries and outputs).
 //
 // The cache's codes are the MMAs' operands as they lie in memory: a page stores them in the 8 x 16-byte cores that
 // tcgen05.mma reads, so a tile of 128 positions is one bulk copy of 32 KiB for K and one for V, and nothing is
@@ -10,6 +10,7 @@
 //                            2^-11 off; E5M2 for its range (2^-16 .. 2^15), and the last code times 2^7: a long context's
 //                            many small weights are not lost next to a large one, and where they are equal, and so is
 //                            what they lose, their sum is right
+// Float32 queries take six codes of each, in two groups.
 // Contractions (M = 128, float32 accumulation in TMEM):
 //   S^T[p][r | R + r] = K[p][:] . q1[r][:] | q2[r][:]   A = K codes (K-major), N = 2 R columns, K = 256 dims
 //   O^T[d][r] += V[:][d] . p_i'[:][r], i = 1..3          A = V codes (MN-major), two halves of 128 dims, K = 128 positions,
@@ -21,7 +22,8 @@
 //
 // Bound: the codes' bytes.  At 8 tokens a tile's 64 KiB take about 2,900 cycles of an SM's share of HBM (655,360 positions
 // of 2 heads: 112 us, 6,000 GB/s; 1 token 103 us, 6,500 GB/s); its 24 MMAs and its softmax, which overlap, less.  9 to 16
-// tokens are two chunks of rows and take twice that (165 and 208 us).  One CTA per SM; warp 0 copies, warps 1-3 issue the MMAs, the others are the softmax: groups of
+// tokens are two chunks of rows: the second reads its tiles from L2, and the chain from scores to codes bounds both (12 tokens 166 us,
+// 16 212 us).  One CTA per SM; warp 0 copies, warps 1-3 issue the MMAs, the others are the softmax: groups of
 // four warps with a thread per position and 8 or 16 rows.
 #include <math_constants.h>
 
