@@ -638,16 +638,17 @@ int q3kv_bs8_verify_attn(void* stream, const q3kv_cache_desc* desc, const void* 
     if (!d_pool || !d_page_table || !d_ctx_len || !d_n_q || !d_q_offsets || !q || !out) return Q3KV_ERR_INVALID_ARG;
     if (!aligned16(d_pool) || !aligned16(q) || !aligned16(out) || !aligned16(d_workspace)) return Q3KV_ERR_INVALID_ARG;
     if (!d_workspace) return Q3KV_ERR_WORKSPACE_TOO_SMALL;
-    const int64_t ws_bytes = (int64_t)workspace_bytes;                // of q and out the call knows where they begin
-    if (over_lists(d_workspace, ws_bytes, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q, d_q_offsets, num_slots, d_status) ||
-        over_lists(out, 16, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q, d_q_offsets, num_slots, d_status) ||
-        overlap(d_workspace, ws_bytes, d_pool, (int64_t)bs8_pool_size(desc)) || overlap(out, 16, d_pool, (int64_t)bs8_pool_size(desc)) ||
-        overlap(d_workspace, ws_bytes, q, 16) || overlap(d_workspace, ws_bytes, out, 16))
+    const int64_t pool_bytes = (int64_t)bs8_pool_size(desc);          // of q and out the call knows where they begin
+    if (over_lists(out, 16, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q, d_q_offsets, num_slots, d_status) || overlap(out, 16, d_pool, pool_bytes))
         return Q3KV_ERR_INVALID_ARG;
     int ctas = 0;
     e = device_sm_count(&ctas);
     if (e != Q3KV_OK) return e;
     if (workspace_bytes < bs8_partials(ctas)) return Q3KV_ERR_WORKSPACE_TOO_SMALL;
+    const int64_t ws_bytes = (int64_t)bs8_partials(ctas);             // other operands may lie behind what the call uses
+    if (over_lists(d_workspace, ws_bytes, d_page_table, max_pages_per_slot, d_ctx_len, d_n_q, d_q_offsets, num_slots, d_status) ||
+        overlap(d_workspace, ws_bytes, d_pool, pool_bytes) || overlap(d_workspace, ws_bytes, q, 16) || overlap(d_workspace, ws_bytes, out, 16))
+        return Q3KV_ERR_INVALID_ARG;
     Bs8Args a{};
     a.pool = static_cast<const uint8_t*>(d_pool);
     a.page_table = d_page_table;

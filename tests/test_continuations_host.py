@@ -348,8 +348,8 @@ def test_count_and_logits_binding(fake):
 
 def test_bs8_outputs_over_lists_are_refused(lib):
     """What a call writes may not be what it, or its merge, still reads: lengths that change under it would send rows anywhere."""
-    pool, ws, out, lists = 1 << 30, 2 << 30, 3 << 30, [1 << 20, 2 << 20, 3 << 20, 4 << 20]
-    size, n = 10 * 3 * 2 * 2 * 65600, 1 << 20
+    pool, out, lists = 1 << 30, 3 << 30, [1 << 20, 2 << 20, 3 << 20, 4 << 20]
+    size = 10 * 3 * 2 * 2 * 65600
     append = dict(table=lists[0], ln=lists[1], new=lists[2], off=lists[3], k=5 << 20, v=6 << 20, status=7 << 20)
     inside = (pool, pool + size - 4, pool - 4)
     for name in append:
@@ -357,18 +357,18 @@ def test_bs8_outputs_over_lists_are_refused(lib):
             a = dict(append, **{name: at})
             assert lib.q3kv_bs8_append(None, _ref(_desc()), pool, a["table"], 4, a["ln"], a["new"], a["off"], 2, 3, 0, a["k"], a["v"], 1,
                                        a["status"]) == INVALID, (name, at)
-    verify = dict(pool=pool, table=lists[0], ctx=lists[1], nq=lists[2], off=lists[3], q=5 << 20, out=out, ws=ws, status=7 << 20)
+    verify = dict(pool=pool, table=lists[0], ctx=lists[1], nq=lists[2], off=lists[3], q=5 << 20, out=out, status=7 << 20)
 
     def call(**kw):
         a = dict(verify, **kw)
         return lib.q3kv_bs8_verify_attn(None, _ref(_desc()), a["pool"], a["table"], 4, a["ctx"], a["nq"], a["off"], 2, 1000, 4, 0, a["q"], 1,
-                                        a["out"], 0, a["ws"], n, a["status"])
+                                        a["out"], 0, 2 << 30, 1 << 20, a["status"])
 
     for name in ("table", "ctx", "nq", "off", "status"):
-        for at in (ws, ws + n - 4, out, out + 12):
+        for at in (out, out + 12):
             assert call(**{name: at}) == INVALID, (name, at)
-    for kw in (dict(ws=pool), dict(ws=pool + size - 16), dict(out=pool), dict(out=pool + size - 16), dict(q=ws), dict(out=ws + n - 16), dict(ws=pool - n + 16)):
-        assert call(**kw) == INVALID, kw
+    for at in (pool, pool + size - 16):
+        assert call(out=at) == INVALID
 
 
 def test_bs8_binding_refuses_outputs_over_lists(fake):

@@ -473,3 +473,32 @@ def test_the_longest_share():
     c = cache.verify([n], [1], q.bfloat16())
     d = cache.verify([n], [1], q.bfloat16().float(), impl=FMA)
     assert float((c.float() - d).abs().max()) <= 2.0 ** -7 * float(d.abs().max())
+
+
+def test_workspaces_over_other_operands_are_refused():
+    """What the call uses of its workspace is nobody else's; what lies behind that in the same buffer may be."""
+    L, T = [300, 40], [2, 1]
+    cache = Bs8Cache(L, kv=1)
+    cache.fill(L, seed=45)
+    q = queries(3, 1, 46, torch.bfloat16)
+    want = cache.verify(L, T, q)
+    need = api.bs8_workspace_bytes(cache.desc, 2, 300, 2)
+    room = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    base, lib = room.data_ptr(), _lib.load()
+    lists = dict(table=cache.page_table, ctx=i32(L), nq=i32(T), off=offsets(T), status=cache.status, pool=cache.pool, q=q, out=torch.zeros_like(q))
+
+    def call(**at):
+        p = {k: at.get(k, t.data_ptr()) for k, t in lists.items()}
+        return lib.q3kv_bs8_verify_attn(None, cache.desc, p["pool"], p["table"], cache.pt.shape[1], p["ctx"], p["nq"], p["off"], 2, 300, 2, 0, p["q"], 1,
+                                        p["out"], 0, base, room.numel(), p["status"])
+
+    for name in lists:
+        for at in (base, base + need - 16):
+            assert call(**{name: at}) == _lib.Q3KV_ERR_INVALID_ARG, name
+    torch.cuda.synchronize()
+    assert bool((lists["out"] == 0).all()) and not bool(room.any())
+    room[need:need + 8].copy_(lists["ctx"].view(torch.uint8))      # the lengths behind it
+    torch.cuda.synchronize()
+    assert call(ctx=base + need) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(lists["out"], want) and int(cache.status) == 0
